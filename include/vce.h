@@ -461,6 +461,96 @@ int lce_backward_shard_scaled(const void* X, const void* W, int64_t M, int64_t H
 int vce_gemm_bf16(const void* P, int64_t ldp, int p_dim, const void* Q, int64_t ldq, int q_dim,
                   int64_t rows, int64_t cols, int64_t K, float* C, int64_t ldc, void* stream);
 
+/*
+ * Residual + RMS norm: what makes the head's input X from the last layer's
+ * output.  Per row of H values,
+ *     h = x + residual   (h = x without a residual)
+ *     r = 1 / sqrt(mean_j h_j^2 + eps)
+ *     y_j = h_j r (w_j + weight_offset)
+ * in FP32 from the inputs to y, rounded once; h is normed before it is rounded
+ * for storage.  The sum of squares is an FP32 sum: it overflows when sqrt(H)
+ * |h| reaches about 1.8e19 (y is 0 then).  A NaN or infinity makes its row's y
+ * NaN where the formula does.  eps = 0 gives NaN for a row of zeros.
+ *
+ *  rms_forward
+ *   x, residual (M, H) of `dtype`; row i starts at element i * ldx (i * ldr),
+ *     its H elements are contiguous; ldx, ldr >= H (with M > 1) or 0 for one
+ *     row read M times.  residual may be NULL.  1 <= H <= 32768
+ *     (VCE_EUNSUPPORTED above).
+ *   weight (H) of `wdtype` (FP32 or BF16, whatever `dtype` is).
+ *   weight_offset finite (0, or 1 for weights stored as w - 1); eps >= 0.
+ *   y (M, H) of `dtype`, contiguous.   h (M, H) of `dtype`, contiguous, or
+ *     NULL: x + residual, the next residual stream (required with a residual).
+ *   rstd (M) FP32 or NULL: r, for rms_backward.
+ *   y or h may be x or residual itself where that input is contiguous (ldx or
+ *     ldr = H); any other overlap of an output with another array is VCE_EALIAS.
+ *   Pointers and leading dimensions of 16 bytes take the wide loads; others
+ *   (odd H, odd strides) are read element by element.
+ *
+ *  rms_forward_mx8: the same with y as microscaled 8 bits instead (E4M3 with
+ *    one scale per 32, see mx_quantize), rounded once from FP32: q (M, H)
+ *    bytes, scales (M, H / 32) bytes, the operand mx_logits takes.  H must be a
+ *    multiple of 32 (VCE_EUNSUPPORTED).  q 16-byte aligned.
+ *
+ *  rms_backward: from dy, the gradient of y,
+ *     g_j = dy_j (w_j + weight_offset),  xh_j = h_j r
+ *     dx_j = r (g_j - xh_j mean_i(g_i xh_i)) + dh_j
+ *     dweight_j = sum_rows dy_j xh_j
+ *   dy, h (M, H) of `dtype`, contiguous; h the forward's h (x without a
+ *     residual); rstd the forward's.  dh (M, H) of `dtype` or NULL: the
+ *     gradient that reaches h by the residual stream.
+ *   dx (M, H) of `dtype`: the gradient of x, and of the residual too.  It may
+ *     be dy, dh or h itself; any other overlap is VCE_EALIAS.
+ *   dweight (H) FP32 or NULL, overwritten (zeros with M = 0).
+ *   workspace: at least rms_backward_workspace_size(M, H) bytes, 16-byte
+ *     aligned, needed with dweight only; its contents need not survive.
+ *   The sums' order depends on M and H only: results are reproducible.
+ */
+int rms_forward(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
+                int64_t ldr, const void* weight, int wdtype, float weight_offset, float eps,
+                void* y, void* h, float* rstd, void* stream);
+int rms_forward_mx8(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
+                    const void* residual, int64_t ldr, const void* weight, int wdtype,
+                    float weight_offset, float eps, uint8_t* q, uint8_t* scales, void* h,
+                    float* rstd, void* stream);
+size_t rms_backward_workspace_size(int64_t M, int64_t H);
+int rms_backward(const void* dy, const void* h, int dtype, int64_t M, int64_t H,
+                 const void* weight, int wdtype, float weight_offset, const float* rstd,
+                 const void* dh, void* dx, float* dweight, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/*
+ * Microscaled (MX) formats: blocks of 32 consecutive values of a row share one
+ * power-of-two scale.  A scale is a byte b standing for 2^(b - 127), 255 for
+ * NaN (E8M0).  Values are
+ *   VCE_MX_E4M3: one byte, sign, 4 exponent bits (bias 7), 3 mantissa bits;
+ *                largest 448; codes 0x7f and 0xff are NaN
+ *   VCE_MX_E2M1: 4 bits, sign, 2 exponent bits (bias 1), 1 mantissa bit (0,
+ *                0.5, 1, 1.5, 2, 3, 4, 6); value 2 i of a row in the low half
+ *                of byte i, value 2 i + 1 in the high half
+ * A row of K values takes K (E4M3) or K / 2 (E2M1) bytes and K / 32 scales; K
+ * is a multiple of 32 (VCE_EUNSUPPORTED otherwise).
+ *
+ *  mx_quantize: x (rows, K) of `dtype`, row i at element i * ldx, to q and
+ *    scales (contiguous).  A block's scale is the least power of two s >=
+ *    2^-127 with max |x| <= Vmax s (Vmax 448 or 6), so that no value is clipped;
+ *    each x / s is rounded to the nearest value of the format, ties to even.
+ *    (A scale one step smaller would clip the values between Vmax and the next
+ *    power of two by up to a third.)  A block with a NaN or an infinity gets
+ *    scale 255 and zero values.  q 16-byte aligned; x needs its element's
+ *    alignment (16-byte rows take the wide loads).
+ *  mx_dequantize: the values q and scales stand for, as FP32 (exact) or BF16
+ *    (exact unless below BF16's normal range, where they round); out (rows, K)
+ *    contiguous, 16-byte aligned.
+ *  Outputs must not overlap inputs (VCE_EALIAS).
+ */
+enum vce_mx_format { VCE_MX_E4M3 = 0, VCE_MX_E2M1 = 1 };
+
+int mx_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx, int format,
+                uint8_t* q, uint8_t* scales, void* stream);
+int mx_dequantize(const uint8_t* q, const uint8_t* scales, int format, int64_t rows, int64_t K,
+                  void* out, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -65,6 +65,15 @@ SIGNATURES = {
                                          _VP, _VP, _VP, _VP, _F32, _I32, _I64, _VP, _VP, _VP,
                                          _SZ, _VP]),
     "vce_gemm_bf16": (_I32, [_VP, _I64, _I32, _VP, _I64, _I32, _I64, _I64, _I64, _VP, _I64, _VP]),
+    "rms_forward": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _I64, _VP, _I32, _F32, _F32, _VP,
+                           _VP, _VP, _VP]),
+    "rms_forward_mx8": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _I64, _VP, _I32, _F32, _F32,
+                               _VP, _VP, _VP, _VP, _VP]),
+    "rms_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "rms_backward": (_I32, [_VP, _VP, _I32, _I64, _I64, _VP, _I32, _F32, _VP, _VP, _VP, _VP, _VP,
+                            _SZ, _VP]),
+    "mx_quantize": (_I32, [_VP, _I32, _I64, _I64, _I64, _I32, _VP, _VP, _VP]),
+    "mx_dequantize": (_I32, [_VP, _VP, _I32, _I64, _I64, _VP, _I32, _VP]),
 }
 
 _lib = None
@@ -717,3 +726,233 @@ def gemm_bf16(P: torch.Tensor, Q: torch.Tensor, K: int | None = None, *, p_dim: 
                              rows, cols, K, _ptr(C), C.stride(0), _stream(stream))
     _check("vce_gemm_bf16", rc)
     return C
+
+
+# ---- around the head: norm, microscaled formats -----------------------------------------
+# These calls run on their tensors' device whatever the current one is, and
+# allocate outputs and scratch under the stream they run on, so that freed
+# scratch is not handed to another stream while a kernel still uses it.
+
+MX_FORMATS = {"e4m3": 0, "e2m1": 1}
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _elem_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_FP32
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _mx_format(fmt: str) -> int:
+    if fmt not in MX_FORMATS:
+        raise ValueError(f"format must be one of {sorted(MX_FORMATS)}, got {fmt!r}")
+    return MX_FORMATS[fmt]
+
+
+def _on_stream(ref: torch.Tensor, stream, fn):
+    """fn(stream handle) with ref's device current and, given ``stream``, allocations under it."""
+    _need_cuda(ref)
+    if stream is None and ref.device.index == torch.cuda.current_device():
+        return fn(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(ref.device):
+        s = torch.cuda.current_stream() if stream is None else stream
+        if s.device != ref.device:
+            raise ValueError(f"stream must be on {ref.device}, got {s.device}")
+        with torch.cuda.stream(s):
+            return fn(s.cuda_stream)
+
+
+def _check_out(t, name: str, shape, dtype, ref: torch.Tensor):
+    """A given output: its shape, dtype, contiguity and device.  None passes."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                         f"{tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != ref.device:
+        raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+
+
+def _rows2d(t: torch.Tensor, name: str):
+    """(rows, cols, row stride) of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.shape[0], t.shape[1], t.stride(0)
+
+
+def _check_weight(weight: torch.Tensor, H: int, ref: torch.Tensor):
+    if weight.dim() != 1 or weight.shape[0] != H or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous with {H} elements")
+    if weight.device != ref.device:
+        raise ValueError(f"weight must be on {ref.device}, got {weight.device}")
+    return _elem_dtype(weight, "weight")
+
+
+def _rms_forward(mx, x, weight, residual, eps, weight_offset, stream, out):
+    dt = _elem_dtype(x, "x")
+    M, H, ldx = _rows2d(x, "x")
+    ldr = 0
+    if residual is not None:
+        if residual.dtype != x.dtype or tuple(residual.shape) != tuple(x.shape):
+            raise ValueError("residual must have the shape and dtype of x")
+        if residual.device != x.device:
+            raise ValueError(f"residual must be on {x.device}, got {residual.device}")
+        ldr = _rows2d(residual, "residual")[2]
+    wdt = _check_weight(weight, H, x)
+    if mx and H % 32:
+        raise ValueError(f"rows of a multiple of 32 elements are needed, got {H}")
+    out = (None,) * (4 if mx else 3) if out is None else tuple(out)
+    if len(out) != (4 if mx else 3):
+        raise ValueError(f"out must hold {4 if mx else 3} tensors (None to allocate)")
+    rstd, h = out[-2:]
+    if mx:
+        _check_out(out[0], "q", (M, H), torch.uint8, x)
+        _check_out(out[1], "scales", (M, H // 32), torch.uint8, x)
+    else:
+        _check_out(out[0], "y", (M, H), x.dtype, x)
+    _check_out(rstd, "rstd", (M,), torch.float32, x)
+    _check_out(h, "h", (M, H), x.dtype, x)
+
+    def call(s):
+        dev = x.device
+        r = torch.empty(M, dtype=torch.float32, device=dev) if rstd is None else rstd
+        ho = h
+        if ho is None and residual is not None:
+            ho = torch.empty((M, H), dtype=x.dtype, device=dev)
+        if mx:
+            q, sc = out[:2]
+            q = torch.empty((M, H), dtype=torch.uint8, device=dev) if q is None else q
+            sc = torch.empty((M, H // 32), dtype=torch.uint8, device=dev) if sc is None else sc
+            _check("rms_forward_mx8", lib().rms_forward_mx8(
+                _at(x), dt, M, H, ldx, _at(residual), ldr, _at(weight), wdt, weight_offset, eps,
+                _at(q), _at(sc), _at(ho), _at(r), s))
+            return q, sc, r, ho
+        y = torch.empty((M, H), dtype=x.dtype, device=dev) if out[0] is None else out[0]
+        _check("rms_forward", lib().rms_forward(
+            _at(x), dt, M, H, ldx, _at(residual), ldr, _at(weight), wdt, weight_offset, eps,
+            _at(y), _at(ho), _at(r), s))
+        return y, r, ho
+    return _on_stream(x, stream, call)
+
+
+def rms_forward(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                eps: float = 1e-6, *, weight_offset: float = 0.0, stream=None, out=None):
+    """Residual + RMS norm: h = x + residual, y = h / sqrt(mean h^2 + eps) * (weight +
+    weight_offset) over the rows of x (M, H), BF16 or FP32; weight (H) of either.  Rows may be
+    strided.  Returns (y, rstd, h), h None without a residual.  ``out`` gives the outputs in
+    that order (None entries are allocated); y or h may be x or residual themselves."""
+    return _rms_forward(False, x, weight, residual, eps, weight_offset, stream, out)
+
+
+def rms_forward_mx8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                    eps: float = 1e-6, *, weight_offset: float = 0.0, stream=None, out=None):
+    """``rms_forward`` with y as microscaled 8 bits (E4M3, one scale per 32), the operand of
+    ``mx_logits``.  Returns (q, scales, rstd, h)."""
+    return _rms_forward(True, x, weight, residual, eps, weight_offset, stream, out)
+
+
+def rms_backward_workspace_size(M: int, H: int) -> int:
+    return int(lib().rms_backward_workspace_size(M, H))
+
+
+def rms_backward_workspace(M: int, H: int, device="cuda") -> torch.Tensor:
+    n = rms_backward_workspace_size(M, H)
+    if n == 0:
+        raise ValueError(f"no workspace plan for M={M}, H={H}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rms_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                 dh: torch.Tensor | None = None, *, weight_offset: float = 0.0,
+                 workspace: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                 dweight: torch.Tensor | None = None, need_dweight: bool = True, stream=None):
+    """Gradient of ``rms_forward``: dy of y, dh (optional) of h by the residual stream; h is the
+    forward's h (x without a residual), rstd its rstd.  Returns (dx, dweight): dx (M, H), the
+    gradient of x and of the residual alike, in their dtype (may be given as dy, dh or h), and
+    dweight (H) FP32, None without ``need_dweight``."""
+    dt = _elem_dtype(h, "h")
+    M, H, _ = _rows2d(h, "h")
+    wdt = _check_weight(weight, H, h)
+    for t, name in ((dy, "dy"), (h, "h"), (dh, "dh"), (dx, "dx")):
+        _check_out(t, name, (M, H), h.dtype, h)
+    _check_buf(rstd, "rstd", M, like=h)
+    _check_out(dweight, "dweight", (H,), torch.float32, h)
+    if workspace is not None:
+        _check_buf(workspace, "workspace", workspace.numel(), torch.uint8, like=h)
+
+    def call(s):
+        o = torch.empty_like(h) if dx is None else dx
+        dw, ws = dweight, workspace
+        if need_dweight or dw is not None:
+            dw = torch.empty(H, dtype=torch.float32, device=h.device) if dw is None else dw
+            ws = rms_backward_workspace(M, H, h.device) if ws is None else ws
+        _check("rms_backward", lib().rms_backward(
+            _at(dy), _at(h), dt, M, H, _at(weight), wdt, weight_offset, _at(rstd), _at(dh),
+            _at(o), _at(dw), _at(ws), 0 if ws is None else ws.numel(), s))
+        return o, dw
+    return _on_stream(h, stream, call)
+
+
+def mx_quantize(x: torch.Tensor, fmt: str = "e2m1", *, stream=None, out=None):
+    """x (rows, K), BF16 or FP32, K a multiple of 32, to a microscaled format ("e4m3" or
+    "e2m1").  Returns uint8 (q, scales): q (rows, K) or (rows, K / 2), scales (rows, K / 32)."""
+    f = _mx_format(fmt)
+    dt = _elem_dtype(x, "x")
+    rows, K, ldx = _rows2d(x, "x")
+    if K == 0 or K % 32:
+        raise ValueError(f"rows of a multiple of 32 elements are needed, got {K}")
+    q, sc = (None, None) if out is None else out
+    qk = K if fmt == "e4m3" else K // 2
+    _check_out(q, "q", (rows, qk), torch.uint8, x)
+    _check_out(sc, "scales", (rows, K // 32), torch.uint8, x)
+
+    def call(s):
+        qo = torch.empty((rows, qk), dtype=torch.uint8, device=x.device) if q is None else q
+        so = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device) if sc is None \
+            else sc
+        _check("mx_quantize", lib().mx_quantize(_at(x), dt, rows, K, ldx, f, _at(qo), _at(so), s))
+        return qo, so
+    return _on_stream(x, stream, call)
+
+
+def _check_mx(q: torch.Tensor, scales: torch.Tensor, fmt: str, name: str):
+    """(rows, K, format code) of a microscaled matrix."""
+    f = _mx_format(fmt)
+    if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError(f"{name} and its scales must be uint8")
+    if q.dim() != 2 or scales.dim() != 2:
+        raise ValueError(f"{name} and its scales must have two dimensions")
+    rows, K = q.shape[0], q.shape[1] * (1 if fmt == "e4m3" else 2)
+    if K == 0 or K % 32 or tuple(scales.shape) != (rows, K // 32):
+        raise ValueError(f"{name} {tuple(q.shape)} in {fmt} needs scales of "
+                         f"({rows}, {K} / 32), got {tuple(scales.shape)}")
+    if not (q.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name} and its scales must be contiguous")
+    if scales.device != q.device:
+        raise ValueError(f"{name} and its scales must be on one device")
+    return rows, K, f
+
+
+def mx_dequantize(q: torch.Tensor, scales: torch.Tensor, fmt: str = "e2m1",
+                  dtype: torch.dtype = torch.bfloat16, *, stream=None, out=None):
+    """The values (rows, K) that q and scales stand for, as BF16 or FP32."""
+    rows, K, f = _check_mx(q, scales, fmt, "q")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    _check_out(out, "out", (rows, K), dtype, q)
+
+    def call(s):
+        o = torch.empty((rows, K), dtype=dtype, device=q.device) if out is None else out
+        _check("mx_dequantize", lib().mx_dequantize(_at(q), _at(scales), f, rows, K, _at(o),
+                                                    _elem_dtype(o, "out"), s))
+        return o
+    return _on_stream(q, stream, call)

@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libvce.so")
-SOURCES = ["vce_api.hip", "ce_kernels.hip", "lce_kernels.hip"]
+SOURCES = ["vce_api.hip", "ce_kernels.hip", "lce_kernels.hip", "rms_kernels.hip",
+           "mx_kernels.hip"]
 ARCH = "gfx950"
 
 

@@ -846,4 +846,217 @@ int vce_gemm_bf16(const void* P, int64_t ldp, int p_dim, const void* Q, int64_t 
                                              static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+
+struct Range {
+  uintptr_t lo, hi;
+};
+
+inline Range range(const void* p, int64_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return p ? Range{a, a + (uintptr_t)bytes} : Range{0, 0};
+}
+
+inline bool overlap(const Range& a, const Range& b) {
+  return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
+}
+
+inline bool dtype_ok(int d) { return d == VCE_DTYPE_FP32 || d == VCE_DTYPE_BF16; }
+inline int64_t dtype_size(int d) { return d == VCE_DTYPE_FP32 ? 4 : 2; }
+
+// Bytes from the first to the last element of (rows, cols) with a row stride.
+inline bool span_ok(int64_t rows, int64_t cols, int64_t ld, int64_t es, int64_t* bytes) {
+  int64_t t;
+  if (!mul_ok(rows - 1, ld, &t) || t > INT64_MAX / 8 - cols) return false;
+  *bytes = (t + cols) * es;
+  return true;
+}
+
+int rms_forward_impl(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
+                     const void* residual, int64_t ldr, const void* weight, int wdtype,
+                     float weight_offset, float eps, void* y, uint8_t* q, uint8_t* scales,
+                     bool mx, void* h, float* rstd, void* stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(wdtype)) return VCE_EDTYPE;
+  if (M < 0 || M > (int64_t)INT32_MAX || H <= 0) return VCE_EINVAL;
+  if (!vce::rms_width_ok(H) || (mx && H % 32 != 0)) return VCE_EUNSUPPORTED;
+  if (!(eps >= 0.0f) || !__builtin_isfinite(eps) || !__builtin_isfinite(weight_offset))
+    return VCE_EINVAL;
+  if (M == 0) return VCE_OK;
+  if (!x || !weight || (mx ? (!q || !scales) : !y) || (residual && !h)) return VCE_EINVAL;
+  if (ldx < 0 || (M > 1 && ldx != 0 && ldx < H)) return VCE_EINVAL;
+  if (residual && (ldr < 0 || (M > 1 && ldr != 0 && ldr < H))) return VCE_EINVAL;
+  const int64_t es = dtype_size(dtype);
+  int64_t xb, rb = 0;
+  if (!span_ok(M, H, ldx, es, &xb) || (residual && !span_ok(M, H, ldr, es, &rb)))
+    return VCE_EINVAL;
+  if (!aligned(x, es) || !aligned(residual, es) || !aligned(weight, dtype_size(wdtype)) ||
+      !aligned(y, es) || !aligned(h, es) || !aligned(rstd, 4) || (mx && !aligned(q, 16)))
+    return VCE_EALIGN;
+  const Range in[3] = {range(x, xb), range(residual, rb), range(weight, H * dtype_size(wdtype))};
+  const Range out[4] = {mx ? range(q, M * H) : range(y, M * H * es),
+                        range(mx ? scales : nullptr, M * (H / 32)), range(h, M * H * es),
+                        range(rstd, M * 4)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return VCE_EALIAS;
+    for (int j = 0; j < 3; ++j) {
+      if (!overlap(out[i], in[j])) continue;
+      // in place: the same rows, read by the threads that write them
+      const bool rows_out = i == 2 || (i == 0 && !mx);
+      const bool rows_in = (j == 0 && (ldx == H || M == 1)) || (j == 1 && (ldr == H || M == 1));
+      if (!(rows_out && rows_in && out[i].lo == in[j].lo)) return VCE_EALIAS;
+    }
+  }
+  vce::RmsFwdParams p;
+  p.x = x;
+  p.residual = residual;
+  p.M = M;
+  p.ldx = M == 1 ? H : ldx;  // one row's stride says nothing
+  p.ldr = M == 1 ? H : ldr;
+  p.H = (int)H;
+  p.weight = weight;
+  p.wdtype = wdtype;
+  p.w0 = weight_offset;
+  p.eps = eps;
+  p.y = mx ? nullptr : y;
+  p.q = mx ? q : nullptr;
+  p.scales = mx ? scales : nullptr;
+  p.h = h;
+  p.rstd = rstd;
+  return launch_status(
+      vce::launch_rms_forward(p, dtype, mx, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+int rms_forward(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
+                int64_t ldr, const void* weight, int wdtype, float weight_offset, float eps,
+                void* y, void* h, float* rstd, void* stream) {
+  return rms_forward_impl(x, dtype, M, H, ldx, residual, ldr, weight, wdtype, weight_offset, eps,
+                          y, nullptr, nullptr, false, h, rstd, stream);
+}
+
+int rms_forward_mx8(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
+                    const void* residual, int64_t ldr, const void* weight, int wdtype,
+                    float weight_offset, float eps, uint8_t* q, uint8_t* scales, void* h,
+                    float* rstd, void* stream) {
+  return rms_forward_impl(x, dtype, M, H, ldx, residual, ldr, weight, wdtype, weight_offset, eps,
+                          nullptr, q, scales, true, h, rstd, stream);
+}
+
+size_t rms_backward_workspace_size(int64_t M, int64_t H) {
+  if (M < 0 || M > (int64_t)INT32_MAX || !vce::rms_width_ok(H)) return 0;
+  return (size_t)vce::rms_bwd_parts(M) * (size_t)H * 4;
+}
+
+int rms_backward(const void* dy, const void* h, int dtype, int64_t M, int64_t H,
+                 const void* weight, int wdtype, float weight_offset, const float* rstd,
+                 const void* dh, void* dx, float* dweight, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(wdtype)) return VCE_EDTYPE;
+  if (M < 0 || M > (int64_t)INT32_MAX || H <= 0) return VCE_EINVAL;
+  if (!vce::rms_width_ok(H)) return VCE_EUNSUPPORTED;
+  if (!__builtin_isfinite(weight_offset)) return VCE_EINVAL;
+  if (M > 0 && (!dy || !h || !weight || !rstd || !dx)) return VCE_EINVAL;
+  const int64_t es = dtype_size(dtype);
+  if (!aligned(dy, es) || !aligned(h, es) || !aligned(weight, dtype_size(wdtype)) ||
+      !aligned(rstd, 4) || !aligned(dh, es) || !aligned(dx, es) || !aligned(dweight, 4))
+    return VCE_EALIGN;
+  if (dweight && M > 0) {
+    if (!workspace) return VCE_EINVAL;
+    if (!aligned(workspace, 16)) return VCE_EALIGN;
+    if (workspace_bytes < rms_backward_workspace_size(M, H)) return VCE_EWORKSPACE;
+  }
+  if (M > 0) {
+    const int64_t nb = M * H * es;
+    const Range in[5] = {range(dy, nb), range(h, nb), range(dh, nb),
+                         range(weight, H * dtype_size(wdtype)), range(rstd, M * 4)};
+    const Range out[3] = {
+        range(dx, nb), range(dweight, H * 4),
+        range(dweight ? workspace : nullptr, (int64_t)rms_backward_workspace_size(M, H))};
+    for (int i = 0; i < 3; ++i) {
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i], out[j])) return VCE_EALIAS;
+      for (int j = 0; j < 5; ++j)
+        if (overlap(out[i], in[j]) && !(i == 0 && j < 3 && out[i].lo == in[j].lo))
+          return VCE_EALIAS;
+    }
+  }
+  vce::RmsBwdParams p;
+  p.dy = dy;
+  p.h = h;
+  p.M = M;
+  p.H = (int)H;
+  p.weight = weight;
+  p.wdtype = wdtype;
+  p.w0 = weight_offset;
+  p.rstd = rstd;
+  p.dh = dh;
+  p.dx = dx;
+  p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+  p.dweight = dweight;
+  return launch_status(vce::launch_rms_backward(p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+// Bytes of (rows, K) values in a microscaled format and of their scales.
+inline int check_mx_shape(int64_t rows, int64_t K, int format, int64_t* qb, int64_t* sb) {
+  if (format != VCE_MX_E4M3 && format != VCE_MX_E2M1) return VCE_EDTYPE;
+  if (rows < 0 || K <= 0) return VCE_EINVAL;
+  if (K % 32 != 0) return VCE_EUNSUPPORTED;
+  int64_t n;
+  if (!mul_ok(rows, K, &n) || n > INT64_MAX / 8) return VCE_EINVAL;
+  *qb = format == VCE_MX_E4M3 ? n : n / 2;
+  *sb = n / 32;
+  return VCE_OK;
+}
+
+}  // namespace
+
+int mx_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx, int format,
+                uint8_t* q, uint8_t* scales, void* stream) {
+  if (!dtype_ok(dtype)) return VCE_EDTYPE;
+  int64_t qb, sb, xb;
+  const int rc = check_mx_shape(rows, K, format, &qb, &sb);
+  if (rc != VCE_OK || rows == 0) return rc;
+  // one thread per 16 bytes, or per element, in a grid of 2^31 workgroups at most
+  if (rows > ((int64_t)1 << 38) / K) return VCE_EUNSUPPORTED;
+  if (!x || !q || !scales) return VCE_EINVAL;
+  if (ldx < 0 || (rows > 1 && ldx != 0 && ldx < K)) return VCE_EINVAL;
+  const int64_t es = dtype_size(dtype);
+  if (!span_ok(rows, K, ldx, es, &xb)) return VCE_EINVAL;
+  if (!aligned(x, es) || !aligned(q, 16)) return VCE_EALIGN;
+  const Range in = range(x, xb), oq = range(q, qb), os = range(scales, sb);
+  if (overlap(in, oq) || overlap(in, os) || overlap(oq, os)) return VCE_EALIAS;
+  vce::MxQuantParams p;
+  p.x = x;
+  p.rows = rows;
+  p.K = K;
+  p.ldx = rows == 1 ? K : ldx;  // one row's stride says nothing
+  p.q = q;
+  p.scales = scales;
+  return launch_status(
+      vce::launch_mx_quantize(p, dtype, format, static_cast<hipStream_t>(stream)));
+}
+
+int mx_dequantize(const uint8_t* q, const uint8_t* scales, int format, int64_t rows, int64_t K,
+                  void* out, int dtype, void* stream) {
+  if (!dtype_ok(dtype)) return VCE_EDTYPE;
+  int64_t qb, sb;
+  const int rc = check_mx_shape(rows, K, format, &qb, &sb);
+  if (rc != VCE_OK || rows == 0) return rc;
+  if (rows > ((int64_t)1 << 38) / K) return VCE_EUNSUPPORTED;
+  if (!q || !scales || !out) return VCE_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16)) return VCE_EALIGN;
+  const Range oo = range(out, rows * K * dtype_size(dtype));
+  if (overlap(oo, range(q, qb)) || overlap(oo, range(scales, sb))) return VCE_EALIAS;
+  vce::MxDequantParams p;
+  p.q = q;
+  p.scales = scales;
+  p.out = out;
+  return launch_status(vce::launch_mx_dequantize(p, rows * K, format, dtype,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

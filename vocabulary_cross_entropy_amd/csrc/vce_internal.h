@@ -147,4 +147,62 @@ hipError_t launch_gemm_bf16(const void* P, int64_t ldp, int p_dim, const void* Q
                             int q_dim, int64_t rows, int64_t cols, int64_t K, float* C,
                             int64_t ldc, hipStream_t stream);
 
+// ---- residual + RMS norm -------------------------------------------------------
+
+struct RmsFwdParams {
+  const void* x;
+  const void* residual;  // optional
+  int64_t M, ldx, ldr;
+  int H;
+  const void* weight;
+  int wdtype;
+  float w0, eps;
+  void* y;          // (M, H), the norm's output (not with q)
+  uint8_t* q;       // (M, H) E4M3 and (M, H / 32) scale bytes instead of y
+  uint8_t* scales;
+  void* h;          // optional (M, H): x + residual
+  float* rstd;      // optional (M)
+};
+
+struct RmsBwdParams {
+  const void* dy;
+  const void* h;
+  int64_t M;
+  int H;
+  const void* weight;
+  int wdtype;
+  float w0;
+  const float* rstd;
+  const void* dh;  // optional (M, H)
+  void* dx;
+  float* partial;  // (rms_bwd_parts(M), H) shares of dw, NULL without dweight
+  float* dweight;  // optional (H)
+};
+
+bool rms_width_ok(int64_t H);
+int rms_bwd_parts(int64_t M);
+hipError_t launch_rms_forward(const RmsFwdParams& p, int dtype, bool mx, hipStream_t stream);
+hipError_t launch_rms_backward(RmsBwdParams p, int dtype, hipStream_t stream);
+
+// ---- microscaled formats -------------------------------------------------------
+
+struct MxQuantParams {
+  const void* x;
+  int64_t rows, K, ldx;
+  uint8_t* q;
+  uint8_t* scales;
+  bool small = false;  // thread index fits 31 bits (set by the launcher)
+};
+
+struct MxDequantParams {
+  const uint8_t* q;
+  const uint8_t* scales;
+  void* out;
+  int64_t n8 = 0;  // groups of 8 values (set by the launcher)
+};
+
+hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, int fmt, hipStream_t stream);
+hipError_t launch_mx_dequantize(MxDequantParams p, int64_t n, int fmt, int dtype,
+                                hipStream_t stream);
+
 }  // namespace vce
