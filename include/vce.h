@@ -551,6 +551,44 @@ int mx_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx, 
 int mx_dequantize(const uint8_t* q, const uint8_t* scales, int format, int64_t rows, int64_t K,
                   void* out, int dtype, void* stream);
 
+/*
+ * ce_sample: one token from each row of logits, from given uniform numbers.
+ * With m the row's maximum and T its temperature, w_i = exp((z_i - m) / T);
+ * tokens are ranked by (logit, largest first; lower index first among equals).
+ * Three filters, each on what the one before it left:
+ *   top-k  the first top_k tokens of the ranking
+ *   top-p  the shortest prefix of it whose mass (sum of w) is at least top_p
+ *          of the mass, at least one token
+ *   min-p  the tokens with w_i >= min_p (the largest w is 1)
+ * The token is the first kept i, in index order, with sum_{kept j <= i} w_j >
+ * u * sum_kept w.  T = 0 takes the first maximum whatever the filters and u.
+ * Weights are formed in FP64 and rounded to 2^-44 of the largest (2^(62 -
+ * ceil(log2 V)) of it above V = 2^18); their sums are exact, so the token does not
+ * depend on how the work is split, and is reproducible.
+ *
+ *  logits   (d0, d1, V) as in ce_forward (V < 2^31).  -inf is a masked token; a
+ *           finite mask far below the maximum has no weight either.  +inf: the
+ *           tokens at +inf share the row.
+ *  temperature, top_p, min_p (N) FP32 and top_k (N) int32, or NULL for 1, 1, 0
+ *           and 0: per row, in flattened row order.  Off: top_k <= 0 or >= V,
+ *           top_p >= 1, min_p <= 0.  top_p <= 0 keeps the first token, min_p >= 1
+ *           the maxima.
+ *  u        (N) FP32 in [0, 1).
+ *  token    (N) int64.  -1 where the row has no answer: a NaN logit, no logit
+ *           above -inf, T negative, infinite or NaN, u outside [0, 1), top_p or
+ *           min_p NaN (the values are on the device: this cannot be a status).
+ *  logprob  (N) FP32 or NULL: ln of the probability the token was drawn with,
+ *           w_token / sum_kept w (0 with T = 0; NaN where token is -1).
+ *  workspace  at least ce_sample_workspace_size(N, V) bytes (N = d0 * d1),
+ *           256-byte aligned; its contents need not survive.  Calls that may
+ *           overlap in time (two streams, two captured graphs) each need their own.
+ */
+size_t ce_sample_workspace_size(int64_t N, int64_t V);
+int ce_sample(const void* logits, int dtype, int64_t d0, int64_t d1, int64_t V, int64_t ls0,
+              int64_t ls1, const float* temperature, const int32_t* top_k, const float* top_p,
+              const float* min_p, const float* u, int64_t* token, float* logprob,
+              void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

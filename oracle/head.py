@@ -115,3 +115,36 @@ def step_at(v, s, fmt):
     with np.errstate(divide="ignore"):
         e = np.floor(np.log2(np.maximum(np.abs(v) / s, 2.0 ** emin)))
     return s * 2.0 ** (e - mb)
+
+
+# ---- drawing a token -------------------------------------------------------------
+
+def sample(z, u, T=1.0, k=0, p=1.0, min_p=0.0):
+    """(token, log-probability) of one row z, by sorting; (-1, nan) without an answer."""
+    z = np.asarray(z, np.float64) + 0.0
+    V = z.size
+    bad = -1, np.nan
+    if np.isnan(z).any() or not (T >= 0 and T < np.inf and 0 <= u < 1) or np.isnan(p) or \
+            np.isnan(min_p):
+        return bad
+    m = z.max()
+    if m == -np.inf:
+        return bad
+    if T == 0:
+        return int(np.argmax(z)), 0.0
+    if m == np.inf:
+        w = (z == m).astype(np.float64)
+    else:
+        w = np.exp((z - m) / np.float64(T))
+    order = np.argsort(-z, kind="stable")
+    order = order[w[order] >= 0]
+    if 0 < k < V:
+        order = order[:k]
+    if p < 1:
+        cum = np.cumsum(w[order])
+        n = int(np.searchsorted(cum, np.float64(p) * cum[-1], side="left")) + 1
+        order = order[:n]
+    keep = np.sort(order[w[order] >= min(np.float64(min_p), 1.0)])
+    cum = np.cumsum(w[keep])
+    j = int(np.searchsorted(cum, np.float64(u) * cum[-1], side="right"))
+    return int(keep[j]), float(np.log(w[keep[j]] / cum[-1]))

@@ -156,3 +156,54 @@ GPU_ONLY = (RuntimeError, "GPU only")
 def test_binding_rejects(call, exc):
     with pytest.raises(exc):
         call()
+
+
+def smp(L, **kw):
+    a = dict(z=A, dtype=1, d0=2, d1=3, V=1000, ls0=3000, ls1=1000, T=A + G, k=A + 2 * G,
+             p=A + 3 * G, mp=A + 4 * G, u=A + 5 * G, tok=A + 6 * G, lp=A + 7 * G, ws=A + 8 * G,
+             n=1 << 30)
+    a.update(kw)
+    return L.ce_sample(a["z"], a["dtype"], a["d0"], a["d1"], a["V"], a["ls0"], a["ls1"], a["T"],
+                       a["k"], a["p"], a["mp"], a["u"], a["tok"], a["lp"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=2), 2), (dict(d0=-1), 1), (dict(V=0), 1), (dict(ls0=-1), 1), (dict(ls1=-1), 1),
+    (dict(d0=1 << 20, d1=1 << 12), 1), (dict(d0=1 << 40, d1=1 << 40), 1), (dict(V=1 << 31), 7),
+    (dict(ls0=1 << 62), 1), (dict(z=None), 1), (dict(u=None), 1), (dict(tok=None), 1),
+    (dict(ws=None), 1), (dict(z=A + 1), 3), (dict(T=A + G + 2), 3), (dict(k=A + 2 * G + 1), 3),
+    (dict(p=A + 3 * G + 1), 3), (dict(mp=A + 4 * G + 1), 3), (dict(u=A + 5 * G + 2), 3),
+    (dict(tok=A + 6 * G + 4), 3), (dict(lp=A + 7 * G + 2), 3), (dict(ws=A + 8 * G + 128), 3),
+    (dict(n=0), 5), (dict(tok=A + 1024), 4), (dict(lp=A + 5 * G), 4), (dict(ws=A + 2 * G), 4),
+    (dict(lp=A + 6 * G + 8), 4), (dict(tok=A + 8 * G + 8), 4),
+])
+def test_ce_sample_rejects(L, kw, code):
+    assert smp(L, **kw) == code
+
+
+def test_ce_sample_sizes(L):
+    f = L.ce_sample_workspace_size
+    assert f(-1, 10) == 0 and f(1, 0) == 0 and f(1 << 31, 10) == 0 and f(1, 1 << 31) == 0
+    assert f(0, 10) > 0 and f(1, 128256) > 0
+    assert smp(L, d0=0) == 0
+
+
+Z, UU = torch.zeros((3, 50)), torch.zeros(3)
+
+
+@pytest.mark.parametrize("call,exc", [
+    (lambda: vce.ce_sample(Z, UU), RuntimeError),
+    (lambda: vce.ce_sample(Z.half(), UU), TypeError),
+    (lambda: vce.ce_sample(Z[0], UU), ValueError),
+    (lambda: vce.ce_sample(Z.t(), torch.zeros(50)), ValueError),
+    (lambda: vce.ce_sample(Z, UU[:2]), ValueError),
+    (lambda: vce.ce_sample(Z, UU.double()), TypeError),
+    (lambda: vce.ce_sample(Z, UU, top_k=UU), TypeError),
+    (lambda: vce.ce_sample(Z, UU, top_k=torch.zeros(3, dtype=torch.int64)), TypeError),
+    (lambda: vce.ce_sample(Z, UU, top_p=torch.zeros(6)[::2]), ValueError),
+    (lambda: vce.ce_sample(Z, UU, out=UU), ValueError),
+    (lambda: vce.ce_sample(Z, UU, workspace=UU), TypeError),
+])
+def test_ce_sample_binding_rejects(call, exc):
+    with pytest.raises(exc):
+        call()

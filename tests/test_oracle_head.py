@@ -59,3 +59,35 @@ def test_quantize_special_blocks():
     x[0, 40], x[0, 70] = np.nan, np.inf
     q, s = head.quantize(x, "e2m1")
     assert s.tolist() == [[0, 255, 255]] and not q.any()
+
+
+def test_sample_by_hand():
+    z = np.log(np.array([0.1, 0.4, 0.2, 0.3]))
+    pick = lambda u, **kw: head.sample(z, u, **kw)[0]
+    assert [pick(u) for u in (0.0, 0.09, 0.11, 0.49, 0.51, 0.69, 0.71, 0.999)] == \
+        [0, 0, 1, 1, 2, 2, 3, 3]
+    assert [pick(u, k=2) for u in (0.0, 0.56, 0.58)] == [1, 1, 3]       # 4/7 of {1, 3}
+    assert [pick(u, p=0.65) for u in (0.56, 0.58)] == [1, 3]            # 0.4 + 0.3 >= 0.65
+    assert [pick(u, min_p=0.6) for u in (0.56, 0.58)] == [1, 3]         # 0.3 >= 0.6 * 0.4
+    assert pick(0.999, p=0.0) == 1 and pick(0.999, min_p=1.0) == 1 and pick(0.9, T=0.0) == 1
+    assert head.sample(z, 0.0, k=2)[1] == pytest.approx(np.log(4 / 7))
+    # top-p counts the mass that top-k left: 0.4 / 0.7 reaches 0.5 alone
+    assert pick(0.999, k=2, p=0.5) == 1
+
+
+def test_sample_ties_masks_and_refusals():
+    z = np.array([1.0, 2.0, 2.0, 2.0, -np.inf])
+    assert {head.sample(z, u, k=2)[0] for u in (0.0, 0.49, 0.51, 0.99)} == {1, 2}
+    assert {head.sample(z[1:4], u, p=0.5)[0] for u in (0.0, 0.99)} == {0, 1}
+    assert head.sample(np.full(4, -np.inf), 0.5)[0] == -1
+    assert head.sample(np.array([0.0, np.nan]), 0.5)[0] == -1
+    assert head.sample(z, 1.0)[0] == -1 and head.sample(z, 0.5, T=-1.0)[0] == -1
+    assert head.sample(np.array([np.inf, 0.0, np.inf]), 0.6)[0] == 2
+
+
+def test_sample_frequencies():
+    rng = np.random.default_rng(8)
+    z = rng.normal(size=50)
+    u = (np.arange(20000) + 0.5) / 20000
+    got = np.bincount([head.sample(z, x)[0] for x in u], minlength=50) / u.size
+    assert np.max(np.abs(got - np.exp(z) / np.exp(z).sum())) <= 1 / u.size + 1e-12

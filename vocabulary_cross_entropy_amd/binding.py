@@ -74,6 +74,9 @@ SIGNATURES = {
                             _SZ, _VP]),
     "mx_quantize": (_I32, [_VP, _I32, _I64, _I64, _I64, _I32, _VP, _VP, _VP]),
     "mx_dequantize": (_I32, [_VP, _VP, _I32, _I64, _I64, _VP, _I32, _VP]),
+    "ce_sample_workspace_size": (_SZ, [_I64, _I64]),
+    "ce_sample": (_I32, [_VP, _I32, _I64, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP,
+                         _VP, _VP, _SZ, _VP]),
 }
 
 _lib = None
@@ -956,3 +959,58 @@ def mx_dequantize(q: torch.Tensor, scales: torch.Tensor, fmt: str = "e2m1",
                                                     _elem_dtype(o, "out"), s))
         return o
     return _on_stream(q, stream, call)
+
+
+def ce_sample_workspace_size(N: int, V: int) -> int:
+    return int(lib().ce_sample_workspace_size(N, V))
+
+
+def ce_sample_workspace(N: int, V: int, device="cuda") -> torch.Tensor:
+    n = ce_sample_workspace_size(N, V)
+    if n == 0:
+        raise ValueError(f"no workspace plan for N={N}, V={V}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def ce_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+              top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+              min_p: torch.Tensor | None = None, *, with_logprob: bool = False,
+              workspace: torch.Tensor | None = None, stream=None, out=None):
+    """One token per row of logits (N, V) or (d0, d1, V), BF16 or FP32, drawn by the uniform
+    numbers u (N or (d0, d1), FP32 in [0, 1)).  temperature, top_p, min_p (FP32) and top_k
+    (int32), per row like u, or None for off: include/vce.h defines the filters and their order.
+    Returns the tokens (int64, shaped like the rows; -1 where a row has no answer), or with
+    ``with_logprob`` (tokens, logprob), the log of the probability each was drawn with.  ``out``
+    gives the tokens, or both, in that order."""
+    dt = _elem_dtype(logits, "logits")
+    if logits.dim() not in (2, 3):
+        raise ValueError(f"logits must be (N, V) or (d0, d1, V), got {tuple(logits.shape)}")
+    lead = tuple(logits.shape[:-1])
+    V = logits.shape[-1]
+    if V > 1 and logits.stride(-1) != 1:
+        raise ValueError("the vocabulary dimension of logits must be contiguous")
+    d0, d1 = (1, lead[0]) if len(lead) == 1 else lead
+    ls0, ls1 = (0, logits.stride(0)) if len(lead) == 1 else logits.stride()[:2]
+    N = d0 * d1
+    for t, name, td in ((u, "u", torch.float32), (temperature, "temperature", torch.float32),
+                        (top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32),
+                        (min_p, "min_p", torch.float32)):
+        _check_buf(t, name, N, td, like=logits)
+    outs = (None, None) if out is None else (tuple(out) if with_logprob else (out, None))
+    _check_out(outs[0], "token", lead, torch.int64, logits)
+    _check_out(outs[1], "logprob", lead, torch.float32, logits)
+    if workspace is not None:
+        _check_buf(workspace, "workspace", workspace.numel(), torch.uint8, like=logits)
+
+    def call(s):
+        dev = logits.device
+        tok, lp = outs
+        tok = torch.empty(lead, dtype=torch.int64, device=dev) if tok is None else tok
+        if lp is None and with_logprob:
+            lp = torch.empty(lead, dtype=torch.float32, device=dev)
+        ws = ce_sample_workspace(N, V, dev) if workspace is None else workspace
+        _check("ce_sample", lib().ce_sample(
+            _at(logits), dt, d0, d1, V, ls0, ls1, _at(temperature), _at(top_k), _at(top_p),
+            _at(min_p), _at(u), _at(tok), _at(lp), _at(ws), ws.numel(), s))
+        return (tok, lp) if with_logprob else tok
+    return _on_stream(logits, stream, call)

@@ -1059,4 +1059,57 @@ int mx_dequantize(const uint8_t* q, const uint8_t* scales, int format, int64_t r
                                                  static_cast<hipStream_t>(stream)));
 }
 
+size_t ce_sample_workspace_size(int64_t N, int64_t V) {
+  if (N < 0 || N > (int64_t)INT32_MAX || V <= 0 || V > (int64_t)INT32_MAX) return 0;
+  return vce::sample_workspace_bytes(N, V);
+}
+
+int ce_sample(const void* logits, int dtype, int64_t d0, int64_t d1, int64_t V, int64_t ls0,
+              int64_t ls1, const float* temperature, const int32_t* top_k, const float* top_p,
+              const float* min_p, const float* u, int64_t* token, float* logprob,
+              void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype)) return VCE_EDTYPE;
+  if (d0 < 0 || d1 < 0 || V <= 0 || ls0 < 0 || ls1 < 0) return VCE_EINVAL;
+  int64_t N, span0, span1;
+  if (!mul_ok(d0, d1, &N) || N > (int64_t)INT32_MAX) return VCE_EINVAL;
+  if (V > (int64_t)INT32_MAX) return VCE_EUNSUPPORTED;
+  if (N == 0) return VCE_OK;
+  if (!logits || !u || !token || !workspace) return VCE_EINVAL;
+  const int64_t es = dtype_size(dtype);
+  if (!mul_ok(d0 - 1, ls0, &span0) || !mul_ok(d1 - 1, ls1, &span1)) return VCE_EINVAL;
+  if (span0 > INT64_MAX / 8 || span1 > INT64_MAX / 8 - V - span0) return VCE_EINVAL;
+  if (!aligned(logits, es) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+      !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(u, 4) || !aligned(token, 8) ||
+      !aligned(logprob, 4) || !aligned(workspace, 256))
+    return VCE_EALIGN;
+  const size_t need = ce_sample_workspace_size(N, V);
+  if (workspace_bytes < need) return VCE_EWORKSPACE;
+  const Range in[6] = {range(logits, (span0 + span1 + V) * es), range(temperature, N * 4),
+                       range(top_k, N * 4), range(top_p, N * 4), range(min_p, N * 4),
+                       range(u, N * 4)};
+  const Range out[3] = {range(token, N * 8), range(logprob, N * 4),
+                        range(workspace, (int64_t)need)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return VCE_EALIAS;
+    for (int j = 0; j < 6; ++j)
+      if (overlap(out[i], in[j])) return VCE_EALIAS;
+  }
+  vce::SampleParams p;
+  p.logits = logits;
+  p.d1 = d1;
+  p.ls0 = ls0;
+  p.ls1 = ls1;
+  p.V = V;
+  p.temperature = temperature;
+  p.top_k = top_k;
+  p.top_p = top_p;
+  p.min_p = min_p;
+  p.u = u;
+  p.token = token;
+  p.logprob = logprob;
+  return launch_status(
+      vce::launch_sample(p, dtype, N, workspace, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

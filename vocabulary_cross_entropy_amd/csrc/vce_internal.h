@@ -205,4 +205,23 @@ hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, int fmt, hipStr
 hipError_t launch_mx_dequantize(MxDequantParams p, int64_t n, int fmt, int dtype,
                                 hipStream_t stream);
 
+// ---- drawing a token -----------------------------------------------------------
+
+struct SampleParams {
+  const void* logits;
+  int64_t d1, ls0, ls1, V;
+  const float* temperature;  // each optional (N) except u
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* u;
+  int64_t* token;
+  float* logprob;  // optional (N)
+  double magic = 0.0, one = 0.0;  // fixed point of the weights (set by the launcher)
+};
+
+size_t sample_workspace_bytes(int64_t N, int64_t V);
+hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
+                         hipStream_t stream);
+
 }  // namespace vce
