@@ -552,6 +552,28 @@ int mx_dequantize(const uint8_t* q, const uint8_t* scales, int format, int64_t r
                   void* out, int dtype, void* stream);
 
 /*
+ * mx_logits: the head's product in serving, out = logit_scale X W^T, from
+ * microscaled X (M, K) and W (V, K) (mx_quantize; X also from rms_forward_mx8), FP32
+ * accumulation on the scaled matrix instructions, rounded once to `dtype`.
+ *
+ *  x, x_scales, w, w_scales: values and scales in x_format and w_format (any
+ *           pair), contiguous, values 16-byte aligned.  A scale of 255 makes the
+ *           row's (token's) logits NaN.
+ *  M >= 0 tokens, V >= 0 rows of W, both below 2^31; K a multiple of 32 up to
+ *           2^20 (VCE_EUNSUPPORTED otherwise).
+ *  logit_scale finite.
+ *  out      (M, V) of `dtype`, row i at element i * ldo, ldo >= V (columns from
+ *           V to ldo are not written), aligned to its element.  ldo a multiple of 4
+ *           and out aligned to four logits take the wide stores.
+ *           Must not overlap an input (VCE_EALIAS).
+ *  Results are reproducible; between different M a token's logits may differ
+ *  by the order in which its FP32 sum is formed.
+ */
+int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uint8_t* w,
+              const uint8_t* w_scales, int w_format, int64_t M, int64_t K, int64_t V,
+              float logit_scale, void* out, int dtype, int64_t ldo, void* stream);
+
+/*
  * ce_sample: one token from each row of logits, from given uniform numbers.
  * With m the row's maximum and T its temperature, w_i = exp((z_i - m) / T);
  * tokens are ranked by (logit, largest first; lower index first among equals).

@@ -207,3 +207,52 @@ Z, UU = torch.zeros((3, 50)), torch.zeros(3)
 def test_ce_sample_binding_rejects(call, exc):
     with pytest.raises(exc):
         call()
+
+
+def gemm(L, **kw):
+    a = dict(x=A, xs=A + G, xf=0, w=A + 2 * G, ws=A + 3 * G, wf=1, M=4, K=64, V=100, s=1.0,
+             o=A + 4 * G, dtype=1, ldo=100)
+    a.update(kw)
+    return L.mx_logits(a["x"], a["xs"], a["xf"], a["w"], a["ws"], a["wf"], a["M"], a["K"],
+                       a["V"], a["s"], a["o"], a["dtype"], a["ldo"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=2), 2), (dict(xf=2), 2), (dict(wf=-1), 2), (dict(M=-1), 1), (dict(V=-1), 1),
+    (dict(K=0), 1), (dict(K=40), 7), (dict(K=(1 << 20) + 32), 7), (dict(M=1 << 31), 7),
+    (dict(V=1 << 31, ldo=1 << 31), 7), (dict(s=NAN), 1), (dict(s=INF), 1), (dict(x=None), 1),
+    (dict(xs=None), 1), (dict(w=None), 1), (dict(ws=None), 1), (dict(o=None), 1),
+    (dict(ldo=99), 1), (dict(ldo=1 << 62), 1), (dict(x=A + 8), 3), (dict(w=A + 2 * G + 4), 3),
+    (dict(o=A + 4 * G + 1), 3), (dict(o=A), 4), (dict(o=A + G), 4), (dict(o=A + 2 * G), 4),
+    (dict(o=A + 3 * G), 4),
+])
+def test_mx_logits_rejects(L, kw, code):
+    assert gemm(L, **kw) == code
+
+
+def test_mx_logits_empty(L):
+    assert gemm(L, M=0) == 0 and gemm(L, V=0, ldo=0) == 0
+
+
+def u8(r, c):
+    return torch.zeros((r, c), dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("call,exc", [
+    (lambda: vce.mx_logits(u8(3, 64), u8(3, 2), u8(9, 32), u8(9, 2)), RuntimeError),
+    (lambda: vce.mx_logits(u8(3, 64), u8(3, 2), u8(9, 64), u8(9, 2)), ValueError),
+    (lambda: vce.mx_logits(u8(3, 32), u8(3, 1), u8(9, 32), u8(9, 2)), ValueError),
+    (lambda: vce.mx_logits(u8(3, 64), u8(2, 2), u8(9, 32), u8(9, 2)), ValueError),
+    (lambda: vce.mx_logits(X, u8(3, 2), u8(9, 32), u8(9, 2)), TypeError),
+    (lambda: vce.mx_logits(u8(3, 64), u8(3, 2), u8(9, 32), u8(9, 2), dtype=torch.float16),
+     TypeError),
+    (lambda: vce.mx_logits(u8(3, 64), u8(3, 2), u8(9, 32), u8(9, 2), out=torch.zeros((3, 8))),
+     ValueError),
+    (lambda: vce.mx_logits(u8(3, 64), u8(3, 2), u8(9, 32), u8(9, 2),
+                           out=torch.zeros((9, 3)).t()), ValueError),
+    (lambda: vce.mx_logits(u8(3, 64), u8(3, 2), u8(9, 32), u8(9, 2), x_fmt="fp8"), ValueError),
+    (lambda: vce.mx_logits(u8(3, 128)[:, ::2], u8(3, 2), u8(9, 32), u8(9, 2)), ValueError),
+])
+def test_mx_logits_binding_rejects(call, exc):
+    with pytest.raises(exc):
+        call()

@@ -10,6 +10,6 @@ from .binding import (ce_backward, ce_backward_shard, ce_forward,  # noqa: F401
                       lce_backward_shard, lce_forward, lce_forward_f32, lce_forward_noalloc,
                       lce_forward_shard,
                       lce_workspace, lce_workspace_size, lce_workspace_size_f32, lib,
-                      mx_dequantize, mx_quantize, rms_backward, rms_backward_workspace,
+                      mx_dequantize, mx_logits, mx_quantize, rms_backward, rms_backward_workspace,
                       rms_backward_workspace_size, rms_forward, rms_forward_mx8,
                       shift_targets, strerror, VceError)

@@ -74,6 +74,8 @@ SIGNATURES = {
                             _SZ, _VP]),
     "mx_quantize": (_I32, [_VP, _I32, _I64, _I64, _I64, _I32, _VP, _VP, _VP]),
     "mx_dequantize": (_I32, [_VP, _VP, _I32, _I64, _I64, _VP, _I32, _VP]),
+    "mx_logits": (_I32, [_VP, _VP, _I32, _VP, _VP, _I32, _I64, _I64, _I64, _F32, _VP, _I32, _I64,
+                         _VP]),
     "ce_sample_workspace_size": (_SZ, [_I64, _I64]),
     "ce_sample": (_I32, [_VP, _I32, _I64, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP,
                          _VP, _VP, _SZ, _VP]),
@@ -959,6 +961,36 @@ def mx_dequantize(q: torch.Tensor, scales: torch.Tensor, fmt: str = "e2m1",
                                                     _elem_dtype(o, "out"), s))
         return o
     return _on_stream(q, stream, call)
+
+
+def mx_logits(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+              *, x_fmt: str = "e4m3", w_fmt: str = "e2m1", logit_scale: float = 1.0,
+              dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """logit_scale * X W^T (M, V) from microscaled X (M, K) and W (V, K), as BF16 or FP32.
+    ``out`` may have padded rows (a row stride above V)."""
+    M, K, xf = _check_mx(x, x_scales, x_fmt, "x")
+    V, Kw, wf = _check_mx(w, w_scales, w_fmt, "w")
+    if K != Kw:
+        raise ValueError(f"x has rows of {K} values, w of {Kw}")
+    if w.device != x.device:
+        raise ValueError(f"w must be on {x.device}, got {w.device}")
+    if out is not None:
+        dtype = out.dtype
+        if tuple(out.shape) != (M, V) or (V > 1 and out.stride(1) != 1):
+            raise ValueError(f"out must be ({M}, {V}) with contiguous rows")
+        if out.device != x.device:
+            raise ValueError(f"out must be on {x.device}, got {out.device}")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+
+    def call(s):
+        o = torch.empty((M, V), dtype=dtype, device=x.device) if out is None else out
+        _check("mx_logits", lib().mx_logits(
+            _at(x), _at(x_scales), xf, _at(w), _at(w_scales), wf, M, K, V, logit_scale, _at(o),
+            _elem_dtype(o, "out"), o.stride(0), s))
+        return o
+    return _on_stream(x, stream, call)
 
 
 def ce_sample_workspace_size(N: int, V: int) -> int:

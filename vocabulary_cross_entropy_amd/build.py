@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libvce.so")
 SOURCES = ["vce_api.hip", "ce_kernels.hip", "lce_kernels.hip", "rms_kernels.hip",
-           "mx_kernels.hip", "sample_kernels.hip"]
+           "mx_kernels.hip", "mx_gemm_kernels.hip", "sample_kernels.hip"]
 ARCH = "gfx950"
 
 

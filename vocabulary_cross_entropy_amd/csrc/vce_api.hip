@@ -1059,6 +1059,42 @@ int mx_dequantize(const uint8_t* q, const uint8_t* scales, int format, int64_t r
                                                  static_cast<hipStream_t>(stream)));
 }
 
+int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uint8_t* w,
+              const uint8_t* w_scales, int w_format, int64_t M, int64_t K, int64_t V,
+              float logit_scale, void* out, int dtype, int64_t ldo, void* stream) {
+  if (!dtype_ok(dtype)) return VCE_EDTYPE;
+  int64_t xb, xsb, wb, wsb, ob;
+  int rc = check_mx_shape(M, K, x_format, &xb, &xsb);
+  if (rc == VCE_OK) rc = check_mx_shape(V, K, w_format, &wb, &wsb);
+  if (rc != VCE_OK) return rc;
+  if (!__builtin_isfinite(logit_scale)) return VCE_EINVAL;
+  if (M > (int64_t)INT32_MAX || V > (int64_t)INT32_MAX || K > ((int64_t)1 << 20))
+    return VCE_EUNSUPPORTED;
+  if (M == 0 || V == 0) return VCE_OK;
+  if (!x || !x_scales || !w || !w_scales || !out) return VCE_EINVAL;
+  const int64_t es = dtype_size(dtype);
+  if (M == 1) ldo = ldo < V ? V : ldo;  // one row's stride says nothing
+  if (ldo < V || !span_ok(M, V, ldo, es, &ob)) return VCE_EINVAL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, es)) return VCE_EALIGN;
+  const Range o = range(out, ob);
+  if (overlap(o, range(x, xb)) || overlap(o, range(x_scales, xsb)) || overlap(o, range(w, wb)) ||
+      overlap(o, range(w_scales, wsb)))
+    return VCE_EALIAS;
+  vce::MxGemmParams p;
+  p.x = x;
+  p.xs = x_scales;
+  p.w = w;
+  p.ws = w_scales;
+  p.M = M;
+  p.K = K;
+  p.V = V;
+  p.scale = logit_scale;
+  p.out = out;
+  p.ldo = ldo;
+  return launch_status(vce::launch_mx_logits(p, x_format, w_format, dtype,
+                                             static_cast<hipStream_t>(stream)));
+}
+
 size_t ce_sample_workspace_size(int64_t N, int64_t V) {
   if (N < 0 || N > (int64_t)INT32_MAX || V <= 0 || V > (int64_t)INT32_MAX) return 0;
   return vce::sample_workspace_bytes(N, V);

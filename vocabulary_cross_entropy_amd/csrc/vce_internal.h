@@ -205,6 +205,18 @@ hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, int fmt, hipStr
 hipError_t launch_mx_dequantize(MxDequantParams p, int64_t n, int fmt, int dtype,
                                 hipStream_t stream);
 
+struct MxGemmParams {
+  const uint8_t *x, *xs, *w, *ws;  // values and scales of X (M, K) and W (V, K)
+  int64_t M, K, V;
+  float scale;
+  void* out;    // (M, V), row i at element i * ldo
+  int64_t ldo;
+  bool wide = false;  // four logits may be stored at once (set by the launcher)
+};
+
+hipError_t launch_mx_logits(MxGemmParams p, int x_format, int w_format, int dtype,
+                            hipStream_t stream);
+
 // ---- drawing a token -----------------------------------------------------------
 
 struct SampleParams {
