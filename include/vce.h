@@ -559,8 +559,8 @@ int mx_dequantize(const uint8_t* q, const uint8_t* scales, int format, int64_t r
  *  x, x_scales, w, w_scales: values and scales in x_format and w_format (any
  *           pair), contiguous, values 16-byte aligned.  A scale of 255 makes the
  *           row's (token's) logits NaN.
- *  M >= 0 tokens, V >= 0 rows of W, both below 2^31; K a multiple of 32 up to
- *           2^20 (VCE_EUNSUPPORTED otherwise).
+ *  M >= 0 tokens (at most 2^22), V >= 0 rows of W (below 2^31); K a multiple of
+ *           32 up to 2^20 (VCE_EUNSUPPORTED otherwise).
  *  logit_scale finite.
  *  out      (M, V) of `dtype`, row i at element i * ldo, ldo >= V (columns from
  *           V to ldo are not written), aligned to its element.  ldo a multiple of 4
@@ -588,7 +588,8 @@ int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uin
  * ceil(log2 V)) of it above V = 2^18); their sums are exact, so the token does not
  * depend on how the work is split, and is reproducible.
  *
- *  logits   (d0, d1, V) as in ce_forward (V < 2^31).  -inf is a masked token; a
+ *  logits   (d0, d1, V) as in ce_forward, V up to 2^28 and N = d0 * d1 below 2^22
+ *           rows (VCE_EUNSUPPORTED otherwise).  -inf is a masked token; a
  *           finite mask far below the maximum has no weight either.  +inf: the
  *           tokens at +inf share the row.
  *  temperature, top_p, min_p (N) FP32 and top_k (N) int32, or NULL for 1, 1, 0

@@ -169,7 +169,7 @@ def smp(L, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=2), 2), (dict(d0=-1), 1), (dict(V=0), 1), (dict(ls0=-1), 1), (dict(ls1=-1), 1),
-    (dict(d0=1 << 20, d1=1 << 12), 1), (dict(d0=1 << 40, d1=1 << 40), 1), (dict(V=1 << 31), 7),
+    (dict(d0=1 << 20, d1=1 << 12), 1), (dict(d0=1 << 40, d1=1 << 40), 1), (dict(V=1 << 31), 7), (dict(d0=1 << 11, d1=1 << 11), 7),
     (dict(ls0=1 << 62), 1), (dict(z=None), 1), (dict(u=None), 1), (dict(tok=None), 1),
     (dict(ws=None), 1), (dict(z=A + 1), 3), (dict(T=A + G + 2), 3), (dict(k=A + 2 * G + 1), 3),
     (dict(p=A + 3 * G + 1), 3), (dict(mp=A + 4 * G + 1), 3), (dict(u=A + 5 * G + 2), 3),

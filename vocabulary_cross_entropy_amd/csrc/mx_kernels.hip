@@ -18,7 +18,7 @@ constexpr int kThreads = 256;
 // split inside a block of 32, so the lanes of a block are active together.
 template <int DT, int VE, int FMT>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxQuantParams p) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
   const int64_t per_row = p.K / VE;
   // rows are taken from 32-bit arithmetic when the count allows it
   int64_t row, e;
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxQuantParams p) 
 // 32 values per 4 threads: a thread takes 8 values of a block.
 template <int DT, int FMT>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxDequantParams p) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;  // 8 values each
+  const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;  // 8 values each
   if (i >= p.n8) return;
   const uint32_t byte = p.scales[i >> 2];
   const float s = byte == 255u ? __builtin_nanf("") : mx_scale_value(byte);
@@ -112,13 +112,12 @@ template <int DT, int VE>
 hipError_t launch_quant(MxQuantParams p, int fmt, hipStream_t stream) {
   const int64_t n = p.rows * (p.K / VE);
   const int64_t wg = (n + kThreads - 1) / kThreads;
-  if (wg > (int64_t)INT32_MAX) return hipErrorInvalidValue;
   p.small = wg * kThreads < ((int64_t)1 << 31);
   if (fmt == kMxE4M3)
-    hipLaunchKernelGGL((mx_quantize_kernel<DT, VE, kMxE4M3>), dim3((unsigned)wg), dim3(kThreads),
+    hipLaunchKernelGGL((mx_quantize_kernel<DT, VE, kMxE4M3>), grid2(wg), dim3(kThreads),
                        0, stream, p);
   else
-    hipLaunchKernelGGL((mx_quantize_kernel<DT, VE, kMxE2M1>), dim3((unsigned)wg), dim3(kThreads),
+    hipLaunchKernelGGL((mx_quantize_kernel<DT, VE, kMxE2M1>), grid2(wg), dim3(kThreads),
                        0, stream, p);
   return hipGetLastError();
 }
@@ -139,9 +138,8 @@ hipError_t launch_mx_dequantize(MxDequantParams p, int64_t n, int fmt, int dtype
   if (n <= 0) return hipSuccess;
   p.n8 = n / 8;
   const int64_t wg = (p.n8 + kThreads - 1) / kThreads;
-  if (wg > (int64_t)INT32_MAX) return hipErrorInvalidValue;
 #define VCE_DEQ(DT, FMT)                                                                     \
-  hipLaunchKernelGGL((mx_dequantize_kernel<DT, FMT>), dim3((unsigned)wg), dim3(kThreads), 0, \
+  hipLaunchKernelGGL((mx_dequantize_kernel<DT, FMT>), grid2(wg), dim3(kThreads), 0, \
                      stream, p)
   if (dtype == 0) {
     if (fmt == kMxE4M3)

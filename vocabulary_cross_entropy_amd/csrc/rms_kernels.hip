@@ -130,9 +130,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_fwd_kernel(RmsFwdPa
   constexpr int NV = EPL / VE;
   constexpr int kBytes = DT == 0 ? 4 : 2;
   __shared__ float sh[TPR > 64 ? TPR / 64 : 1];
-  const int64_t row = (int64_t)blockIdx.x * kRows +
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRows +
                       __builtin_amdgcn_readfirstlane((int)(threadIdx.x / TPR));
-  if (row >= p.M) return;  // whole wavefronts; with one row per workgroup never
+  if (row >= p.M) return;  // whole wavefronts; a row of several has its workgroup to itself
   const int t = threadIdx.x % TPR;
   const int H = p.H;
   const char* xr = static_cast<const char*>(p.x) + row * p.ldx * kBytes;
@@ -347,7 +347,7 @@ hipError_t launch_fwd(const RmsFwdParams& p, hipStream_t stream) {
     constexpr int threads = T < 256 ? 256 : T;
     constexpr int rows = threads / T;
     hipLaunchKernelGGL((rms_fwd_kernel<DT, VE, T, E, MX>),
-                       dim3((unsigned)((p.M + rows - 1) / rows)), dim3(threads), 0, stream, p);
+                       grid2((p.M + rows - 1) / rows), dim3(threads), 0, stream, p);
     return hipGetLastError();
   });
 }

@@ -14,10 +14,22 @@
 // bits.  FP64 costs no more than unpacked FP32 on this chip.
 //
 // No sort: thresholds come from radix selection over order-preserving keys.
-// A histogram over the distance m - z (128 bins per octave, 16 octaves) finds
-// the bin where the count (top-k) or the mass (top-p) is reached; the
-// candidates down to it, or if they are too many those of that bin alone, are
-// gathered in LDS, and selection by eight key bits at a time finishes there.
+//
+// A row is cut into segments of 8192 tokens, 32 to a thread:
+//  * sample_max_kernel (rows x segments) reads the logits once: the maximum of every
+//    thread's 32 tokens (a group) and of the segment.
+//  * sample_mass_kernel (rows x segments), once the row's maximum is known, sums
+//    the segment's weights for rows without filters, and for rows whose top-p stands
+//    alone (or whose top-k is large) adds the segment to the row's histogram over
+//    the distance m - z (128 bins per octave, 16 octaves).
+//  * sample_row_kernel (rows) draws.  Candidates are bounded from below first: by
+//    the k-th largest group maximum (k groups hold at least k tokens as
+//    large), by the histogram's bin where the mass is reached, or by min-p
+//    itself; only groups that reach the bound are read again, their
+//    candidates are gathered in LDS, and selection by eight key bits at a time
+//    finishes there.  A row without filters re-reads the one segment in
+//    which its sum crosses u.
+//
 #include <math.h>
 
 #include "vce_device.h"
@@ -33,6 +45,10 @@ constexpr int kBins = 2048;
 constexpr uint32_t kBinBase = 119u << 7;  // bits of 2^-8 over 2^16: bin 0 lies below
 constexpr int kCap = 4096;                // candidates held in LDS
 constexpr int kLoads = 4;                 // vectors in flight per thread
+constexpr int kSegThreads = 256;
+constexpr int kGroup = 32;                // tokens per thread of a segment
+constexpr int kSeg = kSegThreads * kGroup;
+constexpr int kSmallK = 1024;             // top-k up to here bounds by group maxima
 
 typedef unsigned long long u64;
 
@@ -140,26 +156,29 @@ struct Weights {
   double one;      // 2^fb, the weight of z = m
 
   // 2^x for x <= 0 by 2^n 2^f, |f| <= 1/2, with 2^f - 1 = f g(f), g the
-  // polynomial of degree 9 through 2^f's at ten Chebyshev nodes (relative
-  // error 6e-16, and exactly 1 at f = 0).  x below -64 rounds to no weight.
+  // polynomial of degree 8 through (2^f - 1) / f at nine Chebyshev nodes (relative
+  // error 4e-14, below the 2^-44 of the rounding, and exactly 1 at f = 0).
+  // x below -64 rounds to no weight.
   __device__ __forceinline__ double real(float z) const {
     double x = ((double)z - (double)m) * c;
     x = __builtin_fmax(x, -64.0);
     const double r = x + 0x1.8p52;
     const double f = x - (r - 0x1.8p52);
-    double g = 0x1.e5e9f548e5725p-28;
-    g = __builtin_fma(g, f, 0x1.b6571de2f2351p-24);
-    g = __builtin_fma(g, f, 0x1.62bfe46117445p-20);
-    g = __builtin_fma(g, f, 0x1.ffcb76789860fp-17);
-    g = __builtin_fma(g, f, 0x1.4309130378460p-13);
-    g = __builtin_fma(g, f, 0x1.5d87fe908f88ap-10);
-    g = __builtin_fma(g, f, 0x1.3b2ab6fba385fp-7);
-    g = __builtin_fma(g, f, 0x1.c6b08d7044119p-5);
-    g = __builtin_fma(g, f, 0x1.ebfbdff82c590p-3);
-    g = __builtin_fma(g, f, 0x1.62e42fefa39f7p-1);
+    double g = 0x1.b63880a30e9ffp-24;
+    g = __builtin_fma(g, f, 0x1.63d136366db24p-20);
+    g = __builtin_fma(g, f, 0x1.ffcb9515a8016p-17);
+    g = __builtin_fma(g, f, 0x1.4308ac85aa947p-13);
+    g = __builtin_fma(g, f, 0x1.5d87fe86fe88ep-10);
+    g = __builtin_fma(g, f, 0x1.3b2ab7181b755p-7);
+    g = __builtin_fma(g, f, 0x1.c6b08d7047e52p-5);
+    g = __builtin_fma(g, f, 0x1.ebfbdff823cedp-3);
+    g = __builtin_fma(g, f, 0x1.62e42fefa39efp-1);
     const double p = __builtin_fma(g, f, 1.0);
-    const u64 n = (u64)__builtin_bit_cast(u64, r) << 52;  // n mod 2^12, in the exponent's place
-    return __builtin_bit_cast(double, __builtin_bit_cast(u64, p) + n);
+    // n sits in r's low word; it is added to p's exponent
+    const u64 b = __builtin_bit_cast(u64, p);
+    const uint32_t n = (uint32_t)__builtin_bit_cast(u64, r);
+    const uint32_t hi = (uint32_t)(b >> 32) + (n << 20);
+    return __builtin_bit_cast(double, ((u64)hi << 32) | (uint32_t)b);
   }
   __device__ __forceinline__ u64 fixed(double w) const {
     return __builtin_bit_cast(u64, w + magic) - magic_bits;
@@ -266,11 +285,11 @@ __device__ Sel radix_select(int bits, double target, bool strict, Shared& sh, Vi
         }
         if (pick < 0) {  // not reached: the last bin that holds anything
           pick = last;
-          a -= h[last];
+          a -= last == 0 ? h[0] : last == 1 ? h[1] : last == 2 ? h[2] : h[3];
         }
         sh.out[0] = (u64)(255 - 4 * lane - pick);
         sh.out[1] = a;
-        sh.out[2] = h[pick];
+        sh.out[2] = pick == 0 ? h[0] : pick == 1 ? h[1] : pick == 2 ? h[2] : h[3];
       }
     }
     __syncthreads();
@@ -281,17 +300,16 @@ __device__ Sel radix_select(int bits, double target, bool strict, Shared& sh, Vi
   return Sel{prefix, above, at};
 }
 
-// The first index, in order, at which the running sum of amount(index, z)
-// exceeds target(whole sum); V if it never does.  Each wavefront sums a
+// The first index, in order, of vectors [c0, c1) at which the running sum of
+// amount(index, z), from `before` on, exceeds target(sum of the range); V if it
+// never does.  Each wavefront sums a
 // sixteenth of the range, the sixteenth that holds the crossing is split
 // again, down to one vector per lane.
 template <int DT, class Target, class Amount>
-__device__ int64_t locate(const Row<DT>& row, Shared& sh, Target target, u64* total,
-                          Amount amount) {
+__device__ int64_t locate(const Row<DT>& row, int c0, int c1, Shared& sh, u64 before,
+                          Target target, u64* total, Amount amount) {
   constexpr int VE = Row<DT>::VE;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int c0 = 0, c1 = row.nvec;
-  u64 before = 0;
   double goal = 0.0;
   bool first = true;
   while (true) {
@@ -506,74 +524,348 @@ __device__ void gather(const Row<DT>& row, const Weights& wt, Shared& sh, uint32
   __syncthreads();
 }
 
-template <int DT>
-__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleParams p) {
-  __shared__ Shared sh;
-  typedef Row<DT> R;
-  const int64_t r = blockIdx.x;
-  const int64_t i0 = r / p.d1, i1 = r - i0 * p.d1;
-  R row;
-  row.init(static_cast<const char*>(p.logits) + (i0 * p.ls0 + i1 * p.ls1) * (DT == 0 ? 4 : 2),
-           p.V);
-  const float T = p.temperature ? p.temperature[r] : 1.0f;
+// What a row asks for, from its parameters alone.
+struct Ask {
+  float T, u;
+  double p, minp;
+  int32_t k;
+  bool ok, greedy, has_k, has_p, has_min;
+  // by the histogram: top-p alone, or a top-k too large for the group maxima
+  __device__ __forceinline__ bool hist(int64_t V) const {
+    return ok && !greedy && !list_all(V) && (has_k ? !group_bound(V) : has_p);
+  }
+  __device__ __forceinline__ bool plain(int64_t V) const {
+    return ok && !greedy && !list_all(V) && !has_k && !has_p && !has_min;
+  }
+  // so short a row that all of it is gathered
+  __device__ __forceinline__ bool list_all(int64_t V) const { return V <= kCap; }
+  // few enough tokens asked for that the group maxima bound them closely
+  __device__ __forceinline__ bool group_bound(int64_t V) const {
+    return has_k && k <= kSmallK && k <= V / (4 * kGroup);
+  }
+};
+
+__device__ __forceinline__ Ask ask_of(const SampleParams& p, int64_t r) {
+  Ask a;
+  a.T = p.temperature ? p.temperature[r] : 1.0f;
   const float top_p = p.top_p ? p.top_p[r] : 1.0f;
   const float min_p = p.min_p ? p.min_p[r] : 0.0f;
-  const int32_t top_k = p.top_k ? p.top_k[r] : 0;
-  const float u = p.u[r];
+  a.k = p.top_k ? p.top_k[r] : 0;
+  a.u = p.u[r];
   // written so that a NaN fails
-  bool ok = T >= 0.0f && T < __builtin_huge_valf() && u >= 0.0f && u < 1.0f &&
-            top_p == top_p && min_p == min_p;
+  a.ok = a.T >= 0.0f && a.T < __builtin_huge_valf() && a.u >= 0.0f && a.u < 1.0f &&
+         top_p == top_p && min_p == min_p;
+  a.greedy = a.T == 0.0f;
+  a.has_k = a.k > 0 && a.k < p.V;
+  a.has_p = top_p < 1.0f;
+  a.has_min = min_p > 0.0f;
+  a.p = top_p;
+  a.minp = fminf(min_p, 1.0f);  // the maximum is always kept
+  return a;
+}
 
-  // the maximum, and whether any logit is NaN
-  float m = kNegInf;
-  bool nan = false;
-  row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t, const float* z) {
-#pragma unroll
-    for (int j = 0; j < R::VE; ++j) {
-      m = fmaxf(m, z[j]);
-      nan |= z[j] != z[j];
-    }
-  });
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = __float_as_uint(m);
-  const bool any_nan = __syncthreads_or(nan);
-  m = kNegInf;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) m = fmaxf(m, __uint_as_float((uint32_t)sh.wave[i]));
-  __syncthreads();
-  if (any_nan || m == kNegInf) ok = false;
-  if (!ok) {
-    if (threadIdx.x == 0) {
-      p.token[r] = -1;
-      if (p.logprob) p.logprob[r] = __builtin_nanf("");
-    }
-    return;
-  }
-
+__device__ __forceinline__ Weights weights_of(const SampleParams& p, const Ask& a, float m) {
   Weights wt;
   wt.m = m;
-  wt.hard = T == 0.0f || m == __builtin_huge_valf();
-  wt.c = wt.hard ? 1.0 : 1.4426950408889634 / (double)T;
-  wt.minp = fminf(min_p, 1.0f);  // the maximum is always kept
+  wt.hard = a.greedy || m == __builtin_huge_valf();
+  wt.c = wt.hard ? 1.0 : 1.4426950408889634 / (double)a.T;
+  wt.minp = a.minp;
   wt.magic = p.magic;
   wt.magic_bits = __builtin_bit_cast(u64, p.magic);
   wt.one = p.one;
-  const bool greedy = T == 0.0f;
+  return wt;
+}
 
-  bool has_k = !greedy && top_k > 0 && top_k < row.V;
-  const bool has_p = !greedy && top_p < 1.0f;
+template <int DT>
+__device__ __forceinline__ Row<DT> row_of(const SampleParams& p, int64_t r) {
+  const int64_t i0 = r / p.d1, i1 = r - i0 * p.d1;
+  Row<DT> row;
+  row.init(static_cast<const char*>(p.logits) + (i0 * p.ls0 + i1 * p.ls1) * (DT == 0 ? 4 : 2),
+           p.V);
+  return row;
+}
 
-  // kept: key > tau, or key = tau and index <= last (tau 0, last V: everything)
+// The row's maximum from its segments' (NaN if any is).  Every thread of a
+// workgroup of whole wavefronts gets it.
+__device__ __forceinline__ float row_max(const float* seg_max, int n) {
+  float m = kNegInf;
+  bool nan = false;
+  for (int i = threadIdx.x & 63; i < n; i += 64) {
+    const float v = seg_max[i];
+    nan |= v != v;
+    m = fmaxf(m, v);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  return __any(nan) ? __builtin_nanf("") : m;
+}
+
+// blockIdx.x: row, blockIdx.y: segment.
+template <int DT>
+__global__ __launch_bounds__(kSegThreads) void sample_max_kernel(SampleParams p) {
+  typedef Row<DT> R;
+  constexpr int kVec = kGroup / R::VE;  // vectors per thread
+  __shared__ float sh[kSegThreads / 64];
+  const int64_t r = blockIdx.x;
+  const int seg = blockIdx.y, t = threadIdx.x;
+  const R row = row_of<DT>(p, r);
+  const int v0 = seg * (kSegThreads * kVec) + t;
+  float z[kVec][R::VE];
+  const int last = v0 + (kVec - 1) * kSegThreads;
+  if (last < (int)((row.V + row.off) / R::VE) && (v0 > 0 || row.off == 0)) {
+    u32x4_t raw[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      raw[j] = *reinterpret_cast<const u32x4_t*>(row.base + row.first(v0 + j * kSegThreads) *
+                                                                (DT == 0 ? 4 : 2));
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) R::unpack(raw[j], z[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      if (v0 + j * kSegThreads < row.nvec) {
+        row.load(v0 + j * kSegThreads, z[j]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < R::VE; ++q) z[j][q] = kNegInf;
+      }
+    }
+  }
+  float m = kNegInf;
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < kVec; ++j)
+#pragma unroll
+    for (int q = 0; q < R::VE; ++q) {
+      m = fmaxf(m, z[j][q]);
+      nan |= z[j][q] != z[j][q];
+    }
+  p.group_max[(r * p.segs + seg) * kSegThreads + t] = m;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  if (__any(nan)) m = __builtin_nanf("");
+  if ((t & 63) == 0) sh[t >> 6] = m;
+  // the row's histogram starts at zero, a share of it per segment
+  if (ask_of(p, r).hist(p.V)) {
+    for (int64_t b = seg * kSegThreads + t; b < kBins; b += (int64_t)p.segs * kSegThreads) {
+      p.hist_mass[r * kBins + b] = 0;
+      p.hist_count[r * kBins + b] = 0;
+    }
+  }
+  __syncthreads();
+  if (t == 0) {
+    bool any = false;
+    float s = kNegInf;
+#pragma unroll
+    for (int i = 0; i < kSegThreads / 64; ++i) {
+      any |= sh[i] != sh[i];
+      s = fmaxf(s, sh[i]);
+    }
+    p.seg_max[r * p.segs + seg] = any ? __builtin_nanf("") : s;
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kSegThreads) void sample_mass_kernel(SampleParams p) {
+  typedef Row<DT> R;
+  constexpr int kVec = kGroup / R::VE;
+  __shared__ u64 mass[kBins];
+  __shared__ uint32_t count[kBins];
+  const int64_t r = blockIdx.x;
+  const int seg = blockIdx.y, t = threadIdx.x;
+  const Ask a = ask_of(p, r);
+  const bool plain = a.plain(p.V), hist = a.hist(p.V);
+  if (!plain && !hist) return;
+  const float m = row_max(p.seg_max + r * p.segs, p.segs);
+  if (!(m > kNegInf)) return;  // no admissible token, or NaN
+  const Weights wt = weights_of(p, a, m);
+  const R row = row_of<DT>(p, r);
+  const int c0 = seg * (kSegThreads * kVec), c1 = min(c0 + kSegThreads * kVec, row.nvec);
+  if (plain) {
+    u64 s = 0;
+    row.each(c0, c1, t, kSegThreads, [&](int64_t, const float* z) {
+#pragma unroll
+      for (int j = 0; j < R::VE; ++j) s += wt.all(z[j]);
+    });
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) s += (u64)__shfl_xor((unsigned long long)s, off, 64);
+    if ((t & 63) == 0) mass[t >> 6] = s;
+    __syncthreads();
+    if (t == 0) p.seg_sum[r * p.segs + seg] = mass[0] + mass[1] + mass[2] + mass[3];
+    return;
+  }
+  for (int b = t; b < kBins; b += kSegThreads) {
+    mass[b] = 0;
+    count[b] = 0;
+  }
+  __syncthreads();
+  row.each(c0, c1, t, kSegThreads, [&](int64_t, const float* z) {
+#pragma unroll
+    for (int j = 0; j < R::VE; ++j) {
+      if (z[j] == kNegInf || (wt.hard && z[j] != m)) continue;
+      const uint32_t b = bin_of(m, z[j]);
+      atomicAdd(&count[b], 1u);
+      if (!a.has_k) {  // top-k's candidates are counted, top-p's weighed
+        const u64 q = wt.all(z[j]);
+        if (q != 0) atomicAdd(&mass[b], q);
+      }
+    }
+  });
+  __syncthreads();
+  for (int b = t; b < kBins; b += kSegThreads) {
+    if (count[b]) atomicAdd(&p.hist_count[r * kBins + b], count[b]);
+    if (mass[b]) atomicAdd((u64*)&p.hist_mass[r * kBins + b], mass[b]);
+  }
+}
+
+// Gathers into LDS the tokens for which want(z) holds, from the groups whose
+// maximum passes it (want must hold for the maximum if it does for a token),
+// in no order.  Returns their number; above kCap the list is cut off.
+template <int DT, class Want>
+__device__ uint32_t gather_groups(const Row<DT>& row, const SampleParams& p, int64_t r, Shared& sh,
+                                  Want want) {
+  typedef Row<DT> R;
+  constexpr int kVec = kGroup / R::VE;
+  if (threadIdx.x == 0) sh.n = 0;
+  __syncthreads();
+  const int groups = p.segs * kSegThreads;
+  const float* gm = p.group_max + r * groups;
+  for (int i = threadIdx.x; i < groups; i += kThreads) {
+    const float g = gm[i];
+    if (g == kNegInf || !want(g)) continue;
+    const int v0 = (i / kSegThreads) * (kSegThreads * kVec) + i % kSegThreads;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int v = v0 + j * kSegThreads;
+      if (v >= row.nvec) continue;
+      float z[R::VE];
+      row.load(v, z);
+      const int64_t e = row.first(v);
+#pragma unroll
+      for (int q = 0; q < R::VE; ++q) {
+        if (z[q] == kNegInf || !want(z[q])) continue;
+        const uint32_t at = atomicAdd(&sh.n, 1u);
+        if (at < kCap) {
+          sh.key[at] = __float_as_uint(z[q]);
+          sh.idx[at] = (uint32_t)(e + q);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  return sh.n;
+}
+
+template <int DT>
+__device__ __forceinline__ float key_value(uint32_t k) {
+  if constexpr (DT == 0) return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+  return __uint_as_float((k & 0x8000u ? k ^ 0x8000u : ~k) << 16);
+}
+
+// How many tokens of weight `each` it takes beyond `above` to reach the goal,
+// 1 .. n.
+__device__ __forceinline__ u64 ties_needed(u64 above, u64 each, u64 n, double goal) {
+  u64 t = 1;
+  if (each != 0 && goal > (double)above) {
+    t = (u64)((goal - (double)above) / (double)each);
+    t = t < 1 ? 1 : t;
+    while (t > 1 && (double)(above + (t - 1) * each) >= goal) --t;
+    while (t < n && (double)(above + t * each) < goal) ++t;
+  }
+  return t < n ? t : n;
+}
+
+struct Drawn {
+  int64_t token;
+  u64 total;  // weight of all kept tokens
+};
+
+// Draws from a list of candidates that holds every token the filters can
+// keep.  `mass` is the weight that top-p refers to without top-k.
+template <int DT>
+__device__ Drawn draw_list(const Ask& a, const Weights& wt, int64_t V, uint32_t n_list, u64 mass,
+                           Shared& sh) {
+  typedef Row<DT> R;
+  auto over = [&](auto f) {
+    for (uint32_t i = threadIdx.x; i < n_list; i += kThreads) {
+      const float z = __uint_as_float(sh.key[i]);
+      f(z, R::key(z), sh.idx[i]);
+    }
+  };
+  // kept: key > tau, or key = tau and index <= last
+  uint32_t tau = 0;
+  uint32_t last = 0xffffffffu;
+  u64 ties = ~(u64)0;
+  if (a.has_k && (u64)a.k < n_list) {
+    const Sel s = radix_select(R::kKeyBits, (double)a.k, false, sh, [&](auto f) {
+      over([&](float, uint32_t k, uint32_t) { f(k, (u64)1); });
+    });
+    tau = s.key;
+    ties = (u64)a.k - s.above;
+  }
+  if (a.has_p) {
+    if (a.has_k) {
+      u64 v = 0;
+      over([&](float z, uint32_t k, uint32_t) {
+        if (k > tau || ties == ~(u64)0) v += wt.all(z);
+      });
+      mass = block_sum(v, sh) + (ties == ~(u64)0 ? 0 : ties * wt.all(key_value<DT>(tau)));
+    }
+    const double goal = a.p * (double)mass;
+    const uint32_t tau_k = tau;
+    const Sel s = radix_select(R::kKeyBits, goal, false, sh, [&](auto f) {
+      over([&](float z, uint32_t k, uint32_t) {
+        if (k >= tau_k) f(k, wt.all(z));
+      });
+    });
+    u64 n = 0;
+    over([&](float, uint32_t k, uint32_t) { n += k == s.key; });
+    n = block_sum(n, sh);
+    if (s.key == tau_k && ties < n) n = ties;
+    ties = ties_needed(s.above, wt.all(key_value<DT>(s.key)), n, goal);
+    tau = s.key;
+  }
+  const int bits = 64 - __builtin_clzll((u64)V);
+  if (ties != ~(u64)0) {
+    u64 n = 0;
+    over([&](float, uint32_t k, uint32_t) { n += k == tau; });
+    n = block_sum(n, sh);
+    if (ties < n) {
+      const Sel s = radix_select(bits, (double)ties, false, sh, [&](auto f) {
+        over([&](float, uint32_t k, uint32_t i) {
+          if (k == tau) f((uint32_t)(V - 1 - i), (u64)1);
+        });
+      });
+      last = (uint32_t)(V - 1 - s.key);
+    }
+  }
+  auto amount = [&](float z, uint32_t k, uint32_t i) -> u64 {
+    return k > tau || (k == tau && i <= last) ? wt.kept(z) : 0;
+  };
+  u64 v = 0;
+  over([&](float z, uint32_t k, uint32_t i) { v += amount(z, k, i); });
+  Drawn d;
+  d.total = block_sum(v, sh);
+  const Sel s = radix_select(bits, (double)a.u * (double)d.total, true, sh, [&](auto f) {
+    over([&](float z, uint32_t k, uint32_t i) { f((uint32_t)(V - 1 - i), amount(z, k, i)); });
+  });
+  d.token = V - 1 - (int64_t)s.key;
+  return d;
+}
+
+// Draws where the candidates do not fit in LDS: every pass reads the row.
+template <int DT>
+__device__ Drawn draw_row(const Row<DT>& row, const Ask& a, const Weights& wt, Shared& sh) {
+  typedef Row<DT> R;
+  const float m = wt.m;
+  bool has_k = a.has_k;
   uint32_t tau = 0;
   int64_t last = row.V;
-  bool select = false;   // tau is set
-  bool listed = false;   // every kept token is in the list
+  bool select = false;  // tau is set
+  u64 ties = 0;
   uint32_t n_list = 0;
-  uint64_t ties = 0;     // tokens of key tau that are kept, in index order
-
-  // f(z, index) over the list, or over the row's tokens of bins [lo, hi]
-  auto over = [&](bool list, uint32_t lo, uint32_t hi, auto f) {
+  // f(z, index) over the list, or over the row's tokens of bin b
+  auto over = [&](bool list, uint32_t b, auto f) {
     if (list) {
       for (uint32_t i = threadIdx.x; i < n_list; i += kThreads)
         f(__uint_as_float(sh.key[i]), (int64_t)sh.idx[i]);
@@ -582,169 +874,221 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleParams p) {
 #pragma unroll
         for (int j = 0; j < R::VE; ++j) {
           if (z[j] == kNegInf || (wt.hard && z[j] != m)) continue;
-          const uint32_t b = bin_of(m, z[j]);
-          if (b >= lo && b <= hi) f(z[j], e + j);
+          if (bin_of(m, z[j]) == b) f(z[j], e + j);
         }
       });
     }
   };
-
-  u64 mass_k = 0;  // mass of the tokens that top-k keeps
+  u64 mass_k = 0;
   if (has_k) {
     histogram<DT, false>(row, wt, sh);
     const BinSel b = scan_bins(sh, [&](int i) { return (u64)sh.count[i]; },
-                               [&](u64) { return (double)top_k; });
-    if (b.total <= (u64)top_k) {
+                               [&](u64) { return (double)a.k; });
+    if (b.total <= (u64)a.k) {
       has_k = false;  // fewer admissible tokens than k
     } else {
       select = true;
-      listed = b.n_incl <= kCap;
-      const uint32_t lo = listed ? 0 : b.bin, hi = b.bin;
-      const bool list = listed || b.n_at <= kCap;
+      const bool list = b.n_at <= kCap;
       if (list) {
-        gather<DT>(row, wt, sh, lo, hi);
+        gather<DT>(row, wt, sh, b.bin, b.bin);
         n_list = min(sh.n, (uint32_t)kCap);
       }
-      const u64 base = listed ? 0 : b.above;
-      const Sel s = radix_select(R::kKeyBits, (double)((u64)top_k - base), false, sh,
+      const Sel s = radix_select(R::kKeyBits, (double)((u64)a.k - b.above), false, sh,
                                  [&](auto f) {
-        over(list, lo, hi, [&](float z, int64_t) { f(R::key(z), (u64)1); });
+        over(list, b.bin, [&](float z, int64_t) { f(R::key(z), (u64)1); });
       });
       tau = s.key;
-      ties = (u64)top_k - base - s.above;
-      if (has_p) {
-        u64 v = 0, q_tau = 0;
-        if (listed) {
-          over(true, lo, hi, [&](float z, int64_t) {
-            if (R::key(z) > tau) v += wt.all(z);
-          });
-        } else {
-          row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t, const float* z) {
+      ties = (u64)a.k - b.above - s.above;
+      if (a.has_p) {
+        u64 v = 0;
+        row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t, const float* z) {
 #pragma unroll
-            for (int j = 0; j < R::VE; ++j)
-              if (R::key(z[j]) > tau) v += wt.all(z[j]);
-          });
-        }
-        if constexpr (DT == 0)
-          q_tau = wt.all(__uint_as_float(tau & 0x80000000u ? tau ^ 0x80000000u : ~tau));
-        else
-          q_tau = wt.all(__uint_as_float((tau & 0x8000u ? tau ^ 0x8000u : ~tau) << 16));
-        mass_k = block_sum(v, sh) + ties * q_tau;
+          for (int j = 0; j < R::VE; ++j)
+            if (R::key(z[j]) > tau) v += wt.all(z[j]);
+        });
+        mass_k = block_sum(v, sh) + ties * wt.all(key_value<DT>(tau));
       }
     }
   }
-  if (has_p) {
-    uint32_t lo = 0, hi = kBins - 1;
-    u64 base = 0;
-    double goal = 0.0;
-    bool list = select && listed;
+  if (a.has_p) {
+    histogram<DT, true>(row, wt, sh);
+    const BinSel b = scan_bins(sh, [&](int i) { return sh.mass[i]; }, [&](u64 total) {
+      return a.p * (double)(has_k ? mass_k : total);
+    });
+    const double goal = a.p * (double)(has_k ? mass_k : b.total);
+    const bool list = b.n_at <= kCap;
     if (list) {
-      goal = (double)top_p * (double)mass_k;
-    } else {
-      histogram<DT, true>(row, wt, sh);
-      const bool sub = select;
-      const BinSel b = scan_bins(sh, [&](int i) { return sh.mass[i]; }, [&](u64 total) {
-        return (double)top_p * (double)(sub ? mass_k : total);
-      });
-      goal = (double)top_p * (double)(select ? mass_k : b.total);
-      listed = b.n_incl <= kCap;
-      lo = listed ? 0 : b.bin;
-      hi = b.bin;
-      base = listed ? 0 : b.above;
-      list = listed || b.n_at <= kCap;
-      if (list) {
-        gather<DT>(row, wt, sh, lo, hi);
-        n_list = min(sh.n, (uint32_t)kCap);
-      }
+      gather<DT>(row, wt, sh, b.bin, b.bin);
+      n_list = min(sh.n, (uint32_t)kCap);
     }
     const uint32_t tau_k = tau;
-    const Sel s = radix_select(R::kKeyBits, goal - (double)base, false, sh, [&](auto f) {
-      over(list, lo, hi, [&](float z, int64_t) {
+    const Sel s = radix_select(R::kKeyBits, goal - (double)b.above, false, sh, [&](auto f) {
+      over(list, b.bin, [&](float z, int64_t) {
         if (R::key(z) >= tau_k) f(R::key(z), wt.all(z));
       });
     });
-    const u64 above = base + s.above;
-    // tokens of key tau all weigh the same: as many as reach the goal
     u64 n = 0;
-    over(list, lo, hi, [&](float z, int64_t) { n += R::key(z) == s.key; });
+    over(list, b.bin, [&](float z, int64_t) { n += R::key(z) == s.key; });
     n = block_sum(n, sh);
-    if (select && s.key == tau_k) n = n < ties ? n : ties;
-    const u64 q = n ? s.at : 0;
-    u64 each = 0;
-    if constexpr (DT == 0)
-      each = wt.all(__uint_as_float(s.key & 0x80000000u ? s.key ^ 0x80000000u : ~s.key));
-    else
-      each = wt.all(__uint_as_float((s.key & 0x8000u ? s.key ^ 0x8000u : ~s.key) << 16));
-    u64 t = 1;
-    if (q != 0 && each != 0 && goal > (double)above) {
-      t = (u64)((goal - (double)above) / (double)each);
-      t = t < 1 ? 1 : t;
-      while (t > 1 && (double)(above + (t - 1) * each) >= goal) --t;
-      while (t < n && (double)(above + t * each) < goal) ++t;
-    }
-    ties = t < n ? t : n;
+    if (select && s.key == tau_k && ties < n) n = ties;
+    ties = ties_needed(b.above + s.above, wt.all(key_value<DT>(s.key)), n, goal);
     tau = s.key;
     select = true;
   }
   if (select) {
-    // the last tie kept, where not all are
-    if (listed) {
-      u64 n = 0;
-      over(true, 0, 0, [&](float z, int64_t) { n += R::key(z) == tau; });
-      n = block_sum(n, sh);
-      if (ties < n) {
-        const int bits = 64 - __builtin_clzll((u64)row.V);
-        const Sel s = radix_select(bits, (double)ties, false, sh, [&](auto f) {
-          over(true, 0, 0, [&](float z, int64_t i) {
-            if (R::key(z) == tau) f((uint32_t)(row.V - 1 - i), (u64)1);
-          });
-        });
-        last = row.V - 1 - (int64_t)s.key;
-      }
-    } else {
-      u64 n;
-      last = locate<DT>(row, sh, [&](u64) { return (double)ties - 0.5; }, &n,
-                        [&](int64_t, float z) {
-        return (u64)(z != kNegInf && R::key(z) == tau && !(wt.hard && z != m));
-      });
-    }
+    u64 n;
+    last = locate<DT>(row, 0, row.nvec, sh, 0, [&](u64) { return (double)ties - 0.5; }, &n,
+                      [&](int64_t, float z) {
+      return (u64)(z != kNegInf && R::key(z) == tau && !(wt.hard && z != m));
+    });
   }
+  Drawn d;
+  d.token = locate<DT>(row, 0, row.nvec, sh, 0,
+                       [&](u64 all) { return (double)a.u * (double)all; }, &d.total,
+                       [&](int64_t i, float z) -> u64 {
+    if (!select) return wt.kept(z);
+    const uint32_t k = R::key(z);
+    return k > tau || (k == tau && i <= last) ? wt.kept(z) : 0;
+  });
+  return d;
+}
 
-  u64 total = 0;
-  int64_t token;
-  if (select && listed) {
-    auto amount = [&](float z, int64_t i) -> u64 {
-      const uint32_t k = R::key(z);
-      return k > tau || (k == tau && i <= last) ? wt.kept(z) : 0;
-    };
-    u64 v = 0;
-    over(true, 0, 0, [&](float z, int64_t i) { v += amount(z, i); });
-    total = block_sum(v, sh);
-    const int bits = 64 - __builtin_clzll((u64)row.V);
-    const Sel s = radix_select(bits, (double)u * (double)total, true, sh, [&](auto f) {
-      over(true, 0, 0, [&](float z, int64_t i) { f((uint32_t)(row.V - 1 - i), amount(z, i)); });
-    });
-    token = row.V - 1 - (int64_t)s.key;
+template <int DT>
+__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleParams p) {
+  __shared__ Shared sh;
+  typedef Row<DT> R;
+  const int64_t r = blockIdx.x;
+  const Ask a = ask_of(p, r);
+  const float m = row_max(p.seg_max + r * p.segs, p.segs);
+  if (!a.ok || !(m > kNegInf)) {  // NaN too
+    if (threadIdx.x == 0) {
+      p.token[r] = -1;
+      if (p.logprob) p.logprob[r] = __builtin_nanf("");
+    }
+    return;
+  }
+  const R row = row_of<DT>(p, r);
+  const Weights wt = weights_of(p, a, m);
+  constexpr int kSegVec = kSeg / R::VE;
+  Drawn d;
+  if (a.greedy || a.plain(p.V)) {
+    // the segment that holds the token: the first with the maximum, or the one
+    // in which the running sum crosses
+    if (threadIdx.x < 64) {
+      const int lane = threadIdx.x;
+      u64 total = 0;
+      if (!a.greedy) {
+        for (int i = lane; i < p.segs; i += 64) total += p.seg_sum[r * p.segs + i];
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1)
+          total += (u64)__shfl_xor((unsigned long long)total, off, 64);
+      }
+      const double goal = (double)a.u * (double)total;
+      u64 before = 0;
+      int seg = 0;
+      for (int i = 0; i < p.segs; i += 64) {
+        u64 v = 0;
+        if (i + lane < p.segs)
+          v = a.greedy ? (u64)(p.seg_max[r * p.segs + i + lane] == m)
+                       : p.seg_sum[r * p.segs + i + lane];
+        u64 run = v;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const u64 w = shfl_up64(run, o);
+          if (lane >= o) run += w;
+        }
+        const uint64_t hit =
+            __ballot(v != 0 && (a.greedy || (double)(before + run) > goal));
+        if (hit) {
+          const int who = __builtin_ctzll(hit);
+          seg = i + who;
+          before += (u64)__shfl((unsigned long long)(run - v), who, 64);
+          break;
+        }
+        before += (u64)__shfl((unsigned long long)run, 63, 64);
+      }
+      if (lane == 0) {
+        sh.out[0] = (u64)seg;
+        sh.out[1] = before;
+        sh.out[2] = total;
+      }
+    }
+    __syncthreads();
+    const int seg = (int)sh.out[0];
+    const u64 before = a.greedy ? 0 : sh.out[1];
+    d.total = sh.out[2];
+    // a difference of two doubles below 2^63: the crossing is tested on whole sums
+    const double goal = a.greedy ? 0.0 : (double)a.u * (double)d.total;
+    u64 part;
+    d.token = locate<DT>(row, seg * kSegVec, min((seg + 1) * kSegVec, row.nvec), sh, before,
+                         [&](u64) { return goal; }, &part,
+                         [&](int64_t, float z) { return wt.all(z); });
   } else {
-    token = locate<DT>(row, sh, [&](u64 all) { return greedy ? 0.0 : (double)u * (double)all; },
-                       &total, [&](int64_t i, float z) -> u64 {
-      if (!select) return wt.kept(z);
-      const uint32_t k = R::key(z);
-      return k > tau || (k == tau && i <= last) ? wt.kept(z) : 0;
-    });
+    uint32_t n = kCap + 1;
+    u64 mass = 0;
+    if (a.list_all(p.V)) {
+      n = gather_groups<DT>(row, p, r, sh, [&](float z) { return !wt.hard || z == m; });
+      if (a.has_p && !a.has_k) {
+        u64 v = 0;
+        for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+          v += wt.all(__uint_as_float(sh.key[i]));
+        mass = block_sum(v, sh);
+      }
+    } else if (a.hist(p.V)) {
+      for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        sh.count[i] = p.hist_count[r * kBins + i];
+        sh.mass[i] = p.hist_mass[r * kBins + i];
+      }
+      __syncthreads();
+      BinSel b;
+      if (a.has_k) {
+        b = scan_bins(sh, [&](int i) { return (u64)sh.count[i]; },
+                      [&](u64) { return (double)a.k; });
+      } else {
+        b = scan_bins(sh, [&](int i) { return sh.mass[i]; },
+                      [&](u64 total) { return a.p * (double)total; });
+        mass = b.total;
+      }
+      if (b.n_incl <= kCap)
+        n = gather_groups<DT>(row, p, r, sh, [&](float z) {
+          return (!wt.hard || z == m) && (int)bin_of(m, z) <= b.bin;
+        });
+    } else if (a.has_k) {
+      // k groups with maxima of at least the k-th largest hold k tokens as large
+      const int groups = p.segs * kSegThreads;
+      const float* gm = p.group_max + r * groups;
+      const Sel s = radix_select(R::kKeyBits, (double)a.k, false, sh, [&](auto f) {
+        for (int i = threadIdx.x; i < groups; i += kThreads) {
+          const float g = gm[i];
+          if (g != kNegInf && (!wt.hard || g == m)) f(R::key(g), (u64)1);
+        }
+      });
+      // fewer such groups than k: every token is a candidate
+      const uint32_t bound = s.above + s.at >= (u64)a.k ? s.key : 0u;
+      n = gather_groups<DT>(row, p, r, sh, [&](float z) {
+        return (!wt.hard || z == m) && R::key(z) >= bound;
+      });
+    } else {
+      // min-p alone
+      n = gather_groups<DT>(row, p, r, sh, [&](float z) { return wt.kept(z) != 0; });
+    }
+    if (n <= kCap)
+      d = draw_list<DT>(a, wt, p.V, n, mass, sh);
+    else
+      d = draw_row<DT>(row, a, wt, sh);
   }
   if (threadIdx.x == 0) {
-    p.token[r] = token;
+    p.token[r] = d.token;
     if (p.logprob) {
       float lp = 0.0f;
-      if (!greedy) {
+      if (!a.greedy) {
         float z;
         if constexpr (DT == 0)
-          z = reinterpret_cast<const float*>(row.base)[token];
+          z = reinterpret_cast<const float*>(row.base)[d.token];
         else
-          z = from_bf16(reinterpret_cast<const uint16_t*>(row.base)[token]);
-        const double x = wt.hard ? 0.0 : ((double)z - (double)m) / (double)T;
-        lp = (float)(x - log((double)total / p.one));
+          z = from_bf16(reinterpret_cast<const uint16_t*>(row.base)[d.token]);
+        const double x = wt.hard ? 0.0 : ((double)z - (double)m) / (double)a.T;
+        lp = (float)(x - log((double)d.total / p.one));
       }
       p.logprob[r] = lp;
     }
@@ -761,23 +1105,45 @@ static int weight_bits(int64_t V) {
   return fb < 44 ? fb : 44;
 }
 
+static int64_t segments(int64_t V) { return (V + 8 + kSeg - 1) / kSeg; }
+
+static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 size_t sample_workspace_bytes(int64_t N, int64_t V) {
-  (void)N;
-  (void)V;
-  return 256;
+  const size_t rows = (size_t)N, s = rows * (size_t)segments(V);
+  return 256 + up256(s * kSegThreads * 4) + up256(s * 4) + up256(s * 8) + up256(rows * kBins * 8) +
+         up256(rows * kBins * 4);
 }
 
 hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
                          hipStream_t stream) {
-  (void)workspace;
   if (N <= 0) return hipSuccess;
   const int fb = weight_bits(p.V);
   p.magic = ldexp(1.0, 52 - fb);
   p.one = ldexp(1.0, fb);
-  if (dtype == 0)
-    hipLaunchKernelGGL((sample_row_kernel<0>), dim3((unsigned)N), dim3(kThreads), 0, stream, p);
-  else
-    hipLaunchKernelGGL((sample_row_kernel<1>), dim3((unsigned)N), dim3(kThreads), 0, stream, p);
+  p.segs = (int)segments(p.V);
+  const size_t rows = (size_t)N, s = rows * (size_t)p.segs;
+  char* w = static_cast<char*>(workspace);
+  p.group_max = reinterpret_cast<float*>(w);
+  w += up256(s * kSegThreads * 4);
+  p.seg_max = reinterpret_cast<float*>(w);
+  w += up256(s * 4);
+  p.seg_sum = reinterpret_cast<unsigned long long*>(w);
+  w += up256(s * 8);
+  p.hist_mass = reinterpret_cast<unsigned long long*>(w);
+  w += up256(rows * kBins * 8);
+  p.hist_count = reinterpret_cast<uint32_t*>(w);
+  const dim3 seg_grid((unsigned)N, (unsigned)p.segs);
+#define VCE_SAMPLE(DT)                                                                          \
+  hipLaunchKernelGGL((sample_max_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);       \
+  hipLaunchKernelGGL((sample_mass_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);      \
+  hipLaunchKernelGGL((sample_row_kernel<DT>), dim3((unsigned)N), dim3(kThreads), 0, stream, p)
+  if (dtype == 0) {
+    VCE_SAMPLE(0);
+  } else {
+    VCE_SAMPLE(1);
+  }
+#undef VCE_SAMPLE
   return hipGetLastError();
 }
 

@@ -1020,7 +1020,7 @@ int mx_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx, 
   int64_t qb, sb, xb;
   const int rc = check_mx_shape(rows, K, format, &qb, &sb);
   if (rc != VCE_OK || rows == 0) return rc;
-  // one thread per 16 bytes, or per element, in a grid of 2^31 workgroups at most
+  // one thread per 16 bytes, or per element
   if (rows > ((int64_t)1 << 38) / K) return VCE_EUNSUPPORTED;
   if (!x || !q || !scales) return VCE_EINVAL;
   if (ldx < 0 || (rows > 1 && ldx != 0 && ldx < K)) return VCE_EINVAL;
@@ -1068,7 +1068,7 @@ int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uin
   if (rc == VCE_OK) rc = check_mx_shape(V, K, w_format, &wb, &wsb);
   if (rc != VCE_OK) return rc;
   if (!__builtin_isfinite(logit_scale)) return VCE_EINVAL;
-  if (M > (int64_t)INT32_MAX || V > (int64_t)INT32_MAX || K > ((int64_t)1 << 20))
+  if (M > ((int64_t)1 << 22) || V > (int64_t)INT32_MAX || K > ((int64_t)1 << 20))
     return VCE_EUNSUPPORTED;
   if (M == 0 || V == 0) return VCE_OK;
   if (!x || !x_scales || !w || !w_scales || !out) return VCE_EINVAL;
@@ -1095,8 +1095,13 @@ int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uin
                                              static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+constexpr int64_t kSampleRows = ((int64_t)1 << 22) - 1;  // workgroups of 1024 in one grid axis
+constexpr int64_t kSampleVocab = (int64_t)1 << 28;       // segments in the other
+}  // namespace
+
 size_t ce_sample_workspace_size(int64_t N, int64_t V) {
-  if (N < 0 || N > (int64_t)INT32_MAX || V <= 0 || V > (int64_t)INT32_MAX) return 0;
+  if (N < 0 || N > kSampleRows || V <= 0 || V > kSampleVocab) return 0;
   return vce::sample_workspace_bytes(N, V);
 }
 
@@ -1108,7 +1113,7 @@ int ce_sample(const void* logits, int dtype, int64_t d0, int64_t d1, int64_t V, 
   if (d0 < 0 || d1 < 0 || V <= 0 || ls0 < 0 || ls1 < 0) return VCE_EINVAL;
   int64_t N, span0, span1;
   if (!mul_ok(d0, d1, &N) || N > (int64_t)INT32_MAX) return VCE_EINVAL;
-  if (V > (int64_t)INT32_MAX) return VCE_EUNSUPPORTED;
+  if (V > kSampleVocab || N > kSampleRows) return VCE_EUNSUPPORTED;
   if (N == 0) return VCE_OK;
   if (!logits || !u || !token || !workspace) return VCE_EINVAL;
   const int64_t es = dtype_size(dtype);

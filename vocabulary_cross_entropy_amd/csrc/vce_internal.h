@@ -147,6 +147,14 @@ hipError_t launch_gemm_bf16(const void* P, int64_t ldp, int p_dim, const void* Q
                             int q_dim, int64_t rows, int64_t cols, int64_t K, float* C,
                             int64_t ldc, hipStream_t stream);
 
+// A grid of n workgroups in two dimensions: one dimension holds fewer than 2^32
+// threads.  Workgroup blockIdx.y * gridDim.x + blockIdx.x; those at or past n
+// have nothing to do.
+inline dim3 grid2(int64_t n) {
+  const int64_t x = n < ((int64_t)1 << 21) ? n : ((int64_t)1 << 21);
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
 // ---- residual + RMS norm -------------------------------------------------------
 
 struct RmsFwdParams {
@@ -229,7 +237,14 @@ struct SampleParams {
   const float* u;
   int64_t* token;
   float* logprob;  // optional (N)
-  double magic = 0.0, one = 0.0;  // fixed point of the weights (set by the launcher)
+  // set by the launcher: the weights' fixed point, and the workspace's parts
+  double magic = 0.0, one = 0.0;
+  int segs = 0;                             // segments per row
+  float* group_max = nullptr;               // (N, segs, 256)
+  float* seg_max = nullptr;                 // (N, segs)
+  unsigned long long* seg_sum = nullptr;    // (N, segs)
+  unsigned long long* hist_mass = nullptr;  // (N, 2048)
+  uint32_t* hist_count = nullptr;           // (N, 2048)
 };
 
 size_t sample_workspace_bytes(int64_t N, int64_t V);
