@@ -19,18 +19,26 @@
 //  * sample_max_kernel (rows x segments) reads the logits once: the maximum of every
 //    thread's 32 tokens (a group) and of the segment.
 //  * sample_mass_kernel (rows x segments), once the row's maximum is known, sums
-//    the segment's weights for rows without filters, and for rows whose top-p stands
-//    alone (or whose top-k is large) adds the segment to the row's histogram over
-//    the distance m - z (128 bins per octave, 16 octaves).
-//  * sample_row_kernel (rows) draws.  Candidates are bounded from below first: by
+//    the segment's weights for rows without top-k and min-p, and for rows whose
+//    top-p stands alone (or whose top-k is large) adds the segment to the row's
+//    histogram over the distance m - z (128 bins per octave, 16 octaves).
+//  * sample_pick_kernel (rows) draws.  Candidates are bounded from below first: by
 //    the k-th largest group maximum (k groups hold at least k tokens as
 //    large), by the histogram's bin where the mass is reached, or by min-p
-//    itself; only groups that reach the bound are read again, their
-//    candidates are gathered in LDS, and selection by eight key bits at a time
-//    finishes there.  A row without filters re-reads the one segment in
-//    which its sum crosses u.
+//    itself; only groups that reach the bound are read again and their
+//    candidates gathered in LDS.  Up to 256 are ranked by counting, more go
+//    through selection by eight key bits at a time.  A row without filters
+//    re-reads the one segment in which its sum crosses u.
+//  * rows with more candidates than LDS holds: sample_kept_kernel (rows x
+//    segments) sums what their threshold keeps, sample_rest_kernel (rows) draws;
+//    those whose threshold itself needs more passes it serves from the row.
+// The code that a usual row runs is kept short: a kernel this brief waits for
+// its instructions more than for its data (one row of 128256 with all filters took 67 us
+// in a kernel of 60 KB, most of it instruction fetch).
 //
 #include <math.h>
+
+#include <type_traits>
 
 #include "vce_device.h"
 #include "vce_internal.h"
@@ -145,34 +153,31 @@ struct Row {
   }
 };
 
-// Fixed-point weights of one row.
+// Fixed-point weights of one row.  The coefficients come as kernel
+// arguments, so that they sit in scalar registers and each step of the
+// polynomial is one instruction.
 struct Weights {
   float m;
+  bool inf;        // m is infinite: only z = m has weight, all the same
+  double md;       // m as FP64
   double c;        // log2(e) / T
   double minp;
-  bool hard;       // T = 0, or m infinite: only z = m has weight, all the same
   double magic;    // 2^(52 - fb): a double at least that large ends at 2^-fb
   u64 magic_bits;
-  double one;      // 2^fb, the weight of z = m
+  const double* poly;
 
   // 2^x for x <= 0 by 2^n 2^f, |f| <= 1/2, with 2^f - 1 = f g(f), g the
   // polynomial of degree 8 through (2^f - 1) / f at nine Chebyshev nodes (relative
   // error 4e-14, below the 2^-44 of the rounding, and exactly 1 at f = 0).
-  // x below -64 rounds to no weight.
+  // x below -64 rounds to no weight.  For a finite m.
   __device__ __forceinline__ double real(float z) const {
-    double x = ((double)z - (double)m) * c;
+    double x = ((double)z - md) * c;
     x = __builtin_fmax(x, -64.0);
     const double r = x + 0x1.8p52;
     const double f = x - (r - 0x1.8p52);
-    double g = 0x1.b63880a30e9ffp-24;
-    g = __builtin_fma(g, f, 0x1.63d136366db24p-20);
-    g = __builtin_fma(g, f, 0x1.ffcb9515a8016p-17);
-    g = __builtin_fma(g, f, 0x1.4308ac85aa947p-13);
-    g = __builtin_fma(g, f, 0x1.5d87fe86fe88ep-10);
-    g = __builtin_fma(g, f, 0x1.3b2ab7181b755p-7);
-    g = __builtin_fma(g, f, 0x1.c6b08d7047e52p-5);
-    g = __builtin_fma(g, f, 0x1.ebfbdff823cedp-3);
-    g = __builtin_fma(g, f, 0x1.62e42fefa39efp-1);
+    double g = poly[8];
+#pragma unroll
+    for (int i = 7; i >= 0; --i) g = __builtin_fma(g, f, poly[i]);
     const double p = __builtin_fma(g, f, 1.0);
     // n sits in r's low word; it is added to p's exponent
     const u64 b = __builtin_bit_cast(u64, p);
@@ -180,27 +185,23 @@ struct Weights {
     const uint32_t hi = (uint32_t)(b >> 32) + (n << 20);
     return __builtin_bit_cast(double, ((u64)hi << 32) | (uint32_t)b);
   }
+  __device__ __forceinline__ double weight(float z) const {
+    if (inf) return z == m ? 1.0 : 0.0;
+    return real(z);
+  }
   __device__ __forceinline__ u64 fixed(double w) const {
     return __builtin_bit_cast(u64, w + magic) - magic_bits;
   }
   // The weight of z among all tokens (min-p not applied).
-  __device__ __forceinline__ u64 all(float z) const {
-    if (hard) return z == m ? (u64)one : 0;
-    return fixed(real(z));
-  }
+  __device__ __forceinline__ u64 all(float z) const { return fixed(weight(z)); }
   // The same with the tokens below min-p left out.
   __device__ __forceinline__ u64 kept(float z) const {
-    if (hard) return z == m ? (u64)one : 0;
-    const double w = real(z);
+    const double w = weight(z);
     return w >= minp ? fixed(w) : 0;
   }
 };
 
-struct Shared {
-  u64 mass[kBins];
-  uint32_t count[kBins];
-  uint32_t key[kCap];
-  uint32_t idx[kCap];
+struct Scratch {
   u64 hist[256];
   u64 wave[kWaves];
   u64 wave2[kWaves];
@@ -208,12 +209,32 @@ struct Shared {
   uint32_t n;
 };
 
+struct Shared : Scratch {
+  u64 mass[kBins];
+  uint32_t count[kBins];
+  uint32_t key[kCap];  // candidates: the logit's bits, its index
+  uint32_t idx[kCap];
+};
+
+// A candidate: the key of its logit, its index, and its weight, with the top
+// bit set unless min-p drops it.
+struct alignas(16) Entry {
+  uint32_t key, idx;
+  u64 q;
+};
+constexpr u64 kKeptBit = (u64)1 << 63;
+
+struct PickShared : Scratch {
+  Entry list[kCap];
+};
+
 __device__ __forceinline__ u64 shfl_up64(u64 v, int d) {
   return (u64)__shfl_up((unsigned long long)v, d, 64);
 }
 
 // Sum over the workgroup, the same in every thread.
-__device__ __forceinline__ u64 block_sum(u64 v, Shared& sh) {
+template <int NW, class S>
+__device__ __forceinline__ u64 block_sum(u64 v, S& sh) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += (u64)__shfl_xor((unsigned long long)v, off, 64);
   __syncthreads();
@@ -221,7 +242,7 @@ __device__ __forceinline__ u64 block_sum(u64 v, Shared& sh) {
   __syncthreads();
   v = 0;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) v += sh.wave[i];
+  for (int i = 0; i < NW; ++i) v += sh.wave[i];
   return v;
 }
 
@@ -239,8 +260,9 @@ struct Sel {
 
 // visit(f) calls f(key, amount) for this thread's elements, keys below
 // 2^bits.  If the whole sum does not reach the target, the least key is taken.
-template <class Visit>
-__device__ Sel radix_select(int bits, double target, bool strict, Shared& sh, Visit visit) {
+template <class S, class Visit>
+__device__ __forceinline__ Sel radix_select(int bits, double target, bool strict, S& sh,
+                                            Visit visit) {
   uint32_t prefix = 0;
   u64 above = 0, at = 0;
   for (int shift = (bits - 1) / 8 * 8; shift >= 0; shift -= 8) {
@@ -407,7 +429,7 @@ __device__ void histogram(const Row<DT>& row, const Weights& wt, Shared& sh) {
   row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t, const float* z) {
 #pragma unroll
     for (int j = 0; j < Row<DT>::VE; ++j) {
-      if (z[j] == kNegInf || (wt.hard && z[j] != wt.m)) continue;
+      if (z[j] == kNegInf) continue;
       const uint32_t b = bin_of(wt.m, z[j]);
       if constexpr (MASS) {
         const u64 q = wt.all(z[j]);
@@ -511,7 +533,7 @@ __device__ void gather(const Row<DT>& row, const Weights& wt, Shared& sh, uint32
   row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t e, const float* z) {
 #pragma unroll
     for (int j = 0; j < Row<DT>::VE; ++j) {
-      if (z[j] == kNegInf || (wt.hard && z[j] != wt.m)) continue;
+      if (z[j] == kNegInf) continue;
       const uint32_t b = bin_of(wt.m, z[j]);
       if (b < lo || b > hi) continue;
       const uint32_t at = atomicAdd(&sh.n, 1u);
@@ -530,18 +552,18 @@ struct Ask {
   double p, minp;
   int32_t k;
   bool ok, greedy, has_k, has_p, has_min;
+  // so short a row that all of it is gathered
+  __device__ __forceinline__ bool list_all(int64_t V) const { return V <= kCap; }
+  // few enough tokens asked for that the group maxima bound them closely
+  __device__ __forceinline__ bool group_bound(int64_t V) const {
+    return has_k && k <= kSmallK && k <= V / (4 * kGroup);
+  }
   // by the histogram: top-p alone, or a top-k too large for the group maxima
   __device__ __forceinline__ bool hist(int64_t V) const {
     return ok && !greedy && !list_all(V) && (has_k ? !group_bound(V) : has_p);
   }
   __device__ __forceinline__ bool plain(int64_t V) const {
     return ok && !greedy && !list_all(V) && !has_k && !has_p && !has_min;
-  }
-  // so short a row that all of it is gathered
-  __device__ __forceinline__ bool list_all(int64_t V) const { return V <= kCap; }
-  // few enough tokens asked for that the group maxima bound them closely
-  __device__ __forceinline__ bool group_bound(int64_t V) const {
-    return has_k && k <= kSmallK && k <= V / (4 * kGroup);
   }
 };
 
@@ -559,20 +581,21 @@ __device__ __forceinline__ Ask ask_of(const SampleParams& p, int64_t r) {
   a.has_k = a.k > 0 && a.k < p.V;
   a.has_p = top_p < 1.0f;
   a.has_min = min_p > 0.0f;
-  a.p = top_p;
-  a.minp = fminf(min_p, 1.0f);  // the maximum is always kept
+  a.p = fmaxf(top_p, 0.0f);      // the first token is always kept
+  a.minp = fminf(min_p, 1.0f);   // and so are the maxima
   return a;
 }
 
 __device__ __forceinline__ Weights weights_of(const SampleParams& p, const Ask& a, float m) {
   Weights wt;
   wt.m = m;
-  wt.hard = a.greedy || m == __builtin_huge_valf();
-  wt.c = wt.hard ? 1.0 : 1.4426950408889634 / (double)a.T;
+  wt.inf = m == __builtin_huge_valf();
+  wt.md = (double)m;
+  wt.c = 1.4426950408889634 / (double)a.T;
   wt.minp = a.minp;
   wt.magic = p.magic;
   wt.magic_bits = __builtin_bit_cast(u64, p.magic);
-  wt.one = p.one;
+  wt.poly = p.poly;
   return wt;
 }
 
@@ -585,8 +608,7 @@ __device__ __forceinline__ Row<DT> row_of(const SampleParams& p, int64_t r) {
   return row;
 }
 
-// The row's maximum from its segments' (NaN if any is).  Every thread of a
-// workgroup of whole wavefronts gets it.
+// The row's maximum from its segments' (NaN if any is); whole wavefronts call it.
 __device__ __forceinline__ float row_max(const float* seg_max, int n) {
   float m = kNegInf;
   bool nan = false;
@@ -600,17 +622,30 @@ __device__ __forceinline__ float row_max(const float* seg_max, int n) {
   return __any(nan) ? __builtin_nanf("") : m;
 }
 
-// blockIdx.x: row, blockIdx.y: segment.
+__device__ __forceinline__ u64 wave_sum(u64 v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += (u64)__shfl_xor((unsigned long long)v, off, 64);
+  return v;
+}
+
+// Running sum over the lanes, each with its own share included.
+__device__ __forceinline__ u64 wave_scan(u64 v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const u64 o = shfl_up64(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// The 32 tokens of a thread of a segment: vectors v0, v0 + 256, ... of the row,
+// -inf past its ends.
 template <int DT>
-__global__ __launch_bounds__(kSegThreads) void sample_max_kernel(SampleParams p) {
+__device__ __forceinline__ void load_group(const Row<DT>& row, int v0,
+                                           float (&z)[kGroup / Row<DT>::VE][Row<DT>::VE]) {
   typedef Row<DT> R;
-  constexpr int kVec = kGroup / R::VE;  // vectors per thread
-  __shared__ float sh[kSegThreads / 64];
-  const int64_t r = blockIdx.x;
-  const int seg = blockIdx.y, t = threadIdx.x;
-  const R row = row_of<DT>(p, r);
-  const int v0 = seg * (kSegThreads * kVec) + t;
-  float z[kVec][R::VE];
+  constexpr int kVec = kGroup / R::VE;
   const int last = v0 + (kVec - 1) * kSegThreads;
   if (last < (int)((row.V + row.off) / R::VE) && (v0 > 0 || row.off == 0)) {
     u32x4_t raw[kVec];
@@ -631,6 +666,19 @@ __global__ __launch_bounds__(kSegThreads) void sample_max_kernel(SampleParams p)
       }
     }
   }
+}
+
+// blockIdx.x: row, blockIdx.y: segment.
+template <int DT>
+__global__ __launch_bounds__(kSegThreads) void sample_max_kernel(SampleParams p) {
+  typedef Row<DT> R;
+  constexpr int kVec = kGroup / R::VE;
+  __shared__ float sh[kSegThreads / 64];
+  const int64_t r = blockIdx.x;
+  const int seg = blockIdx.y, t = threadIdx.x;
+  const R row = row_of<DT>(p, r);
+  float z[kVec][R::VE];
+  load_group<DT>(row, seg * (kSegThreads * kVec) + t, z);
   float m = kNegInf;
   bool nan = false;
 #pragma unroll
@@ -665,95 +713,79 @@ __global__ __launch_bounds__(kSegThreads) void sample_max_kernel(SampleParams p)
   }
 }
 
+// For rows without filters the segment's mass; for rows that go by the
+// histogram its counts (top-k) or its masses and the whole (top-p).
+// Top-p needs no token lighter than q0 = (1 - p) L / V, L a lower bound on
+// the row's mass (the sum over the segments' maxima): all such tokens together
+// weigh less than (1 - p) of the row, so its p-th part is reached before them.
+// They stay out of the histogram, which keeps most LDS atomics away.
 template <int DT>
-__global__ __launch_bounds__(kSegThreads) void sample_mass_kernel(SampleParams p) {
+__global__ __launch_bounds__(kSegThreads, 4) void sample_mass_kernel(SampleParams p) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
   __shared__ u64 mass[kBins];
   __shared__ uint32_t count[kBins];
+  __shared__ u64 part[kSegThreads / 64];
   const int64_t r = blockIdx.x;
   const int seg = blockIdx.y, t = threadIdx.x;
   const Ask a = ask_of(p, r);
   const bool plain = a.plain(p.V), hist = a.hist(p.V);
   if (!plain && !hist) return;
-  const float m = row_max(p.seg_max + r * p.segs, p.segs);
+  const float* seg_max = p.seg_max + r * p.segs;
+  const float m = row_max(seg_max, p.segs);
   if (!(m > kNegInf)) return;  // no admissible token, or NaN
   const Weights wt = weights_of(p, a, m);
   const R row = row_of<DT>(p, r);
-  const int c0 = seg * (kSegThreads * kVec), c1 = min(c0 + kSegThreads * kVec, row.nvec);
+  const int v0 = seg * (kSegThreads * kVec) + t;
+  u64 s = 0;
   if (plain) {
-    u64 s = 0;
-    row.each(c0, c1, t, kSegThreads, [&](int64_t, const float* z) {
+    float z[kVec][R::VE];
+    load_group<DT>(row, v0, z);
+    if (wt.inf) {
 #pragma unroll
-      for (int j = 0; j < R::VE; ++j) s += wt.all(z[j]);
-    });
+      for (int j = 0; j < kGroup; ++j) s += wt.fixed(z[j / R::VE][j % R::VE] == m ? 1.0 : 0.0);
+    } else {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) s += (u64)__shfl_xor((unsigned long long)s, off, 64);
-    if ((t & 63) == 0) mass[t >> 6] = s;
-    __syncthreads();
-    if (t == 0) p.seg_sum[r * p.segs + seg] = mass[0] + mass[1] + mass[2] + mass[3];
-    return;
-  }
-  for (int b = t; b < kBins; b += kSegThreads) {
-    mass[b] = 0;
-    count[b] = 0;
-  }
-  __syncthreads();
-  row.each(c0, c1, t, kSegThreads, [&](int64_t, const float* z) {
-#pragma unroll
-    for (int j = 0; j < R::VE; ++j) {
-      if (z[j] == kNegInf || (wt.hard && z[j] != m)) continue;
-      const uint32_t b = bin_of(m, z[j]);
-      atomicAdd(&count[b], 1u);
-      if (!a.has_k) {  // top-k's candidates are counted, top-p's weighed
-        const u64 q = wt.all(z[j]);
-        if (q != 0) atomicAdd(&mass[b], q);
-      }
+      for (int j = 0; j < kGroup; ++j) s += wt.fixed(wt.real(z[j / R::VE][j % R::VE]));
     }
-  });
-  __syncthreads();
-  for (int b = t; b < kBins; b += kSegThreads) {
-    if (count[b]) atomicAdd(&p.hist_count[r * kBins + b], count[b]);
-    if (mass[b]) atomicAdd((u64*)&p.hist_mass[r * kBins + b], mass[b]);
-  }
-}
-
-// Gathers into LDS the tokens for which want(z) holds, from the groups whose
-// maximum passes it (want must hold for the maximum if it does for a token),
-// in no order.  Returns their number; above kCap the list is cut off.
-template <int DT, class Want>
-__device__ uint32_t gather_groups(const Row<DT>& row, const SampleParams& p, int64_t r, Shared& sh,
-                                  Want want) {
-  typedef Row<DT> R;
-  constexpr int kVec = kGroup / R::VE;
-  if (threadIdx.x == 0) sh.n = 0;
-  __syncthreads();
-  const int groups = p.segs * kSegThreads;
-  const float* gm = p.group_max + r * groups;
-  for (int i = threadIdx.x; i < groups; i += kThreads) {
-    const float g = gm[i];
-    if (g == kNegInf || !want(g)) continue;
-    const int v0 = (i / kSegThreads) * (kSegThreads * kVec) + i % kSegThreads;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const int v = v0 + j * kSegThreads;
-      if (v >= row.nvec) continue;
+  } else {
+    for (int b = t; b < kBins; b += kSegThreads) {
+      mass[b] = 0;
+      count[b] = 0;
+    }
+    u64 q0 = 0;
+    if (!a.has_k) {
+      u64 low = 0;
+      for (int i = t & 63; i < p.segs; i += 64) low += wt.all(seg_max[i]);
+      q0 = (u64)((1.0 - a.p) * (double)wave_sum(low) / (double)p.V);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int j = 0; j < kVec && v0 + j * kSegThreads < row.nvec; ++j) {
       float z[R::VE];
-      row.load(v, z);
-      const int64_t e = row.first(v);
+      row.load(v0 + j * kSegThreads, z);
 #pragma unroll
-      for (int q = 0; q < R::VE; ++q) {
-        if (z[q] == kNegInf || !want(z[q])) continue;
-        const uint32_t at = atomicAdd(&sh.n, 1u);
-        if (at < kCap) {
-          sh.key[at] = __float_as_uint(z[q]);
-          sh.idx[at] = (uint32_t)(e + q);
+      for (int i = 0; i < R::VE; ++i) {
+        const u64 q = a.has_k ? 0 : wt.all(z[i]);
+        s += q;
+        if (z[i] != kNegInf && q >= q0) {
+          const uint32_t b = bin_of(m, z[i]);
+          atomicAdd(&count[b], 1u);
+          if (q != 0) atomicAdd(&mass[b], q);
         }
       }
     }
   }
+  s = wave_sum(s);
+  if ((t & 63) == 0) part[t >> 6] = s;
   __syncthreads();
-  return sh.n;
+  if (t == 0) p.seg_sum[r * p.segs + seg] = part[0] + part[1] + part[2] + part[3];
+  if (hist) {
+    for (int b = t; b < kBins; b += kSegThreads) {
+      if (count[b]) atomicAdd(&p.hist_count[r * kBins + b], count[b]);
+      if (mass[b]) atomicAdd((u64*)&p.hist_mass[r * kBins + b], mass[b]);
+    }
+  }
 }
 
 template <int DT>
@@ -775,82 +807,447 @@ __device__ __forceinline__ u64 ties_needed(u64 above, u64 each, u64 n, double go
   return t < n ? t : n;
 }
 
+// m - z, 0 for z = m also where both are infinite.
+__device__ __forceinline__ float distance(float m, float z) { return z == m ? 0.0f : m - z; }
+
+// Gathers into LDS the tokens with lo <= m - z <= hi, from the groups whose
+// maximum is within hi, in no order.  Returns their number; above kCap the
+// list is cut off.
+template <int DT>
+__device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const SampleParams& p,
+                                                  int64_t r, const Weights& wt, float lo, float hi,
+                                                  PickShared& sh) {
+  typedef Row<DT> R;
+  constexpr int kVec = kGroup / R::VE;
+  __syncthreads();
+  if (threadIdx.x == 0) sh.n = 0;
+  __syncthreads();
+  const float* gm = p.group_max + r * p.segs * kSegThreads;
+  for (int g = 0; g < p.segs; ++g) {
+    const float top = gm[g * kSegThreads + threadIdx.x];
+    if (top == kNegInf || distance(wt.m, top) > hi) continue;
+    const int v0 = g * (kSegThreads * kVec) + threadIdx.x;
+#pragma unroll 1
+    for (int j = 0; j < kVec; ++j) {
+      const int v = v0 + j * kSegThreads;
+      if (v >= row.nvec) break;
+      float z[R::VE];
+      row.load(v, z);
+      uint32_t in = 0;
+#pragma unroll
+      for (int q = 0; q < R::VE; ++q) {
+        const float d = distance(wt.m, z[q]);
+        in |= (z[q] != kNegInf && d >= lo && d <= hi ? 1u : 0u) << q;
+      }
+      while (in) {
+        const int q = __builtin_ctz(in);
+        in &= in - 1;
+        float x = z[0];
+#pragma unroll
+        for (int i = 1; i < R::VE; ++i) x = q == i ? z[i] : x;
+        const uint32_t at = atomicAdd(&sh.n, 1u);
+        if (at < kCap) {
+          const double w = wt.weight(x);
+          sh.list[at] = Entry{R::key(x), (uint32_t)(row.first(v) + q),
+                              wt.fixed(w) | (w >= wt.minp ? kKeptBit : 0)};
+        }
+      }
+    }
+  }
+  __syncthreads();
+  return sh.n;
+}
+
 struct Drawn {
   int64_t token;
-  u64 total;  // weight of all kept tokens
+  u64 total;     // weight of all kept tokens
+  // a threshold without a token: kept are the keys above tau, and the first
+  // `ties` tokens of key tau
+  uint32_t tau;
+  u64 ties;
 };
 
-// Draws from a list of candidates that holds every token the filters can
-// keep.  `mass` is the weight that top-p refers to without top-k.
+// Draws from the list of candidates, which holds every token the filters can
+// keep; `mass` is the weight that top-p refers to without top-k.  With
+// `threshold` the list holds one bin of the histogram, `above` is the
+// weight before it, and only top-p's threshold is taken.
 template <int DT>
-__device__ Drawn draw_list(const Ask& a, const Weights& wt, int64_t V, uint32_t n_list, u64 mass,
-                           Shared& sh) {
+__device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int64_t V, uint32_t n,
+                                           u64 mass, bool threshold, u64 above, PickShared& sh) {
   typedef Row<DT> R;
-  auto over = [&](auto f) {
-    for (uint32_t i = threadIdx.x; i < n_list; i += kThreads) {
-      const float z = __uint_as_float(sh.key[i]);
-      f(z, R::key(z), sh.idx[i]);
-    }
-  };
-  // kept: key > tau, or key = tau and index <= last
-  uint32_t tau = 0;
-  uint32_t last = 0xffffffffu;
-  u64 ties = ~(u64)0;
-  if (a.has_k && (u64)a.k < n_list) {
-    const Sel s = radix_select(R::kKeyBits, (double)a.k, false, sh, [&](auto f) {
-      over([&](float, uint32_t k, uint32_t) { f(k, (u64)1); });
-    });
-    tau = s.key;
-    ties = (u64)a.k - s.above;
-  }
-  if (a.has_p) {
-    if (a.has_k) {
-      u64 v = 0;
-      over([&](float z, uint32_t k, uint32_t) {
-        if (k > tau || ties == ~(u64)0) v += wt.all(z);
-      });
-      mass = block_sum(v, sh) + (ties == ~(u64)0 ? 0 : ties * wt.all(key_value<DT>(tau)));
-    }
-    const double goal = a.p * (double)mass;
-    const uint32_t tau_k = tau;
-    const Sel s = radix_select(R::kKeyBits, goal, false, sh, [&](auto f) {
-      over([&](float z, uint32_t k, uint32_t) {
-        if (k >= tau_k) f(k, wt.all(z));
-      });
-    });
-    u64 n = 0;
-    over([&](float, uint32_t k, uint32_t) { n += k == s.key; });
-    n = block_sum(n, sh);
-    if (s.key == tau_k && ties < n) n = ties;
-    ties = ties_needed(s.above, wt.all(key_value<DT>(s.key)), n, goal);
-    tau = s.key;
-  }
-  const int bits = 64 - __builtin_clzll((u64)V);
-  if (ties != ~(u64)0) {
-    u64 n = 0;
-    over([&](float, uint32_t k, uint32_t) { n += k == tau; });
-    n = block_sum(n, sh);
-    if (ties < n) {
-      const Sel s = radix_select(bits, (double)ties, false, sh, [&](auto f) {
-        over([&](float, uint32_t k, uint32_t i) {
-          if (k == tau) f((uint32_t)(V - 1 - i), (u64)1);
-        });
-      });
-      last = (uint32_t)(V - 1 - s.key);
-    }
-  }
-  auto amount = [&](float z, uint32_t k, uint32_t i) -> u64 {
-    return k > tau || (k == tau && i <= last) ? wt.kept(z) : 0;
-  };
-  u64 v = 0;
-  over([&](float z, uint32_t k, uint32_t i) { v += amount(z, k, i); });
+  constexpr int NW = kSegThreads / 64;
+  const uint32_t t = threadIdx.x;
   Drawn d;
-  d.total = block_sum(v, sh);
-  const Sel s = radix_select(bits, (double)a.u * (double)d.total, true, sh, [&](auto f) {
-    over([&](float z, uint32_t k, uint32_t i) { f((uint32_t)(V - 1 - i), amount(z, k, i)); });
-  });
-  d.token = V - 1 - (int64_t)s.key;
+  d.token = 0;
+  d.total = 0;
+  d.tau = 0;
+  d.ties = 0;
+  if (n <= kSegThreads && !threshold) {
+    // one candidate per thread: its rank and the weight ranked before it
+    const bool mine = t < n;
+    const Entry e = mine ? sh.list[t] : Entry{0, 0, 0};
+    const u64 q = e.q & ~kKeptBit;
+    uint32_t rank = 0;
+    u64 before = 0;
+    for (uint32_t j = 0; j < n; ++j) {
+      const Entry o = sh.list[j];
+      if (o.key > e.key || (o.key == e.key && o.idx < e.idx)) {
+        ++rank;
+        before += o.q & ~kKeptBit;
+      }
+    }
+    bool keep = mine && (!a.has_k || rank < (uint32_t)a.k);
+    if (a.has_p) {
+      if (a.has_k) mass = block_sum<NW>(keep ? q : 0, sh);
+      keep = keep && (rank == 0 || (double)before < a.p * (double)mass);
+    }
+    keep = keep && (e.q & kKeptBit);
+    d.total = block_sum<NW>(keep ? q : 0, sh);  // a barrier: the list has been read
+    if (mine) sh.list[t].q = keep ? q : 0;
+    if (t == 0) sh.out[0] = 0;
+    __syncthreads();
+    u64 upto = 0;
+    for (uint32_t j = 0; j < n; ++j) {
+      const Entry o = sh.list[j];
+      if (o.idx <= e.idx) upto += o.q;
+    }
+    const double goal = (double)a.u * (double)d.total;
+    // one kept candidate takes the sum across the goal
+    if (keep && q != 0 && (double)upto > goal && !((double)(upto - q) > goal))
+      sh.out[0] = e.idx;
+    __syncthreads();
+    d.token = (int64_t)sh.out[0];
+    return d;
+  }
+  n = n < kCap ? n : kCap;
+  u64 ties = ~(u64)0;  // none: no threshold
+  uint32_t tau = 0, last = 0xffffffffu;
+  const int idx_bits = 64 - __builtin_clzll((u64)V);
+  for (int stage = threshold ? 1 : 0; stage < (threshold ? 2 : 4); ++stage) {
+    double goal = 0.0;
+    if (stage == 0) {  // top-k
+      if (!a.has_k || (u64)a.k >= n) continue;
+      goal = (double)a.k;
+    } else if (stage == 1) {  // top-p
+      if (!a.has_p) continue;
+      if (a.has_k) {
+        u64 v = 0;
+        for (uint32_t i = t; i < n; i += kSegThreads)
+          if (ties == ~(u64)0 || sh.list[i].key > tau) v += sh.list[i].q & ~kKeptBit;
+        mass = block_sum<NW>(v, sh);
+        if (ties != ~(u64)0) mass += ties * wt.all(key_value<DT>(tau));
+      }
+      goal = a.p * (double)mass - (double)above;
+    } else if (stage == 2) {  // the last tie kept, where not all are
+      if (ties == ~(u64)0) continue;
+      u64 c = 0;
+      for (uint32_t i = t; i < n; i += kSegThreads) c += sh.list[i].key == tau;
+      if (ties >= block_sum<NW>(c, sh)) continue;
+      goal = (double)ties;
+    } else {  // the token
+      u64 v = 0;
+      for (uint32_t i = t; i < n; i += kSegThreads) {
+        const Entry e = sh.list[i];
+        if ((e.q & kKeptBit) && (e.key > tau || (e.key == tau && e.idx <= last)))
+          v += e.q & ~kKeptBit;
+      }
+      d.total = block_sum<NW>(v, sh);
+      goal = (double)a.u * (double)d.total;
+    }
+    const Sel s = radix_select(stage < 2 ? R::kKeyBits : idx_bits, goal, stage == 3, sh,
+                               [&](auto f) {
+      for (uint32_t i = t; i < n; i += kSegThreads) {
+        const Entry e = sh.list[i];
+        const bool in = stage == 0   ? true
+                        : stage == 1 ? e.key >= tau
+                        : stage == 2 ? e.key == tau
+                                     : (e.q & kKeptBit) &&
+                                           (e.key > tau || (e.key == tau && e.idx <= last));
+        const u64 w = stage == 1 || stage == 3 ? e.q & ~kKeptBit : (u64)1;
+        if (in) f(stage < 2 ? e.key : (uint32_t)(V - 1 - e.idx), w);
+      }
+    });
+    if (stage == 0) {
+      tau = s.key;
+      ties = (u64)a.k - s.above;
+    } else if (stage == 1) {
+      u64 c = 0;
+      for (uint32_t i = t; i < n; i += kSegThreads) c += sh.list[i].key == s.key;
+      c = block_sum<NW>(c, sh);
+      if (s.key == tau && ties < c) c = ties;
+      ties = ties_needed(s.above, wt.all(key_value<DT>(s.key)), c, goal);
+      tau = s.key;
+    } else if (stage == 2) {
+      last = (uint32_t)(V - 1 - s.key);
+    } else {
+      d.token = V - 1 - (int64_t)s.key;
+    }
+  }
+  d.tau = tau;
+  d.ties = ties;
   return d;
+}
+
+// The token and its log-probability, by one thread.
+template <int DT>
+__device__ __forceinline__ void write_out(const SampleParams& p, int64_t r, const Row<DT>& row,
+                                          const Ask& a, float m, int64_t token, u64 total) {
+  p.token[r] = token;
+  if (!p.logprob) return;
+  float lp = 0.0f;
+  if (!a.greedy) {
+    float z;
+    if constexpr (DT == 0)
+      z = reinterpret_cast<const float*>(row.base)[token];
+    else
+      z = from_bf16(reinterpret_cast<const uint16_t*>(row.base)[token]);
+    const double x = z == m ? 0.0 : ((double)z - (double)m) / (double)a.T;
+    lp = (float)(x - log((double)total * p.unit));
+  }
+  p.logprob[r] = lp;
+}
+
+enum State : uint32_t { kDone = 0, kThreshold = 1, kRow = 2 };
+
+template <int DT>
+__global__ __launch_bounds__(kSegThreads) void sample_pick_kernel(SampleParams p) {
+  __shared__ PickShared sh;
+  typedef Row<DT> R;
+  constexpr int kVec = kGroup / R::VE;
+  constexpr int NW = kSegThreads / 64;
+  const int64_t r = blockIdx.x;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const Ask a = ask_of(p, r);
+  const float* seg_max = p.seg_max + r * p.segs;
+  const float m = row_max(seg_max, p.segs);
+  if (t == 0 && p.state) p.state[r].what = kDone;
+  if (!a.ok || !(m > kNegInf)) {  // NaN too
+    if (t == 0) {
+      p.token[r] = -1;
+      if (p.logprob) p.logprob[r] = __builtin_nanf("");
+    }
+    return;
+  }
+  const R row = row_of<DT>(p, r);
+  const Weights wt = weights_of(p, a, m);
+  if (a.greedy || a.plain(p.V)) {
+    // the segment that holds the token: the first with the maximum, or the one
+    // in which the running sum crosses; every wavefront finds it
+    u64 total = 0, before = 0;
+    double goal = 0.0;
+    if (!a.greedy) {
+      for (int i = lane; i < p.segs; i += 64) total += p.seg_sum[r * p.segs + i];
+      total = wave_sum(total);
+      goal = (double)a.u * (double)total;
+    }
+    int seg = 0;
+    for (int i = 0; i < p.segs; i += 64) {
+      u64 v = 0;
+      if (i + lane < p.segs)
+        v = a.greedy ? (u64)(seg_max[i + lane] == m) : p.seg_sum[r * p.segs + i + lane];
+      const u64 run = wave_scan(v);
+      const uint64_t hit = __ballot(v != 0 && (double)(before + run) > goal);
+      if (hit) {
+        const int who = __builtin_ctzll(hit);
+        seg = i + who;
+        before += (u64)__shfl((unsigned long long)(run - v), who, 64);
+        break;
+      }
+      before += (u64)__shfl((unsigned long long)run, 63, 64);
+    }
+    // 64 consecutive vectors are a chunk; its sum, then the chunk of the crossing
+    auto amount = [&](float z) -> u64 { return a.greedy ? (u64)(z == m) : wt.all(z); };
+    const int v0 = seg * (kSegThreads * kVec) + t;
+#pragma unroll 1
+    for (int j = 0; j < kVec; ++j) {
+      u64 s = 0;
+      if (v0 + j * kSegThreads < row.nvec) {
+        float z[R::VE];
+        row.load(v0 + j * kSegThreads, z);
+#pragma unroll
+        for (int q = 0; q < R::VE; ++q) s += amount(z[q]);
+      }
+      s = wave_sum(s);
+      if (lane == 0) sh.hist[j * NW + wave] = s;
+    }
+    __syncthreads();
+    const u64 mine = lane < kVec * NW ? sh.hist[lane] : 0;
+    const u64 run = wave_scan(mine);
+    const uint64_t hit = __ballot(mine != 0 && (double)(before + run) > goal);
+    const int chunk = hit ? __builtin_ctzll(hit) : 0;
+    before += (u64)__shfl((unsigned long long)(run - mine), chunk, 64);
+    if (wave == 0) {
+      const int v = seg * (kSegThreads * kVec) + chunk * 64 + lane;
+      u64 w[R::VE], s = 0;
+#pragma unroll
+      for (int q = 0; q < R::VE; ++q) w[q] = 0;
+      if (v < row.nvec) {
+        float z[R::VE];
+        row.load(v, z);
+#pragma unroll
+        for (int q = 0; q < R::VE; ++q) {
+          w[q] = amount(z[q]);
+          s += w[q];
+        }
+      }
+      const u64 upto = before + wave_scan(s);
+      const uint64_t h = __ballot(s != 0 && (double)upto > goal);
+      if (lane == (h ? __builtin_ctzll(h) : 0)) {
+        u64 c = upto - s;
+        int64_t token = -1;
+#pragma unroll
+        for (int q = 0; q < R::VE; ++q) {
+          c += w[q];
+          if (token < 0 && w[q] != 0 && (double)c > goal) token = row.first(v) + q;
+        }
+        write_out<DT>(p, r, row, a, m, token, total);
+      }
+    }
+    return;
+  }
+  // candidates: distances up to hi
+  float lo = 0.0f, hi = __builtin_huge_valf();
+  u64 mass = 0, above = 0;
+  bool threshold = false;
+  if (a.list_all(p.V)) {
+  } else if (a.hist(p.V)) {
+    // the bin where the count or the mass is reached, 8 bins a thread
+    constexpr int kPer = kBins / kSegThreads;
+    const u64* hm = (const u64*)p.hist_mass + r * kBins + t * kPer;
+    const uint32_t* hc = p.hist_count + r * kBins + t * kPer;
+    u64 v = 0, c = 0;
+    for (int j = 0; j < kPer; ++j) {
+      c += hc[j];
+      v += a.has_k ? (u64)hc[j] : hm[j];
+    }
+    if (!a.has_k) {
+      for (int i = lane; i < p.segs; i += 64) mass += p.seg_sum[r * p.segs + i];
+      mass = wave_sum(mass);
+    }
+    const double goal = a.has_k ? (double)a.k : a.p * (double)mass;
+    const u64 rv = wave_scan(v), rc = wave_scan(c);
+    if (lane == 63) {
+      sh.wave[wave] = rv;
+      sh.wave2[wave] = rc;
+    }
+    if (t == 0) {
+      sh.out[0] = kBins - 1;  // never reached: all bins
+      sh.out[1] = sh.out[2] = 0;
+    }
+    __syncthreads();
+    u64 bv = rv - v, bc = rc - c;
+    for (int i = 0; i < wave; ++i) {
+      bv += sh.wave[i];
+      bc += sh.wave2[i];
+    }
+    if (!reached(bv, goal, false) && reached(bv + v, goal, false)) {
+      for (int j = 0; j < kPer; ++j) {
+        const u64 w = a.has_k ? (u64)hc[j] : hm[j];
+        bc += hc[j];
+        if (reached(bv + w, goal, false)) {
+          sh.out[0] = t * kPer + j;
+          sh.out[1] = bv;
+          sh.out[2] = bc;
+          break;
+        }
+        bv += w;
+      }
+    }
+    __syncthreads();
+    const uint32_t bin = (uint32_t)sh.out[0];
+    const uint32_t n_incl = (uint32_t)sh.out[2];
+    // the distances of bin b lie between bits (base + b) << 16 and the next
+    if (bin < kBins - 1) hi = __uint_as_float(((kBinBase + bin + 1) << 16) - 1);
+    if (!a.has_k && n_incl > kCap) {
+      threshold = true;
+      above = sh.out[1];
+      if (bin > 0) lo = __uint_as_float((kBinBase + bin) << 16);
+    }
+  } else if (a.has_k) {
+    // k groups with maxima of at least the k-th largest hold k tokens as
+    // large; the upper 16 bits of a key bound well enough
+    const int groups = p.segs * kSegThreads;
+    const float* gm = p.group_max + r * groups;
+    const Sel s = radix_select(16, (double)a.k, false, sh, [&](auto f) {
+      for (int i = t; i < groups; i += kSegThreads) {
+        const float g = gm[i];
+        if (g != kNegInf) f(Row<0>::key(g) >> 16, (u64)1);
+      }
+    });
+    // fewer such groups than k: every token is a candidate
+    if (s.above + s.at >= (u64)a.k) hi = distance(m, key_value<0>(s.key << 16));
+  } else {
+    // min-p alone: T ln(1 / min_p) and what its rounding may leave out
+    hi = (float)(-(double)a.T * log(a.minp) * (1.0 + 1e-6)) + 1e-30f;
+    hi += hi * 1e-6f;
+  }
+  const uint32_t n = gather_groups<DT>(row, p, r, wt, lo, hi, sh);
+  if (n > kCap) {
+    // min-p alone keeps all it has gathered: no further threshold
+    if (t == 0) {
+      p.state[r].what = !a.has_k && !a.has_p ? kThreshold : kRow;
+      p.state[r].tau = 0;
+      p.state[r].ties = 0;
+    }
+    return;
+  }
+  if (a.list_all(p.V) && a.has_p && !a.has_k) {
+    u64 v = 0;
+    for (uint32_t i = t; i < n; i += kSegThreads) v += sh.list[i].q & ~kKeptBit;
+    mass = block_sum<NW>(v, sh);
+  }
+  const Drawn d = draw_list<DT>(a, wt, p.V, n, mass, threshold, above, sh);
+  if (t == 0) {
+    if (threshold) {
+      p.state[r].what = kThreshold;
+      p.state[r].tau = d.tau;
+      p.state[r].ties = d.ties;
+    } else {
+      write_out<DT>(p, r, row, a, m, d.token, d.total);
+    }
+  }
+}
+
+// Rows with a threshold and no token yet: a segment's kept weight above the
+// threshold's key, and its tokens of that key.
+template <int DT>
+__global__ __launch_bounds__(kSegThreads) void sample_kept_kernel(SampleParams p) {
+  typedef Row<DT> R;
+  constexpr int kVec = kGroup / R::VE;
+  __shared__ u64 part[2][kSegThreads / 64];
+  const int64_t r = blockIdx.x;
+  if (p.state[r].what != kThreshold) return;
+  const int seg = blockIdx.y, t = threadIdx.x;
+  const Ask a = ask_of(p, r);
+  const float m = row_max(p.seg_max + r * p.segs, p.segs);
+  const Weights wt = weights_of(p, a, m);
+  const R row = row_of<DT>(p, r);
+  const uint32_t tau = p.state[r].tau;
+  const int v0 = seg * (kSegThreads * kVec) + t;
+  u64 s = 0, c = 0;
+#pragma unroll 1
+  for (int j = 0; j < kVec && v0 + j * kSegThreads < row.nvec; ++j) {
+    float z[R::VE];
+    row.load(v0 + j * kSegThreads, z);
+#pragma unroll
+    for (int i = 0; i < R::VE; ++i) {
+      const uint32_t k = R::key(z[i]);
+      if (k > tau) s += wt.kept(z[i]);
+      c += k == tau && z[i] != kNegInf;
+    }
+  }
+  s = wave_sum(s);
+  c = wave_sum(c);
+  if ((t & 63) == 0) {
+    part[0][t >> 6] = s;
+    part[1][t >> 6] = c;
+  }
+  __syncthreads();
+  if (t == 0) {
+    p.seg_sum[r * p.segs + seg] = part[0][0] + part[0][1] + part[0][2] + part[0][3];
+    p.seg_ties[r * p.segs + seg] =
+        (uint32_t)(part[1][0] + part[1][1] + part[1][2] + part[1][3]);
+  }
 }
 
 // Draws where the candidates do not fit in LDS: every pass reads the row.
@@ -873,7 +1270,7 @@ __device__ Drawn draw_row(const Row<DT>& row, const Ask& a, const Weights& wt, S
       row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t e, const float* z) {
 #pragma unroll
         for (int j = 0; j < R::VE; ++j) {
-          if (z[j] == kNegInf || (wt.hard && z[j] != m)) continue;
+          if (z[j] == kNegInf) continue;
           if (bin_of(m, z[j]) == b) f(z[j], e + j);
         }
       });
@@ -906,7 +1303,7 @@ __device__ Drawn draw_row(const Row<DT>& row, const Ask& a, const Weights& wt, S
           for (int j = 0; j < R::VE; ++j)
             if (R::key(z[j]) > tau) v += wt.all(z[j]);
         });
-        mass_k = block_sum(v, sh) + ties * wt.all(key_value<DT>(tau));
+        mass_k = block_sum<kWaves>(v, sh) + ties * wt.all(key_value<DT>(tau));
       }
     }
   }
@@ -929,7 +1326,7 @@ __device__ Drawn draw_row(const Row<DT>& row, const Ask& a, const Weights& wt, S
     });
     u64 n = 0;
     over(list, b.bin, [&](float z, int64_t) { n += R::key(z) == s.key; });
-    n = block_sum(n, sh);
+    n = block_sum<kWaves>(n, sh);
     if (select && s.key == tau_k && ties < n) n = ties;
     ties = ties_needed(b.above + s.above, wt.all(key_value<DT>(s.key)), n, goal);
     tau = s.key;
@@ -939,7 +1336,7 @@ __device__ Drawn draw_row(const Row<DT>& row, const Ask& a, const Weights& wt, S
     u64 n;
     last = locate<DT>(row, 0, row.nvec, sh, 0, [&](u64) { return (double)ties - 0.5; }, &n,
                       [&](int64_t, float z) {
-      return (u64)(z != kNegInf && R::key(z) == tau && !(wt.hard && z != m));
+      return (u64)(z != kNegInf && R::key(z) == tau);
     });
   }
   Drawn d;
@@ -954,145 +1351,71 @@ __device__ Drawn draw_row(const Row<DT>& row, const Ask& a, const Weights& wt, S
 }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleParams p) {
+__global__ __launch_bounds__(kThreads) void sample_rest_kernel(SampleParams p) {
   __shared__ Shared sh;
   typedef Row<DT> R;
   const int64_t r = blockIdx.x;
+  const uint32_t what = p.state[r].what;
+  if (what == kDone) return;
   const Ask a = ask_of(p, r);
   const float m = row_max(p.seg_max + r * p.segs, p.segs);
-  if (!a.ok || !(m > kNegInf)) {  // NaN too
-    if (threadIdx.x == 0) {
-      p.token[r] = -1;
-      if (p.logprob) p.logprob[r] = __builtin_nanf("");
-    }
-    return;
-  }
   const R row = row_of<DT>(p, r);
   const Weights wt = weights_of(p, a, m);
-  constexpr int kSegVec = kSeg / R::VE;
   Drawn d;
-  if (a.greedy || a.plain(p.V)) {
-    // the segment that holds the token: the first with the maximum, or the one
-    // in which the running sum crosses
-    if (threadIdx.x < 64) {
-      const int lane = threadIdx.x;
-      u64 total = 0;
-      if (!a.greedy) {
-        for (int i = lane; i < p.segs; i += 64) total += p.seg_sum[r * p.segs + i];
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1)
-          total += (u64)__shfl_xor((unsigned long long)total, off, 64);
-      }
-      const double goal = (double)a.u * (double)total;
-      u64 before = 0;
-      int seg = 0;
-      for (int i = 0; i < p.segs; i += 64) {
-        u64 v = 0;
-        if (i + lane < p.segs)
-          v = a.greedy ? (u64)(p.seg_max[r * p.segs + i + lane] == m)
-                       : p.seg_sum[r * p.segs + i + lane];
-        u64 run = v;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-          const u64 w = shfl_up64(run, o);
-          if (lane >= o) run += w;
-        }
-        const uint64_t hit =
-            __ballot(v != 0 && (a.greedy || (double)(before + run) > goal));
-        if (hit) {
-          const int who = __builtin_ctzll(hit);
-          seg = i + who;
-          before += (u64)__shfl((unsigned long long)(run - v), who, 64);
-          break;
-        }
-        before += (u64)__shfl((unsigned long long)run, 63, 64);
-      }
-      if (lane == 0) {
-        sh.out[0] = (u64)seg;
-        sh.out[1] = before;
-        sh.out[2] = total;
-      }
-    }
-    __syncthreads();
-    const int seg = (int)sh.out[0];
-    const u64 before = a.greedy ? 0 : sh.out[1];
-    d.total = sh.out[2];
-    // a difference of two doubles below 2^63: the crossing is tested on whole sums
-    const double goal = a.greedy ? 0.0 : (double)a.u * (double)d.total;
-    u64 part;
-    d.token = locate<DT>(row, seg * kSegVec, min((seg + 1) * kSegVec, row.nvec), sh, before,
-                         [&](u64) { return goal; }, &part,
-                         [&](int64_t, float z) { return wt.all(z); });
+  if (what == kRow) {
+    d = draw_row<DT>(row, a, wt, sh);
   } else {
-    uint32_t n = kCap + 1;
-    u64 mass = 0;
-    if (a.list_all(p.V)) {
-      n = gather_groups<DT>(row, p, r, sh, [&](float z) { return !wt.hard || z == m; });
-      if (a.has_p && !a.has_k) {
-        u64 v = 0;
-        for (uint32_t i = threadIdx.x; i < n; i += kThreads)
-          v += wt.all(__uint_as_float(sh.key[i]));
-        mass = block_sum(v, sh);
+    // the segment in which the kept sum crosses; the ties kept are the first
+    // in index order, so a segment has those that the ones before it left
+    const int lane = threadIdx.x & 63;
+    const uint32_t tau = p.state[r].tau;
+    const u64 ties = p.state[r].ties;
+    const u64 each = ties ? wt.kept(key_value<DT>(tau)) : 0;
+    const u64* sum = (const u64*)p.seg_sum + r * p.segs;
+    const uint32_t* cnt = p.seg_ties + r * p.segs;
+    u64 total = 0;
+    for (int i = lane; i < p.segs; i += 64) total += sum[i];
+    total = wave_sum(total) + ties * each;
+    const double goal = (double)a.u * (double)total;
+    u64 before = 0, used = 0, here = 0, all_here = 0;
+    int seg = 0;
+    for (int i = 0; i < p.segs; i += 64) {
+      const bool in = i + lane < p.segs;
+      const u64 c = in ? cnt[i + lane] : 0;
+      const u64 c_before = used + wave_scan(c) - c;
+      const u64 left = ties > c_before ? ties - c_before : 0;
+      const u64 k = left < c ? left : c;
+      const u64 v = (in ? sum[i + lane] : 0) + k * each;
+      const u64 run = wave_scan(v);
+      const uint64_t hit = __ballot(v != 0 && (double)(before + run) > goal);
+      if (hit) {
+        const int who = __builtin_ctzll(hit);
+        seg = i + who;
+        before += (u64)__shfl((unsigned long long)(run - v), who, 64);
+        here = (u64)__shfl((unsigned long long)k, who, 64);
+        all_here = (u64)__shfl((unsigned long long)c, who, 64);
+        break;
       }
-    } else if (a.hist(p.V)) {
-      for (int i = threadIdx.x; i < kBins; i += kThreads) {
-        sh.count[i] = p.hist_count[r * kBins + i];
-        sh.mass[i] = p.hist_mass[r * kBins + i];
-      }
-      __syncthreads();
-      BinSel b;
-      if (a.has_k) {
-        b = scan_bins(sh, [&](int i) { return (u64)sh.count[i]; },
-                      [&](u64) { return (double)a.k; });
-      } else {
-        b = scan_bins(sh, [&](int i) { return sh.mass[i]; },
-                      [&](u64 total) { return a.p * (double)total; });
-        mass = b.total;
-      }
-      if (b.n_incl <= kCap)
-        n = gather_groups<DT>(row, p, r, sh, [&](float z) {
-          return (!wt.hard || z == m) && (int)bin_of(m, z) <= b.bin;
-        });
-    } else if (a.has_k) {
-      // k groups with maxima of at least the k-th largest hold k tokens as large
-      const int groups = p.segs * kSegThreads;
-      const float* gm = p.group_max + r * groups;
-      const Sel s = radix_select(R::kKeyBits, (double)a.k, false, sh, [&](auto f) {
-        for (int i = threadIdx.x; i < groups; i += kThreads) {
-          const float g = gm[i];
-          if (g != kNegInf && (!wt.hard || g == m)) f(R::key(g), (u64)1);
-        }
-      });
-      // fewer such groups than k: every token is a candidate
-      const uint32_t bound = s.above + s.at >= (u64)a.k ? s.key : 0u;
-      n = gather_groups<DT>(row, p, r, sh, [&](float z) {
-        return (!wt.hard || z == m) && R::key(z) >= bound;
-      });
-    } else {
-      // min-p alone
-      n = gather_groups<DT>(row, p, r, sh, [&](float z) { return wt.kept(z) != 0; });
+      before += (u64)__shfl((unsigned long long)run, 63, 64);
+      used = (u64)__shfl((unsigned long long)(c_before + c), 63, 64);
     }
-    if (n <= kCap)
-      d = draw_list<DT>(a, wt, p.V, n, mass, sh);
-    else
-      d = draw_row<DT>(row, a, wt, sh);
+    constexpr int kSegVec = kSeg / R::VE;
+    const int c0 = seg * kSegVec, c1 = min(c0 + kSegVec, row.nvec);
+    int64_t last = here == all_here ? row.V : -1;
+    u64 part;
+    if (here != 0 && here < all_here)
+      last = locate<DT>(row, c0, c1, sh, 0, [&](u64) { return (double)here - 0.5; }, &part,
+                        [&](int64_t, float z) {
+        return (u64)(z != kNegInf && R::key(z) == tau);
+      });
+    d.total = total;
+    d.token = locate<DT>(row, c0, c1, sh, before, [&](u64) { return goal; }, &part,
+                         [&](int64_t i, float z) -> u64 {
+      const uint32_t k = R::key(z);
+      return k > tau || (k == tau && i <= last) ? wt.kept(z) : 0;
+    });
   }
-  if (threadIdx.x == 0) {
-    p.token[r] = d.token;
-    if (p.logprob) {
-      float lp = 0.0f;
-      if (!a.greedy) {
-        float z;
-        if constexpr (DT == 0)
-          z = reinterpret_cast<const float*>(row.base)[d.token];
-        else
-          z = from_bf16(reinterpret_cast<const uint16_t*>(row.base)[d.token]);
-        const double x = wt.hard ? 0.0 : ((double)z - (double)m) / (double)a.T;
-        lp = (float)(x - log((double)d.total / p.one));
-      }
-      p.logprob[r] = lp;
-    }
-  }
+  if (threadIdx.x == 0) write_out<DT>(p, r, row, a, m, d.token, d.total);
 }
 
 }  // namespace
@@ -1111,39 +1434,61 @@ static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t sample_workspace_bytes(int64_t N, int64_t V) {
   const size_t rows = (size_t)N, s = rows * (size_t)segments(V);
-  return 256 + up256(s * kSegThreads * 4) + up256(s * 4) + up256(s * 8) + up256(rows * kBins * 8) +
-         up256(rows * kBins * 4);
+  return 256 + up256(s * kSegThreads * 4) + 2 * up256(s * 4) + up256(s * 8) +
+         up256(rows * kBins * 8) + up256(rows * kBins * 4) + up256(rows * sizeof(SampleState));
 }
 
 hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
                          hipStream_t stream) {
   if (N <= 0) return hipSuccess;
+  // (2^f - 1) / f on [-1/2, 1/2], from the constant term up (see Weights)
+  static const double kPoly[9] = {0x1.62e42fefa39efp-1,  0x1.ebfbdff823cedp-3,
+                                  0x1.c6b08d7047e52p-5,  0x1.3b2ab7181b755p-7,
+                                  0x1.5d87fe86fe88ep-10, 0x1.4308ac85aa947p-13,
+                                  0x1.ffcb9515a8016p-17, 0x1.63d136366db24p-20,
+                                  0x1.b63880a30e9ffp-24};
+  for (int i = 0; i < 9; ++i) p.poly[i] = kPoly[i];
   const int fb = weight_bits(p.V);
   p.magic = ldexp(1.0, 52 - fb);
-  p.one = ldexp(1.0, fb);
+  p.unit = ldexp(1.0, -fb);
   p.segs = (int)segments(p.V);
   const size_t rows = (size_t)N, s = rows * (size_t)p.segs;
   char* w = static_cast<char*>(workspace);
-  p.group_max = reinterpret_cast<float*>(w);
-  w += up256(s * kSegThreads * 4);
-  p.seg_max = reinterpret_cast<float*>(w);
-  w += up256(s * 4);
-  p.seg_sum = reinterpret_cast<unsigned long long*>(w);
-  w += up256(s * 8);
-  p.hist_mass = reinterpret_cast<unsigned long long*>(w);
-  w += up256(rows * kBins * 8);
-  p.hist_count = reinterpret_cast<uint32_t*>(w);
+  auto take = [&](size_t n) {
+    char* at = w;
+    w += up256(n);
+    return at;
+  };
+  p.group_max = reinterpret_cast<float*>(take(s * kSegThreads * 4));
+  p.seg_max = reinterpret_cast<float*>(take(s * 4));
+  p.seg_ties = reinterpret_cast<uint32_t*>(take(s * 4));
+  p.seg_sum = reinterpret_cast<unsigned long long*>(take(s * 8));
+  p.hist_mass = reinterpret_cast<unsigned long long*>(take(rows * kBins * 8));
+  p.hist_count = reinterpret_cast<uint32_t*>(take(rows * kBins * 4));
+  p.state = reinterpret_cast<SampleState*>(take(rows * sizeof(SampleState)));
   const dim3 seg_grid((unsigned)N, (unsigned)p.segs);
-#define VCE_SAMPLE(DT)                                                                          \
-  hipLaunchKernelGGL((sample_max_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);       \
-  hipLaunchKernelGGL((sample_mass_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);      \
-  hipLaunchKernelGGL((sample_row_kernel<DT>), dim3((unsigned)N), dim3(kThreads), 0, stream, p)
-  if (dtype == 0) {
-    VCE_SAMPLE(0);
-  } else {
-    VCE_SAMPLE(1);
-  }
-#undef VCE_SAMPLE
+  // rows of at most kCap tokens are gathered whole; without filters no row has
+  // more candidates than LDS holds
+  const bool mass = p.V > kCap;
+  const bool rest = mass && (p.top_k || p.top_p || p.min_p);
+  if (!rest) p.state = nullptr;
+  auto run = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    hipLaunchKernelGGL((sample_max_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);
+    if (mass)
+      hipLaunchKernelGGL((sample_mass_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);
+    hipLaunchKernelGGL((sample_pick_kernel<DT>), dim3((unsigned)N), dim3(kSegThreads), 0, stream,
+                       p);
+    if (rest) {
+      hipLaunchKernelGGL((sample_kept_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);
+      hipLaunchKernelGGL((sample_rest_kernel<DT>), dim3((unsigned)N), dim3(kThreads), 0, stream,
+                         p);
+    }
+  };
+  if (dtype == 0)
+    run(std::integral_constant<int, 0>{});
+  else
+    run(std::integral_constant<int, 1>{});
   return hipGetLastError();
 }
 

@@ -227,6 +227,12 @@ hipError_t launch_mx_logits(MxGemmParams p, int x_format, int w_format, int dtyp
 
 // ---- drawing a token -----------------------------------------------------------
 
+// A row that sample_pick_kernel has left to the kernels after it.
+struct SampleState {
+  uint32_t what, tau;
+  unsigned long long ties;
+};
+
 struct SampleParams {
   const void* logits;
   int64_t d1, ls0, ls1, V;
@@ -237,14 +243,18 @@ struct SampleParams {
   const float* u;
   int64_t* token;
   float* logprob;  // optional (N)
-  // set by the launcher: the weights' fixed point, and the workspace's parts
-  double magic = 0.0, one = 0.0;
+  // set by the launcher: the weights' fixed point and polynomial, and the
+  // workspace's parts
+  double magic = 0.0, unit = 0.0;
+  double poly[9] = {};
   int segs = 0;                             // segments per row
   float* group_max = nullptr;               // (N, segs, 256)
   float* seg_max = nullptr;                 // (N, segs)
+  uint32_t* seg_ties = nullptr;             // (N, segs)
   unsigned long long* seg_sum = nullptr;    // (N, segs)
   unsigned long long* hist_mass = nullptr;  // (N, 2048)
   uint32_t* hist_count = nullptr;           // (N, 2048)
+  SampleState* state = nullptr;             // (N), NULL where every row is done in one kernel
 };
 
 size_t sample_workspace_bytes(int64_t N, int64_t V);
