@@ -47,7 +47,7 @@ namespace vce {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;   // of the kernel that reads whole rows
 constexpr int kWaves = kThreads / 64;
 constexpr int kBins = 2048;
 constexpr uint32_t kBinBase = 119u << 7;  // bits of 2^-8 over 2^16: bin 0 lies below
@@ -224,8 +224,12 @@ struct alignas(16) Entry {
 };
 constexpr u64 kKeptBit = (u64)1 << 63;
 
+constexpr int kGroupBatch = 16;  // segments whose group maxima a thread loads at once
+
 struct PickShared : Scratch {
   Entry list[kCap];
+  uint16_t group[kGroupBatch * kSegThreads];
+  uint32_t n_groups;
 };
 
 __device__ __forceinline__ u64 shfl_up64(u64 v, int d) {
@@ -328,7 +332,7 @@ __device__ __forceinline__ Sel radix_select(int bits, double target, bool strict
 // sixteenth of the range, the sixteenth that holds the crossing is split
 // again, down to one vector per lane.
 template <int DT, class Target, class Amount>
-__device__ int64_t locate(const Row<DT>& row, int c0, int c1, Shared& sh, u64 before,
+__device__ __forceinline__ int64_t locate(const Row<DT>& row, int c0, int c1, Shared& sh, u64 before,
                           Target target, u64* total, Amount amount) {
   constexpr int VE = Row<DT>::VE;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -420,7 +424,7 @@ __device__ __forceinline__ uint32_t bin_of(float m, float z) {
 
 // Histogram of the row over bin_of: tokens per bin, and with MASS their weights.
 template <int DT, bool MASS>
-__device__ void histogram(const Row<DT>& row, const Weights& wt, Shared& sh) {
+__device__ __forceinline__ void histogram(const Row<DT>& row, const Weights& wt, Shared& sh) {
   for (int i = threadIdx.x; i < kBins; i += kThreads) {
     sh.count[i] = 0;
     sh.mass[i] = 0;
@@ -452,7 +456,7 @@ struct BinSel {
 // The first bin where the running amount (mass or count) reaches
 // target(total); the last one if it never does.
 template <class Amount, class Target>
-__device__ BinSel scan_bins(Shared& sh, Amount amount, Target target) {
+__device__ __forceinline__ BinSel scan_bins(Shared& sh, Amount amount, Target target) {
   constexpr int kPer = kBins / kThreads;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   u64 s = 0;
@@ -526,7 +530,7 @@ __device__ BinSel scan_bins(Shared& sh, Amount amount, Target target) {
 
 // Gathers the tokens of bins [lo, hi] (at most kCap of them) into LDS, in no order.
 template <int DT>
-__device__ void gather(const Row<DT>& row, const Weights& wt, Shared& sh, uint32_t lo,
+__device__ __forceinline__ void gather(const Row<DT>& row, const Weights& wt, Shared& sh, uint32_t lo,
                        uint32_t hi) {
   if (threadIdx.x == 0) sh.n = 0;
   __syncthreads();
@@ -736,11 +740,10 @@ __global__ __launch_bounds__(kSegThreads, 4) void sample_mass_kernel(SampleParam
   if (!(m > kNegInf)) return;  // no admissible token, or NaN
   const Weights wt = weights_of(p, a, m);
   const R row = row_of<DT>(p, r);
-  const int v0 = seg * (kSegThreads * kVec) + t;
+  float z[kVec][R::VE];
+  load_group<DT>(row, seg * (kSegThreads * kVec) + t, z);
   u64 s = 0;
   if (plain) {
-    float z[kVec][R::VE];
-    load_group<DT>(row, v0, z);
     if (wt.inf) {
 #pragma unroll
       for (int j = 0; j < kGroup; ++j) s += wt.fixed(z[j / R::VE][j % R::VE] == m ? 1.0 : 0.0);
@@ -760,18 +763,27 @@ __global__ __launch_bounds__(kSegThreads, 4) void sample_mass_kernel(SampleParam
       q0 = (u64)((1.0 - a.p) * (double)wave_sum(low) / (double)p.V);
     }
     __syncthreads();
-#pragma unroll 1
-    for (int j = 0; j < kVec && v0 + j * kSegThreads < row.nvec; ++j) {
-      float z[R::VE];
-      row.load(v0 + j * kSegThreads, z);
+    if (wt.inf || a.has_k) {
 #pragma unroll
-      for (int i = 0; i < R::VE; ++i) {
-        const u64 q = a.has_k ? 0 : wt.all(z[i]);
+      for (int j = 0; j < kGroup; ++j) {
+        const float v = z[j / R::VE][j % R::VE];
+        const u64 q = a.has_k ? 0 : wt.all(v);
         s += q;
-        if (z[i] != kNegInf && q >= q0) {
-          const uint32_t b = bin_of(m, z[i]);
+        if (v != kNegInf && q >= q0) {
+          atomicAdd(&count[bin_of(m, v)], 1u);
+          if (q != 0) atomicAdd(&mass[bin_of(m, v)], q);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        const float v = z[j / R::VE][j % R::VE];
+        const u64 q = wt.fixed(wt.real(v));
+        s += q;
+        if (q >= q0 && q != 0) {
+          const uint32_t b = bin_of(m, v);
           atomicAdd(&count[b], 1u);
-          if (q != 0) atomicAdd(&mass[b], q);
+          atomicAdd(&mass[b], q);
         }
       }
     }
@@ -810,27 +822,45 @@ __device__ __forceinline__ u64 ties_needed(u64 above, u64 each, u64 n, double go
 // m - z, 0 for z = m also where both are infinite.
 __device__ __forceinline__ float distance(float m, float z) { return z == m ? 0.0f : m - z; }
 
-// Gathers into LDS the tokens with lo <= m - z <= hi, from the groups whose
-// maximum is within hi, in no order.  Returns their number; above kCap the
-// list is cut off.
+// f(group, maximum) for this thread's groups of segments g0 .. g0 + 15, their
+// loads in flight together.
+template <class F>
+__device__ __forceinline__ void each_group(const float* gm, int segs, int g0, F f) {
+  float top[kGroupBatch];
+#pragma unroll
+  for (int i = 0; i < kGroupBatch; ++i)
+    top[i] = g0 + i < segs ? gm[(g0 + i) * kSegThreads + threadIdx.x] : kNegInf;
+#pragma unroll
+  for (int i = 0; i < kGroupBatch; ++i)
+    if (top[i] != kNegInf) f(i * kSegThreads + threadIdx.x, top[i]);
+}
+
+// Gathers into LDS the tokens with lo <= m - z <= hi, in no order, from the
+// groups whose maximum is within hi: first those groups are listed, then their
+// vectors are dealt over the threads, so that all loads wait together.
+// Returns the number of tokens; above kCap the list is cut off.
 template <int DT>
 __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const SampleParams& p,
                                                   int64_t r, const Weights& wt, float lo, float hi,
                                                   PickShared& sh) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
+  const float* gm = p.group_max + r * p.segs * kSegThreads;
   __syncthreads();
   if (threadIdx.x == 0) sh.n = 0;
-  __syncthreads();
-  const float* gm = p.group_max + r * p.segs * kSegThreads;
-  for (int g = 0; g < p.segs; ++g) {
-    const float top = gm[g * kSegThreads + threadIdx.x];
-    if (top == kNegInf || distance(wt.m, top) > hi) continue;
-    const int v0 = g * (kSegThreads * kVec) + threadIdx.x;
-#pragma unroll 1
-    for (int j = 0; j < kVec; ++j) {
-      const int v = v0 + j * kSegThreads;
-      if (v >= row.nvec) break;
+  for (int g0 = 0; g0 < p.segs; g0 += kGroupBatch) {
+    if (threadIdx.x == 0) sh.n_groups = 0;
+    __syncthreads();
+    each_group(gm, p.segs, g0, [&](int i, float top) {
+      if (distance(wt.m, top) <= hi) sh.group[atomicAdd(&sh.n_groups, 1u)] = (uint16_t)i;
+    });
+    __syncthreads();
+    const int items = (int)sh.n_groups * kVec;
+    for (int i = threadIdx.x; i < items; i += kSegThreads) {
+      const int g = sh.group[i / kVec];
+      const int v = (g0 + g / kSegThreads) * (kSegThreads * kVec) +
+                    (i % kVec) * kSegThreads + g % kSegThreads;
+      if (v >= row.nvec) continue;
       float z[R::VE];
       row.load(v, z);
       uint32_t in = 0;
@@ -844,7 +874,7 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Samp
         in &= in - 1;
         float x = z[0];
 #pragma unroll
-        for (int i = 1; i < R::VE; ++i) x = q == i ? z[i] : x;
+        for (int j = 1; j < R::VE; ++j) x = q == j ? z[j] : x;
         const uint32_t at = atomicAdd(&sh.n, 1u);
         if (at < kCap) {
           const double w = wt.weight(x);
@@ -853,8 +883,8 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Samp
         }
       }
     }
+    __syncthreads();
   }
-  __syncthreads();
   return sh.n;
 }
 
@@ -1057,18 +1087,17 @@ __global__ __launch_bounds__(kSegThreads) void sample_pick_kernel(SampleParams p
     }
     // 64 consecutive vectors are a chunk; its sum, then the chunk of the crossing
     auto amount = [&](float z) -> u64 { return a.greedy ? (u64)(z == m) : wt.all(z); };
-    const int v0 = seg * (kSegThreads * kVec) + t;
-#pragma unroll 1
-    for (int j = 0; j < kVec; ++j) {
-      u64 s = 0;
-      if (v0 + j * kSegThreads < row.nvec) {
-        float z[R::VE];
-        row.load(v0 + j * kSegThreads, z);
+    {
+      float z[kVec][R::VE];
+      load_group<DT>(row, seg * (kSegThreads * kVec) + t, z);
 #pragma unroll
-        for (int q = 0; q < R::VE; ++q) s += amount(z[q]);
+      for (int j = 0; j < kVec; ++j) {
+        u64 s = 0;
+#pragma unroll
+        for (int q = 0; q < R::VE; ++q) s += amount(z[j][q]);
+        s = wave_sum(s);
+        if (lane == 0) sh.hist[j * NW + wave] = s;
       }
-      s = wave_sum(s);
-      if (lane == 0) sh.hist[j * NW + wave] = s;
     }
     __syncthreads();
     const u64 mine = lane < kVec * NW ? sh.hist[lane] : 0;
@@ -1166,13 +1195,10 @@ __global__ __launch_bounds__(kSegThreads) void sample_pick_kernel(SampleParams p
   } else if (a.has_k) {
     // k groups with maxima of at least the k-th largest hold k tokens as
     // large; the upper 16 bits of a key bound well enough
-    const int groups = p.segs * kSegThreads;
-    const float* gm = p.group_max + r * groups;
+    const float* gm = p.group_max + r * p.segs * kSegThreads;
     const Sel s = radix_select(16, (double)a.k, false, sh, [&](auto f) {
-      for (int i = t; i < groups; i += kSegThreads) {
-        const float g = gm[i];
-        if (g != kNegInf) f(Row<0>::key(g) >> 16, (u64)1);
-      }
+      for (int g0 = 0; g0 < p.segs; g0 += kGroupBatch)
+        each_group(gm, p.segs, g0, [&](int, float g) { f(Row<0>::key(g) >> 16, (u64)1); });
     });
     // fewer such groups than k: every token is a candidate
     if (s.above + s.at >= (u64)a.k) hi = distance(m, key_value<0>(s.key << 16));
@@ -1211,7 +1237,7 @@ __global__ __launch_bounds__(kSegThreads) void sample_pick_kernel(SampleParams p
 // Rows with a threshold and no token yet: a segment's kept weight above the
 // threshold's key, and its tokens of that key.
 template <int DT>
-__global__ __launch_bounds__(kSegThreads) void sample_kept_kernel(SampleParams p) {
+__global__ __launch_bounds__(kSegThreads, 4) void sample_kept_kernel(SampleParams p) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
   __shared__ u64 part[2][kSegThreads / 64];
@@ -1223,18 +1249,15 @@ __global__ __launch_bounds__(kSegThreads) void sample_kept_kernel(SampleParams p
   const Weights wt = weights_of(p, a, m);
   const R row = row_of<DT>(p, r);
   const uint32_t tau = p.state[r].tau;
-  const int v0 = seg * (kSegThreads * kVec) + t;
+  float z[kVec][R::VE];
+  load_group<DT>(row, seg * (kSegThreads * kVec) + t, z);
   u64 s = 0, c = 0;
-#pragma unroll 1
-  for (int j = 0; j < kVec && v0 + j * kSegThreads < row.nvec; ++j) {
-    float z[R::VE];
-    row.load(v0 + j * kSegThreads, z);
 #pragma unroll
-    for (int i = 0; i < R::VE; ++i) {
-      const uint32_t k = R::key(z[i]);
-      if (k > tau) s += wt.kept(z[i]);
-      c += k == tau && z[i] != kNegInf;
-    }
+  for (int j = 0; j < kGroup; ++j) {
+    const float v = z[j / R::VE][j % R::VE];
+    const uint32_t k = R::key(v);
+    if (k > tau) s += wt.kept(v);
+    c += k == tau && v != kNegInf;
   }
   s = wave_sum(s);
   c = wave_sum(c);
@@ -1252,7 +1275,7 @@ __global__ __launch_bounds__(kSegThreads) void sample_kept_kernel(SampleParams p
 
 // Draws where the candidates do not fit in LDS: every pass reads the row.
 template <int DT>
-__device__ Drawn draw_row(const Row<DT>& row, const Ask& a, const Weights& wt, Shared& sh) {
+__device__ __forceinline__ Drawn draw_row(const Row<DT>& row, const Ask& a, const Weights& wt, Shared& sh) {
   typedef Row<DT> R;
   const float m = wt.m;
   bool has_k = a.has_k;
