@@ -30,8 +30,9 @@
 //    through selection by eight key bits at a time.  A row without filters
 //    re-reads the one segment in which its sum crosses u.
 //  * rows with more candidates than LDS holds: sample_kept_kernel (rows x
-//    segments) sums what their threshold keeps, sample_rest_kernel (rows) draws;
-//    those whose threshold itself needs more passes it serves from the row.
+//    segments) sums what lies before the histogram's bin and lists the tokens of
+//    that bin, sample_rest_kernel (rows) finds the threshold in the list and
+//    draws.  What does not fit that either is served from the row, pass by pass.
 // The code that a usual row runs is kept short: a kernel this brief waits for
 // its instructions more than for its data (one row of 128256 with all filters took 67 us
 // in a kernel of 60 KB, most of it instruction fetch).
@@ -47,15 +48,14 @@ namespace vce {
 
 namespace {
 
-constexpr int kThreads = 512;   // of the kernel that reads whole rows
+constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBins = 2048;
 constexpr uint32_t kBinBase = 119u << 7;  // bits of 2^-8 over 2^16: bin 0 lies below
 constexpr int kCap = 4096;                // candidates held in LDS
 constexpr int kLoads = 4;                 // vectors in flight per thread
-constexpr int kSegThreads = 256;
 constexpr int kGroup = 32;                // tokens per thread of a segment
-constexpr int kSeg = kSegThreads * kGroup;
+constexpr int kSeg = kThreads * kGroup;
 constexpr int kSmallK = 1024;             // top-k up to here bounds by group maxima
 
 typedef unsigned long long u64;
@@ -97,6 +97,22 @@ struct Row {
         }
         z[j] = t + 0.0f;
       }
+    }
+  }
+  // The same, with -inf for a vector past the row.  One load is issued whatever the
+  // case, so that several calls wait together.
+  __device__ __forceinline__ void load_or_none(int i, float* z) const {
+    const int64_t e = first(i);
+    const bool full = e >= 0 && e + VE <= V;
+    u32x4_t raw{0, 0, 0, 0};
+    if (full) raw = *reinterpret_cast<const u32x4_t*>(base + e * (DT == 0 ? 4 : 2));
+    if (full) {
+      unpack(raw, z);
+    } else if (i < nvec) {
+      load(i, z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) z[j] = kNegInf;
     }
   }
   static __device__ __forceinline__ void unpack(const u32x4_t& w, float* z) {
@@ -226,21 +242,51 @@ constexpr u64 kKeptBit = (u64)1 << 63;
 
 constexpr int kGroupBatch = 16;  // segments whose group maxima a thread loads at once
 
+constexpr int kKeepSegs = 1024;  // segments of a row that sample_rest_kernel draws from
+
 struct PickShared : Scratch {
   Entry list[kCap];
-  uint16_t group[kGroupBatch * kSegThreads];
+  union {
+    uint16_t group[kGroupBatch * kThreads];
+    u64 keep[kKeepSegs];
+  };
   uint32_t n_groups;
 };
 
-__device__ __forceinline__ u64 shfl_up64(u64 v, int d) {
-  return (u64)__shfl_up((unsigned long long)v, d, 64);
+// v of another lane of the wavefront by data-parallel-primitive control CTRL, 0
+// where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 dpp64(u64 v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+  return ((u64)(uint32_t)hi << 32) | (uint32_t)lo;
 }
+
+// Running sum over the lanes, each with its own share included: within rows of
+// 16 lanes by shifts, then row 0 into row 1 and 2 into 3, then lane 31 into the
+// upper half.  (Register moves; a shuffle through LDS per step took ten times as long.)
+__device__ __forceinline__ u64 wave_scan(u64 v) {
+  v += dpp64<0x111, 0xf>(v);
+  v += dpp64<0x112, 0xf>(v);
+  v += dpp64<0x114, 0xf>(v);
+  v += dpp64<0x118, 0xf>(v);
+  v += dpp64<0x142, 0xa>(v);
+  v += dpp64<0x143, 0xc>(v);
+  return v;
+}
+
+__device__ __forceinline__ u64 lane64(u64 v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return ((u64)hi << 32) | lo;
+}
+
+__device__ __forceinline__ u64 wave_sum(u64 v) { return lane64(wave_scan(v), 63); }
 
 // Sum over the workgroup, the same in every thread.
 template <int NW, class S>
 __device__ __forceinline__ u64 block_sum(u64 v, S& sh) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += (u64)__shfl_xor((unsigned long long)v, off, 64);
+  v = wave_sum(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -286,12 +332,7 @@ __device__ __forceinline__ Sel radix_select(int bits, double target, bool strict
         h[j] = sh.hist[255 - 4 * lane - j];
         s += h[j];
       }
-      u64 run = s;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const u64 o = shfl_up64(run, d);
-        if (lane >= d) run += o;
-      }
+      const u64 run = wave_scan(s);
       const uint64_t hit = __ballot(reached(above + run, target, strict));
       const uint64_t some = __ballot(s != 0);
       // the first lane that reaches it, else the last that holds anything
@@ -346,8 +387,7 @@ __device__ __forceinline__ int64_t locate(const Row<DT>& row, int c0, int c1, Sh
 #pragma unroll
       for (int j = 0; j < VE; ++j) s += amount(e + j, z[j]);
     });
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) s += (u64)__shfl_xor((unsigned long long)s, off, 64);
+    s = wave_sum(s);
     __syncthreads();
     if (lane == 0) sh.wave[wave] = s;
     __syncthreads();
@@ -392,12 +432,7 @@ __device__ __forceinline__ int64_t locate(const Row<DT>& row, int c0, int c1, Sh
 #pragma unroll
       for (int j = 0; j < VE; ++j) q[j] = 0;
     }
-    u64 run = s;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const u64 o = shfl_up64(run, d);
-      if (lane >= d) run += o;
-    }
+    const u64 run = wave_scan(s);
     const uint64_t hit = __ballot(s != 0 && (double)(before + run) > goal);
     const int who = hit ? __builtin_ctzll(hit) : 0;
     if (lane == who) {
@@ -466,15 +501,7 @@ __device__ __forceinline__ BinSel scan_bins(Shared& sh, Amount amount, Target ta
     s += amount(t * kPer + j);
     n += sh.count[t * kPer + j];
   }
-  u64 run = s, cnt = n;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const u64 o = shfl_up64(run, d), c = shfl_up64(cnt, d);
-    if (lane >= d) {
-      run += o;
-      cnt += c;
-    }
-  }
+  const u64 run = wave_scan(s), cnt = wave_scan(n);
   __syncthreads();
   if (lane == 63) {
     sh.wave[wave] = run;
@@ -626,63 +653,55 @@ __device__ __forceinline__ float row_max(const float* seg_max, int n) {
   return __any(nan) ? __builtin_nanf("") : m;
 }
 
-__device__ __forceinline__ u64 wave_sum(u64 v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += (u64)__shfl_xor((unsigned long long)v, off, 64);
-  return v;
-}
-
-// Running sum over the lanes, each with its own share included.
-__device__ __forceinline__ u64 wave_scan(u64 v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const u64 o = shfl_up64(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-
 // The 32 tokens of a thread of a segment: vectors v0, v0 + 256, ... of the row,
-// -inf past its ends.
+// -inf past its ends.  The loads are issued by load() and waited for by get().
 template <int DT>
-__device__ __forceinline__ void load_group(const Row<DT>& row, int v0,
-                                           float (&z)[kGroup / Row<DT>::VE][Row<DT>::VE]) {
+struct Group {
   typedef Row<DT> R;
-  constexpr int kVec = kGroup / R::VE;
-  const int last = v0 + (kVec - 1) * kSegThreads;
-  if (last < (int)((row.V + row.off) / R::VE) && (v0 > 0 || row.off == 0)) {
-    u32x4_t raw[kVec];
+  static constexpr int kVec = kGroup / R::VE;
+  u32x4_t raw[kVec];
+  bool full;
+  __device__ __forceinline__ void load(const R& row, int v0) {
+    const int last = v0 + (kVec - 1) * kThreads;
+    full = last < (int)((row.V + row.off) / R::VE) && (v0 > 0 || row.off == 0);
+    if (full) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j)
-      raw[j] = *reinterpret_cast<const u32x4_t*>(row.base + row.first(v0 + j * kSegThreads) *
-                                                                (DT == 0 ? 4 : 2));
+      for (int j = 0; j < kVec; ++j)
+        raw[j] = *reinterpret_cast<const u32x4_t*>(row.base + row.first(v0 + j * kThreads) *
+                                                                  (DT == 0 ? 4 : 2));
+    }
+  }
+  __device__ __forceinline__ void get(const R& row, int v0, float (&z)[kVec][R::VE]) const {
+    if (full) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) R::unpack(raw[j], z[j]);
-  } else {
+      for (int j = 0; j < kVec; ++j) R::unpack(raw[j], z[j]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (v0 + j * kSegThreads < row.nvec) {
-        row.load(v0 + j * kSegThreads, z[j]);
-      } else {
+      for (int j = 0; j < kVec; ++j) {
+        if (v0 + j * kThreads < row.nvec) {
+          row.load(v0 + j * kThreads, z[j]);
+        } else {
 #pragma unroll
-        for (int q = 0; q < R::VE; ++q) z[j][q] = kNegInf;
+          for (int q = 0; q < R::VE; ++q) z[j][q] = kNegInf;
+        }
       }
     }
   }
-}
+};
 
 // blockIdx.x: row, blockIdx.y: segment.
 template <int DT>
-__global__ __launch_bounds__(kSegThreads) void sample_max_kernel(SampleParams p) {
+__global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleParams p) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
-  __shared__ float sh[kSegThreads / 64];
+  __shared__ float sh[kThreads / 64];
   const int64_t r = blockIdx.x;
   const int seg = blockIdx.y, t = threadIdx.x;
   const R row = row_of<DT>(p, r);
   float z[kVec][R::VE];
-  load_group<DT>(row, seg * (kSegThreads * kVec) + t, z);
+  Group<DT> group;
+  group.load(row, seg * (kThreads * kVec) + t);
+  group.get(row, seg * (kThreads * kVec) + t, z);
   float m = kNegInf;
   bool nan = false;
 #pragma unroll
@@ -692,24 +711,22 @@ __global__ __launch_bounds__(kSegThreads) void sample_max_kernel(SampleParams p)
       m = fmaxf(m, z[j][q]);
       nan |= z[j][q] != z[j][q];
     }
-  p.group_max[(r * p.segs + seg) * kSegThreads + t] = m;
+  p.group_max[(r * p.segs + seg) * kThreads + t] = m;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   if (__any(nan)) m = __builtin_nanf("");
   if ((t & 63) == 0) sh[t >> 6] = m;
   // the row's histogram starts at zero, a share of it per segment
   if (ask_of(p, r).hist(p.V)) {
-    for (int64_t b = seg * kSegThreads + t; b < kBins; b += (int64_t)p.segs * kSegThreads) {
-      p.hist_mass[r * kBins + b] = 0;
-      p.hist_count[r * kBins + b] = 0;
-    }
+    for (int64_t b = seg * kThreads + t; b < kBins; b += (int64_t)p.segs * kThreads)
+      p.hist[r * kBins + b] = 0;
   }
   __syncthreads();
   if (t == 0) {
     bool any = false;
     float s = kNegInf;
 #pragma unroll
-    for (int i = 0; i < kSegThreads / 64; ++i) {
+    for (int i = 0; i < kThreads / 64; ++i) {
       any |= sh[i] != sh[i];
       s = fmaxf(s, sh[i]);
     }
@@ -718,85 +735,73 @@ __global__ __launch_bounds__(kSegThreads) void sample_max_kernel(SampleParams p)
 }
 
 // For rows without filters the segment's mass; for rows that go by the
-// histogram its counts (top-k) or its masses and the whole (top-p).
+// histogram its tokens per bin (top-k), or its mass per bin and in all (top-p).
 // Top-p needs no token lighter than q0 = (1 - p) L / V, L a lower bound on
 // the row's mass (the sum over the segments' maxima): all such tokens together
 // weigh less than (1 - p) of the row, so its p-th part is reached before them.
-// They stay out of the histogram, which keeps most LDS atomics away.
+// They stay out of the histogram, which spares most of the LDS atomics.
 template <int DT>
-__global__ __launch_bounds__(kSegThreads, 4) void sample_mass_kernel(SampleParams p) {
+__global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
-  __shared__ u64 mass[kBins];
-  __shared__ uint32_t count[kBins];
-  __shared__ u64 part[kSegThreads / 64];
+  __shared__ u64 bins[kBins];
+  __shared__ u64 part[kWaves];
   const int64_t r = blockIdx.x;
   const int seg = blockIdx.y, t = threadIdx.x;
   const Ask a = ask_of(p, r);
   const bool plain = a.plain(p.V), hist = a.hist(p.V);
   if (!plain && !hist) return;
+  const R row = row_of<DT>(p, r);
+  const int v0 = seg * (kThreads * kVec) + t;
+  Group<DT> group;
+  group.load(row, v0);
   const float* seg_max = p.seg_max + r * p.segs;
   const float m = row_max(seg_max, p.segs);
   if (!(m > kNegInf)) return;  // no admissible token, or NaN
   const Weights wt = weights_of(p, a, m);
-  const R row = row_of<DT>(p, r);
-  float z[kVec][R::VE];
-  load_group<DT>(row, seg * (kSegThreads * kVec) + t, z);
-  u64 s = 0;
-  if (plain) {
-    if (wt.inf) {
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) s += wt.fixed(z[j / R::VE][j % R::VE] == m ? 1.0 : 0.0);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) s += wt.fixed(wt.real(z[j / R::VE][j % R::VE]));
-    }
-  } else {
-    for (int b = t; b < kBins; b += kSegThreads) {
-      mass[b] = 0;
-      count[b] = 0;
-    }
-    u64 q0 = 0;
+  u64 s = 0, q0 = 0;
+  if (hist) {
+    for (int b = t; b < kBins; b += kThreads) bins[b] = 0;
     if (!a.has_k) {
       u64 low = 0;
       for (int i = t & 63; i < p.segs; i += 64) low += wt.all(seg_max[i]);
       q0 = (u64)((1.0 - a.p) * (double)wave_sum(low) / (double)p.V);
+      q0 = q0 < 1 ? 1 : q0;
     }
     __syncthreads();
-    if (wt.inf || a.has_k) {
+  }
+  float z[kVec][R::VE];
+  group.get(row, v0, z);
+  if (plain && !wt.inf) {
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        const float v = z[j / R::VE][j % R::VE];
-        const u64 q = a.has_k ? 0 : wt.all(v);
-        s += q;
-        if (v != kNegInf && q >= q0) {
-          atomicAdd(&count[bin_of(m, v)], 1u);
-          if (q != 0) atomicAdd(&mass[bin_of(m, v)], q);
-        }
-      }
-    } else {
+    for (int j = 0; j < kGroup; ++j) s += wt.fixed(wt.real(z[j / R::VE][j % R::VE]));
+  } else if (hist && a.has_k) {
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        const float v = z[j / R::VE][j % R::VE];
-        const u64 q = wt.fixed(wt.real(v));
-        s += q;
-        if (q >= q0 && q != 0) {
-          const uint32_t b = bin_of(m, v);
-          atomicAdd(&count[b], 1u);
-          atomicAdd(&mass[b], q);
-        }
-      }
+    for (int j = 0; j < kGroup; ++j) {
+      const float v = z[j / R::VE][j % R::VE];
+      if (v != kNegInf) atomicAdd(&bins[bin_of(m, v)], (u64)1);
     }
+  } else if (!wt.inf) {
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) {
+      const float v = z[j / R::VE][j % R::VE];
+      const u64 q = wt.fixed(wt.real(v));
+      s += q;
+      if (q >= q0) atomicAdd(&bins[bin_of(m, v)], q);
+    }
+  } else {
+    // only the infinite tokens weigh, all in bin 0
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) s += wt.all(z[j / R::VE][j % R::VE]);
+    if (hist && s) atomicAdd(&bins[0], s);
   }
   s = wave_sum(s);
   if ((t & 63) == 0) part[t >> 6] = s;
   __syncthreads();
   if (t == 0) p.seg_sum[r * p.segs + seg] = part[0] + part[1] + part[2] + part[3];
   if (hist) {
-    for (int b = t; b < kBins; b += kSegThreads) {
-      if (count[b]) atomicAdd(&p.hist_count[r * kBins + b], count[b]);
-      if (mass[b]) atomicAdd((u64*)&p.hist_mass[r * kBins + b], mass[b]);
-    }
+    for (int b = t; b < kBins; b += kThreads)
+      if (bins[b]) atomicAdd((u64*)&p.hist[r * kBins + b], bins[b]);
   }
 }
 
@@ -819,111 +824,149 @@ __device__ __forceinline__ u64 ties_needed(u64 above, u64 each, u64 n, double go
   return t < n ? t : n;
 }
 
+template <int DT>
+__device__ __forceinline__ Entry entry_of(const Weights& wt, float z, uint32_t idx) {
+  const double w = wt.weight(z);
+  return Entry{Row<DT>::key(z), idx, wt.fixed(w) | (w >= wt.minp ? kKeptBit : 0)};
+}
+
 // m - z, 0 for z = m also where both are infinite.
 __device__ __forceinline__ float distance(float m, float z) { return z == m ? 0.0f : m - z; }
 
-// f(group, maximum) for this thread's groups of segments g0 .. g0 + 15, their
-// loads in flight together.
-template <class F>
-__device__ __forceinline__ void each_group(const float* gm, int segs, int g0, F f) {
-  float top[kGroupBatch];
+// The maxima of this thread's groups, 16 segments at a time with their loads in
+// flight together; the first 16 stay in registers.
+struct GroupMax {
+  const float* gm;  // (segs, 256) of the row
+  int segs;
+  float first[kGroupBatch];
+  __device__ __forceinline__ void load(int g0, float (&top)[kGroupBatch]) const {
 #pragma unroll
-  for (int i = 0; i < kGroupBatch; ++i)
-    top[i] = g0 + i < segs ? gm[(g0 + i) * kSegThreads + threadIdx.x] : kNegInf;
+    for (int i = 0; i < kGroupBatch; ++i)
+      top[i] = g0 + i < segs ? gm[(g0 + i) * kThreads + threadIdx.x] : kNegInf;
+  }
+  __device__ __forceinline__ void init(const float* p, int n) {
+    gm = p;
+    segs = n;
+    load(0, first);
+  }
+  // f(group, maximum) for the groups of segments g0 .. g0 + 15.
+  template <class F>
+  __device__ __forceinline__ void each(int g0, F f) const {
+    float top[kGroupBatch];
 #pragma unroll
-  for (int i = 0; i < kGroupBatch; ++i)
-    if (top[i] != kNegInf) f(i * kSegThreads + threadIdx.x, top[i]);
-}
+    for (int i = 0; i < kGroupBatch; ++i) top[i] = first[i];
+    if (g0) load(g0, top);
+#pragma unroll
+    for (int i = 0; i < kGroupBatch; ++i)
+      if (top[i] != kNegInf) f(i * kThreads + threadIdx.x, top[i]);
+  }
+};
 
-// Gathers into LDS the tokens with lo <= m - z <= hi, in no order, from the
-// groups whose maximum is within hi: first those groups are listed, then their
-// vectors are dealt over the threads, so that all loads wait together.
-// Returns the number of tokens; above kCap the list is cut off.
+// Gathers into LDS the tokens with m - z <= hi, in no order, from the groups
+// whose maximum is within it: first those groups are listed, then their vectors
+// are dealt over the threads, so that the loads wait together.  Returns the
+// number of tokens; the list is not whole where that is above kCap, or where
+// more than max_groups groups are listed (the number returned is then above
+// kCap as well).
 template <int DT>
-__device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const SampleParams& p,
-                                                  int64_t r, const Weights& wt, float lo, float hi,
-                                                  PickShared& sh) {
+__device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const GroupMax& groups,
+                                                  const Weights& wt, float hi,
+                                                  uint32_t max_groups, PickShared& sh) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
-  const float* gm = p.group_max + r * p.segs * kSegThreads;
   __syncthreads();
   if (threadIdx.x == 0) sh.n = 0;
-  for (int g0 = 0; g0 < p.segs; g0 += kGroupBatch) {
+  for (int g0 = 0; g0 < groups.segs; g0 += kGroupBatch) {
     if (threadIdx.x == 0) sh.n_groups = 0;
     __syncthreads();
-    each_group(gm, p.segs, g0, [&](int i, float top) {
+    groups.each(g0, [&](int i, float top) {
       if (distance(wt.m, top) <= hi) sh.group[atomicAdd(&sh.n_groups, 1u)] = (uint16_t)i;
     });
     __syncthreads();
+    // each listed group holds a token at least
+    if (sh.n_groups > max_groups || sh.n + sh.n_groups > kCap) return kCap + 1;
     const int items = (int)sh.n_groups * kVec;
-    for (int i = threadIdx.x; i < items; i += kSegThreads) {
-      const int g = sh.group[i / kVec];
-      const int v = (g0 + g / kSegThreads) * (kSegThreads * kVec) +
-                    (i % kVec) * kSegThreads + g % kSegThreads;
-      if (v >= row.nvec) continue;
-      float z[R::VE];
-      row.load(v, z);
-      uint32_t in = 0;
+    for (int i0 = threadIdx.x; i0 < items; i0 += kLoads * kThreads) {
+      float z[kLoads][R::VE];
+      int v[kLoads];
 #pragma unroll
-      for (int q = 0; q < R::VE; ++q) {
-        const float d = distance(wt.m, z[q]);
-        in |= (z[q] != kNegInf && d >= lo && d <= hi ? 1u : 0u) << q;
+      for (int l = 0; l < kLoads; ++l) {
+        const int i = i0 + l * kThreads;
+        v[l] = row.nvec;
+        if (i < items) {
+          const int g = sh.group[i / kVec];
+          v[l] = (g0 + g / kThreads) * (kThreads * kVec) + (i % kVec) * kThreads + g % kThreads;
+        }
+        row.load_or_none(v[l], z[l]);
       }
-      while (in) {
-        const int q = __builtin_ctz(in);
-        in &= in - 1;
-        float x = z[0];
 #pragma unroll
-        for (int j = 1; j < R::VE; ++j) x = q == j ? z[j] : x;
-        const uint32_t at = atomicAdd(&sh.n, 1u);
-        if (at < kCap) {
-          const double w = wt.weight(x);
-          sh.list[at] = Entry{R::key(x), (uint32_t)(row.first(v) + q),
-                              wt.fixed(w) | (w >= wt.minp ? kKeptBit : 0)};
+      for (int l = 0; l < kLoads; ++l) {
+        uint32_t in = 0;
+#pragma unroll
+        for (int q = 0; q < R::VE; ++q)
+          in |= (z[l][q] != kNegInf && distance(wt.m, z[l][q]) <= hi ? 1u : 0u) << q;
+        while (in) {
+          const int q = __builtin_ctz(in);
+          in &= in - 1;
+          float x = z[l][0];
+#pragma unroll
+          for (int j = 1; j < R::VE; ++j) x = q == j ? z[l][j] : x;
+          const uint32_t at = atomicAdd(&sh.n, 1u);
+          if (at < kCap)
+            sh.list[at] = Entry{__float_as_uint(x), (uint32_t)(row.first(v[l]) + q), 0};
         }
       }
     }
     __syncthreads();
+    if (sh.n > kCap) return sh.n;
   }
-  return sh.n;
+  // the weights last, when every thread has its share of them
+  const uint32_t n = sh.n;
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+    sh.list[i] = entry_of<DT>(wt, __uint_as_float(sh.list[i].key), sh.list[i].idx);
+  __syncthreads();
+  return n;
 }
 
 struct Drawn {
   int64_t token;
-  u64 total;     // weight of all kept tokens
-  // a threshold without a token: kept are the keys above tau, and the first
-  // `ties` tokens of key tau
-  uint32_t tau;
-  u64 ties;
+  u64 total;  // weight of all kept tokens
+  // the threshold: kept are the keys above tau, and of key tau the tokens up
+  // to index last
+  uint32_t tau, last;
 };
 
 // Draws from the list of candidates, which holds every token the filters can
 // keep; `mass` is the weight that top-p refers to without top-k.  With
-// `threshold` the list holds one bin of the histogram, `above` is the
-// weight before it, and only top-p's threshold is taken.
+// `threshold` the list holds one bin of the histogram, `above` is the weight
+// before it, and only top-p's threshold is taken.
 template <int DT>
 __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int64_t V, uint32_t n,
                                            u64 mass, bool threshold, u64 above, PickShared& sh) {
-  typedef Row<DT> R;
-  constexpr int NW = kSegThreads / 64;
+  constexpr int NW = kWaves;
   const uint32_t t = threadIdx.x;
   Drawn d;
   d.token = 0;
   d.total = 0;
   d.tau = 0;
-  d.ties = 0;
-  if (n <= kSegThreads && !threshold) {
+  d.last = 0xffffffffu;
+  if (n <= kThreads && !threshold) {
     // one candidate per thread: its rank and the weight ranked before it
     const bool mine = t < n;
     const Entry e = mine ? sh.list[t] : Entry{0, 0, 0};
     const u64 q = e.q & ~kKeptBit;
+    // four entries at a time, the last ones filled up with none
+    if (t < 4) sh.list[n + t] = Entry{0, 0xffffffffu, 0};
+    __syncthreads();
     uint32_t rank = 0;
     u64 before = 0;
-    for (uint32_t j = 0; j < n; ++j) {
-      const Entry o = sh.list[j];
-      if (o.key > e.key || (o.key == e.key && o.idx < e.idx)) {
-        ++rank;
-        before += o.q & ~kKeptBit;
+    for (uint32_t j = 0; j < n; j += 4) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const Entry o = sh.list[j + i];
+        const bool better = o.key > e.key || (o.key == e.key && o.idx < e.idx);
+        rank += better;
+        before += better ? o.q & ~kKeptBit : 0;
       }
     }
     bool keep = mine && (!a.has_k || rank < (uint32_t)a.k);
@@ -937,9 +980,12 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
     if (t == 0) sh.out[0] = 0;
     __syncthreads();
     u64 upto = 0;
-    for (uint32_t j = 0; j < n; ++j) {
-      const Entry o = sh.list[j];
-      if (o.idx <= e.idx) upto += o.q;
+    for (uint32_t j = 0; j < n; j += 4) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const Entry o = sh.list[j + i];
+        upto += o.idx <= e.idx ? o.q : 0;
+      }
     }
     const double goal = (double)a.u * (double)d.total;
     // one kept candidate takes the sum across the goal
@@ -950,10 +996,31 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
     return d;
   }
   n = n < kCap ? n : kCap;
+  // keys count from the least one: fewer bits to select by, and the first eight
+  // tell the candidates apart (equal digits queue at one LDS address)
+  uint32_t key0 = 0xffffffffu, key1 = 0;
+  for (uint32_t i = t; i < n; i += kThreads) {
+    key0 = min(key0, sh.list[i].key);
+    key1 = max(key1, sh.list[i].key);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    key0 = min(key0, (uint32_t)__shfl_xor((int)key0, off, 64));
+    key1 = max(key1, (uint32_t)__shfl_xor((int)key1, off, 64));
+  }
+  __syncthreads();
+  if ((t & 63) == 0) sh.wave[t >> 6] = ((u64)key1 << 32) | key0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    key0 = min(key0, (uint32_t)sh.wave[i]);
+    key1 = max(key1, (uint32_t)(sh.wave[i] >> 32));
+  }
+  const int key_bits = key1 > key0 ? 32 - __builtin_clz(key1 - key0) : 1;
+  const int idx_bits = 64 - __builtin_clzll((u64)V);
   u64 ties = ~(u64)0;  // none: no threshold
   uint32_t tau = 0, last = 0xffffffffu;
-  const int idx_bits = 64 - __builtin_clzll((u64)V);
-  for (int stage = threshold ? 1 : 0; stage < (threshold ? 2 : 4); ++stage) {
+  for (int stage = threshold ? 1 : 0; stage < (threshold ? 3 : 4); ++stage) {
     double goal = 0.0;
     if (stage == 0) {  // top-k
       if (!a.has_k || (u64)a.k >= n) continue;
@@ -962,7 +1029,7 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
       if (!a.has_p) continue;
       if (a.has_k) {
         u64 v = 0;
-        for (uint32_t i = t; i < n; i += kSegThreads)
+        for (uint32_t i = t; i < n; i += kThreads)
           if (ties == ~(u64)0 || sh.list[i].key > tau) v += sh.list[i].q & ~kKeptBit;
         mass = block_sum<NW>(v, sh);
         if (ties != ~(u64)0) mass += ties * wt.all(key_value<DT>(tau));
@@ -971,12 +1038,12 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
     } else if (stage == 2) {  // the last tie kept, where not all are
       if (ties == ~(u64)0) continue;
       u64 c = 0;
-      for (uint32_t i = t; i < n; i += kSegThreads) c += sh.list[i].key == tau;
+      for (uint32_t i = t; i < n; i += kThreads) c += sh.list[i].key == tau;
       if (ties >= block_sum<NW>(c, sh)) continue;
       goal = (double)ties;
     } else {  // the token
       u64 v = 0;
-      for (uint32_t i = t; i < n; i += kSegThreads) {
+      for (uint32_t i = t; i < n; i += kThreads) {
         const Entry e = sh.list[i];
         if ((e.q & kKeptBit) && (e.key > tau || (e.key == tau && e.idx <= last)))
           v += e.q & ~kKeptBit;
@@ -984,9 +1051,8 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
       d.total = block_sum<NW>(v, sh);
       goal = (double)a.u * (double)d.total;
     }
-    const Sel s = radix_select(stage < 2 ? R::kKeyBits : idx_bits, goal, stage == 3, sh,
-                               [&](auto f) {
-      for (uint32_t i = t; i < n; i += kSegThreads) {
+    Sel s = radix_select(stage < 2 ? key_bits : idx_bits, goal, stage == 3, sh, [&](auto f) {
+      for (uint32_t i = t; i < n; i += kThreads) {
         const Entry e = sh.list[i];
         const bool in = stage == 0   ? true
                         : stage == 1 ? e.key >= tau
@@ -994,15 +1060,16 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
                                      : (e.q & kKeptBit) &&
                                            (e.key > tau || (e.key == tau && e.idx <= last));
         const u64 w = stage == 1 || stage == 3 ? e.q & ~kKeptBit : (u64)1;
-        if (in) f(stage < 2 ? e.key : (uint32_t)(V - 1 - e.idx), w);
+        if (in) f(stage < 2 ? e.key - key0 : (uint32_t)(V - 1 - e.idx), w);
       }
     });
+    if (stage < 2) s.key += key0;
     if (stage == 0) {
       tau = s.key;
       ties = (u64)a.k - s.above;
     } else if (stage == 1) {
       u64 c = 0;
-      for (uint32_t i = t; i < n; i += kSegThreads) c += sh.list[i].key == s.key;
+      for (uint32_t i = t; i < n; i += kThreads) c += sh.list[i].key == s.key;
       c = block_sum<NW>(c, sh);
       if (s.key == tau && ties < c) c = ties;
       ties = ties_needed(s.above, wt.all(key_value<DT>(s.key)), c, goal);
@@ -1014,8 +1081,72 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
     }
   }
   d.tau = tau;
-  d.ties = ties;
+  d.last = last;
   return d;
+}
+
+// The first token of a segment at which the running sum of amount(index, z),
+// from `before` on, exceeds the goal: 64 consecutive vectors are a chunk; the
+// chunk of the crossing is found from their sums, the vector and the token in
+// it by one wavefront.
+template <int DT, class Amount>
+__device__ __forceinline__ int64_t pick_in_segment(const Row<DT>& row, int seg, u64 before,
+                                                   double goal, Scratch& sh, Amount amount) {
+  typedef Row<DT> R;
+  constexpr int kVec = kGroup / R::VE;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int c0 = seg * (kThreads * kVec);
+  {
+    float z[kVec][R::VE];
+    Group<DT> group;
+    group.load(row, c0 + t);
+    group.get(row, c0 + t, z);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int64_t e = row.first(c0 + t + j * kThreads);
+      u64 s = 0;
+#pragma unroll
+      for (int q = 0; q < R::VE; ++q) s += amount(e + q, z[j][q]);
+      s = wave_sum(s);
+      if (lane == 0) sh.hist[j * kWaves + wave] = s;
+    }
+  }
+  __syncthreads();
+  const u64 mine = lane < kVec * kWaves ? sh.hist[lane] : 0;
+  const u64 run = wave_scan(mine);
+  const uint64_t hit = __ballot(mine != 0 && (double)(before + run) > goal);
+  const int chunk = hit ? __builtin_ctzll(hit) : 0;
+  before += lane64(run - mine, chunk);
+  if (t == 0) sh.out[0] = 0;
+  if (wave == 0) {
+    const int v = c0 + chunk * 64 + lane;
+    u64 w[R::VE], s = 0;
+#pragma unroll
+    for (int q = 0; q < R::VE; ++q) w[q] = 0;
+    if (v < row.nvec) {
+      float z[R::VE];
+      row.load(v, z);
+#pragma unroll
+      for (int q = 0; q < R::VE; ++q) {
+        w[q] = amount(row.first(v) + q, z[q]);
+        s += w[q];
+      }
+    }
+    const u64 upto = before + wave_scan(s);
+    const uint64_t h = __ballot(s != 0 && (double)upto > goal);
+    if (h && lane == __builtin_ctzll(h)) {
+      u64 c = upto - s;
+      int64_t token = -1;
+#pragma unroll
+      for (int q = 0; q < R::VE; ++q) {
+        c += w[q];
+        if (token < 0 && w[q] != 0 && (double)c > goal) token = row.first(v) + q;
+      }
+      sh.out[0] = (u64)token;
+    }
+  }
+  __syncthreads();
+  return (int64_t)sh.out[0];
 }
 
 // The token and its log-probability, by one thread.
@@ -1040,13 +1171,14 @@ __device__ __forceinline__ void write_out(const SampleParams& p, int64_t r, cons
 enum State : uint32_t { kDone = 0, kThreshold = 1, kRow = 2 };
 
 template <int DT>
-__global__ __launch_bounds__(kSegThreads) void sample_pick_kernel(SampleParams p) {
+__global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleParams p) {
   __shared__ PickShared sh;
   typedef Row<DT> R;
-  constexpr int kVec = kGroup / R::VE;
-  constexpr int NW = kSegThreads / 64;
+  constexpr int NW = kWaves;
   const int64_t r = blockIdx.x;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  GroupMax groups;
+  groups.init(p.group_max + r * p.segs * kThreads, p.segs);
   const Ask a = ask_of(p, r);
   const float* seg_max = p.seg_max + r * p.segs;
   const float m = row_max(seg_max, p.segs);
@@ -1080,196 +1212,153 @@ __global__ __launch_bounds__(kSegThreads) void sample_pick_kernel(SampleParams p
       if (hit) {
         const int who = __builtin_ctzll(hit);
         seg = i + who;
-        before += (u64)__shfl((unsigned long long)(run - v), who, 64);
+        before += lane64(run - v, who);
         break;
       }
-      before += (u64)__shfl((unsigned long long)run, 63, 64);
+      before += lane64(run, 63);
     }
-    // 64 consecutive vectors are a chunk; its sum, then the chunk of the crossing
-    auto amount = [&](float z) -> u64 { return a.greedy ? (u64)(z == m) : wt.all(z); };
-    {
-      float z[kVec][R::VE];
-      load_group<DT>(row, seg * (kSegThreads * kVec) + t, z);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        u64 s = 0;
-#pragma unroll
-        for (int q = 0; q < R::VE; ++q) s += amount(z[j][q]);
-        s = wave_sum(s);
-        if (lane == 0) sh.hist[j * NW + wave] = s;
-      }
-    }
-    __syncthreads();
-    const u64 mine = lane < kVec * NW ? sh.hist[lane] : 0;
-    const u64 run = wave_scan(mine);
-    const uint64_t hit = __ballot(mine != 0 && (double)(before + run) > goal);
-    const int chunk = hit ? __builtin_ctzll(hit) : 0;
-    before += (u64)__shfl((unsigned long long)(run - mine), chunk, 64);
-    if (wave == 0) {
-      const int v = seg * (kSegThreads * kVec) + chunk * 64 + lane;
-      u64 w[R::VE], s = 0;
-#pragma unroll
-      for (int q = 0; q < R::VE; ++q) w[q] = 0;
-      if (v < row.nvec) {
-        float z[R::VE];
-        row.load(v, z);
-#pragma unroll
-        for (int q = 0; q < R::VE; ++q) {
-          w[q] = amount(z[q]);
-          s += w[q];
-        }
-      }
-      const u64 upto = before + wave_scan(s);
-      const uint64_t h = __ballot(s != 0 && (double)upto > goal);
-      if (lane == (h ? __builtin_ctzll(h) : 0)) {
-        u64 c = upto - s;
-        int64_t token = -1;
-#pragma unroll
-        for (int q = 0; q < R::VE; ++q) {
-          c += w[q];
-          if (token < 0 && w[q] != 0 && (double)c > goal) token = row.first(v) + q;
-        }
-        write_out<DT>(p, r, row, a, m, token, total);
-      }
-    }
+    const int64_t token = pick_in_segment<DT>(row, seg, before, goal, sh, [&](int64_t, float z) {
+      return a.greedy ? (u64)(z == m) : wt.all(z);
+    });
+    if (t == 0) write_out<DT>(p, r, row, a, m, token, total);
     return;
   }
   // candidates: distances up to hi
-  float lo = 0.0f, hi = __builtin_huge_valf();
-  u64 mass = 0, above = 0;
-  bool threshold = false;
+  float hi = __builtin_huge_valf();
+  u64 mass = 0;
+  SampleState st{kRow, 0.0f, 0.0f, 0, 0, 0};
   if (a.list_all(p.V)) {
-  } else if (a.hist(p.V)) {
-    // the bin where the count or the mass is reached, 8 bins a thread
-    constexpr int kPer = kBins / kSegThreads;
-    const u64* hm = (const u64*)p.hist_mass + r * kBins + t * kPer;
-    const uint32_t* hc = p.hist_count + r * kBins + t * kPer;
-    u64 v = 0, c = 0;
-    for (int j = 0; j < kPer; ++j) {
-      c += hc[j];
-      v += a.has_k ? (u64)hc[j] : hm[j];
+  } else if (a.has_k || a.has_p) {
+    // the bin of the distance where the count or the mass is reached, 8 bins a
+    // thread: of the row's histogram, or of the group maxima (k groups with
+    // maxima of at least the k-th largest hold k tokens as large)
+    constexpr int kPer = kBins / kThreads;
+    u64* bins = reinterpret_cast<u64*>(sh.list);  // the list comes later
+    if (a.hist(p.V)) {
+      for (int i = t; i < kBins; i += kThreads) bins[i] = p.hist[r * kBins + i];
+    } else {
+      for (int i = t; i < kBins; i += kThreads) bins[i] = 0;
+      __syncthreads();
+      for (int g0 = 0; g0 < p.segs; g0 += kGroupBatch)
+        groups.each(g0, [&](int, float g) { atomicAdd(&bins[bin_of(m, g)], (u64)1); });
     }
     if (!a.has_k) {
       for (int i = lane; i < p.segs; i += 64) mass += p.seg_sum[r * p.segs + i];
       mass = wave_sum(mass);
     }
     const double goal = a.has_k ? (double)a.k : a.p * (double)mass;
-    const u64 rv = wave_scan(v), rc = wave_scan(c);
-    if (lane == 63) {
-      sh.wave[wave] = rv;
-      sh.wave2[wave] = rc;
-    }
     if (t == 0) {
       sh.out[0] = kBins - 1;  // never reached: all bins
-      sh.out[1] = sh.out[2] = 0;
+      sh.out[1] = 0;
     }
     __syncthreads();
-    u64 bv = rv - v, bc = rc - c;
-    for (int i = 0; i < wave; ++i) {
-      bv += sh.wave[i];
-      bc += sh.wave2[i];
-    }
-    if (!reached(bv, goal, false) && reached(bv + v, goal, false)) {
+    u64 v = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v += bins[t * kPer + j];
+    const u64 run = wave_scan(v);
+    if (lane == 63) sh.wave[wave] = run;
+    __syncthreads();
+    u64 before = run - v;
+    for (int i = 0; i < wave; ++i) before += sh.wave[i];
+    if (!reached(before, goal, false) && reached(before + v, goal, false)) {
       for (int j = 0; j < kPer; ++j) {
-        const u64 w = a.has_k ? (u64)hc[j] : hm[j];
-        bc += hc[j];
-        if (reached(bv + w, goal, false)) {
+        const u64 w = bins[t * kPer + j];
+        if (reached(before + w, goal, false)) {
           sh.out[0] = t * kPer + j;
-          sh.out[1] = bv;
-          sh.out[2] = bc;
+          sh.out[1] = before;
           break;
         }
-        bv += w;
+        before += w;
       }
     }
     __syncthreads();
     const uint32_t bin = (uint32_t)sh.out[0];
-    const uint32_t n_incl = (uint32_t)sh.out[2];
     // the distances of bin b lie between bits (base + b) << 16 and the next
     if (bin < kBins - 1) hi = __uint_as_float(((kBinBase + bin + 1) << 16) - 1);
-    if (!a.has_k && n_incl > kCap) {
-      threshold = true;
-      above = sh.out[1];
-      if (bin > 0) lo = __uint_as_float((kBinBase + bin) << 16);
+    if (!a.has_k) {
+      st.what = kThreshold;
+      st.lo = bin > 0 ? __uint_as_float((kBinBase + bin) << 16) : 0.0f;
+      st.hi = hi;
+      st.above = sh.out[1];
+      st.mass = mass;
     }
-  } else if (a.has_k) {
-    // k groups with maxima of at least the k-th largest hold k tokens as
-    // large; the upper 16 bits of a key bound well enough
-    const float* gm = p.group_max + r * p.segs * kSegThreads;
-    const Sel s = radix_select(16, (double)a.k, false, sh, [&](auto f) {
-      for (int g0 = 0; g0 < p.segs; g0 += kGroupBatch)
-        each_group(gm, p.segs, g0, [&](int, float g) { f(Row<0>::key(g) >> 16, (u64)1); });
-    });
-    // fewer such groups than k: every token is a candidate
-    if (s.above + s.at >= (u64)a.k) hi = distance(m, key_value<0>(s.key << 16));
   } else {
     // min-p alone: T ln(1 / min_p) and what its rounding may leave out
     hi = (float)(-(double)a.T * log(a.minp) * (1.0 + 1e-6)) + 1e-30f;
     hi += hi * 1e-6f;
+    // nothing but min-p: every token lies before the bin
+    st.what = kThreshold;
+    st.lo = __builtin_huge_valf();
+    st.hi = -1.0f;
   }
-  const uint32_t n = gather_groups<DT>(row, p, r, wt, lo, hi, sh);
+  // rows that other kernels can finish over all segments gather little here
+  const uint32_t n = gather_groups<DT>(row, groups, wt, hi, st.what == kThreshold ? 512 : kCap, sh);
   if (n > kCap) {
-    // min-p alone keeps all it has gathered: no further threshold
-    if (t == 0) {
-      p.state[r].what = !a.has_k && !a.has_p ? kThreshold : kRow;
-      p.state[r].tau = 0;
-      p.state[r].ties = 0;
-    }
+    if (t == 0) p.state[r] = st;
     return;
   }
   if (a.list_all(p.V) && a.has_p && !a.has_k) {
     u64 v = 0;
-    for (uint32_t i = t; i < n; i += kSegThreads) v += sh.list[i].q & ~kKeptBit;
+    for (uint32_t i = t; i < n; i += kThreads) v += sh.list[i].q & ~kKeptBit;
     mass = block_sum<NW>(v, sh);
   }
-  const Drawn d = draw_list<DT>(a, wt, p.V, n, mass, threshold, above, sh);
-  if (t == 0) {
-    if (threshold) {
-      p.state[r].what = kThreshold;
-      p.state[r].tau = d.tau;
-      p.state[r].ties = d.ties;
-    } else {
-      write_out<DT>(p, r, row, a, m, d.token, d.total);
-    }
-  }
+  const Drawn d = draw_list<DT>(a, wt, p.V, n, mass, false, 0, sh);
+  if (t == 0) write_out<DT>(p, r, row, a, m, d.token, d.total);
 }
 
-// Rows with a threshold and no token yet: a segment's kept weight above the
-// threshold's key, and its tokens of that key.
+// Rows whose candidates do not fit in LDS, one segment each: the kept weight of
+// the tokens before the histogram's bin, and the bin's tokens appended to the
+// row's list (over its histogram, which has been read).
 template <int DT>
-__global__ __launch_bounds__(kSegThreads, 4) void sample_kept_kernel(SampleParams p) {
+__global__ __launch_bounds__(kThreads, 4) void sample_kept_kernel(SampleParams p) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
-  __shared__ u64 part[2][kSegThreads / 64];
+  __shared__ u64 part[kWaves];
+  __shared__ uint32_t cnt[kWaves];
+  __shared__ uint32_t base;
   const int64_t r = blockIdx.x;
   if (p.state[r].what != kThreshold) return;
-  const int seg = blockIdx.y, t = threadIdx.x;
+  const int seg = blockIdx.y, t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const Ask a = ask_of(p, r);
+  const R row = row_of<DT>(p, r);
+  const int v0 = seg * (kThreads * kVec) + t;
+  Group<DT> group;
+  group.load(row, v0);
   const float m = row_max(p.seg_max + r * p.segs, p.segs);
   const Weights wt = weights_of(p, a, m);
-  const R row = row_of<DT>(p, r);
-  const uint32_t tau = p.state[r].tau;
+  const float lo = p.state[r].lo, hi = p.state[r].hi;
   float z[kVec][R::VE];
-  load_group<DT>(row, seg * (kSegThreads * kVec) + t, z);
-  u64 s = 0, c = 0;
+  group.get(row, v0, z);
+  u64 s = 0;
+  uint32_t in = 0;  // bit j: token j is in the bin
 #pragma unroll
   for (int j = 0; j < kGroup; ++j) {
-    const float v = z[j / R::VE][j % R::VE];
-    const uint32_t k = R::key(v);
-    if (k > tau) s += wt.kept(v);
-    c += k == tau && v != kNegInf;
+    const float v = z[j / R::VE][j % R::VE], d = distance(m, v);
+    if (d < lo) s += wt.kept(v);
+    in |= (v != kNegInf && d >= lo && d <= hi ? 1u : 0u) << j;
   }
   s = wave_sum(s);
-  c = wave_sum(c);
-  if ((t & 63) == 0) {
-    part[0][t >> 6] = s;
-    part[1][t >> 6] = c;
-  }
+  const uint32_t c = __builtin_popcount(in);
+  const uint32_t run = (uint32_t)wave_scan(c);
+  if (lane == 63) cnt[wave] = run;
+  if (lane == 0) part[wave] = s;
   __syncthreads();
   if (t == 0) {
-    p.seg_sum[r * p.segs + seg] = part[0][0] + part[0][1] + part[0][2] + part[0][3];
-    p.seg_ties[r * p.segs + seg] =
-        (uint32_t)(part[1][0] + part[1][1] + part[1][2] + part[1][3]);
+    p.seg_sum[r * p.segs + seg] = part[0] + part[1] + part[2] + part[3];
+    const uint32_t n = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+    base = n ? atomicAdd(&p.state[r].n, n) : 0;
+  }
+  __syncthreads();
+  uint32_t at = base + run - c;
+  for (int i = 0; i < wave; ++i) at += cnt[i];
+  uint32_t* list = reinterpret_cast<uint32_t*>(p.hist + r * kBins);
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j) {
+    if ((in >> j) & 1u) {
+      if (at < kCap)
+        list[at] = (uint32_t)(row.first(v0 + (j / R::VE) * kThreads) + j % R::VE);
+      ++at;
+    }
   }
 }
 
@@ -1375,67 +1464,74 @@ __device__ __forceinline__ Drawn draw_row(const Row<DT>& row, const Ask& a, cons
 
 template <int DT>
 __global__ __launch_bounds__(kThreads) void sample_rest_kernel(SampleParams p) {
-  __shared__ Shared sh;
+  __shared__ union {
+    PickShared pick;
+    Shared row;
+  } both;
   typedef Row<DT> R;
   const int64_t r = blockIdx.x;
-  const uint32_t what = p.state[r].what;
-  if (what == kDone) return;
+  const SampleState st = p.state[r];
+  if (st.what == kDone) return;
   const Ask a = ask_of(p, r);
   const float m = row_max(p.seg_max + r * p.segs, p.segs);
   const R row = row_of<DT>(p, r);
   const Weights wt = weights_of(p, a, m);
   Drawn d;
-  if (what == kRow) {
-    d = draw_row<DT>(row, a, wt, sh);
+  if (st.what == kRow || st.n > kCap || p.segs > kKeepSegs) {
+    d = draw_row<DT>(row, a, wt, both.row);
   } else {
-    // the segment in which the kept sum crosses; the ties kept are the first
-    // in index order, so a segment has those that the ones before it left
-    const int lane = threadIdx.x & 63;
-    const uint32_t tau = p.state[r].tau;
-    const u64 ties = p.state[r].ties;
-    const u64 each = ties ? wt.kept(key_value<DT>(tau)) : 0;
+    PickShared& sh = both.pick;
+    const int t = threadIdx.x, lane = t & 63;
     const u64* sum = (const u64*)p.seg_sum + r * p.segs;
-    const uint32_t* cnt = p.seg_ties + r * p.segs;
+    const uint32_t* list = reinterpret_cast<const uint32_t*>(p.hist + r * kBins);
+    for (uint32_t i = t; i < st.n; i += kThreads) {
+      const uint32_t idx = list[i];
+      float z;
+      if constexpr (DT == 0)
+        z = reinterpret_cast<const float*>(row.base)[idx] + 0.0f;
+      else
+        z = from_bf16(reinterpret_cast<const uint16_t*>(row.base)[idx]) + 0.0f;
+      sh.list[i] = entry_of<DT>(wt, z, idx);
+    }
+    __syncthreads();
+    d.tau = 0;
+    d.last = 0xffffffffu;
+    if (st.n > 0) d = draw_list<DT>(a, wt, p.V, st.n, st.mass, true, st.above, sh);
+    // what a segment keeps: its sum before the bin and its share of the list
+    __syncthreads();
+    u64* keep = sh.keep;
+    for (int i = t; i < p.segs; i += kThreads) keep[i] = sum[i];
+    __syncthreads();
+    for (uint32_t i = t; i < st.n; i += kThreads) {
+      const Entry e = sh.list[i];
+      if ((e.q & kKeptBit) && (e.key > d.tau || (e.key == d.tau && e.idx <= d.last)))
+        atomicAdd(&keep[(e.idx + (uint32_t)row.off) / kSeg], e.q & ~kKeptBit);
+    }
+    __syncthreads();
     u64 total = 0;
-    for (int i = lane; i < p.segs; i += 64) total += sum[i];
-    total = wave_sum(total) + ties * each;
+    for (int i = lane; i < p.segs; i += 64) total += keep[i];
+    total = wave_sum(total);
     const double goal = (double)a.u * (double)total;
-    u64 before = 0, used = 0, here = 0, all_here = 0;
+    u64 before = 0;
     int seg = 0;
     for (int i = 0; i < p.segs; i += 64) {
-      const bool in = i + lane < p.segs;
-      const u64 c = in ? cnt[i + lane] : 0;
-      const u64 c_before = used + wave_scan(c) - c;
-      const u64 left = ties > c_before ? ties - c_before : 0;
-      const u64 k = left < c ? left : c;
-      const u64 v = (in ? sum[i + lane] : 0) + k * each;
+      const u64 v = i + lane < p.segs ? keep[i + lane] : 0;
       const u64 run = wave_scan(v);
       const uint64_t hit = __ballot(v != 0 && (double)(before + run) > goal);
       if (hit) {
         const int who = __builtin_ctzll(hit);
         seg = i + who;
-        before += (u64)__shfl((unsigned long long)(run - v), who, 64);
-        here = (u64)__shfl((unsigned long long)k, who, 64);
-        all_here = (u64)__shfl((unsigned long long)c, who, 64);
+        before += lane64(run - v, who);
         break;
       }
-      before += (u64)__shfl((unsigned long long)run, 63, 64);
-      used = (u64)__shfl((unsigned long long)(c_before + c), 63, 64);
+      before += lane64(run, 63);
     }
-    constexpr int kSegVec = kSeg / R::VE;
-    const int c0 = seg * kSegVec, c1 = min(c0 + kSegVec, row.nvec);
-    int64_t last = here == all_here ? row.V : -1;
-    u64 part;
-    if (here != 0 && here < all_here)
-      last = locate<DT>(row, c0, c1, sh, 0, [&](u64) { return (double)here - 0.5; }, &part,
-                        [&](int64_t, float z) {
-        return (u64)(z != kNegInf && R::key(z) == tau);
-      });
     d.total = total;
-    d.token = locate<DT>(row, c0, c1, sh, before, [&](u64) { return goal; }, &part,
-                         [&](int64_t i, float z) -> u64 {
+    d.token = pick_in_segment<DT>(row, seg, before, goal, sh, [&](int64_t i, float z) -> u64 {
       const uint32_t k = R::key(z);
-      return k > tau || (k == tau && i <= last) ? wt.kept(z) : 0;
+      return distance(m, z) < st.lo || k > d.tau || (k == d.tau && i <= (int64_t)d.last)
+                 ? wt.kept(z)
+                 : 0;
     });
   }
   if (threadIdx.x == 0) write_out<DT>(p, r, row, a, m, d.token, d.total);
@@ -1457,8 +1553,8 @@ static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t sample_workspace_bytes(int64_t N, int64_t V) {
   const size_t rows = (size_t)N, s = rows * (size_t)segments(V);
-  return 256 + up256(s * kSegThreads * 4) + 2 * up256(s * 4) + up256(s * 8) +
-         up256(rows * kBins * 8) + up256(rows * kBins * 4) + up256(rows * sizeof(SampleState));
+  return 256 + up256(s * kThreads * 4) + up256(s * 4) + up256(s * 8) + up256(rows * kBins * 8) +
+         up256(rows * sizeof(SampleState));
 }
 
 hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
@@ -1482,12 +1578,10 @@ hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
     w += up256(n);
     return at;
   };
-  p.group_max = reinterpret_cast<float*>(take(s * kSegThreads * 4));
+  p.group_max = reinterpret_cast<float*>(take(s * kThreads * 4));
   p.seg_max = reinterpret_cast<float*>(take(s * 4));
-  p.seg_ties = reinterpret_cast<uint32_t*>(take(s * 4));
   p.seg_sum = reinterpret_cast<unsigned long long*>(take(s * 8));
-  p.hist_mass = reinterpret_cast<unsigned long long*>(take(rows * kBins * 8));
-  p.hist_count = reinterpret_cast<uint32_t*>(take(rows * kBins * 4));
+  p.hist = reinterpret_cast<unsigned long long*>(take(rows * kBins * 8));
   p.state = reinterpret_cast<SampleState*>(take(rows * sizeof(SampleState)));
   const dim3 seg_grid((unsigned)N, (unsigned)p.segs);
   // rows of at most kCap tokens are gathered whole; without filters no row has
@@ -1497,13 +1591,13 @@ hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
   if (!rest) p.state = nullptr;
   auto run = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    hipLaunchKernelGGL((sample_max_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);
+    hipLaunchKernelGGL((sample_max_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
     if (mass)
-      hipLaunchKernelGGL((sample_mass_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);
-    hipLaunchKernelGGL((sample_pick_kernel<DT>), dim3((unsigned)N), dim3(kSegThreads), 0, stream,
+      hipLaunchKernelGGL((sample_mass_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((sample_pick_kernel<DT>), dim3((unsigned)N), dim3(kThreads), 0, stream,
                        p);
     if (rest) {
-      hipLaunchKernelGGL((sample_kept_kernel<DT>), seg_grid, dim3(kSegThreads), 0, stream, p);
+      hipLaunchKernelGGL((sample_kept_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
       hipLaunchKernelGGL((sample_rest_kernel<DT>), dim3((unsigned)N), dim3(kThreads), 0, stream,
                          p);
     }

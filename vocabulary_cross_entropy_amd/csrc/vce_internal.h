@@ -227,10 +227,14 @@ hipError_t launch_mx_logits(MxGemmParams p, int x_format, int w_format, int dtyp
 
 // ---- drawing a token -----------------------------------------------------------
 
-// A row that sample_pick_kernel has left to the kernels after it.
+// A row that sample_pick_kernel has left to the kernels after it: the bin of
+// distances lo .. hi that holds its threshold, the weight before the bin, the
+// row's weight, and the number of the bin's tokens listed so far.
 struct SampleState {
-  uint32_t what, tau;
-  unsigned long long ties;
+  uint32_t what;
+  float lo, hi;
+  uint32_t n;
+  unsigned long long above, mass;
 };
 
 struct SampleParams {
@@ -250,10 +254,8 @@ struct SampleParams {
   int segs = 0;                             // segments per row
   float* group_max = nullptr;               // (N, segs, 256)
   float* seg_max = nullptr;                 // (N, segs)
-  uint32_t* seg_ties = nullptr;             // (N, segs)
   unsigned long long* seg_sum = nullptr;    // (N, segs)
-  unsigned long long* hist_mass = nullptr;  // (N, 2048)
-  uint32_t* hist_count = nullptr;           // (N, 2048)
+  unsigned long long* hist = nullptr;       // (N, 2048)
   SampleState* state = nullptr;             // (N), NULL where every row is done in one kernel
 };
 
