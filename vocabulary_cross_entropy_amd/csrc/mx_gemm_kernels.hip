@@ -287,6 +287,498 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxGemmPara
   }
 }
 
+// ---- many tokens: tiles through LDS ---------------------------------------------
+//
+// A workgroup of four wavefronts, two by two, makes 64 NA tokens x 256 rows
+// of W; a wavefront 32 NA x 128 with 32x32 accumulator blocks. K advances in
+// slices of 128 through two LDS stages; every wavefront holds the next two
+// slices of its share in registers (loaded 16 bytes a lane, written to
+// the other stage in steps between matrix instructions), and a slice is two
+// k-steps of 64. The barrier stands early in a slice's second k-step: by then
+// all its operands are in registers and the next slice has been written.
+//
+// LDS rows are K-contiguous (64 bytes a slice in E2M1, 128 in E4M3); the
+// 16-byte chunk c of row r lies at c ^ swizzle(r), so that 16 lanes reading
+// one chunk of 16 consecutive rows meet all banks once.
+//
+// Scales come a superstep of 256 k at a time: 8 bytes of a row, reordered so
+// that lane group g (which gives the scales of the odd or even blocks) reads
+// the bytes of its four k-steps as one dword.
+//
+// Tokens are the instruction's rows and W's rows its columns: a result register
+// then holds 32 consecutive logits of a token across lanes.
+
+constexpr int kTileN = 256;   // rows of W per tile
+constexpr int kSlice = 128;   // k per slice
+constexpr int kTileThreads = 256;
+constexpr uint32_t kOutOfRange = 0x80000000u;  // a buffer offset that reads as 0
+
+#define MX_LDS __attribute__((address_space(3)))
+
+template <int FMT>
+struct SliceOf {
+  static constexpr int kRowBytes = FMT == kMxE4M3 ? 128 : 64;  // of a slice
+  static constexpr int kChunks = kRowBytes / 16;
+  static __device__ __forceinline__ int swizzle(int r) {
+    return FMT == kMxE4M3 ? (r >> 1) & 7 : (r >> 2) & 3;
+  }
+};
+
+// Moves an operand's ROWS x 128 slices in units of 1 KB: UNITS per
+// wavefront, 64 / kChunks rows each.
+template <int FMT, int ROWS>
+struct MxLoader {
+  typedef SliceOf<FMT> S;
+  static constexpr int kRowsPerUnit = 64 / S::kChunks;
+  static constexpr int kUnits = ROWS / kRowsPerUnit / 4;
+  const uint8_t* base;  // the tile's first row
+  int64_t bytes;        // of the tile's rows that exist
+  int64_t row_bytes;    // a row's
+  uint32_t voff;        // this lane's offset in unit 0
+  uint32_t ustep;       // between units
+  int chunk;
+  int lds;              // of this lane's 16 bytes of unit 0 in a stage
+  __device__ __forceinline__ void init(const uint8_t* q, int64_t rb, int64_t r0, int64_t rows,
+                                       int wave, int lane) {
+    base = q + r0 * rb;
+    row_bytes = rb;
+    const int64_t n = rows - r0 < ROWS ? rows - r0 : ROWS;
+    bytes = n * rb;
+    const int row0 = wave * kUnits * kRowsPerUnit + lane / S::kChunks;
+    chunk = lane % S::kChunks;
+    lds = row0 * S::kRowBytes + (chunk ^ S::swizzle(row0)) * 16;
+    voff = (uint32_t)(row0 * rb + chunk * 16);
+    ustep = (uint32_t)(kRowsPerUnit * rb);
+  }
+  // Unit u of slice k.  Rows past the end lie past the buffer; with MASK so do
+  // chunks past K.
+  template <bool MASK>
+  __device__ __forceinline__ u32x4_t get(int k, int u) const {
+    const int64_t at = (int64_t)k * S::kRowBytes;
+    const int64_t left = bytes - at;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(base + at), (short)0, left < 0 ? 0 : (int)left, 0x00020000);
+    uint32_t o = voff;
+    if (MASK && at + chunk * 16 >= row_bytes) o = kOutOfRange;
+    return __builtin_bit_cast(u32x4_t,
+                              __builtin_amdgcn_raw_buffer_load_b128(rs, o, (int)(u * ustep), 0));
+  }
+  // A unit on is 8 rows of E4M3, which turns bit 2 of the swizzle, or 16 of E2M1,
+  // which leaves it.
+  __device__ __forceinline__ void put(uint8_t MX_LDS* stage, int u, const u32x4_t& v) const {
+    const int at = FMT == kMxE4M3 && (u & 1) ? lds ^ 64 : lds;
+    *reinterpret_cast<u32x4_t MX_LDS*>(stage + at + u * 1024) = v;
+  }
+};
+
+// A lane's registers of a 32-row fragment: 16 or 32 bytes.
+template <int FMT>
+struct FragOf {
+  typedef i32x8_t T;
+  static __device__ __forceinline__ i32x8_t full(const T& f) { return f; }
+};
+template <>
+struct FragOf<kMxE2M1> {
+  typedef i32x4_t T;
+  // the instruction reads four registers of an E2M1 operand
+  static __device__ __forceinline__ i32x8_t full(const T& f) {
+    return __builtin_shufflevector(f, f, 0, 1, 2, 3, -1, -1, -1, -1);
+  }
+};
+
+// Reads an operand's fragments: 32 rows from row0 (a multiple of 32), one a
+// lane.  kScaled takes E4M3 in the scaled instruction's halves, kBf16 a whole
+// block per lane group.  A lane's addresses differ by XORs of one.
+template <int FMT, int MODE>
+struct MxReader {
+  typedef SliceOf<FMT> S;
+  int at;
+  __device__ __forceinline__ void init(int row0, int c, int g) {
+    const int first = FMT == kMxE4M3 && MODE == kBf16 ? 2 * g : g;
+    at = (row0 + c) * S::kRowBytes + ((first ^ S::swizzle(c)) * 16);
+  }
+  // Rows 32 i on, k-step ks of the slice.
+  __device__ __forceinline__ typename FragOf<FMT>::T get(const uint8_t MX_LDS* stage, int i,
+                                                         int ks) const {
+    const uint8_t MX_LDS* rows = stage + i * 32 * S::kRowBytes;
+    if constexpr (FMT == kMxE4M3) {
+      const int o = at ^ (ks * 64);
+      const int o2 = o ^ (MODE == kScaled ? 32 : 16);
+      const i32x4_t a = *reinterpret_cast<const i32x4_t MX_LDS*>(rows + o);
+      const i32x4_t b = *reinterpret_cast<const i32x4_t MX_LDS*>(rows + o2);
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      return *reinterpret_cast<const i32x4_t MX_LDS*>(rows + (at ^ (ks * 32)));
+    }
+  }
+};
+
+// Values 8 t .. 8 t + 7 of a kBf16 fragment as BF16, scale byte b applied.
+template <int FMT>
+__device__ __forceinline__ bf16x8_t mx_widen(const typename FragOf<FMT>::T& f, uint32_t sc, int b,
+                                             int t) {
+  const float s = __uint_as_float(((sc >> (8 * b)) & 255u) << 23);
+  bf16x2_t r[4];
+  if constexpr (FMT == kMxE4M3) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      r[2 * j] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[2 * t + j], s, false);
+      r[2 * j + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[2 * t + j], s, true);
+    }
+  } else {
+    r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)f[t], s, 0);
+    r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)f[t], s, 1);
+    r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)f[t], s, 2);
+    r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)f[t], s, 3);
+  }
+  return __builtin_shufflevector(__builtin_shufflevector(r[0], r[1], 0, 1, 2, 3),
+                                 __builtin_shufflevector(r[2], r[3], 0, 1, 2, 3), 0, 1, 2, 3, 4,
+                                 5, 6, 7);
+}
+
+template <int FA, int FB>
+__device__ __forceinline__ f32x16_t mfma32(const i32x8_t& a, const i32x8_t& b, const f32x16_t& c,
+                                           uint32_t sa, uint32_t sb, int s) {
+  constexpr int ca = Fmt<FA>::kCode, cb = Fmt<FB>::kCode;
+  switch (s) {
+    case 0:
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, ca, cb, 0, sa, 0, sb);
+    case 1:
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, ca, cb, 1, sa, 1, sb);
+    case 2:
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, ca, cb, 2, sa, 2, sb);
+    default:
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, ca, cb, 3, sa, 3, sb);
+  }
+}
+
+// The 8 scale bytes of a row's superstep: bytes 0, 2, 4, 6 and 1, 3, 5, 7 as two
+// dwords; 127 for blocks past K (their values are zeros).
+__device__ __forceinline__ u32x2_t mx_scales8(const uint8_t* row, int ss, int nblk) {
+  uint32_t lo = 0x7f7f7f7fu, hi = 0x7f7f7f7fu;
+  const int b = ss * 8;
+  if (b + 8 <= nblk) {
+    __builtin_memcpy(&lo, row + b, 4);
+    __builtin_memcpy(&hi, row + b + 4, 4);
+  } else {
+    for (int j = 0; j < 8 && b + j < nblk; ++j) {
+      uint32_t& w = j < 4 ? lo : hi;
+      w = (w & ~(255u << (8 * (j % 4)))) | ((uint32_t)row[b + j] << (8 * (j % 4)));
+    }
+  }
+  // v_perm: selector bytes 0..3 take from the second argument, 4..7 from the first
+  return u32x2_t{__builtin_amdgcn_perm(hi, lo, 0x06040200u),
+                 __builtin_amdgcn_perm(hi, lo, 0x07050301u)};
+}
+
+template <int FX, int FW, int MODE, int NA>
+struct MxTile {
+  static constexpr int kTileM = 64 * NA;
+  static constexpr int NB = 4;
+  typedef MxLoader<FX, kTileM> LX;
+  typedef MxLoader<FW, kTileN> LW;
+  static constexpr int kXBytes = kTileM * SliceOf<FX>::kRowBytes;
+  static constexpr int kWBytes = kTileN * SliceOf<FW>::kRowBytes;
+  static constexpr int kUnits = LX::kUnits + LW::kUnits;
+  static constexpr int kScaleBytes = (kTileM + kTileN) * 8;  // of a superstep
+  static constexpr int kSmem = 2 * (kXBytes + kWBytes + kScaleBytes);
+
+  f32x16_t acc[NA][NB];
+  typename FragOf<FX>::T fa[NA];
+  typename FragOf<FW>::T fb[2][NB];
+  uint32_t sa[NA], sb[NB];
+  // slices in flight in registers: two, but one beside 256 accumulators and E4M3
+  // fragments (two took 170 to 220 registers too many)
+  static constexpr int kBuf = NA == 4 && (FX == kMxE4M3 || FW == kMxE4M3) ? 1 : 2;
+  u32x4_t r[kBuf][kUnits];
+  u32x2_t scx, scw;  // the next superstep's scales of row threadIdx.x of either operand
+
+  LX lx;
+  LW lw;
+  MxReader<FX, MODE> rx;
+  MxReader<FW, MODE> rw;
+  const uint8_t *xsr, *wsr;
+  int nblk, wm, wn, c, g;
+  int asx, asw;  // this lane's first scale dword of a superstep
+  uint8_t MX_LDS* smem;
+
+  __device__ __forceinline__ uint8_t MX_LDS* xs(int st) const { return smem + st * kXBytes; }
+  __device__ __forceinline__ uint8_t MX_LDS* ws(int st) const {
+    return smem + 2 * kXBytes + st * kWBytes;
+  }
+  __device__ __forceinline__ uint8_t MX_LDS* sx(int st) const {
+    return smem + 2 * (kXBytes + kWBytes) + st * kScaleBytes;
+  }
+  __device__ __forceinline__ uint8_t MX_LDS* sw(int st) const { return sx(st) + kTileM * 8; }
+
+  template <bool MASK>
+  __device__ __forceinline__ u32x4_t get(int k, int u) const {
+    return u < LX::kUnits ? lx.template get<MASK>(k, u) : lw.template get<MASK>(k, u - LX::kUnits);
+  }
+  __device__ __forceinline__ void put(int st, int u, const u32x4_t& v) const {
+    if (u < LX::kUnits)
+      lx.put(xs(st), u, v);
+    else
+      lw.put(ws(st), u - LX::kUnits, v);
+  }
+  __device__ __forceinline__ void load_scales(int ss) {
+    if (xsr) scx = mx_scales8(xsr, ss, nblk);
+    if (wsr) scw = mx_scales8(wsr, ss, nblk);
+  }
+  __device__ __forceinline__ void put_scales(int st) const {
+    if ((int)threadIdx.x < kTileM)
+      *reinterpret_cast<u32x2_t MX_LDS*>(sx(st) + threadIdx.x * 8) = scx;
+    *reinterpret_cast<u32x2_t MX_LDS*>(sw(st) + threadIdx.x * 8) = scw;
+  }
+  __device__ __forceinline__ void get_scales(int st) {
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+      sa[a] = *reinterpret_cast<const uint32_t MX_LDS*>(sx(st) + asx + 256 * a);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      sb[b] = *reinterpret_cast<const uint32_t MX_LDS*>(sw(st) + asw + 256 * b);
+  }
+  __device__ __forceinline__ typename FragOf<FX>::T frag_x(int st, int a, int ks) const {
+    return rx.get(xs(st), a, ks);
+  }
+  __device__ __forceinline__ typename FragOf<FW>::T frag_w(int st, int b, int ks) const {
+    return rw.get(ws(st), b, ks);
+  }
+
+  // Slice k, of parity P (its data in stage P, its first k-step's fragments in fa
+  // and fb[0]).  Slice k + 1 waits in registers; it goes to the other stage before
+  // the barrier, and its buffer is refilled with slice k + 1 + kBuf.
+  template <int P, bool MASK>
+  __device__ __forceinline__ void slice(int k, int klast) {
+    const int next = MASK || k + 1 + kBuf < klast ? k + 1 + kBuf : klast;
+    constexpr int B = kBuf == 2 ? P ^ 1 : 0;
+    if (P == 0) load_scales(k / 2 + 1);
+    uint32_t na[NA], nb[NB];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int a = 0; a < NA; ++a) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int m = a * NB + b;
+          if (ks == 1 && m == 2) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            if (P == 1) {
+              // the next superstep's scales, beside those still in use
+#pragma unroll
+              for (int i = 0; i < NA; ++i)
+                na[i] = *reinterpret_cast<const uint32_t MX_LDS*>(
+                    sx((k / 2 + 1) & 1) + asx + 256 * i);
+#pragma unroll
+              for (int i = 0; i < NB; ++i)
+                nb[i] = *reinterpret_cast<const uint32_t MX_LDS*>(
+                    sw((k / 2 + 1) & 1) + asw + 256 * i);
+            }
+          }
+          if constexpr (MODE == kScaled) {
+            acc[a][b] = mfma32<FX, FW>(FragOf<FX>::full(fa[a]), FragOf<FW>::full(fb[ks][b]),
+                                       acc[a][b], sa[a], sb[b], 2 * P + ks);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  mx_widen<FX>(fa[a], sa[a], 2 * P + ks, t),
+                  mx_widen<FW>(fb[ks][b], sb[b], 2 * P + ks, t), acc[a][b], 0, 0, 0);
+          }
+          // the next k-step's fragments: W's behind the second instruction (the
+          // third, behind the barrier), X's as theirs die
+          if (m == (ks == 1 ? 2 : 1)) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+              fb[ks ^ 1][i] = ks == 0 ? frag_w(P, i, 1) : frag_w(P ^ 1, i, 0);
+          }
+          if (b == NB - 1) fa[a] = ks == 0 ? frag_x(P, a, 1) : frag_x(P ^ 1, a, 0);
+          // writes and refills in the first k-step and up to the barrier
+          if (ks == 0) {
+            constexpr int kSteps = NA * NB;
+#pragma unroll
+            for (int u = m * kUnits / kSteps; u < (m + 1) * kUnits / kSteps; ++u) {
+              put(P ^ 1, u, r[B][u]);
+              r[B][u] = get<MASK>(next, u);
+            }
+            if (P == 1 && m == kSteps - 1) put_scales((k / 2 + 1) & 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    if (P == 1) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i) sa[i] = na[i];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) sb[i] = nb[i];
+    }
+  }
+
+  template <bool MASK>
+  __device__ __forceinline__ void run(const MxGemmParams& p, int64_t m0, int64_t v0,
+                                      uint8_t MX_LDS* sm) {
+    smem = sm;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    wm = (wave >> 1) * 32 * NA;
+    wn = (wave & 1) * 128;
+    c = lane & 31;
+    g = lane >> 5;
+    rx.init(wm, c, g);
+    rw.init(wn, c, g);
+    asx = (wm + c) * 8 + 4 * g;
+    asw = (wn + c) * 8 + 4 * g;
+    nblk = (int)(p.K / kMxBlock);
+    lx.init(p.x, (int64_t)nblk * Fmt<FX>::kBlockBytes, m0, p.M, wave, lane);
+    lw.init(p.w, (int64_t)nblk * Fmt<FW>::kBlockBytes, v0, p.V, wave, lane);
+    const int t = threadIdx.x;
+    xsr = t < kTileM && m0 + t < p.M ? p.xs + (m0 + t) * nblk : nullptr;
+    wsr = v0 + t < p.V ? p.ws + (v0 + t) * nblk : nullptr;
+    scx = scw = u32x2_t{0x7f7f7f7fu, 0x7f7f7f7fu};
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[a][b] = f32x16_t{};
+    // an even number of slices; those past K are zeros
+    const int klast = (int)((p.K + kSlice - 1) / kSlice) - 1;
+    const int nk = (klast + 2) / 2 * 2;
+    load_scales(0);
+    // slice 0 to its stage, the next ones into the buffers
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) r[0][u] = get<MASK>(0, u);
+    if constexpr (kBuf == 2) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) r[1][u] = get<MASK>(MASK || klast >= 1 ? 1 : klast, u);
+    }
+    put_scales(0);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      put(0, u, r[0][u]);
+      r[0][u] = get<MASK>(MASK || klast >= kBuf ? kBuf : klast, u);
+    }
+    __syncthreads();
+    get_scales(0);
+#pragma unroll
+    for (int a = 0; a < NA; ++a) fa[a] = frag_x(0, a, 0);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) fb[0][b] = frag_w(0, b, 0);
+#pragma unroll 1
+    for (int k = 0; k < nk; k += 2) {
+      slice<0, MASK>(k, klast);
+      slice<1, MASK>(k + 1, klast);
+    }
+  }
+
+  // Register q of block (a, b) holds token m0 + wm + 32 a + 8 (q / 4) + 4 g + q % 4,
+  // row v0 + wn + 32 b + c of W.
+  template <int DT>
+  __device__ __forceinline__ void store(const MxGemmParams& p, int64_t m0, int64_t v0) const {
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+#pragma unroll
+      for (int q = 0; q < 16; q += 2) {
+        const int64_t m = m0 + wm + 32 * a + 8 * (q / 4) + 4 * g + q % 4;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int64_t v = v0 + wn + 32 * b + c;
+          const float x = acc[a][b][q] * p.scale, y = acc[a][b][q + 1] * p.scale;
+          if constexpr (DT == 0) {
+            float* o = static_cast<float*>(p.out) + m * p.ldo + v;
+            if (v < p.V && m < p.M) *o = x;
+            if (v < p.V && m + 1 < p.M) o[p.ldo] = y;
+          } else {
+            // lanes pair up: the even one stores two logits of token m, the odd
+            // one two of token m + 1
+            const float xo = __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+                0, (int)__float_as_uint(x), 0xb1, 0xf, 0xf, true));
+            const float yo = __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+                0, (int)__float_as_uint(y), 0xb1, 0xf, 0xf, true));
+            const bool odd = c & 1;
+            const uint32_t w = odd ? pack_bf16x2(yo, y) : pack_bf16x2(x, xo);
+            const int64_t mm = m + odd, vv = v - odd;
+            uint16_t* o = static_cast<uint16_t*>(p.out) + mm * p.ldo + vv;
+            if (mm < p.M) {
+              if (vv + 1 < p.V)
+                __builtin_memcpy(o, &w, 4);
+              else if (vv < p.V)
+                *o = (uint16_t)w;
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+// Is a scale of these rows of an operand outside 2^-63 .. 2^64?
+__device__ __forceinline__ bool mx_far_row(const uint8_t* row, int nblk) {
+  uint32_t far = 0;
+  int b = 0;
+  for (; b + 4 <= nblk; b += 4) {
+    uint32_t w;
+    __builtin_memcpy(&w, row + b, 4);
+    far |= ~(w ^ (w << 1)) & 0x80808080u;
+  }
+  for (; b < nblk; ++b) far |= (uint32_t)row[b] - 64u > 127u;
+  return far != 0;
+}
+
+// Workgroup number -> tile: workgroups go round-robin over the 8 XCDs, so each
+// XCD gets a contiguous range of tiles, walked in bands of 8 token tiles.
+__device__ __forceinline__ void mx_tile_of(int64_t b, int64_t n_ti, int64_t n_tj, int64_t* ti,
+                                           int64_t* tj) {
+  const int64_t n = n_ti * n_tj, q = n >> 3, rem = n & 7;
+  const int64_t x = b & 7, slot = b >> 3;
+  const int64_t t = x * q + (x < rem ? x : rem) + slot;
+  const int64_t band = t / (8 * n_tj), in = t - band * 8 * n_tj;
+  const int64_t left = n_ti - band * 8, w = left < 8 ? left : 8;
+  *ti = band * 8 + in % w;
+  *tj = in / w;
+}
+
+template <int FX, int FW, int MODE, int NA, int DT, bool MASK>
+__global__ __launch_bounds__(kTileThreads, NA == 1 ? 2 : 1) void mx_tile_kernel(MxGemmParams p) {
+  typedef MxTile<FX, FW, MODE, NA> T;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kSmem];
+  const int64_t n_ti = (p.M + T::kTileM - 1) / T::kTileM, n_tj = (p.V + kTileN - 1) / kTileN;
+  int64_t ti, tj;
+  mx_tile_of(blockIdx.x, n_ti, n_tj, &ti, &tj);
+  const int64_t m0 = ti * T::kTileM, v0 = tj * kTileN;
+  uint8_t MX_LDS* sm = (uint8_t MX_LDS*)smem;
+  if constexpr (MODE == kBf16) {
+    // scales that BF16 operands may not carry: the scaled instructions instead
+    const int t = threadIdx.x, nblk = (int)(p.K / kMxBlock);
+    bool far = v0 + t < p.V && mx_far_row(p.ws + (v0 + t) * nblk, nblk);
+    if (t < T::kTileM && m0 + t < p.M) far |= mx_far_row(p.xs + (m0 + t) * nblk, nblk);
+    if (__syncthreads_or(far)) {
+      MxTile<FX, FW, kScaled, NA> s;
+      s.template run<MASK>(p, m0, v0, sm);
+      s.template store<DT>(p, m0, v0);
+      return;
+    }
+  }
+  T s;
+  s.template run<MASK>(p, m0, v0, sm);
+  s.template store<DT>(p, m0, v0);
+}
+
+template <int FX, int FW, int MODE, int NA, int DT>
+hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
+  const int64_t n = ((p.M + 64 * NA - 1) / (64 * NA)) * ((p.V + kTileN - 1) / kTileN);
+  if (n > ((int64_t)1 << 23)) return hipErrorInvalidValue;
+  if (p.K % (2 * kSlice) == 0)
+    hipLaunchKernelGGL((mx_tile_kernel<FX, FW, MODE, NA, DT, false>), dim3((unsigned)n),
+                       dim3(kTileThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((mx_tile_kernel<FX, FW, MODE, NA, DT, true>), dim3((unsigned)n),
+                       dim3(kTileThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
 template <int FX, int FW, int DT>
 hipError_t launch_skinny(const MxGemmParams& p, hipStream_t stream) {
   constexpr int MODE = DT == 0 && (FX == kMxE4M3 || FW == kMxE4M3) ? kBf16 : kScaled;
@@ -295,12 +787,13 @@ hipError_t launch_skinny(const MxGemmParams& p, hipStream_t stream) {
   hipLaunchKernelGGL((mx_skinny_kernel<FX, FW, MODE, NB, DT>),                                    \
                      dim3(gx, (unsigned)((p.M + 16 * NB - 1) / (16 * NB))),                 \
                      dim3(kSkinnyThreads), 0, stream, p)
+  if (p.M > 128) return launch_tile<FX, FW, MODE, 4, DT>(p, stream);
+  if (p.M > 64) return launch_tile<FX, FW, MODE, 2, DT>(p, stream);
+  if (p.M > 32) return launch_tile<FX, FW, MODE, 1, DT>(p, stream);
   if (p.M <= 16)
     VCE_SKINNY(1);
-  else if (p.M <= 32)
-    VCE_SKINNY(2);
   else
-    VCE_SKINNY(4);
+    VCE_SKINNY(2);
 #undef VCE_SKINNY
   return hipGetLastError();
 }
