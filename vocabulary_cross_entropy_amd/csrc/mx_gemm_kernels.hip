@@ -452,13 +452,15 @@ __device__ __forceinline__ f32x16_t mfma32(const i32x8_t& a, const i32x8_t& b, c
   }
 }
 
-// The 8 scale bytes of a row's superstep: bytes 0, 2, 4, 6 and 1, 3, 5, 7 as two
-// dwords; 127 for blocks past K (their values are zeros).
+// The 8 scale bytes of a row's superstep, 127 for blocks past K (their values
+// are zeros).  Without MASK K is a multiple of 256, so all 8 are there.
+template <bool MASK>
 __device__ __forceinline__ u32x2_t mx_scales8(const uint8_t* row, int ss, int nblk) {
-  uint32_t lo = 0x7f7f7f7fu, hi = 0x7f7f7f7fu;
   const int b = ss * 8;
+  if (!MASK) return *reinterpret_cast<const u32x2_t*>(row + b);
+  uint32_t lo = 0x7f7f7f7fu, hi = 0x7f7f7f7fu;
   if (b + 8 <= nblk) {
-    __builtin_memcpy(&lo, row + b, 4);
+    __builtin_memcpy(&lo, row + b, 4);  // rows lie at any byte
     __builtin_memcpy(&hi, row + b + 4, 4);
   } else {
     for (int j = 0; j < 8 && b + j < nblk; ++j) {
@@ -466,9 +468,14 @@ __device__ __forceinline__ u32x2_t mx_scales8(const uint8_t* row, int ss, int nb
       w = (w & ~(255u << (8 * (j % 4)))) | ((uint32_t)row[b + j] << (8 * (j % 4)));
     }
   }
-  // v_perm: selector bytes 0..3 take from the second argument, 4..7 from the first
-  return u32x2_t{__builtin_amdgcn_perm(hi, lo, 0x06040200u),
-                 __builtin_amdgcn_perm(hi, lo, 0x07050301u)};
+  return u32x2_t{lo, hi};
+}
+
+// Bytes 0, 2, 4, 6 and 1, 3, 5, 7 as two dwords (v_perm: selector bytes 0..3 take
+// from the second argument, 4..7 from the first).
+__device__ __forceinline__ u32x2_t mx_deal8(const u32x2_t& w) {
+  return u32x2_t{__builtin_amdgcn_perm(w[1], w[0], 0x06040200u),
+                 __builtin_amdgcn_perm(w[1], w[0], 0x07050301u)};
 }
 
 template <int FX, int FW, int MODE, int NA>
@@ -521,14 +528,16 @@ struct MxTile {
     else
       lw.put(ws(st), u - LX::kUnits, v);
   }
+  // Only loads; they are dealt when they are written, two slices later.
+  template <bool MASK>
   __device__ __forceinline__ void load_scales(int ss) {
-    if (xsr) scx = mx_scales8(xsr, ss, nblk);
-    if (wsr) scw = mx_scales8(wsr, ss, nblk);
+    scx = mx_scales8<MASK>(xsr, ss, nblk);
+    scw = mx_scales8<MASK>(wsr, ss, nblk);
   }
   __device__ __forceinline__ void put_scales(int st) const {
-    if ((int)threadIdx.x < kTileM)
-      *reinterpret_cast<u32x2_t MX_LDS*>(sx(st) + threadIdx.x * 8) = scx;
-    *reinterpret_cast<u32x2_t MX_LDS*>(sw(st) + threadIdx.x * 8) = scw;
+    if (kTileM >= kTileThreads || (int)threadIdx.x < kTileM)
+      *reinterpret_cast<u32x2_t MX_LDS*>(sx(st) + threadIdx.x * 8) = mx_deal8(scx);
+    *reinterpret_cast<u32x2_t MX_LDS*>(sw(st) + threadIdx.x * 8) = mx_deal8(scw);
   }
   __device__ __forceinline__ void get_scales(int st) {
 #pragma unroll
@@ -552,7 +561,7 @@ struct MxTile {
   __device__ __forceinline__ void slice(int k, int klast) {
     const int next = MASK || k + 1 + kBuf < klast ? k + 1 + kBuf : klast;
     constexpr int B = kBuf == 2 ? P ^ 1 : 0;
-    if (P == 0) load_scales(k / 2 + 1);
+    if (P == 0) load_scales<MASK>(min(k / 2 + 1, klast / 2));
     uint32_t na[NA], nb[NB];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
@@ -636,9 +645,10 @@ struct MxTile {
     lx.init(p.x, (int64_t)nblk * Fmt<FX>::kBlockBytes, m0, p.M, wave, lane);
     lw.init(p.w, (int64_t)nblk * Fmt<FW>::kBlockBytes, v0, p.V, wave, lane);
     const int t = threadIdx.x;
-    xsr = t < kTileM && m0 + t < p.M ? p.xs + (m0 + t) * nblk : nullptr;
-    wsr = v0 + t < p.V ? p.ws + (v0 + t) * nblk : nullptr;
-    scx = scw = u32x2_t{0x7f7f7f7fu, 0x7f7f7f7fu};
+    // rows past the end take the last one's scales (their values are zeros, and
+    // their results are not stored)
+    xsr = p.xs + min(m0 + t, p.M - 1) * nblk;
+    wsr = p.ws + min(v0 + t, p.V - 1) * nblk;
 #pragma unroll
     for (int a = 0; a < NA; ++a)
 #pragma unroll
@@ -646,7 +656,7 @@ struct MxTile {
     // an even number of slices; those past K are zeros
     const int klast = (int)((p.K + kSlice - 1) / kSlice) - 1;
     const int nk = (klast + 2) / 2 * 2;
-    load_scales(0);
+    load_scales<MASK>(0);
     // slice 0 to its stage, the next ones into the buffers
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) r[0][u] = get<MASK>(0, u);
