@@ -25,8 +25,6 @@
 // to lane group g in either format, eight values of it to each of four
 // 16x16x32 instructions.
 //
-// Few tokens: W is read once and bounds the time.  Each wavefront keeps 64 rows of W
-// against 16 NB tokens and reads both straight into registers.
 #include <type_traits>
 
 #include "mx_device.h"
@@ -39,8 +37,6 @@ namespace {
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kRowsPerWave = 64;     // of W
-constexpr int kFrags = kRowsPerWave / 16;
 constexpr int kSkinnyThreads = 256;
 
 enum Mode { kScaled, kBf16 };
@@ -190,100 +186,111 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const f32x4_t& v, 
   }
 }
 
-// blockIdx.x: 256 rows of W (64 per wavefront), blockIdx.y: 16 NB tokens.
-template <int FX, int FW, int MODE, int NB, int DT>
+// Up to 16 tokens: every wavefront takes kRows rows of W.  W is read
+// once, 16 bytes a lane straight into operand registers, a superstep ahead of
+// the one being multiplied: with four wavefronts' worth of a superstep waited for
+// and used at once the loads stood still (121 us at 1 x 4096 x 131072 against 53).
+template <int FX, int FW, int MODE>
+struct Skinny {
+  static constexpr int kFrags = FW == kMxE2M1 ? 4 : 2;
+  static constexpr int kRows = 16 * kFrags;
+};
+
+template <int FX, int FW, int MODE, int DT>
 __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxGemmParams p) {
+  constexpr int kFrags = Skinny<FX, FW, MODE>::kFrags;
+  constexpr int kRows = Skinny<FX, FW, MODE>::kRows;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int64_t v0 = (int64_t)blockIdx.x * (kRowsPerWave * 4) + wave * kRowsPerWave;
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * NB);
+  const int64_t v0 = (int64_t)blockIdx.x * (kRows * 4) + wave * kRows;
   if (v0 >= p.V) return;
   const int nblk = (int)(p.K / kMxBlock);
-  const int64_t wb = (int64_t)nblk * Fmt<FW>::kBlockBytes, xb = (int64_t)nblk * Fmt<FX>::kBlockBytes;
-  const uint8_t *wr[kFrags], *ws[kFrags], *xr[NB], *xs[NB];
+  const int64_t wb = (int64_t)nblk * Fmt<FW>::kBlockBytes;
+  const uint8_t *wr[kFrags], *ws[kFrags];
 #pragma unroll
   for (int i = 0; i < kFrags; ++i) {  // rows past the end repeat the last one
     const int64_t r = min(v0 + 16 * i + c, p.V - 1);
     wr[i] = p.w + r * wb;
     ws[i] = p.ws + r * nblk;
   }
+  const int64_t xm = min((int64_t)c, p.M - 1);
+  const uint8_t* xr = p.x + xm * nblk * Fmt<FX>::kBlockBytes;
+  const uint8_t* xs = p.xs + xm * nblk;
+  f32x4_t acc[kFrags];
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int64_t r = min(m0 + 16 * i + c, p.M - 1);
-    xr[i] = p.x + r * xb;
-    xs[i] = p.xs + r * nblk;
-  }
-  f32x4_t acc[kFrags][NB];
-#pragma unroll
-  for (int i = 0; i < kFrags; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  auto step = [&](auto tail, int ss) {
-    constexpr bool TAIL = decltype(tail)::value;
-    SuperFrag<FW, MODE, TAIL> w[kFrags];
-    SuperFrag<FX, MODE, TAIL> x[NB];
-#pragma unroll
-    for (int i = 0; i < kFrags; ++i) w[i].load(wr[i], ws[i], ss, g, nblk);
-#pragma unroll
-    for (int j = 0; j < NB; ++j) x[j].load(xr[j], xs[j], ss, g, nblk);
+  for (int i = 0; i < kFrags; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  // the products of a superstep
+  auto multiply = [&](const auto (&w)[kFrags], const auto& x) {
     if constexpr (MODE == kScaled) {
 #pragma unroll
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int i = 0; i < kFrags; ++i)
-#pragma unroll
-          for (int j = 0; j < NB; ++j)
-            acc[i][j] = mfma16<FW, FX>(w[i].operand(s), x[j].operand(s), acc[i][j], w[i].sc,
-                                       x[j].sc, s);
+          acc[i] = mfma16<FW, FX>(w[i].operand(s), x.operand(s), acc[i], w[i].sc, x.sc, s);
     } else {
-      uint32_t far = 0;
+      uint32_t far = x.far();
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) far |= w[i].far();
-#pragma unroll
-      for (int j = 0; j < NB; ++j) far |= x[j].far();
       if (__any(far != 0)) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 4; ++s) {
+          const i32x8_t b = x.operand_moved(s, lane);
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const i32x8_t b = x[j].operand_moved(s, lane);
-#pragma unroll
-            for (int i = 0; i < kFrags; ++i)
-              acc[i][j] = mfma16<FW, FX>(w[i].operand_moved(s, lane), b, acc[i][j], w[i].sc,
-                                         x[j].sc, s);
-          }
+          for (int i = 0; i < kFrags; ++i)
+            acc[i] = mfma16<FW, FX>(w[i].operand_moved(s, lane), b, acc[i], w[i].sc, x.sc, s);
+        }
       } else {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            bf16x8_t b[NB];
+            const bf16x8_t b = x.wide(s, t);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) b[j] = x[j].wide(s, t);
-#pragma unroll
-            for (int i = 0; i < kFrags; ++i) {
-              const bf16x8_t a = w[i].wide(s, t);
-#pragma unroll
-              for (int j = 0; j < NB; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[j], acc[i][j], 0, 0, 0);
-            }
+            for (int i = 0; i < kFrags; ++i)
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i].wide(s, t), b, acc[i], 0, 0,
+                                                               0);
           }
       }
     }
   };
   const int full = nblk / 16;
-  for (int ss = 0; ss < full; ++ss) step(std::false_type{}, ss);
-  if (nblk % 16) step(std::true_type{}, full);
+  if (full > 0) {
+    SuperFrag<FW, MODE, false> w[2][kFrags];
+    SuperFrag<FX, MODE, false> x[2];
+    auto load = [&](int b, int ss) {
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int64_t m = m0 + 16 * j + c;
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int i = 0; i < kFrags; ++i) {
-      const int64_t v = v0 + 16 * i + 4 * g;
-      const int64_t n = p.V - v;
-      if (n > 0) store4<DT>(p.out, m * p.ldo + v, acc[i][j], p.scale, n < 4 ? (int)n : 4, p.wide);
+      for (int i = 0; i < kFrags; ++i) w[b][i].load(wr[i], ws[i], ss, g, nblk);
+      x[b].load(xr, xs, ss, g, nblk);
+    };
+    load(0, 0);
+    int ss = 0;
+#pragma unroll 1
+    for (; ss + 2 <= full; ss += 2) {
+      load(1, ss + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(w[0], x[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      load(0, min(ss + 2, full - 1));  // past the end: read again, not used
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(w[1], x[1]);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if (ss < full) multiply(w[0], x[0]);
+  }
+  if (nblk % 16) {
+    SuperFrag<FW, MODE, true> w[kFrags];
+    SuperFrag<FX, MODE, true> x;
+#pragma unroll
+    for (int i = 0; i < kFrags; ++i) w[i].load(wr[i], ws[i], full, g, nblk);
+    x.load(xr, xs, full, g, nblk);
+    multiply(w, x);
+  }
+  if (c >= p.M) return;
+#pragma unroll
+  for (int i = 0; i < kFrags; ++i) {
+    const int64_t v = v0 + 16 * i + 4 * g;
+    const int64_t n = p.V - v;
+    if (n > 0) store4<DT>(p.out, c * p.ldo + v, acc[i], p.scale, n < 4 ? (int)n : 4, p.wide);
   }
 }
 
@@ -790,27 +797,21 @@ hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
 }
 
 template <int FX, int FW, int DT>
-hipError_t launch_skinny(const MxGemmParams& p, hipStream_t stream) {
+hipError_t launch_by_tokens(const MxGemmParams& p, hipStream_t stream) {
   constexpr int MODE = DT == 0 && (FX == kMxE4M3 || FW == kMxE4M3) ? kBf16 : kScaled;
-  const unsigned gx = (unsigned)((p.V + 4 * kRowsPerWave - 1) / (4 * kRowsPerWave));
-#define VCE_SKINNY(NB)                                                                      \
-  hipLaunchKernelGGL((mx_skinny_kernel<FX, FW, MODE, NB, DT>),                                    \
-                     dim3(gx, (unsigned)((p.M + 16 * NB - 1) / (16 * NB))),                 \
-                     dim3(kSkinnyThreads), 0, stream, p)
   if (p.M > 128) return launch_tile<FX, FW, MODE, 4, DT>(p, stream);
   if (p.M > 64) return launch_tile<FX, FW, MODE, 2, DT>(p, stream);
-  if (p.M > 32) return launch_tile<FX, FW, MODE, 1, DT>(p, stream);
-  if (p.M <= 16)
-    VCE_SKINNY(1);
-  else
-    VCE_SKINNY(2);
-#undef VCE_SKINNY
+  if (p.M > 16) return launch_tile<FX, FW, MODE, 1, DT>(p, stream);
+  constexpr int rows = 4 * Skinny<FX, FW, MODE>::kRows;
+  hipLaunchKernelGGL((mx_skinny_kernel<FX, FW, MODE, DT>),
+                     dim3((unsigned)((p.V + rows - 1) / rows)), dim3(kSkinnyThreads), 0, stream,
+                     p);
   return hipGetLastError();
 }
 
 template <int FX, int FW>
 hipError_t launch_fmt(const MxGemmParams& p, int dtype, hipStream_t stream) {
-  return dtype == 0 ? launch_skinny<FX, FW, 0>(p, stream) : launch_skinny<FX, FW, 1>(p, stream);
+  return dtype == 0 ? launch_by_tokens<FX, FW, 0>(p, stream) : launch_by_tokens<FX, FW, 1>(p, stream);
 }
 
 }  // namespace
