@@ -186,24 +186,84 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const f32x4_t& v, 
   }
 }
 
-// Up to 16 tokens: every wavefront takes kRows rows of W.  W is read
-// once, 16 bytes a lane straight into operand registers, a superstep ahead of
-// the one being multiplied: with four wavefronts' worth of a superstep waited for
-// and used at once the loads stood still (121 us at 1 x 4096 x 131072 against 53).
-template <int FX, int FW, int MODE>
-struct Skinny {
-  static constexpr int kFrags = FW == kMxE2M1 ? 4 : 2;
-  static constexpr int kRows = 16 * kFrags;
+// Up to 16 tokens: a workgroup holds X in LDS (4096 k of it at a time) and
+// every wavefront streams 16 kFrags rows of W against it.  W is read once, 16
+// bytes a lane straight into operand registers, a superstep ahead of the one
+// being multiplied (waited for and used at once, the loads stood still: 121 us
+// at 1 x 4096 x 131072 against 53).  X from LDS leaves the vector memory path to W
+// (read from L2 by every wavefront it cost 12 us at 8 tokens).
+//
+// X's rows are padded to 256 bytes; the 16-byte chunk q of token c lies at q ^ c
+// in its group of 16, so that 16 lanes reading one chunk of 16 tokens meet
+// all banks once.
+constexpr int kSkinnyK = 4096;
+
+template <int FX>
+struct SkinnyX {
+  static constexpr int kRow = kSkinnyK / 32 * Fmt<FX>::kBlockBytes;
+  static constexpr int kScales = kSkinnyK / 32;
+  uint8_t q[16 * kRow];
+  uint8_t s[16 * kScales];
+  // k0 .. k0 + 4095 (in blocks b0 ..) of the tokens, zeros under scale 1 past M and K.
+  __device__ __forceinline__ void fill(const MxGemmParams& p, int b0, int nblk) {
+    const int rb = nblk * Fmt<FX>::kBlockBytes, at = b0 * Fmt<FX>::kBlockBytes;
+    const int n = min(rb - at, kRow);
+    for (int i = threadIdx.x; i < kRow; i += kSkinnyThreads) {  // 16 kRow / 16 chunks
+      const int c = i / (kRow / 16), k = i % (kRow / 16);
+      u32x4_t v{0, 0, 0, 0};
+      if (c < p.M && k * 16 < n)
+        v = *reinterpret_cast<const u32x4_t*>(p.x + (int64_t)c * rb + at + k * 16);
+      *reinterpret_cast<u32x4_t*>(q + c * kRow + ((k ^ c) * 16)) = v;
+    }
+    for (int i = threadIdx.x; i < 16 * kScales; i += kSkinnyThreads) {
+      const int c = i / kScales, k = i % kScales;
+      s[i] = c < p.M && b0 + k < nblk ? p.xs[(int64_t)c * nblk + b0 + k] : (uint8_t)127;
+    }
+  }
+  __device__ __forceinline__ u32x4_t chunk(int c, int k) const {
+    return *reinterpret_cast<const u32x4_t*>(q + c * kRow + ((k ^ c) * 16));
+  }
+  __device__ __forceinline__ uint32_t scales(int c, int ss, int g) const {
+    return *reinterpret_cast<const uint32_t*>(s + c * kScales + ss * 16 + 4 * g);
+  }
+  // Step st of superstep ss as the scaled instruction's operand.
+  __device__ __forceinline__ i32x8_t operand(int c, int ss, int st, int g) const {
+    i32x8_t r;
+    if constexpr (FX == kMxE4M3) {
+      const int b = ss * 16 + st + 4 * (g / 2);
+      const u32x4_t lo = chunk(c, 2 * b + g % 2), hi = chunk(c, 2 * (b + 8) + g % 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[j] = (int32_t)lo[j];
+        r[4 + j] = (int32_t)hi[j];
+      }
+    } else {
+      const u32x4_t lo = chunk(c, ss * 16 + st + 4 * g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[j] = (int32_t)lo[j];
+        r[4 + j] = 0;
+      }
+    }
+    return r;
+  }
+  // Values 8 t .. of step st's block of this lane group as BF16, scale applied.
+  __device__ __forceinline__ bf16x8_t wide(const u32x4_t* piece, uint32_t sc, int st, int t) const {
+    SuperFrag<FX, kBf16, false> f;
+    f.q[st][0] = piece[0];
+    f.q[st][Fmt<FX>::kPieces - 1] = piece[Fmt<FX>::kPieces - 1];
+    f.sc = sc;
+    return f.wide(st, t);
+  }
 };
 
-template <int FX, int FW, int MODE, int DT>
+template <int FX, int FW, int MODE, int kFrags, int DT>
 __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxGemmParams p) {
-  constexpr int kFrags = Skinny<FX, FW, MODE>::kFrags;
-  constexpr int kRows = Skinny<FX, FW, MODE>::kRows;
+  constexpr int kRows = 16 * kFrags;
+  __shared__ __attribute__((aligned(256))) SkinnyX<FX> x;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t v0 = (int64_t)blockIdx.x * (kRows * 4) + wave * kRows;
-  if (v0 >= p.V) return;
   const int nblk = (int)(p.K / kMxBlock);
   const int64_t wb = (int64_t)nblk * Fmt<FW>::kBlockBytes;
   const uint8_t *wr[kFrags], *ws[kFrags];
@@ -213,77 +273,79 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxGemmPara
     wr[i] = p.w + r * wb;
     ws[i] = p.ws + r * nblk;
   }
-  const int64_t xm = min((int64_t)c, p.M - 1);
-  const uint8_t* xr = p.x + xm * nblk * Fmt<FX>::kBlockBytes;
-  const uint8_t* xs = p.xs + xm * nblk;
   f32x4_t acc[kFrags];
 #pragma unroll
   for (int i = 0; i < kFrags; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  // the products of a superstep
-  auto multiply = [&](const auto (&w)[kFrags], const auto& x) {
-    if constexpr (MODE == kScaled) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int i = 0; i < kFrags; ++i)
-          acc[i] = mfma16<FW, FX>(w[i].operand(s), x.operand(s), acc[i], w[i].sc, x.sc, s);
-    } else {
-      uint32_t far = x.far();
+  // the products of superstep ss (of the part in LDS)
+  auto multiply = [&](const auto (&w)[kFrags], int ss) {
+    const uint32_t sx = x.scales(c, ss, g);
+    bool scaled = MODE == kScaled;
+    if constexpr (MODE == kBf16) {
+      uint32_t far = ~(sx ^ (sx << 1)) & 0x80808080u;
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) far |= w[i].far();
-      if (__any(far != 0)) {
+      scaled = __any(far != 0);
+    }
+    if (scaled) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const i32x8_t b = x.operand_moved(s, lane);
+      for (int s = 0; s < 4; ++s) {
+        const i32x8_t b = x.operand(c, ss, s, g);
+#pragma unroll
+        for (int i = 0; i < kFrags; ++i) {
+          if constexpr (MODE == kScaled)
+            acc[i] = mfma16<FW, FX>(w[i].operand(s), b, acc[i], w[i].sc, sx, s);
+          else
+            acc[i] = mfma16<FW, FX>(w[i].operand_moved(s, lane), b, acc[i], w[i].sc, sx, s);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        u32x4_t piece[2];
+#pragma unroll
+        for (int h = 0; h < Fmt<FX>::kPieces; ++h)
+          piece[h] = x.chunk(c, (ss * 16 + s + 4 * g) * Fmt<FX>::kPieces + h);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const bf16x8_t b = x.wide(piece, sx, s, t);
 #pragma unroll
           for (int i = 0; i < kFrags; ++i)
-            acc[i] = mfma16<FW, FX>(w[i].operand_moved(s, lane), b, acc[i], w[i].sc, x.sc, s);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i].wide(s, t), b, acc[i], 0, 0, 0);
         }
-      } else {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const bf16x8_t b = x.wide(s, t);
-#pragma unroll
-            for (int i = 0; i < kFrags; ++i)
-              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i].wide(s, t), b, acc[i], 0, 0,
-                                                               0);
-          }
       }
     }
   };
-  const int full = nblk / 16;
-  if (full > 0) {
+  constexpr int kSupers = kSkinnyK / 512;
+  for (int s0 = 0; s0 * 16 < nblk; s0 += kSupers) {
     SuperFrag<FW, MODE, false> w[2][kFrags];
-    SuperFrag<FX, MODE, false> x[2];
     auto load = [&](int b, int ss) {
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) w[b][i].load(wr[i], ws[i], ss, g, nblk);
-      x[b].load(xr, xs, ss, g, nblk);
     };
-    load(0, 0);
+    const int full = min(nblk / 16 - s0, kSupers);  // whole supersteps of this part
+    if (full > 0) load(0, s0);
+    if (s0) __syncthreads();
+    x.fill(p, s0 * 16, nblk);
+    __syncthreads();
     int ss = 0;
 #pragma unroll 1
     for (; ss + 2 <= full; ss += 2) {
-      load(1, ss + 1);
+      load(1, s0 + ss + 1);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(w[0], x[0]);
+      multiply(w[0], ss);
       __builtin_amdgcn_sched_barrier(0);
-      load(0, min(ss + 2, full - 1));  // past the end: read again, not used
+      load(0, s0 + min(ss + 2, full - 1));  // past the end: read again, not used
       __builtin_amdgcn_sched_barrier(0);
-      multiply(w[1], x[1]);
+      multiply(w[1], ss + 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (ss < full) multiply(w[0], x[0]);
-  }
-  if (nblk % 16) {
-    SuperFrag<FW, MODE, true> w[kFrags];
-    SuperFrag<FX, MODE, true> x;
+    if (ss < full) multiply(w[0], ss);
+    if (full < kSupers && nblk % 16) {
+      SuperFrag<FW, MODE, true> last[kFrags];
 #pragma unroll
-    for (int i = 0; i < kFrags; ++i) w[i].load(wr[i], ws[i], full, g, nblk);
-    x.load(xr, xs, full, g, nblk);
-    multiply(w, x);
+      for (int i = 0; i < kFrags; ++i) last[i].load(wr[i], ws[i], s0 + full, g, nblk);
+      multiply(last, full);
+    }
   }
   if (c >= p.M) return;
 #pragma unroll
@@ -292,6 +354,15 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxGemmPara
     const int64_t n = p.V - v;
     if (n > 0) store4<DT>(p.out, c * p.ldo + v, acc[i], p.scale, n < 4 ? (int)n : 4, p.wide);
   }
+}
+
+template <int FX, int FW, int MODE, int kFrags, int DT>
+hipError_t launch_skinny(const MxGemmParams& p, hipStream_t stream) {
+  constexpr int rows = 64 * kFrags;
+  hipLaunchKernelGGL((mx_skinny_kernel<FX, FW, MODE, kFrags, DT>),
+                     dim3((unsigned)((p.V + rows - 1) / rows)), dim3(kSkinnyThreads), 0, stream,
+                     p);
+  return hipGetLastError();
 }
 
 // ---- many tokens: tiles through LDS ---------------------------------------------
@@ -802,11 +873,12 @@ hipError_t launch_by_tokens(const MxGemmParams& p, hipStream_t stream) {
   if (p.M > 128) return launch_tile<FX, FW, MODE, 4, DT>(p, stream);
   if (p.M > 64) return launch_tile<FX, FW, MODE, 2, DT>(p, stream);
   if (p.M > 16) return launch_tile<FX, FW, MODE, 1, DT>(p, stream);
-  constexpr int rows = 4 * Skinny<FX, FW, MODE>::kRows;
-  hipLaunchKernelGGL((mx_skinny_kernel<FX, FW, MODE, DT>),
-                     dim3((unsigned)((p.V + rows - 1) / rows)), dim3(kSkinnyThreads), 0, stream,
-                     p);
-  return hipGetLastError();
+  // as many rows of W per wavefront (fewer reads of X) as leave two workgroups
+  // per CU; four fragments of E4M3 do not fit its registers
+  if (FW == kMxE2M1 && p.V >= 256 * 512)
+    return launch_skinny<FX, FW, MODE, FW == kMxE2M1 ? 4 : 2, DT>(p, stream);
+  if (p.V >= 128 * 512) return launch_skinny<FX, FW, MODE, 2, DT>(p, stream);
+  return launch_skinny<FX, FW, MODE, 1, DT>(p, stream);
 }
 
 template <int FX, int FW>
