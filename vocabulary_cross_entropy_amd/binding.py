@@ -761,9 +761,13 @@ def _mx_format(fmt: str) -> int:
 
 def _on_stream(ref: torch.Tensor, stream, fn):
     """fn(stream handle) with ref's device current and, given ``stream``, allocations under it."""
-    _need_cuda(ref)
-    if stream is None and ref.device.index == torch.cuda.current_device():
-        return fn(torch.cuda.current_stream().cuda_stream)
+    if not ref.is_cuda:
+        _need_cuda(ref)
+    if stream is None:
+        index = ref.get_device()
+        if index == torch.cuda.current_device():
+            # the handle alone: a Stream object costs more than the launch
+            return fn(torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(ref.device):
         s = torch.cuda.current_stream() if stream is None else stream
         if s.device != ref.device:
@@ -776,7 +780,7 @@ def _check_out(t, name: str, shape, dtype, ref: torch.Tensor):
     """A given output: its shape, dtype, contiguity and device.  None passes."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
                          f"{tuple(t.shape)}")
     if not t.is_contiguous():
@@ -787,15 +791,18 @@ def _check_out(t, name: str, shape, dtype, ref: torch.Tensor):
 
 def _rows2d(t: torch.Tensor, name: str):
     """(rows, cols, row stride) of a 2-D tensor with contiguous rows."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(shape)}")
+    rows, cols = shape
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.shape[0], t.shape[1], t.stride(0)
+    return rows, cols, ld
 
 
 def _check_weight(weight: torch.Tensor, H: int, ref: torch.Tensor):
-    if weight.dim() != 1 or weight.shape[0] != H or not weight.is_contiguous():
+    if weight.dim() != 1 or weight.numel() != H or not weight.is_contiguous():
         raise ValueError(f"weight must be contiguous with {H} elements")
     if weight.device != ref.device:
         raise ValueError(f"weight must be on {ref.device}, got {weight.device}")
@@ -807,7 +814,7 @@ def _rms_forward(mx, x, weight, residual, eps, weight_offset, stream, out):
     M, H, ldx = _rows2d(x, "x")
     ldr = 0
     if residual is not None:
-        if residual.dtype != x.dtype or tuple(residual.shape) != tuple(x.shape):
+        if residual.dtype != x.dtype or residual.shape != x.shape:
             raise ValueError("residual must have the shape and dtype of x")
         if residual.device != x.device:
             raise ValueError(f"residual must be on {x.device}, got {residual.device}")
@@ -815,37 +822,41 @@ def _rms_forward(mx, x, weight, residual, eps, weight_offset, stream, out):
     wdt = _check_weight(weight, H, x)
     if mx and H % 32:
         raise ValueError(f"rows of a multiple of 32 elements are needed, got {H}")
-    out = (None,) * (4 if mx else 3) if out is None else tuple(out)
-    if len(out) != (4 if mx else 3):
-        raise ValueError(f"out must hold {4 if mx else 3} tensors (None to allocate)")
-    rstd, h = out[-2:]
-    if mx:
-        _check_out(out[0], "q", (M, H), torch.uint8, x)
-        _check_out(out[1], "scales", (M, H // 32), torch.uint8, x)
+    n = 4 if mx else 3
+    if out is None:
+        out = (None,) * n
     else:
-        _check_out(out[0], "y", (M, H), x.dtype, x)
-    _check_out(rstd, "rstd", (M,), torch.float32, x)
-    _check_out(h, "h", (M, H), x.dtype, x)
+        if len(out) != n:
+            raise ValueError(f"out must hold {n} tensors (None to allocate)")
+        if mx:
+            _check_out(out[0], "q", (M, H), torch.uint8, x)
+            _check_out(out[1], "scales", (M, H // 32), torch.uint8, x)
+        else:
+            _check_out(out[0], "y", (M, H), x.dtype, x)
+        _check_out(out[-2], "rstd", (M,), torch.float32, x)
+        _check_out(out[-1], "h", (M, H), x.dtype, x)
 
     def call(s):
-        dev = x.device
-        r = torch.empty(M, dtype=torch.float32, device=dev) if rstd is None else rstd
-        ho = h
-        if ho is None and residual is not None:
-            ho = torch.empty((M, H), dtype=x.dtype, device=dev)
+        r, h = out[-2:]
+        if r is None:
+            r = x.new_empty(M, dtype=torch.float32)
+        if h is None and residual is not None:
+            h = x.new_empty((M, H))
         if mx:
             q, sc = out[:2]
-            q = torch.empty((M, H), dtype=torch.uint8, device=dev) if q is None else q
-            sc = torch.empty((M, H // 32), dtype=torch.uint8, device=dev) if sc is None else sc
+            if q is None:
+                q = x.new_empty((M, H), dtype=torch.uint8)
+            if sc is None:
+                sc = x.new_empty((M, H // 32), dtype=torch.uint8)
             _check("rms_forward_mx8", lib().rms_forward_mx8(
-                _at(x), dt, M, H, ldx, _at(residual), ldr, _at(weight), wdt, weight_offset, eps,
-                _at(q), _at(sc), _at(ho), _at(r), s))
-            return q, sc, r, ho
-        y = torch.empty((M, H), dtype=x.dtype, device=dev) if out[0] is None else out[0]
+                x.data_ptr(), dt, M, H, ldx, _at(residual), ldr, weight.data_ptr(), wdt,
+                weight_offset, eps, q.data_ptr(), sc.data_ptr(), _at(h), r.data_ptr(), s))
+            return q, sc, r, h
+        y = x.new_empty((M, H)) if out[0] is None else out[0]
         _check("rms_forward", lib().rms_forward(
-            _at(x), dt, M, H, ldx, _at(residual), ldr, _at(weight), wdt, weight_offset, eps,
-            _at(y), _at(ho), _at(r), s))
-        return y, r, ho
+            x.data_ptr(), dt, M, H, ldx, _at(residual), ldr, weight.data_ptr(), wdt,
+            weight_offset, eps, y.data_ptr(), _at(h), r.data_ptr(), s))
+        return y, r, h
     return _on_stream(x, stream, call)
 
 
@@ -887,8 +898,11 @@ def rms_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: 
     dt = _elem_dtype(h, "h")
     M, H, _ = _rows2d(h, "h")
     wdt = _check_weight(weight, H, h)
-    for t, name in ((dy, "dy"), (h, "h"), (dh, "dh"), (dx, "dx")):
-        _check_out(t, name, (M, H), h.dtype, h)
+    shape, hdt = (M, H), h.dtype
+    _check_out(dy, "dy", shape, hdt, h)
+    _check_out(h, "h", shape, hdt, h)
+    _check_out(dh, "dh", shape, hdt, h)
+    _check_out(dx, "dx", shape, hdt, h)
     _check_buf(rstd, "rstd", M, like=h)
     _check_out(dweight, "dweight", (H,), torch.float32, h)
     if workspace is not None:
@@ -898,8 +912,10 @@ def rms_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: 
         o = torch.empty_like(h) if dx is None else dx
         dw, ws = dweight, workspace
         if need_dweight or dw is not None:
-            dw = torch.empty(H, dtype=torch.float32, device=h.device) if dw is None else dw
-            ws = rms_backward_workspace(M, H, h.device) if ws is None else ws
+            if dw is None:
+                dw = h.new_empty(H, dtype=torch.float32)
+            if ws is None:
+                ws = rms_backward_workspace(M, H, h.device)
         _check("rms_backward", lib().rms_backward(
             _at(dy), _at(h), dt, M, H, _at(weight), wdt, weight_offset, _at(rstd), _at(dh),
             _at(o), _at(dw), _at(ws), 0 if ws is None else ws.numel(), s))
@@ -921,9 +937,8 @@ def mx_quantize(x: torch.Tensor, fmt: str = "e2m1", *, stream=None, out=None):
     _check_out(sc, "scales", (rows, K // 32), torch.uint8, x)
 
     def call(s):
-        qo = torch.empty((rows, qk), dtype=torch.uint8, device=x.device) if q is None else q
-        so = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device) if sc is None \
-            else sc
+        qo = x.new_empty((rows, qk), dtype=torch.uint8) if q is None else q
+        so = x.new_empty((rows, K // 32), dtype=torch.uint8) if sc is None else sc
         _check("mx_quantize", lib().mx_quantize(_at(x), dt, rows, K, ldx, f, _at(qo), _at(so), s))
         return qo, so
     return _on_stream(x, stream, call)
@@ -934,11 +949,14 @@ def _check_mx(q: torch.Tensor, scales: torch.Tensor, fmt: str, name: str):
     f = _mx_format(fmt)
     if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TypeError(f"{name} and its scales must be uint8")
-    if q.dim() != 2 or scales.dim() != 2:
-        raise ValueError(f"{name} and its scales must have two dimensions")
-    rows, K = q.shape[0], q.shape[1] * (1 if fmt == "e4m3" else 2)
-    if K == 0 or K % 32 or tuple(scales.shape) != (rows, K // 32):
-        raise ValueError(f"{name} {tuple(q.shape)} in {fmt} needs scales of "
+    shape = q.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(shape)}")
+    rows, K = shape
+    if fmt == "e2m1":
+        K *= 2
+    if K == 0 or K % 32 or scales.shape != (rows, K // 32):
+        raise ValueError(f"{name} {tuple(shape)} in {fmt} needs scales of "
                          f"({rows}, {K} / 32), got {tuple(scales.shape)}")
     if not (q.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name} and its scales must be contiguous")
@@ -956,7 +974,7 @@ def mx_dequantize(q: torch.Tensor, scales: torch.Tensor, fmt: str = "e2m1",
     _check_out(out, "out", (rows, K), dtype, q)
 
     def call(s):
-        o = torch.empty((rows, K), dtype=dtype, device=q.device) if out is None else out
+        o = q.new_empty((rows, K), dtype=dtype) if out is None else out
         _check("mx_dequantize", lib().mx_dequantize(_at(q), _at(scales), f, rows, K, _at(o),
                                                     _elem_dtype(o, "out"), s))
         return o
@@ -985,7 +1003,7 @@ def mx_logits(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
 
     def call(s):
-        o = torch.empty((M, V), dtype=dtype, device=x.device) if out is None else out
+        o = x.new_empty((M, V), dtype=dtype) if out is None else out
         _check("mx_logits", lib().mx_logits(
             _at(x), _at(x_scales), xf, _at(w), _at(w_scales), wf, M, K, V, logit_scale, _at(o),
             _elem_dtype(o, "out"), o.stride(0), s))
@@ -1035,12 +1053,12 @@ def ce_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor |
         _check_buf(workspace, "workspace", workspace.numel(), torch.uint8, like=logits)
 
     def call(s):
-        dev = logits.device
         tok, lp = outs
-        tok = torch.empty(lead, dtype=torch.int64, device=dev) if tok is None else tok
+        if tok is None:
+            tok = logits.new_empty(lead, dtype=torch.int64)
         if lp is None and with_logprob:
-            lp = torch.empty(lead, dtype=torch.float32, device=dev)
-        ws = ce_sample_workspace(N, V, dev) if workspace is None else workspace
+            lp = logits.new_empty(lead, dtype=torch.float32)
+        ws = ce_sample_workspace(N, V, logits.device) if workspace is None else workspace
         _check("ce_sample", lib().ce_sample(
             _at(logits), dt, d0, d1, V, ls0, ls1, _at(temperature), _at(top_k), _at(top_p),
             _at(min_p), _at(u), _at(tok), _at(lp), _at(ws), ws.numel(), s))
