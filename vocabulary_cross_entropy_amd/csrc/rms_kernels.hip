@@ -7,10 +7,8 @@
 //
 // All of it is bound by memory traffic: a row is read once, held in registers
 // as FP32 between the sum of squares and the output, and written once.  A row
-// belongs to TPR threads of EPL elements each (one wavefront for many rows,
-// so that no barrier stands between rows; a workgroup of 256 or 1024 where a
-// wavefront would have to hold more than 64 elements a lane, or where there
-// are too few rows to fill the chip with one wavefront each).
+// belongs to TPR threads of EPL elements each: a wavefront, or a workgroup of 256
+// or 1024 (see pick_shape).
 //
 // Loads go through buffer descriptors that end at the row (a lane past it
 // reads zeros), so all loads of a row issue together, without branches.
@@ -225,6 +223,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_bwd_kernel(RmsBwdPa
       dy[i].load(rdy, (i * TPR + t) * VE);
       h[i].load(rh, (i * TPR + t) * VE);
     }
+    // with the others, not behind the sum: one wait for memory per row (95.9 -> 78.2 us
+    // at 16384 x 2304 BF16)
+    Raw<DT, VE> dh[NV];
+    if (p.dh) {
+      const __amdgpu_buffer_rsrc_t rdh = rsrc_of(static_cast<const char*>(p.dh) + row * rowb, rowb);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) dh[i].load(rdh, (i * TPR + t) * VE);
+    }
     const float rstd = p.rstd[row];
     float dot = 0.0f;
 #pragma unroll
@@ -246,14 +252,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_bwd_kernel(RmsBwdPa
       const int e = (i * TPR + t) * VE;
       float w[VE], dx[VE];
       load_weight<VE>(rw, p.wdtype, e, w);
-      Raw<DT, VE> dh;
-      if (p.dh)
-        dh.load(rsrc_of(static_cast<const char*>(p.dh) + row * rowb, rowb), e);
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
         const float g = dy[i].get(j) * (w[j] + p.w0);
         dx[j] = rstd * __builtin_fmaf(-(h[i].get(j) * rstd), dot, g);
-        if (p.dh) dx[j] += dh.get(j);
+        if (p.dh) dx[j] += dh[i].get(j);
       }
       if (e < H) store_elems<DT, VE>(dxr, e, dx);
     }
@@ -290,22 +293,24 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_bwd_kernel(RmsBwdPa
   }
 }
 
-// dw = sum of the workgroups' shares (n_part, H), 64 columns per workgroup,
-// the shares dealt over its 16 wavefronts and added in a fixed order.
+// dw = sum of the workgroups' shares (n_part, H), 16 columns per workgroup, the
+// shares dealt over its 64 groups of 16 lanes and added in a fixed order.
 __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* partial, int n_part, int H,
                                                       float* dw) {
-  __shared__ float sh[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  __shared__ float sh[64][16];
+  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + col;
   float s = 0.0f;
-  if (c < H)
-    for (int k = wave; k < n_part; k += 16) s += partial[(int64_t)k * H + c];
-  sh[wave][lane] = s;
+  if (c < H) {
+#pragma unroll 8
+    for (int k = grp; k < n_part; k += 64) s += partial[(int64_t)k * H + c];
+  }
+  sh[grp][col] = s;
   __syncthreads();
-  if (wave == 0 && c < H) {
+  if (threadIdx.x < 16 && c < H) {
     s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s += sh[k][lane];
+    for (int k = 0; k < 64; ++k) s += sh[k][col];
     dw[c] = s;
   }
 }
@@ -315,8 +320,13 @@ bool vec_ok(int64_t H, int es, int64_t ld) {
 }
 bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Calls f with the threads per row and elements per lane as constants.
-template <int VE, class F>
+// Calls f with the threads per row and elements per lane as constants.  A
+// wavefront per row needs no barrier and wins while it holds 16 elements a lane at
+// most (forward at H = 1024: 40 us against 45 by 256 threads; at 2304 55 against
+// 51); the backward, whose rows meet no other barrier, up to 40 (at 2304 62 us
+// against 66; at 4096 with 64 elements 159 against 101).  Few rows take more threads
+// each whatever H is.
+template <int VE, bool BWD, class F>
 hipError_t pick_shape(int64_t M, int H, F f) {
   using std::integral_constant;
 #define VCE_SHAPE(T, E) f(integral_constant<int, T>{}, integral_constant<int, E>{})
@@ -331,18 +341,20 @@ hipError_t pick_shape(int64_t M, int H, F f) {
     if (H > 16384) return VCE_SHAPE(1024, 32);
     if (H > 8192) return VCE_SHAPE(1024, 16);
     if (H > 4096) return VCE_SHAPE(256, 32);
-    if (M < 1024 && H > 512) return H <= 2048 ? VCE_SHAPE(256, 8) : VCE_SHAPE(256, 16);
     if (H <= 512) return VCE_SHAPE(64, 8);
-    if (H <= 1024) return VCE_SHAPE(64, 16);
-    if (H <= 2560) return VCE_SHAPE(64, 40);
-    return VCE_SHAPE(64, 64);
+    if (M >= 1024) {
+      if (H <= 1024) return VCE_SHAPE(64, 16);
+      if constexpr (BWD)
+        if (H <= 2560) return VCE_SHAPE(64, 40);
+    }
+    return H <= 2048 ? VCE_SHAPE(256, 8) : VCE_SHAPE(256, 16);
   }
 #undef VCE_SHAPE
 }
 
 template <int DT, int VE, bool MX>
 hipError_t launch_fwd(const RmsFwdParams& p, hipStream_t stream) {
-  return pick_shape<VE>(p.M, p.H, [&](auto tpr, auto epl) {
+  return pick_shape<VE, false>(p.M, p.H, [&](auto tpr, auto epl) {
     constexpr int T = decltype(tpr)::value, E = decltype(epl)::value;
     constexpr int threads = T < 256 ? 256 : T;
     constexpr int rows = threads / T;
@@ -354,7 +366,7 @@ hipError_t launch_fwd(const RmsFwdParams& p, hipStream_t stream) {
 
 template <int DT, int VE>
 hipError_t launch_bwd(const RmsBwdParams& p, int n_wg, hipStream_t stream) {
-  return pick_shape<VE>(p.M, p.H, [&](auto tpr, auto epl) {
+  return pick_shape<VE, true>(p.M, p.H, [&](auto tpr, auto epl) {
     constexpr int T = decltype(tpr)::value, E = decltype(epl)::value;
     constexpr int threads = T < 256 ? 256 : T;
     hipLaunchKernelGGL((rms_bwd_kernel<DT, VE, T, E>), dim3((unsigned)n_wg), dim3(threads), 0,
@@ -381,19 +393,22 @@ hipError_t launch_rms_forward(const RmsFwdParams& p, int dtype, bool mx, hipStre
   return vec ? launch_fwd<1, 8, false>(p, stream) : launch_fwd<1, 1, false>(p, stream);
 }
 
-// Workgroups of the backward, and so shares of dw: two per CU, fewer where a
-// workgroup would not have at least four rows.
-int rms_bwd_parts(int64_t M) {
+// Workgroups of the backward, and so shares of dw: two per CU, four where rows
+// are short or read element by element (at 16384 x 2305 BF16 137 -> 103 us), fewer
+// where a workgroup would not have at least four rows.
+static int bwd_parts(int64_t M, int most) {
   const int64_t n = (M + 3) / 4;
-  return (int)(n < 1 ? 1 : n > 512 ? 512 : n);
+  return (int)(n < 1 ? 1 : n > most ? most : n);
 }
+
+int rms_bwd_parts(int64_t M) { return bwd_parts(M, 1024); }
 
 hipError_t launch_rms_backward(RmsBwdParams p, int dtype, hipStream_t stream) {
   const int es = dtype == 0 ? 4 : 2;
-  const int n = rms_bwd_parts(p.M);
+  const bool vec = vec_ok(p.H, es, p.H) && al16(p.dy) && al16(p.h) && al16(p.dh) && al16(p.dx) &&
+                   al16(p.weight);
+  const int n = bwd_parts(p.M, !vec || p.H <= 1024 ? 1024 : 512);
   if (p.M > 0) {
-    const bool vec = vec_ok(p.H, es, p.H) && al16(p.dy) && al16(p.h) && al16(p.dh) &&
-                     al16(p.dx) && al16(p.weight);
     hipError_t e;
     if (dtype == 0)
       e = vec ? launch_bwd<0, 4>(p, n, stream) : launch_bwd<0, 1>(p, n, stream);
@@ -402,7 +417,7 @@ hipError_t launch_rms_backward(RmsBwdParams p, int dtype, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (p.dweight) {
-    hipLaunchKernelGGL(rms_dw_kernel, dim3((unsigned)((p.H + 63) / 64)), dim3(1024), 0, stream,
+    hipLaunchKernelGGL(rms_dw_kernel, dim3((unsigned)((p.H + 15) / 16)), dim3(1024), 0, stream,
                        p.partial, p.M > 0 ? n : 0, p.H, p.dweight);
     return hipGetLastError();
   }

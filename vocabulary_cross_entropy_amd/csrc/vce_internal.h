@@ -183,12 +183,12 @@ struct RmsBwdParams {
   const float* rstd;
   const void* dh;  // optional (M, H)
   void* dx;
-  float* partial;  // (rms_bwd_parts(M), H) shares of dw, NULL without dweight
+  float* partial;  // up to (rms_bwd_parts(M), H) shares of dw, NULL without dweight
   float* dweight;  // optional (H)
 };
 
 bool rms_width_ok(int64_t H);
-int rms_bwd_parts(int64_t M);
+int rms_bwd_parts(int64_t M);  // at most
 hipError_t launch_rms_forward(const RmsFwdParams& p, int dtype, bool mx, hipStream_t stream);
 hipError_t launch_rms_backward(RmsBwdParams p, int dtype, hipStream_t stream);
 
