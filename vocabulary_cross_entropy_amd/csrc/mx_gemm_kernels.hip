@@ -828,8 +828,15 @@ __device__ __forceinline__ void mx_tile_of(int64_t b, int64_t n_ti, int64_t n_tj
   *tj = in / w;
 }
 
+// Two workgroups per CU where 64 tokens leave the registers and LDS for it.
+template <int FX, int FW, int MODE, int NA>
+constexpr int mx_tile_occupancy() {
+  return NA == 1 && MxTile<FX, FW, MODE, NA>::kSmem <= 80 * 1024 ? 2 : 1;
+}
+
 template <int FX, int FW, int MODE, int NA, int DT, bool MASK>
-__global__ __launch_bounds__(kTileThreads, NA == 1 ? 2 : 1) void mx_tile_kernel(MxGemmParams p) {
+__global__ __launch_bounds__(kTileThreads, (mx_tile_occupancy<FX, FW, MODE, NA>())) void
+mx_tile_kernel(MxGemmParams p) {
   typedef MxTile<FX, FW, MODE, NA> T;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kSmem];
   const int64_t n_ti = (p.M + T::kTileM - 1) / T::kTileM, n_tj = (p.V + kTileN - 1) / kTileN;
