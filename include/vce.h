@@ -588,8 +588,8 @@ int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uin
  * ceil(log2 V)) of it above V = 2^18); their sums are exact, so the token does not
  * depend on how the work is split, and is reproducible.
  *
- *  logits   (d0, d1, V) as in ce_forward, V up to 2^28 and N = d0 * d1 below 2^22
- *           rows (VCE_EUNSUPPORTED otherwise).  -inf is a masked token; a
+ *  logits   (d0, d1, V) as in ce_forward, V up to 2^28, N = d0 * d1 below 2^22 rows,
+ *           N * V below 2^44 (VCE_EUNSUPPORTED otherwise).  -inf is a masked token; a
  *           finite mask far below the maximum has no weight either.  +inf: the
  *           tokens at +inf share the row.
  *  temperature, top_p, min_p (N) FP32 and top_k (N) int32, or NULL for 1, 1, 0

@@ -185,9 +185,15 @@ struct Weights {
   // 2^x for x <= 0 by 2^n 2^f, |f| <= 1/2, with 2^f - 1 = f g(f), g the
   // polynomial of degree 8 through (2^f - 1) / f at nine Chebyshev nodes (relative
   // error 4e-14, below the 2^-44 of the rounding, and exactly 1 at f = 0).
-  // x below -64 rounds to no weight.  For a finite m.
-  __device__ __forceinline__ double real(float z) const {
-    double x = ((double)z - md) * c;
+  // x below -64 rounds to no weight.  real() is for a finite m.
+  __device__ __forceinline__ double real(float z) const { return power((double)z - md); }
+  // The same whatever m is: where it is infinite z = m has weight 1, all else
+  // none.  No branch, so that many run interleaved.
+  __device__ __forceinline__ double weight(float z) const {
+    return power(z == m ? 0.0 : (double)z - md);
+  }
+  __device__ __forceinline__ double power(double d) const {
+    double x = d * c;
     x = __builtin_fmax(x, -64.0);
     const double r = x + 0x1.8p52;
     const double f = x - (r - 0x1.8p52);
@@ -201,10 +207,6 @@ struct Weights {
     const uint32_t hi = (uint32_t)(b >> 32) + (n << 20);
     return __builtin_bit_cast(double, ((u64)hi << 32) | (uint32_t)b);
   }
-  __device__ __forceinline__ double weight(float z) const {
-    if (inf) return z == m ? 1.0 : 0.0;
-    return real(z);
-  }
   __device__ __forceinline__ u64 fixed(double w) const {
     return __builtin_bit_cast(u64, w + magic) - magic_bits;
   }
@@ -217,8 +219,17 @@ struct Weights {
   }
 };
 
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;  // of a radix selection
+
+constexpr int kGroupBatch = 16;  // segments whose group maxima a thread loads at once
+constexpr int kKeepSegs = 1024;  // segments of a row that sample_rest_kernel draws from
+
 struct Scratch {
-  u64 hist[256];
+  union {
+    u64 hist[3 * kDigits];
+    uint16_t group[kGroupBatch * kThreads];
+    u64 keep[kKeepSegs];
+  };
   u64 wave[kWaves];
   u64 wave2[kWaves];
   u64 out[4];
@@ -240,16 +251,8 @@ struct alignas(16) Entry {
 };
 constexpr u64 kKeptBit = (u64)1 << 63;
 
-constexpr int kGroupBatch = 16;  // segments whose group maxima a thread loads at once
-
-constexpr int kKeepSegs = 1024;  // segments of a row that sample_rest_kernel draws from
-
 struct PickShared : Scratch {
   Entry list[kCap];
-  union {
-    uint16_t group[kGroupBatch * kThreads];
-    u64 keep[kKeepSegs];
-  };
   uint32_t n_groups;
 };
 
@@ -310,59 +313,62 @@ struct Sel {
 
 // visit(f) calls f(key, amount) for this thread's elements, keys below
 // 2^bits.  If the whole sum does not reach the target, the least key is taken.
+// Every wavefront scans the digit's histogram for itself, and three histograms
+// take turns: one barrier per digit.
 template <class S, class Visit>
 __device__ __forceinline__ Sel radix_select(int bits, double target, bool strict, S& sh,
                                             Visit visit) {
+  constexpr int kPer = kDigits / 64;
+  const int lane = threadIdx.x & 63;
   uint32_t prefix = 0;
   u64 above = 0, at = 0;
-  for (int shift = (bits - 1) / 8 * 8; shift >= 0; shift -= 8) {
-    __syncthreads();
-    if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0;
-    __syncthreads();
+  __syncthreads();
+  for (int i = threadIdx.x; i < kDigits; i += kThreads) sh.hist[i] = 0;
+  __syncthreads();
+  int buf = 0;
+  for (int shift = (bits - 1) / kDigitBits * kDigitBits; shift >= 0; shift -= kDigitBits) {
+    u64* hist = sh.hist + buf * kDigits;
     visit([&](uint32_t k, u64 a) {
-      if (a != 0 && (shift >= 24 || (k >> (shift + 8)) == prefix))
-        atomicAdd(&sh.hist[(k >> shift) & 255u], a);
+      if (a != 0 && (k >> shift >> kDigitBits) == prefix)
+        atomicAdd(&hist[(k >> shift) & (kDigits - 1)], a);
     });
+    // the next digit's, which was scanned two digits ago: every wavefront has
+    // passed the barrier since
+    buf = buf == 2 ? 0 : buf + 1;
+    u64* clear = sh.hist + buf * kDigits;
+    for (int i = threadIdx.x; i < kDigits; i += kThreads) clear[i] = 0;
     __syncthreads();
-    if (threadIdx.x < 64) {
-      const int lane = threadIdx.x;
-      u64 h[4], s = 0;
+    u64 h[kPer], s = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = sh.hist[255 - 4 * lane - j];
-        s += h[j];
-      }
-      const u64 run = wave_scan(s);
-      const uint64_t hit = __ballot(reached(above + run, target, strict));
-      const uint64_t some = __ballot(s != 0);
-      // the first lane that reaches it, else the last that holds anything
-      const int who = hit ? __builtin_ctzll(hit) : some ? 63 - __builtin_clzll(some) : 63;
-      if (lane == who) {
-        u64 a = above + run - s;
-        int pick = -1, last = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (pick < 0) {
-            if (h[j] != 0) last = j;
-            if (reached(a + h[j], target, strict))
-              pick = j;
-            else
-              a += h[j];
-          }
-        }
-        if (pick < 0) {  // not reached: the last bin that holds anything
-          pick = last;
-          a -= last == 0 ? h[0] : last == 1 ? h[1] : last == 2 ? h[2] : h[3];
-        }
-        sh.out[0] = (u64)(255 - 4 * lane - pick);
-        sh.out[1] = a;
-        sh.out[2] = pick == 0 ? h[0] : pick == 1 ? h[1] : pick == 2 ? h[2] : h[3];
-      }
+    for (int j = 0; j < kPer; ++j) {
+      h[j] = hist[kDigits - 1 - kPer * lane - j];
+      s += h[j];
     }
-    __syncthreads();
-    prefix = (prefix << 8) | (uint32_t)sh.out[0];
-    above = sh.out[1];
-    at = sh.out[2];
+    const u64 run = wave_scan(s);
+    const uint64_t hit = __ballot(reached(above + run, target, strict));
+    const uint64_t some = __ballot(s != 0);
+    // the first lane that reaches it, else the last that holds anything
+    const int who = hit ? __builtin_ctzll(hit) : some ? 63 - __builtin_clzll(some) : 63;
+    // in that lane: the first of its digits that reaches it, else its last that
+    // holds anything
+    u64 a = above + run - s, pick_above = a, pick_at = 0;
+    int pick = 0;
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (!found && h[j] != 0) {
+        pick = j;
+        pick_above = a;
+        pick_at = h[j];
+        found = reached(a + h[j], target, strict);
+      }
+      a += h[j];
+    }
+    prefix = (prefix << kDigitBits) |
+             (uint32_t)(kDigits - 1 - kPer * who -
+                        __builtin_amdgcn_readlane(pick, who));
+    above = lane64(pick_above, who);
+    at = lane64(pick_at, who);
   }
   return Sel{prefix, above, at};
 }
@@ -598,22 +604,26 @@ struct Ask {
   }
 };
 
+// The launcher points an absent parameter at u: the loads have no branch
+// between them and wait together.
 __device__ __forceinline__ Ask ask_of(const SampleParams& p, int64_t r) {
   Ask a;
-  a.T = p.temperature ? p.temperature[r] : 1.0f;
-  const float top_p = p.top_p ? p.top_p[r] : 1.0f;
-  const float min_p = p.min_p ? p.min_p[r] : 0.0f;
-  a.k = p.top_k ? p.top_k[r] : 0;
+  const float T = p.temperature[r], top_p = p.top_p[r], min_p = p.min_p[r];
+  const int32_t k = p.top_k[r];
   a.u = p.u[r];
+  a.T = p.has & SampleParams::kT ? T : 1.0f;
+  const float pp = p.has & SampleParams::kP ? top_p : 1.0f;
+  const float mp = p.has & SampleParams::kM ? min_p : 0.0f;
+  a.k = p.has & SampleParams::kK ? k : 0;
   // written so that a NaN fails
-  a.ok = a.T >= 0.0f && a.T < __builtin_huge_valf() && a.u >= 0.0f && a.u < 1.0f &&
-         top_p == top_p && min_p == min_p;
+  a.ok = a.T >= 0.0f && a.T < __builtin_huge_valf() && a.u >= 0.0f && a.u < 1.0f && pp == pp &&
+         mp == mp;
   a.greedy = a.T == 0.0f;
   a.has_k = a.k > 0 && a.k < p.V;
-  a.has_p = top_p < 1.0f;
-  a.has_min = min_p > 0.0f;
-  a.p = fmaxf(top_p, 0.0f);      // the first token is always kept
-  a.minp = fminf(min_p, 1.0f);   // and so are the maxima
+  a.has_p = pp < 1.0f;
+  a.has_min = mp > 0.0f;
+  a.p = fmaxf(pp, 0.0f);      // the first token is always kept
+  a.minp = fminf(mp, 1.0f);   // and so are the maxima
   return a;
 }
 
@@ -632,7 +642,8 @@ __device__ __forceinline__ Weights weights_of(const SampleParams& p, const Ask& 
 
 template <int DT>
 __device__ __forceinline__ Row<DT> row_of(const SampleParams& p, int64_t r) {
-  const int64_t i0 = r / p.d1, i1 = r - i0 * p.d1;
+  // below 2^22 rows
+  const uint32_t i0 = (uint32_t)r / (uint32_t)p.d1, i1 = (uint32_t)r - i0 * (uint32_t)p.d1;
   Row<DT> row;
   row.init(static_cast<const char*>(p.logits) + (i0 * p.ls0 + i1 * p.ls1) * (DT == 0 ? 4 : 2),
            p.V);
@@ -689,14 +700,27 @@ struct Group {
   }
 };
 
-// blockIdx.x: row, blockIdx.y: segment.
+// The workgroup's row and segment.  Segments run fastest: workgroups are dealt
+// round-robin over the XCDs, and rows differ in what they ask for, so each row's
+// segments go to all of them (with rows running fastest 256 mixed rows left some XCDs
+// with half as much again to do).
+__device__ __forceinline__ bool row_and_segment(const SampleParams& p, int64_t* r, int* seg) {
+  const uint32_t b = blockIdx.y * gridDim.x + blockIdx.x;
+  const uint32_t row = b / (uint32_t)p.segs;
+  *r = row;
+  *seg = (int)(b - row * (uint32_t)p.segs);
+  return row < p.rows;
+}
+
 template <int DT>
 __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleParams p) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
   __shared__ float sh[kThreads / 64];
-  const int64_t r = blockIdx.x;
-  const int seg = blockIdx.y, t = threadIdx.x;
+  int64_t r;
+  int seg;
+  if (!row_and_segment(p, &r, &seg)) return;
+  const int t = threadIdx.x;
   const R row = row_of<DT>(p, r);
   float z[kVec][R::VE];
   Group<DT> group;
@@ -736,18 +760,20 @@ __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleParams p) {
 
 // For rows without filters the segment's mass; for rows that go by the
 // histogram its tokens per bin (top-k), or its mass per bin and in all (top-p).
-// Top-p needs no token lighter than q0 = (1 - p) L / V, L a lower bound on
-// the row's mass (the sum over the segments' maxima): all such tokens together
-// weigh less than (1 - p) of the row, so its p-th part is reached before them.
-// They stay out of the histogram, which spares most of the LDS atomics.
+// Top-p needs no token lighter than q0 = (1 - p) / V: the row's mass is at least
+// 1, so all such tokens together weigh less than (1 - p) of it, and its p-th part is
+// reached before them.  They stay out of the histogram, which spares most of the
+// LDS atomics.
 template <int DT>
 __global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
   __shared__ u64 bins[kBins];
   __shared__ u64 part[kWaves];
-  const int64_t r = blockIdx.x;
-  const int seg = blockIdx.y, t = threadIdx.x;
+  int64_t r;
+  int seg;
+  if (!row_and_segment(p, &r, &seg)) return;
+  const int t = threadIdx.x;
   const Ask a = ask_of(p, r);
   const bool plain = a.plain(p.V), hist = a.hist(p.V);
   if (!plain && !hist) return;
@@ -762,19 +788,21 @@ __global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p
   u64 s = 0, q0 = 0;
   if (hist) {
     for (int b = t; b < kBins; b += kThreads) bins[b] = 0;
-    if (!a.has_k) {
-      u64 low = 0;
-      for (int i = t & 63; i < p.segs; i += 64) low += wt.all(seg_max[i]);
-      q0 = (u64)((1.0 - a.p) * (double)wave_sum(low) / (double)p.V);
-      q0 = q0 < 1 ? 1 : q0;
-    }
+    q0 = wt.fixed((1.0 - a.p) * p.inv_v);
+    q0 = q0 < 1 ? 1 : q0;
     __syncthreads();
   }
   float z[kVec][R::VE];
   group.get(row, v0, z);
   if (plain && !wt.inf) {
+    // eight at a time: enough to fill the pipeline, and registers for five workgroups
+    // per CU
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) s += wt.fixed(wt.real(z[j / R::VE][j % R::VE]));
+    for (int j0 = 0; j0 < kGroup; j0 += 8) {
+#pragma unroll
+      for (int j = j0; j < j0 + 8; ++j) s += wt.fixed(wt.real(z[j / R::VE][j % R::VE]));
+      __builtin_amdgcn_sched_barrier(0);
+    }
   } else if (hist && a.has_k) {
 #pragma unroll
     for (int j = 0; j < kGroup; ++j) {
@@ -782,12 +810,19 @@ __global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p
       if (v != kNegInf) atomicAdd(&bins[bin_of(m, v)], (u64)1);
     }
   } else if (!wt.inf) {
+    // eight weights at a time, interleaved, then their atomics
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      const float v = z[j / R::VE][j % R::VE];
-      const u64 q = wt.fixed(wt.real(v));
-      s += q;
-      if (q >= q0) atomicAdd(&bins[bin_of(m, v)], q);
+    for (int j0 = 0; j0 < kGroup; j0 += 8) {
+      u64 q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        q[j] = wt.fixed(wt.real(z[(j0 + j) / R::VE][(j0 + j) % R::VE]));
+        s += q[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (q[j] >= q0) atomicAdd(&bins[bin_of(m, z[(j0 + j) / R::VE][(j0 + j) % R::VE])], q[j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   } else {
     // only the infinite tokens weigh, all in bin 0
@@ -1096,6 +1131,7 @@ __device__ __forceinline__ int64_t pick_in_segment(const Row<DT>& row, int seg, 
   constexpr int kVec = kGroup / R::VE;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int c0 = seg * (kThreads * kVec);
+  __syncthreads();  // the scratch may still be read
   {
     float z[kVec][R::VE];
     Group<DT> group;
@@ -1218,7 +1254,8 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleParams p) {
       before += lane64(run, 63);
     }
     const int64_t token = pick_in_segment<DT>(row, seg, before, goal, sh, [&](int64_t, float z) {
-      return a.greedy ? (u64)(z == m) : wt.all(z);
+      const u64 q = wt.all(z);
+      return a.greedy ? (u64)(z == m) : q;
     });
     if (t == 0) write_out<DT>(p, r, row, a, m, token, total);
     return;
@@ -1316,9 +1353,11 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kept_kernel(SampleParams p
   __shared__ u64 part[kWaves];
   __shared__ uint32_t cnt[kWaves];
   __shared__ uint32_t base;
-  const int64_t r = blockIdx.x;
+  int64_t r;
+  int seg;
+  if (!row_and_segment(p, &r, &seg)) return;
   if (p.state[r].what != kThreshold) return;
-  const int seg = blockIdx.y, t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const Ask a = ask_of(p, r);
   const R row = row_of<DT>(p, r);
   const int v0 = seg * (kThreads * kVec) + t;
@@ -1334,8 +1373,10 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kept_kernel(SampleParams p
 #pragma unroll
   for (int j = 0; j < kGroup; ++j) {
     const float v = z[j / R::VE][j % R::VE], d = distance(m, v);
-    if (d < lo) s += wt.kept(v);
+    const u64 q = wt.kept(v);
+    s += d < lo ? q : 0;
     in |= (v != kNegInf && d >= lo && d <= hi ? 1u : 0u) << j;
+    if (j % 8 == 7) __builtin_amdgcn_sched_barrier(0);
   }
   s = wave_sum(s);
   const uint32_t c = __builtin_popcount(in);
@@ -1529,9 +1570,8 @@ __global__ __launch_bounds__(kThreads) void sample_rest_kernel(SampleParams p) {
     d.total = total;
     d.token = pick_in_segment<DT>(row, seg, before, goal, sh, [&](int64_t i, float z) -> u64 {
       const uint32_t k = R::key(z);
-      return distance(m, z) < st.lo || k > d.tau || (k == d.tau && i <= (int64_t)d.last)
-                 ? wt.kept(z)
-                 : 0;
+      const u64 q = wt.kept(z);
+      return distance(m, z) < st.lo || k > d.tau || (k == d.tau && i <= (int64_t)d.last) ? q : 0;
     });
   }
   if (threadIdx.x == 0) write_out<DT>(p, r, row, a, m, d.token, d.total);
@@ -1550,6 +1590,11 @@ static int weight_bits(int64_t V) {
 static int64_t segments(int64_t V) { return (V + 8 + kSeg - 1) / kSeg; }
 
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+bool sample_size_ok(int64_t N, int64_t V) {
+  return N < ((int64_t)1 << 22) && V <= ((int64_t)1 << 28) &&
+         N * segments(V) < ((int64_t)1 << 31);
+}
 
 size_t sample_workspace_bytes(int64_t N, int64_t V) {
   const size_t rows = (size_t)N, s = rows * (size_t)segments(V);
@@ -1583,11 +1628,19 @@ hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
   p.seg_sum = reinterpret_cast<unsigned long long*>(take(s * 8));
   p.hist = reinterpret_cast<unsigned long long*>(take(rows * kBins * 8));
   p.state = reinterpret_cast<SampleState*>(take(rows * sizeof(SampleState)));
-  const dim3 seg_grid((unsigned)N, (unsigned)p.segs);
+  p.rows = (uint32_t)N;
+  const dim3 seg_grid = grid2(N * p.segs);
   // rows of at most kCap tokens are gathered whole; without filters no row has
   // more candidates than LDS holds
   const bool mass = p.V > kCap;
   const bool rest = mass && (p.top_k || p.top_p || p.min_p);
+  p.has = (p.temperature ? SampleParams::kT : 0) | (p.top_k ? SampleParams::kK : 0) |
+          (p.top_p ? SampleParams::kP : 0) | (p.min_p ? SampleParams::kM : 0);
+  if (!p.temperature) p.temperature = p.u;
+  if (!p.top_k) p.top_k = reinterpret_cast<const int32_t*>(p.u);
+  if (!p.top_p) p.top_p = p.u;
+  if (!p.min_p) p.min_p = p.u;
+  p.inv_v = 1.0 / (double)p.V;
   if (!rest) p.state = nullptr;
   auto run = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;

@@ -1095,13 +1095,8 @@ int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uin
                                              static_cast<hipStream_t>(stream)));
 }
 
-namespace {
-constexpr int64_t kSampleRows = ((int64_t)1 << 22) - 1;  // workgroups of 1024 in one grid axis
-constexpr int64_t kSampleVocab = (int64_t)1 << 28;       // segments in the other
-}  // namespace
-
 size_t ce_sample_workspace_size(int64_t N, int64_t V) {
-  if (N < 0 || N > kSampleRows || V <= 0 || V > kSampleVocab) return 0;
+  if (N < 0 || V <= 0 || !vce::sample_size_ok(N, V)) return 0;
   return vce::sample_workspace_bytes(N, V);
 }
 
@@ -1113,7 +1108,7 @@ int ce_sample(const void* logits, int dtype, int64_t d0, int64_t d1, int64_t V, 
   if (d0 < 0 || d1 < 0 || V <= 0 || ls0 < 0 || ls1 < 0) return VCE_EINVAL;
   int64_t N, span0, span1;
   if (!mul_ok(d0, d1, &N) || N > (int64_t)INT32_MAX) return VCE_EINVAL;
-  if (V > kSampleVocab || N > kSampleRows) return VCE_EUNSUPPORTED;
+  if (!vce::sample_size_ok(N, V)) return VCE_EUNSUPPORTED;
   if (N == 0) return VCE_OK;
   if (!logits || !u || !token || !workspace) return VCE_EINVAL;
   const int64_t es = dtype_size(dtype);

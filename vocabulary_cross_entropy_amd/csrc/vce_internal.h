@@ -249,8 +249,11 @@ struct SampleParams {
   float* logprob;  // optional (N)
   // set by the launcher: the weights' fixed point and polynomial, and the
   // workspace's parts
-  double magic = 0.0, unit = 0.0;
+  enum { kT = 1, kK = 2, kP = 4, kM = 8 };
+  int has = 0;  // which of the optional parameters are given
+  double magic = 0.0, unit = 0.0, inv_v = 0.0;
   double poly[9] = {};
+  uint32_t rows = 0;
   int segs = 0;                             // segments per row
   float* group_max = nullptr;               // (N, segs, 256)
   float* seg_max = nullptr;                 // (N, segs)
@@ -259,6 +262,8 @@ struct SampleParams {
   SampleState* state = nullptr;             // (N), NULL where every row is done in one kernel
 };
 
+// Rows times segments stay below 2^31.
+bool sample_size_ok(int64_t N, int64_t V);
 size_t sample_workspace_bytes(int64_t N, int64_t V);
 hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
                          hipStream_t stream);
