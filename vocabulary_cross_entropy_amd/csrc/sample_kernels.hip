@@ -48,11 +48,14 @@ namespace vce {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a segment's workgroup
 constexpr int kWaves = kThreads / 64;
+constexpr int kRowThreads = 512;  // of a row's
+constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kBins = 2048;
 constexpr uint32_t kBinBase = 119u << 7;  // bits of 2^-8 over 2^16: bin 0 lies below
 constexpr int kCap = 4096;                // candidates held in LDS
+constexpr int kRank = 256;                // ranked by counting: every one against every other
 constexpr int kLoads = 4;                 // vectors in flight per thread
 constexpr int kGroup = 32;                // tokens per thread of a segment
 constexpr int kSeg = kThreads * kGroup;
@@ -99,15 +102,18 @@ struct Row {
       }
     }
   }
-  // The same, with -inf for a vector past the row.  One load is issued whatever the
-  // case, so that several calls wait together.
-  __device__ __forceinline__ void load_or_none(int i, float* z) const {
+  // The same in two parts, so that several vectors' loads wait together: the load
+  // where the row fills the vector, then its logits, -inf for a vector past the row.
+  __device__ __forceinline__ bool full(int i) const {
     const int64_t e = first(i);
-    const bool full = e >= 0 && e + VE <= V;
-    u32x4_t raw{0, 0, 0, 0};
-    if (full) raw = *reinterpret_cast<const u32x4_t*>(base + e * (DT == 0 ? 4 : 2));
-    if (full) {
-      unpack(raw, z);
+    return e >= 0 && e + VE <= V;
+  }
+  __device__ __forceinline__ u32x4_t raw(int i) const {
+    return *reinterpret_cast<const u32x4_t*>(base + first(i) * (DT == 0 ? 4 : 2));
+  }
+  __device__ __forceinline__ void take(int i, const u32x4_t& w, float* z) const {
+    if (full(i)) {
+      unpack(w, z);
     } else if (i < nvec) {
       load(i, z);
     } else {
@@ -221,17 +227,17 @@ struct Weights {
 
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;  // of a radix selection
 
-constexpr int kGroupBatch = 16;  // segments whose group maxima a thread loads at once
+constexpr int kGroupBatch = 8;   // group maxima that a thread loads at once
 constexpr int kKeepSegs = 1024;  // segments of a row that sample_rest_kernel draws from
 
 struct Scratch {
   union {
     u64 hist[3 * kDigits];
-    uint16_t group[kGroupBatch * kThreads];
+    uint16_t group[kGroupBatch * kRowThreads];
     u64 keep[kKeepSegs];
   };
-  u64 wave[kWaves];
-  u64 wave2[kWaves];
+  u64 wave[kRowWaves];
+  u64 wave2[kRowWaves];
   u64 out[4];
   uint32_t n;
 };
@@ -287,7 +293,7 @@ __device__ __forceinline__ u64 lane64(u64 v, int lane) {
 __device__ __forceinline__ u64 wave_sum(u64 v) { return lane64(wave_scan(v), 63); }
 
 // Sum over the workgroup, the same in every thread.
-template <int NW, class S>
+template <class S>
 __device__ __forceinline__ u64 block_sum(u64 v, S& sh) {
   v = wave_sum(v);
   __syncthreads();
@@ -295,7 +301,7 @@ __device__ __forceinline__ u64 block_sum(u64 v, S& sh) {
   __syncthreads();
   v = 0;
 #pragma unroll
-  for (int i = 0; i < NW; ++i) v += sh.wave[i];
+  for (int i = 0; i < kRowWaves; ++i) v += sh.wave[i];
   return v;
 }
 
@@ -323,7 +329,7 @@ __device__ __forceinline__ Sel radix_select(int bits, double target, bool strict
   uint32_t prefix = 0;
   u64 above = 0, at = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < kDigits; i += kThreads) sh.hist[i] = 0;
+  for (int i = threadIdx.x; i < kDigits; i += kRowThreads) sh.hist[i] = 0;
   __syncthreads();
   int buf = 0;
   for (int shift = (bits - 1) / kDigitBits * kDigitBits; shift >= 0; shift -= kDigitBits) {
@@ -336,7 +342,7 @@ __device__ __forceinline__ Sel radix_select(int bits, double target, bool strict
     // passed the barrier since
     buf = buf == 2 ? 0 : buf + 1;
     u64* clear = sh.hist + buf * kDigits;
-    for (int i = threadIdx.x; i < kDigits; i += kThreads) clear[i] = 0;
+    for (int i = threadIdx.x; i < kDigits; i += kRowThreads) clear[i] = 0;
     __syncthreads();
     u64 h[kPer], s = 0;
 #pragma unroll
@@ -386,7 +392,7 @@ __device__ __forceinline__ int64_t locate(const Row<DT>& row, int c0, int c1, Sh
   double goal = 0.0;
   bool first = true;
   while (true) {
-    const int chunk = (c1 - c0 + kWaves - 1) / kWaves;
+    const int chunk = (c1 - c0 + kRowWaves - 1) / kRowWaves;
     const int a = min(c0 + wave * chunk, c1), b = min(a + chunk, c1);
     u64 s = 0;
     row.each(a, b, lane, 64, [&](int64_t e, const float* z) {
@@ -400,13 +406,13 @@ __device__ __forceinline__ int64_t locate(const Row<DT>& row, int c0, int c1, Sh
     if (first) {
       u64 all = 0;
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) all += sh.wave[i];
+      for (int i = 0; i < kRowWaves; ++i) all += sh.wave[i];
       *total = all;
       goal = target(all);
       first = false;
     }
     int w = -1;
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < kRowWaves; ++i) {
       const u64 t = sh.wave[i];
       if ((double)(before + t) > goal && t != 0) {
         w = i;
@@ -466,12 +472,12 @@ __device__ __forceinline__ uint32_t bin_of(float m, float z) {
 // Histogram of the row over bin_of: tokens per bin, and with MASS their weights.
 template <int DT, bool MASS>
 __device__ __forceinline__ void histogram(const Row<DT>& row, const Weights& wt, Shared& sh) {
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+  for (int i = threadIdx.x; i < kBins; i += kRowThreads) {
     sh.count[i] = 0;
     sh.mass[i] = 0;
   }
   __syncthreads();
-  row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t, const float* z) {
+  row.each(0, row.nvec, threadIdx.x, kRowThreads, [&](int64_t, const float* z) {
 #pragma unroll
     for (int j = 0; j < Row<DT>::VE; ++j) {
       if (z[j] == kNegInf) continue;
@@ -498,7 +504,7 @@ struct BinSel {
 // target(total); the last one if it never does.
 template <class Amount, class Target>
 __device__ __forceinline__ BinSel scan_bins(Shared& sh, Amount amount, Target target) {
-  constexpr int kPer = kBins / kThreads;
+  constexpr int kPer = kBins / kRowThreads;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   u64 s = 0;
   uint32_t n = 0;
@@ -516,7 +522,7 @@ __device__ __forceinline__ BinSel scan_bins(Shared& sh, Amount amount, Target ta
   __syncthreads();
   u64 base = 0, nbase = 0, total = 0;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
+  for (int i = 0; i < kRowWaves; ++i) {
     if (i < wave) {
       base += sh.wave[i];
       nbase += sh.wave2[i];
@@ -526,7 +532,7 @@ __device__ __forceinline__ BinSel scan_bins(Shared& sh, Amount amount, Target ta
   const double goal = target(total);
   // exactly one thread's bins hold the crossing: before it not reached, with it reached
   const u64 before = base + run - s, upto = base + run;
-  if (t == kThreads - 1) {
+  if (t == kRowThreads - 1) {
     sh.out[0] = kBins - 1;
     sh.out[1] = total - amount(kBins - 1);
     sh.out[2] = nbase + cnt;
@@ -567,7 +573,7 @@ __device__ __forceinline__ void gather(const Row<DT>& row, const Weights& wt, Sh
                        uint32_t hi) {
   if (threadIdx.x == 0) sh.n = 0;
   __syncthreads();
-  row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t e, const float* z) {
+  row.each(0, row.nvec, threadIdx.x, kRowThreads, [&](int64_t e, const float* z) {
 #pragma unroll
     for (int j = 0; j < Row<DT>::VE; ++j) {
       if (z[j] == kNegInf) continue;
@@ -664,21 +670,22 @@ __device__ __forceinline__ float row_max(const float* seg_max, int n) {
   return __any(nan) ? __builtin_nanf("") : m;
 }
 
-// The 32 tokens of a thread of a segment: vectors v0, v0 + 256, ... of the row,
-// -inf past its ends.  The loads are issued by load() and waited for by get().
-template <int DT>
+// The tokens of a thread of a segment that NT threads share: vectors v0, v0 + NT,
+// ... of the row, -inf past its ends.  The loads are issued by load() and waited
+// for by get().
+template <int DT, int NT>
 struct Group {
   typedef Row<DT> R;
-  static constexpr int kVec = kGroup / R::VE;
+  static constexpr int kVec = kSeg / NT / R::VE;
   u32x4_t raw[kVec];
   bool full;
   __device__ __forceinline__ void load(const R& row, int v0) {
-    const int last = v0 + (kVec - 1) * kThreads;
+    const int last = v0 + (kVec - 1) * NT;
     full = last < (int)((row.V + row.off) / R::VE) && (v0 > 0 || row.off == 0);
     if (full) {
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
-        raw[j] = *reinterpret_cast<const u32x4_t*>(row.base + row.first(v0 + j * kThreads) *
+        raw[j] = *reinterpret_cast<const u32x4_t*>(row.base + row.first(v0 + j * NT) *
                                                                   (DT == 0 ? 4 : 2));
     }
   }
@@ -689,8 +696,8 @@ struct Group {
     } else {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        if (v0 + j * kThreads < row.nvec) {
-          row.load(v0 + j * kThreads, z[j]);
+        if (v0 + j * NT < row.nvec) {
+          row.load(v0 + j * NT, z[j]);
         } else {
 #pragma unroll
           for (int q = 0; q < R::VE; ++q) z[j][q] = kNegInf;
@@ -723,7 +730,7 @@ __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleParams p) {
   const int t = threadIdx.x;
   const R row = row_of<DT>(p, r);
   float z[kVec][R::VE];
-  Group<DT> group;
+  Group<DT, kThreads> group;
   group.load(row, seg * (kThreads * kVec) + t);
   group.get(row, seg * (kThreads * kVec) + t, z);
   float m = kNegInf;
@@ -779,7 +786,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p
   if (!plain && !hist) return;
   const R row = row_of<DT>(p, r);
   const int v0 = seg * (kThreads * kVec) + t;
-  Group<DT> group;
+  Group<DT, kThreads> group;
   group.load(row, v0);
   const float* seg_max = p.seg_max + r * p.segs;
   const float m = row_max(seg_max, p.segs);
@@ -868,23 +875,26 @@ __device__ __forceinline__ Entry entry_of(const Weights& wt, float z, uint32_t i
 // m - z, 0 for z = m also where both are infinite.
 __device__ __forceinline__ float distance(float m, float z) { return z == m ? 0.0f : m - z; }
 
-// The maxima of this thread's groups, 16 segments at a time with their loads in
-// flight together; the first 16 stay in registers.
+// The maxima of the row's groups, kGroupBatch per thread at a time with their
+// loads in flight together; the first ones stay in registers.
 struct GroupMax {
+  static constexpr int kBatch = kGroupBatch * kRowThreads;
   const float* gm;  // (segs, 256) of the row
-  int segs;
+  int n;
   float first[kGroupBatch];
   __device__ __forceinline__ void load(int g0, float (&top)[kGroupBatch]) const {
 #pragma unroll
-    for (int i = 0; i < kGroupBatch; ++i)
-      top[i] = g0 + i < segs ? gm[(g0 + i) * kThreads + threadIdx.x] : kNegInf;
+    for (int i = 0; i < kGroupBatch; ++i) {
+      const int g = g0 + i * kRowThreads + (int)threadIdx.x;
+      top[i] = g < n ? gm[g] : kNegInf;
+    }
   }
-  __device__ __forceinline__ void init(const float* p, int n) {
+  __device__ __forceinline__ void init(const float* p, int segs) {
     gm = p;
-    segs = n;
+    n = segs * kThreads;
     load(0, first);
   }
-  // f(group, maximum) for the groups of segments g0 .. g0 + 15.
+  // f(group, maximum) for the groups g0 .. g0 + kBatch - 1, counted from g0.
   template <class F>
   __device__ __forceinline__ void each(int g0, F f) const {
     float top[kGroupBatch];
@@ -893,7 +903,7 @@ struct GroupMax {
     if (g0) load(g0, top);
 #pragma unroll
     for (int i = 0; i < kGroupBatch; ++i)
-      if (top[i] != kNegInf) f(i * kThreads + threadIdx.x, top[i]);
+      if (top[i] != kNegInf) f(i * kRowThreads + (int)threadIdx.x, top[i]);
   }
 };
 
@@ -909,9 +919,10 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Grou
                                                   uint32_t max_groups, PickShared& sh) {
   typedef Row<DT> R;
   constexpr int kVec = kGroup / R::VE;
+  constexpr int kItems = 2;  // vectors in flight per thread
   __syncthreads();
   if (threadIdx.x == 0) sh.n = 0;
-  for (int g0 = 0; g0 < groups.segs; g0 += kGroupBatch) {
+  for (int g0 = 0; g0 < groups.n; g0 += GroupMax::kBatch) {
     if (threadIdx.x == 0) sh.n_groups = 0;
     __syncthreads();
     groups.each(g0, [&](int i, float top) {
@@ -921,34 +932,47 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Grou
     // each listed group holds a token at least
     if (sh.n_groups > max_groups || sh.n + sh.n_groups > kCap) return kCap + 1;
     const int items = (int)sh.n_groups * kVec;
-    for (int i0 = threadIdx.x; i0 < items; i0 += kLoads * kThreads) {
-      float z[kLoads][R::VE];
-      int v[kLoads];
+    for (int b0 = 0; b0 < items; b0 += kItems * kRowThreads) {
+      const int i0 = b0 + threadIdx.x;
+      float z[kItems][R::VE];
+      int v[kItems];
+      u32x4_t raw[kItems];
 #pragma unroll
-      for (int l = 0; l < kLoads; ++l) {
-        const int i = i0 + l * kThreads;
+      for (int l = 0; l < kItems; ++l) {
+        const int i = i0 + l * kRowThreads;
         v[l] = row.nvec;
         if (i < items) {
-          const int g = sh.group[i / kVec];
-          v[l] = (g0 + g / kThreads) * (kThreads * kVec) + (i % kVec) * kThreads + g % kThreads;
+          const int g = g0 + sh.group[i / kVec];
+          v[l] = g / kThreads * (kThreads * kVec) + (i % kVec) * kThreads + g % kThreads;
         }
-        row.load_or_none(v[l], z[l]);
+        raw[l] = u32x4_t{0, 0, 0, 0};
+        if (row.full(v[l])) raw[l] = row.raw(v[l]);
       }
 #pragma unroll
-      for (int l = 0; l < kLoads; ++l) {
-        uint32_t in = 0;
+      for (int l = 0; l < kItems; ++l) row.take(v[l], raw[l], z[l]);
+      // places for all of the wavefront's hits at once
+      uint32_t in = 0;
 #pragma unroll
-        for (int q = 0; q < R::VE; ++q)
-          in |= (z[l][q] != kNegInf && distance(wt.m, z[l][q]) <= hi ? 1u : 0u) << q;
-        while (in) {
-          const int q = __builtin_ctz(in);
-          in &= in - 1;
-          float x = z[l][0];
+      for (int l = 0; l < kItems; ++l)
 #pragma unroll
-          for (int j = 1; j < R::VE; ++j) x = q == j ? z[l][j] : x;
-          const uint32_t at = atomicAdd(&sh.n, 1u);
-          if (at < kCap)
-            sh.list[at] = Entry{__float_as_uint(x), (uint32_t)(row.first(v[l]) + q), 0};
+        for (int q = 0; q < R::VE; ++q) {
+          const float x = z[l][q];
+          in |= (x != kNegInf && distance(wt.m, x) <= hi ? 1u : 0u) << (l * R::VE + q);
+        }
+      const uint32_t c = __builtin_popcount(in);
+      const uint32_t run = (uint32_t)wave_scan(c);
+      uint32_t at = 0;
+      if ((threadIdx.x & 63) == 63) at = atomicAdd(&sh.n, run);
+      at = (uint32_t)__builtin_amdgcn_readlane((int)at, 63) + run - c;
+#pragma unroll
+      for (int l = 0; l < kItems; ++l) {
+        const uint32_t e = (uint32_t)row.first(v[l]);
+#pragma unroll
+        for (int q = 0; q < R::VE; ++q) {
+          if ((in >> (l * R::VE + q)) & 1u) {
+            if (at < kCap) sh.list[at] = Entry{__float_as_uint(z[l][q]), e + q, 0};
+            ++at;
+          }
         }
       }
     }
@@ -957,7 +981,7 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Grou
   }
   // the weights last, when every thread has its share of them
   const uint32_t n = sh.n;
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+  for (uint32_t i = threadIdx.x; i < n; i += kRowThreads)
     sh.list[i] = entry_of<DT>(wt, __uint_as_float(sh.list[i].key), sh.list[i].idx);
   __syncthreads();
   return n;
@@ -978,24 +1002,24 @@ struct Drawn {
 template <int DT>
 __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int64_t V, uint32_t n,
                                            u64 mass, bool threshold, u64 above, PickShared& sh) {
-  constexpr int NW = kWaves;
   const uint32_t t = threadIdx.x;
   Drawn d;
   d.token = 0;
   d.total = 0;
   d.tau = 0;
   d.last = 0xffffffffu;
-  if (n <= kThreads && !threshold) {
+  if (n <= kRank && !threshold) {
     // one candidate per thread: its rank and the weight ranked before it
     const bool mine = t < n;
     const Entry e = mine ? sh.list[t] : Entry{0, 0, 0};
     const u64 q = e.q & ~kKeptBit;
+    const uint32_t n_wave = __any(mine) ? n : 0;  // a wavefront without any skips the loops
     // four entries at a time, the last ones filled up with none
     if (t < 4) sh.list[n + t] = Entry{0, 0xffffffffu, 0};
     __syncthreads();
     uint32_t rank = 0;
     u64 before = 0;
-    for (uint32_t j = 0; j < n; j += 4) {
+    for (uint32_t j = 0; j < n_wave; j += 4) {
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i) {
         const Entry o = sh.list[j + i];
@@ -1006,16 +1030,16 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
     }
     bool keep = mine && (!a.has_k || rank < (uint32_t)a.k);
     if (a.has_p) {
-      if (a.has_k) mass = block_sum<NW>(keep ? q : 0, sh);
+      if (a.has_k) mass = block_sum(keep ? q : 0, sh);
       keep = keep && (rank == 0 || (double)before < a.p * (double)mass);
     }
     keep = keep && (e.q & kKeptBit);
-    d.total = block_sum<NW>(keep ? q : 0, sh);  // a barrier: the list has been read
+    d.total = block_sum(keep ? q : 0, sh);  // a barrier: the list has been read
     if (mine) sh.list[t].q = keep ? q : 0;
     if (t == 0) sh.out[0] = 0;
     __syncthreads();
     u64 upto = 0;
-    for (uint32_t j = 0; j < n; j += 4) {
+    for (uint32_t j = 0; j < n_wave; j += 4) {
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i) {
         const Entry o = sh.list[j + i];
@@ -1034,7 +1058,7 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
   // keys count from the least one: fewer bits to select by, and the first eight
   // tell the candidates apart (equal digits queue at one LDS address)
   uint32_t key0 = 0xffffffffu, key1 = 0;
-  for (uint32_t i = t; i < n; i += kThreads) {
+  for (uint32_t i = t; i < n; i += kRowThreads) {
     key0 = min(key0, sh.list[i].key);
     key1 = max(key1, sh.list[i].key);
   }
@@ -1047,7 +1071,7 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
   if ((t & 63) == 0) sh.wave[t >> 6] = ((u64)key1 << 32) | key0;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < NW; ++i) {
+  for (int i = 0; i < kRowWaves; ++i) {
     key0 = min(key0, (uint32_t)sh.wave[i]);
     key1 = max(key1, (uint32_t)(sh.wave[i] >> 32));
   }
@@ -1064,30 +1088,30 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
       if (!a.has_p) continue;
       if (a.has_k) {
         u64 v = 0;
-        for (uint32_t i = t; i < n; i += kThreads)
+        for (uint32_t i = t; i < n; i += kRowThreads)
           if (ties == ~(u64)0 || sh.list[i].key > tau) v += sh.list[i].q & ~kKeptBit;
-        mass = block_sum<NW>(v, sh);
+        mass = block_sum(v, sh);
         if (ties != ~(u64)0) mass += ties * wt.all(key_value<DT>(tau));
       }
       goal = a.p * (double)mass - (double)above;
     } else if (stage == 2) {  // the last tie kept, where not all are
       if (ties == ~(u64)0) continue;
       u64 c = 0;
-      for (uint32_t i = t; i < n; i += kThreads) c += sh.list[i].key == tau;
-      if (ties >= block_sum<NW>(c, sh)) continue;
+      for (uint32_t i = t; i < n; i += kRowThreads) c += sh.list[i].key == tau;
+      if (ties >= block_sum(c, sh)) continue;
       goal = (double)ties;
     } else {  // the token
       u64 v = 0;
-      for (uint32_t i = t; i < n; i += kThreads) {
+      for (uint32_t i = t; i < n; i += kRowThreads) {
         const Entry e = sh.list[i];
         if ((e.q & kKeptBit) && (e.key > tau || (e.key == tau && e.idx <= last)))
           v += e.q & ~kKeptBit;
       }
-      d.total = block_sum<NW>(v, sh);
+      d.total = block_sum(v, sh);
       goal = (double)a.u * (double)d.total;
     }
     Sel s = radix_select(stage < 2 ? key_bits : idx_bits, goal, stage == 3, sh, [&](auto f) {
-      for (uint32_t i = t; i < n; i += kThreads) {
+      for (uint32_t i = t; i < n; i += kRowThreads) {
         const Entry e = sh.list[i];
         const bool in = stage == 0   ? true
                         : stage == 1 ? e.key >= tau
@@ -1104,8 +1128,8 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
       ties = (u64)a.k - s.above;
     } else if (stage == 1) {
       u64 c = 0;
-      for (uint32_t i = t; i < n; i += kThreads) c += sh.list[i].key == s.key;
-      c = block_sum<NW>(c, sh);
+      for (uint32_t i = t; i < n; i += kRowThreads) c += sh.list[i].key == s.key;
+      c = block_sum(c, sh);
       if (s.key == tau && ties < c) c = ties;
       ties = ties_needed(s.above, wt.all(key_value<DT>(s.key)), c, goal);
       tau = s.key;
@@ -1128,27 +1152,28 @@ template <int DT, class Amount>
 __device__ __forceinline__ int64_t pick_in_segment(const Row<DT>& row, int seg, u64 before,
                                                    double goal, Scratch& sh, Amount amount) {
   typedef Row<DT> R;
-  constexpr int kVec = kGroup / R::VE;
+  typedef Group<DT, kRowThreads> G;
+  constexpr int kVec = G::kVec;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int c0 = seg * (kThreads * kVec);
+  const int c0 = seg * (kSeg / R::VE);
   __syncthreads();  // the scratch may still be read
   {
     float z[kVec][R::VE];
-    Group<DT> group;
+    G group;
     group.load(row, c0 + t);
     group.get(row, c0 + t, z);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      const int64_t e = row.first(c0 + t + j * kThreads);
+      const int64_t e = row.first(c0 + t + j * kRowThreads);
       u64 s = 0;
 #pragma unroll
       for (int q = 0; q < R::VE; ++q) s += amount(e + q, z[j][q]);
       s = wave_sum(s);
-      if (lane == 0) sh.hist[j * kWaves + wave] = s;
+      if (lane == 0) sh.hist[j * kRowWaves + wave] = s;
     }
   }
   __syncthreads();
-  const u64 mine = lane < kVec * kWaves ? sh.hist[lane] : 0;
+  const u64 mine = lane < kVec * kRowWaves ? sh.hist[lane] : 0;
   const u64 run = wave_scan(mine);
   const uint64_t hit = __ballot(mine != 0 && (double)(before + run) > goal);
   const int chunk = hit ? __builtin_ctzll(hit) : 0;
@@ -1207,10 +1232,9 @@ __device__ __forceinline__ void write_out(const SampleParams& p, int64_t r, cons
 enum State : uint32_t { kDone = 0, kThreshold = 1, kRow = 2 };
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleParams p) {
+__global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p) {
   __shared__ PickShared sh;
   typedef Row<DT> R;
-  constexpr int NW = kWaves;
   const int64_t r = blockIdx.x;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   GroupMax groups;
@@ -1269,14 +1293,14 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleParams p) {
     // the bin of the distance where the count or the mass is reached, 8 bins a
     // thread: of the row's histogram, or of the group maxima (k groups with
     // maxima of at least the k-th largest hold k tokens as large)
-    constexpr int kPer = kBins / kThreads;
+    constexpr int kPer = kBins / kRowThreads;
     u64* bins = reinterpret_cast<u64*>(sh.list);  // the list comes later
     if (a.hist(p.V)) {
-      for (int i = t; i < kBins; i += kThreads) bins[i] = p.hist[r * kBins + i];
+      for (int i = t; i < kBins; i += kRowThreads) bins[i] = p.hist[r * kBins + i];
     } else {
-      for (int i = t; i < kBins; i += kThreads) bins[i] = 0;
+      for (int i = t; i < kBins; i += kRowThreads) bins[i] = 0;
       __syncthreads();
-      for (int g0 = 0; g0 < p.segs; g0 += kGroupBatch)
+      for (int g0 = 0; g0 < groups.n; g0 += GroupMax::kBatch)
         groups.each(g0, [&](int, float g) { atomicAdd(&bins[bin_of(m, g)], (u64)1); });
     }
     if (!a.has_k) {
@@ -1336,8 +1360,8 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleParams p) {
   }
   if (a.list_all(p.V) && a.has_p && !a.has_k) {
     u64 v = 0;
-    for (uint32_t i = t; i < n; i += kThreads) v += sh.list[i].q & ~kKeptBit;
-    mass = block_sum<NW>(v, sh);
+    for (uint32_t i = t; i < n; i += kRowThreads) v += sh.list[i].q & ~kKeptBit;
+    mass = block_sum(v, sh);
   }
   const Drawn d = draw_list<DT>(a, wt, p.V, n, mass, false, 0, sh);
   if (t == 0) write_out<DT>(p, r, row, a, m, d.token, d.total);
@@ -1361,7 +1385,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kept_kernel(SampleParams p
   const Ask a = ask_of(p, r);
   const R row = row_of<DT>(p, r);
   const int v0 = seg * (kThreads * kVec) + t;
-  Group<DT> group;
+  Group<DT, kThreads> group;
   group.load(row, v0);
   const float m = row_max(p.seg_max + r * p.segs, p.segs);
   const Weights wt = weights_of(p, a, m);
@@ -1417,10 +1441,10 @@ __device__ __forceinline__ Drawn draw_row(const Row<DT>& row, const Ask& a, cons
   // f(z, index) over the list, or over the row's tokens of bin b
   auto over = [&](bool list, uint32_t b, auto f) {
     if (list) {
-      for (uint32_t i = threadIdx.x; i < n_list; i += kThreads)
+      for (uint32_t i = threadIdx.x; i < n_list; i += kRowThreads)
         f(__uint_as_float(sh.key[i]), (int64_t)sh.idx[i]);
     } else {
-      row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t e, const float* z) {
+      row.each(0, row.nvec, threadIdx.x, kRowThreads, [&](int64_t e, const float* z) {
 #pragma unroll
         for (int j = 0; j < R::VE; ++j) {
           if (z[j] == kNegInf) continue;
@@ -1451,12 +1475,12 @@ __device__ __forceinline__ Drawn draw_row(const Row<DT>& row, const Ask& a, cons
       ties = (u64)a.k - b.above - s.above;
       if (a.has_p) {
         u64 v = 0;
-        row.each(0, row.nvec, threadIdx.x, kThreads, [&](int64_t, const float* z) {
+        row.each(0, row.nvec, threadIdx.x, kRowThreads, [&](int64_t, const float* z) {
 #pragma unroll
           for (int j = 0; j < R::VE; ++j)
             if (R::key(z[j]) > tau) v += wt.all(z[j]);
         });
-        mass_k = block_sum<kWaves>(v, sh) + ties * wt.all(key_value<DT>(tau));
+        mass_k = block_sum(v, sh) + ties * wt.all(key_value<DT>(tau));
       }
     }
   }
@@ -1479,7 +1503,7 @@ __device__ __forceinline__ Drawn draw_row(const Row<DT>& row, const Ask& a, cons
     });
     u64 n = 0;
     over(list, b.bin, [&](float z, int64_t) { n += R::key(z) == s.key; });
-    n = block_sum<kWaves>(n, sh);
+    n = block_sum(n, sh);
     if (select && s.key == tau_k && ties < n) n = ties;
     ties = ties_needed(b.above + s.above, wt.all(key_value<DT>(s.key)), n, goal);
     tau = s.key;
@@ -1504,7 +1528,7 @@ __device__ __forceinline__ Drawn draw_row(const Row<DT>& row, const Ask& a, cons
 }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void sample_rest_kernel(SampleParams p) {
+__global__ __launch_bounds__(kRowThreads) void sample_rest_kernel(SampleParams p) {
   __shared__ union {
     PickShared pick;
     Shared row;
@@ -1525,7 +1549,7 @@ __global__ __launch_bounds__(kThreads) void sample_rest_kernel(SampleParams p) {
     const int t = threadIdx.x, lane = t & 63;
     const u64* sum = (const u64*)p.seg_sum + r * p.segs;
     const uint32_t* list = reinterpret_cast<const uint32_t*>(p.hist + r * kBins);
-    for (uint32_t i = t; i < st.n; i += kThreads) {
+    for (uint32_t i = t; i < st.n; i += kRowThreads) {
       const uint32_t idx = list[i];
       float z;
       if constexpr (DT == 0)
@@ -1541,9 +1565,9 @@ __global__ __launch_bounds__(kThreads) void sample_rest_kernel(SampleParams p) {
     // what a segment keeps: its sum before the bin and its share of the list
     __syncthreads();
     u64* keep = sh.keep;
-    for (int i = t; i < p.segs; i += kThreads) keep[i] = sum[i];
+    for (int i = t; i < p.segs; i += kRowThreads) keep[i] = sum[i];
     __syncthreads();
-    for (uint32_t i = t; i < st.n; i += kThreads) {
+    for (uint32_t i = t; i < st.n; i += kRowThreads) {
       const Entry e = sh.list[i];
       if ((e.q & kKeptBit) && (e.key > d.tau || (e.key == d.tau && e.idx <= d.last)))
         atomicAdd(&keep[(e.idx + (uint32_t)row.off) / kSeg], e.q & ~kKeptBit);
@@ -1647,12 +1671,12 @@ hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
     hipLaunchKernelGGL((sample_max_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
     if (mass)
       hipLaunchKernelGGL((sample_mass_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
-    hipLaunchKernelGGL((sample_pick_kernel<DT>), dim3((unsigned)N), dim3(kThreads), 0, stream,
-                       p);
+    hipLaunchKernelGGL((sample_pick_kernel<DT>), dim3((unsigned)N), dim3(kRowThreads), 0,
+                       stream, p);
     if (rest) {
       hipLaunchKernelGGL((sample_kept_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
-      hipLaunchKernelGGL((sample_rest_kernel<DT>), dim3((unsigned)N), dim3(kThreads), 0, stream,
-                         p);
+      hipLaunchKernelGGL((sample_rest_kernel<DT>), dim3((unsigned)N), dim3(kRowThreads), 0,
+                         stream, p);
     }
   };
   if (dtype == 0)
