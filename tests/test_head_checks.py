@@ -230,6 +230,13 @@ def test_mx_logits_rejects(L, kw, code):
     assert gemm(L, **kw) == code
 
 
+def test_mx_logits_rejects_more_than_a_launch_holds(L):
+    b = 1 << 60  # apart enough for every operand
+    far = dict(x=A, xs=A + b, w=A + 2 * b, ws=A + 3 * b, o=A + 4 * b, K=32)
+    for M, V in ((1, (1 << 30) + 1), (1 << 38, 256), ((1 << 30) + 256, 256), (1 << 20, 1 << 20)):
+        assert gemm(L, M=M, V=V, ldo=V, **far) == 7
+
+
 def test_mx_logits_empty(L):
     assert gemm(L, M=0) == 0 and gemm(L, V=0, ldo=0) == 0
 

@@ -164,3 +164,86 @@ def test_streams_and_graph(M):
         e = vce.mx_logits(x, xs, w, ws)
         torch.cuda.synchronize()
         assert torch.equal(o, e)
+
+
+# ---- vocabularies large enough for the tiles of 128 and 256 tokens -----------------
+
+LARGE = [(65, 49153, 96), (100, 49300, 160), (128, 49152, 512), (130, 49200, 288),
+         (256, 49407, 992), (300, 24700, 544), (513, 16400, 1056), (769, 12300, 256)]
+
+
+@pytest.mark.parametrize("xf,wf", PAIRS)
+@pytest.mark.parametrize("M,V,K", LARGE)
+def test_exact_sums_large(M, V, K, xf, wf):
+    rng = np.random.default_rng(M + V + K)
+    x, xs = small_integers(M, K, xf, rng)
+    w, ws = small_integers(V, K, wf, rng)
+    ref = head.dequantize(x, xs, xf) @ head.dequantize(w, ws, wf).T
+    for dt in (torch.float32, torch.bfloat16):
+        got = vce.mx_logits(cuda(x), cuda(xs), cuda(w), cuda(ws), x_fmt=xf, w_fmt=wf, dtype=dt)
+        assert torch.equal(got.cpu(), torch.from_numpy(ref).to(dt))
+
+
+@pytest.mark.parametrize("xf,wf", PAIRS)
+@pytest.mark.parametrize("M,V,K", [(100, 49300, 288), (300, 24700, 544)])
+def test_random_large(M, V, K, xf, wf):
+    test_random(M, V, K, xf, wf)
+
+
+@pytest.mark.parametrize("M,V", [(100, 49300), (300, 24700)])
+@pytest.mark.parametrize("xf,wf", PAIRS)
+def test_extreme_scales_large(M, V, xf, wf):
+    """As test_extreme_and_nan_scales; the values are 2^0 and small integers, exact."""
+    rng = np.random.default_rng(12)
+    K = 128
+    x, xs = small_integers(M, K, xf, rng)
+    w, ws = small_integers(V, K, wf, rng)
+    x = np.zeros_like(x)
+    x[:, :32 if xf == "e4m3" else 16] = 0x38 if xf == "e4m3" else 0x22
+    xs[:, 0], ws[:, 0] = 227, 27
+    xs[:, 1:], ws[:, 1:] = 0, 254
+    xs[1, 2], ws[33, 3] = 255, 255
+    ref = head.dequantize(x, np.where(xs == 255, 0, xs), xf) @ \
+        head.dequantize(w, np.where(ws == 255, 254, ws), wf).T
+    ref[1], ref[:, 33] = np.nan, np.nan
+    got = vce.mx_logits(cuda(x), cuda(xs), cuda(w), cuda(ws), x_fmt=xf, w_fmt=wf,
+                        dtype=torch.float32)
+    assert np.array_equal(f64(got), ref, equal_nan=True)
+
+
+@pytest.mark.parametrize("xf,wf", PAIRS)
+@pytest.mark.parametrize("M,V,K", [(5, 300, 512), (40, 300, 512), (300, 300, 512),
+                                   (300, 24700, 256), (20, 70, 544)])
+def test_scales_at_any_byte(M, V, K, xf, wf):
+    rng = np.random.default_rng(K)
+    x, xs = (cuda(t) for t in small_integers(M, K, xf, rng))
+    w, ws = (cuda(t) for t in small_integers(V, K, wf, rng))
+    ref = vce.mx_logits(x, xs, w, ws, x_fmt=xf, w_fmt=wf)
+
+    def moved(t, by):
+        b = torch.empty(t.numel() + 8, dtype=torch.uint8, device="cuda")
+        b = b[by:by + t.numel()].view(t.shape)
+        b.copy_(t)
+        return b
+    for i, j in ((1, 0), (0, 3), (5, 7), (2, 4)):
+        got = vce.mx_logits(x, moved(xs, i), w, moved(ws, j), x_fmt=xf, w_fmt=wf)
+        assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,V", [(100, 49301), (280, 24701)])
+def test_padded_and_offset_outputs_large(M, V, dt):
+    rng = np.random.default_rng(13)
+    K = 128
+    x, xs = small_integers(M, K, "e4m3", rng)
+    w, ws = small_integers(V, K, "e2m1", rng)
+    a = [cuda(t) for t in (x, xs, w, ws)]
+    ref = vce.mx_logits(*a, dtype=dt)
+    for ld, off in ((V, 1), (V + 3, 0), (V + 11, 5)):
+        buf = torch.full(((M + 1) * ld + 32,), 7.0, dtype=dt, device="cuda")
+        out = buf.as_strided((M, V), (ld, 1), off)
+        vce.mx_logits(*a, out=out)
+        assert torch.equal(out, ref)
+        mask = torch.ones_like(buf, dtype=torch.bool)
+        mask.as_strided((M, V), (ld, 1), off).fill_(False)
+        assert (buf[mask] == 7).all()

@@ -535,10 +535,14 @@ __device__ __forceinline__ f32x16_t mfma32(const i32x8_t& a, const i32x8_t& b, c
 template <bool MASK>
 __device__ __forceinline__ u32x2_t mx_scales8(const uint8_t* row, int ss, int nblk) {
   const int b = ss * 8;
-  if (!MASK) return *reinterpret_cast<const u32x2_t*>(row + b);
+  if (!MASK) {
+    u32x2_t w;
+    __builtin_memcpy(&w, row + b, 8);  // the scales lie at any byte
+    return w;
+  }
   uint32_t lo = 0x7f7f7f7fu, hi = 0x7f7f7f7fu;
   if (b + 8 <= nblk) {
-    __builtin_memcpy(&lo, row + b, 4);  // rows lie at any byte
+    __builtin_memcpy(&lo, row + b, 4);
     __builtin_memcpy(&hi, row + b + 4, 4);
   } else {
     for (int j = 0; j < 8 && b + j < nblk; ++j) {
@@ -828,14 +832,15 @@ __device__ __forceinline__ void mx_tile_of(int64_t b, int64_t n_ti, int64_t n_tj
   *tj = in / w;
 }
 
-// Two workgroups per CU where 64 tokens leave the registers and LDS for it.
-template <int FX, int FW, int MODE, int NA>
+// Two workgroups per CU where 64 tokens leave the registers and LDS for it: not with
+// W in E4M3 (E2M1 X at 64 x 4096 x 131072 spilled and took 346 us against 138).
+template <int FW, int NA>
 constexpr int mx_tile_occupancy() {
-  return NA == 1 && MxTile<FX, FW, MODE, NA>::kSmem <= 80 * 1024 ? 2 : 1;
+  return NA == 1 && FW == kMxE2M1 ? 2 : 1;
 }
 
 template <int FX, int FW, int MODE, int NA, int DT, bool MASK>
-__global__ __launch_bounds__(kTileThreads, (mx_tile_occupancy<FX, FW, MODE, NA>())) void
+__global__ __launch_bounds__(kTileThreads, (mx_tile_occupancy<FW, NA>())) void
 mx_tile_kernel(MxGemmParams p) {
   typedef MxTile<FX, FW, MODE, NA> T;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kSmem];
@@ -864,7 +869,6 @@ mx_tile_kernel(MxGemmParams p) {
 template <int FX, int FW, int MODE, int NA, int DT>
 hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
   const int64_t n = ((p.M + 64 * NA - 1) / (64 * NA)) * ((p.V + kTileN - 1) / kTileN);
-  if (n > ((int64_t)1 << 23)) return hipErrorInvalidValue;
   if (p.K % (2 * kSlice) == 0)
     hipLaunchKernelGGL((mx_tile_kernel<FX, FW, MODE, NA, DT, false>), dim3((unsigned)n),
                        dim3(kTileThreads), 0, stream, p);
@@ -877,9 +881,20 @@ hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
 template <int FX, int FW, int DT>
 hipError_t launch_by_tokens(const MxGemmParams& p, hipStream_t stream) {
   constexpr int MODE = DT == 0 && (FX == kMxE4M3 || FW == kMxE4M3) ? kBf16 : kScaled;
-  if (p.M > 128) return launch_tile<FX, FW, MODE, 4, DT>(p, stream);
-  if (p.M > 64) return launch_tile<FX, FW, MODE, 2, DT>(p, stream);
-  if (p.M > 16) return launch_tile<FX, FW, MODE, 1, DT>(p, stream);
+  if (p.M > 16) {
+    // The most tokens per tile that leave three quarters of the 256 CUs a tile at
+    // least (E4M3 x E2M1 to BF16, K = 4096: 256 x 32000 43 us with 250 tiles of 128 tokens,
+    // 50 with 125 of 256; 256 x 131072 170 us by 128 and 124 by 256), and no tile
+    // half empty.  Both operands in E4M3 do not fit beside 256 tokens' accumulators
+    // (4096 x 4096 x 32000 1182 us with spills against 738 by 128).
+    auto fills = [&](int64_t t) {
+      return p.M > t / 2 && ((p.M + t - 1) / t) * ((p.V + kTileN - 1) / kTileN) >= 192;
+    };
+    if constexpr (FX == kMxE2M1 || FW == kMxE2M1)
+      if (fills(256)) return launch_tile<FX, FW, MODE, 4, DT>(p, stream);
+    if (fills(128)) return launch_tile<FX, FW, MODE, 2, DT>(p, stream);
+    return launch_tile<FX, FW, MODE, 1, DT>(p, stream);
+  }
   // as many rows of W per wavefront (fewer reads of X) as leave two workgroups
   // per CU; four fragments of E4M3 do not fit its registers
   if (FW == kMxE2M1 && p.V >= 256 * 512)
@@ -894,6 +909,12 @@ hipError_t launch_fmt(const MxGemmParams& p, int dtype, hipStream_t stream) {
 }
 
 }  // namespace
+
+// A workgroup per 256 or more logits' rows of W, and launches below 2^32 threads.
+bool mx_logits_size_ok(int64_t M, int64_t V) {
+  return V <= ((int64_t)1 << 30) &&
+         ((M + 255) / 256) * ((V + kTileN - 1) / kTileN) <= ((int64_t)1 << 22);
+}
 
 hipError_t launch_mx_logits(MxGemmParams p, int x_format, int w_format, int dtype,
                             hipStream_t stream) {

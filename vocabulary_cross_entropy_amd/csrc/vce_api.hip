@@ -1068,8 +1068,7 @@ int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uin
   if (rc == VCE_OK) rc = check_mx_shape(V, K, w_format, &wb, &wsb);
   if (rc != VCE_OK) return rc;
   if (!__builtin_isfinite(logit_scale)) return VCE_EINVAL;
-  if (M > ((int64_t)1 << 22) || V > (int64_t)INT32_MAX || K > ((int64_t)1 << 20))
-    return VCE_EUNSUPPORTED;
+  if (!vce::mx_logits_size_ok(M, V) || K > ((int64_t)1 << 20)) return VCE_EUNSUPPORTED;
   if (M == 0 || V == 0) return VCE_OK;
   if (!x || !x_scales || !w || !w_scales || !out) return VCE_EINVAL;
   const int64_t es = dtype_size(dtype);

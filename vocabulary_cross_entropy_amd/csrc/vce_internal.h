@@ -222,6 +222,7 @@ struct MxGemmParams {
   bool wide = false;  // four logits may be stored at once (set by the launcher)
 };
 
+bool mx_logits_size_ok(int64_t M, int64_t V);
 hipError_t launch_mx_logits(MxGemmParams p, int x_format, int w_format, int dtype,
                             hipStream_t stream);
 
