@@ -597,18 +597,18 @@ struct Ask {
   double p, minp;
   int32_t k;
   bool ok, greedy, has_k, has_p, has_min;
-  // so short a row that all of it is gathered
-  __device__ __forceinline__ bool list_all(int64_t V) const { return V <= kCap; }
+  // so short a row that LDS holds all of it: sample_pick_kernel alone serves it
+  __device__ __forceinline__ bool small(int64_t V) const { return V <= kCap; }
   // few enough tokens asked for that the group maxima bound them closely
   __device__ __forceinline__ bool group_bound(int64_t V) const {
     return has_k && k <= kSmallK && k <= V / (4 * kGroup);
   }
   // by the histogram: top-p alone, or a top-k too large for the group maxima
   __device__ __forceinline__ bool hist(int64_t V) const {
-    return ok && !greedy && !list_all(V) && (has_k ? !group_bound(V) : has_p);
+    return ok && !greedy && !small(V) && (has_k ? !group_bound(V) : has_p);
   }
-  __device__ __forceinline__ bool plain(int64_t V) const {
-    return ok && !greedy && !list_all(V) && !has_k && !has_p && !has_min;
+  __device__ __forceinline__ bool plain() const {
+    return ok && !greedy && !has_k && !has_p && !has_min;
   }
 };
 
@@ -784,7 +784,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p
   if (!row_and_segment(p, &r, &seg)) return;
   const int t = threadIdx.x;
   const Ask a = ask_of(p, r);
-  const bool plain = a.plain(p.V), hist = a.hist(p.V);
+  const bool plain = a.plain(), hist = a.hist(p.V);
   if (!plain && !hist) return;
   const R row = row_of<DT>(p, r);
   const int v0 = seg * (kThreads * kVec) + t;
@@ -1255,18 +1255,27 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p
   }
   const R row = row_of<DT>(p, r);
   const Weights wt = weights_of(p, a, m);
-  if (a.greedy || a.plain(p.V)) {
+  if (a.greedy || a.plain()) {
     // the segment that holds the token: the first with the maximum, or the one
     // in which the running sum crosses; every wavefront finds it
     u64 total = 0, before = 0;
     double goal = 0.0;
     if (!a.greedy) {
-      for (int i = lane; i < p.segs; i += 64) total += p.seg_sum[r * p.segs + i];
-      total = wave_sum(total);
+      if (a.small(p.V)) {
+        row.each(0, row.nvec, t, kRowThreads, [&](int64_t, const float* z) {
+#pragma unroll
+          for (int j = 0; j < R::VE; ++j) total += wt.all(z[j]);
+        });
+        total = block_sum(total, sh);
+      } else {
+        for (int i = lane; i < p.segs; i += 64) total += p.seg_sum[r * p.segs + i];
+        total = wave_sum(total);
+      }
       goal = (double)a.u * (double)total;
     }
     int seg = 0;
-    for (int i = 0; i < p.segs; i += 64) {
+    // a small row is one segment
+    for (int i = 0; i < p.segs && !a.small(p.V); i += 64) {
       u64 v = 0;
       if (i + lane < p.segs)
         v = a.greedy ? (u64)(seg_max[i + lane] == m) : p.seg_sum[r * p.segs + i + lane];
@@ -1291,11 +1300,10 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p
   float hi = __builtin_huge_valf();
   u64 mass = 0;
   SampleState st{kRow, 0.0f, 0.0f, 0, 0, 0};
-  if (a.list_all(p.V)) {
-  } else if (a.has_k || a.has_p) {
-    // the bin of the distance where the count or the mass is reached, 8 bins a
-    // thread: of the row's histogram, or of the group maxima (k groups with
-    // maxima of at least the k-th largest hold k tokens as large)
+  if (a.has_k || a.has_p) {
+    // the bin of the distance where the count or the mass is reached, 4 bins a
+    // thread: of the row's histogram (made here for a small row), or of the group
+    // maxima (k groups with maxima of at least the k-th largest hold k tokens as large)
     constexpr int kPer = kBins / kRowThreads;
     u64* bins = reinterpret_cast<u64*>(sh.list);  // the list comes later
     if (a.hist(p.V)) {
@@ -1303,10 +1311,22 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p
     } else {
       for (int i = t; i < kBins; i += kRowThreads) bins[i] = 0;
       __syncthreads();
-      for (int g0 = 0; g0 < groups.n; g0 += GroupMax::kBatch)
-        groups.each(g0, [&](int, float g) { atomicAdd(&bins[bin_of(m, g)], (u64)1); });
+      if (!a.has_k || !a.group_bound(p.V)) {
+        row.each(0, row.nvec, t, kRowThreads, [&](int64_t, const float* z) {
+#pragma unroll
+          for (int j = 0; j < R::VE; ++j) {
+            const u64 q = a.has_k ? (u64)(z[j] != kNegInf) : wt.all(z[j]);
+            mass += q;
+            if (q != 0) atomicAdd(&bins[bin_of(m, z[j])], q);
+          }
+        });
+        mass = block_sum(mass, sh);
+      } else {
+        for (int g0 = 0; g0 < groups.n; g0 += GroupMax::kBatch)
+          groups.each(g0, [&](int, float g) { atomicAdd(&bins[bin_of(m, g)], (u64)1); });
+      }
     }
-    if (!a.has_k) {
+    if (!a.has_k && !a.small(p.V)) {
       for (int i = lane; i < p.segs; i += 64) mass += p.seg_sum[r * p.segs + i];
       mass = wave_sum(mass);
     }
@@ -1360,11 +1380,6 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p
   if (n > kCap) {
     if (t == 0) p.state[r] = st;
     return;
-  }
-  if (a.list_all(p.V) && a.has_p && !a.has_k) {
-    u64 v = 0;
-    for (uint32_t i = t; i < n; i += kRowThreads) v += sh.list[i].q & ~kKeptBit;
-    mass = block_sum(v, sh);
   }
   const Drawn d = draw_list<DT>(a, wt, p.V, n, mass, false, 0, sh);
   if (t == 0) write_out<DT>(p, r, row, a, m, d.token, d.total);
@@ -1657,8 +1672,8 @@ hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
   p.state = reinterpret_cast<SampleState*>(take(rows * sizeof(SampleState)));
   p.rows = (uint32_t)N;
   const dim3 seg_grid = grid2(N * p.segs);
-  // rows of at most kCap tokens are gathered whole; without filters no row has
-  // more candidates than LDS holds
+  // rows of at most kCap tokens are served by the pick kernel alone; without filters no
+  // row has candidates
   const bool mass = p.V > kCap;
   const bool rest = mass && (p.top_k || p.top_p || p.min_p);
   p.has = (p.temperature ? SampleParams::kT : 0) | (p.top_k ? SampleParams::kK : 0) |
