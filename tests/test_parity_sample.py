@@ -197,3 +197,36 @@ def test_streams_and_graph():
         ep = vce.ce_sample(z, u)
         torch.cuda.synchronize()
         assert torch.equal(tok, e[0]) and torch.equal(lp, e[1]) and torch.equal(plain, ep)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [5000, 50000, 200003])
+def test_large_top_k(V, dtype):
+    """Top-k beyond what a row's candidates have room for, alone and with the rest; with k at
+    and beside the number of tokens above a mask."""
+    N, live = 24, V // 3
+    z = normal(N, V, dtype, 21)
+    z[12:, live:] = -INF
+    ks = [1024, 1025, 4096, 4097, 4100, V // 2, V - 1, V, live - 1, live, live + 1, V // 5]
+    u = np.random.default_rng(22).random(N, dtype=np.float32).tolist()
+    run(z, u, k=ks * 2)
+    run(z, u, k=ks * 2, T=[3.0, 0.2] * 12, mp=[0.0, 1e-3, 0.3] * 8)
+    run(z, u, k=ks * 2, p=[0.999, 0.5] * 12)
+    run(torch.round(z), u, k=ks * 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [129, 1000, 4095, 4096])
+def test_short_rows(V, dtype):
+    """Rows that are served whole, with every filter alone and together."""
+    N = 40
+    z = normal(N, V, dtype, V)
+    z[:10] = torch.round(z[:10])
+    z[10:15, ::2] = -INF
+    g = params(N, V + 1)
+    run(z, g["u"])
+    run(z, g["u"], T=g["T"])
+    run(z, g["u"], k=[1, 7, 8, 30, 100, V // 2, V - 1, V] * 5)
+    run(z, g["u"], p=g["p"])
+    run(z, g["u"], mp=[1e-6, 0.01, 0.5, 1.0] * 10)
+    run(z, **g)

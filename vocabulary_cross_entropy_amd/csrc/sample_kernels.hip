@@ -999,8 +999,8 @@ struct Drawn {
 
 // Draws from the list of candidates, which holds every token the filters can
 // keep; `mass` is the weight that top-p refers to without top-k.  With
-// `threshold` the list holds one bin of the histogram, `above` is the weight
-// before it, and only top-p's threshold is taken.
+// `threshold` the list holds one bin of the histogram, `above` is the weight (for
+// top-k the number) before it, and only the threshold is taken, of one of the two.
 template <int DT>
 __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int64_t V, uint32_t n,
                                            u64 mass, bool threshold, u64 above, PickShared& sh) {
@@ -1082,11 +1082,15 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
   const int idx_bits = 64 - __builtin_clzll((u64)V);
   u64 ties = ~(u64)0;  // none: no threshold
   uint32_t tau = 0, last = 0xffffffffu;
-  for (int stage = threshold ? 1 : 0; stage < (threshold ? 3 : 4); ++stage) {
+  for (int stage = 0; stage < (threshold ? 3 : 4); ++stage) {
     double goal = 0.0;
     if (stage == 0) {  // top-k
-      if (!a.has_k || (u64)a.k >= n) continue;
-      goal = (double)a.k;
+      if (!a.has_k) continue;
+      if ((u64)a.k - above >= n) {
+        if (threshold) tau = key0;  // all of the bin, nothing behind it
+        continue;
+      }
+      goal = (double)((u64)a.k - above);
     } else if (stage == 1) {  // top-p
       if (!a.has_p) continue;
       if (a.has_k) {
@@ -1128,7 +1132,7 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
     if (stage < 2) s.key += key0;
     if (stage == 0) {
       tau = s.key;
-      ties = (u64)a.k - s.above;
+      ties = (u64)a.k - above - s.above;
     } else if (stage == 1) {
       u64 c = 0;
       for (uint32_t i = t; i < n; i += kRowThreads) c += sh.list[i].key == s.key;
@@ -1235,7 +1239,7 @@ __device__ __forceinline__ void write_out(const SampleParams& p, int64_t r, cons
 enum State : uint32_t { kDone = 0, kThreshold = 1, kRow = 2 };
 
 template <int DT>
-__global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p) {
+__global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParams p) {
   __shared__ PickShared sh;
   typedef Row<DT> R;
   const int64_t r = blockIdx.x;
@@ -1262,10 +1266,12 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p
     double goal = 0.0;
     if (!a.greedy) {
       if (a.small(p.V)) {
-        row.each(0, row.nvec, t, kRowThreads, [&](int64_t, const float* z) {
+        for (int i = t; i < row.nvec; i += kRowThreads) {
+          float z[R::VE];
+          row.load(i, z);
 #pragma unroll
           for (int j = 0; j < R::VE; ++j) total += wt.all(z[j]);
-        });
+        }
         total = block_sum(total, sh);
       } else {
         for (int i = lane; i < p.segs; i += 64) total += p.seg_sum[r * p.segs + i];
@@ -1312,14 +1318,16 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p
       for (int i = t; i < kBins; i += kRowThreads) bins[i] = 0;
       __syncthreads();
       if (!a.has_k || !a.group_bound(p.V)) {
-        row.each(0, row.nvec, t, kRowThreads, [&](int64_t, const float* z) {
+        for (int i = t; i < row.nvec; i += kRowThreads) {
+          float z[R::VE];
+          row.load(i, z);
 #pragma unroll
           for (int j = 0; j < R::VE; ++j) {
             const u64 q = a.has_k ? (u64)(z[j] != kNegInf) : wt.all(z[j]);
             mass += q;
             if (q != 0) atomicAdd(&bins[bin_of(m, z[j])], q);
           }
-        });
+        }
         mass = block_sum(mass, sh);
       } else {
         for (int g0 = 0; g0 < groups.n; g0 += GroupMax::kBatch)
@@ -1359,7 +1367,8 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p
     const uint32_t bin = (uint32_t)sh.out[0];
     // the distances of bin b lie between bits (base + b) << 16 and the next
     if (bin < kBins - 1) hi = __uint_as_float(((kBinBase + bin + 1) << 16) - 1);
-    if (!a.has_k) {
+    // the threshold lies in this bin, unless top-p follows a top-k
+    if (!a.has_k || (!a.has_p && a.hist(p.V))) {
       st.what = kThreshold;
       st.lo = bin > 0 ? __uint_as_float((kBinBase + bin) << 16) : 0.0f;
       st.hi = hi;
@@ -1375,8 +1384,10 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleParams p
     st.lo = __builtin_huge_valf();
     st.hi = -1.0f;
   }
-  // rows that other kernels can finish over all segments gather little here
-  const uint32_t n = gather_groups<DT>(row, groups, wt, hi, st.what == kThreshold ? 512 : kCap, sh);
+  // rows that other kernels can finish over all segments gather little here, those
+  // that cannot fit nothing
+  const uint32_t most = a.has_k ? (a.k > kCap ? 0 : kCap) : st.what == kThreshold ? 512 : kCap;
+  const uint32_t n = gather_groups<DT>(row, groups, wt, hi, a.small(p.V) ? kCap : most, sh);
   if (n > kCap) {
     if (t == 0) p.state[r] = st;
     return;
@@ -1546,7 +1557,7 @@ __device__ __forceinline__ Drawn draw_row(const Row<DT>& row, const Ask& a, cons
 }
 
 template <int DT>
-__global__ __launch_bounds__(kRowThreads) void sample_rest_kernel(SampleParams p) {
+__global__ __launch_bounds__(kRowThreads, 4) void sample_rest_kernel(SampleParams p) {
   __shared__ union {
     PickShared pick;
     Shared row;
