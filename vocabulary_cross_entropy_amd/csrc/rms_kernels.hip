@@ -8,7 +8,10 @@
 // All of it is bound by memory traffic: a row is read once, held in registers
 // as FP32 between the sum of squares and the output, and written once.  A row
 // belongs to TPR threads of EPL elements each: a wavefront, or a workgroup of 256
-// or 1024 (see pick_shape).
+// or 1024 (see pick_shape).  Measured at 16384 x 2304 BF16 with a residual (302 MB either
+// way): forward 47 us, 6.4 TB/s; backward 65 us, 4.7 TB/s, and 5 us more for dw's shares.
+// The backward holds three rows and dw in 225 registers, two wavefronts a SIMD; held to
+// 168 registers it spilled and took 170 us.
 //
 // Loads go through buffer descriptors that end at the row (a lane past it
 // reads zeros), so all loads of a row issue together, without branches.

@@ -19,23 +19,33 @@
 //  * sample_max_kernel (rows x segments) reads the logits once: the maximum of every
 //    thread's 32 tokens (a group) and of the segment.
 //  * sample_mass_kernel (rows x segments), once the row's maximum is known, sums
-//    the segment's weights for rows without top-k and min-p, and for rows whose
-//    top-p stands alone (or whose top-k is large) adds the segment to the row's
+//    the segment's weights for rows without filters, and for rows whose top-p stands
+//    alone (or whose top-k is large) adds the segment to the row's
 //    histogram over the distance m - z (128 bins per octave, 16 octaves).
 //  * sample_pick_kernel (rows) draws.  Candidates are bounded from below first: by
 //    the k-th largest group maximum (k groups hold at least k tokens as
-//    large), by the histogram's bin where the mass is reached, or by min-p
+//    large), by the histogram's bin where the mass or the count is reached, or by min-p
 //    itself; only groups that reach the bound are read again and their
-//    candidates gathered in LDS.  Up to 256 are ranked by counting, more go
-//    through selection by eight key bits at a time.  A row without filters
-//    re-reads the one segment in which its sum crosses u.
+//    candidates gathered in LDS.  Up to 64 are ranked by counting, more go
+//    through selection by nine key bits at a time.  A row without filters
+//    re-reads the one segment in which its sum crosses u.  Rows of up to 4096 tokens
+//    make their own histogram here and need none of the other kernels but the first.
 //  * rows with more candidates than LDS holds: sample_kept_kernel (rows x
 //    segments) sums what lies before the histogram's bin and lists the tokens of
 //    that bin, sample_rest_kernel (rows) finds the threshold in the list and
-//    draws.  What does not fit that either is served from the row, pass by pass.
-// The code that a usual row runs is kept short: a kernel this brief waits for
-// its instructions more than for its data (one row of 128256 with all filters took 67 us
-// in a kernel of 60 KB, most of it instruction fetch).
+//    draws.  What does not fit that either (a large top-k together with top-p, more ties
+//    than the list holds) is served from the row, pass by pass: 16 x 200000 with top-k
+//    20000 and top-p 0.99 take 370 us against 43 for a top-k of 5000.
+//
+// What bounds it: sample_max_kernel memory (256 x 128256 BF16 14 us, 4.7 TB/s), the
+// weights of a segment FP64 issue (22 instructions a token: 61 x 256003 FP32 without
+// filters 21 us), and sample_pick_kernel and sample_rest_kernel, one workgroup a row,
+// the latency of some dozen steps between barriers (256 rows of top-k 50 17 us, of
+// top-k 1000 33 us).  256 x 128256 BF16 of mixed parameters take 103 us (max 14, mass
+// 21, pick 34, kept 17, rest 19), one row with all filters 26 us.  512 threads a row: with 256
+// the mixed rows took 118 us, with 1024 no less than with 512.  The code that a usual row
+// runs is kept short, too: a kernel this brief waits for its instructions as well as for its
+// data.
 //
 #include <math.h>
 
@@ -384,7 +394,7 @@ __device__ __forceinline__ Sel radix_select(int bits, double target, bool strict
 // The first index, in order, of vectors [c0, c1) at which the running sum of
 // amount(index, z), from `before` on, exceeds target(sum of the range); V if it
 // never does.  Each wavefront sums a
-// sixteenth of the range, the sixteenth that holds the crossing is split
+// share of the range, the share that holds the crossing is split
 // again, down to one vector per lane.
 template <int DT, class Target, class Amount>
 __device__ __forceinline__ int64_t locate(const Row<DT>& row, int c0, int c1, Shared& sh, u64 before,
@@ -804,7 +814,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p
   float z[kVec][R::VE];
   group.get(row, v0, z);
   if (plain && !wt.inf) {
-    // eight at a time: enough to fill the pipeline, and registers for five workgroups
+    // eight at a time: enough to fill the pipeline, and registers for four workgroups
     // per CU
 #pragma unroll
     for (int j0 = 0; j0 < kGroup; j0 += 8) {
@@ -1058,7 +1068,7 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
     return d;
   }
   n = n < kCap ? n : kCap;
-  // keys count from the least one: fewer bits to select by, and the first eight
+  // keys count from the least one: fewer bits to select by, and the first nine
   // tell the candidates apart (equal digits queue at one LDS address)
   uint32_t key0 = 0xffffffffu, key1 = 0;
   for (uint32_t i = t; i < n; i += kRowThreads) {
