@@ -33,7 +33,8 @@
 //  * rows with more candidates than LDS holds: sample_kept_kernel (rows x
 //    segments) sums what lies before the histogram's bin and lists the tokens of
 //    that bin, sample_rest_kernel (rows) finds the threshold in the list and
-//    draws.  What does not fit that either (a large top-k together with top-p, more ties
+//    draws.  (For few segments each of these pairs, mass and pick, kept and rest, is
+//    one launch; the last workgroup of a row goes on with the row.)  What does not fit that either (a large top-k together with top-p, more ties
 //    than the list holds) is served from the row, pass by pass: 16 x 200000 with top-k
 //    20000 and top-p 0.99 take 370 us against 43 for a top-k of 5000.
 //
@@ -42,7 +43,7 @@
 // filters 21 us), and sample_pick_kernel and sample_rest_kernel, one workgroup a row,
 // the latency of some dozen steps between barriers (256 rows of top-k 50 17 us, of
 // top-k 1000 33 us).  256 x 128256 BF16 of mixed parameters take 103 us (max 14, mass
-// 21, pick 34, kept 17, rest 19), one row with all filters 26 us.  512 threads a row: with 256
+// 21, pick 34, kept 16, rest 19), one row with all filters 20 us.  512 threads a row: with 256
 // the mixed rows took 118 us, with 1024 no less than with 512.  The code that a usual row
 // runs is kept short, too: a kernel this brief waits for its instructions as well as for its
 // data.
@@ -71,6 +72,11 @@ constexpr int kRank = 64;
 constexpr int kLoads = 4;                 // vectors in flight per thread
 constexpr int kGroup = 32;                // tokens per thread of a segment
 constexpr int kSeg = kThreads * kGroup;
+// Row segments up to which a segments' and a rows' kernel are one launch: a workgroup per
+// CU.  Below, a launch less saves 1 to 4 us (one row of 128256 with all filters 23.6 ->
+// 21.0 us); with more, the segments run at the rows' kernels' two workgroups per CU
+// (1024 segments of top-p 70 -> 96 us).
+constexpr int kJoined = 256;
 constexpr int kSmallK = 1024;             // top-k up to here bounds by group maxima
 
 typedef unsigned long long u64;
@@ -759,6 +765,7 @@ __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleParams p) {
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   if (__any(nan)) m = __builtin_nanf("");
   if ((t & 63) == 0) sh[t >> 6] = m;
+  if (seg == 0 && t < 2) p.done[2 * r + t] = 0;
   // the row's histogram starts at zero, a share of it per segment
   if (ask_of(p, r).hist(p.V)) {
     for (int64_t b = seg * kThreads + t; b < kBins; b += (int64_t)p.segs * kThreads)
@@ -777,36 +784,55 @@ __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleParams p) {
   }
 }
 
+// Words that the workgroups of a row hand to the last of them within a launch go past the
+// caches of the XCDs, by device-scope atomic stores and loads.
+template <class T>
+__device__ __forceinline__ void put_shared(T* at, T v) {
+  __hip_atomic_store(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T get_shared(const T* at) {
+  return __hip_atomic_load(const_cast<T*>(at), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// True in the last of a row's workgroups to come here.  Every wavefront first waits
+// until its device-scope stores and atomics are done; then the workgroup is counted.  (A
+// release fence at device scope writes a whole L2 back: with one per workgroup 256 mixed
+// rows took 521 us.)
+__device__ __forceinline__ bool last_of_row(uint32_t* count, int segs, Scratch& sh) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) sh.n = atomicAdd(count, 1u);
+  __syncthreads();
+  const bool last = sh.n == (uint32_t)segs - 1;
+  __syncthreads();
+  return last;
+}
+
 // For rows without filters the segment's mass; for rows that go by the
 // histogram its tokens per bin (top-k), or its mass per bin and in all (top-p).
 // Top-p needs no token lighter than q0 = (1 - p) / V: the row's mass is at least
 // 1, so all such tokens together weigh less than (1 - p) of it, and its p-th part is
 // reached before them.  They stay out of the histogram, which spares most of the
 // LDS atomics.
-template <int DT>
-__global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p) {
+template <int DT, int NT>
+__device__ __forceinline__ void mass_of_segment(const SampleParams& p, const Row<DT>& row,
+                                                const Ask& a, int64_t r, int seg, u64* bins,
+                                                u64* part) {
   typedef Row<DT> R;
-  constexpr int kVec = kGroup / R::VE;
-  __shared__ u64 bins[kBins];
-  __shared__ u64 part[kWaves];
-  int64_t r;
-  int seg;
-  if (!row_and_segment(p, &r, &seg)) return;
+  typedef Group<DT, NT> G;
+  constexpr int kVec = G::kVec, kTokens = kVec * R::VE;
+  const bool plain = a.plain(), hist = !plain;
   const int t = threadIdx.x;
-  const Ask a = ask_of(p, r);
-  const bool plain = a.plain(), hist = a.hist(p.V);
-  if (!plain && !hist) return;
-  const R row = row_of<DT>(p, r);
-  const int v0 = seg * (kThreads * kVec) + t;
-  Group<DT, kThreads> group;
+  const int v0 = seg * (kSeg / R::VE) + t;
+  G group;
   group.load(row, v0);
-  const float* seg_max = p.seg_max + r * p.segs;
-  const float m = row_max(seg_max, p.segs);
+  const float m = row_max(p.seg_max + r * p.segs, p.segs);
   if (!(m > kNegInf)) return;  // no admissible token, or NaN
   const Weights wt = weights_of(p, a, m);
   u64 s = 0, q0 = 0;
   if (hist) {
-    for (int b = t; b < kBins; b += kThreads) bins[b] = 0;
+    for (int b = t; b < kBins; b += NT) bins[b] = 0;
     q0 = wt.fixed((1.0 - a.p) * p.inv_v);
     q0 = q0 < 1 ? 1 : q0;
     __syncthreads();
@@ -814,24 +840,23 @@ __global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p
   float z[kVec][R::VE];
   group.get(row, v0, z);
   if (plain && !wt.inf) {
-    // eight at a time: enough to fill the pipeline, and registers for four workgroups
-    // per CU
+    // eight at a time: enough to fill the pipeline
 #pragma unroll
-    for (int j0 = 0; j0 < kGroup; j0 += 8) {
+    for (int j0 = 0; j0 < kTokens; j0 += 8) {
 #pragma unroll
       for (int j = j0; j < j0 + 8; ++j) s += wt.fixed(wt.real(z[j / R::VE][j % R::VE]));
       __builtin_amdgcn_sched_barrier(0);
     }
   } else if (hist && a.has_k) {
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
+    for (int j = 0; j < kTokens; ++j) {
       const float v = z[j / R::VE][j % R::VE];
       if (v != kNegInf) atomicAdd(&bins[bin_of(m, v)], (u64)1);
     }
   } else if (!wt.inf) {
     // eight weights at a time, interleaved, then their atomics
 #pragma unroll
-    for (int j0 = 0; j0 < kGroup; j0 += 8) {
+    for (int j0 = 0; j0 < kTokens; j0 += 8) {
       u64 q[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -846,17 +871,39 @@ __global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p
   } else {
     // only the infinite tokens weigh, all in bin 0
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) s += wt.all(z[j / R::VE][j % R::VE]);
+    for (int j = 0; j < kTokens; ++j) s += wt.all(z[j / R::VE][j % R::VE]);
     if (hist && s) atomicAdd(&bins[0], s);
   }
   s = wave_sum(s);
   if ((t & 63) == 0) part[t >> 6] = s;
   __syncthreads();
-  if (t == 0) p.seg_sum[r * p.segs + seg] = part[0] + part[1] + part[2] + part[3];
+  if (t == 0) {
+    s = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) s += part[i];
+    put_shared(&p.seg_sum[r * p.segs + seg], s);
+  }
   if (hist) {
-    for (int b = t; b < kBins; b += kThreads)
+    for (int b = t; b < kBins; b += NT)
       if (bins[b]) atomicAdd((u64*)&p.hist[r * kBins + b], bins[b]);
   }
+}
+
+// What sample_mass_kernel has to do for a row.
+__device__ __forceinline__ bool needs_mass(const Ask& a, int64_t V) {
+  return a.hist(V) || (a.plain() && !a.small(V));
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads, 4) void sample_mass_kernel(SampleParams p) {
+  __shared__ u64 bins[kBins];
+  __shared__ u64 part[kWaves];
+  int64_t r;
+  int seg;
+  if (!row_and_segment(p, &r, &seg)) return;
+  const Ask a = ask_of(p, r);
+  if (!needs_mass(a, p.V)) return;
+  mass_of_segment<DT, kThreads>(p, row_of<DT>(p, r), a, r, seg, bins, part);
 }
 
 template <int DT>
@@ -1248,15 +1295,14 @@ __device__ __forceinline__ void write_out(const SampleParams& p, int64_t r, cons
 
 enum State : uint32_t { kDone = 0, kThreshold = 1, kRow = 2 };
 
+// Draws row r, or leaves it to sample_rest_kernel.
 template <int DT>
-__global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParams p) {
-  __shared__ PickShared sh;
+__device__ __forceinline__ void pick_row(const SampleParams& p, const Row<DT>& row, const Ask& a,
+                                         int64_t r, PickShared& sh) {
   typedef Row<DT> R;
-  const int64_t r = blockIdx.x;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   GroupMax groups;
   groups.init(p.group_max + r * p.segs * kThreads, p.segs);
-  const Ask a = ask_of(p, r);
   const float* seg_max = p.seg_max + r * p.segs;
   const float m = row_max(seg_max, p.segs);
   if (t == 0 && p.state) p.state[r].what = kDone;
@@ -1267,7 +1313,6 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParam
     }
     return;
   }
-  const R row = row_of<DT>(p, r);
   const Weights wt = weights_of(p, a, m);
   if (a.greedy || a.plain()) {
     // the segment that holds the token: the first with the maximum, or the one
@@ -1284,7 +1329,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParam
         }
         total = block_sum(total, sh);
       } else {
-        for (int i = lane; i < p.segs; i += 64) total += p.seg_sum[r * p.segs + i];
+        for (int i = lane; i < p.segs; i += 64) total += get_shared(&p.seg_sum[r * p.segs + i]);
         total = wave_sum(total);
       }
       goal = (double)a.u * (double)total;
@@ -1294,7 +1339,8 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParam
     for (int i = 0; i < p.segs && !a.small(p.V); i += 64) {
       u64 v = 0;
       if (i + lane < p.segs)
-        v = a.greedy ? (u64)(seg_max[i + lane] == m) : p.seg_sum[r * p.segs + i + lane];
+        v = a.greedy ? (u64)(seg_max[i + lane] == m)
+                     : get_shared(&p.seg_sum[r * p.segs + i + lane]);
       const u64 run = wave_scan(v);
       const uint64_t hit = __ballot(v != 0 && (double)(before + run) > goal);
       if (hit) {
@@ -1323,7 +1369,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParam
     constexpr int kPer = kBins / kRowThreads;
     u64* bins = reinterpret_cast<u64*>(sh.list);  // the list comes later
     if (a.hist(p.V)) {
-      for (int i = t; i < kBins; i += kRowThreads) bins[i] = p.hist[r * kBins + i];
+      for (int i = t; i < kBins; i += kRowThreads) bins[i] = get_shared(&p.hist[r * kBins + i]);
     } else {
       for (int i = t; i < kBins; i += kRowThreads) bins[i] = 0;
       __syncthreads();
@@ -1345,7 +1391,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParam
       }
     }
     if (!a.has_k && !a.small(p.V)) {
-      for (int i = lane; i < p.segs; i += 64) mass += p.seg_sum[r * p.segs + i];
+      for (int i = lane; i < p.segs; i += 64) mass += get_shared(&p.seg_sum[r * p.segs + i]);
       mass = wave_sum(mass);
     }
     const double goal = a.has_k ? (double)a.k : a.p * (double)mass;
@@ -1406,36 +1452,56 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParam
   if (t == 0) write_out<DT>(p, r, row, a, m, d.token, d.total);
 }
 
+// A row per workgroup, or JOINED with sample_mass_kernel a segment per workgroup, the
+// last of a row's drawing.
+template <int DT, bool JOINED>
+__global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParams p) {
+  __shared__ PickShared sh;
+  int64_t r = blockIdx.x;
+  int seg = 0;
+  if (JOINED && !row_and_segment(p, &r, &seg)) return;
+  const Ask a = ask_of(p, r);
+  const Row<DT> row = row_of<DT>(p, r);
+  if (JOINED) {
+    if (needs_mass(a, p.V)) {
+      mass_of_segment<DT, kRowThreads>(p, row, a, r, seg, reinterpret_cast<u64*>(sh.list),
+                                       sh.wave);
+      if (!last_of_row(p.done + 2 * r, p.segs, sh)) return;
+    } else if (seg != 0) {
+      return;
+    }
+  }
+  pick_row<DT>(p, row, a, r, sh);
+}
+
 // Rows whose candidates do not fit in LDS, one segment each: the kept weight of
 // the tokens before the histogram's bin, and the bin's tokens appended to the
 // row's list (over its histogram, which has been read).
-template <int DT>
-__global__ __launch_bounds__(kThreads, 4) void sample_kept_kernel(SampleParams p) {
+template <int NT>
+struct KeepShared {
+  u64 part[NT / 64];
+  uint32_t cnt[NT / 64], base;
+};
+
+template <int DT, int NT>
+__device__ __forceinline__ void keep_segment(const SampleParams& p, const Row<DT>& row,
+                                             const Ask& a, int64_t r, int seg, KeepShared<NT>& sh) {
   typedef Row<DT> R;
-  constexpr int kVec = kGroup / R::VE;
-  __shared__ u64 part[kWaves];
-  __shared__ uint32_t cnt[kWaves];
-  __shared__ uint32_t base;
-  int64_t r;
-  int seg;
-  if (!row_and_segment(p, &r, &seg)) return;
-  if (p.state[r].what != kThreshold) return;
+  typedef Group<DT, NT> G;
+  constexpr int kVec = G::kVec, kTokens = kVec * R::VE;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const Ask a = ask_of(p, r);
-  const R row = row_of<DT>(p, r);
-  const int v0 = seg * (kThreads * kVec) + t;
-  Group<DT, kThreads> group;
+  const int v0 = seg * (kSeg / R::VE) + t;
+  G group;
   group.load(row, v0);
-  const float m = row_max(p.seg_max + r * p.segs, p.segs);
-  const Weights wt = weights_of(p, a, m);
+  const Weights wt = weights_of(p, a, row_max(p.seg_max + r * p.segs, p.segs));
   const float lo = p.state[r].lo, hi = p.state[r].hi;
   float z[kVec][R::VE];
   group.get(row, v0, z);
   u64 s = 0;
   uint32_t in = 0;  // bit j: token j is in the bin
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) {
-    const float v = z[j / R::VE][j % R::VE], d = distance(m, v);
+  for (int j = 0; j < kTokens; ++j) {
+    const float v = z[j / R::VE][j % R::VE], d = distance(wt.m, v);
     const u64 q = wt.kept(v);
     s += d < lo ? q : 0;
     in |= (v != kNegInf && d >= lo && d <= hi ? 1u : 0u) << j;
@@ -1444,26 +1510,43 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kept_kernel(SampleParams p
   s = wave_sum(s);
   const uint32_t c = __builtin_popcount(in);
   const uint32_t run = (uint32_t)wave_scan(c);
-  if (lane == 63) cnt[wave] = run;
-  if (lane == 0) part[wave] = s;
+  if (lane == 63) sh.cnt[wave] = run;
+  if (lane == 0) sh.part[wave] = s;
   __syncthreads();
+  uint32_t n = 0, at = run - c;
+#pragma unroll
+  for (int i = 0; i < NT / 64; ++i) {
+    at += i < wave ? sh.cnt[i] : 0;
+    n += sh.cnt[i];
+  }
   if (t == 0) {
-    p.seg_sum[r * p.segs + seg] = part[0] + part[1] + part[2] + part[3];
-    const uint32_t n = cnt[0] + cnt[1] + cnt[2] + cnt[3];
-    base = n ? atomicAdd(&p.state[r].n, n) : 0;
+    s = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) s += sh.part[i];
+    put_shared(&p.seg_sum[r * p.segs + seg], s);
+    sh.base = n ? atomicAdd(&p.state[r].n, n) : 0;
   }
   __syncthreads();
-  uint32_t at = base + run - c;
-  for (int i = 0; i < wave; ++i) at += cnt[i];
+  at += sh.base;
   uint32_t* list = reinterpret_cast<uint32_t*>(p.hist + r * kBins);
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) {
+  for (int j = 0; j < kTokens; ++j) {
     if ((in >> j) & 1u) {
       if (at < kCap)
-        list[at] = (uint32_t)(row.first(v0 + (j / R::VE) * kThreads) + j % R::VE);
+        put_shared(&list[at], (uint32_t)(row.first(v0 + (j / R::VE) * NT) + j % R::VE));
       ++at;
     }
   }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads, 4) void sample_kept_kernel(SampleParams p) {
+  __shared__ KeepShared<kThreads> sh;
+  int64_t r;
+  int seg;
+  if (!row_and_segment(p, &r, &seg)) return;
+  if (p.state[r].what != kThreshold) return;
+  keep_segment<DT, kThreads>(p, row_of<DT>(p, r), ask_of(p, r), r, seg, sh);
 }
 
 // Draws where the candidates do not fit in LDS: every pass reads the row.
@@ -1566,20 +1649,30 @@ __device__ __forceinline__ Drawn draw_row(const Row<DT>& row, const Ask& a, cons
   return d;
 }
 
-template <int DT>
+// A row per workgroup, or JOINED with sample_kept_kernel a segment per workgroup.
+template <int DT, bool JOINED>
 __global__ __launch_bounds__(kRowThreads, 4) void sample_rest_kernel(SampleParams p) {
   __shared__ union {
     PickShared pick;
     Shared row;
+    KeepShared<kRowThreads> keep;
   } both;
   typedef Row<DT> R;
-  const int64_t r = blockIdx.x;
-  const SampleState st = p.state[r];
-  if (st.what == kDone) return;
+  int64_t r = blockIdx.x;
+  int seg = 0;
+  if (JOINED && !row_and_segment(p, &r, &seg)) return;
+  const uint32_t what = p.state[r].what;
+  if (what == kDone || (what == kRow && seg != 0)) return;
   const Ask a = ask_of(p, r);
-  const float m = row_max(p.seg_max + r * p.segs, p.segs);
   const R row = row_of<DT>(p, r);
+  if (JOINED && what == kThreshold) {
+    keep_segment<DT, kRowThreads>(p, row, a, r, seg, both.keep);
+    if (!last_of_row(p.done + 2 * r + 1, p.segs, both.pick)) return;
+  }
+  const float m = row_max(p.seg_max + r * p.segs, p.segs);
   const Weights wt = weights_of(p, a, m);
+  SampleState st = p.state[r];
+  st.n = get_shared(&p.state[r].n);
   Drawn d;
   if (st.what == kRow || st.n > kCap || p.segs > kKeepSegs) {
     d = draw_row<DT>(row, a, wt, both.row);
@@ -1589,7 +1682,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_rest_kernel(SampleParam
     const u64* sum = (const u64*)p.seg_sum + r * p.segs;
     const uint32_t* list = reinterpret_cast<const uint32_t*>(p.hist + r * kBins);
     for (uint32_t i = t; i < st.n; i += kRowThreads) {
-      const uint32_t idx = list[i];
+      const uint32_t idx = get_shared(&list[i]);
       float z;
       if constexpr (DT == 0)
         z = reinterpret_cast<const float*>(row.base)[idx] + 0.0f;
@@ -1604,7 +1697,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_rest_kernel(SampleParam
     // what a segment keeps: its sum before the bin and its share of the list
     __syncthreads();
     u64* keep = sh.keep;
-    for (int i = t; i < p.segs; i += kRowThreads) keep[i] = sum[i];
+    for (int i = t; i < p.segs; i += kRowThreads) keep[i] = get_shared(&sum[i]);
     __syncthreads();
     for (uint32_t i = t; i < st.n; i += kRowThreads) {
       const Entry e = sh.list[i];
@@ -1617,7 +1710,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_rest_kernel(SampleParam
     total = wave_sum(total);
     const double goal = (double)a.u * (double)total;
     u64 before = 0;
-    int seg = 0;
+    seg = 0;
     for (int i = 0; i < p.segs; i += 64) {
       const u64 v = i + lane < p.segs ? keep[i + lane] : 0;
       const u64 run = wave_scan(v);
@@ -1662,7 +1755,7 @@ bool sample_size_ok(int64_t N, int64_t V) {
 size_t sample_workspace_bytes(int64_t N, int64_t V) {
   const size_t rows = (size_t)N, s = rows * (size_t)segments(V);
   return 256 + up256(s * kThreads * 4) + up256(s * 4) + up256(s * 8) + up256(rows * kBins * 8) +
-         up256(rows * sizeof(SampleState));
+         up256(rows * sizeof(SampleState)) + up256(rows * 8);
 }
 
 hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
@@ -1691,12 +1784,14 @@ hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
   p.seg_sum = reinterpret_cast<unsigned long long*>(take(s * 8));
   p.hist = reinterpret_cast<unsigned long long*>(take(rows * kBins * 8));
   p.state = reinterpret_cast<SampleState*>(take(rows * sizeof(SampleState)));
+  p.done = reinterpret_cast<uint32_t*>(take(rows * 8));
   p.rows = (uint32_t)N;
   const dim3 seg_grid = grid2(N * p.segs);
   // rows of at most kCap tokens are served by the pick kernel alone; without filters no
   // row has candidates
   const bool mass = p.V > kCap;
   const bool rest = mass && (p.top_k || p.top_p || p.min_p);
+  const bool joined = mass && N * p.segs <= kJoined;
   p.has = (p.temperature ? SampleParams::kT : 0) | (p.top_k ? SampleParams::kK : 0) |
           (p.top_p ? SampleParams::kP : 0) | (p.min_p ? SampleParams::kM : 0);
   if (!p.temperature) p.temperature = p.u;
@@ -1708,14 +1803,22 @@ hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
   auto run = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     hipLaunchKernelGGL((sample_max_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
+    if (joined) {
+      hipLaunchKernelGGL((sample_pick_kernel<DT, true>), seg_grid, dim3(kRowThreads), 0, stream,
+                         p);
+      if (rest)
+        hipLaunchKernelGGL((sample_rest_kernel<DT, true>), seg_grid, dim3(kRowThreads), 0,
+                           stream, p);
+      return;
+    }
     if (mass)
       hipLaunchKernelGGL((sample_mass_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
-    hipLaunchKernelGGL((sample_pick_kernel<DT>), dim3((unsigned)N), dim3(kRowThreads), 0,
+    hipLaunchKernelGGL((sample_pick_kernel<DT, false>), dim3((unsigned)N), dim3(kRowThreads), 0,
                        stream, p);
     if (rest) {
       hipLaunchKernelGGL((sample_kept_kernel<DT>), seg_grid, dim3(kThreads), 0, stream, p);
-      hipLaunchKernelGGL((sample_rest_kernel<DT>), dim3((unsigned)N), dim3(kRowThreads), 0,
-                         stream, p);
+      hipLaunchKernelGGL((sample_rest_kernel<DT, false>), dim3((unsigned)N), dim3(kRowThreads),
+                         0, stream, p);
     }
   };
   if (dtype == 0)

@@ -261,6 +261,7 @@ struct SampleParams {
   unsigned long long* seg_sum = nullptr;    // (N, segs)
   unsigned long long* hist = nullptr;       // (N, 2048)
   SampleState* state = nullptr;             // (N), NULL where every row is done in one kernel
+  uint32_t* done = nullptr;                 // (N, 2): workgroups of the row past each kernel
 };
 
 // Rows times segments stay below 2^31.
