@@ -946,7 +946,7 @@ int rms_forward_mx8(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
 
 size_t rms_backward_workspace_size(int64_t M, int64_t H) {
   if (M < 0 || M > (int64_t)INT32_MAX || !vce::rms_width_ok(H)) return 0;
-  return (size_t)vce::rms_bwd_parts(M) * (size_t)H * 4;
+  return (size_t)vce::rms_bwd_parts(M) * (size_t)vce::rms_share_width(H) * 4;
 }
 
 int rms_backward(const void* dy, const void* h, int dtype, int64_t M, int64_t H,

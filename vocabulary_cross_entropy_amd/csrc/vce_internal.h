@@ -183,12 +183,15 @@ struct RmsBwdParams {
   const float* rstd;
   const void* dh;  // optional (M, H)
   void* dx;
-  float* partial;  // up to (rms_bwd_parts(M), H) shares of dw, NULL without dweight
+  // up to rms_bwd_parts(M) shares of dw, rms_share_width(H) apart; NULL without dweight
+  float* partial;
   float* dweight;  // optional (H)
 };
 
 bool rms_width_ok(int64_t H);
 int rms_bwd_parts(int64_t M);  // at most
+// A share of dw starts on a cache line, whatever H is.
+__host__ __device__ inline int64_t rms_share_width(int64_t H) { return (H + 31) / 32 * 32; }
 hipError_t launch_rms_forward(const RmsFwdParams& p, int dtype, bool mx, hipStream_t stream);
 hipError_t launch_rms_backward(RmsBwdParams p, int dtype, hipStream_t stream);
 
