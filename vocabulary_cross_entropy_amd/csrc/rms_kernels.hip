@@ -306,8 +306,18 @@ __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* partial, int 
   const int c = blockIdx.x * 32 + col;
   float s = 0.0f;
   if (c < H) {
-#pragma unroll 16
-    for (int k = grp; k < n_part; k += 32) s += partial[(int64_t)k * rms_share_width(H) + c];
+    // 16 loads in flight, whatever the number of shares
+    constexpr int kLoads = 16;
+    for (int k0 = grp; k0 < n_part; k0 += 32 * kLoads) {
+      float v[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int k = min(k0 + 32 * i, n_part - 1);
+        v[i] = partial[(int64_t)k * rms_share_width(H) + c];
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) s += k0 + 32 * i < n_part ? v[i] : 0.0f;
+    }
   }
   sh[grp][col] = s;
   __syncthreads();
