@@ -9,7 +9,7 @@
 // as FP32 between the sum of squares and the output, and written once.  A row
 // belongs to TPR threads of EPL elements each: a wavefront, or a workgroup of 256
 // or 1024 (see pick_shape).  Measured at 16384 x 2304 BF16 with a residual (302 MB either
-// way): forward 47 us, 6.4 TB/s; backward 65 us, 4.7 TB/s, and 5 us more for dw's shares.
+// way): forward 47 us, 6.4 TB/s; backward 64 us, 4.8 TB/s, and 5 us more for dw's shares.
 // The backward holds three rows and dw in 225 registers, two wavefronts a SIMD; held to
 // 168 registers it spilled and took 170 us.
 //
