@@ -991,24 +991,31 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Grou
     // each listed group holds a token at least
     if (sh.n_groups > max_groups || sh.n + sh.n_groups > kCap) return kCap + 1;
     const int items = (int)sh.n_groups * kVec;
-    for (int b0 = 0; b0 < items; b0 += kItems * kRowThreads) {
-      const int i0 = b0 + threadIdx.x;
-      float z[kItems][R::VE];
-      int v[kItems];
-      u32x4_t raw[kItems];
+    int next_v[kItems];
+    u32x4_t next[kItems];
+    auto fetch = [&](int b0) {
 #pragma unroll
       for (int l = 0; l < kItems; ++l) {
-        const int i = i0 + l * kRowThreads;
-        v[l] = row.nvec;
+        const int i = b0 + (int)threadIdx.x + l * kRowThreads;
+        next_v[l] = row.nvec;
         if (i < items) {
           const int g = g0 + sh.group[i / kVec];
-          v[l] = g / kThreads * (kThreads * kVec) + (i % kVec) * kThreads + g % kThreads;
+          next_v[l] = g / kThreads * (kThreads * kVec) + (i % kVec) * kThreads + g % kThreads;
         }
-        raw[l] = u32x4_t{0, 0, 0, 0};
-        if (row.full(v[l])) raw[l] = row.raw(v[l]);
+        next[l] = u32x4_t{0, 0, 0, 0};
+        if (row.full(next_v[l])) next[l] = row.raw(next_v[l]);
       }
+    };
+    fetch(0);
+    for (int b0 = 0; b0 < items; b0 += kItems * kRowThreads) {
+      float z[kItems][R::VE];
+      int v[kItems];
 #pragma unroll
-      for (int l = 0; l < kItems; ++l) row.take(v[l], raw[l], z[l]);
+      for (int l = 0; l < kItems; ++l) {
+        v[l] = next_v[l];
+        row.take(v[l], next[l], z[l]);
+      }
+      fetch(b0 + kItems * kRowThreads);  // waits behind this round's work
       // places for all of the wavefront's hits at once
       uint32_t in = 0;
 #pragma unroll
@@ -1162,7 +1169,26 @@ __device__ __forceinline__ Drawn draw_list(const Ask& a, const Weights& wt, int6
       if (ties == ~(u64)0) continue;
       u64 c = 0;
       for (uint32_t i = t; i < n; i += kRowThreads) c += sh.list[i].key == tau;
-      if (ties >= block_sum(c, sh)) continue;
+      c = block_sum(c, sh);
+      if (ties >= c) continue;
+      if (c <= kRank) {
+        // few: their indexes side by side, and the rank of each by counting
+        uint32_t* idx = reinterpret_cast<uint32_t*>(sh.hist);
+        if (t == 0) sh.n = 0;
+        __syncthreads();
+        for (uint32_t i = t; i < n; i += kRowThreads)
+          if (sh.list[i].key == tau) idx[atomicAdd(&sh.n, 1u)] = sh.list[i].idx;
+        __syncthreads();
+        if (t < c) {
+          const uint32_t mine = idx[t];
+          uint32_t before = 0;
+          for (uint32_t i = 0; i < c; ++i) before += idx[i] < mine;
+          if (before == ties - 1) sh.out[0] = mine;
+        }
+        __syncthreads();
+        last = (uint32_t)sh.out[0];
+        continue;
+      }
       goal = (double)ties;
     } else {  // the token
       u64 v = 0;
