@@ -38,15 +38,15 @@
 //    than the list holds) is served from the row, pass by pass: 16 x 200000 with top-k
 //    20000 and top-p 0.99 take 370 us against 43 for a top-k of 5000.
 //
-// What bounds it: sample_max_kernel memory (256 x 128256 BF16 14 us, 4.7 TB/s), the
+// What bounds it: sample_max_kernel memory (256 x 128256 BF16 14 us, 4.8 TB/s), the
 // weights of a segment FP64 issue (22 instructions a token: 61 x 256003 FP32 without
 // filters 21 us), and sample_pick_kernel and sample_rest_kernel, one workgroup a row,
-// the latency of some dozen steps between barriers (256 rows of top-k 50 17 us, of
-// top-k 1000 33 us).  256 x 128256 BF16 of mixed parameters take 103 us (max 14, mass
-// 21, pick 34, kept 16, rest 19), one row with all filters 20 us.  512 threads a row: with 256
-// the mixed rows took 118 us, with 1024 no less than with 512.  The code that a usual row
-// runs is kept short, too: a kernel this brief waits for its instructions as well as for its
-// data.
+// the latency of some dozen steps between barriers (256 rows of top-k 50 18 us, of
+// top-k 1000 29 us).  256 x 128256 BF16 of mixed parameters take 95 us (max 14, mass
+// 21, pick 32, kept 10, rest 20), one row with all filters 18 to 21 us.  512 threads a
+// row: with 256 the mixed rows took 118 us where 512 took 110, with 1024 no less.  The code
+// that a usual row runs is kept short, too: a kernel this brief waits for its instructions
+// as well as for its data.
 //
 #include <math.h>
 
@@ -1461,9 +1461,9 @@ __device__ __forceinline__ void pick_row(const SampleParams& p, const Row<DT>& r
     // min-p alone: T ln(1 / min_p) and what its rounding may leave out
     hi = (float)(-(double)a.T * log(a.minp) * (1.0 + 1e-6)) + 1e-30f;
     hi += hi * 1e-6f;
-    // nothing but min-p: every token lies before the bin
+    // nothing but min-p: every token that it can keep lies before the bin, and none in it
     st.what = kThreshold;
-    st.lo = __builtin_huge_valf();
+    st.lo = hi;
     st.hi = -1.0f;
   }
   // rows that other kernels can finish over all segments gather little here, those
@@ -1505,6 +1505,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_pick_kernel(SampleParam
 // row's list (over its histogram, which has been read).
 template <int NT>
 struct KeepShared {
+  float low[NT / 64][64 * (kSeg / NT)];  // a wavefront's tokens before the bin, side by side
   u64 part[NT / 64];
   uint32_t cnt[NT / 64], base;
 };
@@ -1523,15 +1524,37 @@ __device__ __forceinline__ void keep_segment(const SampleParams& p, const Row<DT
   const float lo = p.state[r].lo, hi = p.state[r].hi;
   float z[kVec][R::VE];
   group.get(row, v0, z);
-  u64 s = 0;
-  uint32_t in = 0;  // bit j: token j is in the bin
+  // bit j: token j is in the bin, or before it
+  uint32_t in = 0, low = 0;
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) {
     const float v = z[j / R::VE][j % R::VE], d = distance(wt.m, v);
-    const u64 q = wt.kept(v);
-    s += d < lo ? q : 0;
     in |= (v != kNegInf && d >= lo && d <= hi ? 1u : 0u) << j;
+    low |= (d < lo ? 1u : 0u) << j;
     if (j % 8 == 7) __builtin_amdgcn_sched_barrier(0);
+  }
+  // The weights are what takes time: first the tokens before the bin move together, so that
+  // every lane forms one (256 rows of top-p 0.9: a weight for every token 48 us, for these
+  // 31; four at a time instead of two spilled and took 38).
+  float* mine = sh.low[wave];
+  const uint32_t n_low = __builtin_popcount(low), run_low = (uint32_t)wave_scan(n_low);
+  const int all_low = __builtin_amdgcn_readlane((int)run_low, 63);
+  uint32_t to = run_low - n_low;
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    if ((low >> j) & 1u) mine[to++] = z[j / R::VE][j % R::VE];
+    if (j % 8 == 7) __builtin_amdgcn_sched_barrier(0);
+  }
+  __syncthreads();
+  u64 s = 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < all_low; i0 += 2 * 64) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = i0 + 64 * j + lane;
+      const u64 q = wt.kept(mine[min(i, all_low - 1)]);
+      s += i < all_low ? q : 0;
+    }
   }
   s = wave_sum(s);
   const uint32_t c = __builtin_popcount(in);
@@ -1555,13 +1578,10 @@ __device__ __forceinline__ void keep_segment(const SampleParams& p, const Row<DT
   __syncthreads();
   at += sh.base;
   uint32_t* list = reinterpret_cast<uint32_t*>(p.hist + r * kBins);
-#pragma unroll
-  for (int j = 0; j < kTokens; ++j) {
-    if ((in >> j) & 1u) {
-      if (at < kCap)
-        put_shared(&list[at], (uint32_t)(row.first(v0 + (j / R::VE) * NT) + j % R::VE));
-      ++at;
-    }
+  for (; in; in &= in - 1, ++at) {
+    const int j = __builtin_ctz(in);
+    if (at < kCap)
+      put_shared(&list[at], (uint32_t)(row.first(v0 + (j / R::VE) * NT) + j % R::VE));
   }
 }
 
