@@ -230,3 +230,20 @@ def test_short_rows(V, dtype):
     run(z, g["u"], p=g["p"])
     run(z, g["u"], mp=[1e-6, 0.01, 0.5, 1.0] * 10)
     run(z, **g)
+
+
+@pytest.mark.parametrize("N,V", [(256, 5000), (257, 5000), (32, 60000), (33, 60000)])
+def test_few_and_many_segments(N, V):
+    """At and past the number of row segments up to which a row's workgroups join."""
+    z = normal(N, V, "bf16", N)
+    g = params(N, N)
+    run(z, **g)
+    ws = vce.ce_sample_workspace(N, V)
+    ws.fill_(255)
+    args = [t32(g["T"]), torch.tensor(g["k"], dtype=torch.int32, device="cuda"), t32(g["p"]),
+            t32(g["mp"])]
+    first = vce.ce_sample(z, t32(g["u"]), *args, with_logprob=True, workspace=ws)
+    for _ in range(3):  # what a call leaves in the workspace means nothing to the next
+        again = vce.ce_sample(z, t32(g["u"]), *args, with_logprob=True, workspace=ws)
+        assert torch.equal(first[0], again[0])
+        assert torch.equal(first[1].nan_to_num(7.0), again[1].nan_to_num(7.0))
