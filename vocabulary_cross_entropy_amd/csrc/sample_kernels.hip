@@ -981,6 +981,10 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Grou
   constexpr int kItems = 2;  // vectors in flight per thread
   __syncthreads();
   if (threadIdx.x == 0) sh.n = 0;
+  // sh.n as every batch of groups starts.  It decides whether the batch still fits, and comes from
+  // a register: wavefronts that are already gathering the batch add to sh.n, and one that read it
+  // late could leave alone.
+  uint32_t have = 0;
   for (int g0 = 0; g0 < groups.n; g0 += GroupMax::kBatch) {
     if (threadIdx.x == 0) sh.n_groups = 0;
     __syncthreads();
@@ -989,8 +993,9 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Grou
     });
     __syncthreads();
     // each listed group holds a token at least
-    if (sh.n_groups > max_groups || sh.n + sh.n_groups > kCap) return kCap + 1;
-    const int items = (int)sh.n_groups * kVec;
+    const uint32_t listed = sh.n_groups;
+    if (listed > max_groups || have + listed > kCap) return kCap + 1;
+    const int items = (int)listed * kVec;
     int next_v[kItems];
     u32x4_t next[kItems];
     auto fetch = [&](int b0) {
@@ -1043,14 +1048,14 @@ __device__ __forceinline__ uint32_t gather_groups(const Row<DT>& row, const Grou
       }
     }
     __syncthreads();
-    if (sh.n > kCap) return sh.n;
+    have = sh.n;  // not added to before the next batch's second barrier
+    if (have > kCap) return have;
   }
   // the weights last, when every thread has its share of them
-  const uint32_t n = sh.n;
-  for (uint32_t i = threadIdx.x; i < n; i += kRowThreads)
+  for (uint32_t i = threadIdx.x; i < have; i += kRowThreads)
     sh.list[i] = entry_of<DT>(wt, __uint_as_float(sh.list[i].key), sh.list[i].idx);
   __syncthreads();
-  return n;
+  return have;
 }
 
 struct Drawn {
@@ -1471,7 +1476,8 @@ __device__ __forceinline__ void pick_row(const SampleParams& p, const Row<DT>& r
   const uint32_t most = a.has_k ? (a.k > kCap ? 0 : kCap) : st.what == kThreshold ? 512 : kCap;
   const uint32_t n = gather_groups<DT>(row, groups, wt, hi, a.small(p.V) ? kCap : most, sh);
   if (n > kCap) {
-    if (t == 0) p.state[r] = st;
+    // (a call without state has rows of at most kCap tokens, which always fit)
+    if (t == 0 && p.state) p.state[r] = st;
     return;
   }
   const Drawn d = draw_list<DT>(a, wt, p.V, n, mass, false, 0, sh);
