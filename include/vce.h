@@ -560,8 +560,10 @@ int mx_dequantize(const uint8_t* q, const uint8_t* scales, int format, int64_t r
  * largest of the eight: with an E4M3 operand a logit is off by at most 2^-10 of the sum,
  * over its groups of eight, of each group's largest product.  (E2M1 products are never
  * cut.)  FP32 results with an E4M3 operand are multiplied in BF16, where every product is
- * exact, at half the rate; only K ranges with scales outside 2^-63 .. 2^64 fall
- * back to the scaled instructions.
+ * exact, at half the rate.  Only the logits of a token or a row of W that holds a block
+ * with a scale outside 2^-63 .. 2^64 and a value other than zero, or a NaN scale, come from
+ * the scaled instructions, in a second pass over the tile; other tokens and rows do not
+ * change by it.
  *
  *  x, x_scales, w, w_scales: values and scales in x_format and w_format (any
  *           pair), contiguous, values 16-byte aligned.  A scale of 255 makes the

@@ -10,9 +10,11 @@
 //    2^-13 of the largest beside it, which a BF16 result (2^-8) does not show.
 //  * kBf16: the operands are widened to BF16 in registers, scale included
 //    (exact: 4 significant bits), and multiplied by the BF16 instructions at half
-//    the rate.  FP32 results with an E4M3 operand take this one.  Supersteps that
-//    hold a scale outside 2^-63 .. 2^64 (or a NaN one) could leave BF16's range
-//    and go through the scaled instructions instead.
+//    the rate.  FP32 results with an E4M3 operand take this one.  A token or a row of W
+//    with a scale outside 2^-63 .. 2^64 could leave BF16's range: it is far, and its
+//    logits, no others, come from a second pass through the scaled instructions.  A
+//    block of zeros is not far, whatever its scale (mx_quantize gives it the least);
+//    a NaN scale is.
 //
 // Operand layout of the scaled instruction (measured): lane l holds row l % 16; with
 // g = l / 16 its E2M1 slots 0..31 are k = 32 g .. 32 g + 31, its E4M3 slots
@@ -41,12 +43,22 @@ constexpr int kSkinnyThreads = 256;
 
 enum Mode { kScaled, kBf16 };
 
+// Bit 7 of every byte of four scales that lies outside 64 .. 191.
+__device__ __forceinline__ uint32_t far_scales(uint32_t sc) {
+  return ~(sc ^ (sc << 1)) & 0x80808080u;
+}
+
 template <int FMT>
 struct Fmt {
   static constexpr int kCode = FMT == kMxE4M3 ? 0 : 4;  // the instruction's format field
   static constexpr int kPieces = FMT == kMxE4M3 ? 2 : 1;  // 16-byte pieces per lane and step
   // bytes per 32 values
   static constexpr int kBlockBytes = FMT == kMxE4M3 ? 32 : 16;
+  static constexpr uint32_t kMagnitudes = FMT == kMxE4M3 ? 0x7f7f7f7fu : 0x77777777u;
+  // Not 0 where one of a piece's values is not.
+  static __device__ __forceinline__ uint32_t some(const u32x4_t& q) {
+    return (q[0] | q[1] | q[2] | q[3]) & kMagnitudes;
+  }
 };
 
 // One row's operands of a superstep for one lane: the 16-byte pieces of its
@@ -99,23 +111,17 @@ struct SuperFrag {
     }
     return r;
   }
-  // Not 0 where one of the four scales lies outside 64 .. 191.
-  __device__ __forceinline__ uint32_t far() const {
-    return ~(sc ^ (sc << 1)) & 0x80808080u;
-  }
-  // operand(s) from kBf16's layout: an E4M3 lane's pieces come from the lanes
-  // that hold blocks g / 2 and 2 + g / 2 of the instruction.
-  __device__ __forceinline__ i32x8_t operand_moved(int s, int lane) const {
-    if constexpr (FMT == kMxE2M1) return operand(s);
-    const int g = lane >> 4, src = (lane & 15) + 16 * (g / 2);
-    i32x8_t r;
+  // Is one of the four blocks far?  (In kBf16's layout, whole blocks of a row to a lane.)
+  __device__ __forceinline__ bool far() const {
+    const uint32_t f = far_scales(sc);
+    bool r = false;
+    if (f) {  // a block of zeros, as a rule
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int lo = __shfl((int)q[s][0][j], src + 32 * h, 64);
-        const int hi = __shfl((int)q[s][Fmt<FMT>::kPieces - 1][j], src + 32 * h, 64);
-        r[4 * h + j] = g % 2 ? hi : lo;
+      for (int s = 0; s < 4; ++s) {
+        const uint32_t byte = (sc >> (8 * s)) & 255u;
+        uint32_t any = byte == 255u ? 1u : Fmt<FMT>::some(q[s][0]);
+        if constexpr (Fmt<FMT>::kPieces == 2) any |= Fmt<FMT>::some(q[s][1]);
+        r |= ((f >> (8 * s)) & 0x80u) && any;
       }
     }
     return r;
@@ -248,6 +254,21 @@ struct SkinnyX {
     }
     return r;
   }
+  // Is one of the lane group's blocks 4 g .. of superstep ss, with scales sc, far?
+  __device__ __forceinline__ bool far(int c, int ss, int g, uint32_t sc) const {
+    bool r = false;
+    if (const uint32_t f = far_scales(sc)) {
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s) {
+        uint32_t any = ((sc >> (8 * s)) & 255u) == 255u;
+#pragma unroll
+        for (int h = 0; h < Fmt<FX>::kPieces; ++h)
+          any |= Fmt<FX>::some(chunk(c, (ss * 16 + s + 4 * g) * Fmt<FX>::kPieces + h));
+        r |= ((f >> (8 * s)) & 0x80u) && any;
+      }
+    }
+    return r;
+  }
   // Values 8 t .. of step st's block of this lane group as BF16, scale applied.
   __device__ __forceinline__ bf16x8_t wide(const u32x4_t* piece, uint32_t sc, int st, int t) const {
     SuperFrag<FX, kBf16, false> f;
@@ -258,48 +279,31 @@ struct SkinnyX {
   }
 };
 
-template <int FX, int FW, int MODE, int kFrags, int DT>
-__global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxGemmParams p) {
-  constexpr int kRows = 16 * kFrags;
-  __shared__ __attribute__((aligned(256))) SkinnyX<FX> x;
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int64_t v0 = (int64_t)blockIdx.x * (kRows * 4) + wave * kRows;
+// acc += the products of this lane's rows of W (16 kFrags of the wavefront's) and tokens.
+// kBf16 also tells whether this lane's blocks of token c or of its row of fragment i are
+// far.  Every thread of the workgroup calls it.
+template <int FX, int FW, int MODE, int kFrags>
+__device__ __forceinline__ void skinny_pass(const MxGemmParams& p, SkinnyX<FX>& x,
+                                            const uint8_t* const (&wr)[kFrags],
+                                            const uint8_t* const (&ws)[kFrags], int g, int c,
+                                            f32x4_t (&acc)[kFrags], bool& far_x,
+                                            bool (&far_w)[kFrags]) {
   const int nblk = (int)(p.K / kMxBlock);
-  const int64_t wb = (int64_t)nblk * Fmt<FW>::kBlockBytes;
-  const uint8_t *wr[kFrags], *ws[kFrags];
-#pragma unroll
-  for (int i = 0; i < kFrags; ++i) {  // rows past the end repeat the last one
-    const int64_t r = min(v0 + 16 * i + c, p.V - 1);
-    wr[i] = p.w + r * wb;
-    ws[i] = p.ws + r * nblk;
-  }
-  f32x4_t acc[kFrags];
-#pragma unroll
-  for (int i = 0; i < kFrags; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   // the products of superstep ss (of the part in LDS)
   auto multiply = [&](const auto (&w)[kFrags], int ss) {
     const uint32_t sx = x.scales(c, ss, g);
-    bool scaled = MODE == kScaled;
-    if constexpr (MODE == kBf16) {
-      uint32_t far = ~(sx ^ (sx << 1)) & 0x80808080u;
-#pragma unroll
-      for (int i = 0; i < kFrags; ++i) far |= w[i].far();
-      scaled = __any(far != 0);
-    }
-    if (scaled) {
+    if constexpr (MODE == kScaled) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const i32x8_t b = x.operand(c, ss, s, g);
 #pragma unroll
-        for (int i = 0; i < kFrags; ++i) {
-          if constexpr (MODE == kScaled)
-            acc[i] = mfma16<FW, FX>(w[i].operand(s), b, acc[i], w[i].sc, sx, s);
-          else
-            acc[i] = mfma16<FW, FX>(w[i].operand_moved(s, lane), b, acc[i], w[i].sc, sx, s);
-        }
+        for (int i = 0; i < kFrags; ++i)
+          acc[i] = mfma16<FW, FX>(w[i].operand(s), b, acc[i], w[i].sc, sx, s);
       }
     } else {
+      far_x |= x.far(c, ss, g, sx);
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) far_w[i] |= w[i].far();
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         u32x4_t piece[2];
@@ -346,6 +350,55 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxGemmPara
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) last[i].load(wr[i], ws[i], s0 + full, g, nblk);
       multiply(last, full);
+    }
+  }
+}
+
+template <int FX, int FW, int MODE, int kFrags, int DT>
+__global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxGemmParams p) {
+  constexpr int kRows = 16 * kFrags;
+  __shared__ __attribute__((aligned(256))) SkinnyX<FX> x;
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t v0 = (int64_t)blockIdx.x * (kRows * 4) + wave * kRows;
+  const int nblk = (int)(p.K / kMxBlock);
+  const int64_t wb = (int64_t)nblk * Fmt<FW>::kBlockBytes;
+  const uint8_t *wr[kFrags], *ws[kFrags];
+  f32x4_t acc[kFrags];
+  bool far_x = false, far_w[kFrags];
+#pragma unroll
+  for (int i = 0; i < kFrags; ++i) {  // rows past the end repeat the last one
+    const int64_t r = min(v0 + 16 * i + c, p.V - 1);
+    wr[i] = p.w + r * wb;
+    ws[i] = p.ws + r * nblk;
+    acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    far_w[i] = false;
+  }
+  skinny_pass<FX, FW, MODE, kFrags>(p, x, wr, ws, g, c, acc, far_x, far_w);
+  if constexpr (MODE == kBf16) {
+    bool any = far_x;
+#pragma unroll
+    for (int i = 0; i < kFrags; ++i) any |= far_w[i];
+    if (__syncthreads_or(any)) {  // every wavefront has read X
+      f32x4_t scaled[kFrags];
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) scaled[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      skinny_pass<FX, FW, kScaled, kFrags>(p, x, wr, ws, g, c, scaled, far_x, far_w);
+      // the four lane groups hold a token's and a row's blocks; bit r of a ballot folded over
+      // them is token or row r
+      auto fold = [](bool f) {
+        uint64_t m = __ballot(f);
+        m |= m >> 32;
+        return (uint32_t)(m | m >> 16) & 0xffffu;
+      };
+      const uint32_t tokens = fold(far_x);
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) {
+        const uint32_t rows = fold(far_w[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = ((tokens >> c | rows >> (4 * g + j)) & 1u) ? scaled[i][j] : acc[i][j];
+      }
     }
   }
   if (c >= p.M) return;
@@ -771,9 +824,15 @@ struct MxTile {
   }
 
   // Register q of block (a, b) holds token m0 + wm + 32 a + 8 (q / 4) + 4 g + q % 4,
-  // row v0 + wn + 32 b + c of W.
-  template <int DT>
-  __device__ __forceinline__ void store(const MxGemmParams& p, int64_t m0, int64_t v0) const {
+  // row v0 + wn + 32 b + c of W.  PICK, given `far`: the logits whose token or row is far, or
+  // (far_ones false) the others only.
+  template <int DT, bool PICK = false>
+  __device__ __forceinline__ void store(const MxGemmParams& p, int64_t m0, int64_t v0,
+                                        const uint8_t* far = nullptr,
+                                        bool far_ones = false) const {
+    bool fv[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) fv[b] = PICK && far && far[kTileM + wn + 32 * b + c];
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
 #pragma unroll
@@ -785,8 +844,13 @@ struct MxTile {
           const float x = acc[a][b][q] * p.scale, y = acc[a][b][q + 1] * p.scale;
           if constexpr (DT == 0) {
             float* o = static_cast<float*>(p.out) + m * p.ldo + v;
-            if (v < p.V && m < p.M) *o = x;
-            if (v < p.V && m + 1 < p.M) o[p.ldo] = y;
+            bool ok0 = v < p.V && m < p.M, ok1 = v < p.V && m + 1 < p.M;
+            if (PICK && far) {
+              ok0 = ok0 && (fv[b] || far[m - m0]) == far_ones;
+              ok1 = ok1 && (fv[b] || far[m - m0 + 1]) == far_ones;
+            }
+            if (ok0) *o = x;
+            if (ok1) o[p.ldo] = y;
           } else {
             // lanes pair up: the even one stores two logits of token m, the odd
             // one two of token m + 1
@@ -811,17 +875,51 @@ struct MxTile {
   }
 };
 
-// Is a scale of these rows of an operand outside 2^-63 .. 2^64?
-__device__ __forceinline__ bool mx_far_row(const uint8_t* row, int nblk) {
-  uint32_t far = 0;
-  int b = 0;
-  for (; b + 4 <= nblk; b += 4) {
-    uint32_t w;
-    __builtin_memcpy(&w, row + b, 4);
-    far |= ~(w ^ (w << 1)) & 0x80808080u;
+// Scales 4 i .. 4 i + 3 of a row, 127 past its end.
+__device__ __forceinline__ uint32_t mx_scales4(const uint8_t* srow, int i, int nblk) {
+  uint32_t sc = 0x7f7f7f7fu;
+  if (4 * i + 4 <= nblk) {
+    __builtin_memcpy(&sc, srow + 4 * i, 4);
+  } else {
+    for (int s = 0; 4 * i + s < nblk; ++s)
+      sc = (sc & ~(255u << (8 * s))) | ((uint32_t)srow[4 * i + s] << (8 * s));
   }
-  for (; b < nblk; ++b) far |= (uint32_t)row[b] - 64u > 127u;
-  return far != 0;
+  return sc;
+}
+
+// Is a block of this row of an operand far?
+template <int FMT>
+__device__ __forceinline__ bool mx_far_row(const uint8_t* row, const uint8_t* srow, int nblk) {
+  constexpr int kPieces = Fmt<FMT>::kPieces;
+  // the scales alone first, without a branch between their loads: a tile of 128 tokens took
+  // 6 us longer at K = 4096 with the values behind a branch on each four
+  uint32_t f = 0;
+  const int whole = nblk / 4, n4 = (nblk + 3) / 4;
+  for (int i = 0; i < whole; ++i) f |= far_scales(mx_scales4(srow, i, nblk));
+  if (whole < n4) f |= far_scales(mx_scales4(srow, whole, nblk));
+  if (f == 0) return false;
+  // blocks of zeros, as a rule, or a whole row of them: eight blocks' values in flight
+  // together (100 zeros of 256 tokens, 32000 rows, K = 4096: 84 us, four at a time 89, no zeros 70)
+  for (int i = 0; i < n4; i += 2) {
+    const uint32_t sc[2] = {mx_scales4(srow, i, nblk), mx_scales4(srow, i + 1, nblk)};
+    if ((far_scales(sc[0]) | far_scales(sc[1])) == 0) continue;
+    u32x4_t q[8][kPieces];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h)
+        q[s][h] = reinterpret_cast<const u32x4_t*>(row)[min(4 * i + s, nblk - 1) * kPieces + h];
+    uint32_t any = 0;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint32_t b = sc[s / 4] >> (8 * (s % 4));
+      uint32_t v = (b & 255u) == 255u ? 1u : Fmt<FMT>::some(q[s][0]);
+      if constexpr (kPieces == 2) v |= Fmt<FMT>::some(q[s][1]);
+      if ((far_scales(sc[s / 4]) >> (8 * (s % 4))) & 0x80u) any |= v;
+    }
+    if (any) return true;
+  }
+  return false;
 }
 
 // Workgroup number -> tile: workgroups go round-robin over the 8 XCDs, so each
@@ -854,21 +952,33 @@ mx_tile_kernel(MxGemmParams p) {
   mx_tile_of(blockIdx.x, n_ti, n_tj, &ti, &tj);
   const int64_t m0 = ti * T::kTileM, v0 = tj * kTileN;
   uint8_t MX_LDS* sm = (uint8_t MX_LDS*)smem;
-  if constexpr (MODE == kBf16) {
-    // scales that BF16 operands may not carry: the scaled instructions instead
-    const int t = threadIdx.x, nblk = (int)(p.K / kMxBlock);
-    bool far = v0 + t < p.V && mx_far_row(p.ws + (v0 + t) * nblk, nblk);
-    if (t < T::kTileM && m0 + t < p.M) far |= mx_far_row(p.xs + (m0 + t) * nblk, nblk);
-    if (__syncthreads_or(far)) {
-      MxTile<FX, FW, kScaled, NA> s;
-      s.template run<MASK>(p, m0, v0, sm);
-      s.template store<DT>(p, m0, v0);
-      return;
-    }
-  }
   T s;
-  s.template run<MASK>(p, m0, v0, sm);
-  s.template store<DT>(p, m0, v0);
+  if constexpr (MODE == kBf16) {
+    // the tile's far tokens and rows
+    __shared__ uint8_t far[T::kTileM + kTileN];
+    const int t = threadIdx.x, nblk = (int)(p.K / kMxBlock);
+    const int64_t v = v0 + t, m = m0 + t;
+    const bool fw = v < p.V && mx_far_row<FW>(p.w + v * nblk * Fmt<FW>::kBlockBytes,
+                                              p.ws + v * nblk, nblk);
+    const bool fx = t < T::kTileM && m < p.M &&
+                    mx_far_row<FX>(p.x + m * nblk * Fmt<FX>::kBlockBytes, p.xs + m * nblk, nblk);
+    far[T::kTileM + t] = fw;
+    if (t < T::kTileM) far[t] = fx;
+    const bool any = __syncthreads_or(fw | fx);
+    s.template run<MASK>(p, m0, v0, sm);
+    s.template store<DT, true>(p, m0, v0, any ? far : nullptr, false);
+    if (!any) return;
+    __syncthreads();  // the stages have been read
+    // the compiler is kept from holding the first pass's addresses for the second (spills)
+    int64_t m1 = m0, v1 = v0;
+    asm volatile("" : "+s"(m1), "+s"(v1));
+    MxTile<FX, FW, kScaled, NA> far_tile;
+    far_tile.template run<MASK>(p, m1, v1, sm);
+    far_tile.template store<DT, true>(p, m1, v1, far, true);
+  } else {
+    s.template run<MASK>(p, m0, v0, sm);
+    s.template store<DT>(p, m0, v0);
+  }
 }
 
 template <int FX, int FW, int MODE, int NA, int DT>
