@@ -1466,9 +1466,11 @@ __device__ __forceinline__ void pick_row(const SampleParams& p, const Row<DT>& r
     // min-p alone: T ln(1 / min_p) and what its rounding may leave out
     hi = (float)(-(double)a.T * log(a.minp) * (1.0 + 1e-6)) + 1e-30f;
     hi += hi * 1e-6f;
-    // nothing but min-p: every token that it can keep lies before the bin, and none in it
+    // nothing but min-p: every token that it can keep lies before the bin, and none in it.
+    // A bound beyond FP32 bounds nothing, nor do the distances that overflow with it: NaN,
+    // before which every token lies
     st.what = kThreshold;
-    st.lo = hi;
+    st.lo = hi < __builtin_huge_valf() ? hi : __builtin_nanf("");
     st.hi = -1.0f;
   }
   // rows that other kernels can finish over all segments gather little here, those
@@ -1536,7 +1538,7 @@ __device__ __forceinline__ void keep_segment(const SampleParams& p, const Row<DT
   for (int j = 0; j < kTokens; ++j) {
     const float v = z[j / R::VE][j % R::VE], d = distance(wt.m, v);
     in |= (v != kNegInf && d >= lo && d <= hi ? 1u : 0u) << j;
-    low |= (d < lo ? 1u : 0u) << j;
+    low |= (!(d >= lo) ? 1u : 0u) << j;
     if (j % 8 == 7) __builtin_amdgcn_sched_barrier(0);
   }
   // The weights are what takes time: first the tokens before the bin move together, so that
