@@ -605,7 +605,8 @@ int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uin
  *  temperature, top_p, min_p (N) FP32 and top_k (N) int32, or NULL for 1, 1, 0
  *           and 0: per row, in flattened row order.  Off: top_k <= 0 or >= V,
  *           top_p >= 1, min_p <= 0.  top_p <= 0 keeps the first token, min_p >= 1
- *           the maxima.
+ *           those of weight 1 (in FP64: the maxima, and at temperatures 2^53 times a
+ *           token's distance from them that token too).
  *  u        (N) FP32 in [0, 1).
  *  token    (N) int64.  -1 where the row has no answer: a NaN logit, no logit
  *           above -inf, T negative, infinite or NaN, u outside [0, 1), top_p or

@@ -4,13 +4,26 @@ import pytest
 import torch
 
 from head_testutil import DT
-from test_parity_sample import FMAX, run
+from test_parity_sample import FMAX, normal, run
 
 pytestmark = pytest.mark.gpu
 
 
 def uniform(N, seed):
     return np.random.default_rng(seed).random(N, dtype=np.float32).tolist()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [300, 4096, 5000, 40000])
+def test_min_p_where_every_weight_is_one(V, dtype):
+    """T so large that each weight is 1 in FP64: min_p = 1 keeps every token, alone as after
+    the other filters."""
+    N = 24
+    z, u = normal(N, V, dtype, V), uniform(N, V)
+    T = [1e20, 1e30] * (N // 2)
+    run(z, u, T=T, mp=[1.0] * N)
+    run(z, u, T=T, mp=[2.0] * N, k=[V // 2] * N)
+    run(z, u, T=T, mp=[1.0] * N, p=[0.7] * N)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])

@@ -1463,8 +1463,9 @@ __device__ __forceinline__ void pick_row(const SampleParams& p, const Row<DT>& r
       st.mass = mass;
     }
   } else {
-    // min-p alone: T ln(1 / min_p) and what its rounding may leave out
-    hi = (float)(-(double)a.T * log(a.minp) * (1.0 + 1e-6)) + 1e-30f;
+    // min-p alone: T ln(1 / min_p) and what its rounding, or a weight's (1e-12 covers its error
+    // of 4e-14, and the tokens that weigh 1 in FP64 beside the maxima), may leave out
+    hi = (float)((double)a.T * (1e-12 - log(a.minp) * (1.0 + 1e-6))) + 1e-30f;
     hi += hi * 1e-6f;
     // nothing but min-p: every token that it can keep lies before the bin, and none in it.
     // A bound beyond FP32 bounds nothing, nor do the distances that overflow with it: NaN,
