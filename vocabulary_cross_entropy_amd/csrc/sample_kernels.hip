@@ -765,7 +765,7 @@ __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleParams p) {
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   if (__any(nan)) m = __builtin_nanf("");
   if ((t & 63) == 0) sh[t >> 6] = m;
-  if (seg == 0 && t < 2) p.done[2 * r + t] = 0;
+  if (seg == 0 && t < 2 && p.done) p.done[2 * r + t] = 0;
   // the row's histogram starts at zero, a share of it per segment
   if (ask_of(p, r).hist(p.V)) {
     for (int64_t b = seg * kThreads + t; b < kBins; b += (int64_t)p.segs * kThreads)
@@ -1807,10 +1807,14 @@ bool sample_size_ok(int64_t N, int64_t V) {
          N * segments(V) < ((int64_t)1 << 31);
 }
 
+// Rows of at most kCap tokens are served by sample_max_kernel and sample_pick_kernel alone:
+// they need no sums, histogram, state or counters.
 size_t sample_workspace_bytes(int64_t N, int64_t V) {
   const size_t rows = (size_t)N, s = rows * (size_t)segments(V);
-  return 256 + up256(s * kThreads * 4) + up256(s * 4) + up256(s * 8) + up256(rows * kBins * 8) +
-         up256(rows * sizeof(SampleState)) + up256(rows * 8);
+  const size_t maxima = 256 + up256(s * kThreads * 4) + up256(s * 4);
+  if (V <= kCap) return maxima;
+  return maxima + up256(s * 8) + up256(rows * kBins * 8) + up256(rows * sizeof(SampleState)) +
+         up256(rows * 8);
 }
 
 hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
@@ -1836,15 +1840,16 @@ hipError_t launch_sample(SampleParams p, int dtype, int64_t N, void* workspace,
   };
   p.group_max = reinterpret_cast<float*>(take(s * kThreads * 4));
   p.seg_max = reinterpret_cast<float*>(take(s * 4));
-  p.seg_sum = reinterpret_cast<unsigned long long*>(take(s * 8));
-  p.hist = reinterpret_cast<unsigned long long*>(take(rows * kBins * 8));
-  p.state = reinterpret_cast<SampleState*>(take(rows * sizeof(SampleState)));
-  p.done = reinterpret_cast<uint32_t*>(take(rows * 8));
+  const bool mass = p.V > kCap;
+  if (mass) {
+    p.seg_sum = reinterpret_cast<unsigned long long*>(take(s * 8));
+    p.hist = reinterpret_cast<unsigned long long*>(take(rows * kBins * 8));
+    p.state = reinterpret_cast<SampleState*>(take(rows * sizeof(SampleState)));
+    p.done = reinterpret_cast<uint32_t*>(take(rows * 8));
+  }
   p.rows = (uint32_t)N;
   const dim3 seg_grid = grid2(N * p.segs);
-  // rows of at most kCap tokens are served by the pick kernel alone; without filters no
-  // row has candidates
-  const bool mass = p.V > kCap;
+  // without filters no row has candidates
   const bool rest = mass && (p.top_k || p.top_p || p.min_p);
   const bool joined = mass && N * p.segs <= kJoined;
   p.has = (p.temperature ? SampleParams::kT : 0) | (p.top_k ? SampleParams::kK : 0) |

@@ -261,6 +261,7 @@ struct SampleParams {
   int segs = 0;                             // segments per row
   float* group_max = nullptr;               // (N, segs, 256)
   float* seg_max = nullptr;                 // (N, segs)
+  // the others only for rows that LDS does not hold whole
   unsigned long long* seg_sum = nullptr;    // (N, segs)
   unsigned long long* hist = nullptr;       // (N, 2048)
   SampleState* state = nullptr;             // (N), NULL where every row is done in one kernel
