@@ -469,8 +469,10 @@ int vce_gemm_bf16(const void* P, int64_t ldp, int p_dim, const void* Q, int64_t 
  *     y_j = h_j r (w_j + weight_offset)
  * in FP32 from the inputs to y, rounded once; h is normed before it is rounded
  * for storage.  The sum of squares is an FP32 sum: it overflows when sqrt(H)
- * |h| reaches about 1.8e19 (y is 0 then).  A NaN or infinity makes its row's y
- * NaN where the formula does.  eps = 0 gives NaN for a row of zeros.
+ * |h| reaches about 1.8e19 (y is 0 then), and squares below 2^-149 (|h| below
+ * about 2.6e-23) add nothing, which shows where eps is 0 or as small.  A NaN or
+ * infinity makes its row's y NaN where the formula does.  eps = 0 gives NaN for
+ * a row of zeros.
  *
  *  rms_forward
  *   x, residual (M, H) of `dtype`; row i starts at element i * ldx (i * ldr),
@@ -504,7 +506,9 @@ int vce_gemm_bf16(const void* P, int64_t ldp, int p_dim, const void* Q, int64_t 
  *   dweight (H) FP32 or NULL, overwritten (zeros with M = 0).
  *   workspace: at least rms_backward_workspace_size(M, H) bytes, 16-byte
  *     aligned, needed with dweight only; its contents need not survive.
- *   The sums' order depends on M and H only: results are reproducible.
+ *   The sums' order depends on M, H and dtype, and on whether the rows, weight
+ *   and H allow 16-byte loads: the same call on the same pointers gives the same
+ *   bits.  A pointer moved off a 16-byte boundary may change the last ones.
  */
 int rms_forward(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
                 int64_t ldr, const void* weight, int wdtype, float weight_offset, float eps,
@@ -540,8 +544,9 @@ int rms_backward(const void* dy, const void* h, int dtype, int64_t M, int64_t H,
  *    scale 255 and zero values.  q 16-byte aligned; x needs its element's
  *    alignment (16-byte rows take the wide loads).
  *  mx_dequantize: the values q and scales stand for, as FP32 (exact) or BF16
- *    (exact unless below BF16's normal range, where they round); out (rows, K)
- *    contiguous, 16-byte aligned.
+ *    (exact unless below BF16's normal range, where they round); infinite where the
+ *    value lies past the type's range (inputs next to FP32's largest round up to 2^128);
+ *    out (rows, K) contiguous, 16-byte aligned.
  *  Outputs must not overlap inputs (VCE_EALIAS).
  */
 enum vce_mx_format { VCE_MX_E4M3 = 0, VCE_MX_E2M1 = 1 };
