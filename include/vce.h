@@ -598,7 +598,8 @@ int mx_logits(const uint8_t* x, const uint8_t* x_scales, int x_format, const uin
  *          of the mass, at least one token
  *   min-p  the tokens with w_i >= min_p (the largest w is 1)
  * The token is the first kept i, in index order, with sum_{kept j <= i} w_j >
- * u * sum_kept w.  T = 0 takes the first maximum whatever the filters and u.
+ * u * sum_kept w.  T = 0 takes the first maximum whatever the filters and u, as long as they
+ * are valid.
  * Weights are formed in FP64 and rounded to 2^-44 of the largest (2^(62 -
  * ceil(log2 V)) of it above V = 2^18); their sums are exact, so the token does not
  * depend on how the work is split, and is reproducible.

@@ -441,8 +441,9 @@ hipError_t launch_skinny(const MxGemmParams& p, hipStream_t stream) {
 // then holds 32 consecutive logits of a token across lanes.
 //
 // Few tokens are bound by reading W (61 x 2304 x 256003 E2M1 to FP32, 376 MB: 84 us, 4.5
-// TB/s), many by the matrix unit (4096 x 4096 x 32000 E4M3 x E2M1 to BF16: 450 us, 2.39
-// PFLOP/s; with kBf16 to FP32 859 us, 1.25 PFLOP/s).
+// TB/s), many by the matrix unit (4096 x 4096 x 32000 to BF16, E4M3 x E2M1: 436 to 462 us,
+// 2.32 to 2.46 PFLOP/s; E2M1 x E2M1 359 us; E4M3 x E4M3 733 us; with kBf16 to FP32 847 to 886 us,
+// 1.21 to 1.27 PFLOP/s, E4M3 x E4M3 1110 to 1150 us).
 
 constexpr int kTileN = 256;   // rows of W per tile
 constexpr int kSlice = 128;   // k per slice
@@ -635,7 +636,7 @@ struct MxTile {
   typename FragOf<FW>::T fb[2][NB];
   uint32_t sa[NA], sb[NB];
   // slices in flight in registers: two, but one beside 256 accumulators and E4M3
-  // fragments (two took 170 to 220 registers too many)
+  // fragments (two took 170 to 220 registers too many; with one, kBf16 still spills 14 at most)
   static constexpr int kBuf = NA == 4 && (FX == kMxE4M3 || FW == kMxE4M3) ? 1 : 2;
   u32x4_t r[kBuf][kUnits];
   u32x2_t scx, scw;  // the next superstep's scales of row threadIdx.x of either operand

@@ -4,9 +4,10 @@
 //
 // Both directions move memory: a wavefront reads 16 bytes a lane, forms each
 // block's largest magnitude across the 4 (BF16) or 8 (FP32) lanes that hold
-// it, and writes the packed bytes.  32000 x 4096 BF16 to E2M1 (332 MB) takes 65 us, back
-// 62 us: 5.1 and 5.3 TB/s; four places a thread and the scales of a wavefront in one
-// store were no faster (63 us, E4M3 74 against 70).
+// it, and writes the packed bytes.  32000 x 4096 BF16 to E2M1 (332 MB) takes 57 to 65 us,
+// back 53 to 59, each called again and again; in turn 75 and 54 us.  E4M3
+// (397 MB) 68 to 74 us and 66.  Four places a thread and the scales of a wavefront in one store
+// were no faster (63 us, E4M3 74 against 70).
 #include "mx_device.h"
 #include "vce_internal.h"
 

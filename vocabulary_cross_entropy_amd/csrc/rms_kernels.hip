@@ -10,8 +10,12 @@
 // belongs to TPR threads of EPL elements each: a wavefront, or a workgroup of 256
 // or 1024 (see pick_shape).  Measured at 16384 x 2304 BF16 with a residual (302 MB either
 // way): forward 47 us, 6.4 TB/s; backward 64 us, 4.8 TB/s, and 5 us more for dw's shares.
-// The backward holds three rows and dw in 225 registers, two wavefronts a SIMD; held to
-// 168 registers it spilled and took 170 us.
+// The backward takes 225 registers at 40 elements a lane, two wavefronts a SIMD: three packed
+// rows and dw are 100 of them, the rest unpacked values kept from one use to the next; held to
+// 168 registers it spilled and took 170 us.  Its workgroups of 1024 threads are held to 128
+// registers, and where a lane has 32 elements (rows above 16384) or 16 read one by one (odd
+// rows above 8192) 27 to 178 of them spill: 2048 x 32768 BF16 319 us, 2048 x 17024 254, 4096
+// x 9001 271, 2048 x 16385 797, against 45 to 89 of memory traffic.
 //
 // Loads go through buffer descriptors that end at the row (a lane past it
 // reads zeros), so all loads of a row issue together, without branches.
@@ -337,9 +341,12 @@ bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 // Calls f with the threads per row and elements per lane as constants.  A
 // wavefront per row needs no barrier and wins while it holds 16 elements a lane at
 // most (forward at H = 1024: 40 us against 45 by 256 threads; at 2304 55 against
-// 51); the backward, whose rows meet no other barrier, up to 40 (at 2304 62 us
-// against 66; at 4096 with 64 elements 159 against 101).  Few rows take more threads
-// each whatever H is.
+// 51); the backward, whose rows meet no other barrier, up to 40 (16384 rows of BF16, calls
+// with dw, against 256 threads: H = 1056 41 us and 49, 1536 46 and 50, 2048 57 and 61, 2304
+// 68 and 86, 2560 77 and 90; at 4096 with 64 elements 159 against 101).  Rows read one by
+// one take 10 elements a lane up to 2560 (against 16: 8192 x 1029 FP32 backward 34 us and
+// 54, 1537 40 and 61, 2559 73 and 100; 16384 x 2305 BF16 forward 75 and 90, backward 103
+// and 206).  Few rows take more threads each whatever H is.
 template <int VE, bool BWD, class F>
 hipError_t pick_shape(int64_t M, int H, F f) {
   using std::integral_constant;
