@@ -107,3 +107,51 @@ def test_zero_blocks(M, V, K, xf, wf):
     for bx, bw in ((0, 127), (127, 0), (0, 0), (254, 3)):
         xs[hx], ws[hw] = bx, bw
         assert same_bits(vce.mx_logits(x, xs, w, ws, **args), want)
+
+
+@pytest.mark.parametrize("xf,wf", [("e4m3", "e2m1"), ("e4m3", "e4m3")])
+@pytest.mark.parametrize("M,V,K", [(1, 1, 32), (2, 5, 32), (13, 333, 608), (17, 1, 32), (70, 301, 288),
+                                   (100, 49301, 160), (280, 24701, 128)])
+def test_padded_outputs(M, V, K, xf, wf):
+    """Far and NaN rows write their own logits only, whatever the output's rows and alignment."""
+    x, xs, w, ws = operands(M, V, K, xf, wf)
+    args = dict(x_fmt=xf, w_fmt=wf, dtype=torch.float32)
+    xs[M - 1] -= 90
+    ws[V // 2] -= 80
+    if M > 1:
+        xs[0, 0] = 255
+    ref = vce.mx_logits(x, xs, w, ws, **args)
+    assert torch.isnan(ref[0]).all() == (M > 1) and not torch.isnan(ref[1:]).any()
+    for ld, off in ((V, 1), (V + 3, 0), (V + 11, 5), ((V + 7) // 4 * 4, 0)):
+        buf = torch.full(((M + 1) * ld + 32,), 7.0, device="cuda")
+        out = buf.as_strided((M, V), (ld, 1), off)
+        vce.mx_logits(x, xs, w, ws, x_fmt=xf, w_fmt=wf, out=out)
+        assert same_bits(out.contiguous(), ref)
+        mask = torch.ones_like(buf, dtype=torch.bool)
+        mask.as_strided((M, V), (ld, 1), off).fill_(False)
+        assert (buf[mask] == 7).all()
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_graph(M):
+    """A captured call finds the far rows of what it is replayed with."""
+    V, K = 1500, 544
+    x, xs, w, ws = operands(M, V, K, "e4m3", "e2m1")
+    kw = dict(dtype=torch.float32)
+    clean = xs.clone()
+    vce.mx_logits(x, xs, w, ws, **kw)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = vce.mx_logits(x, xs, w, ws, **kw)
+    base = vce.mx_logits(x, clean, w, ws, **kw)
+    for r in range(5):
+        xs.copy_(clean)
+        if r % 2:
+            xs[r, r] = 255
+            xs[0] -= 90
+        g.replay()
+        e = vce.mx_logits(x, xs, w, ws, **kw)
+        torch.cuda.synchronize()
+        assert same_bits(out, e)
+        rest = [i for i in range(M) if not (r % 2 and i in (0, r))]
+        assert same_bits(out[rest], base[rest])
