@@ -629,6 +629,72 @@ int ce_sample(const void* logits, int dtype, int64_t d0, int64_t d1, int64_t V, 
               const float* min_p, const float* u, int64_t* token, float* logprob,
               void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * adamw_step: one AdamW step over many tensors at once, with FP32 or 8-bit states.
+ * Per element, in FP32, g' = grad_scale * g:
+ *     m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2
+ *     p = (1 - lr weight_decay) p
+ *         - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ *
+ *  tensors  count entries in HOST memory, read before the call returns: a parameter
+ *           and its gradient, n contiguous elements each, FP32 or BF16 (each of its
+ *           own type), aligned to their element, and where its states begin:
+ *           element `offset` of the flat arrays below, a multiple of 128; the
+ *           tensors' states [offset, offset + n rounded up to 128) do not overlap and lie
+ *           below `total`.  Places between n and that end are kept zero.  n = 0 is
+ *           skipped.  16-byte aligned parameters and gradients take the wide loads.
+ *  bits     32: m and v are FP32 (total).  8: m and the square root of v are
+ *           microscaled E4M3 (mx_quantize's format over the flat array):
+ *           m, v total bytes, m_scales, v_scales total / 32 bytes.  All of them
+ *           zero before the first step.  8-bit states are rounded up or down at random
+ *           (to nearest, an average that moves by less than half a place would
+ *           stand still): with t the part of a value below its last place, up where
+ *           65536 t > r, r 16 bits of a hash of (seed, step, place), the low half for m, the
+ *           high half for v; a root other than zero does not become zero.  The same
+ *           call gives the same bits.  The parameter's own step takes m and v before they are
+ *           rounded.  A block of 32 with a NaN or an infinity becomes NaN.
+ *  master   FP32 (total) or NULL: the parameters' values that are stepped, p then
+ *           receiving them rounded.  Without it BF16 parameters are read, stepped in FP32
+ *           and rounded to nearest, so steps below half a place are lost.
+ *  total    elements of the flat arrays, a multiple of 128.  m, v and master 16-byte
+ *           aligned.
+ *  lr, weight_decay, eps >= 0; 0 <= beta1, beta2 < 1; step >= 1, all finite.
+ *  lr_device, step_device  one FP32, one int64 on the device, or NULL: taken in the
+ *           place of lr and step when the kernels run (a captured call follows them).
+ *  grad_scale  one FP32 on the device, or NULL for 1: grad_norm's scale, or the
+ *           inverse of a loss scale.  Where it is not finite nothing is changed.
+ *  Outputs must not overlap one another or an input (VCE_EALIAS).
+ *
+ * grad_norm: norm = sqrt(sum of all squares) over the tensors, in FP64 in a fixed order, and
+ *  scale = max_norm / norm where norm exceeds max_norm, else 1 (NaN where norm is not
+ *  finite): adamw_step's grad_scale.
+ *  tensors  count entries in HOST memory; FP32 or BF16, contiguous.
+ *  max_norm > 0, infinite for none.  norm, scale: one FP32 each, either may be NULL.
+ *  workspace  grad_norm_workspace_size(sum of n, count) bytes, 8-byte aligned; its
+ *           contents need not survive.
+ */
+typedef struct vce_adamw_tensor {
+  void* param;
+  const void* grad;
+  int64_t n, offset;
+  int32_t param_dtype, grad_dtype;
+} vce_adamw_tensor;
+
+typedef struct vce_grad_tensor {
+  const void* grad;
+  int64_t n;
+  int64_t dtype;
+} vce_grad_tensor;
+
+int adamw_step(const vce_adamw_tensor* tensors, int64_t count, int bits, void* m, void* v,
+               uint8_t* m_scales, uint8_t* v_scales, float* master, int64_t total, double lr,
+               double beta1, double beta2, double eps, double weight_decay, int64_t step,
+               const float* lr_device, const int64_t* step_device, const float* grad_scale,
+               uint64_t seed, void* stream);
+size_t grad_norm_workspace_size(int64_t total, int64_t count);
+int grad_norm(const vce_grad_tensor* tensors, int64_t count, double max_norm, float* norm,
+              float* scale, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

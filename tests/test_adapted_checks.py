@@ -1,0 +1,158 @@
+"""Refusals of the operators of an adapted head, by the C-ABI (fake addresses, nothing is
+launched) and by the binding (CPU tensors)."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import vocabulary_cross_entropy_amd as vce
+from vocabulary_cross_entropy_amd import binding
+
+A = 0x7F0000000000  # a fake, 256-byte aligned device address (never touched)
+G = 1 << 33         # apart enough for every size below
+NAN, INF = float("nan"), float("inf")
+GPU_ONLY = (RuntimeError, "GPU only")
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(binding.LIB_PATH):
+        from vocabulary_cross_entropy_amd import build
+        build.build()
+    return binding.lib()
+
+
+# ---- the optimizer step ----------------------------------------------------------
+
+def entry(p=A, g=A + G, n=1000, off=0, pd=1, gd=0):
+    return (p, g, n, off, pd | gd << 32)
+
+
+def adamw(L, entries=(entry(),), **kw):
+    a = dict(count=None, bits=8, m=A + 2 * G, v=A + 3 * G, ms=A + 4 * G, vs=A + 5 * G,
+             master=A + 6 * G, total=1024, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.01, step=1,
+             lrd=A + 7 * G, std=A + 7 * G + 8, gs=A + 7 * G + 16)
+    a.update(kw)
+    flat = [x for e in entries for x in e]
+    tab = (ctypes.c_int64 * len(flat))(*flat) if entries else None
+    return L.adamw_step(tab, len(entries) if a["count"] is None else a["count"], a["bits"],
+                        a["m"], a["v"], a["ms"], a["vs"], a["master"], a["total"], a["lr"],
+                        a["b1"], a["b2"], a["eps"], a["wd"], a["step"], a["lrd"], a["std"],
+                        a["gs"], 7, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(count=-1), 1), (dict(total=-128), 1), (dict(total=1000), 1), (dict(bits=16), 1),
+    (dict(bits=4), 1), (dict(total=1 << 41), 7), (dict(lr=-1.0), 1), (dict(lr=NAN), 1),
+    (dict(lr=INF), 1), (dict(eps=-1e-9), 1), (dict(eps=NAN), 1), (dict(eps=INF), 1),
+    (dict(wd=-0.1), 1), (dict(wd=NAN), 1), (dict(wd=INF), 1), (dict(b1=1.0), 1),
+    (dict(b1=-0.1), 1), (dict(b1=NAN), 1), (dict(b2=1.0), 1), (dict(b2=NAN), 1),
+    (dict(step=0), 1), (dict(step=-3), 1), (dict(m=None), 1), (dict(v=None), 1),
+    (dict(ms=None), 1), (dict(vs=None), 1), (dict(total=0), 1), (dict(total=896), 1),
+    (dict(m=A + 2 * G + 8), 3), (dict(v=A + 3 * G + 4), 3), (dict(master=A + 6 * G + 8), 3),
+    (dict(lrd=A + 7 * G + 2), 3), (dict(std=A + 7 * G + 4), 3), (dict(gs=A + 7 * G + 1), 3),
+    (dict(m=A), 4), (dict(v=A + G), 4), (dict(m=A + 3 * G), 4), (dict(ms=A + 5 * G), 4),
+    (dict(vs=A + 2 * G + 1023), 4), (dict(master=A), 4), (dict(lrd=A + 2 * G), 4),
+    (dict(std=A + 6 * G + 4088), 4), (dict(gs=A + 1000), 4), (dict(lrd=A + 3 * G + 1020), 4),
+])
+def test_adamw_rejects(L, kw, code):
+    assert adamw(L, **kw) == code
+
+
+@pytest.mark.parametrize("e,code", [
+    ((entry(pd=2),), 2), ((entry(gd=-1),), 2), ((entry(n=-1),), 1), ((entry(p=0),), 1),
+    ((entry(g=0),), 1), ((entry(off=-128),), 1), ((entry(off=64),), 1), ((entry(off=128),), 1),
+    ((entry(n=1025),), 1), ((entry(n=1 << 62),), 1), ((entry(p=A + 1),), 3),
+    ((entry(g=A + G + 2),), 3), ((entry(g=A),), 4), ((entry(g=A + 1996),), 4),
+    ((entry(n=100), entry(n=100)), 4),                              # one tensor twice
+    ((entry(n=100), entry(p=A + 200, g=A + 2 * G - 400, n=10, off=0)), 4),   # one place
+    ((entry(n=129), entry(p=A + 4096, g=A + G + 4096, n=1, off=128)), 4),
+    ((entry(n=100), entry(p=A + 198, g=A + G + 400, n=1, off=128)), 4),
+    ((entry(n=100), entry(p=A + 200, g=A + 100, n=1, off=128)), 4),  # a gradient in a parameter
+])
+def test_adamw_rejects_tensors(L, e, code):
+    assert adamw(L, e) == code
+
+
+def test_adamw_nothing_to_do(L):
+    assert adamw(L, (), total=0, m=None, v=None, ms=None, vs=None) == 0
+    assert adamw(L, (entry(0, 0, 0),), total=0) == 0
+    assert adamw(L, (), count=1, total=0) == 1 and adamw(L, (), count=1) == 1
+    assert adamw(L, count=(1 << 20) + 1) == 7
+
+
+def norm(L, entries=((A, 1000, 1),), **kw):
+    a = dict(count=len(entries), most=1.0, norm=A + G, scale=A + G + 4, ws=A + 2 * G, n=1 << 16)
+    a.update(kw)
+    flat = [x for e in entries for x in e]
+    tab = (ctypes.c_int64 * len(flat))(*flat) if entries else None
+    return L.grad_norm(tab, a["count"], a["most"], a["norm"], a["scale"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(count=-1), 1), (dict(most=0.0), 1), (dict(most=-1.0), 1), (dict(most=NAN), 1),
+    (dict(ws=None), 1), (dict(n=7), 5), (dict(norm=A + G + 2), 3), (dict(scale=A + 2), 3),
+    (dict(ws=A + 2 * G + 4), 3), (dict(scale=A + G), 4), (dict(norm=A + 1996), 4),
+    (dict(ws=A), 4), (dict(norm=A + 2 * G), 4), (dict(entries=((A, -1, 0),)), 1),
+    (dict(entries=((0, 5, 0),)), 1), (dict(entries=((A, 5, 2),)), 2),
+    (dict(entries=((A + 1, 5, 1),)), 3), (dict(entries=((A, 1 << 41, 0),)), 7),
+    (dict(entries=(), count=1), 1), (dict(norm=None, scale=None), 0),
+    (dict(count=(1 << 20) + 1), 7),
+])
+def test_grad_norm_rejects(L, kw, code):
+    assert norm(L, **kw) == code
+
+
+def test_grad_norm_workspace(L):
+    f = L.grad_norm_workspace_size
+    assert f(-1, 1) == 0 and f(1, -1) == 0 and f(1 << 41, 1) == 0 and f(1, 1 << 21) == 0
+    assert f(0, 0) >= 8 and f(1 << 20, 3) >= 64 * 8
+
+
+P = [torch.zeros(40), torch.zeros((3, 5), dtype=torch.bfloat16)]
+BAD_STEP = [
+    (dict(params=P[:1]), ValueError, "holds 2"),
+    (dict(grads=P[:1]), ValueError, "holds 2"),
+    (dict(params=[P[0].double(), P[1]]), TypeError, "float32 or bfloat16"),
+    (dict(grads=[P[0].half(), P[1]]), TypeError, "float32 or bfloat16"),
+    (dict(params=[torch.zeros(41), P[1]]), ValueError, "40 elements"),
+    (dict(grads=[torch.zeros((8, 5)), P[1]]), ValueError, "one shape"),
+    (dict(grads=[P[0], torch.zeros((5, 3)).t()]), ValueError, "contiguous"),
+    (dict(lr=torch.zeros(1, dtype=torch.float64)), TypeError, "lr must be"),
+    (dict(lr=torch.zeros(2)), ValueError, "lr must hold 1"),
+    (dict(step=torch.zeros(1)), TypeError, "step must be"),
+    (dict(grad_scale=torch.zeros(3)), ValueError, "grad_scale must hold 1"),
+    (dict(), *GPU_ONLY),
+]
+
+
+@pytest.mark.parametrize("kw,err,text", BAD_STEP)
+def test_binding_adamw(kw, err, text):
+    a = dict(params=P, grads=P, lr=1e-3, step=1)
+    a.update(kw)
+    with pytest.raises(err, match=text):
+        vce.adamw_step(a.pop("params"), a.pop("grads"), vce.adamw_state(P), a.pop("lr"),
+                       a.pop("step"), **a)
+
+
+def test_binding_adamw_state():
+    st = vce.adamw_state(P, 8, True)
+    assert st.offsets == [0, 128] and st.sizes == [40, 15] and st.total == 256
+    assert st.m.dtype == torch.uint8 and st.m_scales.numel() == 8 and st.master.numel() == 256
+    for bad, err in (([], ValueError), ([torch.zeros(3).double()], TypeError),
+                     ([torch.zeros((4, 4)).t()[:2]], ValueError)):
+        with pytest.raises(err):
+            vce.adamw_state(bad)
+    with pytest.raises(ValueError):
+        vce.adamw_state(P, 16)
+
+
+def test_binding_grad_norm():
+    for grads, kw, err in (([], {}, ValueError), ([None], {}, ValueError),
+                           ([P[0].double()], {}, TypeError), ([torch.zeros((4, 6)).t()], {},
+                                                              ValueError),
+                           (P, dict(out=(torch.zeros(1), None)), ValueError),
+                           (P, dict(workspace=torch.zeros(9)), TypeError), (P, {}, RuntimeError)):
+        with pytest.raises(err):
+            vce.grad_norm(grads, **kw)

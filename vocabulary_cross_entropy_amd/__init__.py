@@ -3,9 +3,10 @@
 The computation lives in ``libvce.so`` (HIP kernels behind the C-ABI declared
 in ``include/vce.h``); ``binding`` marshals torch tensors into it.
 """
-from .binding import (ce_backward, ce_backward_shard, ce_forward,  # noqa: F401
+from .binding import (AdamWState, adamw_state, adamw_step, ce_backward, ce_backward_shard, ce_forward,  # noqa: F401
                       ce_sample, ce_sample_workspace, ce_sample_workspace_size,
                       ce_forward_backward, ce_forward_shard, ce_merge_shards, gemm_bf16,
+                      grad_norm,
                       lce_backward, lce_backward_f32,
                       lce_backward_shard, lce_forward, lce_forward_f32, lce_forward_noalloc,
                       lce_forward_shard,

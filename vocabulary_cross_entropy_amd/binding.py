@@ -23,6 +23,7 @@ STATUS = {0: "VCE_OK", 1: "VCE_EINVAL", 2: "VCE_EDTYPE", 3: "VCE_EALIGN", 4: "VC
 
 # (name, restype, argtypes) for every symbol include/vce.h declares.
 _I64, _I32, _F32, _VP, _SZ = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+_F64, _U64 = ctypes.c_double, ctypes.c_uint64
 SIGNATURES = {
     "vce_strerror": (ctypes.c_char_p, [_I32]),
     "ce_forward": (_I32, [_VP, _I32, _I64, _I64, _I64, _I64, _I64, _VP, _I64, _I64, _F32, _I32, _I64,
@@ -79,6 +80,10 @@ SIGNATURES = {
     "ce_sample_workspace_size": (_SZ, [_I64, _I64]),
     "ce_sample": (_I32, [_VP, _I32, _I64, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP,
                          _VP, _VP, _SZ, _VP]),
+    "adamw_step": (_I32, [_VP, _I64, _I32, _VP, _VP, _VP, _VP, _VP, _I64, _F64, _F64, _F64, _F64,
+                          _F64, _I64, _VP, _VP, _VP, _U64, _VP]),
+    "grad_norm_workspace_size": (_SZ, [_I64, _I64]),
+    "grad_norm": (_I32, [_VP, _I64, _F64, _VP, _VP, _VP, _SZ, _VP]),
 }
 
 _lib = None
@@ -1064,3 +1069,139 @@ def ce_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor |
             _at(min_p), _at(u), _at(tok), _at(lp), _at(ws), ws.numel(), s))
         return (tok, lp) if with_logprob else tok
     return _on_stream(logits, stream, call)
+
+
+class AdamWState:
+    """Moments of a list of parameters in flat arrays: parameter i's begin at ``offsets[i]``, a
+    multiple of 128.  ``bits`` 32: ``m`` and ``v`` FP32.  8: ``m`` and the root of v as E4M3
+    bytes with a scale byte per 32 in ``m_scales`` and ``v_scales`` (``mx_dequantize`` reads them
+    as rows of any multiple of 32).  ``master``: FP32 copies of the parameters in the same places, or None."""
+
+    def __init__(self, params, bits: int = 32, master: bool = False):
+        if bits not in (8, 32):
+            raise ValueError(f"bits must be 8 or 32, got {bits}")
+        params = list(params)
+        if not params:
+            raise ValueError("no parameters")
+        dev = params[0].device
+        self.bits, self.sizes, self.offsets, at = bits, [], [], 0
+        for i, p in enumerate(params):
+            _elem_dtype(p, f"params[{i}]")
+            if p.device != dev:
+                raise ValueError(f"params[{i}] must be on {dev}, got {p.device}")
+            if not p.is_contiguous():
+                raise ValueError(f"params[{i}] must be contiguous")
+            self.sizes.append(p.numel())
+            self.offsets.append(at)
+            at += (p.numel() + 127) // 128 * 128
+        self.total = at
+        td = torch.float32 if bits == 32 else torch.uint8
+        self.m = torch.zeros(at, dtype=td, device=dev)
+        self.v = torch.zeros(at, dtype=td, device=dev)
+        self.m_scales = self.v_scales = self.master = None
+        if bits == 8:
+            self.m_scales = torch.zeros(at // 32, dtype=torch.uint8, device=dev)
+            self.v_scales = torch.zeros(at // 32, dtype=torch.uint8, device=dev)
+        if master:
+            self.master = torch.zeros(at, dtype=torch.float32, device=dev)
+            for p, n, o in zip(params, self.sizes, self.offsets):
+                self.master[o:o + n].copy_(p.detach().reshape(-1))
+
+
+def adamw_state(params, bits: int = 32, master: bool = False) -> AdamWState:
+    """Zero moments for ``adamw_step`` over these parameters, in FP32 or 8 bits; ``master``
+    keeps FP32 copies of the parameters that are stepped in their place."""
+    return AdamWState(params, bits, master)
+
+
+def _scalar(t, name: str, dtype, like: torch.Tensor):
+    if t is not None:
+        _check_buf(t, name, 1, dtype, like=like)
+    return _at(t)
+
+
+def adamw_step(params, grads, state: AdamWState, lr, step, *, betas=(0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 0.01,
+               grad_scale: torch.Tensor | None = None, seed: int = 0, stream=None) -> None:
+    """One AdamW step in place over the parameters that ``state`` was made for, in one launch
+    per 64 of them.  A gradient may be None: that parameter and its moments stay.  lr and
+    step (1 for the first) are numbers, or tensors of one element on the device (FP32, int64), read
+    when the kernels run.  grad_scale: ``grad_norm``'s scale; not finite, nothing changes.
+    seed: of the random rounding of 8-bit states (the step and place enter it too)."""
+    sizes = state.sizes
+    if len(params) != len(sizes) or len(grads) != len(sizes):
+        raise ValueError(f"state holds {len(sizes)} parameters, got {len(params)} and "
+                         f"{len(grads)} gradients")
+    ref = state.m
+    dev, f32, bf16 = ref.device, torch.float32, torch.bfloat16
+    entries = []
+    for p, g, n, off in zip(params, grads, sizes, state.offsets):
+        if g is None:
+            continue
+        pd, gd = p.dtype, g.dtype
+        if not ((pd is f32 or pd is bf16) and (gd is f32 or gd is bf16)):
+            raise TypeError(f"parameters and gradients must be float32 or bfloat16, got {pd}, {gd}")
+        if p.numel() != n or g.shape != p.shape:
+            raise ValueError(f"a parameter of {n} elements and its gradient must have one "
+                             f"shape, got {tuple(p.shape)} and {tuple(g.shape)}")
+        if p.device != dev or g.device != dev:
+            raise ValueError(f"parameters and gradients must be on {dev}, got {p.device}, "
+                             f"{g.device}")
+        if not (p.is_contiguous() and g.is_contiguous()):
+            raise ValueError("parameters and gradients must be contiguous")
+        entries += (p.data_ptr(), g.data_ptr(), n, off,
+                    (pd is bf16) * DTYPE_BF16 | (gd is bf16) * DTYPE_BF16 << 32)
+    lr_t = lr if isinstance(lr, torch.Tensor) else None
+    step_t = step if isinstance(step, torch.Tensor) else None
+    scalars = (_scalar(lr_t, "lr", f32, ref), _scalar(step_t, "step", torch.int64, ref),
+               _scalar(grad_scale, "grad_scale", f32, ref))
+    host = (0.0 if lr_t is not None else float(lr), float(betas[0]), float(betas[1]), float(eps),
+            float(weight_decay), 1 if step_t is not None else int(step))
+    count = len(entries) // 5
+    # the C structs' fields in order: two pointers, two int64, two int32
+    table = (ctypes.c_int64 * len(entries))(*entries)
+
+    def call(s):
+        _check("adamw_step", lib().adamw_step(
+            table, count, state.bits, _at(state.m), _at(state.v), _at(state.m_scales),
+            _at(state.v_scales), _at(state.master), state.total, *host, *scalars,
+            seed & 0xFFFFFFFFFFFFFFFF, s))
+    _on_stream(ref, stream, call)
+
+
+def grad_norm(grads, max_norm: float = float("inf"), *, workspace: torch.Tensor | None = None,
+              stream=None, out=None):
+    """(norm, scale) of a list of gradients (FP32 or BF16, None entries left out): the root of
+    the sum of all squares, and max_norm / norm where that is below 1, else 1 (NaN where norm is
+    not finite), as FP32 scalars on the device.  ``out`` gives both."""
+    ref, entries, total = None, [], 0
+    for g in grads:
+        if g is None:
+            continue
+        if ref is None:
+            ref = g
+        if g.device != ref.device:
+            raise ValueError(f"gradients must be on {ref.device}, got {g.device}")
+        if not g.is_contiguous():
+            raise ValueError("gradients must be contiguous")
+        n = g.numel()
+        entries += (g.data_ptr(), n, _elem_dtype(g, "a gradient"))
+        total += n
+    if ref is None:
+        raise ValueError("no gradients")
+    outs = (None, None) if out is None else out
+    _check_out(outs[0], "norm", (), torch.float32, ref)
+    _check_out(outs[1], "scale", (), torch.float32, ref)
+    if workspace is not None:
+        _check_buf(workspace, "workspace", workspace.numel(), torch.uint8, like=ref)
+    count = len(entries) // 3
+    table = (ctypes.c_int64 * len(entries))(*entries)
+
+    def call(s):
+        nrm, sc = (ref.new_empty((), dtype=torch.float32) if t is None else t for t in outs)
+        need = int(lib().grad_norm_workspace_size(total, count))
+        ws = ref.new_empty(need, dtype=torch.uint8) if workspace is None else workspace
+        _check("grad_norm", lib().grad_norm(table, count, max_norm, _at(nrm), _at(sc), _at(ws),
+                                            ws.numel(), s))
+        return nrm, sc
+    return _on_stream(ref, stream, call)

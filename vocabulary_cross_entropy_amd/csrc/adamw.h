@@ -1,0 +1,63 @@
+// Parameter blocks and launchers of the optimizer step and the gradients' norm.  Not part of
+// the public interface.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+struct vce_adamw_tensor;
+struct vce_grad_tensor;
+
+namespace vce {
+
+constexpr int kAdamTensors = 64;  // of a launch: the table stays below 4 KB of arguments
+
+struct AdamTensor {
+  void* p;
+  const void* g;
+  int64_t n, offset;
+  uint32_t types;
+};
+
+struct AdamTable {
+  int n;
+  uint32_t first[kAdamTensors];  // first chunk of each tensor
+  AdamTensor t[kAdamTensors];
+};
+
+struct AdamParams {
+  void* m;
+  void* v;
+  uint8_t* m_scales;  // 8-bit states
+  uint8_t* v_scales;
+  float* master;      // optional
+  float b1, c1, b2, c2, eps;
+  float decay, a, rs;  // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  double lr, wd, ln_b1, ln_b2;
+  int64_t step;
+  const float* lr_device;      // in place of lr and step
+  const int64_t* step_device;
+  const float* grad_scale;     // optional
+  uint64_t seed;
+  uint32_t seed_key, key;  // of the random bits (set by the launcher)
+};
+
+struct NormTensor {
+  const void* g;
+  int64_t n;
+  uint32_t types;
+};
+
+struct NormTable {
+  int n;
+  uint32_t first[kAdamTensors];
+  NormTensor t[kAdamTensors];
+};
+
+int64_t norm_chunks(int64_t n);  // partial sums of a tensor of n elements
+hipError_t launch_adamw(AdamParams p, const vce_adamw_tensor* tensors, int64_t count, int bits,
+                        hipStream_t stream);
+hipError_t launch_grad_norm(const vce_grad_tensor* tensors, int64_t count, double max_norm,
+                            float* norm, float* scale, double* partial, hipStream_t stream);
+
+}  // namespace vce

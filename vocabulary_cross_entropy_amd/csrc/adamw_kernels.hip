@@ -1,0 +1,474 @@
+// The AdamW step over many tensors in one launch, and the norm that clips it.
+//   g' = s g,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+//   p  = (1 - lr wd) p - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+//
+// The tensors of a launch come as a table in the kernel's arguments, so nothing is copied
+// to the device and a captured launch keeps its own.  A workgroup takes one chunk of one
+// tensor, found by one comparison per lane with the tensors' first chunks.
+//
+// 8-bit states: m and sqrt(v) as E4M3 with a power-of-two scale per 32 (mx_device.h).  The
+// root halves the range that v needs.  Rounding to nearest would stop the averages: with
+// b2 = 0.999 a step changes v by a thousandth, and a value of three mantissa bits would
+// stay where it is.  So a value goes up or down by 16 random bits, hashed from the
+// seed, the step and the place: its mean is the unrounded value, and the same call
+// gives the same bits.  A root other than zero never becomes zero, so a small one cannot
+// make its step large.
+//
+// The arithmetic of m, v and the rounding is written without fused products, so
+// that it is the same wherever the formula is computed in FP32.
+#include "adamw.h"
+#include "mx_device.h"
+#include "vce.h"
+
+namespace vce {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 4096;       // elements of a tensor per workgroup of the step
+constexpr int kNormChunk = 16384;  // and of the norm
+
+template <int D>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  if constexpr (D == 0)
+    return static_cast<const float*>(p)[i];
+  else
+    return from_bf16(static_cast<const uint16_t*>(p)[i]);
+}
+
+// Elements e .. e + VE - 1 of n as FP32, 0 past the end.  WIDE: the array allows vectors.
+template <int D, int VE, bool WIDE>
+__device__ __forceinline__ void load(const void* p, int64_t e, int64_t n, float* v) {
+  if (WIDE && e + VE <= n) {
+    if constexpr (D == 0) {
+#pragma unroll
+      for (int h = 0; h < VE; h += 4) {
+        const f32x4_t t = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + e + h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[h + j] = t[j];
+      }
+    } else if constexpr (VE == 8) {
+      const u32x4_t t = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(t[j]);
+        v[2 * j + 1] = bf16_hi(t[j]);
+      }
+    } else {
+      const u32x2_t t = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(p) + e);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[2 * j] = bf16_lo(t[j]);
+        v[2 * j + 1] = bf16_hi(t[j]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) v[j] = e + j < n ? load1<D>(p, e + j) : 0.0f;
+  }
+}
+
+template <int D, int VE, bool WIDE>
+__device__ __forceinline__ void store(void* p, int64_t e, int64_t n, const float* v) {
+  if (WIDE && e + VE <= n) {
+    if constexpr (D == 0) {
+#pragma unroll
+      for (int h = 0; h < VE; h += 4)
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + e + h) =
+            f32x4_t{v[h], v[h + 1], v[h + 2], v[h + 3]};
+    } else {
+#pragma unroll
+      for (int h = 0; h < VE; h += 4)
+        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p) + e + h) =
+            u32x2_t{pack_bf16x2(v[h], v[h + 1]), pack_bf16x2(v[h + 2], v[h + 3])};
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      if (e + j < n) {
+        if constexpr (D == 0)
+          static_cast<float*>(p)[e + j] = v[j];
+        else
+          static_cast<uint16_t*>(p)[e + j] = to_bf16(v[j]);
+      }
+    }
+  }
+}
+
+// The table's tensor that holds chunk c: the number of first chunks at or below c, less one.
+__device__ __forceinline__ int tensor_of(const uint32_t* first, int n, uint32_t c) {
+  const int lane = threadIdx.x & 63;
+  int at = -1;
+#pragma unroll
+  for (int b = 0; b < kAdamTensors; b += 64)
+    at += __builtin_popcountll(__ballot(b + lane < n && first[b + lane] <= c));
+  return at;
+}
+
+// 32 bits to 32 bits, one to one (multipliers: the fractions of the golden ratio and of
+// the square root of 2).
+__host__ __device__ inline uint32_t mix(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x9E3779B9u;
+  x = (x ^ (x >> 15)) * 0x6A09E667u;
+  return x ^ (x >> 16);
+}
+
+// E4M3 code of |x| <= 448, up or down by 16 random bits: up where the part below the
+// code's last place, in 65536ths of it, exceeds r.  (x in FP32's bits: exponent and three
+// mantissa bits are the code, the 20 bits below are that part.)
+__device__ __forceinline__ uint32_t code_of(float x, uint32_t r) {
+  const uint32_t a = abs_bits(x);
+  const int c = (int)((a + (0xfffffu - (r << 4))) >> 20) - (120 << 3);
+  return (uint32_t)(c < 0 ? 0 : c);  // 0 for x = 0; below 2^-6 see code_small
+}
+// The same below the least normal value, 2^-6: steps of 2^-9.
+__device__ __forceinline__ uint32_t code_small(float x, uint32_t r) {
+  const float t = fabsf(x) * 512.0f;
+  const float k = floorf(t);
+  return (uint32_t)(k + ((t - k) * 65536.0f > (float)r ? 1.0f : 0.0f));
+}
+__device__ __forceinline__ bool is_small(float x) { return abs_bits(x) - 1u < 0x3c7fffffu; }
+
+// Eight values of a block of 32 that four lanes hold: their codes and the block's scale byte.
+template <bool KEEP>
+__device__ __forceinline__ u32x2_t round_block(const float* v, const uint32_t* r, int shift,
+                                               uint32_t& byte) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = abs_bits(v[j]);
+    a = a > b ? a : b;
+  }
+  // lanes 4 q .. 4 q + 3: neighbours, then pairs
+  uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0xb1, 0xf, 0xf, false);
+  a = a > b ? a : b;
+  b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0x4e, 0xf, 0xf, false);
+  a = a > b ? a : b;
+  byte = mx_scale_byte<kMxE4M3>(a);
+  if (byte == 255u) return u32x2_t{0, 0};
+  const float inv = __uint_as_float((254u - byte) << 23);
+  uint32_t code[8];
+  bool small = false;
+  float x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    x[j] = v[j] * inv;  // exact
+    small |= is_small(x[j]);
+    code[j] = code_of(x[j], (r[j] >> shift) & 0xffffu);
+  }
+  if (small) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (is_small(x[j])) {
+        code[j] = code_small(x[j], (r[j] >> shift) & 0xffffu);
+        if (KEEP && code[j] == 0) code[j] = 1;
+      }
+  }
+  u32x2_t w = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t c = code[j] | (KEEP ? 0u : (__float_as_uint(x[j]) >> 31) << 7);
+    w[j / 4] |= c << (8 * (j % 4));
+  }
+  return w;
+}
+
+// Eight E4M3 codes under a scale byte as FP32 (a code's bits in FP32's fields stand for the
+// value times 2^-120; exact for denormal codes too).
+__device__ __forceinline__ void decode8(const u32x2_t& q, uint32_t byte, float* v) {
+  const float s = byte == 255u ? __builtin_nanf("") : mx_scale_value(byte);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t c = q[j / 4] >> (8 * (j % 4));
+    v[j] = __uint_as_float(((c & 128u) << 24) | ((c & 127u) << 20)) * 0x1p120f * s;
+  }
+}
+
+struct Coef {
+  float scale, decay, a, rs;
+};
+
+// One chunk of one tensor.
+template <int PD, int GD, int BITS, bool MASTER, bool WIDE>
+__device__ __forceinline__ void chunk(const AdamParams& p, const Coef& k, const AdamTensor& t,
+                                      int64_t e0) {
+#pragma clang fp contract(off)
+  constexpr int VE = BITS == 8 ? 8 : 4;
+  constexpr int U = kChunk / kThreads / VE;  // places per thread, their loads in flight together
+  float g[U][VE], w[U][VE], m[U][VE], v[U][VE];
+  u32x2_t mq[U], vq[U];
+  uint32_t mb[U], vb[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t e = e0 + ((int64_t)u * kThreads + threadIdx.x) * VE;
+    if constexpr (BITS == 8) {
+      mq[u] = vq[u] = u32x2_t{0, 0};
+      mb[u] = vb[u] = 0;
+    }
+    if (e >= t.n) continue;
+    const int64_t s = t.offset + e;
+    if constexpr (BITS == 8) {
+      mq[u] = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(p.m) + s);
+      vq[u] = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(p.v) + s);
+      mb[u] = p.m_scales[s / kMxBlock];
+      vb[u] = p.v_scales[s / kMxBlock];
+    } else {
+      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.m) + s);
+      const f32x4_t b = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.v) + s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        m[u][j] = a[j];
+        v[u][j] = b[j];
+      }
+    }
+    load<GD, VE, WIDE>(t.g, e, t.n, g[u]);
+    if constexpr (MASTER)
+      load<0, VE, true>(p.master + t.offset, e, (t.n + 127) / 128 * 128, w[u]);
+    else
+      load<PD, VE, WIDE>(t.p, e, t.n, w[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t e = e0 + ((int64_t)u * kThreads + threadIdx.x) * VE;
+    const int64_t s = t.offset + e;
+    // in 8 bits every lane goes on: the lanes of a block compare their values
+    const bool on = e < t.n;
+    if (BITS != 8 && !on) continue;
+    if constexpr (BITS == 8) {
+      decode8(mq[u], mb[u], m[u]);
+      decode8(vq[u], vb[u], v[u]);
+    }
+    float root[VE];
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      if constexpr (BITS == 8) v[u][j] = v[u][j] * v[u][j];
+      const float gs = g[u][j] * k.scale;
+      m[u][j] = m[u][j] * p.b1 + gs * p.c1;
+      v[u][j] = v[u][j] * p.b2 + (gs * gs) * p.c2;
+      root[j] = __builtin_sqrtf(v[u][j]);
+      const float d = root[j] * k.rs + p.eps;
+      w[u][j] = w[u][j] * k.decay - k.a * m[u][j] * __builtin_amdgcn_rcpf(d);
+      if (e + j >= t.n) {  // places behind the tensor stay zero
+        m[u][j] = v[u][j] = root[j] = 0.0f;
+        if (MASTER) w[u][j] = 0.0f;
+      }
+    }
+    if (on) store<PD, VE, WIDE>(t.p, e, t.n, w[u]);
+    if (MASTER && on)
+      store<0, VE, true>(p.master + t.offset, e, (t.n + 127) / 128 * 128, w[u]);
+    if constexpr (BITS == 8) {
+      uint32_t r[8];
+      const uint32_t key = mix(p.key + (uint32_t)((uint64_t)s >> 32));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = mix(((uint32_t)s + j) ^ key);
+      uint32_t mbyte, vbyte;
+      const u32x2_t mw = round_block<false>(m[u], r, 0, mbyte);
+      const u32x2_t vw = round_block<true>(root, r, 16, vbyte);
+      if (!on) continue;
+      *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.m) + s) = mw;
+      *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.v) + s) = vw;
+      if (s % kMxBlock == 0) {
+        p.m_scales[s / kMxBlock] = (uint8_t)mbyte;
+        p.v_scales[s / kMxBlock] = (uint8_t)vbyte;
+      }
+    } else {
+      *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.m) + s) =
+          f32x4_t{m[u][0], m[u][1], m[u][2], m[u][3]};
+      *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.v) + s) =
+          f32x4_t{v[u][0], v[u][1], v[u][2], v[u][3]};
+    }
+  }
+}
+
+template <int BITS, bool MASTER>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamParams p, AdamTable tab) {
+  Coef k{1.0f, p.decay, p.a, p.rs};
+  if (p.grad_scale) {
+    k.scale = *p.grad_scale;
+    if (!(fabsf(k.scale) < __builtin_huge_valf())) return;  // nothing changes
+  }
+  if (p.lr_device || p.step_device) {
+    const double lr = p.lr_device ? (double)*p.lr_device : p.lr;
+    const double t = (double)(p.step_device ? *p.step_device : p.step);
+    const double bc1 = -expm1(t * p.ln_b1), bc2 = -expm1(t * p.ln_b2);
+    k.decay = (float)(1.0 - lr * p.wd);
+    k.a = (float)(lr / bc1);
+    k.rs = (float)(1.0 / sqrt(bc2));
+    if (p.step_device) p.key = mix(p.seed_key + (uint32_t)*p.step_device);
+  }
+  const int i = tensor_of(tab.first, tab.n, blockIdx.x);
+  const AdamTensor t = tab.t[i];
+  const int64_t e0 = (int64_t)(blockIdx.x - tab.first[i]) * kChunk;
+  const uint32_t ty = t.types;  // bits 0, 1: types of p and g, bit 2: vectors allowed
+  switch (ty & 7u) {
+    case 4: return chunk<0, 0, BITS, MASTER, true>(p, k, t, e0);
+    case 5: return chunk<1, 0, BITS, MASTER, true>(p, k, t, e0);
+    case 6: return chunk<0, 1, BITS, MASTER, true>(p, k, t, e0);
+    case 7: return chunk<1, 1, BITS, MASTER, true>(p, k, t, e0);
+    case 0: return chunk<0, 0, BITS, MASTER, false>(p, k, t, e0);
+    case 1: return chunk<1, 0, BITS, MASTER, false>(p, k, t, e0);
+    case 2: return chunk<0, 1, BITS, MASTER, false>(p, k, t, e0);
+    default: return chunk<1, 1, BITS, MASTER, false>(p, k, t, e0);
+  }
+}
+
+// ---- the norm -----------------------------------------------------------------------
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+template <int D, bool WIDE>
+__device__ __forceinline__ double squares(const void* g, int64_t n, int64_t e0) {
+  constexpr int VE = D == 0 ? 4 : 8;
+  double s[2] = {0.0, 0.0};
+#pragma unroll 4
+  for (int u = 0; u < kNormChunk / kThreads / VE; ++u) {
+    const int64_t e = e0 + ((int64_t)u * kThreads + threadIdx.x) * VE;
+    if (e >= n) break;
+    float v[VE];
+    load<D, VE, WIDE>(g, e, n, v);
+#pragma unroll
+    for (int j = 0; j < VE; ++j) s[j & 1] = __builtin_fma((double)v[j], (double)v[j], s[j & 1]);
+  }
+  return s[0] + s[1];
+}
+
+// A chunk's sum of squares in FP64 (exact squares; FP64 runs at full rate here).
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormTable tab, double* partial) {
+  __shared__ double sh[kThreads / 64];
+  const int i = tensor_of(tab.first, tab.n, blockIdx.x);
+  const NormTensor t = tab.t[i];
+  const int64_t e0 = (int64_t)(blockIdx.x - tab.first[i]) * kNormChunk;
+  double s;
+  switch (t.types) {
+    case 2: s = squares<0, true>(t.g, t.n, e0); break;
+    case 3: s = squares<1, true>(t.g, t.n, e0); break;
+    case 0: s = squares<0, false>(t.g, t.n, e0); break;
+    default: s = squares<1, false>(t.g, t.n, e0); break;
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) partial[blockIdx.x] = (sh[0] + sh[1]) + (sh[2] + sh[3]);
+}
+
+__global__ __launch_bounds__(1024) void norm_end_kernel(const double* partial, int64_t n,
+                                                        double max_norm, float* norm,
+                                                        float* scale) {
+  __shared__ double sh[16];
+  double s = 0.0;
+#pragma unroll 8
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += partial[i];
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  s = 0.0;
+  for (int i = 0; i < 16; ++i) s += sh[i];
+  const double r = sqrt(s);
+  if (norm) *norm = (float)r;
+  // not finite: NaN, which the step takes as nothing to do
+  if (scale)
+    *scale = !(r < __builtin_huge_val()) ? __builtin_nanf("")
+                                         : (r > max_norm ? (float)(max_norm / r) : 1.0f);
+}
+
+inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+int64_t norm_chunks(int64_t n) { return (n + kNormChunk - 1) / kNormChunk; }
+
+hipError_t launch_adamw(AdamParams p, const vce_adamw_tensor* tensors, int64_t count, int bits,
+                        hipStream_t stream) {
+  const uint32_t lo = (uint32_t)p.seed, hi = (uint32_t)(p.seed >> 32);
+  p.seed_key = mix(lo ^ mix(hi));
+  p.key = mix(p.seed_key + (uint32_t)p.step);
+  int64_t done = 0, at = 0;  // tensor `at`, of which `done` elements are launched
+  while (at < count) {
+    AdamTable tab;
+    tab.n = 0;
+    int64_t chunks = 0;
+    constexpr int64_t kMost = (int64_t)1 << 23;  // workgroups per launch: below 2^32 threads
+    while (at < count && tab.n < kAdamTensors && chunks < kMost) {
+      const vce_adamw_tensor& t = tensors[at];
+      const int64_t left = t.n - done;
+      if (left <= 0) {
+        ++at;
+        done = 0;
+        continue;
+      }
+      int64_t c = (left + kChunk - 1) / kChunk;
+      if (c > kMost - chunks) c = kMost - chunks;
+      AdamTensor& o = tab.t[tab.n];
+      const int ps = t.param_dtype == 0 ? 4 : 2, gs = t.grad_dtype == 0 ? 4 : 2;
+      o.p = static_cast<char*>(t.param) + done * ps;
+      o.g = static_cast<const char*>(t.grad) + done * gs;
+      o.n = left < c * kChunk ? left : c * kChunk;
+      o.offset = t.offset + done;
+      o.types = (uint32_t)(t.param_dtype | t.grad_dtype << 1 | (al16(o.p) && al16(o.g)) << 2);
+      tab.first[tab.n++] = (uint32_t)chunks;
+      chunks += c;
+      done += o.n;
+    }
+    if (chunks == 0) break;
+    const dim3 grid((unsigned)chunks), block(kThreads);
+    if (bits == 8) {
+      if (p.master)
+        hipLaunchKernelGGL((adamw_kernel<8, true>), grid, block, 0, stream, p, tab);
+      else
+        hipLaunchKernelGGL((adamw_kernel<8, false>), grid, block, 0, stream, p, tab);
+    } else {
+      if (p.master)
+        hipLaunchKernelGGL((adamw_kernel<32, true>), grid, block, 0, stream, p, tab);
+      else
+        hipLaunchKernelGGL((adamw_kernel<32, false>), grid, block, 0, stream, p, tab);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_grad_norm(const vce_grad_tensor* tensors, int64_t count, double max_norm,
+                            float* norm, float* scale, double* partial, hipStream_t stream) {
+  int64_t done = 0, at = 0, total = 0;
+  while (at < count) {
+    NormTable tab;
+    tab.n = 0;
+    int64_t chunks = 0;
+    constexpr int64_t kMost = (int64_t)1 << 23;
+    while (at < count && tab.n < kAdamTensors && chunks < kMost) {
+      const vce_grad_tensor& t = tensors[at];
+      const int64_t left = t.n - done;
+      if (left <= 0) {
+        ++at;
+        done = 0;
+        continue;
+      }
+      int64_t c = norm_chunks(left);
+      if (c > kMost - chunks) c = kMost - chunks;
+      NormTensor& o = tab.t[tab.n];
+      o.g = static_cast<const char*>(t.grad) + done * (t.dtype == 0 ? 4 : 2);
+      o.n = left < c * kNormChunk ? left : c * kNormChunk;
+      o.types = (uint32_t)(t.dtype | al16(o.g) << 1);
+      tab.first[tab.n++] = (uint32_t)chunks;
+      chunks += c;
+      done += o.n;
+    }
+    if (chunks == 0) break;
+    hipLaunchKernelGGL(norm_kernel, dim3((unsigned)chunks), dim3(kThreads), 0, stream, tab,
+                       partial + total);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    total += chunks;
+  }
+  hipLaunchKernelGGL(norm_end_kernel, dim3(1), dim3(1024), 0, stream, partial, total, max_norm,
+                     norm, scale);
+  return hipGetLastError();
+}
+
+}  // namespace vce

@@ -6,9 +6,12 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 
+#include <algorithm>
 #include <mutex>
 
+#include "adamw.h"
 #include "vce.h"
 #include "vce_internal.h"
 
@@ -1145,6 +1148,159 @@ int ce_sample(const void* logits, int dtype, int64_t d0, int64_t d1, int64_t V, 
   p.logprob = logprob;
   return launch_status(
       vce::launch_sample(p, dtype, N, workspace, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+// Does one of the first n_out ranges overlap another one of the n?  Sorted by their
+// beginnings, an overlap shows against the furthest end so far of the outputs, and of all for
+// an output.  The array is reordered.
+struct Marked {
+  Range r;
+  bool out;
+};
+inline bool any_overlap(Marked* a, int64_t n) {
+  std::sort(a, a + n, [](const Marked& x, const Marked& y) { return x.r.lo < y.r.lo; });
+  uintptr_t all = 0, outs = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (a[i].r.lo >= a[i].r.hi) continue;
+    if (a[i].r.lo < (a[i].out ? all : outs)) return true;
+    all = std::max(all, a[i].r.hi);
+    if (a[i].out) outs = std::max(outs, a[i].r.hi);
+  }
+  return false;
+}
+
+constexpr int64_t kMostTensors = (int64_t)1 << 20;
+constexpr int64_t kMostElements = (int64_t)1 << 40;
+
+}  // namespace
+
+int adamw_step(const vce_adamw_tensor* tensors, int64_t count, int bits, void* m, void* v,
+               uint8_t* m_scales, uint8_t* v_scales, float* master, int64_t total, double lr,
+               double beta1, double beta2, double eps, double weight_decay, int64_t step,
+               const float* lr_device, const int64_t* step_device, const float* grad_scale,
+               uint64_t seed, void* stream) {
+  if (count < 0 || total < 0 || total % 128 != 0 || (bits != 8 && bits != 32)) return VCE_EINVAL;
+  if (count > kMostTensors || total > kMostElements) return VCE_EUNSUPPORTED;
+  // the comparisons fail for NaN too
+  if (!(lr >= 0.0) || !(eps >= 0.0) || !(weight_decay >= 0.0) || !__builtin_isfinite(lr) ||
+      !__builtin_isfinite(eps) || !__builtin_isfinite(weight_decay) ||
+      !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || step < 1)
+    return VCE_EINVAL;
+  if (count == 0 || total == 0) {
+    for (int64_t i = 0; tensors && i < count; ++i)
+      if (tensors[i].n != 0) return VCE_EINVAL;
+    return count > 0 && !tensors ? VCE_EINVAL : VCE_OK;
+  }
+  if (!tensors || !m || !v || (bits == 8 && (!m_scales || !v_scales))) return VCE_EINVAL;
+  if (!aligned(m, 16) || !aligned(v, 16) || !aligned(master, 16) || !aligned(lr_device, 4) ||
+      !aligned(step_device, 8) || !aligned(grad_scale, 4))
+    return VCE_EALIGN;
+  for (int64_t i = 0; i < count; ++i) {
+    const vce_adamw_tensor& t = tensors[i];
+    if (!dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype)) return VCE_EDTYPE;
+    if (t.n < 0 || t.offset < 0 || t.offset % 128 != 0) return VCE_EINVAL;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || t.n > total || t.offset > total - (t.n + 127) / 128 * 128)
+      return VCE_EINVAL;
+    if (!aligned(t.param, dtype_size(t.param_dtype)) || !aligned(t.grad, dtype_size(t.grad_dtype)))
+      return VCE_EALIGN;
+  }
+  // the memory, and the tensors' places in the flat arrays
+  Marked* a = static_cast<Marked*>(malloc(sizeof(Marked) * (size_t)(2 * count + 8)));
+  if (!a) return VCE_EHIP;
+  int64_t k = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const vce_adamw_tensor& t = tensors[i];
+    if (t.n > 0)
+      a[k++] = Marked{Range{(uintptr_t)t.offset, (uintptr_t)(t.offset + (t.n + 127) / 128 * 128)},
+                      true};
+  }
+  bool bad = any_overlap(a, k);
+  if (!bad) {
+    k = 0;
+    for (int64_t i = 0; i < count; ++i) {
+      const vce_adamw_tensor& t = tensors[i];
+      a[k++] = Marked{range(t.n ? t.param : nullptr, t.n * dtype_size(t.param_dtype)), true};
+      a[k++] = Marked{range(t.n ? t.grad : nullptr, t.n * dtype_size(t.grad_dtype)), false};
+    }
+    const int64_t es = bits == 8 ? 1 : 4;
+    a[k++] = Marked{range(m, total * es), true};
+    a[k++] = Marked{range(v, total * es), true};
+    a[k++] = Marked{range(bits == 8 ? m_scales : nullptr, total / 32), true};
+    a[k++] = Marked{range(bits == 8 ? v_scales : nullptr, total / 32), true};
+    a[k++] = Marked{range(master, total * 4), true};
+    a[k++] = Marked{range(lr_device, 4), false};
+    a[k++] = Marked{range(step_device, 8), false};
+    a[k++] = Marked{range(grad_scale, 4), false};
+    bad = any_overlap(a, k);
+  }
+  free(a);
+  if (bad) return VCE_EALIAS;
+  vce::AdamParams p;
+  p.m = m;
+  p.v = v;
+  p.m_scales = m_scales;
+  p.v_scales = v_scales;
+  p.master = master;
+  p.b1 = (float)beta1;
+  p.c1 = (float)(1.0 - beta1);
+  p.b2 = (float)beta2;
+  p.c2 = (float)(1.0 - beta2);
+  p.eps = (float)eps;
+  p.ln_b1 = log(beta1);
+  p.ln_b2 = log(beta2);
+  p.decay = (float)(1.0 - lr * weight_decay);
+  p.a = (float)(lr / -expm1((double)step * p.ln_b1));
+  p.rs = (float)(1.0 / sqrt(-expm1((double)step * p.ln_b2)));
+  p.lr = lr;
+  p.wd = weight_decay;
+  p.step = step;
+  p.lr_device = lr_device;
+  p.step_device = step_device;
+  p.grad_scale = grad_scale;
+  p.seed = seed;
+  return launch_status(
+      vce::launch_adamw(p, tensors, count, bits, static_cast<hipStream_t>(stream)));
+}
+
+size_t grad_norm_workspace_size(int64_t total, int64_t count) {
+  if (total < 0 || count < 0 || total > kMostElements || count > kMostTensors) return 0;
+  // every tensor's last chunk may be a partial one, and so may the last of a launch
+  return (size_t)(vce::norm_chunks(total) + 2 * count + 1) * 8;
+}
+
+int grad_norm(const vce_grad_tensor* tensors, int64_t count, double max_norm, float* norm,
+              float* scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (count < 0 || !(max_norm > 0.0) || (count > 0 && !tensors)) return VCE_EINVAL;
+  if (count > kMostTensors) return VCE_EUNSUPPORTED;
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const vce_grad_tensor& t = tensors[i];
+    if (t.dtype != VCE_DTYPE_FP32 && t.dtype != VCE_DTYPE_BF16) return VCE_EDTYPE;
+    if (t.n < 0 || (t.n > 0 && !t.grad)) return VCE_EINVAL;
+    if (t.n > kMostElements - total) return VCE_EUNSUPPORTED;
+    if (!aligned(t.grad, dtype_size((int)t.dtype))) return VCE_EALIGN;
+    total += t.n;
+  }
+  if (!norm && !scale) return VCE_OK;
+  if (!workspace) return VCE_EINVAL;
+  if (!aligned(norm, 4) || !aligned(scale, 4) || !aligned(workspace, 8)) return VCE_EALIGN;
+  const size_t need = grad_norm_workspace_size(total, count);
+  if (workspace_bytes < need) return VCE_EWORKSPACE;
+  const Range out[3] = {range(norm, 4), range(scale, 4), range(workspace, (int64_t)need)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return VCE_EALIAS;
+    for (int64_t j = 0; j < count; ++j)
+      if (overlap(out[i], range(tensors[j].n ? tensors[j].grad : nullptr,
+                                tensors[j].n * dtype_size((int)tensors[j].dtype))))
+        return VCE_EALIAS;
+  }
+  return launch_status(vce::launch_grad_norm(tensors, count, max_norm, norm, scale,
+                                             static_cast<double*>(workspace),
+                                             static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
