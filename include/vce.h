@@ -695,6 +695,52 @@ size_t grad_norm_workspace_size(int64_t total, int64_t count);
 int grad_norm(const vce_grad_tensor* tensors, int64_t count, double max_norm, float* norm,
               float* scale, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * beam_step: one step of beam search over B requests of K beams: the n_out best of a
+ * request's K * V continuations, by
+ *     value(k, v) = scores[k] + (z[k][v] - lse[k]),   lse = ln sum_v exp(z[k][v])
+ * in FP64, largest first, equal values by the lower k, then the lower v.  (Beams with equal
+ * scores and logits have equal values.)
+ *
+ *  logits   (B, K, V) as in ce_forward: request b, beam k at element b * ls0 + k * ls1.
+ *           -inf is a masked token and no candidate.
+ *  scores   (B, K) FP32: the beams' log-probabilities so far.  A beam whose score is not
+ *           finite (-inf: an empty one) has no candidates, nor has one with a NaN or +inf logit
+ *           or none above -inf.
+ *  ended    (B, K) bytes or NULL: a beam that is not 0 here has one candidate, itself, with its
+ *           score unchanged and end_token (0 <= end_token < V) as its token; its
+ *           logits are not read.
+ *  n_out    1 to 256; K up to 128, V up to 2^28, K ceil(V / 8192) up to 2^23, B K below 2^22
+ *           (VCE_EUNSUPPORTED).
+ *  score    (B, n_out) FP32: the value rounded.   parent (B, n_out) int32: k.
+ *  token    (B, n_out) int64: v.  Places without a candidate: -inf, -1, -1.
+ *  workspace  beam_workspace_size(B, K, V) bytes, 256-byte aligned; its contents need not
+ *           survive.  Calls that may overlap in time each need their own.
+ *
+ * beam_reorder: states of the beams in place, row (b, k) := row (b, parent[b][k]), many of them in
+ * one launch.  Only rows that change are moved.
+ *
+ *  states   count entries in HOST memory, read before the call returns.  Row (b, k) is `outer`
+ *           pieces of `inner` bytes, piece o at data + b * stride_batch + k * stride_beam +
+ *           o * stride_outer bytes.  Any alignment.  The pieces of a state must not overlap,
+ *           nor those of two states (VCE_EALIAS; states that interleave, as slices of one
+ *           array do, must have equal strides of which one divides the others).
+ *  parent   request b's K entries int32 from element b * parent_stride on (beam_step's parent of
+ *           n_out = K, or the first K of more).  One outside 0 .. K - 1 leaves its row.
+ */
+typedef struct vce_beam_state {
+  void* data;
+  int64_t inner, outer, stride_outer, stride_beam, stride_batch;
+} vce_beam_state;
+
+size_t beam_workspace_size(int64_t B, int64_t K, int64_t V);
+int beam_step(const void* logits, int dtype, int64_t B, int64_t K, int64_t V, int64_t ls0,
+              int64_t ls1, const float* scores, const uint8_t* ended, int64_t end_token,
+              int64_t n_out, float* score, int32_t* parent, int64_t* token, void* workspace,
+              size_t workspace_bytes, void* stream);
+int beam_reorder(const vce_beam_state* states, int64_t count, int64_t B, int64_t K,
+                 const int32_t* parent, int64_t parent_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -156,3 +156,122 @@ def test_binding_grad_norm():
                            (P, dict(workspace=torch.zeros(9)), TypeError), (P, {}, RuntimeError)):
         with pytest.raises(err):
             vce.grad_norm(grads, **kw)
+
+
+# ---- beam search -----------------------------------------------------------------
+
+def bstep(L, **kw):
+    a = dict(z=A, dtype=1, B=2, K=3, V=1000, ls0=3000, ls1=1000, s=A + G, ended=A + 2 * G, end=5,
+             n=6, score=A + 3 * G, parent=A + 4 * G, token=A + 5 * G, ws=A + 6 * G, wb=1 << 20)
+    a.update(kw)
+    return L.beam_step(a["z"], a["dtype"], a["B"], a["K"], a["V"], a["ls0"], a["ls1"], a["s"],
+                       a["ended"], a["end"], a["n"], a["score"], a["parent"], a["token"],
+                       a["ws"], a["wb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=2), 2), (dict(B=-1), 1), (dict(K=0), 1), (dict(V=0), 1), (dict(ls0=-1), 1),
+    (dict(ls1=-1), 1), (dict(n=0), 1), (dict(n=257), 7), (dict(K=129), 7),
+    (dict(V=(1 << 28) + 1), 7), (dict(B=1 << 22), 7), (dict(B=1 << 21, K=2), 7),
+    (dict(end=-1), 1), (dict(end=1000), 1), (dict(z=None), 1), (dict(s=None), 1),
+    (dict(score=None), 1), (dict(parent=None), 1), (dict(token=None), 1), (dict(ws=None), 1),
+    (dict(ls0=1 << 61), 1), (dict(z=A + 1), 3), (dict(s=A + G + 2), 3),
+    (dict(score=A + 3 * G + 2), 3), (dict(parent=A + 4 * G + 1), 3), (dict(token=A + 5 * G + 4), 3),
+    (dict(ws=A + 6 * G + 128), 3), (dict(wb=100), 5), (dict(score=A), 4), (dict(parent=A + G), 4),
+    (dict(token=A + 2 * G), 4), (dict(ws=A), 4), (dict(parent=A + 3 * G), 4),
+    (dict(token=A + 6 * G), 4), (dict(B=0), 0), (dict(ended=None, end=-1, B=0), 0),
+])
+def test_beam_step_rejects(L, kw, code):
+    assert bstep(L, **kw) == code
+
+
+def test_beam_workspace_size(L):
+    f = L.beam_workspace_size
+    assert f(-1, 1, 1) == 0 and f(1, 0, 1) == 0 and f(1, 1, 0) == 0 and f(1, 129, 1) == 0
+    assert f(0, 4, 10) > 0 and f(2, 3, 8193) >= 2 * f(2, 3, 8192) - 1024
+
+
+def piece(data=A, inner=64, outer=1, so=0, sk=64, sb=192):
+    return (data, inner, outer, so, sk, sb)
+
+
+def reorder(L, states=(piece(),), **kw):
+    a = dict(count=len(states), B=2, K=3, parent=A + G, stride=3)
+    a.update(kw)
+    flat = [x for e in states for x in e]
+    tab = (ctypes.c_int64 * len(flat))(*flat) if states else None
+    return L.beam_reorder(tab, a["count"], a["B"], a["K"], a["parent"], a["stride"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(count=-1), 1), (dict(B=-1), 1), (dict(K=0), 1), (dict(stride=-1), 1), (dict(K=129), 7),
+    (dict(B=1 << 22), 7), (dict(count=1025), 7), (dict(parent=None), 1), (dict(parent=A + G + 2), 3),
+    (dict(stride=1 << 62), 1), (dict(states=(), count=1), 1), (dict(parent=A + 380), 4),
+    (dict(states=(piece(inner=-1),)), 1), (dict(states=(piece(outer=-1),)), 1),
+    (dict(states=(piece(sk=-64),)), 1), (dict(states=(piece(0),)), 1),
+    (dict(states=(piece(inner=1 << 41, sk=1 << 41, sb=1 << 43),)), 7),
+    (dict(states=(piece(inner=1 << 39, sk=1 << 39, sb=1 << 41),)), 7),
+    (dict(states=(piece(sk=0),)), 4), (dict(states=(piece(sb=0),)), 4),
+    (dict(states=(piece(sk=63),)), 4), (dict(states=(piece(sb=191),)), 4),
+    (dict(states=(piece(outer=2, so=32),)), 4), (dict(states=(piece(outer=2, so=64),)), 4),
+    (dict(states=(piece(sb=1 << 61),)), 1),
+    (dict(states=(piece(), piece())), 4),                      # one state twice
+    (dict(states=(piece(), piece(A + 320))), 4),               # the last row of one
+    (dict(states=(piece(sk=128, sb=384), piece(A + 60, sk=128, sb=384))), 4),
+    (dict(states=(piece(sk=128, sb=384), piece(A + 64, 65, sk=128, sb=384))), 4),
+    (dict(states=(piece(sk=128, sb=384), piece(A + 64, sk=128, sb=512))), 4),
+    (dict(states=(piece(inner=0), piece(0, outer=0)), B=0), 0),
+])
+def test_beam_reorder_rejects(L, kw, code):
+    assert reorder(L, **kw) == code
+
+
+Z, SC = torch.zeros((2, 3, 50)), torch.zeros((2, 3))
+BAD_BEAM = [
+    (dict(logits=Z.double()), TypeError, "float32 or bfloat16"),
+    (dict(logits=Z[0]), ValueError, r"\(B, K, V\)"),
+    (dict(logits=Z.transpose(1, 2)), ValueError, "contiguous"),
+    (dict(scores=SC.double()), ValueError, "scores must be"),
+    (dict(scores=SC[:1]), ValueError, "scores must be"),
+    (dict(ended=torch.zeros((2, 3), dtype=torch.uint8)), ValueError, "ended must be"),
+    (dict(out=(None, None)), ValueError, "3 tensors"),
+    (dict(out=(None, torch.zeros((2, 3), dtype=torch.int64), None)), ValueError, "parent must be"),
+    (dict(workspace=torch.zeros(10)), TypeError, "workspace must be"),
+    (dict(), *GPU_ONLY),
+]
+
+
+@pytest.mark.parametrize("kw,err,text", BAD_BEAM)
+def test_binding_beam_step(kw, err, text):
+    a = dict(logits=Z, scores=SC)
+    a.update(kw)
+    with pytest.raises(err, match=text):
+        vce.beam_step(a.pop("logits"), a.pop("scores"), **a)
+
+
+PA = torch.zeros((2, 3), dtype=torch.int32)
+
+
+@pytest.mark.parametrize("states,parent,err,text", [
+    ([SC], PA.long(), TypeError, "int32"), ([SC], PA[0], TypeError, "int32"),
+    ([SC], PA.t().contiguous().t(), ValueError, "contiguous"),
+    ([torch.zeros((2, 4, 5))], PA, ValueError, r"\(2, 3, \.\.\.\)"),
+    ([torch.zeros(6)], PA, ValueError, r"\(2, 3, \.\.\.\)"),
+    ([torch.zeros((2, 3, 5, 6, 7))[:, :, :3, :4, :5]], PA, ValueError, "equally spaced"),
+    ([torch.zeros((2, 3, 5, 6)).transpose(2, 3)], PA, ValueError, "equally spaced"),
+    ([SC], PA, *GPU_ONLY),
+])
+def test_binding_beam_reorder(states, parent, err, text):
+    with pytest.raises(err, match=text):
+        vce.beam_reorder(states, parent)
+
+
+def test_beam_pieces():
+    f = binding._beam_pieces
+    t = torch.zeros((2, 3, 4, 50, 8))
+    assert f(t, "t") == (6400, 1, 0, 6400, 19200)
+    assert f(t[:, :, :, :33], "t") == (33 * 32, 4, 1600, 6400, 19200)
+    assert f(t[:, :, 1:2, :7], "t") == (7 * 32, 1, 0, 6400, 19200)
+    assert f(t[..., :3], "t") == (12, 200, 32, 6400, 19200)
+    assert f(torch.zeros((2, 3)), "t") == (4, 1, 0, 4, 12)
+    assert f(torch.zeros((2, 3, 0, 5)), "t")[0] == 0

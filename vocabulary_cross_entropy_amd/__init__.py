@@ -3,7 +3,8 @@
 The computation lives in ``libvce.so`` (HIP kernels behind the C-ABI declared
 in ``include/vce.h``); ``binding`` marshals torch tensors into it.
 """
-from .binding import (AdamWState, adamw_state, adamw_step, ce_backward, ce_backward_shard, ce_forward,  # noqa: F401
+from .binding import (AdamWState, adamw_state, adamw_step, beam_reorder, beam_step,
+                      beam_workspace, beam_workspace_size, ce_backward, ce_backward_shard, ce_forward,  # noqa: F401
                       ce_sample, ce_sample_workspace, ce_sample_workspace_size,
                       ce_forward_backward, ce_forward_shard, ce_merge_shards, gemm_bf16,
                       grad_norm,

@@ -84,6 +84,10 @@ SIGNATURES = {
                           _F64, _I64, _VP, _VP, _VP, _U64, _VP]),
     "grad_norm_workspace_size": (_SZ, [_I64, _I64]),
     "grad_norm": (_I32, [_VP, _I64, _F64, _VP, _VP, _VP, _SZ, _VP]),
+    "beam_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "beam_step": (_I32, [_VP, _I32, _I64, _I64, _I64, _I64, _I64, _VP, _VP, _I64, _I64, _VP, _VP,
+                         _VP, _VP, _SZ, _VP]),
+    "beam_reorder": (_I32, [_VP, _I64, _I64, _I64, _VP, _I64, _VP]),
 }
 
 _lib = None
@@ -1205,3 +1209,105 @@ def grad_norm(grads, max_norm: float = float("inf"), *, workspace: torch.Tensor 
                                             ws.numel(), s))
         return nrm, sc
     return _on_stream(ref, stream, call)
+
+
+def beam_workspace_size(B: int, K: int, V: int) -> int:
+    return int(lib().beam_workspace_size(B, K, V))
+
+
+def beam_workspace(B: int, K: int, V: int, device="cuda") -> torch.Tensor:
+    n = beam_workspace_size(B, K, V)
+    if n == 0:
+        raise ValueError(f"no workspace plan for B={B}, K={K}, V={V}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def beam_step(logits: torch.Tensor, scores: torch.Tensor, n_out: int | None = None, *,
+              ended: torch.Tensor | None = None, end_token: int = 0,
+              workspace: torch.Tensor | None = None, stream=None, out=None):
+    """The n_out (K unless given) best continuations of every request: logits (B, K, V), BF16 or
+    FP32, scores (B, K) FP32, the beams' log-probabilities so far (-inf: an empty beam).  ``ended``
+    (B, K) bool: beams that go on as they are, with end_token.  Returns (score, parent, token),
+    (B, n_out) each, FP32, int32 and int64, best first (-inf, -1, -1 where candidates run out).
+    ``out`` gives the three."""
+    dt = _elem_dtype(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError(f"logits must be (B, K, V), got {tuple(logits.shape)}")
+    B, K, V = logits.shape
+    if V > 1 and logits.stride(2) != 1:
+        raise ValueError("the vocabulary dimension of logits must be contiguous")
+    n = K if n_out is None else int(n_out)
+    _check_out(scores, "scores", (B, K), torch.float32, logits)
+    _check_out(ended, "ended", (B, K), torch.bool, logits)
+    outs = (None,) * 3 if out is None else out
+    if len(outs) != 3:
+        raise ValueError("out must hold 3 tensors (None to allocate)")
+    for t, name, td in zip(outs, ("score", "parent", "token"),
+                           (torch.float32, torch.int32, torch.int64)):
+        _check_out(t, name, (B, n), td, logits)
+    if workspace is not None:
+        _check_buf(workspace, "workspace", workspace.numel(), torch.uint8, like=logits)
+
+    def call(s):
+        sc, pa, tok = outs
+        if sc is None:
+            sc = logits.new_empty((B, n), dtype=torch.float32)
+        if pa is None:
+            pa = logits.new_empty((B, n), dtype=torch.int32)
+        if tok is None:
+            tok = logits.new_empty((B, n), dtype=torch.int64)
+        ws = beam_workspace(B, K, V, logits.device) if workspace is None else workspace
+        _check("beam_step", lib().beam_step(
+            _at(logits), dt, B, K, V, logits.stride(0), logits.stride(1), _at(scores), _at(ended),
+            end_token, n, _at(sc), _at(pa), _at(tok), _at(ws), ws.numel(), s))
+        return sc, pa, tok
+    return _on_stream(logits, stream, call)
+
+
+def _beam_pieces(t: torch.Tensor, name: str):
+    """(inner, outer, stride_outer, stride_beam, stride_batch) in bytes of a state (B, K, ...): its
+    rows as equally spaced pieces without gaps."""
+    es, shape, st = t.element_size(), t.shape, t.stride()
+    inner, outer, stride = es, 1, 0
+    for n, s in zip(reversed(shape[2:]), reversed(st[2:])):
+        if n == 1:
+            continue
+        if outer == 1 and s * es == inner:
+            inner *= n
+        elif outer == 1:
+            outer, stride = n, s * es
+        elif s * es == outer * stride:
+            outer *= n
+        else:
+            raise ValueError(f"the rows of {name} must be contiguous, or equally spaced pieces, got "
+                             f"strides {tuple(st)}")
+    if t.numel() == 0:
+        inner = 0
+    return inner, outer, stride, st[1] * es, st[0] * es
+
+
+def beam_reorder(states, parent: torch.Tensor, *, stream=None) -> None:
+    """Every state (B, K, ...) in place: row (b, k) becomes row (b, parent[b, k]), in one launch.
+    parent (B, K) int32 as of ``beam_step`` (rows may be strided); an entry outside 0 .. K - 1
+    leaves its row.  A state's rows may be views with gaps (the used part of a longer cache)."""
+    states = [states] if isinstance(states, torch.Tensor) else list(states)
+    if parent.dim() != 2 or parent.dtype != torch.int32:
+        raise TypeError(f"parent must be int32 of shape (B, K), got {parent.dtype} of "
+                        f"{tuple(parent.shape)}")
+    B, K = parent.shape
+    if K > 1 and parent.stride(1) != 1:
+        raise ValueError("the rows of parent must be contiguous")
+    entries = []
+    for i, t in enumerate(states):
+        if t.dim() < 2 or tuple(t.shape[:2]) != (B, K):
+            raise ValueError(f"states[{i}] must be ({B}, {K}, ...), got {tuple(t.shape)}")
+        if t.device != parent.device:
+            raise ValueError(f"states[{i}] must be on {parent.device}, got {t.device}")
+        entries += (t.data_ptr(), *_beam_pieces(t, f"states[{i}]"))
+    table = (ctypes.c_int64 * len(entries))(*entries)
+
+    def call(s):
+        _check("beam_reorder", lib().beam_reorder(table, len(states), B, K, _at(parent),
+                                                  parent.stride(0), s))
+    if K > 0:
+        _on_stream(parent, stream, call)

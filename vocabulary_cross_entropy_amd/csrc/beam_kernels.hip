@@ -1,0 +1,659 @@
+// Beam search: the best continuations over a request's beams and the whole vocabulary,
+//   value(k, v) = score_k + (z_kv - lse_k),  lse_k = m_k + ln sum_v exp(z_kv - m_k)
+// in FP64, ties to the lower (k, v); and the reordering of the beams' states in place.
+//
+// The logits are read once.  A row is cut into segments of 8192 tokens, each a workgroup's
+// (beam_scan_kernel): it keeps the segment's maximum, the FP64 sum of exp(z - maximum), and the
+// maximum of each group of 16 vectors (128 tokens in BF16, 64 in FP32).  Segments and groups lie
+// at the same tokens whatever the row's alignment, so equal rows have equal sums.
+//
+// beam_pick_kernel (a workgroup per request) joins the segments to the beams' lse and bounds
+// the answer from below before it looks at a logit again: the n-th largest segment maximum is
+// reached by n candidates at least, then the n-th largest group maximum among what is left.  Only
+// groups that reach the bound (n of them and ties) are read again, their candidates listed
+// in LDS and ranked by counting.  Where more tie than the lists hold, the answer is taken one by
+// one from all logits.  Bounds are FP32 numbers rounded down, the comparison of
+// candidates is FP64.
+#include <math.h>
+
+#include "beam.h"
+#include "vce.h"
+#include "vce_device.h"
+#include "vce_internal.h"
+
+namespace vce {
+
+namespace {
+
+constexpr int kThreads = 256;      // of a segment's workgroup
+constexpr int kSeg = 8192;         // tokens
+constexpr int kPickThreads = 512;  // of a request's
+constexpr int kPickWaves = kPickThreads / 64;
+constexpr int kGroups = 2048;      // groups listed
+constexpr int kCands = 1024;       // candidates listed
+constexpr int kMostGroups = kSeg / 64;
+
+template <int DT>
+struct Seg {
+  static constexpr int VE = DT == 0 ? 4 : 8;
+  static constexpr int kVecs = kSeg / (kThreads * VE);  // vectors per thread
+  static constexpr int kGroup = 16 * VE;                // tokens of a group
+  static constexpr int kPer = kSeg / kGroup;            // groups of a segment
+};
+
+// Tokens e .. e + VE - 1 of a row of V, -inf past its end.  Rows need not be aligned.
+template <int DT>
+__device__ __forceinline__ void load(const char* row, int64_t e, int64_t V, float* z) {
+  constexpr int VE = Seg<DT>::VE;
+  if (e + VE <= V) {
+    u32x4_t w;
+    __builtin_memcpy(&w, row + e * (DT == 0 ? 4 : 2), 16);
+    if constexpr (DT == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = __uint_as_float(w[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z[2 * j] = bf16_lo(w[j]);
+        z[2 * j + 1] = bf16_hi(w[j]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      z[j] = kNegInf;
+      if (e + j < V) {
+        if constexpr (DT == 0)
+          z[j] = reinterpret_cast<const float*>(row)[e + j];
+        else
+          z[j] = from_bf16(reinterpret_cast<const uint16_t*>(row)[e + j]);
+      }
+    }
+  }
+}
+
+// The larger, NaN if either is.
+__device__ __forceinline__ float maxn(float a, float b) {
+  return __builtin_elementwise_maximum(a, b);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float row_move(float v) {
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, false));
+}
+
+// Maximum over the 16 lanes of a row, in all of them.
+__device__ __forceinline__ float row_max(float v) {
+  v = maxn(v, row_move<0xb1>(v));   // neighbours
+  v = maxn(v, row_move<0x4e>(v));   // pairs
+  v = maxn(v, row_move<0x141>(v));  // halves of eight, mirrored
+  v = maxn(v, row_move<0x140>(v));  // sixteen, mirrored
+  return v;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+  v = row_max(v);
+  v = maxn(v, __shfl_xor(v, 16, 64));
+  return maxn(v, __shfl_xor(v, 32, 64));
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// exp(z - m) from x = z log2(e) - m log2(e) <= 0: 2^n 2^f, |f| <= 1/2, by the Taylor
+// polynomial of degree 9 (relative error below 7e-12).  Below 2^-200 it stays there.
+__device__ __forceinline__ double power(double x, const double* poly) {
+  x = __builtin_fmax(x, -200.0);
+  const double r = x + 0x1.8p52;
+  const double f = x - (r - 0x1.8p52);
+  double g = poly[9];
+#pragma unroll
+  for (int i = 8; i >= 0; --i) g = __builtin_fma(g, f, poly[i]);
+  const uint64_t b = __builtin_bit_cast(uint64_t, g);
+  const uint32_t hi = (uint32_t)(b >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, r) << 20);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)b);
+}
+
+constexpr double kLog2eD = 1.4426950408889634;
+
+// Bound by FP64 issue (20 instructions a token) and reading at about the same rate.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamParams p) {
+  using S = Seg<DT>;
+  __shared__ float smax[kThreads / 64];
+  __shared__ double ssum[kThreads / 64];
+  const int64_t i = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (i >= p.n) return;
+  const int64_t row = i / p.segs;
+  const int seg = (int)(i - row * p.segs);
+  const int64_t b = row / p.K;
+  if (p.ended && p.ended[row]) return;  // nobody reads it
+  const char* base = static_cast<const char*>(p.logits) +
+                     (b * p.ls0 + (row - b * p.K) * p.ls1) * (DT == 0 ? 4 : 2);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t e0 = (int64_t)seg * kSeg + threadIdx.x * S::VE;
+  float z[S::kVecs][S::VE];
+#pragma unroll
+  for (int j = 0; j < S::kVecs; ++j) load<DT>(base, e0 + j * kThreads * S::VE, p.V, z[j]);
+  float m = kNegInf;
+#pragma unroll
+  for (int j = 0; j < S::kVecs; ++j) {
+    float g = z[j][0];
+#pragma unroll
+    for (int t = 1; t < S::VE; ++t) g = maxn(g, z[j][t]);
+    g = row_max(g);
+    m = maxn(m, g);
+    if ((threadIdx.x & 15) == 0)
+      p.group_max[i * S::kPer + j * (kThreads / 16) + threadIdx.x / 16] = g;
+  }
+  m = maxn(m, __shfl_xor(m, 16, 64));
+  m = maxn(m, __shfl_xor(m, 32, 64));
+  if (lane == 0) smax[wave] = m;
+  __syncthreads();
+  m = maxn(maxn(smax[0], smax[1]), maxn(smax[2], smax[3]));
+  // nothing but masked tokens: any reference will do, the sum is not used
+  const double ml = -(m == kNegInf ? 0.0 : (double)m) * kLog2eD;
+  double s[2] = {0.0, 0.0};
+#pragma unroll
+  for (int j = 0; j < S::kVecs; ++j)
+#pragma unroll
+    for (int t = 0; t < S::VE; ++t)
+      s[t & 1] += power(__builtin_fma((double)z[j][t], kLog2eD, ml), p.poly);
+  const double sum = wave_sum(s[0] + s[1]);
+  if (lane == 0) ssum[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.seg_max[i] = m;
+    p.seg_sum[i] = (ssum[0] + ssum[1]) + (ssum[2] + ssum[3]);
+  }
+}
+
+// ---- the answer ------------------------------------------------------------------------
+
+// Larger values have larger keys; -inf has the least of a number, 0 is below all.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+// The key of an FP32 number at or below v: v rounded, and one below that where it went up.
+__device__ __forceinline__ uint32_t floor_key(double v) {
+  const float f = (float)v;
+  return key_of(f) - ((double)f > v ? 1u : 0u);
+}
+
+constexpr uint32_t kLeast = 0x007fffffu;  // the key of -inf
+
+struct Beam {
+  double lse, score;
+  int what;  // kDead, kEnded or kLive
+};
+enum { kDead, kEnded, kLive };
+
+struct PickShared {
+  Beam beam[kBeamMost];
+  uint64_t group[kGroups];  // key of the bound, and the segment and group
+  double value[kCands];
+  uint64_t index[kCands];
+  uint32_t keys[64];
+  uint32_t n_groups, n_cands, bound;
+  double best[kPickWaves];
+  uint64_t best_at[kPickWaves];
+};
+
+// The n-th largest of the keys that visit(f) gives this wavefront's lanes (each calls f with the same
+// number of keys, 0 for none); 0 with fewer than n above 0.
+template <class Visit>
+__device__ __forceinline__ uint32_t nth_key(int n, Visit visit) {
+  uint32_t t = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = t | 1u << bit;
+    int have = 0;
+    visit([&](uint32_t k) { have += __builtin_popcountll(__ballot(k >= c)); });
+    if (have >= n) t = c;
+  }
+  return t;
+}
+
+__device__ __forceinline__ bool better(double a, uint64_t ai, double b, uint64_t bi) {
+  return a > b || (a == b && ai < bi);
+}
+
+template <int DT>
+struct Pick {
+  using S = Seg<DT>;
+  const BeamParams& p;
+  PickShared& sh;
+  int64_t b;     // the request
+  int64_t row0;  // its first row
+  int n_segs;    // segments of all its beams
+
+  // The key of segment s of the request's: a bound that one of its candidates reaches.
+  __device__ __forceinline__ uint32_t segment_key(int s) const {
+    const int k = s / p.segs;
+    const Beam& q = sh.beam[k];
+    if (q.what == kEnded) return s == k * p.segs ? floor_key(q.score) : 0u;
+    if (q.what != kLive) return 0u;
+    const float m = p.seg_max[row0 * p.segs + s];
+    return m == kNegInf ? 0u : floor_key(q.score + ((double)m - q.lse));
+  }
+  __device__ __forceinline__ uint32_t group_key(int s, int g) const {
+    const int k = s / p.segs;
+    const Beam& q = sh.beam[k];
+    if (q.what == kEnded) return s == k * p.segs && g == 0 ? floor_key(q.score) : 0u;
+    if (q.what != kLive) return 0u;
+    const float m = p.group_max[(row0 * p.segs + s) * S::kPer + g];
+    return m == kNegInf ? 0u : floor_key(q.score + ((double)m - q.lse));
+  }
+  __device__ __forceinline__ const char* row(int k) const {
+    return static_cast<const char*>(p.logits) +
+           (b * p.ls0 + k * p.ls1) * (DT == 0 ? 4 : 2);
+  }
+  // f(value, index) for the candidates of vector `lane16` of group g of segment s.
+  template <class F>
+  __device__ __forceinline__ void candidates(int s, int g, int lane16, F f) const {
+    const int k = s / p.segs;
+    const Beam& q = sh.beam[k];
+    if (q.what == kEnded) {
+      if (lane16 == 0) f(q.score, (uint64_t)k * (uint64_t)p.V + (uint64_t)p.end_token);
+      return;
+    }
+    // group g of a segment: vectors 16 g .. 16 g + 15
+    const int64_t e = (int64_t)(s - k * p.segs) * kSeg + (int64_t)(g * 16 + lane16) * S::VE;
+    float z[S::VE];
+    load<DT>(row(k), e, p.V, z);
+#pragma unroll
+    for (int j = 0; j < S::VE; ++j)
+      if (z[j] != kNegInf)
+        f(q.score + ((double)z[j] - q.lse), (uint64_t)k * (uint64_t)p.V + (uint64_t)(e + j));
+  }
+  __device__ __forceinline__ void write(int at, double v, uint64_t index) const {
+    const int64_t o = b * p.n_out + at;
+    const uint64_t k = index / (uint64_t)p.V;
+    p.score[o] = (float)v;
+    p.parent[o] = (int32_t)k;
+    p.token[o] = (int64_t)(index - k * (uint64_t)p.V);
+  }
+
+  // lse of beam k by one wavefront, in a fixed order.
+  __device__ void join(int k, int lane) const {
+    const int64_t r = row0 + k;
+    const double score = (double)p.scores[r];
+    Beam q{0.0, score, kDead};
+    const bool finite = fabs(score) < __builtin_huge_val();
+    if (p.ended && p.ended[r]) {
+      if (finite) q.what = kEnded;
+    } else {
+      float m = kNegInf;
+      for (int s = lane; s < p.segs; s += 64) m = maxn(m, p.seg_max[r * p.segs + s]);
+      m = wave_max(m);
+      if (finite && fabsf(m) < __builtin_huge_valf()) {  // not NaN either
+        double sum = 0.0;
+        for (int s = lane; s < p.segs; s += 64) {
+          const float t = p.seg_max[r * p.segs + s];
+          if (t != kNegInf)
+            sum += p.seg_sum[r * p.segs + s] *
+                   power(((double)t - (double)m) * kLog2eD, p.poly);
+        }
+        q.lse = (double)m + log(wave_sum(sum));
+        q.what = kLive;
+      }
+    }
+    if (lane == 0) sh.beam[k] = q;
+  }
+
+  // Groups whose key reaches `bound`, listed; returns how many there are.
+  __device__ uint32_t list_groups(uint32_t bound) const {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+    if (threadIdx.x == 0) sh.n_groups = 0;
+    __syncthreads();
+    for (int s = wave; s < n_segs; s += kPickWaves) {
+      if (segment_key(s) < bound) continue;  // the same in all lanes
+      for (int g = lane; g < S::kPer; g += 64) {
+        const uint32_t key = group_key(s, g);
+        const bool in = key >= bound && key != 0;
+        const uint64_t mask = __ballot(in);
+        if (mask == 0) continue;
+        uint32_t at = 0;
+        if (lane == 0) at = atomicAdd(&sh.n_groups, (uint32_t)__builtin_popcountll(mask));
+        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+        at += __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                        __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        if (in && at < kGroups)
+          sh.group[at] = ((uint64_t)key << 32) | (uint32_t)(s * S::kPer + g);
+      }
+    }
+    __syncthreads();
+    return sh.n_groups;
+  }
+
+  // The n_out-th largest of `n` keys in LDS, by wavefront 0, for all.
+  template <class Key>
+  __device__ uint32_t nth_listed(int n, Key key) const {
+    if (threadIdx.x < 64) {
+      const uint32_t t = nth_key(p.n_out, [&](auto f) {
+        for (int i = 0; i < n; i += 64)
+          f(i + (int)threadIdx.x < n ? key(i + (int)threadIdx.x) : 0u);
+      });
+      if (threadIdx.x == 0) sh.bound = t;
+    }
+    __syncthreads();
+    const uint32_t t = sh.bound;
+    __syncthreads();
+    return t;
+  }
+
+  // Candidates at or above `bound` of the listed groups; returns how many there are.
+  __device__ uint32_t list_candidates(uint32_t n_groups, uint32_t bound) const {
+    const double least = (double)of_key(bound);
+    if (threadIdx.x == 0) sh.n_cands = 0;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x / 16; i < n_groups; i += kPickThreads / 16) {
+      const uint64_t e = sh.group[i];
+      if ((uint32_t)(e >> 32) < bound) continue;
+      const int at = (int)(uint32_t)e;
+      candidates(at / S::kPer, at % S::kPer, threadIdx.x & 15, [&](double v, uint64_t index) {
+        if (v >= least) {
+          const uint32_t c = atomicAdd(&sh.n_cands, 1u);
+          if (c < kCands) {
+            sh.value[c] = v;
+            sh.index[c] = index;
+          }
+        }
+      });
+    }
+    __syncthreads();
+    return sh.n_cands;
+  }
+
+  // One by one from all logits: the best candidate after the last one.
+  __device__ void one_by_one() const {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double last = __builtin_huge_val();
+    uint64_t last_at = 0;
+    for (int n = 0; n < p.n_out; ++n) {
+      double v = -__builtin_huge_val();
+      uint64_t at = ~(uint64_t)0;
+      const int groups = n_segs * S::kPer;
+      for (int i = threadIdx.x / 16; i < groups; i += kPickThreads / 16) {
+        const int s = i / S::kPer;
+        if (group_key(s, i % S::kPer) == 0) continue;
+        candidates(s, i % S::kPer, threadIdx.x & 15, [&](double w, uint64_t index) {
+          if ((n == 0 || better(last, last_at, w, index)) && better(w, index, v, at)) {
+            v = w;
+            at = index;
+          }
+        });
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) {
+        const double w = __shfl_xor(v, off, 64);
+        const uint64_t wi = (uint64_t)__shfl_xor((unsigned long long)at, off, 64);
+        if (better(w, wi, v, at)) {
+          v = w;
+          at = wi;
+        }
+      }
+      __syncthreads();
+      if (lane == 0) {
+        sh.best[wave] = v;
+        sh.best_at[wave] = at;
+      }
+      __syncthreads();
+      v = sh.best[0];
+      at = sh.best_at[0];
+      for (int w = 1; w < kPickWaves; ++w)
+        if (better(sh.best[w], sh.best_at[w], v, at)) {
+          v = sh.best[w];
+          at = sh.best_at[w];
+        }
+      if (at == ~(uint64_t)0) return;  // no more candidates
+      if (threadIdx.x == 0) write(n, v, at);
+      last = v;
+      last_at = at;
+    }
+  }
+
+  __device__ void run() const {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int i = threadIdx.x; i < p.n_out; i += kPickThreads) {
+      p.score[b * p.n_out + i] = kNegInf;
+      p.parent[b * p.n_out + i] = -1;
+      p.token[b * p.n_out + i] = -1;
+    }
+    for (int k = wave; k < p.K; k += kPickWaves) join(k, lane);
+    __syncthreads();
+    // the n_out-th largest segment; 0 where there are fewer
+    uint32_t bound = 0;
+    if (n_segs >= p.n_out) {
+      if (wave == 0) {
+        uint32_t keys[8];  // of up to 512 segments; more are formed anew for every bit
+        if (n_segs <= 512) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            keys[j] = j * 64 + lane < n_segs ? segment_key(j * 64 + lane) : 0u;
+          const int used = (n_segs + 63) / 64;
+          bound = nth_key(p.n_out, [&](auto f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < used) f(keys[j]);
+          });
+        } else {
+          bound = nth_key(p.n_out, [&](auto f) {
+            for (int i = 0; i < n_segs; i += 64)
+              f(i + lane < n_segs ? segment_key(i + lane) : 0u);
+          });
+        }
+        if (lane == 0) sh.bound = bound;
+      }
+      __syncthreads();
+      bound = sh.bound;
+      __syncthreads();
+    }
+    uint32_t n;
+    while ((n = list_groups(bound)) > kGroups) {
+      // those listed reach the bound; so do n_out of them a higher one
+      const uint32_t t = nth_listed(kGroups, [&](int i) { return (uint32_t)(sh.group[i] >> 32); });
+      if (t <= bound) return one_by_one();
+      bound = t;
+    }
+    if ((int)n > p.n_out) {
+      const uint32_t t = nth_listed((int)n, [&](int i) { return (uint32_t)(sh.group[i] >> 32); });
+      bound = t > bound ? t : bound;
+    }
+    bound = bound > kLeast ? bound : kLeast;
+    uint32_t c;
+    while ((c = list_candidates(n, bound)) > kCands) {
+      const uint32_t t = nth_listed(kCands, [&](int i) { return floor_key(sh.value[i]); });
+      if (t <= bound) return one_by_one();
+      bound = t;
+    }
+    // a candidate's place is the number of better ones
+    for (uint32_t i = threadIdx.x; i < c; i += kPickThreads) {
+      const double v = sh.value[i];
+      const uint64_t at = sh.index[i];
+      int place = 0;
+      for (uint32_t j = 0; j < c; ++j) place += better(sh.value[j], sh.index[j], v, at);
+      if (place < p.n_out) write(place, v, at);
+    }
+  }
+};
+
+template <int DT>
+__global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamParams p) {
+  __shared__ PickShared sh;
+  const Pick<DT> q{p, sh, (int64_t)blockIdx.x, (int64_t)blockIdx.x * p.K, (int)(p.K * p.segs)};
+  q.run();
+}
+
+// ---- reordering ------------------------------------------------------------------------
+
+constexpr int kColumn = 16;  // bytes
+
+// A thread holds one column of 16 bytes (or, past the last whole one of a row, of one byte) of all
+// beams: the rows that another takes are read, then those that take another are written.
+// No thread reads what another writes, so a state is reordered in place.  The columns lie in
+// LDS, each thread's its own; four rows' loads are in flight together.
+template <int THREADS, int BEAMS>
+__global__ __launch_bounds__(THREADS) void beam_reorder_kernel(BeamTable tab, int K,
+                                                               const int32_t* parent,
+                                                               int64_t stride) {
+  __shared__ u32x4_t column[BEAMS * THREADS];
+  __shared__ int from[BEAMS];
+  __shared__ int read[BEAMS], moved[BEAMS], n_read, n_moved;
+  int at = tab.n - 1;
+  while (at > 0 && tab.first[at] > blockIdx.x) --at;
+  const BeamState t = tab.t[at];
+  const uint32_t w = blockIdx.x - tab.first[at];
+  const int64_t b = w / t.blocks;
+  for (int k = threadIdx.x; k < K; k += THREADS) {
+    const int f = parent[b * stride + k];
+    from[k] = f >= 0 && f < K ? f : k;  // no such beam: the row stays
+  }
+  __syncthreads();
+  // the rows that are read and those that are written, in order
+  if (threadIdx.x < 64) {
+    int nr = 0, nm = 0;
+    for (int k0 = 0; k0 < K; k0 += 64) {
+      const int k = k0 + (int)threadIdx.x;
+      const bool mv = k < K && from[k] != k;
+      bool rd = false;
+      for (int j = 0; j < K; ++j) rd |= from[j] == k && j != k;
+      const uint64_t r = __ballot(k < K && rd), m = __ballot(mv);
+      const uint64_t before = ((uint64_t)1 << threadIdx.x) - 1;
+      if (k < K && rd) read[nr + __builtin_popcountll(r & before)] = k;
+      if (mv) moved[nm + __builtin_popcountll(m & before)] = k;
+      nr += __builtin_popcountll(r);
+      nm += __builtin_popcountll(m);
+    }
+    if (threadIdx.x == 0) {
+      n_read = nr;
+      n_moved = nm;
+    }
+  }
+  __syncthreads();
+  const int64_t whole = t.inner / kColumn, per = whole + t.inner % kColumn;
+  const int64_t c = (int64_t)(w - (uint32_t)b * t.blocks) * THREADS + threadIdx.x;
+  if (c >= per * t.outer) return;
+  const int64_t o = c / per, x = c - o * per;
+  char* const base = t.data + b * t.stride_batch + o * t.stride_outer;
+  u32x4_t* const mine = column + threadIdx.x;
+  const int nr = n_read, nm = n_moved;
+  if (x < whole) {
+    char* const q = base + x * kColumn;
+    for (int i = 0; i < nr; i += 4) {
+      int k[4];
+      u32x4_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // past the end the last row again
+        k[j] = read[i + j < nr ? i + j : nr - 1];
+        __builtin_memcpy(&v[j], q + k[j] * t.stride_beam, 16);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mine[k[j] * THREADS] = v[j];
+    }
+    for (int i = 0; i < nm; ++i) {
+      const int k = moved[i];
+      const u32x4_t v = mine[from[k] * THREADS];
+      __builtin_memcpy(q + k * t.stride_beam, &v, 16);
+    }
+  } else {
+    char* const q = base + whole * kColumn + (x - whole);
+    for (int i = 0; i < nr; ++i)
+      *reinterpret_cast<char*>(&mine[read[i] * THREADS]) = q[read[i] * t.stride_beam];
+    for (int i = 0; i < nm; ++i)
+      q[moved[i] * t.stride_beam] = *reinterpret_cast<const char*>(&mine[from[moved[i]] * THREADS]);
+  }
+}
+
+template <int THREADS, int BEAMS>
+hipError_t reorder(const BeamTable& tab, uint32_t blocks, int K, const int32_t* parent,
+                   int64_t stride, hipStream_t stream) {
+  hipLaunchKernelGGL((beam_reorder_kernel<THREADS, BEAMS>), dim3(blocks), dim3(THREADS), 0,
+                     stream, tab, K, parent, stride);
+  return hipGetLastError();
+}
+
+inline int reorder_threads(int64_t K) { return K <= 8 ? 256 : K <= 32 ? 128 : 64; }
+
+}  // namespace
+
+bool beam_size_ok(int64_t B, int64_t K, int64_t V) {
+  if (K > kBeamMost || V > (int64_t)1 << 28 || B >= (int64_t)1 << 22) return false;
+  const int64_t segs = (V + kSeg - 1) / kSeg;
+  // places of segments and groups of a request in 31 bits, workgroups below 2^31
+  return K * segs <= (int64_t)1 << 23 && B * K < (int64_t)1 << 22 &&
+         B * K * segs < (int64_t)1 << 31;
+}
+
+size_t beam_workspace_bytes(int64_t B, int64_t K, int64_t V) {
+  const int64_t n = B * K * ((V + kSeg - 1) / kSeg);
+  return (size_t)(n * (8 + 4 + 4 * kMostGroups) + 512);
+}
+
+hipError_t launch_beam_step(BeamParams p, int dtype, int64_t B, void* workspace,
+                            hipStream_t stream) {
+  double c = 1.0;
+  for (int i = 0; i < 10; ++i) {
+    p.poly[i] = c;
+    c *= 0.6931471805599453 / (i + 1);
+  }
+  p.segs = (int)((p.V + kSeg - 1) / kSeg);
+  p.n = B * p.K * p.segs;
+  p.seg_sum = static_cast<double*>(workspace);
+  p.seg_max = reinterpret_cast<float*>(p.seg_sum + p.n);
+  p.group_max = p.seg_max + p.n;
+  const dim3 grid = grid2(p.n);
+  if (dtype == 0)
+    hipLaunchKernelGGL(beam_scan_kernel<0>, grid, dim3(kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL(beam_scan_kernel<1>, grid, dim3(kThreads), 0, stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (dtype == 0)
+    hipLaunchKernelGGL(beam_pick_kernel<0>, dim3((unsigned)B), dim3(kPickThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL(beam_pick_kernel<1>, dim3((unsigned)B), dim3(kPickThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_beam_reorder(const vce_beam_state* states, int64_t count, int64_t B, int64_t K,
+                               const int32_t* parent, int64_t stride, hipStream_t stream) {
+  const int threads = reorder_threads(K);
+  int64_t at = 0;
+  while (at < count) {
+    BeamTable tab;
+    tab.n = 0;
+    uint64_t blocks = 0;
+    for (; at < count && tab.n < kBeamTensors; ++at) {
+      const vce_beam_state& s = states[at];
+      if (s.inner == 0 || s.outer == 0) continue;
+      const int64_t cols = s.outer * (s.inner / kColumn + s.inner % kColumn);
+      const uint64_t per = (uint64_t)((cols + threads - 1) / threads);
+      // below 2^32 threads a launch (a state alone: see the check of its size)
+      if (tab.n > 0 && (blocks + per * B) * threads >= (uint64_t)1 << 32) break;
+      BeamState& t = tab.t[tab.n];
+      t = BeamState{static_cast<char*>(s.data), s.inner, s.outer, s.stride_outer, s.stride_beam,
+                    s.stride_batch, (uint32_t)per};
+      tab.first[tab.n++] = (uint32_t)blocks;
+      blocks += per * B;
+    }
+    if (tab.n == 0) break;
+    const uint32_t n = (uint32_t)blocks;
+    const hipError_t e =
+        threads == 256 ? reorder<256, 8>(tab, n, (int)K, parent, stride, stream)
+        : threads == 128 ? reorder<128, 32>(tab, n, (int)K, parent, stride, stream)
+                         : reorder<64, kBeamMost>(tab, n, (int)K, parent, stride, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace vce

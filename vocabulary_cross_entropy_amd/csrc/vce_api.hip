@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "adamw.h"
+#include "beam.h"
 #include "vce.h"
 #include "vce_internal.h"
 
@@ -1301,6 +1302,149 @@ int grad_norm(const vce_grad_tensor* tensors, int64_t count, double max_norm, fl
   return launch_status(vce::launch_grad_norm(tensors, count, max_norm, norm, scale,
                                              static_cast<double*>(workspace),
                                              static_cast<hipStream_t>(stream)));
+}
+
+size_t beam_workspace_size(int64_t B, int64_t K, int64_t V) {
+  if (B < 0 || K <= 0 || V <= 0 || !vce::beam_size_ok(B, K, V)) return 0;
+  return vce::beam_workspace_bytes(B, K, V);
+}
+
+int beam_step(const void* logits, int dtype, int64_t B, int64_t K, int64_t V, int64_t ls0,
+              int64_t ls1, const float* scores, const uint8_t* ended, int64_t end_token,
+              int64_t n_out, float* score, int32_t* parent, int64_t* token, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype)) return VCE_EDTYPE;
+  if (B < 0 || K <= 0 || V <= 0 || ls0 < 0 || ls1 < 0 || n_out < 1) return VCE_EINVAL;
+  if (ended && (end_token < 0 || end_token >= V)) return VCE_EINVAL;
+  if (!vce::beam_size_ok(B, K, V) || n_out > vce::kBeamOutMost) return VCE_EUNSUPPORTED;
+  if (B == 0) return VCE_OK;
+  if (!logits || !scores || !score || !parent || !token || !workspace) return VCE_EINVAL;
+  const int64_t es = dtype_size(dtype);
+  int64_t span0, span1;
+  if (!mul_ok(B - 1, ls0, &span0) || !mul_ok(K - 1, ls1, &span1)) return VCE_EINVAL;
+  if (span0 > INT64_MAX / 8 || span1 > INT64_MAX / 8 - V - span0) return VCE_EINVAL;
+  if (!aligned(logits, es) || !aligned(scores, 4) || !aligned(score, 4) || !aligned(parent, 4) ||
+      !aligned(token, 8) || !aligned(workspace, 256))
+    return VCE_EALIGN;
+  const size_t need = beam_workspace_size(B, K, V);
+  if (workspace_bytes < need) return VCE_EWORKSPACE;
+  const Range in[3] = {range(logits, (span0 + span1 + V) * es), range(scores, B * K * 4),
+                       range(ended, B * K)};
+  const Range out[4] = {range(score, B * n_out * 4), range(parent, B * n_out * 4),
+                        range(token, B * n_out * 8), range(workspace, (int64_t)need)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return VCE_EALIAS;
+    for (int j = 0; j < 3; ++j)
+      if (overlap(out[i], in[j])) return VCE_EALIAS;
+  }
+  vce::BeamParams p;
+  p.logits = logits;
+  p.K = K;
+  p.V = V;
+  p.ls0 = ls0;
+  p.ls1 = ls1;
+  p.scores = scores;
+  p.ended = ended;
+  p.end_token = end_token;
+  p.n_out = (int)n_out;
+  p.score = score;
+  p.parent = parent;
+  p.token = token;
+  return launch_status(
+      vce::launch_beam_step(p, dtype, B, workspace, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+struct Axis {
+  int64_t n, stride;
+};
+
+// The strided pieces of one state: its axes by stride (those of one entry left out), the
+// bytes from its first to past its last, and whether pieces overlap.
+struct Pieces {
+  Axis axis[3];
+  int axes;
+  int64_t bytes;
+  bool apart;
+};
+
+inline bool pieces_of(const vce_beam_state& s, int64_t B, int64_t K, Pieces* p) {
+  const Axis all[3] = {{s.outer, s.stride_outer}, {K, s.stride_beam}, {B, s.stride_batch}};
+  p->axes = 0;
+  for (const Axis& a : all) {
+    if (a.n == 1) continue;
+    int at = p->axes++;
+    for (; at > 0 && p->axis[at - 1].stride > a.stride; --at) p->axis[at] = p->axis[at - 1];
+    p->axis[at] = a;
+  }
+  p->bytes = s.inner;
+  p->apart = true;
+  for (int i = 0; i < p->axes; ++i) {
+    int64_t t;
+    if (p->axis[i].stride < p->bytes) p->apart = false;
+    if (!mul_ok(p->axis[i].n - 1, p->axis[i].stride, &t) || t > ((int64_t)1 << 60) - p->bytes)
+      return false;
+    p->bytes += t;
+  }
+  return true;
+}
+
+// May a piece of one state share a byte with one of the other?
+inline bool pieces_meet(const vce_beam_state& a, const Pieces& pa, const vce_beam_state& b,
+                        const Pieces& pb) {
+  if (!overlap(range(a.data, pa.bytes), range(b.data, pb.bytes))) return false;
+  if (pa.axes == 0 || pa.axes != pb.axes) return true;
+  // one comb of teeth apart by the least stride: the other's pieces lie between its teeth
+  const int64_t s = pa.axis[0].stride;
+  for (int i = 0; i < pa.axes; ++i)
+    if (pa.axis[i].stride != pb.axis[i].stride || pa.axis[i].stride % s != 0) return true;
+  const uintptr_t lo = std::min((uintptr_t)a.data, (uintptr_t)b.data);
+  const int64_t oa = (int64_t)(((uintptr_t)a.data - lo) % (uintptr_t)s);
+  const int64_t ob = (int64_t)(((uintptr_t)b.data - lo) % (uintptr_t)s);
+  // from each tooth to the next of the other, around the comb
+  const int64_t d = ob >= oa ? ob - oa : ob - oa + s;
+  return d < a.inner || s - d < b.inner;
+}
+
+}  // namespace
+
+int beam_reorder(const vce_beam_state* states, int64_t count, int64_t B, int64_t K,
+                 const int32_t* parent, int64_t parent_stride, void* stream) {
+  if (count < 0 || B < 0 || K <= 0 || parent_stride < 0) return VCE_EINVAL;
+  if (K > vce::kBeamMost || B >= ((int64_t)1 << 22) || count > 1024) return VCE_EUNSUPPORTED;
+  if (B == 0 || count == 0) return VCE_OK;
+  if (!states || !parent) return VCE_EINVAL;
+  if (!aligned(parent, 4)) return VCE_EALIGN;
+  int64_t span;
+  if (!mul_ok(B - 1, parent_stride, &span) || span > INT64_MAX / 8 - K) return VCE_EINVAL;
+  const Range pr = range(parent, (span + K) * 4);
+  for (int64_t i = 0; i < count; ++i) {
+    const vce_beam_state& s = states[i];
+    if (s.inner < 0 || s.outer < 0 || s.stride_outer < 0 || s.stride_beam < 0 ||
+        s.stride_batch < 0)
+      return VCE_EINVAL;
+    if (s.inner == 0 || s.outer == 0) continue;
+    if (!s.data) return VCE_EINVAL;
+    if (s.inner > ((int64_t)1 << 40) || s.outer > ((int64_t)1 << 40)) return VCE_EUNSUPPORTED;
+    int64_t cols;
+    if (!mul_ok(s.outer, s.inner / 16 + s.inner % 16, &cols) ||
+        cols / 64 + 1 > (((int64_t)1 << 24) - 1) / B)  // workgroups of one state
+      return VCE_EUNSUPPORTED;
+    Pieces p;
+    if (!pieces_of(s, B, K, &p)) return VCE_EINVAL;
+    if (!p.apart || overlap(pr, range(s.data, p.bytes))) return VCE_EALIAS;
+    for (int64_t j = 0; j < i; ++j) {
+      const vce_beam_state& t = states[j];
+      if (t.inner == 0 || t.outer == 0) continue;
+      Pieces q;
+      pieces_of(t, B, K, &q);
+      if (pieces_meet(s, p, t, q)) return VCE_EALIAS;
+    }
+  }
+  return launch_status(vce::launch_beam_reorder(states, count, B, K, parent, parent_stride,
+                                                static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
