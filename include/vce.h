@@ -741,6 +741,56 @@ int beam_step(const void* logits, int dtype, int64_t B, int64_t K, int64_t V, in
 int beam_reorder(const vce_beam_state* states, int64_t count, int64_t B, int64_t K,
                  const int32_t* parent, int64_t parent_stride, void* stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared projection.  Token i has adapter k =
+ * adapter[i] of n (a number outside 0 .. n - 1: none), of scale s_k:
+ *     y_i = x_i W^T + s_k (x_i A_k^T) B_k^T
+ * All operands BF16, FP32 accumulation; the r numbers between A and B are FP32 (for a BF16
+ * result kept to 2^-16), so a result is rounded once.  Adapters of smaller rank are filled up with zeros.
+ *
+ *  lora_forward
+ *   x        (M, H), row i at element i * ldx (ldx >= H, a multiple of 8 up to 2^22; 16-byte
+ *            aligned).  M up to 2^21, H a multiple of 8 up to 2^20, V up to 2^22, n up to 1024, r a
+ *            multiple of 8 up to 128 (VCE_EUNSUPPORTED).
+ *   a, b     (n, r, H) and (n, V, r), contiguous, 16-byte aligned.   adapter (M) int32.
+ *   scale    (n) FP32, or NULL for 1.
+ *   w        (V, H), contiguous, 16-byte aligned, or NULL.
+ *   base     (M, V) of `dtype`, row i at element i * ldb, or NULL: what the shared projection has
+ *            given already (mx_logits), in the place of x W^T.  Not with w (VCE_EINVAL).
+ *   out      (M, V) of `dtype` (FP32 or BF16), row i at element i * ldo; ldb, ldo >= V.  It may be
+ *            base itself (with ldo = ldb); any other overlap is VCE_EALIAS.
+ *   workspace  lora_forward_workspace_size(M, H, V, n, r) bytes, 256-byte aligned; its contents
+ *            need not survive.  Calls that may overlap in time each need their own.
+ *  An infinity or a NaN in an adapter's weights reaches the tokens of that adapter only (as an
+ *  infinity or a NaN).  A token's result does not depend on which adapters the others have, but
+ *  between different M it may differ by the order of its FP32 sums.
+ *
+ *  lora_backward: from dy, the gradient of y, with ds_i = s_k dy_i B_k:
+ *     dx_i = dy_i W + ds_i A_k,   dA_k = sum_i ds_i^T x_i,   dB_k = sum_i dy_i^T s_k (x_i A_k^T)
+ *   over the tokens i of adapter k, in a fixed order; W itself is frozen.
+ *   dy       (M, V) of `dtype`, row i at element i * ldy, aligned to its element (ce_backward's
+ *            gradient).  FP32 enters da and db whole and the BF16 dx to 2^-16.  BF16 rows of a multiple of 8
+ *            that are 16-byte aligned are read in place by the product with W, others are laid out
+ *            anew in the workspace.
+ *   dx_base  (M, H) BF16, contiguous, or NULL: in the place of dy W where w is NULL.
+ *   dx       (M, H) BF16, contiguous, 16-byte aligned, or NULL (not wanted); may be dx_base.
+ *   da, db   (n, r, H) and (n, V, r) FP32, 16-byte aligned, overwritten (zeros for an adapter without
+ *            tokens), either NULL where it is not wanted.
+ *   workspace  lora_backward_workspace_size(M, H, V, n, r, dtype) bytes, as above.
+ */
+size_t lora_forward_workspace_size(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r);
+int lora_forward(const void* x, int64_t ldx, int64_t M, int64_t H, int64_t V, const void* a,
+                 const void* b, int64_t n, int64_t r, const int32_t* adapter, const float* scale,
+                 const void* w, const void* base, int64_t ldb, void* out, int dtype, int64_t ldo,
+                 void* workspace, size_t workspace_bytes, void* stream);
+size_t lora_backward_workspace_size(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r,
+                                    int dtype);
+int lora_backward(const void* dy, int dtype, int64_t ldy, const void* x, int64_t ldx, int64_t M,
+                  int64_t H, int64_t V, const void* a, const void* b, int64_t n, int64_t r,
+                  const int32_t* adapter, const float* scale, const void* w, const void* dx_base,
+                  void* dx, float* da, float* db, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

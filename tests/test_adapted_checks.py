@@ -275,3 +275,121 @@ def test_beam_pieces():
     assert f(t[..., :3], "t") == (12, 200, 32, 6400, 19200)
     assert f(torch.zeros((2, 3)), "t") == (4, 1, 0, 4, 12)
     assert f(torch.zeros((2, 3, 0, 5)), "t")[0] == 0
+
+
+# ---- adapters ----------------------------------------------------------------------
+
+def lfwd(L, **kw):
+    a = dict(x=A, ldx=64, M=4, H=64, V=100, a=A + G, b=A + 2 * G, n=3, r=16, k=A + 3 * G,
+             s=A + 4 * G, w=A + 5 * G, base=None, ldb=0, out=A + 6 * G, dt=1, ldo=100,
+             ws=A + 7 * G, wb=1 << 20)
+    a.update(kw)
+    return L.lora_forward(a["x"], a["ldx"], a["M"], a["H"], a["V"], a["a"], a["b"], a["n"],
+                          a["r"], a["k"], a["s"], a["w"], a["base"], a["ldb"], a["out"], a["dt"],
+                          a["ldo"], a["ws"], a["wb"], None)
+
+
+COMMON = [
+    (dict(M=-1), 1), (dict(H=0), 1), (dict(V=0), 1), (dict(n=0), 1), (dict(r=0), 1),
+    (dict(H=68), 7), (dict(r=12), 7), (dict(r=136), 7), (dict(n=1025), 7),
+    (dict(M=(1 << 21) + 1), 7), (dict(H=(1 << 20) + 8), 7), (dict(V=(1 << 22) + 1), 7),
+    (dict(dt=2), 2), (dict(ldx=56), 1), (dict(ldx=68), 7), (dict(ldx=(1 << 22) + 8), 7),
+    (dict(x=None), 1), (dict(a=None), 1), (dict(b=None), 1), (dict(k=None), 1), (dict(ws=None), 1),
+    (dict(x=A + 8), 3), (dict(a=A + G + 8), 3), (dict(b=A + 2 * G + 2), 3),
+    (dict(k=A + 3 * G + 2), 3), (dict(s=A + 4 * G + 1), 3), (dict(w=A + 5 * G + 8), 3),
+    (dict(ws=A + 7 * G + 64), 3), (dict(wb=100), 5), (dict(ws=A), 4), (dict(ws=A + 5 * G), 4),
+]
+
+
+@pytest.mark.parametrize("kw,code", COMMON + [
+    (dict(base=A + 8 * G, ldb=100), 1), (dict(w=None, base=A + 8 * G, ldb=99), 1),
+    (dict(ldo=99), 1), (dict(ldo=1 << 62), 1), (dict(out=None), 1), (dict(out=A + 6 * G + 1), 3),
+    (dict(w=None, base=A + 8 * G + 1, ldb=100), 3), (dict(out=A), 4), (dict(out=A + G), 4),
+    (dict(out=A + 2 * G + 9598), 4), (dict(out=A + 3 * G), 4), (dict(out=A + 4 * G), 4),
+    (dict(out=A + 5 * G), 4), (dict(out=A + 7 * G), 4),
+    (dict(w=None, base=A + 6 * G, ldb=104, ldo=100), 4),
+    (dict(w=None, base=A + 6 * G + 2, ldb=100), 4), (dict(w=None, base=A + 7 * G, ldb=100), 4),
+    (dict(M=0), 0), (dict(M=0, x=None, k=None, out=None, ws=None), 0),
+])
+def test_lora_forward_rejects(L, kw, code):
+    assert lfwd(L, **kw) == code
+
+
+def lbwd(L, **kw):
+    a = dict(dy=A + 8 * G, dt=1, ldy=100, x=A, ldx=64, M=4, H=64, V=100, a=A + G, b=A + 2 * G,
+             n=3, r=16, k=A + 3 * G, s=A + 4 * G, w=A + 5 * G, base=None, dx=A + 6 * G,
+             da=A + 9 * G, db=A + 10 * G, ws=A + 7 * G, wb=1 << 20)
+    a.update(kw)
+    return L.lora_backward(a["dy"], a["dt"], a["ldy"], a["x"], a["ldx"], a["M"], a["H"], a["V"],
+                           a["a"], a["b"], a["n"], a["r"], a["k"], a["s"], a["w"], a["base"],
+                           a["dx"], a["da"], a["db"], a["ws"], a["wb"], None)
+
+
+@pytest.mark.parametrize("kw,code", COMMON + [
+    (dict(base=A + 11 * G), 1), (dict(ldy=99), 1), (dict(ldy=1 << 62), 1), (dict(dy=None), 1),
+    (dict(dy=A + 8 * G + 1), 3), (dict(dt=0, dy=A + 8 * G + 2), 3), (dict(dx=A + 6 * G + 8), 3),
+    (dict(da=A + 9 * G + 8), 3), (dict(db=A + 10 * G + 4), 3),
+    (dict(w=None, base=A + 11 * G + 8), 3), (dict(dx=A + 8 * G), 4), (dict(dx=A), 4),
+    (dict(da=A + G), 4), (dict(db=A + 8 * G + 784), 4), (dict(da=A + 10 * G), 4),
+    (dict(ws=A + 8 * G), 4), (dict(w=None, base=A + 6 * G + 16), 4),
+    (dict(w=None, base=A + 9 * G), 4), (dict(dx=None, da=None, db=None), 0),
+    (dict(M=0, da=None, db=None), 0),
+])
+def test_lora_backward_rejects(L, kw, code):
+    assert lbwd(L, **kw) == code
+
+
+def test_lora_workspace_sizes(L):
+    f, g = L.lora_forward_workspace_size, L.lora_backward_workspace_size
+    for bad in ((-1, 64, 100, 3, 16), (4, 0, 100, 3, 16), (4, 64, 0, 3, 16), (4, 64, 100, 0, 16),
+                (4, 64, 100, 3, 12), (4, 60, 100, 3, 16)):
+        assert f(*bad) == 0 and g(*bad, 1) == 0
+    assert g(4, 64, 100, 3, 16, 2) == 0
+    assert f(0, 64, 100, 3, 16) > 0 and g(0, 64, 100, 3, 16, 1) > 0
+    assert g(1000, 64, 4096, 3, 16, 0) >= g(1000, 64, 4096, 3, 16, 1) + 1000 * 4096 * 2
+
+
+BF = torch.bfloat16
+LX, LA, LB = torch.zeros((4, 64), dtype=BF), torch.zeros((3, 16, 64), dtype=BF), \
+    torch.zeros((3, 100, 16), dtype=BF)
+LK, LW = torch.zeros(4, dtype=torch.int32), torch.zeros((100, 64), dtype=BF)
+LY = torch.zeros((4, 100), dtype=BF)
+BAD_LORA = [
+    (dict(x=LX.float()), TypeError, "x must be bfloat16"),
+    (dict(a=LA.float()), TypeError, "a must be bfloat16"),
+    (dict(a=LA[:, :, :56].contiguous()), ValueError, "a must be"),
+    (dict(b=LB[:2]), ValueError, "a must be"), (dict(b=LB[:, :, :8].contiguous()), ValueError, "a must"),
+    (dict(a=LA.transpose(1, 2).contiguous().transpose(1, 2)), ValueError, "a must be contiguous"),
+    (dict(k=LK.long()), ValueError, "adapter must be"), (dict(k=LK[:3]), ValueError, "adapter must"),
+    (dict(scale=torch.zeros(4)), ValueError, "scale must be"),
+    (dict(w=LW[:50]), ValueError, "w must be"), (dict(w=LW.float()), ValueError, "w must be"),
+    (dict(workspace=torch.zeros(8)), TypeError, "workspace"),
+    (dict(), *GPU_ONLY),
+]
+
+
+@pytest.mark.parametrize("kw,err,text", BAD_LORA + [
+    (dict(base=LY), ValueError, "not both"), (dict(dtype=torch.float16), TypeError, "float32 or"),
+    (dict(w=None, base=LY.float(), out=LY), ValueError, "base must be"),
+    (dict(w=None, base=LY[:, :99]), ValueError, "base must be"),
+    (dict(out=LY.t().contiguous().t()), ValueError, "contiguous"),
+])
+def test_binding_lora_forward(kw, err, text):
+    a = dict(x=LX, a=LA, b=LB, k=LK, w=LW)
+    a.update(kw)
+    with pytest.raises(err, match=text):
+        vce.lora_forward(a.pop("x"), a.pop("a"), a.pop("b"), a.pop("k"), a.pop("w"), **a)
+
+
+@pytest.mark.parametrize("kw,err,text", BAD_LORA + [
+    (dict(dx_base=LX), ValueError, "not both"), (dict(dy=LY.half()), TypeError, "dy must be"),
+    (dict(dy=LY[:, :99]), ValueError, "dy must be"), (dict(out=(None, None)), ValueError, "3 tensors"),
+    (dict(out=(None, LA.float(), LB)), ValueError, "db must be"),
+    (dict(w=None, dx_base=LX.float()), ValueError, "dx_base must be"),
+])
+def test_binding_lora_backward(kw, err, text):
+    a = dict(dy=LY, x=LX, a=LA, b=LB, k=LK, w=LW)
+    a.update(kw)
+    with pytest.raises(err, match=text):
+        vce.lora_backward(a.pop("dy"), a.pop("x"), a.pop("a"), a.pop("b"), a.pop("k"),
+                          a.pop("w"), **a)

@@ -88,6 +88,12 @@ SIGNATURES = {
     "beam_step": (_I32, [_VP, _I32, _I64, _I64, _I64, _I64, _I64, _VP, _VP, _I64, _I64, _VP, _VP,
                          _VP, _VP, _SZ, _VP]),
     "beam_reorder": (_I32, [_VP, _I64, _I64, _I64, _VP, _I64, _VP]),
+    "lora_forward_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "lora_forward": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP,
+                            _I64, _VP, _I32, _I64, _VP, _SZ, _VP]),
+    "lora_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I32]),
+    "lora_backward": (_I32, [_VP, _I32, _I64, _VP, _I64, _I64, _I64, _I64, _VP, _VP, _I64, _I64,
+                             _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
 }
 
 _lib = None
@@ -1311,3 +1317,124 @@ def beam_reorder(states, parent: torch.Tensor, *, stream=None) -> None:
                                                   parent.stride(0), s))
     if K > 0:
         _on_stream(parent, stream, call)
+
+
+def lora_forward_workspace_size(M: int, H: int, V: int, n: int, r: int) -> int:
+    return int(lib().lora_forward_workspace_size(M, H, V, n, r))
+
+
+def lora_forward_workspace(M: int, H: int, V: int, n: int, r: int, device="cuda") -> torch.Tensor:
+    size = lora_forward_workspace_size(M, H, V, n, r)
+    if size == 0:
+        raise ValueError(f"no workspace plan for M={M}, H={H}, V={V}, n={n}, r={r}")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def lora_backward_workspace_size(M: int, H: int, V: int, n: int, r: int,
+                                 dtype: torch.dtype = torch.bfloat16) -> int:
+    code = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_FP32
+    return int(lib().lora_backward_workspace_size(M, H, V, n, r, code))
+
+
+def lora_backward_workspace(M: int, H: int, V: int, n: int, r: int,
+                            dtype: torch.dtype = torch.bfloat16, device="cuda") -> torch.Tensor:
+    size = lora_backward_workspace_size(M, H, V, n, r, dtype)
+    if size == 0:
+        raise ValueError(f"no workspace plan for M={M}, H={H}, V={V}, n={n}, r={r}")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _check_lora(x, a, b, adapter, w, base, scale, workspace):
+    """(M, H, V, n, r, ldx) of an adapter call."""
+    for t, name in ((x, "x"), (a, "a"), (b, "b")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    M, H, ldx = _rows2d(x, "x")
+    if a.dim() != 3 or b.dim() != 3 or a.shape[2] != H or b.shape[0] != a.shape[0] or \
+            b.shape[2] != a.shape[1]:
+        raise ValueError(f"a must be (n, r, {H}) and b (n, V, r), got {tuple(a.shape)} and "
+                         f"{tuple(b.shape)}")
+    n, r, V = a.shape[0], a.shape[1], b.shape[1]
+    _check_out(a, "a", a.shape, torch.bfloat16, x)
+    _check_out(b, "b", b.shape, torch.bfloat16, x)
+    _check_out(adapter, "adapter", (M,), torch.int32, x)
+    _check_out(scale, "scale", (n,), torch.float32, x)
+    _check_out(w, "w", (V, H), torch.bfloat16, x)
+    if w is not None and base is not None:
+        raise ValueError("either w or what it has given already, not both")
+    if workspace is not None:
+        _check_buf(workspace, "workspace", workspace.numel(), torch.uint8, like=x)
+    return M, H, V, n, r, ldx
+
+
+def _check_rows_of(t, name, shape, dtype, ref):
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                         f"{tuple(t.shape)}")
+    if t.device != ref.device:
+        raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+    return _rows2d(t, name)[2]
+
+
+def lora_forward(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: torch.Tensor,
+                 w: torch.Tensor | None = None, *, base: torch.Tensor | None = None,
+                 scale: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """x W^T + scale[k] (x A_k^T) B_k^T (M, V) for tokens x (M, H), each with its adapter k =
+    adapter[i] (int32; outside 0 .. n - 1: none) of a (n, r, H) and b (n, V, r), all BF16; r a
+    multiple of 8 up to 128.  ``base`` (M, V): what the shared projection has given already, in the
+    place of w; neither: the adapters' share alone.  Result in ``dtype`` (``base``'s and ``out``'s
+    where given), BF16 or FP32; ``out`` may have padded rows and may be ``base``."""
+    M, H, V, n, r, ldx = _check_lora(x, a, b, adapter, w, base, scale, workspace)
+    dtype = out.dtype if out is not None else base.dtype if base is not None else dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    ldb = _check_rows_of(base, "base", (M, V), dtype, x)
+    _check_rows_of(out, "out", (M, V), dtype, x)
+
+    def call(s):
+        o = x.new_empty((M, V), dtype=dtype) if out is None else out
+        ws = lora_forward_workspace(M, H, V, n, r, x.device) if workspace is None else workspace
+        _check("lora_forward", lib().lora_forward(
+            _at(x), ldx, M, H, V, _at(a), _at(b), n, r, _at(adapter), _at(scale), _at(w),
+            _at(base), ldb, _at(o), _elem_dtype(o, "out"), o.stride(0), _at(ws), ws.numel(), s))
+        return o
+    return _on_stream(x, stream, call)
+
+
+def lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                  adapter: torch.Tensor, w: torch.Tensor | None = None, *,
+                  dx_base: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                  need_dx: bool = True, need_adapters: bool = True, out=None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of ``lora_forward`` from dy (M, V), BF16 or FP32: (dx, da, db), dx (M, H) BF16 =
+    dy W + ds A_k (``dx_base`` in the place of dy W where the shared projection lies elsewhere), da
+    (n, r, H) and db (n, V, r) FP32, zeros for adapters without tokens; None for what is not
+    needed.  W is frozen.  ``out`` gives the three (None entries are allocated); dx may be
+    dx_base."""
+    M, H, V, n, r, ldx = _check_lora(x, a, b, adapter, w, dx_base, scale, workspace)
+    dt = _elem_dtype(dy, "dy")
+    ldy = _check_rows_of(dy, "dy", (M, V), dy.dtype, x)
+    _check_out(dx_base, "dx_base", (M, H), torch.bfloat16, x)
+    outs = (None,) * 3 if out is None else out
+    if len(outs) != 3:
+        raise ValueError("out must hold 3 tensors (None to allocate)")
+    shapes = (((M, H), torch.bfloat16), ((n, r, H), torch.float32), ((n, V, r), torch.float32))
+    for t, name, (shape, td) in zip(outs, ("dx", "da", "db"), shapes):
+        _check_out(t, name, shape, td, x)
+
+    def call(s):
+        need = (need_dx, need_adapters, need_adapters)
+        dx, da, db = (x.new_empty(shape, dtype=td) if t is None and wanted else t
+                      for t, wanted, (shape, td) in zip(outs, need, shapes))
+        ws = workspace
+        if ws is None:
+            ws = lora_backward_workspace(M, H, V, n, r, dy.dtype, x.device)
+        _check("lora_backward", lib().lora_backward(
+            _at(dy), dt, ldy, _at(x), ldx, M, H, V, _at(a), _at(b), n, r, _at(adapter),
+            _at(scale), _at(w), _at(dx_base), _at(dx), _at(da), _at(db), _at(ws), ws.numel(), s))
+        return dx, da, db
+    return _on_stream(x, stream, call)

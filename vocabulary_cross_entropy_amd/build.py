@@ -15,7 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libvce.so")
 SOURCES = ["vce_api.hip", "ce_kernels.hip", "lce_kernels.hip", "rms_kernels.hip",
            "mx_kernels.hip", "mx_gemm_kernels.hip", "sample_kernels.hip", "adamw_kernels.hip",
-           "beam_kernels.hip"]
+           "beam_kernels.hip", "lora_kernels.hip"]
 ARCH = "gfx950"
 
 

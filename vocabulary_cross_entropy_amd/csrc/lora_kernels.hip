@@ -1,0 +1,1273 @@
+// Low-rank adapters of many requests beside a shared projection:
+//   y_i  = x_i W^T + s_k (x_i A_k^T) B_k^T,   k the adapter of token i (or none)
+//   ds_i = s_k dy_i B_k,  dx_i = dy_i W + ds_i A_k
+//   dA_k = sum_i ds_i^T x_i,  dB_k = sum_i dy_i^T s_i,  s_i = s_k x_i A_k^T
+// over the tokens i that have adapter k.
+//
+// The r numbers per token, s and ds, are FP32 sums and go into the matrix unit as BF16
+// parts, each the rounded rest of the ones before: three parts hold an FP32 number (to 2^-24),
+// two, enough for a BF16 result, to 2^-16.
+//
+//  * Tokens in their own order: the product with W and the adapters' share of it.  A tile's
+//    epilogue walks the adapters that its tokens have and multiplies those tokens' s by B_k,
+//    32 rows at a time, into the same accumulators; a token takes only its own adapter's
+//    product (a select, where a block of tokens is mixed, so that an infinity in one
+//    adapter's weights cannot reach another's tokens).
+//  * Tokens sorted by adapter (lora_plan_kernel: places of 32, each of one adapter): s and ds,
+//    and the adapters' gradients, which sum over the tokens of one adapter.
+#include "gemm_core.h"
+#include "lora.h"
+
+namespace vce {
+
+namespace {
+
+constexpr int kTile = 32;  // sorted places of one adapter
+
+__device__ __forceinline__ bf16x8_t as_bf16x8(const u32x4_t& v) {
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+__device__ __forceinline__ u32x4_t load16(const void* p) {
+  u32x4_t v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
+constexpr int kParts = 3;  // of s and ds, as they are stored
+
+// v in BF16 parts.  A part of an infinity or a NaN behind the first is 0.
+__device__ __forceinline__ void parts_of(float v, uint16_t* part) {
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    part[i] = to_bf16(v);
+    v -= from_bf16(part[i]);
+    v = v == v ? v : 0.0f;
+  }
+}
+
+// ---- the plan ------------------------------------------------------------------------
+
+// order[place]: the token there, -1 for none; first[k] .. first[k + 1]: the tiles of adapter k;
+// owner[tile].  One workgroup; a wavefront counts and then places its own contiguous
+// share of the tokens, so the order within an adapter is the tokens'.
+struct LoraPlan {
+  int32_t* order;
+  int32_t* first;
+  int32_t* owner;
+};
+
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+
+// f(k, lanes that have adapter k) for the adapters among 64 ids (negative: none).
+template <class F>
+__device__ __forceinline__ void each_adapter(int id, F f) {
+  uint64_t left = __ballot(id >= 0);
+  while (left) {
+    const int k = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    const uint64_t match = __ballot(id == k);
+    left &= ~match;
+    f(k, match);
+  }
+}
+
+__device__ __forceinline__ int adapter_of(const int32_t* adapter, int64_t i, int64_t M, int n) {
+  if (i >= M) return -1;
+  const int k = adapter[i];
+  return k >= 0 && k < n ? k : -1;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* adapter, int64_t M,
+                                                                 int n, LoraPlan plan) {
+  // read and written by the lanes of one wavefront in turn
+  __shared__ volatile int32_t count[kPlanWaves][kLoraAdapters];
+  __shared__ int32_t tiles[kLoraAdapters];
+  __shared__ int32_t part[kPlanWaves];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  for (int i = t; i < kPlanWaves * n; i += kPlanThreads) count[i / n][i % n] = 0;
+  __syncthreads();
+  const int64_t per = (M + kPlanThreads - 1) / kPlanThreads * 64;
+  const int64_t i0 = wave * per, i1 = i0 + per < M ? i0 + per : M;
+  for (int64_t i = i0; i < i1; i += 64)
+    each_adapter(adapter_of(adapter, i + lane, i1, n), [&](int k, uint64_t match) {
+      if (lane == 0) count[wave][k] = count[wave][k] + __builtin_popcountll(match);
+    });
+  __syncthreads();
+  // every adapter's tiles, and their running sum
+  int total = 0, mine = 0;
+  if (t < n) {
+    for (int w = 0; w < kPlanWaves; ++w) total += count[w][t];
+    mine = (total + kTile - 1) / kTile;
+  }
+  int run = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int v = __shfl_up(run, off, 64);
+    if (lane >= off) run += v;
+  }
+  if (lane == 63) part[wave] = run;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) run += part[w];
+  if (t < n) {
+    const int begin = run - mine;
+    tiles[t] = begin;
+    plan.first[t] = begin;
+    if (t == n - 1) plan.first[n] = run;
+    int at = begin * kTile;
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int c = count[w][t];
+      count[w][t] = at;
+      at += c;
+    }
+    for (; at < run * kTile; ++at) plan.order[at] = -1;
+  }
+  __syncthreads();
+  int all = 0;
+  for (int w = 0; w < kPlanWaves; ++w) all += part[w];
+  for (int i = t; i < all; i += kPlanThreads) {
+    int lo = 0, hi = n - 1;  // the last adapter that begins at or before tile i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (tiles[mid] <= i)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    plan.owner[i] = lo;
+  }
+  for (int64_t i = i0; i < i1; i += 64) {
+    const int id = adapter_of(adapter, i + lane, i1, n);
+    each_adapter(id, [&](int k, uint64_t match) {
+      const int at = count[wave][k];
+      if (id == k)
+        plan.order[at + __builtin_popcountll(match & (((uint64_t)1 << lane) - 1))] =
+            (int32_t)(i + lane);
+      if (lane == 0) count[wave][k] = at + __builtin_popcountll(match);
+    });
+  }
+}
+
+// ---- s and ds ----------------------------------------------------------------------------
+
+// Few tokens: a workgroup per token and eight of the r sums.  A lane takes 16 bytes of x and of
+// eight rows of A_k at a time.
+__global__ __launch_bounds__(256) void lora_token_kernel(LoraFwdArgs p, uint16_t* s2) {
+  __shared__ float sh[4][8];
+  const int64_t i = blockIdx.x;
+  const int c0 = blockIdx.y * 8, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int k = adapter_of(p.adapter, i, p.M, p.n);
+  if (k < 0) return;  // nobody reads it
+  const uint16_t* x = p.x + i * p.ldx;
+  const uint16_t* a = p.a + ((int64_t)k * p.r + c0) * p.H;
+  float acc[8] = {};
+  for (int64_t h = threadIdx.x * 8; h < p.H; h += 256 * 8) {
+    const u32x4_t xv = load16(x + h);
+    u32x4_t av[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) av[c] = load16(a + c * p.H + h);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[c] = __builtin_fmaf(bf16_lo(xv[j]), bf16_lo(av[c][j]), acc[c]);
+        acc[c] = __builtin_fmaf(bf16_hi(xv[j]), bf16_hi(av[c][j]), acc[c]);
+      }
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) acc[c] += __shfl_xor(acc[c], off, 64);
+    if (lane == 0) sh[wave][c] = acc[c];
+  }
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    const int c = threadIdx.x;
+    const float v = ((sh[0][c] + sh[1][c]) + (sh[2][c] + sh[3][c])) * (p.scale ? p.scale[k] : 1.0f);
+    uint16_t part[kParts];
+    parts_of(v, part);
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) s2[(i * kParts + q) * p.r + c0 + c] = part[q];
+  }
+}
+
+// Sums over k of a tile's token rows times its adapter's rows: part[split][place][c] =
+// sum over the split's k of X(order[place], k) U_adapter(c, k), X (M, K) and U (n, r, ldu).
+struct ShrinkProblem {
+  const void* x;
+  int64_t ldx, K;
+  const uint16_t* u;
+  int64_t ldu;
+  float* part;
+  int splits;
+  int64_t per;  // k of a split: a multiple of 512
+};
+
+// Eight elements of a row from `at` on, `left` of them before its end and 0 past it, in N BF16
+// parts (one for a BF16 row).
+template <int DT, int N>
+__device__ __forceinline__ void row8(const void* x, int64_t at, int64_t left, u32x4_t (&part)[N]) {
+  if constexpr (DT == 1) {
+    static_assert(N == 1, "BF16 has one part");
+    const uint16_t* q = static_cast<const uint16_t*>(x) + at;
+    if (left >= 8) {
+      part[0] = load16(q);
+    } else {
+      uint32_t e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = j < left ? q[j] : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[0][j] = e[2 * j] | e[2 * j + 1] << 16;
+    }
+  } else {
+    const float* q = static_cast<const float*>(x) + at;
+    float v[8];
+    if (left >= 8) {
+      __builtin_memcpy(v, q, 32);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < left ? q[j] : 0.0f;
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        part[n][j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        // what the part leaves; nothing of an infinity or a NaN, whose difference is NaN
+        const float a = v[2 * j] - bf16_lo(part[n][j]), b = v[2 * j + 1] - bf16_hi(part[n][j]);
+        v[2 * j] = a == a ? a : 0.0f;
+        v[2 * j + 1] = b == b ? b : 0.0f;
+      }
+  }
+}
+
+// Parts of a row of type DT that the FP32 results take.
+template <int DT>
+constexpr int row_parts() { return DT == 0 ? kParts : 1; }
+
+// A workgroup takes a tile of 32 places and a split of k, its wavefronts a quarter of that
+// each, 128 k at a time: lane l holds row l % 16 and of the 128 k the 32 from 32 (l / 16) on,
+// eight to an instruction (any order of k will do, the same for both operands).
+template <int DT, int NC>
+__device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& plan, int r,
+                                       int tile, int split, int64_t n_places, f32x4_t* sh) {
+  constexpr int N = row_parts<DT>();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, c = lane & 15;
+  const int k_adapter = plan.owner[tile];
+  int64_t row[2];
+  bool have[2];
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    const int i = plan.order[tile * kTile + 16 * f + c];
+    have[f] = i >= 0;
+    row[f] = (int64_t)(i < 0 ? 0 : i) * q.ldx;
+  }
+  const uint16_t* u[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int cc = 16 * j + c < r ? 16 * j + c : r - 1;
+    u[j] = q.u + ((int64_t)k_adapter * r + cc) * q.ldu;
+  }
+  f32x4_t acc[2][NC];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) acc[f][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t k0 = split * q.per + wave * (q.per / 4);
+  const int64_t k1 = k0 + q.per / 4 < q.K ? k0 + q.per / 4 : q.K;
+  for (int64_t k = k0; k < k1; k += 128) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int64_t at = k + 32 * g + 8 * s, left = q.K - at;
+      u32x4_t xv[2][N];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) xv[f][i] = u32x4_t{0, 0, 0, 0};
+        if (have[f] && left > 0) row8<DT, N>(q.x, row[f] + at, left, xv[f]);
+      }
+      u32x4_t uv[NC];
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        uv[j] = u32x4_t{0, 0, 0, 0};
+        if (left > 0) uv[j] = load16(u[j] + at);
+      }
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+          // D: rows (four of this lane) are sums c, the column is the token
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                as_bf16x8(uv[j]), as_bf16x8(xv[f][i]), acc[f][j], 0, 0, 0);
+    }
+  }
+  // the four wavefronts' sums in order
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      __syncthreads();
+      sh[wave * 64 + lane] = acc[f][j];
+      __syncthreads();
+      if (wave == 0) {
+        const f32x4_t v = (sh[lane] + sh[64 + lane]) + (sh[128 + lane] + sh[192 + lane]);
+        const int cc = 16 * j + 4 * g;
+        if (cc < r) {  // r is a multiple of 8
+          const int64_t place = (int64_t)tile * kTile + 16 * f + c;
+          *reinterpret_cast<f32x4_t*>(q.part + (split * n_places + place) * r + cc) = v;
+        }
+      }
+    }
+}
+
+// Two problems in one grid: s from x (BF16) and, in the backward, ds from dy.
+template <int DT, int NC>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(ShrinkProblem s, ShrinkProblem d,
+                                                          LoraPlan plan, int n, int r,
+                                                          int n_tiles) {
+  __shared__ f32x4_t sh[256];
+  const int tile = blockIdx.x, split = blockIdx.y;
+  if (tile >= plan.first[n]) return;
+  const int64_t places = (int64_t)n_tiles * kTile;
+  if (split < d.splits)
+    shrink<DT, NC>(d, plan, r, tile, split, places, sh);
+  else
+    shrink<1, NC>(s, plan, r, tile, split - d.splits, places, sh);
+}
+
+// The splits' sums joined in order, scaled, in parts: by token (M, parts, r) for the tiles and by
+// place (parts, r, places) for the gradients.
+struct JoinProblem {
+  const float* part;
+  int splits;
+  uint16_t* by_token;  // optional
+  uint16_t* by_place;  // optional
+};
+
+__global__ __launch_bounds__(256) void lora_join_kernel(JoinProblem s, JoinProblem d,
+                                                        LoraPlan plan, const float* scale, int n,
+                                                        int r, int n_tiles) {
+  const JoinProblem q = blockIdx.y ? d : s;
+  const int64_t places = (int64_t)n_tiles * kTile;
+  const int tile = blockIdx.x;
+  if (tile >= plan.first[n]) return;
+  const float f = scale ? scale[plan.owner[tile]] : 1.0f;
+  for (int e = threadIdx.x; e < kTile * r; e += 256) {
+    const int c = e % r;
+    const int64_t place = (int64_t)tile * kTile + e / r;
+    const int i = plan.order[place];
+    float v = 0.0f;
+    if (i >= 0) {
+      for (int t = 0; t < q.splits; ++t) v += q.part[(t * places + place) * r + c];
+      v *= f;
+    }
+    uint16_t part[kParts];
+    parts_of(v, part);
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) {
+      if (q.by_token && i >= 0) q.by_token[((int64_t)i * kParts + h) * r + c] = part[h];
+      if (q.by_place) q.by_place[((int64_t)h * r + c) * places + place] = part[h];
+    }
+  }
+}
+
+// ---- the adapters' share of a tile -------------------------------------------------------
+
+// Rows are output features (rows of U_k, (n, rows, r)), columns tokens.
+struct LoraShare {
+  const uint16_t* u;
+  const uint16_t* s2;  // (cols, kParts, r)
+  const int32_t* adapter;
+  int n, r;
+  int parts;  // that the result's type needs
+  int64_t rows, cols;
+};
+
+// Stores a 32 x 32 block to out[col][row]: lanes l and l + 32 hold rows 8 q + [0, 4) and
+// 8 q + [4, 8) of one column.  `left`: rows below the end, the same in all lanes; `in`: the
+// column is one.
+template <int DT>
+__device__ __forceinline__ void store_block(void* out, int64_t at, const f32x16_t& v, int half,
+                                            int64_t left, bool in) {
+  if constexpr (DT == 1) {
+    uint16_t* o = static_cast<uint16_t*>(out) + at;
+    if (left >= 32) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      // the two lanes trade, so that each has eight consecutive rows twice
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const auto sw = __builtin_amdgcn_permlane32_swap(w[4 * h + d], w[4 * h + 2 + d], false,
+                                                           false);
+          w[4 * h + d] = sw[0];
+          w[4 * h + 2 + d] = sw[1];
+        }
+      const u32x4_t a = {w[0], w[1], w[2], w[3]}, b = {w[4], w[5], w[6], w[7]};
+      if (in) {
+        __builtin_memcpy(o + 8 * half, &a, 16);
+        __builtin_memcpy(o + 16 + 8 * half, &b, 16);
+      }
+    } else if (in) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = 8 * (i >> 2) + 4 * half + (i & 3);
+        if (row < left) o[row] = to_bf16(v[i]);
+      }
+    }
+  } else {
+    float* o = static_cast<float*>(out) + at;
+    if (left >= 32) {
+      if (in) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t t = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+          __builtin_memcpy(o + 8 * q + 4 * half, &t, 16);
+        }
+      }
+    } else if (in) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = 8 * (i >> 2) + 4 * half + (i & 3);
+        if (row < left) o[row] = v[i];
+      }
+    }
+  }
+}
+
+// Is one of the eight BF16 numbers an infinity or a NaN?
+__device__ __forceinline__ bool not_finite(const u32x4_t& w) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m |= (w[j] & 0x7f807f80u) + 0x00800080u;
+  return (m & 0x80008000u) != 0;
+}
+
+// The epilogue of the product: the adapters' share, then the store to out (cols, rows).  Tokens
+// without the adapter enter its product with zeros; rows of U_k that are not finite would make
+// NaN of these, so they are left out there and added, for the adapter's own tokens, behind
+// the store (the sum is an infinity or a NaN then, whatever was stored).
+template <int DT>
+struct EpiLora {
+  struct Params {
+    LoraShare a;
+    void* out;
+    int64_t ldo;
+  };
+  // The adapters among the tile's four columns of this lane, one after the other:
+  // f(k, which of them).
+  template <class F>
+  __device__ __forceinline__ static void each(const LoraShare& a, int64_t j0, int lane, F f) {
+    int id[NB];
+    uint64_t left[NB], some = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      id[b] = adapter_of(a.adapter, j0 + 32 * b + (lane & 31), a.cols, a.n);
+      left[b] = __ballot(id[b] >= 0);
+      some |= left[b];
+    }
+    while (some) {
+      int k = 0;
+#pragma unroll
+      for (int b = NB - 1; b >= 0; --b)
+        if (left[b]) k = __builtin_amdgcn_readlane(id[b], __builtin_ctzll(left[b]));
+      bool own[NB];
+      some = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        own[b] = id[b] == k;
+        left[b] &= ~__ballot(own[b]);
+        some |= left[b];
+      }
+      f(k, own);
+    }
+  }
+  __device__ static void apply(const Params& p, f32x16_t (&acc)[NA][NB], int64_t i0, int64_t j0,
+                               int wr, int wc, int lane, uint16_t*) {
+    const LoraShare& a = p.a;
+    const int half = lane >> 5, chunks = a.r / 8, all = chunks * a.parts;
+    i0 += wr * WM;
+    j0 += wc * WN;
+    uint64_t odd = 0;
+    each(a, j0, lane, [&](int k, const bool (&own)[NB]) {
+      for (int c = 0; c < all; c += 2) {  // 16 of the r parts at a time
+        const int q = c + half;           // may pass the end by one: s is 0 there
+        u32x4_t uf[NA], sf[NB];
+#pragma unroll
+        for (int t = 0; t < NA; ++t) {
+          int64_t i = i0 + 32 * t + (lane & 31);
+          i = i < a.rows ? i : a.rows - 1;
+          uf[t] = load16(a.u + ((int64_t)k * a.rows + i) * a.r + 8 * (q % chunks));
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          sf[b] = u32x4_t{0, 0, 0, 0};
+          if (own[b] && q < all)
+            sf[b] = load16(a.s2 + (j0 + 32 * b + (lane & 31)) * kParts * a.r + 8 * q);
+        }
+#pragma unroll
+        for (int t = 0; t < NA; ++t) {
+          const bool bad = not_finite(uf[t]);
+          odd |= __ballot(bad);
+          if (bad) uf[t] = u32x4_t{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int t = 0; t < NA; ++t)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            acc[t][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(uf[t]), as_bf16x8(sf[b]),
+                                                                acc[t][b], 0, 0, 0);
+      }
+    });
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int64_t j = j0 + 32 * b + (lane & 31);
+#pragma unroll
+      for (int t = 0; t < NA; ++t) {
+        const int64_t i = i0 + 32 * t;
+        store_block<DT>(p.out, j * p.ldo + i, acc[t][b], half, a.rows - i, j < a.cols);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (odd) add_odd(p, i0, j0, lane);
+  }
+  // Each 8 numbers of U_k of which one is not finite, times s, onto the stored values.
+  __device__ __attribute__((noinline)) static void add_odd(const Params& p, int64_t i0, int64_t j0,
+                                                           int lane) {
+    const LoraShare& a = p.a;
+    __threadfence_block();
+    const int chunks = a.r / 8;
+    each(a, j0, lane, [&](int k, const bool (&own)[NB]) {
+      for (int64_t i = i0; i < i0 + WM && i < a.rows; ++i)
+        for (int c = 0; c < chunks; ++c) {
+          const u32x4_t u = load16(a.u + ((int64_t)k * a.rows + i) * a.r + 8 * c);
+          if (!not_finite(u) || lane >= 32) continue;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            if (!own[b]) continue;
+            const int64_t j = j0 + 32 * b + lane;
+            const uint16_t* s = a.s2 + j * kParts * a.r + 8 * c;
+            float v = 0.0f;
+            for (int e = 0; e < 8; ++e)
+              v += from_bf16((uint16_t)(u[e / 2] >> (16 * (e % 2)))) *
+                   (from_bf16(s[e]) + from_bf16(s[a.r + e]));
+            if constexpr (DT == 1) {
+              uint16_t* o = static_cast<uint16_t*>(p.out) + j * p.ldo + i;
+              *o = to_bf16(from_bf16(*o) + v);
+            } else {
+              static_cast<float*>(p.out)[j * p.ldo + i] += v;
+            }
+          }
+        }
+    });
+  }
+};
+
+// base + the adapters' share, without a product of its own: a wavefront takes 32 rows and 64
+// tokens.
+struct AddParams {
+  LoraShare a;
+  const void* base;  // optional, of the output's type
+  int64_t ldb;
+  void* out;
+  int64_t ldo;
+};
+
+template <int DT>
+__global__ __launch_bounds__(256) void lora_add_kernel(AddParams p) {
+  const LoraShare& a = p.a;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t i0 = ((int64_t)blockIdx.x * 4 + wave) * 32, j0 = (int64_t)blockIdx.y * 64;
+  if (i0 >= a.rows) return;
+  int64_t i = i0 + (lane & 31);
+  i = i < a.rows ? i : a.rows - 1;
+  f32x16_t acc[2];
+  int id[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int64_t j = j0 + 32 * b + (lane & 31);
+    id[b] = adapter_of(a.adapter, j, a.cols, a.n);
+    acc[b] = f32x16_t{};
+    if (p.base && j < a.cols) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t row = i0 + 8 * q + 4 * half, at = j * p.ldb + row;
+        if (row + 4 <= a.rows) {
+          if constexpr (DT == 1) {
+            u32x2_t w;
+            __builtin_memcpy(&w, static_cast<const uint16_t*>(p.base) + at, 8);
+            acc[b][4 * q] = bf16_lo(w[0]);
+            acc[b][4 * q + 1] = bf16_hi(w[0]);
+            acc[b][4 * q + 2] = bf16_lo(w[1]);
+            acc[b][4 * q + 3] = bf16_hi(w[1]);
+          } else {
+            f32x4_t w;
+            __builtin_memcpy(&w, static_cast<const float*>(p.base) + at, 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[b][4 * q + e] = w[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (row + e < a.rows) {
+              if constexpr (DT == 1)
+                acc[b][4 * q + e] = from_bf16(static_cast<const uint16_t*>(p.base)[at + e]);
+              else
+                acc[b][4 * q + e] = static_cast<const float*>(p.base)[at + e];
+            }
+        }
+      }
+    }
+  }
+  const int chunks = a.r / 8, all = chunks * a.parts;
+  uint64_t left[2] = {__ballot(id[0] >= 0), __ballot(id[1] >= 0)};
+  while (left[0] | left[1]) {
+    const int k = left[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(left[0]))
+                          : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(left[1]));
+    const uint16_t* u = a.u + ((int64_t)k * a.rows + i) * a.r;
+    f32x16_t v[2] = {};
+    uint64_t match[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      match[b] = __ballot(id[b] == k);
+      left[b] &= ~match[b];
+    }
+    for (int c = 0; c < all; c += 2) {
+      const int q = c + half;  // may pass the end by one: s is 0 there
+      const bf16x8_t uf = as_bf16x8(load16(u + 8 * (q % chunks)));
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (!match[b]) continue;
+        u32x4_t sf = {0, 0, 0, 0};
+        if (id[b] == k && q < all)
+          sf = load16(a.s2 + (j0 + 32 * b + (lane & 31)) * kParts * a.r + 8 * q);
+        v[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf, as_bf16x8(sf), v[b], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const bool own = id[b] == k;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[b][e] += own ? v[b][e] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int64_t j = j0 + 32 * b + (lane & 31);
+    store_block<DT>(p.out, j * p.ldo + i0, acc[b], half, a.rows - i0, j < a.cols);
+  }
+}
+
+// ---- the adapters' gradients ------------------------------------------------------------------
+
+// out_k[c][d] = sum over the places of adapter k of S(c, place) Y(token, d), S by place in parts
+// (parts, r, places), Y (M, D) token rows: a workgroup takes an adapter and 128 columns d.
+// Written (n, D, r) with BYCOL (dB), else (n, r, D) (dA).  Products of parts below 2^-24 of the
+// whole (part i of S with part j of Y, i + j > 2) are left out.
+struct OuterProblem {
+  const uint16_t* s;
+  const void* y;
+  int64_t ldy, D;
+  float* out;
+  int blocks;  // column tiles
+};
+
+constexpr int kOuter = 128;  // columns of a workgroup
+
+// A slab of 32 token rows of 128 columns in LDS, 256 bytes a row, 16-byte chunk c of row k at
+// c ^ 4 (k % 4), read back transposed (the layout of the product's dim-contiguous operand).
+__device__ __forceinline__ bf16x8_t slab_frag(const uint16_t LDS_AS* s, int d0, int ks, int lane) {
+  const int g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
+  const int d = d0 + 16 * (g & 1) + 4 * q;
+  const int k = 16 * ks + 8 * (g >> 1) + j;
+  const uint16_t LDS_AS* p = s + k * kOuter + (((d >> 3) ^ (4 * j)) * 8) + (d & 7);
+  const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v4i16_t LDS_AS*)p);
+  const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v4i16_t LDS_AS*)(p + 4 * kOuter));
+  const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
+  return __builtin_bit_cast(bf16x8_t, u32x4_t{a[0], a[1], b[0], b[1]});
+}
+
+template <int DT, int NC, bool BYCOL>
+__device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& plan, int r, int k,
+                                      int block, int64_t places, uint16_t* smem) {
+  constexpr int P = row_parts<DT>();  // of Y
+  constexpr int kSlab = kTile * kOuter;
+  uint16_t LDS_AS* const lds = (uint16_t LDS_AS*)smem;  // [2][P][kSlab]
+  const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t d0 = (int64_t)block * kOuter;
+  f32x16_t acc[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) acc[c] = f32x16_t{};
+  const int t0 = plan.first[k], t1 = plan.first[k + 1];
+  // this thread's two 16-byte chunks of a slab: rows t / 16 and 16 + t / 16
+  const int chunk = t & 15;
+  u32x4_t yv[2][P];
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = plan.order[tile * kTile + 16 * h + (t >> 4)];
+      const int64_t d = d0 + 8 * chunk, left = p.D - d;
+#pragma unroll
+      for (int q = 0; q < P; ++q) yv[h][q] = u32x4_t{0, 0, 0, 0};
+      if (i >= 0 && left > 0) row8<DT, P>(p.y, (int64_t)i * p.ldy + d, left, yv[h]);
+    }
+  };
+  if (t0 < t1) fetch(t0);
+  for (int tile = t0; tile < t1; ++tile) {
+    uint16_t LDS_AS* const stage = lds + ((tile - t0) & 1) * P * kSlab;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = 16 * h + (t >> 4);
+      const int at = row * kOuter + ((chunk ^ (4 * (row & 3))) * 8);
+#pragma unroll
+      for (int q = 0; q < P; ++q)
+        *reinterpret_cast<u32x4_t LDS_AS*>(stage + q * kSlab + at) = yv[h][q];
+    }
+    if (tile + 1 < t1) fetch(tile + 1);
+    u32x4_t sv[2][NC][kParts];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int row = 32 * c + (lane & 31) < r ? 32 * c + (lane & 31) : r - 1;
+        const uint16_t* s = p.s + row * places + (int64_t)tile * kTile + 16 * ks + 8 * half;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+          sv[ks][c][q] = *reinterpret_cast<const u32x4_t*>(s + q * r * places);
+      }
+    __syncthreads();  // one barrier a slab: the other stage is written behind the next
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int pl = 0; pl < P; ++pl) {
+        const bf16x8_t y = slab_frag(stage + pl * kSlab, 32 * wave, ks, lane);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int h = 0; h + pl < kParts; ++h)
+            acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(sv[ks][c][h]), y, acc[c],
+                                                             0, 0, 0);
+      }
+  }
+  const int64_t d = d0 + 32 * wave + (lane & 31);
+  if (d >= p.D) return;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int row = 32 * c + 8 * q + 4 * half;
+      if (row >= r) continue;
+      if constexpr (BYCOL) {
+        *reinterpret_cast<f32x4_t*>(p.out + ((int64_t)k * p.D + d) * r + row) =
+            f32x4_t{acc[c][4 * q], acc[c][4 * q + 1], acc[c][4 * q + 2], acc[c][4 * q + 3]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          p.out[((int64_t)k * r + row + e) * p.D + d] = acc[c][4 * q + e];
+      }
+    }
+}
+
+// dB's tiles first, then dA's.
+template <int DT, int NC>
+__global__ __launch_bounds__(256) void lora_outer_kernel(OuterProblem b, OuterProblem a,
+                                                         LoraPlan plan, int n, int r,
+                                                         int n_tiles) {
+  __shared__ __attribute__((aligned(256))) uint16_t smem[2 * row_parts<DT>() * kTile * kOuter];
+  const int64_t places = (int64_t)n_tiles * kTile;
+  const int64_t nb = (int64_t)n * b.blocks;
+  int64_t w = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (w < nb) {
+    outer<DT, NC, true>(b, plan, r, (int)(w / b.blocks), (int)(w % b.blocks), places, smem);
+  } else {
+    w -= nb;
+    if (w >= (int64_t)n * a.blocks) return;
+    outer<1, NC, false>(a, plan, r, (int)(w / a.blocks), (int)(w % a.blocks), places, smem);
+  }
+}
+
+// ---- layouts ----------------------------------------------------------------------------------
+
+// (n, R, C) to (n, C, ldr), the places from R to ldr zero; adapters without tokens are left out.
+struct TransposeProblem {
+  const uint16_t* in;
+  uint16_t* out;
+  int64_t R, C, ldr;
+};
+
+__global__ __launch_bounds__(256) void lora_transpose_kernel(TransposeProblem a,
+                                                             TransposeProblem b, LoraPlan plan,
+                                                             int64_t tiles_a) {
+  __shared__ uint16_t sh[64][66];
+  const int k = blockIdx.y;
+  if (plan.first[k] == plan.first[k + 1]) return;
+  const bool second = (int64_t)blockIdx.x >= tiles_a;
+  const TransposeProblem q = second ? b : a;
+  const int64_t w = second ? blockIdx.x - tiles_a : blockIdx.x;
+  const int64_t nc = (q.C + 63) / 64;
+  const int64_t r0 = w / nc * 64, c0 = w % nc * 64;
+  const uint16_t* in = q.in + k * q.R * q.C;
+  uint16_t* out = q.out + k * q.C * q.ldr;
+  const int x = threadIdx.x & 63;
+  for (int y = threadIdx.x >> 6; y < 64; y += 4)
+    sh[y][x] = r0 + y < q.R && c0 + x < q.C ? in[(r0 + y) * q.C + c0 + x] : (uint16_t)0;
+  __syncthreads();
+  for (int y = threadIdx.x >> 6; y < 64; y += 4)
+    if (c0 + y < q.C && r0 + x < q.ldr) out[(c0 + y) * q.ldr + r0 + x] = sh[x][y];
+}
+
+// dy (M, V) as rows of ldv BF16 numbers, zeros behind V: for rows that the product cannot read in
+// place.  FP32 as two planes, its first two parts: the product's result is BF16.
+template <int DT>
+__global__ __launch_bounds__(256) void lora_rows_kernel(const void* dy, int64_t V, int64_t ldy,
+                                                        int64_t ldv, uint16_t* out,
+                                                        int64_t plane) {
+  const int64_t i = blockIdx.x, v = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+  if (v >= ldv) return;
+  constexpr int N = DT == 0 ? 2 : 1;
+  u32x4_t part[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) part[q] = u32x4_t{0, 0, 0, 0};
+  if (V - v > 0) row8<DT, N>(dy, i * ldy + v, V - v, part);
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+    *reinterpret_cast<u32x4_t*>(out + q * plane + i * ldv + v) = part[q];
+}
+
+// ---- few tokens -------------------------------------------------------------------------------
+
+// Up to 64 tokens: W is streamed once against X in LDS, 16 kFrags rows a wavefront, straight
+// into operand registers, a superstep of 128 k ahead.  X's rows of kX elements; the 16-byte chunk q of
+// token c lies at q ^ (c % 16) in its group of 16, so that 16 tokens' reads of one chunk
+// meet all banks once.
+template <int T>
+constexpr int skinny_k() { return T == 16 ? 2048 : T == 32 ? 1024 : 512; }
+
+struct SkinnyParams {
+  const uint16_t* x;
+  int64_t ldx, K;
+  const uint16_t* w;
+  LoraShare a;
+  void* out;
+  int64_t ldo;
+};
+
+template <int T, int F, int DT>
+__global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
+  constexpr int KX = skinny_k<T>(), NT16 = T / 16;
+  __shared__ __attribute__((aligned(256))) uint16_t xs[T * KX];
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t v0 = (int64_t)blockIdx.x * (64 * F) + wave * (16 * F);
+  const uint16_t* wr[F];
+  f32x4_t acc[F][NT16];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int64_t row = v0 + 16 * f + c;
+    wr[f] = p.w + (row < p.a.rows ? row : p.a.rows - 1) * p.K;  // past the end the last row
+#pragma unroll
+    for (int t = 0; t < NT16; ++t) acc[f][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  typedef u32x4_t Frag[F][4];
+  auto fetch = [&](Frag& q, int64_t k) {
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int64_t at = k + 32 * g + 8 * s;
+        q[f][s] = u32x4_t{0, 0, 0, 0};
+        if (at < p.K) q[f][s] = load16(wr[f] + at);
+      }
+  };
+  auto multiply = [&](const Frag& q, int kk) {  // kk: of the part in LDS
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      bf16x8_t xv[NT16];
+#pragma unroll
+      for (int t = 0; t < NT16; ++t) {
+        const int ch = kk / 8 + 4 * g + s;
+        xv[t] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(xs + (16 * t + c) * KX + (ch ^ c) * 8));
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int t = 0; t < NT16; ++t)
+          acc[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(q[f][s]), xv[t],
+                                                              acc[f][t], 0, 0, 0);
+    }
+  };
+  Frag q[2];
+  fetch(q[0], 0);
+  for (int64_t k0 = 0; k0 < p.K; k0 += KX) {
+    if (k0) __syncthreads();
+    for (int e = threadIdx.x; e < T * KX / 8; e += 256) {
+      const int tok = e / (KX / 8), ch = e % (KX / 8);
+      u32x4_t v = {0, 0, 0, 0};
+      if (tok < p.a.cols && k0 + ch * 8 < p.K) v = load16(p.x + tok * p.ldx + k0 + ch * 8);
+      *reinterpret_cast<u32x4_t*>(xs + tok * KX + (ch ^ (tok & 15)) * 8) = v;
+    }
+    __syncthreads();
+    const int n = (int)((p.K - k0 < KX ? p.K - k0 : KX) + 127) / 128;  // supersteps
+    for (int ss = 0; ss < n; ss += 2) {
+      fetch(q[1], k0 + 128 * (ss + 1));
+      multiply(q[0], 128 * ss);
+      // an odd number of supersteps is the last part's alone: q[1] is past K then
+      fetch(q[0], k0 + 128 * (ss + 2));
+      if (ss + 1 < n) multiply(q[1], 128 * (ss + 1));
+    }
+  }
+  // the adapters' share: 32 of the r parts an instruction
+  const LoraShare& a = p.a;
+  const int chunks = a.r / 8, all = chunks * a.parts;
+  int id[NT16];
+  uint64_t left[NT16], some = 0;
+#pragma unroll
+  for (int t = 0; t < NT16; ++t) {
+    id[t] = adapter_of(a.adapter, 16 * t + c, a.cols, a.n);
+    left[t] = __ballot(id[t] >= 0);
+    some |= left[t];
+  }
+  while (some) {
+    int k = 0;
+    bool found = false;
+#pragma unroll
+    for (int t = 0; t < NT16; ++t)
+      if (!found && left[t]) {
+        k = __builtin_amdgcn_readlane(id[t], __builtin_ctzll(left[t]));
+        found = true;
+      }
+    uint64_t match[NT16];
+    some = 0;
+#pragma unroll
+    for (int t = 0; t < NT16; ++t) {
+      match[t] = __ballot(id[t] == k);
+      left[t] &= ~match[t];
+      some |= left[t];
+    }
+    f32x4_t v[F][NT16] = {};
+    for (int c0 = 0; c0 < all; c0 += 4) {
+      const int ch = c0 + g;
+      u32x4_t uf[F];
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int64_t row = v0 + 16 * f + c;
+        uf[f] = u32x4_t{0, 0, 0, 0};
+        if (ch < all)
+          uf[f] = load16(a.u + ((int64_t)k * a.rows + (row < a.rows ? row : a.rows - 1)) * a.r +
+                         8 * (ch % chunks));
+      }
+#pragma unroll
+      for (int t = 0; t < NT16; ++t) {
+        if (!match[t]) continue;
+        u32x4_t sf = {0, 0, 0, 0};
+        if (id[t] == k && ch < all)
+          sf = load16(a.s2 + (int64_t)(16 * t + c) * kParts * a.r + 8 * ch);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          v[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(uf[f]), as_bf16x8(sf),
+                                                            v[f][t], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT16; ++t) {
+      const bool own = id[t] == k;
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[f][t][e] += own ? v[f][t][e] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT16; ++t) {
+    const int64_t j = 16 * t + c;
+    if (j >= a.cols) continue;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int64_t row = v0 + 16 * f + 4 * g;
+      const f32x4_t& v = acc[f][t];
+      if (row + 4 <= a.rows) {
+        if constexpr (DT == 1) {
+          const u32x2_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+          __builtin_memcpy(static_cast<uint16_t*>(p.out) + j * p.ldo + row, &w, 8);
+        } else {
+          __builtin_memcpy(static_cast<float*>(p.out) + j * p.ldo + row, &v, 16);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row + e < a.rows) {
+            if constexpr (DT == 1)
+              static_cast<uint16_t*>(p.out)[j * p.ldo + row + e] = to_bf16(v[e]);
+            else
+              static_cast<float*>(p.out)[j * p.ldo + row + e] = v[e];
+          }
+      }
+    }
+  }
+}
+
+// ---- host side --------------------------------------------------------------------------------
+
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Tokens up to which a workgroup per token forms s.
+constexpr int64_t kTokenWise = 256;
+constexpr int64_t kSkinny = 64;
+
+inline int64_t most_tiles(int64_t M, int64_t n) {
+  const int64_t t = (M + kTile - 1) / kTile + (n < M ? n : M);
+  return t > 0 ? t : 1;
+}
+
+// Splits of k so that the tiles make some four workgroups per CU, 512 k at least each.
+struct Split {
+  int n;
+  int64_t per;
+};
+inline Split split_of(int64_t K, int64_t tiles) {
+  int64_t s = (1024 + tiles - 1) / tiles;
+  const int64_t most = (K + 511) / 512;
+  s = s > most ? most : s;
+  s = s < 1 ? 1 : s;
+  Split r;
+  r.per = (K + s * 512 - 1) / (s * 512) * 512;
+  r.n = (int)((K + r.per - 1) / r.per);
+  return r;
+}
+
+struct Places {
+  size_t order, first, owner, end;
+  Places(int64_t M, int64_t n, size_t at) {
+    const int64_t t = most_tiles(M, n);
+    order = at;
+    first = up256(order + (size_t)t * kTile * 4);
+    owner = up256(first + (size_t)(n + 1) * 4);
+    end = up256(owner + (size_t)t * 4);
+  }
+  LoraPlan plan(char* ws) const {
+    return LoraPlan{reinterpret_cast<int32_t*>(ws + order), reinterpret_cast<int32_t*>(ws + first),
+                    reinterpret_cast<int32_t*>(ws + owner)};
+  }
+};
+
+template <int DT>
+hipError_t run_shrink(const ShrinkProblem& s, const ShrinkProblem& d, const LoraPlan& plan, int n,
+                      int r, int tiles, hipStream_t stream) {
+  const dim3 grid((unsigned)tiles, (unsigned)(s.splits + d.splits));
+  if (r <= 16)
+    hipLaunchKernelGGL((lora_shrink_kernel<DT, 1>), grid, dim3(256), 0, stream, s, d, plan, n, r,
+                       tiles);
+  else if (r <= 32)
+    hipLaunchKernelGGL((lora_shrink_kernel<DT, 2>), grid, dim3(256), 0, stream, s, d, plan, n, r,
+                       tiles);
+  else if (r <= 64)
+    hipLaunchKernelGGL((lora_shrink_kernel<DT, 4>), grid, dim3(256), 0, stream, s, d, plan, n, r,
+                       tiles);
+  else
+    hipLaunchKernelGGL((lora_shrink_kernel<DT, 8>), grid, dim3(256), 0, stream, s, d, plan, n, r,
+                       tiles);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run_outer(const OuterProblem& b, const OuterProblem& a, const LoraPlan& plan, int n,
+                     int r, int tiles, hipStream_t stream) {
+  const dim3 grid = grid2((int64_t)n * (b.blocks + a.blocks));
+  if (r <= 32)
+    hipLaunchKernelGGL((lora_outer_kernel<DT, 1>), grid, dim3(256), 0, stream, b, a, plan, n, r,
+                       tiles);
+  else if (r <= 64)
+    hipLaunchKernelGGL((lora_outer_kernel<DT, 2>), grid, dim3(256), 0, stream, b, a, plan, n, r,
+                       tiles);
+  else
+    hipLaunchKernelGGL((lora_outer_kernel<DT, 4>), grid, dim3(256), 0, stream, b, a, plan, n, r,
+                       tiles);
+  return hipGetLastError();
+}
+
+template <int T, int DT>
+hipError_t run_skinny(const SkinnyParams& p, hipStream_t stream) {
+  // two fragments of rows a wavefront where that still fills the chip
+  if (p.a.rows >= 65536)
+    hipLaunchKernelGGL((lora_skinny_kernel<T, 2, DT>), dim3((unsigned)((p.a.rows + 127) / 128)),
+                       dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL((lora_skinny_kernel<T, 1, DT>), dim3((unsigned)((p.a.rows + 63) / 64)),
+                       dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t forward_tiles(const LoraFwdArgs& p, const LoraShare& a, hipStream_t stream) {
+  if (!p.w) {
+    const AddParams q{a, p.base, p.ldb, p.out, p.ldo};
+    hipLaunchKernelGGL((lora_add_kernel<DT>),
+                       dim3((unsigned)((p.V + 127) / 128), (unsigned)((p.M + 63) / 64)), dim3(256),
+                       0, stream, q);
+    return hipGetLastError();
+  }
+  if (p.M <= kSkinny) {
+    const SkinnyParams q{p.x, p.ldx, p.H, p.w, a, p.out, p.ldo};
+    return p.M <= 16 ? run_skinny<16, DT>(q, stream)
+           : p.M <= 32 ? run_skinny<32, DT>(q, stream) : run_skinny<64, DT>(q, stream);
+  }
+  const Operand W{p.w, p.H, p.V, p.H}, X{p.x, p.ldx, p.M, p.H};
+  const typename EpiLora<DT>::Params ep{a, p.out, p.ldo};
+  return run_gemm<EpiLora<DT>, false, false>(W, X, p.V, p.M, p.H, ep, stream);
+}
+
+}  // namespace
+
+bool lora_size_ok(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r) {
+  if (r % 8 != 0 || H % 8 != 0 || r > kLoraRank || n > kLoraAdapters) return false;
+  return M <= (int64_t)1 << 21 && H <= (int64_t)1 << 20 && V <= (int64_t)1 << 22;
+}
+
+size_t lora_forward_bytes(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r) {
+  size_t at = up256((size_t)M * kParts * r * 2);
+  if (M <= kTokenWise) return at + 256;
+  const int64_t tiles = most_tiles(M, n);
+  at = Places(M, n, at).end;
+  return up256(at + (size_t)split_of(H, tiles).n * tiles * kTile * r * 4) + 256;
+}
+
+hipError_t launch_lora_forward(const LoraFwdArgs& p, char* ws, hipStream_t stream) {
+  uint16_t* s2 = reinterpret_cast<uint16_t*>(ws);
+  hipError_t e;
+  if (p.M <= kTokenWise) {
+    hipLaunchKernelGGL(lora_token_kernel, dim3((unsigned)p.M, (unsigned)(p.r / 8)), dim3(256), 0,
+                       stream, p, s2);
+    e = hipGetLastError();
+  } else {
+    const int64_t tiles = most_tiles(p.M, p.n);
+    const Places pl(p.M, p.n, up256((size_t)p.M * kParts * p.r * 2));
+    const LoraPlan plan = pl.plan(ws);
+    const Split sp = split_of(p.H, tiles);
+    float* part = reinterpret_cast<float*>(ws + pl.end);
+    hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.adapter, p.M,
+                       p.n, plan);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const ShrinkProblem s{p.x, p.ldx, p.H, p.a, p.H, part, sp.n, sp.per};
+    const ShrinkProblem none{};
+    if ((e = run_shrink<1>(s, none, plan, p.n, p.r, (int)tiles, stream)) != hipSuccess) return e;
+    const JoinProblem j{part, sp.n, s2, nullptr};
+    hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)tiles, 1), dim3(256), 0, stream, j, j, plan,
+                       p.scale, p.n, p.r, (int)tiles);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess) return e;
+  const LoraShare a{p.b, s2, p.adapter, p.n, p.r, p.dtype == 0 ? kParts : 2, p.V, p.M};
+  return p.dtype == 0 ? forward_tiles<0>(p, a, stream) : forward_tiles<1>(p, a, stream);
+}
+
+namespace {
+
+struct BwdPlan {
+  int64_t tiles, ldv;
+  Split ss, sd;
+  size_t s_part, d_part, s_place, d_place, d_token, at, bt, rows, total;
+  Places places;
+  BwdPlan(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r, int dtype)
+      : places(M, n, 0) {
+    tiles = most_tiles(M, n);
+    ldv = (V + 7) / 8 * 8;
+    ss = split_of(H, tiles);
+    sd = split_of(V, tiles);
+    const size_t per = (size_t)tiles * kTile * r;
+    s_part = places.end;
+    d_part = up256(s_part + (size_t)ss.n * per * 4);
+    s_place = up256(d_part + (size_t)sd.n * per * 4);
+    d_place = up256(s_place + per * kParts * 2);
+    d_token = up256(d_place + per * kParts * 2);
+    at = up256(d_token + (size_t)M * kParts * r * 2);
+    bt = up256(at + (size_t)n * r * H * 2);
+    rows = up256(bt + (size_t)n * r * ldv * 2);
+    total = up256(rows + (size_t)M * ldv * 2 * (dtype == 0 ? 2 : 1)) + 256;
+  }
+};
+
+template <int DT>
+hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
+  const BwdPlan b(p.M, p.H, p.V, p.n, p.r, p.dtype);
+  const LoraPlan plan = b.places.plan(ws);
+  const int tiles = (int)b.tiles;
+  auto bf = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
+  auto fp = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  hipError_t e;
+  hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.adapter, p.M, p.n,
+                     plan);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const TransposeProblem ta{p.a, bf(b.at), p.r, p.H, p.r}, tb{p.b, bf(b.bt), p.V, p.r, b.ldv};
+  auto n_tr = [](const TransposeProblem& t) { return (t.ldr + 63) / 64 * ((t.C + 63) / 64); };
+  hipLaunchKernelGGL(lora_transpose_kernel, dim3((unsigned)(n_tr(ta) + n_tr(tb)), (unsigned)p.n),
+                     dim3(256), 0, stream, ta, tb, plan, n_tr(ta));
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const ShrinkProblem s{p.x, p.ldx, p.H, p.a, p.H, fp(b.s_part), b.ss.n, b.ss.per};
+  const ShrinkProblem d{p.dy, p.ldy, p.V, bf(b.bt), b.ldv, fp(b.d_part), b.sd.n, b.sd.per};
+  if ((e = run_shrink<DT>(s, d, plan, p.n, p.r, tiles, stream)) != hipSuccess) return e;
+  const JoinProblem js{fp(b.s_part), b.ss.n, nullptr, bf(b.s_place)};
+  const JoinProblem jd{fp(b.d_part), b.sd.n, bf(b.d_token), bf(b.d_place)};
+  hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)tiles, 2), dim3(256), 0, stream, js, jd, plan,
+                     p.scale, p.n, p.r, tiles);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (p.dx && p.M > 0) {
+    const LoraShare a{bf(b.at), bf(b.d_token), p.adapter, p.n, p.r, 2, p.H, p.M};
+    if (!p.w) {
+      const AddParams q{a, p.dx_base, p.H, p.dx, p.H};
+      hipLaunchKernelGGL((lora_add_kernel<1>),
+                         dim3((unsigned)((p.H + 127) / 128), (unsigned)((p.M + 63) / 64)),
+                         dim3(256), 0, stream, q);
+      e = hipGetLastError();
+    } else {
+      const uint16_t* rows = static_cast<const uint16_t*>(p.dy);
+      int64_t ld = p.ldy;
+      const bool fits = DT == 1 && p.V % 8 == 0 && p.ldy % 8 == 0 && p.ldy <= (int64_t)1 << 22 &&
+                        reinterpret_cast<uintptr_t>(p.dy) % 16 == 0;
+      if (!fits) {
+        hipLaunchKernelGGL((lora_rows_kernel<DT>),
+                           dim3((unsigned)p.M, (unsigned)((b.ldv / 8 + 255) / 256)), dim3(256), 0,
+                           stream, p.dy, p.V, p.ldy, b.ldv, bf(b.rows), p.M * b.ldv);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        rows = bf(b.rows);
+        ld = b.ldv;
+      }
+      // W (V, H): element (h, v) at v H + h
+      const Operand W{p.w, p.H, p.H, p.V};
+      const typename EpiLora<1>::Params ep{a, p.dx, p.H};
+      if constexpr (DT == 0) {
+        const Operand hi{rows, ld, p.M, p.V}, lo{rows + p.M * b.ldv, ld, p.M, p.V};
+        e = run_gemm<EpiLora<1>, true, false, 2>(Segs<2>{{W, W}, {hi, lo}}, p.H, p.M, p.V, ep,
+                                                 stream);
+      } else {
+        const Operand Y{rows, ld, p.M, p.V};
+        e = run_gemm<EpiLora<1>, true, false>(W, Y, p.H, p.M, p.V, ep, stream);
+      }
+    }
+    if (e != hipSuccess) return e;
+  }
+  if (p.da || p.db) {
+    const OuterProblem ob{bf(b.s_place), p.dy, p.ldy, p.V, p.db,
+                          p.db ? (int)((p.V + kOuter - 1) / kOuter) : 0};
+    const OuterProblem oa{bf(b.d_place), p.x, p.ldx, p.H, p.da,
+                          p.da ? (int)((p.H + kOuter - 1) / kOuter) : 0};
+    e = run_outer<DT>(ob, oa, plan, p.n, p.r, tiles, stream);
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t lora_backward_bytes(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r, int dtype) {
+  return BwdPlan(M, H, V, n, r, dtype).total;
+}
+
+hipError_t launch_lora_backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
+  return p.dtype == 0 ? backward<0>(p, ws, stream) : backward<1>(p, ws, stream);
+}
+
+}  // namespace vce

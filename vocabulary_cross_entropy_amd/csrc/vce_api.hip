@@ -13,6 +13,7 @@
 
 #include "adamw.h"
 #include "beam.h"
+#include "lora.h"
 #include "vce.h"
 #include "vce_internal.h"
 
@@ -1445,6 +1446,157 @@ int beam_reorder(const vce_beam_state* states, int64_t count, int64_t B, int64_t
   }
   return launch_status(vce::launch_beam_reorder(states, count, B, K, parent, parent_stride,
                                                 static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+// What both directions have: sizes, x, the adapters, W.
+int check_lora(const void* x, int64_t ldx, int64_t M, int64_t H, int64_t V, const void* a,
+               const void* b, int64_t n, int64_t r, const int32_t* adapter, const float* scale,
+               const void* w, const void* base) {
+  if (M < 0 || H <= 0 || V <= 0 || n <= 0 || r <= 0) return VCE_EINVAL;
+  if (!vce::lora_size_ok(M, H, V, n, r)) return VCE_EUNSUPPORTED;
+  if (w && base) return VCE_EINVAL;
+  if (!a || !b || (M > 0 && (!x || !adapter))) return VCE_EINVAL;
+  if (M > 1 && ldx < H) return VCE_EINVAL;
+  if (M > 1 && (ldx % 8 != 0 || ldx > ((int64_t)1 << 22))) return VCE_EUNSUPPORTED;
+  if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(adapter, 4) ||
+      !aligned(scale, 4) || !aligned(w, 16))
+    return VCE_EALIGN;
+  return VCE_OK;
+}
+
+// The inputs of both as ranges.
+struct LoraInputs {
+  Range r[6];
+  LoraInputs(const void* x, int64_t ldx, int64_t M, int64_t H, int64_t V, const void* a,
+             const void* b, int64_t n, int64_t rank, const int32_t* adapter, const float* scale,
+             const void* w)
+      : r{range(M > 0 ? x : nullptr, M > 0 ? ((M - 1) * ldx + H) * 2 : 0),
+          range(a, n * rank * H * 2), range(b, n * rank * V * 2),
+          range(M > 0 ? adapter : nullptr, M * 4), range(scale, n * 4), range(w, V * H * 2)} {}
+};
+
+}  // namespace
+
+size_t lora_forward_workspace_size(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r) {
+  if (M < 0 || H <= 0 || V <= 0 || n <= 0 || r <= 0 || !vce::lora_size_ok(M, H, V, n, r)) return 0;
+  return vce::lora_forward_bytes(M, H, V, n, r);
+}
+
+int lora_forward(const void* x, int64_t ldx, int64_t M, int64_t H, int64_t V, const void* a,
+                 const void* b, int64_t n, int64_t r, const int32_t* adapter, const float* scale,
+                 const void* w, const void* base, int64_t ldb, void* out, int dtype, int64_t ldo,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype)) return VCE_EDTYPE;
+  const int rc = check_lora(x, ldx, M, H, V, a, b, n, r, adapter, scale, w, base);
+  if (rc != VCE_OK) return rc;
+  if (M == 0) return VCE_OK;
+  if (!out || !workspace) return VCE_EINVAL;
+  if (M == 1) {  // one row's stride says nothing
+    ldx = H;
+    ldb = ldb < V ? V : ldb;
+    ldo = ldo < V ? V : ldo;
+  }
+  const int64_t es = dtype_size(dtype);
+  int64_t ob, bb = 0;
+  if (ldo < V || !span_ok(M, V, ldo, es, &ob)) return VCE_EINVAL;
+  if (base && (ldb < V || !span_ok(M, V, ldb, es, &bb))) return VCE_EINVAL;
+  if (!aligned(out, es) || !aligned(base, es) || !aligned(workspace, 256)) return VCE_EALIGN;
+  const size_t need = vce::lora_forward_bytes(M, H, V, n, r);
+  if (workspace_bytes < need) return VCE_EWORKSPACE;
+  const LoraInputs in(x, ldx, M, H, V, a, b, n, r, adapter, scale, w);
+  const Range o = range(out, ob), ws = range(workspace, (int64_t)need), br = range(base, bb);
+  if (overlap(o, ws) || overlap(ws, br)) return VCE_EALIAS;
+  for (const Range& q : in.r)
+    if (overlap(o, q) || overlap(ws, q)) return VCE_EALIAS;
+  if (overlap(o, br) && !(out == base && ldo == ldb)) return VCE_EALIAS;
+  vce::LoraFwdArgs p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.M = M;
+  p.H = H;
+  p.V = V;
+  p.ldx = ldx;
+  p.n = (int)n;
+  p.r = (int)r;
+  p.a = static_cast<const uint16_t*>(a);
+  p.b = static_cast<const uint16_t*>(b);
+  p.adapter = adapter;
+  p.scale = scale;
+  p.w = static_cast<const uint16_t*>(w);
+  p.base = base;
+  p.ldb = ldb;
+  p.out = out;
+  p.ldo = ldo;
+  p.dtype = dtype;
+  return launch_status(vce::launch_lora_forward(p, static_cast<char*>(workspace),
+                                                static_cast<hipStream_t>(stream)));
+}
+
+size_t lora_backward_workspace_size(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r,
+                                    int dtype) {
+  if (M < 0 || H <= 0 || V <= 0 || n <= 0 || r <= 0 || !vce::lora_size_ok(M, H, V, n, r) ||
+      !dtype_ok(dtype))
+    return 0;
+  return vce::lora_backward_bytes(M, H, V, n, r, dtype);
+}
+
+int lora_backward(const void* dy, int dtype, int64_t ldy, const void* x, int64_t ldx, int64_t M,
+                  int64_t H, int64_t V, const void* a, const void* b, int64_t n, int64_t r,
+                  const int32_t* adapter, const float* scale, const void* w, const void* dx_base,
+                  void* dx, float* da, float* db, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  if (!dtype_ok(dtype)) return VCE_EDTYPE;
+  const int rc = check_lora(x, ldx, M, H, V, a, b, n, r, adapter, scale, w, dx_base);
+  if (rc != VCE_OK) return rc;
+  if ((M == 0 || !dx) && !da && !db) return VCE_OK;
+  if ((M > 0 && !dy) || !workspace) return VCE_EINVAL;
+  if (M <= 1) {
+    ldx = H;
+    ldy = ldy < V ? V : ldy;
+  }
+  const int64_t es = dtype_size(dtype);
+  int64_t yb = 0;
+  if (M > 0 && (ldy < V || !span_ok(M, V, ldy, es, &yb))) return VCE_EINVAL;
+  if (!aligned(dy, es) || !aligned(dx_base, 16) || !aligned(dx, 16) || !aligned(da, 16) ||
+      !aligned(db, 16) || !aligned(workspace, 256))
+    return VCE_EALIGN;
+  const size_t need = vce::lora_backward_bytes(M, H, V, n, r, dtype);
+  if (workspace_bytes < need) return VCE_EWORKSPACE;
+  const LoraInputs in(x, ldx, M, H, V, a, b, n, r, adapter, scale, w);
+  const Range yr = range(M > 0 ? dy : nullptr, yb), br = range(dx_base, M * H * 2);
+  const Range out[4] = {range(dx, M * H * 2), range(da, n * r * H * 4), range(db, n * r * V * 4),
+                        range(workspace, (int64_t)need)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return VCE_EALIAS;
+    for (const Range& q : in.r)
+      if (overlap(out[i], q)) return VCE_EALIAS;
+    if (overlap(out[i], yr)) return VCE_EALIAS;
+    if (overlap(out[i], br) && !(i == 0 && dx == dx_base)) return VCE_EALIAS;
+  }
+  vce::LoraBwdArgs p;
+  p.dy = dy;
+  p.dtype = dtype;
+  p.M = M;
+  p.H = H;
+  p.V = V;
+  p.ldy = ldy;
+  p.ldx = ldx;
+  p.x = static_cast<const uint16_t*>(x);
+  p.n = (int)n;
+  p.r = (int)r;
+  p.a = static_cast<const uint16_t*>(a);
+  p.b = static_cast<const uint16_t*>(b);
+  p.adapter = adapter;
+  p.scale = scale;
+  p.w = static_cast<const uint16_t*>(w);
+  p.dx_base = static_cast<const uint16_t*>(dx_base);
+  p.dx = static_cast<uint16_t*>(dx);
+  p.da = da;
+  p.db = db;
+  return launch_status(vce::launch_lora_backward(p, static_cast<char*>(workspace),
+                                                 static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
