@@ -35,6 +35,16 @@ __device__ __forceinline__ u32x4_t load16(const void* p) {
 
 constexpr int kParts = 3;  // of s and ds, as they are stored
 
+// Everything written to LDS so far is seen by the workgroup's waves; loads from memory stay in
+// flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
 // v in BF16 parts.  A part of an infinity or a NaN behind the first is 0.
 __device__ __forceinline__ void parts_of(float v, uint16_t* part) {
 #pragma unroll
@@ -76,8 +86,7 @@ __device__ __forceinline__ int adapter_of(const int32_t* adapter, int64_t i, int
   return k >= 0 && k < n ? k : -1;
 }
 
-__global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* adapter, int64_t M,
-                                                                 int n, LoraPlan plan) {
+__device__ void make_plan(const int32_t* adapter, int64_t M, int n, const LoraPlan& plan) {
   // read and written by the lanes of one wavefront in turn
   __shared__ volatile int32_t count[kPlanWaves][kLoraAdapters];
   __shared__ int32_t tiles[kLoraAdapters];
@@ -144,6 +153,60 @@ __global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* 
       if (lane == 0) count[wave][k] = at + __builtin_popcountll(match);
     });
   }
+}
+
+// (n, R, C) to (n, C, ldr), the places from R to ldr zero.
+struct TransposeProblem {
+  const uint16_t* in;
+  uint16_t* out;
+  int64_t R, C, ldr;
+  int64_t tiles;  // of an adapter
+};
+
+inline TransposeProblem transpose_of(const uint16_t* in, uint16_t* out, int64_t R, int64_t C,
+                                     int64_t ldr) {
+  return TransposeProblem{in, out, R, C, ldr, (ldr + 63) / 64 * ((C + 63) / 64)};
+}
+
+constexpr int64_t kScan = 16384;  // tokens that a tile looks through for its adapter
+
+__device__ void transpose(const TransposeProblem& q, int k, int64_t w, const int32_t* adapter,
+                          int64_t M) {
+  __shared__ uint16_t sh[64][66];
+  if (M <= kScan) {  // an adapter without tokens is left out
+    bool used = false;
+    for (int64_t i = threadIdx.x; i < M; i += kPlanThreads) used |= adapter[i] == k;
+    if (!__syncthreads_or(used)) return;
+  }
+  const int64_t nc = (q.C + 63) / 64;
+  const int64_t r0 = w / nc * 64, c0 = w % nc * 64;
+  const uint16_t* in = q.in + k * q.R * q.C;
+  uint16_t* out = q.out + k * q.C * q.ldr;
+  const int x = threadIdx.x & 63;
+#pragma unroll
+  for (int y = threadIdx.x >> 6; y < 64; y += kPlanWaves)
+    sh[y][x] = r0 + y < q.R && c0 + x < q.C ? in[(r0 + y) * q.C + c0 + x] : (uint16_t)0;
+  __syncthreads();
+#pragma unroll
+  for (int y = threadIdx.x >> 6; y < 64; y += kPlanWaves)
+    if (c0 + y < q.C && r0 + x < q.ldr) out[(c0 + y) * q.ldr + r0 + x] = sh[x][y];
+}
+
+// Workgroup (0, 0) makes the plan; the others lay out the adapters' weights along what a product
+// sums over (the backward; tiles of 64 x 64).
+__global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* adapter, int64_t M,
+                                                                 int n, LoraPlan plan,
+                                                                 TransposeProblem a,
+                                                                 TransposeProblem b) {
+  if (blockIdx.x == 0) {
+    if (blockIdx.y == 0) make_plan(adapter, M, n, plan);
+    return;
+  }
+  const int64_t w = (int64_t)blockIdx.x - 1;
+  if (w < a.tiles)
+    transpose(a, blockIdx.y, w, adapter, M);
+  else
+    transpose(b, blockIdx.y, w - a.tiles, adapter, M);
 }
 
 // ---- s and ds ----------------------------------------------------------------------------
@@ -244,8 +307,7 @@ template <int DT>
 constexpr int row_parts() { return DT == 0 ? kParts : 1; }
 
 // A workgroup takes a tile of 32 places and a split of k, its wavefronts a quarter of that
-// each, 128 k at a time: lane l holds row l % 16 and of the 128 k the 32 from 32 (l / 16) on,
-// eight to an instruction (any order of k will do, the same for both operands).
+// each, 128 k at a time: lane l holds row l % 16 and, of each 32 k, the eight from 8 (l / 16) on.
 template <int DT, int NC>
 __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& plan, int r,
                                        int tile, int split, int64_t n_places, f32x4_t* sh) {
@@ -277,7 +339,7 @@ __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& p
   for (int64_t k = k0; k < k1; k += 128) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int64_t at = k + 32 * g + 8 * s, left = q.K - at;
+      const int64_t at = k + 32 * s + 8 * g, left = q.K - at;
       u32x4_t xv[2][N];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
@@ -359,6 +421,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(JoinProblem s, JoinProbl
     const int i = plan.order[place];
     float v = 0.0f;
     if (i >= 0) {
+#pragma unroll 8
       for (int t = 0; t < q.splits; ++t) v += q.part[(t * places + place) * r + c];
       v *= f;
     }
@@ -566,25 +629,73 @@ struct EpiLora {
   }
 };
 
+// The adapters of T tokens from j0 on, listed in LDS in the order of their first tokens by
+// wavefront 0.  The caller places a barrier behind.
+struct AdapterList {
+  int k[64];
+  int n;
+};
+
+template <int T>
+__device__ __forceinline__ void list_adapters(const LoraShare& a, int64_t j0, AdapterList& list) {
+  static_assert(T <= 64, "a token a lane");
+  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x;
+  int n = 0;
+  each_adapter(lane < T ? adapter_of(a.adapter, j0 + lane, a.cols, a.n) : -1,
+               [&](int k, uint64_t) {
+                 if (lane == 0) list.k[n] = k;
+                 ++n;
+               });
+  if (lane == 0) list.n = n;
+}
+
+// Steps of 16 or 32 of the r parts whose loads wait together.
+constexpr int kShareSteps = 4;
+
 // base + the adapters' share, without a product of its own: a wavefront takes 32 rows and 64
 // tokens.
 struct AddParams {
   LoraShare a;
-  const void* base;  // optional, of the output's type
-  int64_t ldb;
+  const void* base;  // optional: `sums` arrays (cols, ldb) of type BT, `stride` elements apart
+  int64_t ldb, stride;
+  int sums;
   void* out;
   int64_t ldo;
 };
 
+// Rows row .. row + 3 of a column, those below `rows`.
 template <int DT>
+__device__ __forceinline__ f32x4_t load4(const void* p, int64_t at, int64_t row, int64_t rows) {
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (row + 4 <= rows) {
+    if constexpr (DT == 1) {
+      u32x2_t w;
+      __builtin_memcpy(&w, static_cast<const uint16_t*>(p) + at, 8);
+      v = f32x4_t{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+    } else {
+      __builtin_memcpy(&v, static_cast<const float*>(p) + at, 16);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (row + e < rows) {
+        if constexpr (DT == 1)
+          v[e] = from_bf16(static_cast<const uint16_t*>(p)[at + e]);
+        else
+          v[e] = static_cast<const float*>(p)[at + e];
+      }
+  }
+  return v;
+}
+
+template <int DT, int BT>
 __global__ __launch_bounds__(256) void lora_add_kernel(AddParams p) {
+  __shared__ AdapterList list;
   const LoraShare& a = p.a;
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t i0 = ((int64_t)blockIdx.x * 4 + wave) * 32, j0 = (int64_t)blockIdx.y * 64;
-  if (i0 >= a.rows) return;
-  int64_t i = i0 + (lane & 31);
-  i = i < a.rows ? i : a.rows - 1;
   f32x16_t acc[2];
   int id[2];
 #pragma unroll
@@ -595,64 +706,64 @@ __global__ __launch_bounds__(256) void lora_add_kernel(AddParams p) {
     if (p.base && j < a.cols) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t row = i0 + 8 * q + 4 * half, at = j * p.ldb + row;
-        if (row + 4 <= a.rows) {
-          if constexpr (DT == 1) {
-            u32x2_t w;
-            __builtin_memcpy(&w, static_cast<const uint16_t*>(p.base) + at, 8);
-            acc[b][4 * q] = bf16_lo(w[0]);
-            acc[b][4 * q + 1] = bf16_hi(w[0]);
-            acc[b][4 * q + 2] = bf16_lo(w[1]);
-            acc[b][4 * q + 3] = bf16_hi(w[1]);
-          } else {
-            f32x4_t w;
-            __builtin_memcpy(&w, static_cast<const float*>(p.base) + at, 16);
+        const int64_t row = i0 + 8 * q + 4 * half;
+        const f32x4_t v = load4<BT>(p.base, j * p.ldb + row, row, a.rows);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[b][4 * q + e] = w[e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (row + e < a.rows) {
-              if constexpr (DT == 1)
-                acc[b][4 * q + e] = from_bf16(static_cast<const uint16_t*>(p.base)[at + e]);
-              else
-                acc[b][4 * q + e] = static_cast<const float*>(p.base)[at + e];
-            }
-        }
+        for (int e = 0; e < 4; ++e) acc[b][4 * q + e] = v[e];
       }
     }
   }
-  const int chunks = a.r / 8, all = chunks * a.parts;
-  uint64_t left[2] = {__ballot(id[0] >= 0), __ballot(id[1] >= 0)};
-  while (left[0] | left[1]) {
-    const int k = left[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(left[0]))
-                          : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(left[1]));
-    const uint16_t* u = a.u + ((int64_t)k * a.rows + i) * a.r;
-    f32x16_t v[2] = {};
-    uint64_t match[2];
+  // further sums of a split product, in order
+  for (int t = 1; t < p.sums; ++t)
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      match[b] = __ballot(id[b] == k);
-      left[b] &= ~match[b];
+      const int64_t j = j0 + 32 * b + (lane & 31);
+      if (j >= a.cols) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t row = i0 + 8 * q + 4 * half;
+        const f32x4_t v = load4<BT>(p.base, t * p.stride + j * p.ldb + row, row, a.rows);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[b][4 * q + e] += v[e];
+      }
     }
-    for (int c = 0; c < all; c += 2) {
-      const int q = c + half;  // may pass the end by one: s is 0 there
-      const bf16x8_t uf = as_bf16x8(load16(u + 8 * (q % chunks)));
+  list_adapters<64>(a, j0, list);
+  lds_barrier();
+  if (i0 >= a.rows) return;
+  int64_t i = i0 + (lane & 31);
+  i = i < a.rows ? i : a.rows - 1;
+  const int chunks = a.r / 8, all = chunks * a.parts;
+  const int steps = (all + 1) / 2, total = list.n * steps;
+  // a step: 16 of the r parts of one adapter
+  for (int s0 = 0; s0 < total; s0 += kShareSteps) {
+    u32x4_t uf[kShareSteps], sf[kShareSteps][2];
+    int kk[kShareSteps];
+#pragma unroll
+    for (int t = 0; t < kShareSteps; ++t) {
+      const int s = s0 + t < total ? s0 + t : total - 1;  // past the end: read again, not used
+      const int k = __builtin_amdgcn_readfirstlane(list.k[s / steps]);
+      const int q = 2 * (s % steps) + half;  // may pass the end by one: s is 0 there
+      kk[t] = k;
+      uf[t] = load16(a.u + ((int64_t)k * a.rows + i) * a.r + 8 * (q % chunks));
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        if (!match[b]) continue;
-        u32x4_t sf = {0, 0, 0, 0};
+        sf[t][b] = u32x4_t{0, 0, 0, 0};
         if (id[b] == k && q < all)
-          sf = load16(a.s2 + (j0 + 32 * b + (lane & 31)) * kParts * a.r + 8 * q);
-        v[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf, as_bf16x8(sf), v[b], 0, 0, 0);
+          sf[t][b] = load16(a.s2 + (j0 + 32 * b + (lane & 31)) * kParts * a.r + 8 * q);
       }
     }
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const bool own = id[b] == k;
+    for (int t = 0; t < kShareSteps; ++t) {
+      if (s0 + t >= total) break;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[b][e] += own ? v[b][e] : 0.0f;
+      for (int b = 0; b < 2; ++b) {
+        const bool own = id[b] == kk[t];
+        if (!__ballot(own)) continue;
+        const f32x16_t v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            as_bf16x8(uf[t]), as_bf16x8(sf[t][b]), f32x16_t{}, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[b][e] += own ? v[e] : 0.0f;
+      }
     }
   }
 #pragma unroll
@@ -660,6 +771,62 @@ __global__ __launch_bounds__(256) void lora_add_kernel(AddParams p) {
     const int64_t j = j0 + 32 * b + (lane & 31);
     store_block<DT>(p.out, j * p.ldo + i0, acc[b], half, a.rows - i0, j < a.cols);
   }
+}
+
+template <int DT, int BT>
+hipError_t run_add(const AddParams& p, hipStream_t stream) {
+  if (p.a.cols == 0) return hipSuccess;
+  hipLaunchKernelGGL((lora_add_kernel<DT, BT>),
+                     dim3((unsigned)((p.a.rows + 127) / 128), (unsigned)((p.a.cols + 63) / 64)),
+                     dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+// ---- a product split over k -------------------------------------------------------------------
+
+// Few tiles with a long sum: split t takes k from t per on and stores its FP32 sums (cols, rows) at
+// out + t stride; lora_add_kernel adds them up.
+struct EpiSum {
+  struct Params {
+    float* out;
+    int64_t rows, cols;
+  };
+  __device__ static void apply(const Params& p, f32x16_t (&acc)[NA][NB], int64_t i0, int64_t j0,
+                               int wr, int wc, int lane, uint16_t*) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int64_t j = j0 + wc * WN + 32 * b + (lane & 31);
+      if (j >= p.cols) continue;
+#pragma unroll
+      for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t i = i0 + wr * WM + 32 * t + 8 * q + 4 * (lane >> 5);
+          if (i < p.rows)  // a multiple of 8
+            *reinterpret_cast<f32x4_t*>(p.out + j * p.rows + i) =
+                f32x4_t{acc[t][b][4 * q], acc[t][b][4 * q + 1], acc[t][b][4 * q + 2],
+                        acc[t][b][4 * q + 3]};
+        }
+    }
+  }
+};
+
+template <bool MASK, int NSEG>
+__global__ __launch_bounds__(NT, 1) void lora_split_kernel(Segs<NSEG> G, int64_t K, int64_t per,
+                                                           int n_ti, int n_tj, EpiSum::Params ep) {
+  __shared__ __attribute__((aligned(1024))) uint16_t smem[kSmemElems];
+  const int n = n_ti * n_tj, t = blockIdx.x / n;
+  const int64_t k0 = t * per;
+#pragma unroll
+  for (int s = 0; s < NSEG; ++s) {
+    G.P[s].base += k0 * G.P[s].ld;  // dim-contiguous
+    G.P[s].k_limit -= k0;
+    G.Q[s].base += k0;
+    G.Q[s].k_limit -= k0;
+  }
+  ep.out += t * ep.rows * ep.cols;
+  gemm_tile<EpiSum, true, false, MASK, NSEG>(G, K - k0 < per ? K - k0 : per, blockIdx.x - t * n,
+                                             n_ti, n_tj, ep, smem);
 }
 
 // ---- the adapters' gradients ------------------------------------------------------------------
@@ -793,34 +960,6 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterProblem b, OuterPr
 
 // ---- layouts ----------------------------------------------------------------------------------
 
-// (n, R, C) to (n, C, ldr), the places from R to ldr zero; adapters without tokens are left out.
-struct TransposeProblem {
-  const uint16_t* in;
-  uint16_t* out;
-  int64_t R, C, ldr;
-};
-
-__global__ __launch_bounds__(256) void lora_transpose_kernel(TransposeProblem a,
-                                                             TransposeProblem b, LoraPlan plan,
-                                                             int64_t tiles_a) {
-  __shared__ uint16_t sh[64][66];
-  const int k = blockIdx.y;
-  if (plan.first[k] == plan.first[k + 1]) return;
-  const bool second = (int64_t)blockIdx.x >= tiles_a;
-  const TransposeProblem q = second ? b : a;
-  const int64_t w = second ? blockIdx.x - tiles_a : blockIdx.x;
-  const int64_t nc = (q.C + 63) / 64;
-  const int64_t r0 = w / nc * 64, c0 = w % nc * 64;
-  const uint16_t* in = q.in + k * q.R * q.C;
-  uint16_t* out = q.out + k * q.C * q.ldr;
-  const int x = threadIdx.x & 63;
-  for (int y = threadIdx.x >> 6; y < 64; y += 4)
-    sh[y][x] = r0 + y < q.R && c0 + x < q.C ? in[(r0 + y) * q.C + c0 + x] : (uint16_t)0;
-  __syncthreads();
-  for (int y = threadIdx.x >> 6; y < 64; y += 4)
-    if (c0 + y < q.C && r0 + x < q.ldr) out[(c0 + y) * q.ldr + r0 + x] = sh[x][y];
-}
-
 // dy (M, V) as rows of ldv BF16 numbers, zeros behind V: for rows that the product cannot read in
 // place.  FP32 as two planes, its first two parts: the product's result is BF16.
 template <int DT>
@@ -841,12 +980,13 @@ __global__ __launch_bounds__(256) void lora_rows_kernel(const void* dy, int64_t 
 
 // ---- few tokens -------------------------------------------------------------------------------
 
-// Up to 64 tokens: W is streamed once against X in LDS, 16 kFrags rows a wavefront, straight
-// into operand registers, a superstep of 128 k ahead.  X's rows of kX elements; the 16-byte chunk q of
-// token c lies at q ^ (c % 16) in its group of 16, so that 16 tokens' reads of one chunk
-// meet all banks once.
+// Up to 64 tokens: W is streamed once against X in LDS, 16 F rows a wavefront, straight into
+// operand registers, 128 k ahead of the product.  X lies in two parts of KX k that take turns: the
+// next one's loads go to registers while this one is multiplied.  In LDS the 16-byte
+// chunk q of token c lies at q ^ (c % 16) in its group of 16, so that 16 tokens' reads of one
+// chunk meet all banks once.  The adapters' share comes first, under W's first loads.
 template <int T>
-constexpr int skinny_k() { return T == 16 ? 2048 : T == 32 ? 1024 : 512; }
+constexpr int skinny_k() { return 16384 / T; }  // 32 KB
 
 struct SkinnyParams {
   const uint16_t* x;
@@ -859,17 +999,21 @@ struct SkinnyParams {
 
 template <int T, int F, int DT>
 __global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
-  constexpr int KX = skinny_k<T>(), NT16 = T / 16;
-  __shared__ __attribute__((aligned(256))) uint16_t xs[T * KX];
+  constexpr int KX = skinny_k<T>(), NT16 = T / 16, kX = T * KX / 8 / 256;  // 16-byte chunks each
+  __shared__ __attribute__((aligned(256))) uint16_t xs[2][T * KX];
+  __shared__ AdapterList list;
+  const LoraShare& a = p.a;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t v0 = (int64_t)blockIdx.x * (64 * F) + wave * (16 * F);
   const uint16_t* wr[F];
+  int64_t vrow[F];
   f32x4_t acc[F][NT16];
 #pragma unroll
   for (int f = 0; f < F; ++f) {
     const int64_t row = v0 + 16 * f + c;
-    wr[f] = p.w + (row < p.a.rows ? row : p.a.rows - 1) * p.K;  // past the end the last row
+    vrow[f] = row < a.rows ? row : a.rows - 1;  // past the end the last row
+    wr[f] = p.w + vrow[f] * p.K;
 #pragma unroll
     for (int t = 0; t < NT16; ++t) acc[f][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -879,19 +1023,35 @@ __global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
     for (int f = 0; f < F; ++f)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const int64_t at = k + 32 * g + 8 * s;
+        const int64_t at = k + 32 * s + 8 * g;
         q[f][s] = u32x4_t{0, 0, 0, 0};
         if (at < p.K) q[f][s] = load16(wr[f] + at);
       }
   };
-  auto multiply = [&](const Frag& q, int kk) {  // kk: of the part in LDS
+  u32x4_t xr[kX];
+  auto fetch_x = [&](int64_t k0) {
+#pragma unroll
+    for (int e = 0; e < kX; ++e) {
+      const int at = e * 256 + threadIdx.x, tok = at / (KX / 8), ch = at % (KX / 8);
+      xr[e] = u32x4_t{0, 0, 0, 0};
+      if (tok < a.cols && k0 + ch * 8 < p.K) xr[e] = load16(p.x + tok * p.ldx + k0 + ch * 8);
+    }
+  };
+  auto put_x = [&](uint16_t* to) {
+#pragma unroll
+    for (int e = 0; e < kX; ++e) {
+      const int at = e * 256 + threadIdx.x, tok = at / (KX / 8), ch = at % (KX / 8);
+      *reinterpret_cast<u32x4_t*>(to + tok * KX + (ch ^ (tok & 15)) * 8) = xr[e];
+    }
+  };
+  auto multiply = [&](const Frag& q, const uint16_t* x, int kk) {  // kk: of the part in LDS
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       bf16x8_t xv[NT16];
 #pragma unroll
       for (int t = 0; t < NT16; ++t) {
-        const int ch = kk / 8 + 4 * g + s;
-        xv[t] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(xs + (16 * t + c) * KX + (ch ^ c) * 8));
+        const int ch = kk / 8 + 4 * s + g;
+        xv[t] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(x + (16 * t + c) * KX + (ch ^ c) * 8));
       }
 #pragma unroll
       for (int f = 0; f < F; ++f)
@@ -902,85 +1062,74 @@ __global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
     }
   };
   Frag q[2];
+  fetch_x(0);
   fetch(q[0], 0);
-  for (int64_t k0 = 0; k0 < p.K; k0 += KX) {
-    if (k0) __syncthreads();
-    for (int e = threadIdx.x; e < T * KX / 8; e += 256) {
-      const int tok = e / (KX / 8), ch = e % (KX / 8);
-      u32x4_t v = {0, 0, 0, 0};
-      if (tok < p.a.cols && k0 + ch * 8 < p.K) v = load16(p.x + tok * p.ldx + k0 + ch * 8);
-      *reinterpret_cast<u32x4_t*>(xs + tok * KX + (ch ^ (tok & 15)) * 8) = v;
+  int id[NT16];
+#pragma unroll
+  for (int t = 0; t < NT16; ++t) id[t] = adapter_of(a.adapter, 16 * t + c, a.cols, a.n);
+  list_adapters<T>(a, 0, list);
+  put_x(xs[0]);
+  lds_barrier();
+  {
+    // a step: 32 of the r parts of one adapter
+    const int chunks = a.r / 8, all = chunks * a.parts;
+    const int steps = (all + 3) / 4, total = list.n * steps;
+    for (int s0 = 0; s0 < total; s0 += kShareSteps) {
+      u32x4_t uf[kShareSteps][F], sf[kShareSteps][NT16];
+      int kk[kShareSteps];
+#pragma unroll
+      for (int j = 0; j < kShareSteps; ++j) {
+        const int s = s0 + j < total ? s0 + j : total - 1;  // past the end: read again, not used
+        const int k = __builtin_amdgcn_readfirstlane(list.k[s / steps]);
+        const int ch = 4 * (s % steps) + g;
+        kk[j] = k;
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          uf[j][f] = u32x4_t{0, 0, 0, 0};
+          if (ch < all)
+            uf[j][f] = load16(a.u + ((int64_t)k * a.rows + vrow[f]) * a.r + 8 * (ch % chunks));
+        }
+#pragma unroll
+        for (int t = 0; t < NT16; ++t) {
+          sf[j][t] = u32x4_t{0, 0, 0, 0};
+          if (id[t] == k && ch < all)
+            sf[j][t] = load16(a.s2 + (int64_t)(16 * t + c) * kParts * a.r + 8 * ch);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kShareSteps; ++j) {
+        if (s0 + j >= total) break;
+#pragma unroll
+        for (int t = 0; t < NT16; ++t) {
+          const bool own = id[t] == kk[j];
+          if (!__ballot(own)) continue;
+#pragma unroll
+          for (int f = 0; f < F; ++f) {
+            const f32x4_t v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                as_bf16x8(uf[j][f]), as_bf16x8(sf[j][t]), f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0,
+                0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[f][t][e] += own ? v[e] : 0.0f;
+          }
+        }
+      }
     }
-    __syncthreads();
-    const int n = (int)((p.K - k0 < KX ? p.K - k0 : KX) + 127) / 128;  // supersteps
+  }
+  int part = 0;
+  for (int64_t k0 = 0; k0 < p.K; k0 += KX, part ^= 1) {
+    const bool more = k0 + KX < p.K;
+    if (more) fetch_x(k0 + KX);
+    const int n = (int)((p.K - k0 < KX ? p.K - k0 : KX) + 127) / 128;  // of 128 k
     for (int ss = 0; ss < n; ss += 2) {
       fetch(q[1], k0 + 128 * (ss + 1));
-      multiply(q[0], 128 * ss);
-      // an odd number of supersteps is the last part's alone: q[1] is past K then
+      multiply(q[0], xs[part], 128 * ss);
+      // an odd number is the last part's alone: q[1] is past K then
       fetch(q[0], k0 + 128 * (ss + 2));
-      if (ss + 1 < n) multiply(q[1], 128 * (ss + 1));
+      if (ss + 1 < n) multiply(q[1], xs[part], 128 * (ss + 1));
     }
-  }
-  // the adapters' share: 32 of the r parts an instruction
-  const LoraShare& a = p.a;
-  const int chunks = a.r / 8, all = chunks * a.parts;
-  int id[NT16];
-  uint64_t left[NT16], some = 0;
-#pragma unroll
-  for (int t = 0; t < NT16; ++t) {
-    id[t] = adapter_of(a.adapter, 16 * t + c, a.cols, a.n);
-    left[t] = __ballot(id[t] >= 0);
-    some |= left[t];
-  }
-  while (some) {
-    int k = 0;
-    bool found = false;
-#pragma unroll
-    for (int t = 0; t < NT16; ++t)
-      if (!found && left[t]) {
-        k = __builtin_amdgcn_readlane(id[t], __builtin_ctzll(left[t]));
-        found = true;
-      }
-    uint64_t match[NT16];
-    some = 0;
-#pragma unroll
-    for (int t = 0; t < NT16; ++t) {
-      match[t] = __ballot(id[t] == k);
-      left[t] &= ~match[t];
-      some |= left[t];
-    }
-    f32x4_t v[F][NT16] = {};
-    for (int c0 = 0; c0 < all; c0 += 4) {
-      const int ch = c0 + g;
-      u32x4_t uf[F];
-#pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const int64_t row = v0 + 16 * f + c;
-        uf[f] = u32x4_t{0, 0, 0, 0};
-        if (ch < all)
-          uf[f] = load16(a.u + ((int64_t)k * a.rows + (row < a.rows ? row : a.rows - 1)) * a.r +
-                         8 * (ch % chunks));
-      }
-#pragma unroll
-      for (int t = 0; t < NT16; ++t) {
-        if (!match[t]) continue;
-        u32x4_t sf = {0, 0, 0, 0};
-        if (id[t] == k && ch < all)
-          sf = load16(a.s2 + (int64_t)(16 * t + c) * kParts * a.r + 8 * ch);
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-          v[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(uf[f]), as_bf16x8(sf),
-                                                            v[f][t], 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < NT16; ++t) {
-      const bool own = id[t] == k;
-#pragma unroll
-      for (int f = 0; f < F; ++f)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[f][t][e] += own ? v[f][t][e] : 0.0f;
-    }
+    // the other part was read before the last barrier
+    if (more) put_x(xs[part ^ 1]);
+    lds_barrier();
   }
 #pragma unroll
   for (int t = 0; t < NT16; ++t) {
@@ -1038,6 +1187,26 @@ inline Split split_of(int64_t K, int64_t tiles) {
   r.per = (K + s * 512 - 1) / (s * 512) * 512;
   r.n = (int)((K + r.per - 1) / r.per);
   return r;
+}
+
+// Splits of the sum over V in dy W.  A tile's 256 k take about 5 us with all CUs at work, and
+// a part's sums are written and read again at some 5 TB/s; parts of 1024 at least.
+inline Split product_split(int64_t M, int64_t H, int64_t V) {
+  const int64_t tiles = (M + BN - 1) / BN * ((H + BM - 1) / BM);
+  Split best{1, V};
+  double least = 0.0;
+  for (int s = 1; s <= 16; ++s) {
+    const int64_t per = (V + s * 2 * BK - 1) / (s * 2 * BK) * 2 * BK;
+    const int64_t n = (V + per - 1) / per;
+    if (s > 1 && per < 1024) break;
+    const double t = (double)((tiles * n + 255) / 256) * (double)per * 0.02 +
+                     (n > 1 ? (double)(n * M * H) * 1.6e-6 : 0.0);
+    if (s == 1 || t < 0.95 * least) {
+      least = t;
+      best = Split{(int)n, per};
+    }
+  }
+  return best;
 }
 
 struct Places {
@@ -1105,11 +1274,7 @@ hipError_t run_skinny(const SkinnyParams& p, hipStream_t stream) {
 template <int DT>
 hipError_t forward_tiles(const LoraFwdArgs& p, const LoraShare& a, hipStream_t stream) {
   if (!p.w) {
-    const AddParams q{a, p.base, p.ldb, p.out, p.ldo};
-    hipLaunchKernelGGL((lora_add_kernel<DT>),
-                       dim3((unsigned)((p.V + 127) / 128), (unsigned)((p.M + 63) / 64)), dim3(256),
-                       0, stream, q);
-    return hipGetLastError();
+    return run_add<DT, DT>(AddParams{a, p.base, p.ldb, 0, 1, p.out, p.ldo}, stream);
   }
   if (p.M <= kSkinny) {
     const SkinnyParams q{p.x, p.ldx, p.H, p.w, a, p.out, p.ldo};
@@ -1150,7 +1315,7 @@ hipError_t launch_lora_forward(const LoraFwdArgs& p, char* ws, hipStream_t strea
     const Split sp = split_of(p.H, tiles);
     float* part = reinterpret_cast<float*>(ws + pl.end);
     hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.adapter, p.M,
-                       p.n, plan);
+                       p.n, plan, TransposeProblem{}, TransposeProblem{});
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const ShrinkProblem s{p.x, p.ldx, p.H, p.a, p.H, part, sp.n, sp.per};
     const ShrinkProblem none{};
@@ -1170,7 +1335,8 @@ namespace {
 struct BwdPlan {
   int64_t tiles, ldv;
   Split ss, sd;
-  size_t s_part, d_part, s_place, d_place, d_token, at, bt, rows, total;
+  Split dx;
+  size_t s_part, d_part, s_place, d_place, d_token, at, bt, rows, dx_part, total;
   Places places;
   BwdPlan(int64_t M, int64_t H, int64_t V, int64_t n, int64_t r, int dtype)
       : places(M, n, 0) {
@@ -1187,9 +1353,33 @@ struct BwdPlan {
     at = up256(d_token + (size_t)M * kParts * r * 2);
     bt = up256(at + (size_t)n * r * H * 2);
     rows = up256(bt + (size_t)n * r * ldv * 2);
-    total = up256(rows + (size_t)M * ldv * 2 * (dtype == 0 ? 2 : 1)) + 256;
+    dx = product_split(M, H, V);
+    dx_part = up256(rows + (size_t)M * ldv * 2 * (dtype == 0 ? 2 : 1));
+    total = up256(dx_part + (dx.n > 1 ? (size_t)dx.n * M * H * 4 : 0)) + 256;
   }
 };
+
+// dx = dy W + the adapters' share, the sum over V in sp.n parts.
+template <int NSEG>
+hipError_t dx_product(const Segs<NSEG>& G, const LoraBwdArgs& p, const LoraShare& a,
+                      const Split& sp, float* part, hipStream_t stream) {
+  if (sp.n == 1)
+    return run_gemm<EpiLora<1>, true, false, NSEG>(G, p.H, p.M, p.V,
+                                                   typename EpiLora<1>::Params{a, p.dx, p.H},
+                                                   stream);
+  const int n_ti = (int)((p.H + BM - 1) / BM), n_tj = (int)((p.M + BN - 1) / BN);
+  const EpiSum::Params ep{part, p.H, p.M};
+  const dim3 grid((unsigned)(n_ti * n_tj * sp.n));
+  if (p.V % (2 * BK) != 0)
+    hipLaunchKernelGGL((lora_split_kernel<true, NSEG>), grid, dim3(NT), 0, stream, G, p.V, sp.per,
+                       n_ti, n_tj, ep);
+  else
+    hipLaunchKernelGGL((lora_split_kernel<false, NSEG>), grid, dim3(NT), 0, stream, G, p.V, sp.per,
+                       n_ti, n_tj, ep);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return run_add<1, 0>(AddParams{a, part, p.H, p.M * p.H, sp.n, p.dx, p.H}, stream);
+}
 
 template <int DT>
 hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
@@ -1199,13 +1389,10 @@ hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
   auto bf = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
   auto fp = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   hipError_t e;
-  hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.adapter, p.M, p.n,
-                     plan);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const TransposeProblem ta{p.a, bf(b.at), p.r, p.H, p.r}, tb{p.b, bf(b.bt), p.V, p.r, b.ldv};
-  auto n_tr = [](const TransposeProblem& t) { return (t.ldr + 63) / 64 * ((t.C + 63) / 64); };
-  hipLaunchKernelGGL(lora_transpose_kernel, dim3((unsigned)(n_tr(ta) + n_tr(tb)), (unsigned)p.n),
-                     dim3(256), 0, stream, ta, tb, plan, n_tr(ta));
+  const TransposeProblem ta = transpose_of(p.a, bf(b.at), p.r, p.H, p.r);
+  const TransposeProblem tb = transpose_of(p.b, bf(b.bt), p.V, p.r, b.ldv);
+  hipLaunchKernelGGL(lora_plan_kernel, dim3((unsigned)(1 + ta.tiles + tb.tiles), (unsigned)p.n),
+                     dim3(kPlanThreads), 0, stream, p.adapter, p.M, p.n, plan, ta, tb);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const ShrinkProblem s{p.x, p.ldx, p.H, p.a, p.H, fp(b.s_part), b.ss.n, b.ss.per};
   const ShrinkProblem d{p.dy, p.ldy, p.V, bf(b.bt), b.ldv, fp(b.d_part), b.sd.n, b.sd.per};
@@ -1218,11 +1405,7 @@ hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
   if (p.dx && p.M > 0) {
     const LoraShare a{bf(b.at), bf(b.d_token), p.adapter, p.n, p.r, 2, p.H, p.M};
     if (!p.w) {
-      const AddParams q{a, p.dx_base, p.H, p.dx, p.H};
-      hipLaunchKernelGGL((lora_add_kernel<1>),
-                         dim3((unsigned)((p.H + 127) / 128), (unsigned)((p.M + 63) / 64)),
-                         dim3(256), 0, stream, q);
-      e = hipGetLastError();
+      e = run_add<1, 1>(AddParams{a, p.dx_base, p.H, 0, 1, p.dx, p.H}, stream);
     } else {
       const uint16_t* rows = static_cast<const uint16_t*>(p.dy);
       int64_t ld = p.ldy;
@@ -1238,14 +1421,12 @@ hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
       }
       // W (V, H): element (h, v) at v H + h
       const Operand W{p.w, p.H, p.H, p.V};
-      const typename EpiLora<1>::Params ep{a, p.dx, p.H};
       if constexpr (DT == 0) {
         const Operand hi{rows, ld, p.M, p.V}, lo{rows + p.M * b.ldv, ld, p.M, p.V};
-        e = run_gemm<EpiLora<1>, true, false, 2>(Segs<2>{{W, W}, {hi, lo}}, p.H, p.M, p.V, ep,
-                                                 stream);
+        e = dx_product<2>(Segs<2>{{W, W}, {hi, lo}}, p, a, b.dx, fp(b.dx_part), stream);
       } else {
         const Operand Y{rows, ld, p.M, p.V};
-        e = run_gemm<EpiLora<1>, true, false>(W, Y, p.H, p.M, p.V, ep, stream);
+        e = dx_product<1>(Segs<1>{{W}, {Y}}, p, a, b.dx, fp(b.dx_part), stream);
       }
     }
     if (e != hipSuccess) return e;
