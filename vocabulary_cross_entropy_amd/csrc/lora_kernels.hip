@@ -15,6 +15,8 @@
 //    adapter's weights cannot reach another's tokens).
 //  * Tokens sorted by adapter (lora_plan_kernel: places of 32, each of one adapter): s and ds,
 //    and the adapters' gradients, which sum over the tokens of one adapter.
+#include <math.h>
+
 #include "gemm_core.h"
 #include "lora.h"
 
@@ -253,7 +255,8 @@ __global__ __launch_bounds__(256) void lora_token_kernel(LoraFwdArgs p, uint16_t
 }
 
 // Sums over k of a tile's token rows times its adapter's rows: part[split][place][c] =
-// sum over the split's k of X(order[place], k) U_adapter(c, k), X (M, K) and U (n, r, ldu).
+// sum over the split's k of X(order[place], k) U_adapter(c, k), X (M, K) and U (n, r, ldu).  One
+// split alone finishes them itself.
 struct ShrinkProblem {
   const void* x;
   int64_t ldx, K;
@@ -261,8 +264,22 @@ struct ShrinkProblem {
   int64_t ldu;
   float* part;
   int splits;
-  int64_t per;  // k of a split: a multiple of 512
+  int64_t per;         // k of a split: a multiple of 512
+  uint16_t* by_token;  // optional: the sums times the scale in parts, (M, parts, r),
+  uint16_t* by_place;  // optional: and (parts, r, places) for the gradients
 };
+
+// One sum of a place (token i, or none: 0) and its parts.
+__device__ __forceinline__ void finish_sum(const ShrinkProblem& q, float v, int i, int64_t place,
+                                           int c, int r, int64_t places) {
+  uint16_t part[kParts];
+  parts_of(i >= 0 ? v : 0.0f, part);
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) {
+    if (q.by_token && i >= 0) q.by_token[((int64_t)i * kParts + h) * r + c] = part[h];
+    if (q.by_place) q.by_place[((int64_t)h * r + c) * places + place] = part[h];
+  }
+}
 
 // Eight elements of a row from `at` on, `left` of them before its end and 0 past it, in N BF16
 // parts (one for a BF16 row).
@@ -307,52 +324,64 @@ template <int DT>
 constexpr int row_parts() { return DT == 0 ? kParts : 1; }
 
 // A workgroup takes a tile of 32 places and a split of k, its wavefronts a quarter of that
-// each, 128 k at a time: lane l holds row l % 16 and, of each 32 k, the eight from 8 (l / 16) on.
+// each, 128 k at a time, the next 128 k's loads in flight: lane l holds row l % 16 and, of each
+// 32 k, the eight from 8 (l / 16) on.  Places without a token read row 0; nobody reads their sums.
 template <int DT, int NC>
-__device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& plan, int r,
-                                       int tile, int split, int64_t n_places, f32x4_t* sh) {
+__device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& plan,
+                                       const float* scale, int r, int tile, int split,
+                                       int64_t places, f32x4_t* sh) {
   constexpr int N = row_parts<DT>();
+  constexpr int S = DT == 1 && NC <= 2 ? 4 : 1;  // steps of 32 k whose loads wait together
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, c = lane & 15;
   const int k_adapter = plan.owner[tile];
+  int token[2];
   int64_t row[2];
-  bool have[2];
 #pragma unroll
   for (int f = 0; f < 2; ++f) {
-    const int i = plan.order[tile * kTile + 16 * f + c];
-    have[f] = i >= 0;
-    row[f] = (int64_t)(i < 0 ? 0 : i) * q.ldx;
+    token[f] = plan.order[tile * kTile + 16 * f + c];
+    row[f] = (int64_t)(token[f] < 0 ? 0 : token[f]) * q.ldx + 8 * g;
   }
   const uint16_t* u[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int cc = 16 * j + c < r ? 16 * j + c : r - 1;
-    u[j] = q.u + ((int64_t)k_adapter * r + cc) * q.ldu;
+    u[j] = q.u + ((int64_t)k_adapter * r + cc) * q.ldu + 8 * g;
   }
   f32x4_t acc[2][NC];
 #pragma unroll
   for (int f = 0; f < 2; ++f)
 #pragma unroll
     for (int j = 0; j < NC; ++j) acc[f][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t k0 = split * q.per + wave * (q.per / 4);
-  const int64_t k1 = k0 + q.per / 4 < q.K ? k0 + q.per / 4 : q.K;
-  for (int64_t k = k0; k < k1; k += 128) {
+  struct Buf {
+    u32x4_t x[S][2][N], u[S][NC];
+  };
+  // 32 S k from k on; TAIL: they may pass the end
+  auto load = [&](Buf& b, int64_t k, auto tail) {
+    constexpr bool TAIL = decltype(tail)::value;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int64_t at = k + 32 * s + 8 * g, left = q.K - at;
-      u32x4_t xv[2][N];
+    for (int s = 0; s < S; ++s) {
+      const int64_t at = k + 32 * s, left = q.K - at - 8 * g;
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
+        if constexpr (TAIL) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) xv[f][i] = u32x4_t{0, 0, 0, 0};
-        if (have[f] && left > 0) row8<DT, N>(q.x, row[f] + at, left, xv[f]);
+          for (int i = 0; i < N; ++i) b.x[s][f][i] = u32x4_t{0, 0, 0, 0};
+          if (left > 0) row8<DT, N>(q.x, row[f] + at, left, b.x[s][f]);
+        } else {
+          row8<DT, N>(q.x, row[f] + at, 8, b.x[s][f]);
+        }
       }
-      u32x4_t uv[NC];
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        uv[j] = u32x4_t{0, 0, 0, 0};
-        if (left > 0) uv[j] = load16(u[j] + at);
+        if (TAIL) b.u[s][j] = u32x4_t{0, 0, 0, 0};
+        if (!TAIL || left > 0) b.u[s][j] = load16(u[j] + at);
       }
+    }
+  };
+  auto multiply = [&](const Buf& b) {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int f = 0; f < 2; ++f)
 #pragma unroll
@@ -361,10 +390,33 @@ __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& p
 #pragma unroll
           for (int i = 0; i < N; ++i)
             acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                as_bf16x8(uv[j]), as_bf16x8(xv[f][i]), acc[f][j], 0, 0, 0);
-    }
+                as_bf16x8(b.u[s][j]), as_bf16x8(b.x[s][f][i]), acc[f][j], 0, 0, 0);
+  };
+  const int64_t k0 = split * q.per + wave * (q.per / 4);
+  const int64_t k1 = k0 + q.per / 4 < q.K ? k0 + q.per / 4 : q.K;
+  const int64_t whole = k1 > k0 ? (k1 - k0) / (32 * S) : 0;  // steps that lie inside
+  Buf b[2];
+  int64_t k = k0;
+  if (whole > 0) load(b[0], k, std::false_type{});
+  for (int64_t n = 0; n + 2 <= whole; n += 2, k += 64 * S) {
+    load(b[1], k + 32 * S, std::false_type{});
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b[0]);
+    // past the end the last step again, not used
+    load(b[0], n + 2 < whole ? k + 64 * S : k, std::false_type{});
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b[1]);
+  }
+  if (whole & 1) {
+    multiply(b[0]);
+    k += 32 * S;
+  }
+  for (; k < k1; k += 32 * S) {
+    load(b[0], k, std::true_type{});
+    multiply(b[0]);
   }
   // the four wavefronts' sums in order
+  const float factor = scale ? scale[k_adapter] : 1.0f;
 #pragma unroll
   for (int f = 0; f < 2; ++f)
 #pragma unroll
@@ -372,12 +424,17 @@ __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& p
       __syncthreads();
       sh[wave * 64 + lane] = acc[f][j];
       __syncthreads();
-      if (wave == 0) {
+      if (wave == ((2 * j + f) & 3)) {
         const f32x4_t v = (sh[lane] + sh[64 + lane]) + (sh[128 + lane] + sh[192 + lane]);
         const int cc = 16 * j + 4 * g;
-        if (cc < r) {  // r is a multiple of 8
-          const int64_t place = (int64_t)tile * kTile + 16 * f + c;
-          *reinterpret_cast<f32x4_t*>(q.part + (split * n_places + place) * r + cc) = v;
+        const int64_t place = (int64_t)tile * kTile + 16 * f + c;
+        if (cc >= r) continue;  // r is a multiple of 8
+        if (q.splits > 1) {
+          *reinterpret_cast<f32x4_t*>(q.part + (split * places + place) * r + cc) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            finish_sum(q, v[e] * factor, token[f], place, cc + e, r, places);
         }
       }
     }
@@ -386,52 +443,34 @@ __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& p
 // Two problems in one grid: s from x (BF16) and, in the backward, ds from dy.
 template <int DT, int NC>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(ShrinkProblem s, ShrinkProblem d,
-                                                          LoraPlan plan, int n, int r,
-                                                          int n_tiles) {
+                                                          LoraPlan plan, const float* scale, int n,
+                                                          int r, int n_tiles) {
   __shared__ f32x4_t sh[256];
   const int tile = blockIdx.x, split = blockIdx.y;
   if (tile >= plan.first[n]) return;
   const int64_t places = (int64_t)n_tiles * kTile;
   if (split < d.splits)
-    shrink<DT, NC>(d, plan, r, tile, split, places, sh);
+    shrink<DT, NC>(d, plan, scale, r, tile, split, places, sh);
   else
-    shrink<1, NC>(s, plan, r, tile, split - d.splits, places, sh);
+    shrink<1, NC>(s, plan, scale, r, tile, split - d.splits, places, sh);
 }
 
-// The splits' sums joined in order, scaled, in parts: by token (M, parts, r) for the tiles and by
-// place (parts, r, places) for the gradients.
-struct JoinProblem {
-  const float* part;
-  int splits;
-  uint16_t* by_token;  // optional
-  uint16_t* by_place;  // optional
-};
-
-__global__ __launch_bounds__(256) void lora_join_kernel(JoinProblem s, JoinProblem d,
+// The splits' sums joined in order.
+__global__ __launch_bounds__(256) void lora_join_kernel(ShrinkProblem s, ShrinkProblem d,
                                                         LoraPlan plan, const float* scale, int n,
                                                         int r, int n_tiles) {
-  const JoinProblem q = blockIdx.y ? d : s;
+  const ShrinkProblem q = blockIdx.y ? d : s;
   const int64_t places = (int64_t)n_tiles * kTile;
   const int tile = blockIdx.x;
-  if (tile >= plan.first[n]) return;
-  const float f = scale ? scale[plan.owner[tile]] : 1.0f;
+  if (q.splits <= 1 || tile >= plan.first[n]) return;
+  const float factor = scale ? scale[plan.owner[tile]] : 1.0f;
   for (int e = threadIdx.x; e < kTile * r; e += 256) {
     const int c = e % r;
     const int64_t place = (int64_t)tile * kTile + e / r;
-    const int i = plan.order[place];
     float v = 0.0f;
-    if (i >= 0) {
 #pragma unroll 8
-      for (int t = 0; t < q.splits; ++t) v += q.part[(t * places + place) * r + c];
-      v *= f;
-    }
-    uint16_t part[kParts];
-    parts_of(v, part);
-#pragma unroll
-    for (int h = 0; h < kParts; ++h) {
-      if (q.by_token && i >= 0) q.by_token[((int64_t)i * kParts + h) * r + c] = part[h];
-      if (q.by_place) q.by_place[((int64_t)h * r + c) * places + place] = part[h];
-    }
+    for (int t = 0; t < q.splits; ++t) v += q.part[(t * places + place) * r + c];
+    finish_sum(q, v * factor, plan.order[place], place, c, r, places);
   }
 }
 
@@ -650,7 +689,7 @@ __device__ __forceinline__ void list_adapters(const LoraShare& a, int64_t j0, Ad
   if (lane == 0) list.n = n;
 }
 
-// Steps of 16 or 32 of the r parts whose loads wait together.
+// Adapters whose weights' loads wait together.
 constexpr int kShareSteps = 4;
 
 // base + the adapters' share, without a product of its own: a wavefront takes 32 rows and 64
@@ -732,37 +771,38 @@ __global__ __launch_bounds__(256) void lora_add_kernel(AddParams p) {
   if (i0 >= a.rows) return;
   int64_t i = i0 + (lane & 31);
   i = i < a.rows ? i : a.rows - 1;
-  const int chunks = a.r / 8, all = chunks * a.parts;
-  const int steps = (all + 1) / 2, total = list.n * steps;
-  // a step: 16 of the r parts of one adapter
-  for (int s0 = 0; s0 < total; s0 += kShareSteps) {
-    u32x4_t uf[kShareSteps], sf[kShareSteps][2];
-    int kk[kShareSteps];
+  const int chunks = a.r / 8, all = chunks * a.parts, n = list.n;
+  for (int c = 0; c < all && n > 0; c += 2) {  // 16 of the r parts
+    const int q = c + half;                     // may pass the end by one: s is 0 there
+    const uint16_t* u = a.u + i * a.r + 8 * (q % chunks);
+    u32x4_t sv[2];
 #pragma unroll
-    for (int t = 0; t < kShareSteps; ++t) {
-      const int s = s0 + t < total ? s0 + t : total - 1;  // past the end: read again, not used
-      const int k = __builtin_amdgcn_readfirstlane(list.k[s / steps]);
-      const int q = 2 * (s % steps) + half;  // may pass the end by one: s is 0 there
-      kk[t] = k;
-      uf[t] = load16(a.u + ((int64_t)k * a.rows + i) * a.r + 8 * (q % chunks));
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        sf[t][b] = u32x4_t{0, 0, 0, 0};
-        if (id[b] == k && q < all)
-          sf[t][b] = load16(a.s2 + (j0 + 32 * b + (lane & 31)) * kParts * a.r + 8 * q);
-      }
+    for (int b = 0; b < 2; ++b) {
+      sv[b] = u32x4_t{0, 0, 0, 0};
+      if (id[b] >= 0 && q < all)
+        sv[b] = load16(a.s2 + (j0 + 32 * b + (lane & 31)) * kParts * a.r + 8 * q);
     }
+    for (int s0 = 0; s0 < n; s0 += kShareSteps) {
+      u32x4_t uf[kShareSteps];
+      int kk[kShareSteps];
 #pragma unroll
-    for (int t = 0; t < kShareSteps; ++t) {
-      if (s0 + t >= total) break;
+      for (int t = 0; t < kShareSteps; ++t) {  // past the end the last one again, not used
+        kk[t] = __builtin_amdgcn_readfirstlane(list.k[s0 + t < n ? s0 + t : n - 1]);
+        uf[t] = load16(u + (int64_t)kk[t] * a.rows * a.r);
+      }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const bool own = id[b] == kk[t];
-        if (!__ballot(own)) continue;
-        const f32x16_t v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            as_bf16x8(uf[t]), as_bf16x8(sf[t][b]), f32x16_t{}, 0, 0, 0);
+      for (int t = 0; t < kShareSteps; ++t) {
+        if (s0 + t >= n) break;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[b][e] += own ? v[e] : 0.0f;
+        for (int b = 0; b < 2; ++b) {
+          const bool own = id[b] == kk[t];
+          if (!__ballot(own)) continue;
+          const u32x4_t sf = own ? sv[b] : u32x4_t{0, 0, 0, 0};
+          const f32x16_t v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              as_bf16x8(uf[t]), as_bf16x8(sf), f32x16_t{}, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[b][e] += own ? v[e] : 0.0f;
+        }
       }
     }
   }
@@ -845,7 +885,18 @@ struct OuterProblem {
 
 constexpr int kOuter = 128;  // columns of a workgroup
 
-// A slab of 32 token rows of 128 columns in LDS, 256 bytes a row, 16-byte chunk c of row k at
+// Places of a step, and a stage of LDS: SP token rows of 128 columns in Y's parts, then S's
+// parts, 32 NC rows of SP places.
+template <int DT, int NC>
+struct OuterShape {
+  static constexpr int P = row_parts<DT>();
+  static constexpr int SP = P == 1 && NC == 1 ? 64 : 32;
+  static constexpr int kSlab = SP * kOuter;
+  static constexpr int kRows = kParts * 32 * NC;
+  static constexpr int kStage = P * kSlab + kRows * SP;  // elements
+};
+
+// A slab of SP token rows of 128 columns in LDS, 256 bytes a row, 16-byte chunk c of row k at
 // c ^ 4 (k % 4), read back transposed (the layout of the product's dim-contiguous operand).
 __device__ __forceinline__ bf16x8_t slab_frag(const uint16_t LDS_AS* s, int d0, int ks, int lane) {
   const int g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
@@ -858,71 +909,114 @@ __device__ __forceinline__ bf16x8_t slab_frag(const uint16_t LDS_AS* s, int d0, 
   return __builtin_bit_cast(bf16x8_t, u32x4_t{a[0], a[1], b[0], b[1]});
 }
 
+// Steps of SP places go through two stages of LDS; the next step's rows are on their way in
+// registers, and the tokens of the one after.
 template <int DT, int NC, bool BYCOL>
 __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& plan, int r, int k,
                                       int block, int64_t places, uint16_t* smem) {
-  constexpr int P = row_parts<DT>();  // of Y
-  constexpr int kSlab = kTile * kOuter;
-  uint16_t LDS_AS* const lds = (uint16_t LDS_AS*)smem;  // [2][P][kSlab]
+  using O = OuterShape<DT, NC>;
+  constexpr int P = O::P, SP = O::SP;
+  constexpr int kY = SP / 16;                      // rows of a thread
+  constexpr int kPieces = SP / 8;                  // 16-byte pieces of a row of S
+  constexpr int kS = (O::kRows * kPieces + 255) / 256;  // of a thread
+  uint16_t LDS_AS* const lds = (uint16_t LDS_AS*)smem;
   const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t d0 = (int64_t)block * kOuter;
   f32x16_t acc[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) acc[c] = f32x16_t{};
-  const int t0 = plan.first[k], t1 = plan.first[k + 1];
-  // this thread's two 16-byte chunks of a slab: rows t / 16 and 16 + t / 16
+  const int a0 = plan.first[k] * kTile, a1 = plan.first[k + 1] * kTile;
   const int chunk = t & 15;
-  u32x4_t yv[2][P];
-  auto fetch = [&](int tile) {
+  const int64_t d = d0 + 8 * chunk;
+  const bool whole = d0 + kOuter <= p.D;  // the same for all threads
+  int token[kY];
+  u32x4_t yv[kY][P], sv[kS];
+  auto fetch_tokens = [&](int a) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = plan.order[tile * kTile + 16 * h + (t >> 4)];
-      const int64_t d = d0 + 8 * chunk, left = p.D - d;
-#pragma unroll
-      for (int q = 0; q < P; ++q) yv[h][q] = u32x4_t{0, 0, 0, 0};
-      if (i >= 0 && left > 0) row8<DT, P>(p.y, (int64_t)i * p.ldy + d, left, yv[h]);
+    for (int h = 0; h < kY; ++h) {
+      const int place = a + 16 * h + (t >> 4);
+      token[h] = place < a1 ? plan.order[place] : -1;
     }
   };
-  if (t0 < t1) fetch(t0);
-  for (int tile = t0; tile < t1; ++tile) {
-    uint16_t LDS_AS* const stage = lds + ((tile - t0) & 1) * P * kSlab;
+  auto fetch = [&](int a) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kY; ++h) {
+      const int64_t at = (int64_t)(token[h] < 0 ? 0 : token[h]) * p.ldy + d;
+      if (whole) {
+        row8<DT, P>(p.y, at, 8, yv[h]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < P; ++q) yv[h][q] = u32x4_t{0, 0, 0, 0};
+        if (d < p.D) row8<DT, P>(p.y, at, p.D - d, yv[h]);
+      }
+      // no token there: not even what is not finite
+#pragma unroll
+      for (int q = 0; q < P; ++q) yv[h][q] = token[h] < 0 ? u32x4_t{0, 0, 0, 0} : yv[h][q];
+    }
+#pragma unroll
+    for (int e = 0; e < kS; ++e) {
+      const int at = e * 256 + t, row = at / kPieces, piece = at % kPieces;
+      const int c = row % (32 * NC), q = row / (32 * NC);
+      sv[e] = u32x4_t{0, 0, 0, 0};
+      if (row < O::kRows && c < r && a + 8 * piece < a1)
+        sv[e] = *reinterpret_cast<const u32x4_t*>(p.s + ((int64_t)q * r + c) * places + a +
+                                                  8 * piece);
+    }
+  };
+  // piece `piece` of row c: rows of 128 bytes swapped by c % 8, of 64 by c / 2 % 4
+  auto s_at = [](int row, int c, int piece) {
+    return row * SP + (piece ^ (SP == 64 ? c & 7 : (c >> 1) & 3)) * 8;
+  };
+  if (a0 < a1) {
+    fetch_tokens(a0);
+    fetch(a0);
+    fetch_tokens(a0 + SP);
+  }
+  for (int a = a0; a < a1; a += SP) {
+    uint16_t LDS_AS* const stage = lds + ((a - a0) / SP & 1) * O::kStage;
+    uint16_t LDS_AS* const ss = stage + P * O::kSlab;
+#pragma unroll
+    for (int h = 0; h < kY; ++h) {
       const int row = 16 * h + (t >> 4);
       const int at = row * kOuter + ((chunk ^ (4 * (row & 3))) * 8);
 #pragma unroll
       for (int q = 0; q < P; ++q)
-        *reinterpret_cast<u32x4_t LDS_AS*>(stage + q * kSlab + at) = yv[h][q];
+        *reinterpret_cast<u32x4_t LDS_AS*>(stage + q * O::kSlab + at) = yv[h][q];
     }
-    if (tile + 1 < t1) fetch(tile + 1);
-    u32x4_t sv[2][NC][kParts];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (int e = 0; e < kS; ++e) {
+      const int at = e * 256 + t, row = at / kPieces;
+      if (row < O::kRows)
+        *reinterpret_cast<u32x4_t LDS_AS*>(ss + s_at(row, row % (32 * NC), at % kPieces)) = sv[e];
+    }
+    if (a + SP < a1) {
+      fetch(a + SP);
+      fetch_tokens(a + 2 * SP);
+    }
+    lds_barrier();  // one a step: the other stage is written behind the next
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int row = 32 * c + (lane & 31) < r ? 32 * c + (lane & 31) : r - 1;
-        const uint16_t* s = p.s + row * places + (int64_t)tile * kTile + 16 * ks + 8 * half;
+    for (int ks = 0; ks < SP / 16; ++ks) {
+      bf16x8_t y[P];
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
-          sv[ks][c][q] = *reinterpret_cast<const u32x4_t*>(s + q * r * places);
-      }
-    __syncthreads();  // one barrier a slab: the other stage is written behind the next
+      for (int q = 0; q < P; ++q) y[q] = slab_frag(stage + q * O::kSlab, 32 * wave, ks, lane);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int pl = 0; pl < P; ++pl) {
-        const bf16x8_t y = slab_frag(stage + pl * kSlab, 32 * wave, ks, lane);
+        for (int h = 0; h < kParts; ++h) {
+          const int cc = 32 * c + (lane & 31);
+          const u32x4_t sw = *reinterpret_cast<const u32x4_t LDS_AS*>(
+              ss + s_at(h * 32 * NC + cc, cc, 2 * ks + half));
+          const bf16x8_t s = as_bf16x8(sw);
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int h = 0; h + pl < kParts; ++h)
-            acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(sv[ks][c][h]), y, acc[c],
-                                                             0, 0, 0);
-      }
+          for (int q = 0; q < P; ++q)
+            if (h + q < kParts)
+              acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(s, y[q], acc[c], 0, 0, 0);
+        }
+    }
   }
-  const int64_t d = d0 + 32 * wave + (lane & 31);
-  if (d >= p.D) return;
+  const int64_t col = d0 + 32 * wave + (lane & 31);
+  if (col >= p.D) return;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -930,14 +1024,21 @@ __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& pla
       const int row = 32 * c + 8 * q + 4 * half;
       if (row >= r) continue;
       if constexpr (BYCOL) {
-        *reinterpret_cast<f32x4_t*>(p.out + ((int64_t)k * p.D + d) * r + row) =
+        *reinterpret_cast<f32x4_t*>(p.out + ((int64_t)k * p.D + col) * r + row) =
             f32x4_t{acc[c][4 * q], acc[c][4 * q + 1], acc[c][4 * q + 2], acc[c][4 * q + 3]};
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          p.out[((int64_t)k * r + row + e) * p.D + d] = acc[c][4 * q + e];
+          p.out[((int64_t)k * r + row + e) * p.D + col] = acc[c][4 * q + e];
       }
     }
+}
+
+// Of dB's rows or, where that needs more, of dA's BF16 ones.
+template <int DT, int NC>
+constexpr int lora_outer_stage() {
+  return OuterShape<DT, NC>::kStage > OuterShape<1, NC>::kStage ? OuterShape<DT, NC>::kStage
+                                                                : OuterShape<1, NC>::kStage;
 }
 
 // dB's tiles first, then dA's.
@@ -945,7 +1046,7 @@ template <int DT, int NC>
 __global__ __launch_bounds__(256) void lora_outer_kernel(OuterProblem b, OuterProblem a,
                                                          LoraPlan plan, int n, int r,
                                                          int n_tiles) {
-  __shared__ __attribute__((aligned(256))) uint16_t smem[2 * row_parts<DT>() * kTile * kOuter];
+  __shared__ __attribute__((aligned(256))) uint16_t smem[2 * lora_outer_stage<DT, NC>()];
   const int64_t places = (int64_t)n_tiles * kTile;
   const int64_t nb = (int64_t)n * b.blocks;
   int64_t w = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -1071,45 +1172,41 @@ __global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
   put_x(xs[0]);
   lds_barrier();
   {
-    // a step: 32 of the r parts of one adapter
-    const int chunks = a.r / 8, all = chunks * a.parts;
-    const int steps = (all + 3) / 4, total = list.n * steps;
-    for (int s0 = 0; s0 < total; s0 += kShareSteps) {
-      u32x4_t uf[kShareSteps][F], sf[kShareSteps][NT16];
-      int kk[kShareSteps];
+    const int chunks = a.r / 8, all = chunks * a.parts, n = list.n;
+    for (int c0 = 0; c0 < all && n > 0; c0 += 4) {  // 32 of the r parts
+      const int ch = c0 + g;
+      u32x4_t sv[NT16];
 #pragma unroll
-      for (int j = 0; j < kShareSteps; ++j) {
-        const int s = s0 + j < total ? s0 + j : total - 1;  // past the end: read again, not used
-        const int k = __builtin_amdgcn_readfirstlane(list.k[s / steps]);
-        const int ch = 4 * (s % steps) + g;
-        kk[j] = k;
-#pragma unroll
-        for (int f = 0; f < F; ++f) {
-          uf[j][f] = u32x4_t{0, 0, 0, 0};
-          if (ch < all)
-            uf[j][f] = load16(a.u + ((int64_t)k * a.rows + vrow[f]) * a.r + 8 * (ch % chunks));
-        }
-#pragma unroll
-        for (int t = 0; t < NT16; ++t) {
-          sf[j][t] = u32x4_t{0, 0, 0, 0};
-          if (id[t] == k && ch < all)
-            sf[j][t] = load16(a.s2 + (int64_t)(16 * t + c) * kParts * a.r + 8 * ch);
-        }
+      for (int t = 0; t < NT16; ++t) {
+        sv[t] = u32x4_t{0, 0, 0, 0};
+        if (id[t] >= 0 && ch < all)
+          sv[t] = load16(a.s2 + (int64_t)(16 * t + c) * kParts * a.r + 8 * ch);
       }
+      for (int s0 = 0; s0 < n; s0 += kShareSteps) {
+        u32x4_t uf[kShareSteps][F];
+        int kk[kShareSteps];
 #pragma unroll
-      for (int j = 0; j < kShareSteps; ++j) {
-        if (s0 + j >= total) break;
+        for (int j = 0; j < kShareSteps; ++j) {  // past the end the last one again, not used
+          kk[j] = __builtin_amdgcn_readfirstlane(list.k[s0 + j < n ? s0 + j : n - 1]);
 #pragma unroll
-        for (int t = 0; t < NT16; ++t) {
-          const bool own = id[t] == kk[j];
-          if (!__ballot(own)) continue;
+          for (int f = 0; f < F; ++f)
+            uf[j][f] = load16(a.u + ((int64_t)kk[j] * a.rows + vrow[f]) * a.r + 8 * (ch % chunks));
+        }
 #pragma unroll
-          for (int f = 0; f < F; ++f) {
-            const f32x4_t v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                as_bf16x8(uf[j][f]), as_bf16x8(sf[j][t]), f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0,
-                0);
+        for (int j = 0; j < kShareSteps; ++j) {
+          if (s0 + j >= n) break;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[f][t][e] += own ? v[e] : 0.0f;
+          for (int t = 0; t < NT16; ++t) {
+            const bool own = id[t] == kk[j];
+            if (!__ballot(own)) continue;
+            const u32x4_t sf = own ? sv[t] : u32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+              const f32x4_t v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  as_bf16x8(uf[j][f]), as_bf16x8(sf), f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[f][t][e] += own ? v[e] : 0.0f;
+            }
           }
         }
       }
@@ -1173,14 +1270,15 @@ inline int64_t most_tiles(int64_t M, int64_t n) {
   return t > 0 ? t : 1;
 }
 
-// Splits of k so that the tiles make some four workgroups per CU, 512 k at least each.
+// Splits of k so that the tiles make some three workgroups per CU, 4096 k at least each (eight
+// steps of a wavefront); up to that one workgroup finishes a tile.
 struct Split {
   int n;
   int64_t per;
 };
 inline Split split_of(int64_t K, int64_t tiles) {
-  int64_t s = (1024 + tiles - 1) / tiles;
-  const int64_t most = (K + 511) / 512;
+  int64_t s = (768 + tiles - 1) / tiles;
+  const int64_t most = K / 4096;
   s = s > most ? most : s;
   s = s < 1 ? 1 : s;
   Split r;
@@ -1189,19 +1287,22 @@ inline Split split_of(int64_t K, int64_t tiles) {
   return r;
 }
 
-// Splits of the sum over V in dy W.  A tile's 256 k take about 5 us with all CUs at work, and
-// a part's sums are written and read again at some 5 TB/s; parts of 1024 at least.
+// Splits of the sum over V in dy W: with few tiles the chip is not full (99 tiles of 32000 k 566
+// us, in two parts 320 and their joining 20; five parts are no faster, the matrix units
+// being at their power limit).  A CU takes some 18 ns a k, the chip 1.2 PFLOP/s; a part's
+// sums are written and read again at some 5 TB/s.  Parts of 1024 at least.
 inline Split product_split(int64_t M, int64_t H, int64_t V) {
   const int64_t tiles = (M + BN - 1) / BN * ((H + BM - 1) / BM);
+  const double all = (double)tiles * BM * BN * 2 * (double)V / 1.2e9;  // us
   Split best{1, V};
   double least = 0.0;
   for (int s = 1; s <= 16; ++s) {
     const int64_t per = (V + s * 2 * BK - 1) / (s * 2 * BK) * 2 * BK;
     const int64_t n = (V + per - 1) / per;
     if (s > 1 && per < 1024) break;
-    const double t = (double)((tiles * n + 255) / 256) * (double)per * 0.02 +
-                     (n > 1 ? (double)(n * M * H) * 1.6e-6 : 0.0);
-    if (s == 1 || t < 0.95 * least) {
+    const double t = fmax((double)((tiles * n + 255) / 256) * (double)per * 0.018, all) +
+                     (n > 1 ? (double)(n * M * H) * 1.6e-6 + 4.0 : 0.0);
+    if (s == 1 || t < 0.97 * least) {
       least = t;
       best = Split{(int)n, per};
     }
@@ -1224,22 +1325,29 @@ struct Places {
   }
 };
 
+// s and ds: the sums, and where one is split their joining.
 template <int DT>
-hipError_t run_shrink(const ShrinkProblem& s, const ShrinkProblem& d, const LoraPlan& plan, int n,
-                      int r, int tiles, hipStream_t stream) {
+hipError_t run_shrink(const ShrinkProblem& s, const ShrinkProblem& d, const LoraPlan& plan,
+                      const float* scale, int n, int r, int tiles, hipStream_t stream) {
   const dim3 grid((unsigned)tiles, (unsigned)(s.splits + d.splits));
   if (r <= 16)
-    hipLaunchKernelGGL((lora_shrink_kernel<DT, 1>), grid, dim3(256), 0, stream, s, d, plan, n, r,
-                       tiles);
+    hipLaunchKernelGGL((lora_shrink_kernel<DT, 1>), grid, dim3(256), 0, stream, s, d, plan, scale,
+                       n, r, tiles);
   else if (r <= 32)
-    hipLaunchKernelGGL((lora_shrink_kernel<DT, 2>), grid, dim3(256), 0, stream, s, d, plan, n, r,
-                       tiles);
+    hipLaunchKernelGGL((lora_shrink_kernel<DT, 2>), grid, dim3(256), 0, stream, s, d, plan, scale,
+                       n, r, tiles);
   else if (r <= 64)
-    hipLaunchKernelGGL((lora_shrink_kernel<DT, 4>), grid, dim3(256), 0, stream, s, d, plan, n, r,
-                       tiles);
+    hipLaunchKernelGGL((lora_shrink_kernel<DT, 4>), grid, dim3(256), 0, stream, s, d, plan, scale,
+                       n, r, tiles);
   else
-    hipLaunchKernelGGL((lora_shrink_kernel<DT, 8>), grid, dim3(256), 0, stream, s, d, plan, n, r,
-                       tiles);
+    hipLaunchKernelGGL((lora_shrink_kernel<DT, 8>), grid, dim3(256), 0, stream, s, d, plan, scale,
+                       n, r, tiles);
+  if (s.splits > 1 || d.splits > 1) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)tiles, d.splits > 0 ? 2 : 1), dim3(256), 0,
+                       stream, s, d, plan, scale, n, r, tiles);
+  }
   return hipGetLastError();
 }
 
@@ -1317,13 +1425,8 @@ hipError_t launch_lora_forward(const LoraFwdArgs& p, char* ws, hipStream_t strea
     hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.adapter, p.M,
                        p.n, plan, TransposeProblem{}, TransposeProblem{});
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const ShrinkProblem s{p.x, p.ldx, p.H, p.a, p.H, part, sp.n, sp.per};
-    const ShrinkProblem none{};
-    if ((e = run_shrink<1>(s, none, plan, p.n, p.r, (int)tiles, stream)) != hipSuccess) return e;
-    const JoinProblem j{part, sp.n, s2, nullptr};
-    hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)tiles, 1), dim3(256), 0, stream, j, j, plan,
-                       p.scale, p.n, p.r, (int)tiles);
-    e = hipGetLastError();
+    const ShrinkProblem s{p.x, p.ldx, p.H, p.a, p.H, part, sp.n, sp.per, s2, nullptr};
+    e = run_shrink<1>(s, ShrinkProblem{}, plan, p.scale, p.n, p.r, (int)tiles, stream);
   }
   if (e != hipSuccess) return e;
   const LoraShare a{p.b, s2, p.adapter, p.n, p.r, p.dtype == 0 ? kParts : 2, p.V, p.M};
@@ -1394,14 +1497,12 @@ hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
   hipLaunchKernelGGL(lora_plan_kernel, dim3((unsigned)(1 + ta.tiles + tb.tiles), (unsigned)p.n),
                      dim3(kPlanThreads), 0, stream, p.adapter, p.M, p.n, plan, ta, tb);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const ShrinkProblem s{p.x, p.ldx, p.H, p.a, p.H, fp(b.s_part), b.ss.n, b.ss.per};
-  const ShrinkProblem d{p.dy, p.ldy, p.V, bf(b.bt), b.ldv, fp(b.d_part), b.sd.n, b.sd.per};
-  if ((e = run_shrink<DT>(s, d, plan, p.n, p.r, tiles, stream)) != hipSuccess) return e;
-  const JoinProblem js{fp(b.s_part), b.ss.n, nullptr, bf(b.s_place)};
-  const JoinProblem jd{fp(b.d_part), b.sd.n, bf(b.d_token), bf(b.d_place)};
-  hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)tiles, 2), dim3(256), 0, stream, js, jd, plan,
-                     p.scale, p.n, p.r, tiles);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const ShrinkProblem s{p.x, p.ldx, p.H, p.a, p.H, fp(b.s_part), b.ss.n, b.ss.per, nullptr,
+                        bf(b.s_place)};
+  const ShrinkProblem d{p.dy, p.ldy, p.V, bf(b.bt), b.ldv, fp(b.d_part), b.sd.n, b.sd.per,
+                        bf(b.d_token), bf(b.d_place)};
+  if (p.M > 0 && (e = run_shrink<DT>(s, d, plan, p.scale, p.n, p.r, tiles, stream)) != hipSuccess)
+    return e;
   if (p.dx && p.M > 0) {
     const LoraShare a{bf(b.at), bf(b.d_token), p.adapter, p.n, p.r, 2, p.H, p.M};
     if (!p.w) {
