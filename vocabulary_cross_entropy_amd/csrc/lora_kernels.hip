@@ -331,7 +331,7 @@ __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& p
                                        const float* scale, int r, int tile, int split,
                                        int64_t places, f32x4_t* sh) {
   constexpr int N = row_parts<DT>();
-  constexpr int S = DT == 1 && NC <= 2 ? 4 : 1;  // steps of 32 k whose loads wait together
+  constexpr int S = NC > 2 ? 1 : DT == 1 ? 4 : 2;  // steps of 32 k whose loads wait together
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, c = lane & 15;
   const int k_adapter = plan.owner[tile];
@@ -459,19 +459,18 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(ShrinkProblem s, Shrin
 __global__ __launch_bounds__(256) void lora_join_kernel(ShrinkProblem s, ShrinkProblem d,
                                                         LoraPlan plan, const float* scale, int n,
                                                         int r, int n_tiles) {
-  const ShrinkProblem q = blockIdx.y ? d : s;
+  const ShrinkProblem q = blockIdx.z ? d : s;
   const int64_t places = (int64_t)n_tiles * kTile;
   const int tile = blockIdx.x;
   if (q.splits <= 1 || tile >= plan.first[n]) return;
   const float factor = scale ? scale[plan.owner[tile]] : 1.0f;
-  for (int e = threadIdx.x; e < kTile * r; e += 256) {
-    const int c = e % r;
-    const int64_t place = (int64_t)tile * kTile + e / r;
-    float v = 0.0f;
+  const int e = blockIdx.y * 256 + threadIdx.x, c = e % r;  // kTile r is a multiple of 256
+  const int64_t place = (int64_t)tile * kTile + e / r;
+  const int token = plan.order[place];
+  float v = 0.0f;
 #pragma unroll 8
-    for (int t = 0; t < q.splits; ++t) v += q.part[(t * places + place) * r + c];
-    finish_sum(q, v * factor, plan.order[place], place, c, r, places);
-  }
+  for (int t = 0; t < q.splits; ++t) v += q.part[(t * places + place) * r + c];
+  finish_sum(q, v * factor, token, place, c, r, places);
 }
 
 // ---- the adapters' share of a tile -------------------------------------------------------
@@ -1082,12 +1081,16 @@ __global__ __launch_bounds__(256) void lora_rows_kernel(const void* dy, int64_t 
 // ---- few tokens -------------------------------------------------------------------------------
 
 // Up to 64 tokens: W is streamed once against X in LDS, 16 F rows a wavefront, straight into
-// operand registers, 128 k ahead of the product.  X lies in two parts of KX k that take turns: the
-// next one's loads go to registers while this one is multiplied.  In LDS the 16-byte
+// operand registers, A steps ahead of the product.  A step is 256 k, 512 bytes of each of
+// 16 rows: what the memory gives depends on how much of a row is asked for together (8 x 4096 x
+// 131072: 256 bytes 211 us, 512 200; more steps ahead 203).  X lies in two parts of KX k that take
+// turns: the next one's loads go to registers while this one is multiplied.  In LDS the 16-byte
 // chunk q of token c lies at q ^ (c % 16) in its group of 16, so that 16 tokens' reads of one
 // chunk meet all banks once.  The adapters' share comes first, under W's first loads.
+// Bound by reading W: 8 x 4096 x 131072 (1.07 GB) 194 us, 5.5 TB/s.
 template <int T>
 constexpr int skinny_k() { return 16384 / T; }  // 32 KB
+constexpr int kStepK = 256;
 
 struct SkinnyParams {
   const uint16_t* x;
@@ -1098,15 +1101,15 @@ struct SkinnyParams {
   int64_t ldo;
 };
 
-template <int T, int F, int DT>
-__global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
-  constexpr int KX = skinny_k<T>(), NT16 = T / 16, kX = T * KX / 8 / 256;  // 16-byte chunks each
+template <int T, int NW, int F, int A, int DT>
+__global__ __launch_bounds__(64 * NW, 8 / NW) void lora_skinny_kernel(SkinnyParams p) {
+  constexpr int KX = skinny_k<T>(), NT16 = T / 16, kX = T * KX / 8 / (64 * NW);  // 16-byte chunks each
   __shared__ __attribute__((aligned(256))) uint16_t xs[2][T * KX];
   __shared__ AdapterList list;
   const LoraShare& a = p.a;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int64_t v0 = (int64_t)blockIdx.x * (64 * F) + wave * (16 * F);
+  const int64_t v0 = (int64_t)blockIdx.x * (NW * 16 * F) + wave * (16 * F);
   const uint16_t* wr[F];
   int64_t vrow[F];
   f32x4_t acc[F][NT16];
@@ -1118,22 +1121,30 @@ __global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
 #pragma unroll
     for (int t = 0; t < NT16; ++t) acc[f][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  typedef u32x4_t Frag[F][4];
+  constexpr int KS = kStepK / 32;
+  typedef u32x4_t Frag[F][KS];
   auto fetch = [&](Frag& q, int64_t k) {
+    if (k + kStepK <= p.K) {
 #pragma unroll
-    for (int f = 0; f < F; ++f)
+      for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int64_t at = k + 32 * s + 8 * g;
-        q[f][s] = u32x4_t{0, 0, 0, 0};
-        if (at < p.K) q[f][s] = load16(wr[f] + at);
-      }
+        for (int s = 0; s < KS; ++s) q[f][s] = load16(wr[f] + k + 32 * s + 8 * g);
+    } else {
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int64_t at = k + 32 * s + 8 * g;
+          q[f][s] = u32x4_t{0, 0, 0, 0};
+          if (at < p.K) q[f][s] = load16(wr[f] + at);
+        }
+    }
   };
   u32x4_t xr[kX];
   auto fetch_x = [&](int64_t k0) {
 #pragma unroll
     for (int e = 0; e < kX; ++e) {
-      const int at = e * 256 + threadIdx.x, tok = at / (KX / 8), ch = at % (KX / 8);
+      const int at = e * (64 * NW) + threadIdx.x, tok = at / (KX / 8), ch = at % (KX / 8);
       xr[e] = u32x4_t{0, 0, 0, 0};
       if (tok < a.cols && k0 + ch * 8 < p.K) xr[e] = load16(p.x + tok * p.ldx + k0 + ch * 8);
     }
@@ -1141,13 +1152,13 @@ __global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
   auto put_x = [&](uint16_t* to) {
 #pragma unroll
     for (int e = 0; e < kX; ++e) {
-      const int at = e * 256 + threadIdx.x, tok = at / (KX / 8), ch = at % (KX / 8);
+      const int at = e * (64 * NW) + threadIdx.x, tok = at / (KX / 8), ch = at % (KX / 8);
       *reinterpret_cast<u32x4_t*>(to + tok * KX + (ch ^ (tok & 15)) * 8) = xr[e];
     }
   };
   auto multiply = [&](const Frag& q, const uint16_t* x, int kk) {  // kk: of the part in LDS
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < KS; ++s) {
       bf16x8_t xv[NT16];
 #pragma unroll
       for (int t = 0; t < NT16; ++t) {
@@ -1162,9 +1173,10 @@ __global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
                                                               acc[f][t], 0, 0, 0);
     }
   };
-  Frag q[2];
+  Frag q[A];
   fetch_x(0);
-  fetch(q[0], 0);
+#pragma unroll
+  for (int i = 0; i < A; ++i) fetch(q[i], kStepK * i);
   int id[NT16];
 #pragma unroll
   for (int t = 0; t < NT16; ++t) id[t] = adapter_of(a.adapter, 16 * t + c, a.cols, a.n);
@@ -1212,21 +1224,26 @@ __global__ __launch_bounds__(256, 2) void lora_skinny_kernel(SkinnyParams p) {
       }
     }
   }
-  int part = 0;
-  for (int64_t k0 = 0; k0 < p.K; k0 += KX, part ^= 1) {
-    const bool more = k0 + KX < p.K;
-    if (more) fetch_x(k0 + KX);
-    const int n = (int)((p.K - k0 < KX ? p.K - k0 : KX) + 127) / 128;  // of 128 k
-    for (int ss = 0; ss < n; ss += 2) {
-      fetch(q[1], k0 + 128 * (ss + 1));
-      multiply(q[0], xs[part], 128 * ss);
-      // an odd number is the last part's alone: q[1] is past K then
-      fetch(q[0], k0 + 128 * (ss + 2));
-      if (ss + 1 < n) multiply(q[1], xs[part], 128 * (ss + 1));
+  constexpr int kPer = KX / kStepK;  // steps of a part of X
+  const int n = (int)((p.K + kStepK - 1) / kStepK);
+  if (KX < p.K) fetch_x(KX);
+  const uint16_t* x = xs[0];
+  for (int s0 = 0; s0 < n; s0 += A) {
+#pragma unroll
+    for (int i = 0; i < A; ++i) {
+      const int s = s0 + i;
+      if (s >= n) break;
+      if (s % kPer == 0 && s > 0) {
+        // on to the next part; the other one was read before the last barrier
+        uint16_t* const next = xs[(s / kPer) & 1];
+        put_x(next);
+        lds_barrier();
+        x = next;
+        if ((int64_t)(s + kPer) * kStepK < p.K) fetch_x((int64_t)(s + kPer) * kStepK);
+      }
+      multiply(q[i], x, s % kPer * kStepK);
+      fetch(q[i], (int64_t)(s + A) * kStepK);
     }
-    // the other part was read before the last barrier
-    if (more) put_x(xs[part ^ 1]);
-    lds_barrier();
   }
 #pragma unroll
   for (int t = 0; t < NT16; ++t) {
@@ -1270,15 +1287,15 @@ inline int64_t most_tiles(int64_t M, int64_t n) {
   return t > 0 ? t : 1;
 }
 
-// Splits of k so that the tiles make some three workgroups per CU, 4096 k at least each (eight
-// steps of a wavefront); up to that one workgroup finishes a tile.
+// Splits of k so that the tiles make some four workgroups per CU, 1024 k at least each (two steps
+// of a wavefront: a step takes about 2 us, whatever else runs).
 struct Split {
   int n;
   int64_t per;
 };
 inline Split split_of(int64_t K, int64_t tiles) {
-  int64_t s = (768 + tiles - 1) / tiles;
-  const int64_t most = K / 4096;
+  int64_t s = (1024 + tiles - 1) / tiles;
+  const int64_t most = K / 1024;
   s = s > most ? most : s;
   s = s < 1 ? 1 : s;
   Split r;
@@ -1345,8 +1362,9 @@ hipError_t run_shrink(const ShrinkProblem& s, const ShrinkProblem& d, const Lora
   if (s.splits > 1 || d.splits > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)tiles, d.splits > 0 ? 2 : 1), dim3(256), 0,
-                       stream, s, d, plan, scale, n, r, tiles);
+    hipLaunchKernelGGL(lora_join_kernel,
+                       dim3((unsigned)tiles, (unsigned)(kTile * r / 256), d.splits > 0 ? 2 : 1),
+                       dim3(256), 0, stream, s, d, plan, scale, n, r, tiles);
   }
   return hipGetLastError();
 }
@@ -1369,14 +1387,17 @@ hipError_t run_outer(const OuterProblem& b, const OuterProblem& a, const LoraPla
 
 template <int T, int DT>
 hipError_t run_skinny(const SkinnyParams& p, hipStream_t stream) {
-  // two fragments of rows a wavefront where that still fills the chip
-  if (p.a.rows >= 65536)
-    hipLaunchKernelGGL((lora_skinny_kernel<T, 2, DT>), dim3((unsigned)((p.a.rows + 127) / 128)),
-                       dim3(256), 0, stream, p);
-  else
-    hipLaunchKernelGGL((lora_skinny_kernel<T, 1, DT>), dim3((unsigned)((p.a.rows + 63) / 64)),
-                       dim3(256), 0, stream, p);
-  return hipGetLastError();
+  // Workgroups of 64 rows, or of 256, which read X a quarter as often, where there are enough
+  // of them: V = 256003, 8 / 32 / 64 tokens 221 / 260 / 302 us in the first, 211 / 228 / 244 in the
+  // second, V = 131072 198 / 217 / 246 and 207 / 219 / 231, V = 32000 58 / 63 / 70 and 72 / 80 / 88.
+  const auto go = [&](auto kernel, int rows, int threads) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.a.rows + rows - 1) / rows)), dim3(threads), 0,
+                       stream, p);
+    return hipGetLastError();
+  };
+  if (p.a.rows >= (T == 64 ? 131072 : 196608))
+    return go(lora_skinny_kernel<T, 8, 2, 1, DT>, 256, 512);
+  return go(lora_skinny_kernel<T, 4, 1, 2, DT>, 64, 256);
 }
 
 template <int DT>
