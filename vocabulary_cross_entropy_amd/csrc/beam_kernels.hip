@@ -31,6 +31,7 @@ constexpr int kPickThreads = 512;  // of a request's
 constexpr int kPickWaves = kPickThreads / 64;
 constexpr int kGroups = 2048;      // groups listed
 constexpr int kCands = 1024;       // candidates listed
+constexpr int kSegsHeld = 2048;    // segments of a request whose keys are kept
 constexpr int kMostGroups = kSeg / 64;
 
 template <int DT>
@@ -199,6 +200,9 @@ enum { kDead, kEnded, kLive };
 struct PickShared {
   Beam beam[kBeamMost];
   uint64_t group[kGroups];  // key of the bound, and the segment and group
+  uint32_t seg[kSegsHeld];  // keys of the segments
+  uint16_t seg_list[kSegsHeld];
+  uint32_t n_listed;
   double value[kCands];
   uint64_t index[kCands];
   uint32_t keys[64];
@@ -308,14 +312,29 @@ struct Pick {
     if (lane == 0) sh.beam[k] = q;
   }
 
+  __device__ __forceinline__ bool held() const { return n_segs <= kSegsHeld; }
+
   // Groups whose key reaches `bound`, listed; returns how many there are.
   __device__ uint32_t list_groups(uint32_t bound) const {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     __syncthreads();
-    if (threadIdx.x == 0) sh.n_groups = 0;
+    if (threadIdx.x == 0) sh.n_groups = sh.n_listed = 0;
     __syncthreads();
-    for (int s = wave; s < n_segs; s += kPickWaves) {
-      if (segment_key(s) < bound) continue;  // the same in all lanes
+    int n = n_segs;
+    if (held()) {  // the segments that reach it first, so that no wavefront waits for others' keys
+      for (int s = threadIdx.x; s < n_segs; s += kPickThreads) {
+        const uint32_t key = sh.seg[s];
+        if (key >= bound && key != 0) sh.seg_list[atomicAdd(&sh.n_listed, 1u)] = (uint16_t)s;
+      }
+      __syncthreads();
+      n = (int)sh.n_listed;
+    }
+    for (int i = wave; i < n; i += kPickWaves) {
+      int s = i;
+      if (held())
+        s = __builtin_amdgcn_readfirstlane((int)sh.seg_list[i]);
+      else if (segment_key(s) < bound)  // the same in all lanes
+        continue;
       for (int g = lane; g < S::kPer; g += 64) {
         const uint32_t key = group_key(s, g);
         const bool in = key >= bound && key != 0;
@@ -334,15 +353,32 @@ struct Pick {
     return sh.n_groups;
   }
 
-  // The n_out-th largest of `n` keys in LDS, by wavefront 0, for all.
+  // The n_out-th largest of n keys, by wavefront 0, for all; up to 512 of them stay in
+  // registers.
   template <class Key>
   __device__ uint32_t nth_listed(int n, Key key) const {
     if (threadIdx.x < 64) {
-      const uint32_t t = nth_key(p.n_out, [&](auto f) {
-        for (int i = 0; i < n; i += 64)
-          f(i + (int)threadIdx.x < n ? key(i + (int)threadIdx.x) : 0u);
-      });
-      if (threadIdx.x == 0) sh.bound = t;
+      const int lane = threadIdx.x;
+      uint32_t t;
+      if (n <= 64) {
+        const uint32_t k = lane < n ? key(lane) : 0u;
+        t = nth_key(p.n_out, [&](auto f) { f(k); });
+      } else if (n <= 512) {
+        uint32_t keys[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) keys[j] = j * 64 + lane < n ? key(j * 64 + lane) : 0u;
+        const int used = (n + 63) / 64;
+        t = nth_key(p.n_out, [&](auto f) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < used) f(keys[j]);
+        });
+      } else {
+        t = nth_key(p.n_out, [&](auto f) {
+          for (int i = 0; i < n; i += 64) f(i + lane < n ? key(i + lane) : 0u);
+        });
+      }
+      if (lane == 0) sh.bound = t;
     }
     __syncthreads();
     const uint32_t t = sh.bound;
@@ -430,33 +466,15 @@ struct Pick {
     }
     for (int k = wave; k < p.K; k += kPickWaves) join(k, lane);
     __syncthreads();
-    // the n_out-th largest segment; 0 where there are fewer
-    uint32_t bound = 0;
-    if (n_segs >= p.n_out) {
-      if (wave == 0) {
-        uint32_t keys[8];  // of up to 512 segments; more are formed anew for every bit
-        if (n_segs <= 512) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            keys[j] = j * 64 + lane < n_segs ? segment_key(j * 64 + lane) : 0u;
-          const int used = (n_segs + 63) / 64;
-          bound = nth_key(p.n_out, [&](auto f) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < used) f(keys[j]);
-          });
-        } else {
-          bound = nth_key(p.n_out, [&](auto f) {
-            for (int i = 0; i < n_segs; i += 64)
-              f(i + lane < n_segs ? segment_key(i + lane) : 0u);
-          });
-        }
-        if (lane == 0) sh.bound = bound;
-      }
-      __syncthreads();
-      bound = sh.bound;
+    if (held()) {
+      for (int s = threadIdx.x; s < n_segs; s += kPickThreads) sh.seg[s] = segment_key(s);
       __syncthreads();
     }
+    // the n_out-th largest segment; 0 where there are fewer
+    uint32_t bound = 0;
+    if (n_segs >= p.n_out)
+      bound = held() ? nth_listed(n_segs, [&](int i) { return sh.seg[i]; })
+                     : nth_listed(n_segs, [&](int i) { return segment_key(i); });
     uint32_t n;
     while ((n = list_groups(bound)) > kGroups) {
       // those listed reach the bound; so do n_out of them a higher one

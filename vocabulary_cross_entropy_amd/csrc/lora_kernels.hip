@@ -10,9 +10,7 @@
 //
 //  * Tokens in their own order: the product with W and the adapters' share of it.  A tile's
 //    epilogue walks the adapters that its tokens have and multiplies those tokens' s by B_k,
-//    32 rows at a time, into the same accumulators; a token takes only its own adapter's
-//    product (a select, where a block of tokens is mixed, so that an infinity in one
-//    adapter's weights cannot reach another's tokens).
+//    32 rows at a time, into the same accumulators, the other tokens' s being zero.
 //  * Tokens sorted by adapter (lora_plan_kernel: places of 32, each of one adapter): s and ds,
 //    and the adapters' gradients, which sum over the tokens of one adapter.
 #include <math.h>
@@ -69,6 +67,7 @@ struct LoraPlan {
 };
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+constexpr int kHeld = 4;  // tokens of a lane
 
 // f(k, lanes that have adapter k) for the adapters among 64 ids (negative: none).
 template <class F>
@@ -98,10 +97,17 @@ __device__ void make_plan(const int32_t* adapter, int64_t M, int n, const LoraPl
   __syncthreads();
   const int64_t per = (M + kPlanThreads - 1) / kPlanThreads * 64;
   const int64_t i0 = wave * per, i1 = i0 + per < M ? i0 + per : M;
-  for (int64_t i = i0; i < i1; i += 64)
-    each_adapter(adapter_of(adapter, i + lane, i1, n), [&](int k, uint64_t match) {
+  int ids[kHeld];  // the first tokens' adapters stay in registers
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) ids[h] = adapter_of(adapter, i0 + 64 * h + lane, i1, n);
+  const auto tally = [&](int id) {
+    each_adapter(id, [&](int k, uint64_t match) {
       if (lane == 0) count[wave][k] = count[wave][k] + __builtin_popcountll(match);
     });
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) tally(ids[h]);
+  for (int64_t i = i0 + 64 * kHeld; i < i1; i += 64) tally(adapter_of(adapter, i + lane, i1, n));
   __syncthreads();
   // every adapter's tiles, and their running sum
   int total = 0, mine = 0;
@@ -145,8 +151,7 @@ __device__ void make_plan(const int32_t* adapter, int64_t M, int n, const LoraPl
     }
     plan.owner[i] = lo;
   }
-  for (int64_t i = i0; i < i1; i += 64) {
-    const int id = adapter_of(adapter, i + lane, i1, n);
+  const auto place = [&](int id, int64_t i) {
     each_adapter(id, [&](int k, uint64_t match) {
       const int at = count[wave][k];
       if (id == k)
@@ -154,7 +159,11 @@ __device__ void make_plan(const int32_t* adapter, int64_t M, int n, const LoraPl
             (int32_t)(i + lane);
       if (lane == 0) count[wave][k] = at + __builtin_popcountll(match);
     });
-  }
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) place(ids[h], i0 + 64 * h);
+  for (int64_t i = i0 + 64 * kHeld; i < i1; i += 64)
+    place(adapter_of(adapter, i + lane, i1, n), i);
 }
 
 // (n, R, C) to (n, C, ldr), the places from R to ldr zero.
@@ -475,6 +484,16 @@ __global__ __launch_bounds__(256) void lora_join_kernel(ShrinkProblem s, ShrinkP
 
 // ---- the adapters' share of a tile -------------------------------------------------------
 
+// Is one of the eight BF16 numbers an infinity or a NaN?
+__device__ __forceinline__ bool not_finite(const u32x4_t& w) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m |= (w[j] & 0x7f807f80u) + 0x00800080u;
+  return (m & 0x80008000u) != 0;
+}
+
+// Tokens without an adapter enter its product with zeros.  Weights that are not finite would make
+// NaN of these: they are left out there and multiplied apart, for the adapter's own tokens.
 // Rows are output features (rows of U_k, (n, rows, r)), columns tokens.
 struct LoraShare {
   const uint16_t* u;
@@ -539,14 +558,6 @@ __device__ __forceinline__ void store_block(void* out, int64_t at, const f32x16_
   }
 }
 
-// Is one of the eight BF16 numbers an infinity or a NaN?
-__device__ __forceinline__ bool not_finite(const u32x4_t& w) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) m |= (w[j] & 0x7f807f80u) + 0x00800080u;
-  return (m & 0x80008000u) != 0;
-}
-
 // The epilogue of the product: the adapters' share, then the store to out (cols, rows).  Tokens
 // without the adapter enter its product with zeros; rows of U_k that are not finite would make
 // NaN of these, so they are left out there and added, for the adapter's own tokens, behind
@@ -589,38 +600,43 @@ struct EpiLora {
   __device__ static void apply(const Params& p, f32x16_t (&acc)[NA][NB], int64_t i0, int64_t j0,
                                int wr, int wc, int lane, uint16_t*) {
     const LoraShare& a = p.a;
-    const int half = lane >> 5, chunks = a.r / 8, all = chunks * a.parts;
+    const int half = lane >> 5, chunks = a.r / 8;
     i0 += wr * WM;
     j0 += wc * WN;
     uint64_t odd = 0;
     each(a, j0, lane, [&](int k, const bool (&own)[NB]) {
-      for (int c = 0; c < all; c += 2) {  // 16 of the r parts at a time
-        const int q = c + half;           // may pass the end by one: s is 0 there
+      for (int c = 0; c < chunks; c += 2) {  // 16 of r
+        const bool in = c + half < chunks;    // r may end in the middle: s is 0 there
         u32x4_t uf[NA], sf[NB];
 #pragma unroll
         for (int t = 0; t < NA; ++t) {
           int64_t i = i0 + 32 * t + (lane & 31);
           i = i < a.rows ? i : a.rows - 1;
-          uf[t] = load16(a.u + ((int64_t)k * a.rows + i) * a.r + 8 * (q % chunks));
+          uf[t] = load16(a.u + ((int64_t)k * a.rows + i) * a.r + 8 * (in ? c + half : c));
         }
+        for (int h = 0; h < a.parts; ++h) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          sf[b] = u32x4_t{0, 0, 0, 0};
-          if (own[b] && q < all)
-            sf[b] = load16(a.s2 + (j0 + 32 * b + (lane & 31)) * kParts * a.r + 8 * q);
+          for (int b = 0; b < NB; ++b) {
+            sf[b] = u32x4_t{0, 0, 0, 0};
+            if (own[b] && in)
+              sf[b] = load16(a.s2 + ((j0 + 32 * b + (lane & 31)) * kParts + h) * a.r +
+                             8 * (c + half));
+          }
+          if (h == 0) {
+#pragma unroll
+            for (int t = 0; t < NA; ++t) {
+              const bool bad = not_finite(uf[t]);
+              odd |= __ballot(bad);
+              if (bad) uf[t] = u32x4_t{0, 0, 0, 0};
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < NA; ++t)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              acc[t][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  as_bf16x8(uf[t]), as_bf16x8(sf[b]), acc[t][b], 0, 0, 0);
         }
-#pragma unroll
-        for (int t = 0; t < NA; ++t) {
-          const bool bad = not_finite(uf[t]);
-          odd |= __ballot(bad);
-          if (bad) uf[t] = u32x4_t{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int t = 0; t < NA; ++t)
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            acc[t][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(uf[t]), as_bf16x8(sf[b]),
-                                                                acc[t][b], 0, 0, 0);
       }
     });
 #pragma unroll
@@ -729,6 +745,7 @@ __device__ __forceinline__ f32x4_t load4(const void* p, int64_t at, int64_t row,
 
 template <int DT, int BT>
 __global__ __launch_bounds__(256) void lora_add_kernel(AddParams p) {
+  constexpr int PARTS = DT == 0 ? kParts : 2;
   __shared__ AdapterList list;
   const LoraShare& a = p.a;
   const int lane = threadIdx.x & 63, half = lane >> 5;
@@ -770,17 +787,20 @@ __global__ __launch_bounds__(256) void lora_add_kernel(AddParams p) {
   if (i0 >= a.rows) return;
   int64_t i = i0 + (lane & 31);
   i = i < a.rows ? i : a.rows - 1;
-  const int chunks = a.r / 8, all = chunks * a.parts, n = list.n;
-  for (int c = 0; c < all && n > 0; c += 2) {  // 16 of the r parts
-    const int q = c + half;                     // may pass the end by one: s is 0 there
-    const uint16_t* u = a.u + i * a.r + 8 * (q % chunks);
-    u32x4_t sv[2];
+  const int chunks = a.r / 8, n = list.n;
+  for (int c = 0; c < chunks && n > 0; c += 2) {  // 16 of r
+    const bool in = c + half < chunks;             // r may end in the middle: s is 0 there
+    const uint16_t* u = a.u + i * a.r + 8 * (in ? c + half : c);
+    u32x4_t sv[2][PARTS];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      sv[b] = u32x4_t{0, 0, 0, 0};
-      if (id[b] >= 0 && q < all)
-        sv[b] = load16(a.s2 + (j0 + 32 * b + (lane & 31)) * kParts * a.r + 8 * q);
-    }
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        sv[b][h] = u32x4_t{0, 0, 0, 0};
+        if (id[b] >= 0 && in)
+          sv[b][h] = load16(a.s2 + ((j0 + 32 * b + (lane & 31)) * kParts + h) * a.r +
+                            8 * (c + half));
+      }
     for (int s0 = 0; s0 < n; s0 += kShareSteps) {
       u32x4_t uf[kShareSteps];
       int kk[kShareSteps];
@@ -792,15 +812,24 @@ __global__ __launch_bounds__(256) void lora_add_kernel(AddParams p) {
 #pragma unroll
       for (int t = 0; t < kShareSteps; ++t) {
         if (s0 + t >= n) break;
+        const u32x4_t zero = {0, 0, 0, 0};
+        const bool odd = not_finite(uf[t]), some = __ballot(odd) != 0;
+        const bf16x8_t fine = as_bf16x8(odd ? zero : uf[t]), rest = as_bf16x8(odd ? uf[t] : zero);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const bool own = id[b] == kk[t];
           if (!__ballot(own)) continue;
-          const u32x4_t sf = own ? sv[b] : u32x4_t{0, 0, 0, 0};
-          const f32x16_t v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              as_bf16x8(uf[t]), as_bf16x8(sf), f32x16_t{}, 0, 0, 0);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[b][e] += own ? v[e] : 0.0f;
+          for (int h = 0; h < PARTS; ++h) {
+            const bf16x8_t sf = as_bf16x8(own ? sv[b][h] : zero);
+            acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fine, sf, acc[b], 0, 0, 0);
+            if (some) {
+              const f32x16_t v =
+                  __builtin_amdgcn_mfma_f32_32x32x16_bf16(rest, sf, f32x16_t{}, 0, 0, 0);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[b][e] += own ? v[e] : 0.0f;
+            }
+          }
         }
       }
     }
@@ -1207,17 +1236,25 @@ __global__ __launch_bounds__(64 * NW, 8 / NW) void lora_skinny_kernel(SkinnyPara
 #pragma unroll
         for (int j = 0; j < kShareSteps; ++j) {
           if (s0 + j >= n) break;
+          const u32x4_t zero = {0, 0, 0, 0};
 #pragma unroll
-          for (int t = 0; t < NT16; ++t) {
-            const bool own = id[t] == kk[j];
-            if (!__ballot(own)) continue;
-            const u32x4_t sf = own ? sv[t] : u32x4_t{0, 0, 0, 0};
+          for (int f = 0; f < F; ++f) {
+            const bool odd = not_finite(uf[j][f]), some = __ballot(odd) != 0;
+            const bf16x8_t fine = as_bf16x8(odd ? zero : uf[j][f]);
+            const bf16x8_t rest = as_bf16x8(odd ? uf[j][f] : zero);
 #pragma unroll
-            for (int f = 0; f < F; ++f) {
-              const f32x4_t v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  as_bf16x8(uf[j][f]), as_bf16x8(sf), f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+            for (int t = 0; t < NT16; ++t) {
+              const bool own = id[t] == kk[j];
+              if (!__ballot(own)) continue;
+              const bf16x8_t sf = as_bf16x8(own ? sv[t] : zero);
+              acc[f][t] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(fine, sf, acc[f][t], 0, 0, 0);
+              if (some) {
+                const f32x4_t v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    rest, sf, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[f][t][e] += own ? v[e] : 0.0f;
+                for (int e = 0; e < 4; ++e) acc[f][t][e] += own ? v[e] : 0.0f;
+              }
             }
           }
         }
