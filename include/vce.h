@@ -658,7 +658,8 @@ int ce_sample(const void* logits, int dtype, int64_t d0, int64_t d1, int64_t V, 
  *           and rounded to nearest, so steps below half a place are lost.
  *  total    elements of the flat arrays, a multiple of 128.  m, v and master 16-byte
  *           aligned.
- *  lr, weight_decay, eps >= 0; 0 <= beta1, beta2 < 1; step >= 1, all finite.
+ *  lr, weight_decay, eps >= 0; 0 <= beta1, beta2 < 1; step >= 1, all finite; eps not between 0
+ *           and 2^-126.  Squares of g' below 2^-149 add nothing to v.
  *  lr_device, step_device  one FP32, one int64 on the device, or NULL: taken in the
  *           place of lr and step when the kernels run (a captured call follows them).
  *  grad_scale  one FP32 on the device, or NULL for 1: grad_norm's scale, or the

@@ -46,7 +46,7 @@ def adamw(L, entries=(entry(),), **kw):
     (dict(count=-1), 1), (dict(total=-128), 1), (dict(total=1000), 1), (dict(bits=16), 1),
     (dict(bits=4), 1), (dict(total=1 << 41), 7), (dict(lr=-1.0), 1), (dict(lr=NAN), 1),
     (dict(lr=INF), 1), (dict(eps=-1e-9), 1), (dict(eps=NAN), 1), (dict(eps=INF), 1),
-    (dict(wd=-0.1), 1), (dict(wd=NAN), 1), (dict(wd=INF), 1), (dict(b1=1.0), 1),
+    (dict(eps=1e-38), 1), (dict(wd=-0.1), 1), (dict(wd=NAN), 1), (dict(wd=INF), 1), (dict(b1=1.0), 1),
     (dict(b1=-0.1), 1), (dict(b1=NAN), 1), (dict(b2=1.0), 1), (dict(b2=NAN), 1),
     (dict(step=0), 1), (dict(step=-3), 1), (dict(m=None), 1), (dict(v=None), 1),
     (dict(ms=None), 1), (dict(vs=None), 1), (dict(total=0), 1), (dict(total=896), 1),

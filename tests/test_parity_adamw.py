@@ -91,8 +91,16 @@ def check(params, grads, st, call, scale=1.0, step=3, lr=LR, betas=(B1, B2), eps
         # p: decay (constant, product, difference: 3 u of p); the step: m's error above,
         # root 4.5 u with v's, the reciprocal 1 ulp = 2 u, eps and the factors 5 u, products 2 u
         bc1, bc2 = 1 - b1 ** step, 1 - b2 ** step
-        size = lr / bc1 * S / (np.sqrt(v1 / bc2) + eps)
-        bp = 3 * U * np.abs(old[i]) + 20 * U * size + TINY
+        # v may also lie 2^-148 off: below the normal range its old value's square, g'^2, the two
+        # products and their sum are each rounded by 2^-150 at most (the sum exactly).  The root of
+        # an interval around v then bounds the step.
+        d = np.sqrt(v1 / bc2) + eps
+        lo = np.sqrt(np.maximum(v1 - 2.0 ** -148, 0) / bc2) + eps
+        hi = np.sqrt((v1 + 2.0 ** -148) / bc2) + eps
+        with np.errstate(all="ignore"):
+            size = lr / bc1 * S / d
+            spread = np.where(lo > 0, lr / bc1 * np.abs(m1) * (1 / lo - 1 / hi), 0)
+        bp = 3 * U * np.abs(old[i]) + 20 * U * (size + spread) + spread + TINY
         if st.master is not None:
             assert_within(f64(st.master[at]), p1, bp + U * np.abs(p1), f"master {i}")
             assert bool((st.master[o + n:end] == 0).all())
@@ -136,6 +144,23 @@ def test_first_step_from_zero(bits):
     G[0][:700] = 0  # rows without a gradient: nothing but the decay
     st = vce.adamw_state(P, bits)
     check(P, G, st, lambda: vce.adamw_step(P, G, st, LR, 1, weight_decay=WD), step=1)
+
+
+@pytest.mark.parametrize("scale", [1e-37, 1e-30, 1e-21, 1e-12, 1e6, 1e17])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_small_and_large(bits, scale):
+    """Gradients far from one, down to where their squares leave FP32's normal range."""
+    P, G, st = make([700], "fp32", "fp32", 6, bits)
+    st.m.zero_(), st.v.zero_()
+    G[0] *= scale / 1e-3
+    G[0][64:128] *= 1e-5
+    if 0.1 * scale < 2.0 ** -126:  # an eps below FP32's normal range is refused
+        with pytest.raises(vce.VceError, match="VCE_EINVAL"):
+            vce.adamw_step(P, G, st, LR, 1, eps=0.1 * scale)
+        return
+    for step in (1, 2):
+        check(P, G, st, lambda: vce.adamw_step(P, G, st, LR, step, eps=0.1 * scale,
+                                               weight_decay=WD), step=step, eps=0.1 * scale)
 
 
 def test_many_tensors_shapes_and_none():

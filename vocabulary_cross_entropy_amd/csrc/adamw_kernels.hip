@@ -113,74 +113,80 @@ __host__ __device__ inline uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// E4M3 code of |x| <= 448, up or down by 16 random bits: up where the part below the
-// code's last place, in 65536ths of it, exceeds r.  (x in FP32's bits: exponent and three
-// mantissa bits are the code, the 20 bits below are that part.)
-__device__ __forceinline__ uint32_t code_of(float x, uint32_t r) {
-  const uint32_t a = abs_bits(x);
-  const int c = (int)((a + (0xfffffu - (r << 4))) >> 20) - (120 << 3);
-  return (uint32_t)(c < 0 ? 0 : c);  // 0 for x = 0; below 2^-6 see code_small
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  return __builtin_elementwise_maximum(fabsf(a), fabsf(b));
 }
-// The same below the least normal value, 2^-6: steps of 2^-9.
-__device__ __forceinline__ uint32_t code_small(float x, uint32_t r) {
-  const float t = fabsf(x) * 512.0f;
-  const float k = floorf(t);
-  return (uint32_t)(k + ((t - k) * 65536.0f > (float)r ? 1.0f : 0.0f));
-}
-__device__ __forceinline__ bool is_small(float x) { return abs_bits(x) - 1u < 0x3c7fffffu; }
 
-// Eight values of a block of 32 that four lanes hold: their codes and the block's scale byte.
+// Square root, rounded to nearest: two Newton steps from the reciprocal root, where nothing
+// leaves the normal range (`plain`; all 2^24 significands of two octaves checked against the
+// compiler's, which takes half as many instructions again).
+__device__ __forceinline__ float root_of(float x) {
+  const float r = __builtin_amdgcn_rsqf(x);
+  float s = x * r, h = 0.5f * r;
+  const float e = __builtin_fmaf(-h, s, 0.5f);
+  h = __builtin_fmaf(h, e, h);
+  s = __builtin_fmaf(s, e, s);
+  return __builtin_fmaf(__builtin_fmaf(-s, s, x), h, s);
+}
+__device__ __forceinline__ bool plain(float x) {  // 2^-96 .. 2^126
+  return __float_as_uint(x) - 0x0f800000u < 0x6f000000u;
+}
+
+// Eight values of a block of 32 that four lanes hold: their codes and the block's scale byte.  The
+// conversion adds the upper 20 bits of a number to the part of a value below its last place (in
+// units of 2^-20 of it) and cuts that off; with 2^20 - 1 - 16 r there a value goes up
+// where its part, in 65536ths, exceeds r.
 template <bool KEEP>
-__device__ __forceinline__ u32x2_t round_block(const float* v, const uint32_t* r, int shift,
-                                               uint32_t& byte) {
-  uint32_t a = 0;
+__device__ __forceinline__ u32x2_t round_block(const float* v, const uint32_t* r, uint32_t& byte) {
+  float a = max_abs(v[0], v[1]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = abs_bits(v[j]);
-    a = a > b ? a : b;
-  }
+  for (int j = 2; j < 8; ++j) a = max_abs(a, v[j]);
   // lanes 4 q .. 4 q + 3: neighbours, then pairs
-  uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0xb1, 0xf, 0xf, false);
-  a = a > b ? a : b;
-  b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0x4e, 0xf, 0xf, false);
-  a = a > b ? a : b;
-  byte = mx_scale_byte<kMxE4M3>(a);
+  a = max_abs(a, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+                     0, (int)__float_as_uint(a), 0xb1, 0xf, 0xf, false)));
+  a = max_abs(a, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+                     0, (int)__float_as_uint(a), 0x4e, 0xf, 0xf, false)));
+  byte = mx_scale_byte<kMxE4M3>(abs_bits(a));
   if (byte == 255u) return u32x2_t{0, 0};
-  const float inv = __uint_as_float((254u - byte) << 23);
-  uint32_t code[8];
-  bool small = false;
-  float x[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[j] = v[j] * inv;  // exact
-    small |= is_small(x[j]);
-    code[j] = code_of(x[j], (r[j] >> shift) & 0xffffu);
-  }
-  if (small) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (is_small(x[j])) {
-        code[j] = code_small(x[j], (r[j] >> shift) & 0xffffu);
-        if (KEEP && code[j] == 0) code[j] = 1;
-      }
-  }
+  const float scale = __uint_as_float(byte << 23);  // read as the byte
+  const float least = mx_scale_value(byte) * 0x1p-9f;
   u32x2_t w = {0, 0};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t c = code[j] | (KEEP ? 0u : (__float_as_uint(x[j]) >> 31) << 7);
-    w[j / 4] |= c << (8 * (j % 4));
+    // not 0: at least the least place (roots lie within 2^-75 .. 2^64)
+    const float x = KEEP ? __builtin_amdgcn_fmed3f(v[j], least, v[j] * 0x1p127f) : v[j];
+    const uint32_t n = KEEP ? r[j] | 0xffffu : r[j] << 16 | 0xffffu;
+    switch (j % 4) {  // the byte is an immediate
+      case 0:
+        w[j / 4] = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w[j / 4], x, n, scale, 0);
+        break;
+      case 1:
+        w[j / 4] = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w[j / 4], x, n, scale, 1);
+        break;
+      case 2:
+        w[j / 4] = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w[j / 4], x, n, scale, 2);
+        break;
+      default:
+        w[j / 4] = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w[j / 4], x, n, scale, 3);
+    }
   }
   return w;
 }
 
-// Eight E4M3 codes under a scale byte as FP32 (a code's bits in FP32's fields stand for the
-// value times 2^-120; exact for denormal codes too).
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+// Eight E4M3 codes under a scale byte as FP32 (exact; NaN under 255).
 __device__ __forceinline__ void decode8(const u32x2_t& q, uint32_t byte, float* v) {
-  const float s = byte == 255u ? __builtin_nanf("") : mx_scale_value(byte);
+  const float scale = __uint_as_float(byte << 23);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t c = q[j / 4] >> (8 * (j % 4));
-    v[j] = __uint_as_float(((c & 128u) << 24) | ((c & 127u) << 20)) * 0x1p120f * s;
+  for (int h = 0; h < 2; ++h) {
+    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[h], scale, false);
+    const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[h], scale, true);
+    v[4 * h] = a[0];
+    v[4 * h + 1] = a[1];
+    v[4 * h + 2] = b[0];
+    v[4 * h + 3] = b[1];
   }
 }
 
@@ -239,19 +245,34 @@ __device__ __forceinline__ void chunk(const AdamParams& p, const Coef& k, const 
       decode8(vq[u], vb[u], v[u]);
     }
     float root[VE];
+    bool normal = true;
 #pragma unroll
     for (int j = 0; j < VE; ++j) {
       if constexpr (BITS == 8) v[u][j] = v[u][j] * v[u][j];
       const float gs = g[u][j] * k.scale;
       m[u][j] = m[u][j] * p.b1 + gs * p.c1;
       v[u][j] = v[u][j] * p.b2 + (gs * gs) * p.c2;
-      root[j] = __builtin_sqrtf(v[u][j]);
+      normal &= plain(v[u][j]);
+    }
+    if (normal) {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) root[j] = root_of(v[u][j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) root[j] = __builtin_sqrtf(v[u][j]);
+    }
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
       const float d = root[j] * k.rs + p.eps;
       w[u][j] = w[u][j] * k.decay - k.a * m[u][j] * __builtin_amdgcn_rcpf(d);
-      if (e + j >= t.n) {  // places behind the tensor stay zero
-        m[u][j] = v[u][j] = root[j] = 0.0f;
-        if (MASTER) w[u][j] = 0.0f;
-      }
+    }
+    if (e + VE > t.n) {  // places behind the tensor stay zero
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        if (e + j >= t.n) {
+          m[u][j] = v[u][j] = root[j] = 0.0f;
+          if (MASTER) w[u][j] = 0.0f;
+        }
     }
     if (on) store<PD, VE, WIDE>(t.p, e, t.n, w[u]);
     if (MASTER && on)
@@ -260,10 +281,10 @@ __device__ __forceinline__ void chunk(const AdamParams& p, const Coef& k, const 
       uint32_t r[8];
       const uint32_t key = mix(p.key + (uint32_t)((uint64_t)s >> 32));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = mix(((uint32_t)s + j) ^ key);
+      for (int j = 0; j < 8; ++j) r[j] = ~mix(((uint32_t)s + j) ^ key);
       uint32_t mbyte, vbyte;
-      const u32x2_t mw = round_block<false>(m[u], r, 0, mbyte);
-      const u32x2_t vw = round_block<true>(root, r, 16, vbyte);
+      const u32x2_t mw = round_block<false>(m[u], r, mbyte);
+      const u32x2_t vw = round_block<true>(root, r, vbyte);
       if (!on) continue;
       *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.m) + s) = mw;
       *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.v) + s) = vw;

@@ -1188,7 +1188,7 @@ int adamw_step(const vce_adamw_tensor* tensors, int64_t count, int bits, void* m
   // the comparisons fail for NaN too
   if (!(lr >= 0.0) || !(eps >= 0.0) || !(weight_decay >= 0.0) || !__builtin_isfinite(lr) ||
       !__builtin_isfinite(eps) || !__builtin_isfinite(weight_decay) ||
-      !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || step < 1)
+      (eps > 0.0 && eps < 0x1p-126) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || step < 1)
     return VCE_EINVAL;
   if (count == 0 || total == 0) {
     for (int64_t i = 0; tensors && i < count; ++i)
