@@ -1143,7 +1143,7 @@ def adamw_step(params, grads, state: AdamWState, lr, step, *, betas=(0.9, 0.999)
         raise ValueError(f"state holds {len(sizes)} parameters, got {len(params)} and "
                          f"{len(grads)} gradients")
     ref = state.m
-    dev, f32, bf16 = ref.device, torch.float32, torch.bfloat16
+    index, f32, bf16 = ref.get_device(), torch.float32, torch.bfloat16
     entries = []
     for p, g, n, off in zip(params, grads, sizes, state.offsets):
         if g is None:
@@ -1151,11 +1151,11 @@ def adamw_step(params, grads, state: AdamWState, lr, step, *, betas=(0.9, 0.999)
         pd, gd = p.dtype, g.dtype
         if not ((pd is f32 or pd is bf16) and (gd is f32 or gd is bf16)):
             raise TypeError(f"parameters and gradients must be float32 or bfloat16, got {pd}, {gd}")
-        if p.numel() != n or g.shape != p.shape:
+        if p.numel() != n or not p.is_same_size(g):
             raise ValueError(f"a parameter of {n} elements and its gradient must have one "
                              f"shape, got {tuple(p.shape)} and {tuple(g.shape)}")
-        if p.device != dev or g.device != dev:
-            raise ValueError(f"parameters and gradients must be on {dev}, got {p.device}, "
+        if p.get_device() != index or g.get_device() != index:
+            raise ValueError(f"parameters and gradients must be on {ref.device}, got {p.device}, "
                              f"{g.device}")
         if not (p.is_contiguous() and g.is_contiguous()):
             raise ValueError("parameters and gradients must be contiguous")
@@ -1189,8 +1189,8 @@ def grad_norm(grads, max_norm: float = float("inf"), *, workspace: torch.Tensor 
         if g is None:
             continue
         if ref is None:
-            ref = g
-        if g.device != ref.device:
+            ref, index = g, g.get_device()
+        elif g.get_device() != index:
             raise ValueError(f"gradients must be on {ref.device}, got {g.device}")
         if not g.is_contiguous():
             raise ValueError("gradients must be contiguous")

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = 4096;       // elements of a tensor per workgroup of the step
-constexpr int kNormChunk = 16384;  // and of the norm
+constexpr int kNormChunk = 8192;   // and of the norm
 
 template <int D>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -263,10 +263,12 @@ __device__ __forceinline__ void chunk(const AdamParams& p, const Coef& k, const 
     }
 #pragma unroll
     for (int j = 0; j < VE; ++j) {
-      const float d = root[j] * k.rs + p.eps;
-      w[u][j] = w[u][j] * k.decay - k.a * m[u][j] * __builtin_amdgcn_rcpf(d);
+      // the parameter need not be the same to the last bit: fused
+      const float d = __builtin_fmaf(root[j], k.rs, p.eps);
+      w[u][j] = __builtin_fmaf(-k.a * m[u][j], __builtin_amdgcn_rcpf(d), w[u][j] * k.decay);
     }
-    if (e + VE > t.n) {  // places behind the tensor stay zero
+    // places behind the tensor stay zero (a branch of the wavefront: few are at an end)
+    if (__ballot(e + VE > t.n)) {
 #pragma unroll
       for (int j = 0; j < VE; ++j)
         if (e + j >= t.n) {
@@ -344,16 +346,23 @@ __device__ __forceinline__ double wave_sum(double v) {
 template <int D, bool WIDE>
 __device__ __forceinline__ double squares(const void* g, int64_t n, int64_t e0) {
   constexpr int VE = D == 0 ? 4 : 8;
-  double s[2] = {0.0, 0.0};
-#pragma unroll 4
-  for (int u = 0; u < kNormChunk / kThreads / VE; ++u) {
-    const int64_t e = e0 + ((int64_t)u * kThreads + threadIdx.x) * VE;
-    if (e >= n) break;
-    float v[VE];
-    load<D, VE, WIDE>(g, e, n, v);
+  constexpr int U = kNormChunk / kThreads / VE;
+  float v[U][VE];
+  if (WIDE && e0 + kNormChunk <= n) {  // all loads wait together
 #pragma unroll
-    for (int j = 0; j < VE; ++j) s[j & 1] = __builtin_fma((double)v[j], (double)v[j], s[j & 1]);
+    for (int u = 0; u < U; ++u)
+      load<D, VE, true>(g, e0 + ((int64_t)u * kThreads + threadIdx.x) * VE, INT64_MAX, v[u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      load<D, VE, WIDE>(g, e0 + ((int64_t)u * kThreads + threadIdx.x) * VE, n, v[u]);
   }
+  double s[2] = {0.0, 0.0};
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < VE; ++j)
+      s[j & 1] = __builtin_fma((double)v[u][j], (double)v[u][j], s[j & 1]);
   return s[0] + s[1];
 }
 
