@@ -116,8 +116,8 @@ BAD_STEP = [
     (dict(grads=P[:1]), ValueError, "holds 2"),
     (dict(params=[P[0].double(), P[1]]), TypeError, "float32 or bfloat16"),
     (dict(grads=[P[0].half(), P[1]]), TypeError, "float32 or bfloat16"),
-    (dict(params=[torch.zeros(41), P[1]]), ValueError, "40 elements"),
-    (dict(grads=[torch.zeros((8, 5)), P[1]]), ValueError, "one shape"),
+    (dict(params=[torch.zeros(41), P[1]]), ValueError, "size"),
+    (dict(grads=[torch.zeros((8, 5)), P[1]]), ValueError, "shape"),
     (dict(grads=[P[0], torch.zeros((5, 3)).t()]), ValueError, "contiguous"),
     (dict(lr=torch.zeros(1, dtype=torch.float64)), TypeError, "lr must be"),
     (dict(lr=torch.zeros(2)), ValueError, "lr must hold 1"),

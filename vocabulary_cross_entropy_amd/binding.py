@@ -1130,6 +1130,26 @@ def _scalar(t, name: str, dtype, like: torch.Tensor):
     return _at(t)
 
 
+_DATA_PTR, _NUMEL = torch.Tensor.data_ptr, torch.Tensor.numel
+_SAME_SIZE, _CONTIGUOUS = torch.Tensor.is_same_size, torch.Tensor.is_contiguous
+
+
+def _dtype_codes(ts, name: str):
+    """Library codes of a list's types."""
+    types = [t.dtype for t in ts]
+    if not set(types) <= {torch.float32, torch.bfloat16}:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {set(types)}")
+    return [DTYPE_BF16 if d is torch.bfloat16 else DTYPE_FP32 for d in types]
+
+
+def _check_tensors(ts, name: str, ref: torch.Tensor):
+    """A list of contiguous tensors on ref's device."""
+    if not set(map(torch.Tensor.get_device, ts)) <= {ref.get_device()}:
+        raise ValueError(f"{name} must be on {ref.device}, got {set(t.device for t in ts)}")
+    if not all(map(_CONTIGUOUS, ts)):
+        raise ValueError(f"{name} must be contiguous")
+
+
 def adamw_step(params, grads, state: AdamWState, lr, step, *, betas=(0.9, 0.999),
                eps: float = 1e-8, weight_decay: float = 0.01,
                grad_scale: torch.Tensor | None = None, seed: int = 0, stream=None) -> None:
@@ -1138,37 +1158,37 @@ def adamw_step(params, grads, state: AdamWState, lr, step, *, betas=(0.9, 0.999)
     step (1 for the first) are numbers, or tensors of one element on the device (FP32, int64), read
     when the kernels run.  grad_scale: ``grad_norm``'s scale; not finite, nothing changes.
     seed: of the random rounding of 8-bit states (the step and place enter it too)."""
-    sizes = state.sizes
+    sizes, offsets = state.sizes, state.offsets
     if len(params) != len(sizes) or len(grads) != len(sizes):
         raise ValueError(f"state holds {len(sizes)} parameters, got {len(params)} and "
                          f"{len(grads)} gradients")
     ref = state.m
-    index, f32, bf16 = ref.get_device(), torch.float32, torch.bfloat16
-    entries = []
-    for p, g, n, off in zip(params, grads, sizes, state.offsets):
-        if g is None:
-            continue
-        pd, gd = p.dtype, g.dtype
-        if not ((pd is f32 or pd is bf16) and (gd is f32 or gd is bf16)):
-            raise TypeError(f"parameters and gradients must be float32 or bfloat16, got {pd}, {gd}")
-        if p.numel() != n or not p.is_same_size(g):
-            raise ValueError(f"a parameter of {n} elements and its gradient must have one "
-                             f"shape, got {tuple(p.shape)} and {tuple(g.shape)}")
-        if p.get_device() != index or g.get_device() != index:
-            raise ValueError(f"parameters and gradients must be on {ref.device}, got {p.device}, "
-                             f"{g.device}")
-        if not (p.is_contiguous() and g.is_contiguous()):
-            raise ValueError("parameters and gradients must be contiguous")
-        entries += (p.data_ptr(), g.data_ptr(), n, off,
-                    (pd is bf16) * DTYPE_BF16 | (gd is bf16) * DTYPE_BF16 << 32)
+    have = [g is not None for g in grads]
+    if not all(have):
+        params, grads, sizes, offsets = (
+            [t for t, h in zip(l, have) if h] for l in (params, grads, sizes, offsets))
+    # every check over all tensors at once: a call may bring hundreds of small ones
+    pt, gt = _dtype_codes(params, "parameters"), _dtype_codes(grads, "gradients")
+    if list(map(_NUMEL, params)) != list(sizes) or not all(map(_SAME_SIZE, params, grads)):
+        raise ValueError("a parameter has not the size its state was made for, or its gradient "
+                         "another shape than it")
+    _check_tensors(params, "parameters", ref)
+    _check_tensors(grads, "gradients", ref)
+    count = len(params)
+    # the C structs' fields in order: two pointers, two int64, two int32
+    entries = [0] * (5 * count)
+    entries[0::5] = map(_DATA_PTR, params)
+    entries[1::5] = map(_DATA_PTR, grads)
+    entries[2::5] = sizes
+    entries[3::5] = offsets
+    entries[4::5] = [p | g << 32 for p, g in zip(pt, gt)]
     lr_t = lr if isinstance(lr, torch.Tensor) else None
     step_t = step if isinstance(step, torch.Tensor) else None
-    scalars = (_scalar(lr_t, "lr", f32, ref), _scalar(step_t, "step", torch.int64, ref),
-               _scalar(grad_scale, "grad_scale", f32, ref))
+    scalars = (_scalar(lr_t, "lr", torch.float32, ref),
+               _scalar(step_t, "step", torch.int64, ref),
+               _scalar(grad_scale, "grad_scale", torch.float32, ref))
     host = (0.0 if lr_t is not None else float(lr), float(betas[0]), float(betas[1]), float(eps),
             float(weight_decay), 1 if step_t is not None else int(step))
-    count = len(entries) // 5
-    # the C structs' fields in order: two pointers, two int64, two int32
     table = (ctypes.c_int64 * len(entries))(*entries)
 
     def call(s):
@@ -1184,27 +1204,23 @@ def grad_norm(grads, max_norm: float = float("inf"), *, workspace: torch.Tensor 
     """(norm, scale) of a list of gradients (FP32 or BF16, None entries left out): the root of
     the sum of all squares, and max_norm / norm where that is below 1, else 1 (NaN where norm is
     not finite), as FP32 scalars on the device.  ``out`` gives both."""
-    ref, entries, total = None, [], 0
-    for g in grads:
-        if g is None:
-            continue
-        if ref is None:
-            ref, index = g, g.get_device()
-        elif g.get_device() != index:
-            raise ValueError(f"gradients must be on {ref.device}, got {g.device}")
-        if not g.is_contiguous():
-            raise ValueError("gradients must be contiguous")
-        n = g.numel()
-        entries += (g.data_ptr(), n, _elem_dtype(g, "a gradient"))
-        total += n
-    if ref is None:
+    grads = [g for g in grads if g is not None]
+    if not grads:
         raise ValueError("no gradients")
+    ref, count = grads[0], len(grads)
+    codes = _dtype_codes(grads, "gradients")
+    _check_tensors(grads, "gradients", ref)
+    sizes = list(map(_NUMEL, grads))
+    total = sum(sizes)
+    entries = [0] * (3 * count)
+    entries[0::3] = map(_DATA_PTR, grads)
+    entries[1::3] = sizes
+    entries[2::3] = codes
     outs = (None, None) if out is None else out
     _check_out(outs[0], "norm", (), torch.float32, ref)
     _check_out(outs[1], "scale", (), torch.float32, ref)
     if workspace is not None:
         _check_buf(workspace, "workspace", workspace.numel(), torch.uint8, like=ref)
-    count = len(entries) // 3
     table = (ctypes.c_int64 * len(entries))(*entries)
 
     def call(s):
