@@ -921,7 +921,8 @@ struct OuterShape {
   static constexpr int SP = P == 1 && NC == 1 ? 64 : 32;
   static constexpr int kSlab = SP * kOuter;
   static constexpr int kRows = kParts * 32 * NC;
-  static constexpr int kStage = P * kSlab + kRows * SP;  // elements
+  static constexpr int kLdS = SP + 8;  // a row of S, padded: 16 rows meet all banks once
+  static constexpr int kStage = P * kSlab + kRows * kLdS;  // elements
 };
 
 // A slab of SP token rows of 128 columns in LDS, 256 bytes a row, 16-byte chunk c of row k at
@@ -992,10 +993,6 @@ __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& pla
                                                   8 * piece);
     }
   };
-  // piece `piece` of row c: rows of 128 bytes swapped by c % 8, of 64 by c / 2 % 4
-  auto s_at = [](int row, int c, int piece) {
-    return row * SP + (piece ^ (SP == 64 ? c & 7 : (c >> 1) & 3)) * 8;
-  };
   if (a0 < a1) {
     fetch_tokens(a0);
     fetch(a0);
@@ -1016,7 +1013,7 @@ __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& pla
     for (int e = 0; e < kS; ++e) {
       const int at = e * 256 + t, row = at / kPieces;
       if (row < O::kRows)
-        *reinterpret_cast<u32x4_t LDS_AS*>(ss + s_at(row, row % (32 * NC), at % kPieces)) = sv[e];
+        *reinterpret_cast<u32x4_t LDS_AS*>(ss + row * O::kLdS + at % kPieces * 8) = sv[e];
     }
     if (a + SP < a1) {
       fetch(a + SP);
@@ -1034,7 +1031,7 @@ __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& pla
         for (int h = 0; h < kParts; ++h) {
           const int cc = 32 * c + (lane & 31);
           const u32x4_t sw = *reinterpret_cast<const u32x4_t LDS_AS*>(
-              ss + s_at(h * 32 * NC + cc, cc, 2 * ks + half));
+              ss + (h * 32 * NC + cc) * O::kLdS + (2 * ks + half) * 8);
           const bf16x8_t s = as_bf16x8(sw);
 #pragma unroll
           for (int q = 0; q < P; ++q)
