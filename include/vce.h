@@ -661,7 +661,8 @@ int ce_sample(const void* logits, int dtype, int64_t d0, int64_t d1, int64_t V, 
  *  lr, weight_decay, eps >= 0; 0 <= beta1, beta2 < 1; step >= 1, all finite; eps not between 0
  *           and 2^-126.  Squares of g' below 2^-149 add nothing to v.
  *  lr_device, step_device  one FP32, one int64 on the device, or NULL: taken in the
- *           place of lr and step when the kernels run (a captured call follows them).
+ *           place of lr and step when the kernels run (a captured call follows them).  Where
+ *           lr is negative or not finite there, or step below 1, nothing is changed.
  *  grad_scale  one FP32 on the device, or NULL for 1: grad_norm's scale, or the
  *           inverse of a loss scale.  Where it is not finite nothing is changed.
  *  Outputs must not overlap one another or an input (VCE_EALIAS).

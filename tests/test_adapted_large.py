@@ -38,9 +38,11 @@ def test_adapted_logits_past_2_31():
         assert bool(((base[i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-3).all()), i
 
 
-def test_adapters_gradients_past_2_31():
-    """dy of 2.2e9 elements with odd rows; the gradients of two adapters and some rows of dx."""
-    M, H, V, n, r = 17000, 64, 130001, 2, 8
+@pytest.mark.parametrize("V", [130001, 130048])
+def test_adapters_gradients_past_2_31(V):
+    """dy of 2.2e9 elements with odd rows, laid out anew, and with rows read in place; the
+    gradients of two adapters and some rows of dx."""
+    M, H, n, r = 17000, 64, 2, 8
     x, w = rand((M, H), "bf16", 1), rand((V, H), "bf16", 4, H ** -0.5)
     a, b = rand((n, r, H), "bf16", 2, H ** -0.5), rand((n, V, r), "bf16", 3, r ** -0.5)
     dy = torch.empty((M, V), dtype=torch.bfloat16, device="cuda")

@@ -330,3 +330,19 @@ def test_two_streams():
     torch.cuda.synchronize()
     for w, (P, G, st) in zip(want, (a, b)):
         assert all(torch.equal(x, y) for x, y in zip(w, P + [st.m, st.v]))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("lr,t", [(float("nan"), 1), (float("inf"), 1), (-1e-3, 1), (1e-3, 0), (1e-3, -(1 << 40))])
+def test_numbers_on_the_device_that_are_none(lr, t, bits):
+    """A rate or a step on the device that the host would refuse: nothing changes."""
+    p, g = torch.randn(300, device="cuda"), torch.randn(300, device="cuda")
+    st = vce.adamw_state([p], bits)
+    vce.adamw_step([p], [g], st, 1e-3, 1)
+    held = [x.clone() for x in (p, st.m, st.v)]
+    lr_t = torch.tensor([lr], device="cuda")
+    t_t = torch.tensor([t], dtype=torch.int64, device="cuda")
+    vce.adamw_step([p], [g], st, lr_t, t_t)
+    assert all(torch.equal(x, y) for x, y in zip(held, (p, st.m, st.v)))
+    vce.adamw_step([p], [g], st, lr_t.fill_(1e-3), t_t.fill_(2))
+    assert not torch.equal(held[0], p)

@@ -1156,7 +1156,8 @@ def adamw_step(params, grads, state: AdamWState, lr, step, *, betas=(0.9, 0.999)
     """One AdamW step in place over the parameters that ``state`` was made for, in one launch
     per 64 of them.  A gradient may be None: that parameter and its moments stay.  lr and
     step (1 for the first) are numbers, or tensors of one element on the device (FP32, int64), read
-    when the kernels run.  grad_scale: ``grad_norm``'s scale; not finite, nothing changes.
+    when the kernels run.  grad_scale: ``grad_norm``'s scale; not finite (or such an lr, or a step
+    below 1, on the device), nothing changes.
     seed: of the random rounding of 8-bit states (the step and place enter it too)."""
     sizes, offsets = state.sizes, state.offsets
     if len(params) != len(sizes) or len(grads) != len(sizes):

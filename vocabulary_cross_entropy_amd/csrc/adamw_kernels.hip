@@ -313,6 +313,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamParams p, AdamTable
   if (p.lr_device || p.step_device) {
     const double lr = p.lr_device ? (double)*p.lr_device : p.lr;
     const double t = (double)(p.step_device ? *p.step_device : p.step);
+    if (!(lr >= 0.0 && lr < __builtin_huge_val()) || t < 1.0) return;  // nor here
     const double bc1 = -expm1(t * p.ln_b1), bc2 = -expm1(t * p.ln_b2);
     k.decay = (float)(1.0 - lr * p.wd);
     k.a = (float)(lr / bc1);
