@@ -166,45 +166,57 @@ __device__ void make_plan(const int32_t* adapter, int64_t M, int n, const LoraPl
     place(adapter_of(adapter, i + lane, i1, n), i);
 }
 
-// (n, R, C) to (n, C, ldr), the places from R to ldr zero.
+// (n, R, C) to (n, C, ldr), the places from R to ldr zero; C and ldr multiples of 8.  A workgroup
+// takes a tile of 8192 elements, 16 bytes a thread, as narrow as the rank.
 struct TransposeProblem {
   const uint16_t* in;
   uint16_t* out;
   int64_t R, C, ldr;
+  int tr, tc;     // rows and columns of a tile, powers of two from 8 on
   int64_t tiles;  // of an adapter
 };
 
+constexpr int kTransposed = kPlanThreads * 8;
+
 inline TransposeProblem transpose_of(const uint16_t* in, uint16_t* out, int64_t R, int64_t C,
-                                     int64_t ldr) {
-  return TransposeProblem{in, out, R, C, ldr, (ldr + 63) / 64 * ((C + 63) / 64)};
+                                     int64_t ldr, int64_t rank) {
+  int narrow = 8;
+  while (narrow < rank) narrow *= 2;
+  const int tr = R == rank ? narrow : kTransposed / narrow, tc = kTransposed / tr;
+  return TransposeProblem{in, out, R, C, ldr, tr, tc, (ldr + tr - 1) / tr * ((C + tc - 1) / tc)};
 }
 
 constexpr int64_t kScan = 16384;  // tokens that a tile looks through for its adapter
 
 __device__ void transpose(const TransposeProblem& q, int k, int64_t w, const int32_t* adapter,
                           int64_t M) {
-  __shared__ uint16_t sh[64][66];
+  __shared__ __attribute__((aligned(16))) uint16_t sh[2 * kTransposed];  // and 8 a column
   if (M <= kScan) {  // an adapter without tokens is left out
     bool used = false;
     for (int64_t i = threadIdx.x; i < M; i += kPlanThreads) used |= adapter[i] == k;
     if (!__syncthreads_or(used)) return;
   }
-  const int64_t nc = (q.C + 63) / 64;
-  const int64_t r0 = w / nc * 64, c0 = w % nc * 64;
+  const int64_t nc = (q.C + q.tc - 1) / q.tc;
+  const int64_t r0 = w / nc * q.tr, c0 = w % nc * q.tc;
   const uint16_t* in = q.in + k * q.R * q.C;
   uint16_t* out = q.out + k * q.C * q.ldr;
-  const int x = threadIdx.x & 63;
+  const int ld = q.tr + 8;  // of a column in LDS
+  {
+    const int per = q.tc / 8, y = threadIdx.x / per, x = threadIdx.x % per * 8;
+    u32x4_t v = {0, 0, 0, 0};
+    if (r0 + y < q.R && c0 + x < q.C) v = load16(in + (r0 + y) * q.C + c0 + x);
 #pragma unroll
-  for (int y = threadIdx.x >> 6; y < 64; y += kPlanWaves)
-    sh[y][x] = r0 + y < q.R && c0 + x < q.C ? in[(r0 + y) * q.C + c0 + x] : (uint16_t)0;
+    for (int e = 0; e < 8; ++e) sh[(x + e) * ld + y] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+  }
   __syncthreads();
-#pragma unroll
-  for (int y = threadIdx.x >> 6; y < 64; y += kPlanWaves)
-    if (c0 + y < q.C && r0 + x < q.ldr) out[(c0 + y) * q.ldr + r0 + x] = sh[x][y];
+  const int per = q.tr / 8, y = threadIdx.x / per, x = threadIdx.x % per * 8;
+  if (c0 + y < q.C && r0 + x < q.ldr)
+    *reinterpret_cast<u32x4_t*>(out + (c0 + y) * q.ldr + r0 + x) =
+        *reinterpret_cast<const u32x4_t*>(sh + y * ld + x);
 }
 
 // Workgroup (0, 0) makes the plan; the others lay out the adapters' weights along what a product
-// sums over (the backward; tiles of 64 x 64).
+// sums over (the backward).
 __global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* adapter, int64_t M,
                                                                  int n, LoraPlan plan,
                                                                  TransposeProblem a,
@@ -290,31 +302,50 @@ __device__ __forceinline__ void finish_sum(const ShrinkProblem& q, float v, int 
   }
 }
 
-// Eight elements of a row from `at` on, `left` of them before its end and 0 past it, in N BF16
-// parts (one for a BF16 row).
+// Eight elements of a row as they lie in memory.
+template <int DT>
+struct Raw8 {
+  u32x4_t w[DT == 0 ? 2 : 1];
+};
+
+// Elements from `at` on, `left` of them before the row's end and 0 past it.
+template <int DT>
+__device__ __forceinline__ void load8(const void* x, int64_t at, int64_t left, Raw8<DT>& v) {
+  if (left >= 8) {
+    if constexpr (DT == 1)
+      v.w[0] = load16(static_cast<const uint16_t*>(x) + at);
+    else
+      __builtin_memcpy(&v, static_cast<const float*>(x) + at, 32);
+  } else if constexpr (DT == 1) {
+    const uint16_t* q = static_cast<const uint16_t*>(x) + at;
+    uint32_t e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = j < left ? q[j] : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v.w[0][j] = e[2 * j] | e[2 * j + 1] << 16;
+  } else {
+    const uint32_t* q = static_cast<const uint32_t*>(x) + at;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v.w[DT == 0 ? j / 4 : 0][j % 4] = j < left ? q[j] : 0;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void zero8(Raw8<DT>& v) {
+#pragma unroll
+  for (auto& w : v.w) w = u32x4_t{0, 0, 0, 0};
+}
+
+// In N BF16 parts (one for a BF16 row).  Apart from the loading, so that it waits where it is used.
 template <int DT, int N>
-__device__ __forceinline__ void row8(const void* x, int64_t at, int64_t left, u32x4_t (&part)[N]) {
+__device__ __forceinline__ void parts8(const Raw8<DT>& x, u32x4_t (&part)[N]) {
   if constexpr (DT == 1) {
     static_assert(N == 1, "BF16 has one part");
-    const uint16_t* q = static_cast<const uint16_t*>(x) + at;
-    if (left >= 8) {
-      part[0] = load16(q);
-    } else {
-      uint32_t e[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = j < left ? q[j] : 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) part[0][j] = e[2 * j] | e[2 * j + 1] << 16;
-    }
+    part[0] = x.w[0];
   } else {
-    const float* q = static_cast<const float*>(x) + at;
     float v[8];
-    if (left >= 8) {
-      __builtin_memcpy(v, q, 32);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < left ? q[j] : 0.0f;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(x.w[j / 4][j % 4]);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -363,7 +394,8 @@ __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& p
 #pragma unroll
     for (int j = 0; j < NC; ++j) acc[f][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   struct Buf {
-    u32x4_t x[S][2][N], u[S][NC];
+    Raw8<DT> x[S][2];
+    u32x4_t u[S][NC];
   };
   // 32 S k from k on; TAIL: they may pass the end
   auto load = [&](Buf& b, int64_t k, auto tail) {
@@ -373,13 +405,8 @@ __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& p
       const int64_t at = k + 32 * s, left = q.K - at - 8 * g;
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        if constexpr (TAIL) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) b.x[s][f][i] = u32x4_t{0, 0, 0, 0};
-          if (left > 0) row8<DT, N>(q.x, row[f] + at, left, b.x[s][f]);
-        } else {
-          row8<DT, N>(q.x, row[f] + at, 8, b.x[s][f]);
-        }
+        if (TAIL) zero8<DT>(b.x[s][f]);
+        if (!TAIL || left > 0) load8<DT>(q.x, row[f] + at, TAIL ? left : 8, b.x[s][f]);
       }
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
@@ -392,14 +419,17 @@ __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& p
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int f = 0; f < 2; ++f) {
+        u32x4_t x[N];
+        parts8<DT, N>(b.x[s][f], x);
 #pragma unroll
         for (int j = 0; j < NC; ++j)
           // D: rows (four of this lane) are sums c, the column is the token
 #pragma unroll
           for (int i = 0; i < N; ++i)
             acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                as_bf16x8(b.u[s][j]), as_bf16x8(b.x[s][f][i]), acc[f][j], 0, 0, 0);
+                as_bf16x8(b.u[s][j]), as_bf16x8(x[i]), acc[f][j], 0, 0, 0);
+      }
   };
   const int64_t k0 = split * q.per + wave * (q.per / 4);
   const int64_t k1 = k0 + q.per / 4 < q.K ? k0 + q.per / 4 : q.K;
@@ -879,24 +909,6 @@ struct EpiSum {
   }
 };
 
-template <bool MASK, int NSEG>
-__global__ __launch_bounds__(NT, 1) void lora_split_kernel(Segs<NSEG> G, int64_t K, int64_t per,
-                                                           int n_ti, int n_tj, EpiSum::Params ep) {
-  __shared__ __attribute__((aligned(1024))) uint16_t smem[kSmemElems];
-  const int n = n_ti * n_tj, t = blockIdx.x / n;
-  const int64_t k0 = t * per;
-#pragma unroll
-  for (int s = 0; s < NSEG; ++s) {
-    G.P[s].base += k0 * G.P[s].ld;  // dim-contiguous
-    G.P[s].k_limit -= k0;
-    G.Q[s].base += k0;
-    G.Q[s].k_limit -= k0;
-  }
-  ep.out += t * ep.rows * ep.cols;
-  gemm_tile<EpiSum, true, false, MASK, NSEG>(G, K - k0 < per ? K - k0 : per, blockIdx.x - t * n,
-                                             n_ti, n_tj, ep, smem);
-}
-
 // ---- the adapters' gradients ------------------------------------------------------------------
 
 // out_k[c][d] = sum over the places of adapter k of S(c, place) Y(token, d), S by place in parts
@@ -911,12 +923,11 @@ struct OuterProblem {
   int blocks;  // column tiles
 };
 
-constexpr int kOuter = 128;  // columns of a workgroup
-
-// Places of a step, and a stage of LDS: SP token rows of 128 columns in Y's parts, then S's
-// parts, 32 NC rows of SP places.
-template <int DT, int NC>
+// Columns of a workgroup; places of a step; and a stage of LDS: SP token rows of Y's columns in
+// its parts, then S's parts, 32 NC rows of SP places.
+template <int DT, int NC, int W>
 struct OuterShape {
+  static constexpr int kOuter = 128 * W;
   static constexpr int P = row_parts<DT>();
   static constexpr int SP = P == 1 && NC == 1 ? 64 : 32;
   static constexpr int kSlab = SP * kOuter;
@@ -925,77 +936,83 @@ struct OuterShape {
   static constexpr int kStage = P * kSlab + kRows * kLdS;  // elements
 };
 
-// A slab of SP token rows of 128 columns in LDS, 256 bytes a row, 16-byte chunk c of row k at
-// c ^ 4 (k % 4), read back transposed (the layout of the product's dim-contiguous operand).
+// A slab of SP token rows in LDS, LD columns a row, 16-byte chunk c of row k at c ^ 4 (k % 4), read
+// back transposed (the layout of the product's dim-contiguous operand).
+template <int LD>
 __device__ __forceinline__ bf16x8_t slab_frag(const uint16_t LDS_AS* s, int d0, int ks, int lane) {
   const int g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
   const int d = d0 + 16 * (g & 1) + 4 * q;
   const int k = 16 * ks + 8 * (g >> 1) + j;
-  const uint16_t LDS_AS* p = s + k * kOuter + (((d >> 3) ^ (4 * j)) * 8) + (d & 7);
+  const uint16_t LDS_AS* p = s + k * LD + (((d >> 3) ^ (4 * j)) * 8) + (d & 7);
   const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v4i16_t LDS_AS*)p);
-  const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v4i16_t LDS_AS*)(p + 4 * kOuter));
+  const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v4i16_t LDS_AS*)(p + 4 * LD));
   const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
   return __builtin_bit_cast(bf16x8_t, u32x4_t{a[0], a[1], b[0], b[1]});
 }
 
 // Steps of SP places go through two stages of LDS; the next step's rows are on their way in
 // registers, and the tokens of the one after.
-template <int DT, int NC, bool BYCOL>
+template <int DT, int NC, int W, bool BYCOL>
 __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& plan, int r, int k,
                                       int block, int64_t places, uint16_t* smem) {
-  using O = OuterShape<DT, NC>;
-  constexpr int P = O::P, SP = O::SP;
-  constexpr int kY = SP / 16;                      // rows of a thread
+  using O = OuterShape<DT, NC, W>;
+  constexpr int P = O::P, SP = O::SP, kOuter = O::kOuter;
+  constexpr int kChunks = kOuter / 8, kPass = 256 / kChunks;  // 16-byte chunks, rows of a pass
+  constexpr int kY = SP / kPass;                              // rows of a thread
   constexpr int kPieces = SP / 8;                  // 16-byte pieces of a row of S
   constexpr int kS = (O::kRows * kPieces + 255) / 256;  // of a thread
   uint16_t LDS_AS* const lds = (uint16_t LDS_AS*)smem;
   const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t d0 = (int64_t)block * kOuter;
-  f32x16_t acc[NC];
+  f32x16_t acc[W][NC];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) acc[c] = f32x16_t{};
+  for (int w = 0; w < W; ++w)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[w][c] = f32x16_t{};
   const int a0 = plan.first[k] * kTile, a1 = plan.first[k + 1] * kTile;
-  const int chunk = t & 15;
+  const int chunk = t % kChunks;
   const int64_t d = d0 + 8 * chunk;
   const bool whole = d0 + kOuter <= p.D;  // the same for all threads
   int token[kY];
-  u32x4_t yv[kY][P], sv[kS];
+  struct Buf {
+    Raw8<DT> y[kY];
+    u32x4_t s[kS];
+    uint32_t none;  // bits of the rows without a token
+  } buf;
   auto fetch_tokens = [&](int a) {
 #pragma unroll
     for (int h = 0; h < kY; ++h) {
-      const int place = a + 16 * h + (t >> 4);
+      const int place = a + kPass * h + t / kChunks;
       token[h] = place < a1 ? plan.order[place] : -1;
     }
   };
-  auto fetch = [&](int a) {
+  auto fetch = [&](Buf& b, int a) {
+    b.none = 0;
 #pragma unroll
     for (int h = 0; h < kY; ++h) {
       const int64_t at = (int64_t)(token[h] < 0 ? 0 : token[h]) * p.ldy + d;
+      b.none |= token[h] < 0 ? 1u << h : 0u;
       if (whole) {
-        row8<DT, P>(p.y, at, 8, yv[h]);
+        load8<DT>(p.y, at, 8, b.y[h]);
       } else {
-#pragma unroll
-        for (int q = 0; q < P; ++q) yv[h][q] = u32x4_t{0, 0, 0, 0};
-        if (d < p.D) row8<DT, P>(p.y, at, p.D - d, yv[h]);
+        zero8<DT>(b.y[h]);
+        if (d < p.D) load8<DT>(p.y, at, p.D - d, b.y[h]);
       }
-      // no token there: not even what is not finite
-#pragma unroll
-      for (int q = 0; q < P; ++q) yv[h][q] = token[h] < 0 ? u32x4_t{0, 0, 0, 0} : yv[h][q];
     }
 #pragma unroll
     for (int e = 0; e < kS; ++e) {
       const int at = e * 256 + t, row = at / kPieces, piece = at % kPieces;
       const int c = row % (32 * NC), q = row / (32 * NC);
-      sv[e] = u32x4_t{0, 0, 0, 0};
+      b.s[e] = u32x4_t{0, 0, 0, 0};
       if (row < O::kRows && c < r && a + 8 * piece < a1)
-        sv[e] = *reinterpret_cast<const u32x4_t*>(p.s + ((int64_t)q * r + c) * places + a +
+        b.s[e] = *reinterpret_cast<const u32x4_t*>(p.s + ((int64_t)q * r + c) * places + a +
                                                   8 * piece);
     }
   };
   if (a0 < a1) {
     fetch_tokens(a0);
-    fetch(a0);
+    fetch(buf, a0);
     fetch_tokens(a0 + SP);
   }
   for (int a = a0; a < a1; a += SP) {
@@ -1003,28 +1020,35 @@ __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& pla
     uint16_t LDS_AS* const ss = stage + P * O::kSlab;
 #pragma unroll
     for (int h = 0; h < kY; ++h) {
-      const int row = 16 * h + (t >> 4);
+      const int row = kPass * h + t / kChunks;
       const int at = row * kOuter + ((chunk ^ (4 * (row & 3))) * 8);
+      // no token there: not even what is not finite
+      if (buf.none >> h & 1) zero8<DT>(buf.y[h]);
+      u32x4_t part[P];
+      parts8<DT, P>(buf.y[h], part);
 #pragma unroll
       for (int q = 0; q < P; ++q)
-        *reinterpret_cast<u32x4_t LDS_AS*>(stage + q * O::kSlab + at) = yv[h][q];
+        *reinterpret_cast<u32x4_t LDS_AS*>(stage + q * O::kSlab + at) = part[q];
     }
 #pragma unroll
     for (int e = 0; e < kS; ++e) {
       const int at = e * 256 + t, row = at / kPieces;
       if (row < O::kRows)
-        *reinterpret_cast<u32x4_t LDS_AS*>(ss + row * O::kLdS + at % kPieces * 8) = sv[e];
+        *reinterpret_cast<u32x4_t LDS_AS*>(ss + row * O::kLdS + at % kPieces * 8) = buf.s[e];
     }
     if (a + SP < a1) {
-      fetch(a + SP);
+      fetch(buf, a + SP);
       fetch_tokens(a + 2 * SP);
     }
     lds_barrier();  // one a step: the other stage is written behind the next
 #pragma unroll
     for (int ks = 0; ks < SP / 16; ++ks) {
-      bf16x8_t y[P];
+      bf16x8_t y[W][P];
 #pragma unroll
-      for (int q = 0; q < P; ++q) y[q] = slab_frag(stage + q * O::kSlab, 32 * wave, ks, lane);
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+          y[w][q] = slab_frag<kOuter>(stage + q * O::kSlab, 32 * (W * wave + w), ks, lane);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -1034,54 +1058,96 @@ __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& pla
               ss + (h * 32 * NC + cc) * O::kLdS + (2 * ks + half) * 8);
           const bf16x8_t s = as_bf16x8(sw);
 #pragma unroll
-          for (int q = 0; q < P; ++q)
-            if (h + q < kParts)
-              acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(s, y[q], acc[c], 0, 0, 0);
+          for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+              if (h + q < kParts)
+                acc[w][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(s, y[w][q], acc[w][c], 0, 0, 0);
         }
     }
   }
-  const int64_t col = d0 + 32 * wave + (lane & 31);
-  if (col >= p.D) return;
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
+  for (int w = 0; w < W; ++w) {
+    const int64_t col = d0 + 32 * (W * wave + w) + (lane & 31);
+    if (col >= p.D) return;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int row = 32 * c + 8 * q + 4 * half;
-      if (row >= r) continue;
-      if constexpr (BYCOL) {
-        *reinterpret_cast<f32x4_t*>(p.out + ((int64_t)k * p.D + col) * r + row) =
-            f32x4_t{acc[c][4 * q], acc[c][4 * q + 1], acc[c][4 * q + 2], acc[c][4 * q + 3]};
-      } else {
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          p.out[((int64_t)k * r + row + e) * p.D + col] = acc[c][4 * q + e];
+      for (int q = 0; q < 4; ++q) {
+        const int row = 32 * c + 8 * q + 4 * half;
+        if (row >= r) continue;
+        const f32x16_t& v = acc[w][c];
+        if constexpr (BYCOL) {
+          *reinterpret_cast<f32x4_t*>(p.out + ((int64_t)k * p.D + col) * r + row) =
+              f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p.out[((int64_t)k * r + row + e) * p.D + col] = v[4 * q + e];
+        }
       }
-    }
+  }
 }
 
 // Of dB's rows or, where that needs more, of dA's BF16 ones.
-template <int DT, int NC>
+template <int DT, int NC, int W>
 constexpr int lora_outer_stage() {
-  return OuterShape<DT, NC>::kStage > OuterShape<1, NC>::kStage ? OuterShape<DT, NC>::kStage
-                                                                : OuterShape<1, NC>::kStage;
+  return OuterShape<DT, NC, W>::kStage > OuterShape<1, NC, W>::kStage
+             ? OuterShape<DT, NC, W>::kStage
+             : OuterShape<1, NC, W>::kStage;
 }
 
-// dB's tiles first, then dA's.
-template <int DT, int NC>
-__global__ __launch_bounds__(256) void lora_outer_kernel(OuterProblem b, OuterProblem a,
-                                                         LoraPlan plan, int n, int r,
-                                                         int n_tiles) {
-  __shared__ __attribute__((aligned(256))) uint16_t smem[2 * lora_outer_stage<DT, NC>()];
-  const int64_t places = (int64_t)n_tiles * kTile;
-  const int64_t nb = (int64_t)n * b.blocks;
-  int64_t w = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+struct OuterPair {
+  OuterProblem b, a;  // dB's tiles first, then dA's
+  LoraPlan plan;
+  int n, r, n_tiles;
+};
+
+template <int DT, int NC, int W>
+__device__ __forceinline__ void outer_tile(const OuterPair& p, int64_t w, uint16_t* smem) {
+  const int64_t places = (int64_t)p.n_tiles * kTile, nb = (int64_t)p.n * p.b.blocks;
   if (w < nb) {
-    outer<DT, NC, true>(b, plan, r, (int)(w / b.blocks), (int)(w % b.blocks), places, smem);
+    outer<DT, NC, W, true>(p.b, p.plan, p.r, (int)(w / p.b.blocks), (int)(w % p.b.blocks), places,
+                           smem);
   } else {
     w -= nb;
-    if (w >= (int64_t)n * a.blocks) return;
-    outer<1, NC, false>(a, plan, r, (int)(w / a.blocks), (int)(w % a.blocks), places, smem);
+    if (w >= (int64_t)p.n * p.a.blocks) return;
+    outer<1, NC, W, false>(p.a, p.plan, p.r, (int)(w / p.a.blocks), (int)(w % p.a.blocks), places,
+                           smem);
   }
+}
+
+template <int DT, int NC, int W>
+__global__ __launch_bounds__(256) void lora_outer_kernel(OuterPair p) {
+  __shared__ __attribute__((aligned(256))) uint16_t smem[2 * lora_outer_stage<DT, NC, W>()];
+  outer_tile<DT, NC, W>(p, (int64_t)blockIdx.y * gridDim.x + blockIdx.x, smem);
+}
+
+// dy W in parts and behind them the adapters' gradients, in one grid: the product's tiles leave CUs
+// idle that the gradients, bound by their loads, need not wait for.  Their workgroups take 256
+// columns, since only one lies on a CU here.
+template <bool MASK, int NSEG, int DT, int NC>
+__global__ __launch_bounds__(NT, 1) void lora_split_kernel(Segs<NSEG> G, int64_t K, int64_t per,
+                                                           int n_ti, int n_tj, int blocks,
+                                                           EpiSum::Params ep, OuterPair p) {
+  constexpr int kOuterElems = NC > 0 ? 2 * lora_outer_stage<DT, (NC > 0 ? NC : 1), 2>() : 0;
+  constexpr int kElems = kOuterElems > kSmemElems ? kOuterElems : kSmemElems;
+  __shared__ __attribute__((aligned(1024))) uint16_t smem[kElems];
+  if constexpr (NC > 0) {
+    if ((int)blockIdx.x >= blocks) return outer_tile<DT, NC, 2>(p, (int)blockIdx.x - blocks, smem);
+  }
+  const int n = n_ti * n_tj, t = blockIdx.x / n;
+  const int64_t k0 = t * per;
+#pragma unroll
+  for (int s = 0; s < NSEG; ++s) {
+    G.P[s].base += k0 * G.P[s].ld;  // dim-contiguous
+    G.P[s].k_limit -= k0;
+    G.Q[s].base += k0;
+    G.Q[s].k_limit -= k0;
+  }
+  ep.out += t * ep.rows * ep.cols;
+  gemm_tile<EpiSum, true, false, MASK, NSEG>(G, K - k0 < per ? K - k0 : per, blockIdx.x - t * n,
+                                             n_ti, n_tj, ep, smem);
 }
 
 // ---- layouts ----------------------------------------------------------------------------------
@@ -1095,10 +1161,11 @@ __global__ __launch_bounds__(256) void lora_rows_kernel(const void* dy, int64_t 
   const int64_t i = blockIdx.x, v = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
   if (v >= ldv) return;
   constexpr int N = DT == 0 ? 2 : 1;
+  Raw8<DT> x;
+  zero8<DT>(x);
+  if (V - v > 0) load8<DT>(dy, i * ldy + v, V - v, x);
   u32x4_t part[N];
-#pragma unroll
-  for (int q = 0; q < N; ++q) part[q] = u32x4_t{0, 0, 0, 0};
-  if (V - v > 0) row8<DT, N>(dy, i * ldy + v, V - v, part);
+  parts8<DT, N>(x, part);
 #pragma unroll
   for (int q = 0; q < N; ++q)
     *reinterpret_cast<u32x4_t*>(out + q * plane + i * ldv + v) = part[q];
@@ -1403,19 +1470,19 @@ hipError_t run_shrink(const ShrinkProblem& s, const ShrinkProblem& d, const Lora
   return hipGetLastError();
 }
 
+constexpr int kOuterW = 1;  // columns / 128 of a workgroup of the gradients alone
+
+inline int outer_blocks(int64_t D, int W) { return (int)((D + 128 * W - 1) / (128 * W)); }
+
 template <int DT>
-hipError_t run_outer(const OuterProblem& b, const OuterProblem& a, const LoraPlan& plan, int n,
-                     int r, int tiles, hipStream_t stream) {
-  const dim3 grid = grid2((int64_t)n * (b.blocks + a.blocks));
-  if (r <= 32)
-    hipLaunchKernelGGL((lora_outer_kernel<DT, 1>), grid, dim3(256), 0, stream, b, a, plan, n, r,
-                       tiles);
-  else if (r <= 64)
-    hipLaunchKernelGGL((lora_outer_kernel<DT, 2>), grid, dim3(256), 0, stream, b, a, plan, n, r,
-                       tiles);
+hipError_t run_outer(const OuterPair& p, hipStream_t stream) {
+  const dim3 grid = grid2((int64_t)p.n * (p.b.blocks + p.a.blocks));
+  if (p.r <= 32)
+    hipLaunchKernelGGL((lora_outer_kernel<DT, 1, kOuterW>), grid, dim3(256), 0, stream, p);
+  else if (p.r <= 64)
+    hipLaunchKernelGGL((lora_outer_kernel<DT, 2, kOuterW>), grid, dim3(256), 0, stream, p);
   else
-    hipLaunchKernelGGL((lora_outer_kernel<DT, 4>), grid, dim3(256), 0, stream, b, a, plan, n, r,
-                       tiles);
+    hipLaunchKernelGGL((lora_outer_kernel<DT, 4, kOuterW>), grid, dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -1517,24 +1584,40 @@ struct BwdPlan {
   }
 };
 
+// dy W in sp.n parts, and the adapters' gradients where `p` has any.
+template <int DT, bool MASK, int NC, int NSEG>
+hipError_t run_split(const Segs<NSEG>& G, int64_t K, const Split& sp, int n_ti, int n_tj,
+                     const EpiSum::Params& ep, const OuterPair& p, hipStream_t stream) {
+  const int blocks = n_ti * n_tj * sp.n;
+  const int64_t more = NC > 0 ? (int64_t)p.n * (p.b.blocks + p.a.blocks) : 0;
+  hipLaunchKernelGGL((lora_split_kernel<MASK, NSEG, DT, NC>), dim3((unsigned)(blocks + more)),
+                     dim3(NT), 0, stream, G, K, sp.per, n_ti, n_tj, blocks, ep, p);
+  return hipGetLastError();
+}
+
 // dx = dy W + the adapters' share, the sum over V in sp.n parts.
-template <int NSEG>
+template <int DT, int NSEG>
 hipError_t dx_product(const Segs<NSEG>& G, const LoraBwdArgs& p, const LoraShare& a,
-                      const Split& sp, float* part, hipStream_t stream) {
+                      const Split& sp, float* part, const OuterPair* outer, hipStream_t stream) {
   if (sp.n == 1)
     return run_gemm<EpiLora<1>, true, false, NSEG>(G, p.H, p.M, p.V,
                                                    typename EpiLora<1>::Params{a, p.dx, p.H},
                                                    stream);
   const int n_ti = (int)((p.H + BM - 1) / BM), n_tj = (int)((p.M + BN - 1) / BN);
   const EpiSum::Params ep{part, p.H, p.M};
-  const dim3 grid((unsigned)(n_ti * n_tj * sp.n));
-  if (p.V % (2 * BK) != 0)
-    hipLaunchKernelGGL((lora_split_kernel<true, NSEG>), grid, dim3(NT), 0, stream, G, p.V, sp.per,
-                       n_ti, n_tj, ep);
-  else
-    hipLaunchKernelGGL((lora_split_kernel<false, NSEG>), grid, dim3(NT), 0, stream, G, p.V, sp.per,
-                       n_ti, n_tj, ep);
-  const hipError_t e = hipGetLastError();
+  const bool mask = p.V % (2 * BK) != 0;
+  const int nc = !outer ? 0 : p.r <= 32 ? 1 : p.r <= 64 ? 2 : 4;
+  const OuterPair none{};
+  const auto go = [&](auto m) {
+    constexpr bool MASK = decltype(m)::value;
+    switch (nc) {
+      case 0: return run_split<DT, MASK, 0>(G, p.V, sp, n_ti, n_tj, ep, none, stream);
+      case 1: return run_split<DT, MASK, 1>(G, p.V, sp, n_ti, n_tj, ep, *outer, stream);
+      case 2: return run_split<DT, MASK, 2>(G, p.V, sp, n_ti, n_tj, ep, *outer, stream);
+      default: return run_split<DT, MASK, 4>(G, p.V, sp, n_ti, n_tj, ep, *outer, stream);
+    }
+  };
+  const hipError_t e = mask ? go(std::true_type{}) : go(std::false_type{});
   if (e != hipSuccess) return e;
   return run_add<1, 0>(AddParams{a, part, p.H, p.M * p.H, sp.n, p.dx, p.H}, stream);
 }
@@ -1547,8 +1630,8 @@ hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
   auto bf = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
   auto fp = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   hipError_t e;
-  const TransposeProblem ta = transpose_of(p.a, bf(b.at), p.r, p.H, p.r);
-  const TransposeProblem tb = transpose_of(p.b, bf(b.bt), p.V, p.r, b.ldv);
+  const TransposeProblem ta = transpose_of(p.a, bf(b.at), p.r, p.H, p.r, p.r);
+  const TransposeProblem tb = transpose_of(p.b, bf(b.bt), p.V, p.r, b.ldv, p.r);
   hipLaunchKernelGGL(lora_plan_kernel, dim3((unsigned)(1 + ta.tiles + tb.tiles), (unsigned)p.n),
                      dim3(kPlanThreads), 0, stream, p.adapter, p.M, p.n, plan, ta, tb);
   if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1558,6 +1641,17 @@ hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
                         bf(b.d_token), bf(b.d_place)};
   if (p.M > 0 && (e = run_shrink<DT>(s, d, plan, p.scale, p.n, p.r, tiles, stream)) != hipSuccess)
     return e;
+  const auto gradients = [&](int W) {
+    return OuterPair{
+        OuterProblem{bf(b.s_place), p.dy, p.ldy, p.V, p.db, p.db ? outer_blocks(p.V, W) : 0},
+        OuterProblem{bf(b.d_place), p.x, p.ldx, p.H, p.da, p.da ? outer_blocks(p.H, W) : 0},
+        plan, p.n, p.r, tiles};
+  };
+  const OuterPair beside = gradients(2);
+  // with a split product, in its grid
+  const bool joined = p.dx && p.M > 0 && p.w && b.dx.n > 1 && (p.da || p.db) &&
+                      (int64_t)p.n * (beside.b.blocks + beside.a.blocks) <= (int64_t)1 << 20;
+  const OuterPair* const with = joined ? &beside : nullptr;
   if (p.dx && p.M > 0) {
     const LoraShare a{bf(b.at), bf(b.d_token), p.adapter, p.n, p.r, 2, p.H, p.M};
     if (!p.w) {
@@ -1579,21 +1673,15 @@ hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
       const Operand W{p.w, p.H, p.H, p.V};
       if constexpr (DT == 0) {
         const Operand hi{rows, ld, p.M, p.V}, lo{rows + p.M * b.ldv, ld, p.M, p.V};
-        e = dx_product<2>(Segs<2>{{W, W}, {hi, lo}}, p, a, b.dx, fp(b.dx_part), stream);
+        e = dx_product<0>(Segs<2>{{W, W}, {hi, lo}}, p, a, b.dx, fp(b.dx_part), with, stream);
       } else {
         const Operand Y{rows, ld, p.M, p.V};
-        e = dx_product<1>(Segs<1>{{W}, {Y}}, p, a, b.dx, fp(b.dx_part), stream);
+        e = dx_product<1>(Segs<1>{{W}, {Y}}, p, a, b.dx, fp(b.dx_part), with, stream);
       }
     }
     if (e != hipSuccess) return e;
   }
-  if (p.da || p.db) {
-    const OuterProblem ob{bf(b.s_place), p.dy, p.ldy, p.V, p.db,
-                          p.db ? (int)((p.V + kOuter - 1) / kOuter) : 0};
-    const OuterProblem oa{bf(b.d_place), p.x, p.ldx, p.H, p.da,
-                          p.da ? (int)((p.H + kOuter - 1) / kOuter) : 0};
-    e = run_outer<DT>(ob, oa, plan, p.n, p.r, tiles, stream);
-  }
+  if (!with && (p.da || p.db)) e = run_outer<DT>(gradients(kOuterW), stream);
   return e;
 }
 
