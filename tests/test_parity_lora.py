@@ -250,6 +250,17 @@ def test_gradients_by_differences():
 
 # ---- calls ------------------------------------------------------------------------------
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,V", [(70, 17536), (70, 17541), (257, 4352), (1, 9000)])
+def test_backward_uneven_parts(M, V, dtype):
+    """The sum over V of dy W in parts of which the last is shorter, with the gradients in its grid."""
+    H, n, r = 64, 2, 8
+    x, a, b = rand((M, H), "bf16", 1), rand((n, r, H), "bf16", 2, 0.1), rand((n, V, r), "bf16", 3)
+    w = rand((V, H), "bf16", 4, 0.1)
+    k = (torch.arange(M) % 3 - 1).to(torch.int32).cuda()
+    check_backward(rand((M, V), dtype, 5, 0.1), x, a, b, k, w)
+
+
 @pytest.mark.parametrize("M", [7, 50, 90, 400])
 def test_captured(M):
     """Forward and backward captured once, replayed over new tokens and adapters."""

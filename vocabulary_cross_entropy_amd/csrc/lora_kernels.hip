@@ -57,6 +57,7 @@ __device__ __forceinline__ void parts_of(float v, uint16_t* part) {
 
 // ---- the plan ------------------------------------------------------------------------
 
+// Latency: 2048 tokens of 4 adapters 7 us, a chain of loads, ballots and barriers.
 // order[place]: the token there, -1 for none; first[k] .. first[k + 1]: the tiles of adapter k;
 // owner[tile].  One workgroup; a wavefront counts and then places its own contiguous
 // share of the tokens, so the order within an adapter is the tokens'.
@@ -167,7 +168,8 @@ __device__ void make_plan(const int32_t* adapter, int64_t M, int n, const LoraPl
 }
 
 // (n, R, C) to (n, C, ldr), the places from R to ldr zero; C and ldr multiples of 8.  A workgroup
-// takes a tile of 8192 elements, 16 bytes a thread, as narrow as the rank.
+// takes a tile of 8192 elements, 16 bytes a thread, as narrow as the rank (two adapters of rank 32
+// for 2304 and 32000 and the plan 9.5 us; tiles of 64 x 64 element by element 15.5).
 struct TransposeProblem {
   const uint16_t* in;
   uint16_t* out;
@@ -235,7 +237,7 @@ __global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* 
 // ---- s and ds ----------------------------------------------------------------------------
 
 // Few tokens: a workgroup per token and eight of the r sums.  A lane takes 16 bytes of x and of
-// eight rows of A_k at a time.
+// eight rows of A_k at a time.  Latency: 64 tokens of 4096, r = 16, 5.3 us.
 __global__ __launch_bounds__(256) void lora_token_kernel(LoraFwdArgs p, uint16_t* s2) {
   __shared__ float sh[4][8];
   const int64_t i = blockIdx.x;
@@ -366,6 +368,8 @@ constexpr int row_parts() { return DT == 0 ? kParts : 1; }
 // A workgroup takes a tile of 32 places and a split of k, its wavefronts a quarter of that
 // each, 128 k at a time, the next 128 k's loads in flight: lane l holds row l % 16 and, of each
 // 32 k, the eight from 8 (l / 16) on.  Places without a token read row 0; nobody reads their sums.
+// Bound by the latency of its loads, of which U's rows from L2 are as many as X's: 2600 x 32000 and
+// 2600 x 2304 for r = 32 (178 MB) 48 us, 3.7 TB/s; 2048 x 4096 for r = 16 13 us.
 template <int DT, int NC>
 __device__ __forceinline__ void shrink(const ShrinkProblem& q, const LoraPlan& plan,
                                        const float* scale, int r, int tile, int split,
@@ -588,7 +592,9 @@ __device__ __forceinline__ void store_block(void* out, int64_t at, const f32x16_
   }
 }
 
-// The epilogue of the product: the adapters' share, then the store to out (cols, rows).  Tokens
+// The epilogue of the product: the adapters' share, then the store to out (cols, rows), so that y is
+// written once.  Bound by the product: 2048 x 4096 x 32000 with four adapters of rank 16 456 us,
+// 1.18 PFLOP/s, the library's product alone 451.  Tokens
 // without the adapter enter its product with zeros; rows of U_k that are not finite would make
 // NaN of these, so they are left out there and added, for the adapter's own tokens, behind
 // the store (the sum is an infinity or a NaN then, whatever was stored).
@@ -738,7 +744,9 @@ __device__ __forceinline__ void list_adapters(const LoraShare& a, int64_t j0, Ad
 constexpr int kShareSteps = 4;
 
 // base + the adapters' share, without a product of its own: a wavefront takes 32 rows and 64
-// tokens.
+// tokens, so that the adapters' weights are read once for up to 64 tokens.  64 x 128256 of 16
+// adapters, rank 16 (99 MB) 24 us, 4.1 TB/s: a wavefront's chain of token, list and weights, whose
+// loads go in fours (in ones the call took 62 us, in fours 42).  2600 x 2304 on two FP32 sums (62 MB) 17 us.
 struct AddParams {
   LoraShare a;
   const void* base;  // optional: `sums` arrays (cols, ldb) of type BT, `stride` elements apart
@@ -951,7 +959,9 @@ __device__ __forceinline__ bf16x8_t slab_frag(const uint16_t LDS_AS* s, int d0, 
 }
 
 // Steps of SP places go through two stages of LDS; the next step's rows are on their way in
-// registers, and the tokens of the one after.
+// registers, as they lie in memory (split into parts where they are used, or the loads are waited
+// for at once: 78 us for the following instead of 62), and the tokens of the one after.
+// Bound by reading dy and S: 2600 x 32000 and 2600 x 2304 for two adapters of rank 32 62 us.
 template <int DT, int NC, int W, bool BYCOL>
 __device__ __forceinline__ void outer(const OuterProblem& p, const LoraPlan& plan, int r, int k,
                                       int block, int64_t places, uint16_t* smem) {
@@ -1124,8 +1134,10 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterPair p) {
 }
 
 // dy W in parts and behind them the adapters' gradients, in one grid: the product's tiles leave CUs
-// idle that the gradients, bound by their loads, need not wait for.  Their workgroups take 256
-// columns, since only one lies on a CU here.
+// idle that the gradients, bound by their loads, need not wait for (2600 x 2304 x 32000 in two
+// parts, 198 tiles: 346 us and 62 apart, 357 together; the matrix units at their power
+// limit, 1.1 PFLOP/s).  The gradients' workgroups take 256 columns, since only one lies on a
+// CU here (alone on the chip they are slower so, 493 us for the backward instead of 478).
 template <bool MASK, int NSEG, int DT, int NC>
 __global__ __launch_bounds__(NT, 1) void lora_split_kernel(Segs<NSEG> G, int64_t K, int64_t per,
                                                            int n_ti, int n_tj, int blocks,
@@ -1379,8 +1391,11 @@ __global__ __launch_bounds__(64 * NW, 8 / NW) void lora_skinny_kernel(SkinnyPara
 
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Tokens up to which a workgroup per token forms s.
-constexpr int64_t kTokenWise = 256;
+// Tokens up to which a workgroup per token forms s: 512 of H = 4096 with r = 16 (and the share of
+// 1024 features) 13 us, the plan and its sums 21; r = 64 28 and 29, r = 128 of H = 2304 44 and 47; 1024
+// tokens 16 and 21, 39 and 32, 63 and 49.  And up to which W is streamed past X in LDS: 64 x 4096 x
+// 131072 235 us, in tiles 257; x 32000 63 and 94; 64 x 2304 x 256003 251 and 332.
+constexpr int64_t kTokenWise = 512;
 constexpr int64_t kSkinny = 64;
 
 inline int64_t most_tiles(int64_t M, int64_t n) {
@@ -1648,7 +1663,8 @@ hipError_t backward(const LoraBwdArgs& p, char* ws, hipStream_t stream) {
         plan, p.n, p.r, tiles};
   };
   const OuterPair beside = gradients(2);
-  // with a split product, in its grid
+  // with a split product, in its grid: 1000 x 2304 x 32000 with r = 32 199 us, apart 214; 2600 tokens
+  // 460 and 470, with r = 128 655 and 690; 256 x 4096 x 32000 122 and 133
   const bool joined = p.dx && p.M > 0 && p.w && b.dx.n > 1 && (p.da || p.db) &&
                       (int64_t)p.n * (beside.b.blocks + beside.a.blocks) <= (int64_t)1 << 20;
   const OuterPair* const with = joined ? &beside : nullptr;
