@@ -22,6 +22,10 @@
  *     fused with NLL/LSE; Backward: dZ from recomputed logits, then dX and dW;
  *     a caller-owned reusable workspace with a size query).
  *
+ * Beside them, each described at its declaration: the operators around the head
+ * (rms_*, mx_*, ce_sample) and those of an adapted head (lora_*, adamw_step,
+ * grad_norm, beam_*).
+ *
  * Definitions (per row r with logits z, target t, smoothing eps, vocabulary V):
  *     m = max_v z_v,  d = sum_v exp(z_v - m),  lse = m + ln d
  *     q_v = (1 - eps) [v = t] + eps / V        (eps/V on every class)
