@@ -740,7 +740,8 @@ __device__ __forceinline__ void list_adapters(const LoraShare& a, int64_t j0, Ad
   if (lane == 0) list.n = n;
 }
 
-// Adapters whose weights' loads wait together.
+// Adapters whose weights' loads wait together (64 x 128256 of 16 adapters: four 30 us, eight 34, and
+// 61 x 2304 x 256003 of five 260 and 295, since what is past the end is loaded too).
 constexpr int kShareSteps = 4;
 
 // base + the adapters' share, without a product of its own: a wavefront takes 32 rows and 64
