@@ -1320,13 +1320,19 @@ def beam_reorder(states, parent: torch.Tensor, *, stream=None) -> None:
     B, K = parent.shape
     if K > 1 and parent.stride(1) != 1:
         raise ValueError("the rows of parent must be contiguous")
-    entries = []
+    lead, entries = (B, K), []
+    same = set(map(torch.Tensor.get_device, states)) <= {parent.get_device()}
     for i, t in enumerate(states):
-        if t.dim() < 2 or tuple(t.shape[:2]) != (B, K):
+        if t.shape[:2] != lead:
             raise ValueError(f"states[{i}] must be ({B}, {K}, ...), got {tuple(t.shape)}")
-        if t.device != parent.device:
+        if not same and t.device != parent.device:
             raise ValueError(f"states[{i}] must be on {parent.device}, got {t.device}")
-        entries += (t.data_ptr(), *_beam_pieces(t, f"states[{i}]"))
+        size = t.nbytes
+        if size and _CONTIGUOUS(t):  # rows without gaps, one after the other
+            row = size // (B * K)
+            entries += (t.data_ptr(), row, 1, 0, row, row * K)
+        else:
+            entries += (t.data_ptr(), *_beam_pieces(t, f"states[{i}]"))
     table = (ctypes.c_int64 * len(entries))(*entries)
 
     def call(s):

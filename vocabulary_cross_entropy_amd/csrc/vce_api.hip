@@ -1409,6 +1409,31 @@ inline bool pieces_meet(const vce_beam_state& a, const Pieces& pa, const vce_bea
   return d < a.inner || s - d < b.inner;
 }
 
+// The states of a reordering: their strides, and that no two of them, nor one and `parent`, share memory.
+int check_states(const vce_beam_state* states, int64_t count, int64_t B, int64_t K,
+                 const Range& parent, Pieces* pieces) {
+  for (int64_t i = 0; i < count; ++i) {
+    const vce_beam_state& s = states[i];
+    if (s.inner < 0 || s.outer < 0 || s.stride_outer < 0 || s.stride_beam < 0 ||
+        s.stride_batch < 0)
+      return VCE_EINVAL;
+    pieces[i].bytes = 0;  // of an empty one
+    if (s.inner == 0 || s.outer == 0) continue;
+    if (!s.data) return VCE_EINVAL;
+    if (s.inner > ((int64_t)1 << 40) || s.outer > ((int64_t)1 << 40)) return VCE_EUNSUPPORTED;
+    int64_t cols;
+    if (!mul_ok(s.outer, s.inner / 16 + s.inner % 16, &cols) ||
+        cols / 64 + 1 > (((int64_t)1 << 24) - 1) / B)  // workgroups of one state
+      return VCE_EUNSUPPORTED;
+    Pieces& p = pieces[i];
+    if (!pieces_of(s, B, K, &p)) return VCE_EINVAL;
+    if (!p.apart || overlap(parent, range(s.data, p.bytes))) return VCE_EALIAS;
+    for (int64_t j = 0; j < i; ++j)
+      if (pieces[j].bytes > 0 && pieces_meet(s, p, states[j], pieces[j])) return VCE_EALIAS;
+  }
+  return VCE_OK;
+}
+
 }  // namespace
 
 int beam_reorder(const vce_beam_state* states, int64_t count, int64_t B, int64_t K,
@@ -1421,29 +1446,12 @@ int beam_reorder(const vce_beam_state* states, int64_t count, int64_t B, int64_t
   int64_t span;
   if (!mul_ok(B - 1, parent_stride, &span) || span > INT64_MAX / 8 - K) return VCE_EINVAL;
   const Range pr = range(parent, (span + K) * 4);
-  for (int64_t i = 0; i < count; ++i) {
-    const vce_beam_state& s = states[i];
-    if (s.inner < 0 || s.outer < 0 || s.stride_outer < 0 || s.stride_beam < 0 ||
-        s.stride_batch < 0)
-      return VCE_EINVAL;
-    if (s.inner == 0 || s.outer == 0) continue;
-    if (!s.data) return VCE_EINVAL;
-    if (s.inner > ((int64_t)1 << 40) || s.outer > ((int64_t)1 << 40)) return VCE_EUNSUPPORTED;
-    int64_t cols;
-    if (!mul_ok(s.outer, s.inner / 16 + s.inner % 16, &cols) ||
-        cols / 64 + 1 > (((int64_t)1 << 24) - 1) / B)  // workgroups of one state
-      return VCE_EUNSUPPORTED;
-    Pieces p;
-    if (!pieces_of(s, B, K, &p)) return VCE_EINVAL;
-    if (!p.apart || overlap(pr, range(s.data, p.bytes))) return VCE_EALIAS;
-    for (int64_t j = 0; j < i; ++j) {
-      const vce_beam_state& t = states[j];
-      if (t.inner == 0 || t.outer == 0) continue;
-      Pieces q;
-      pieces_of(t, B, K, &q);
-      if (pieces_meet(s, p, t, q)) return VCE_EALIAS;
-    }
-  }
+  // every state's pieces once: a call may bring hundreds of states
+  Pieces* const pieces = static_cast<Pieces*>(malloc(sizeof(Pieces) * (size_t)count));
+  if (!pieces) return VCE_EHIP;
+  const int rc = check_states(states, count, B, K, pr, pieces);
+  free(pieces);
+  if (rc != VCE_OK) return rc;
   return launch_status(vce::launch_beam_reorder(states, count, B, K, parent, parent_stride,
                                                 static_cast<hipStream_t>(stream)));
 }
